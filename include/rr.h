@@ -352,6 +352,69 @@ rr_status_t rr_bucket_allreduce(const rr_bucket_plan_t* plan, int bucket, void* 
 rr_status_t rr_bucket_allreduce_range(const rr_bucket_plan_t* plan, int first_bucket, int nbuckets,
                                       void* const* grads, int nranks, rr_op_t op, cudaStream_t stream);
 
+/* ------------------------------------------------ global norm, clipping -- */
+
+/* A list of gradient tensors on one or more ranks: tensor t has numels[t]
+ * elements of type dtypes[t] (RR_F32, RR_BF16 or RR_F16; a list may mix them)
+ * on every rank; ptrs holds nranks*ntensors device pointers, rank-major (rank
+ * r's copy of tensor t at r*ntensors + t).  The arrays are the caller's and
+ * are read during the call only. */
+typedef struct rr_tensor_list {
+    void* const* ptrs;
+    const size_t* numels;
+    const rr_dtype_t* dtypes;
+    int32_t ntensors;
+    int32_t nranks;
+} rr_tensor_list_t;
+
+/* The calls below keep fp64 partial sums in a device workspace that the
+ * caller provides (8-byte aligned; its contents need not be set and are not
+ * kept): one call at a time per workspace, so calls on different streams, and
+ * captured graphs that may run at the same time, take one each.
+ * rr_clip_workspace gives the bytes a call needs (host only): for
+ * rr_bucket_allreduce_clip with its plan, bucket range, rank count and synced
+ * list (or NULL); for rr_grad_norm and rr_clip_grads with a NULL plan and
+ * their list. */
+rr_status_t rr_clip_workspace(const rr_bucket_plan_t* plan, int first_bucket, int nbuckets, int nranks,
+                              const rr_tensor_list_t* list, size_t* bytes);
+
+/* The global 2-norm of rank 0's tensors, sqrt(sum over tensors and elements
+ * of x^2), as one fp32 value in *norm (device memory).  It is right over
+ * fp32's whole range (squares that leave it are summed in fp64), 0 for an
+ * empty list, infinite or NaN where the gradients are.  The same bits for the
+ * same tensors on every call.  Tensors may repeat or overlap. */
+rr_status_t rr_grad_norm(const rr_tensor_list_t* grads, float* norm, void* workspace, size_t workspace_bytes,
+                         cudaStream_t stream);
+
+/* Clips gradients that are alike on every rank (the data-parallel step after
+ * its sync): ||g|| is the global norm of rank 0's tensors, c = 1 where
+ * ||g|| + eps <= max_norm and max_norm / (||g|| + eps) elsewhere, and
+ * afterwards every rank's copy of every tensor holds round(c * rank 0's value),
+ * one rounding to nearest even.  With nranks 1 the tensors are clipped in
+ * place; with more, the other ranks' copies are only written (so rank 0 alone
+ * need hold the gradients).  *norm receives ||g||.  A NaN norm makes every
+ * value NaN, an infinite one zeroes the finite values (c is 0).  max_norm may
+ * be 0 or infinite.  Buffers must not overlap. */
+rr_status_t rr_clip_grads(const rr_tensor_list_t* grads, float max_norm, float eps, float* norm, void* workspace,
+                          size_t workspace_bytes, cudaStream_t stream);
+
+/* The sync of buckets first_bucket .. first_bucket + nbuckets - 1 and the
+ * clipping by the global norm of what was synced, in one call: a = the fold of
+ * rr_bucket_allreduce_range in fp32 (the same operations, before its
+ * rounding), ||g|| = the norm of all a and of the synced list's tensors, and
+ * every rank's gradients become round(c * a), rounded once.  synced (or NULL)
+ * lists tensors whose gradients are already alike on every rank -- an
+ * embedding's, say (rr_embedding_grad) -- with the same nranks: they count
+ * into the norm and are clipped as rr_clip_grads does, from rank 0's copy.
+ * Between its two passes the call keeps the fp32 sums in the gradients' own
+ * buffers (ranks 0 and 1).  op: SUM or AVG.  With nranks 1 it is the clipping
+ * alone.  Other arguments and errors as rr_bucket_allreduce_range and
+ * rr_clip_grads. */
+rr_status_t rr_bucket_allreduce_clip(const rr_bucket_plan_t* plan, int first_bucket, int nbuckets, void* const* grads,
+                                     int nranks, rr_op_t op, const rr_tensor_list_t* synced, float max_norm,
+                                     float eps, float* norm, void* workspace, size_t workspace_bytes,
+                                     cudaStream_t stream);
+
 /* ------------------------------------------------ overlapped bucket sync -- */
 
 /* Opaque reducer (host memory and CUDA events owned by the library). */

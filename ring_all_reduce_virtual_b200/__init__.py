@@ -17,11 +17,11 @@ from __future__ import annotations
 import ctypes
 from typing import Sequence
 
-from ._lib import MAX_RANKS, Cost, RingEvent, RRError, Stats, check, lib
+from ._lib import MAX_RANKS, Cost, RingEvent, RRError, Stats, TensorList, check, lib
 
 __all__ = [
     "all_reduce", "all_reduce_wire", "all_reduce_host", "all_reduce_host_noalloc", "ring_step", "ring_schedule", "reduce_scatter", "all_gather", "all_to_all",
-    "RankSet", "BucketPlan", "GradSet", "Reducer", "cost_model", "pick_algo", "set_picker_params", "last_stats",
+    "RankSet", "BucketPlan", "GradSet", "Reducer", "GradList", "grad_norm", "clip_grads", "cost_model", "pick_algo", "set_picker_params", "last_stats",
     "check_timeouts", "RRError",
     "OPS", "ALGOS", "MAX_RANKS",
 ]
@@ -255,6 +255,141 @@ class GradSet:
         self.ptrs = _ptr_array([g for rank in grads for g in rank])
         self._keep = [list(rank) for rank in grads]  # the tensors must outlive the pointers
         self._plans = weakref.WeakSet()  # plans this set was checked against
+        self._list = None  # this set as a GradList, made when a norm or a clipping first asks for it
+
+
+class GradList:
+    """The gradient tensors whose global norm is taken and that are clipped,
+    checked and with their device pointers marshalled once: a list of tensors
+    (one rank), or one list per rank (``grads[r][t]``) whose ranks hold the
+    same sizes and types.  Unlike a ``GradSet`` a list may mix float32,
+    bfloat16 and float16 tensors.  ``grad_norm``, ``clip_grads`` and
+    ``BucketPlan.all_reduce_clip`` accept this, a ``GradSet`` or the lists; it
+    keeps the tensors alive and stays valid while they keep their storage."""
+
+    def __init__(self, grads):
+        grads = list(grads)
+        if grads and hasattr(grads[0], "data_ptr"):
+            grads = [grads]
+        ranks = [list(rank) for rank in grads] or [[]]
+        if len(ranks) > MAX_RANKS:
+            raise ValueError(f"GradList: need 1..{MAX_RANKS} ranks, got {len(ranks)}")
+        flat = [g for rank in ranks for g in rank]
+        for rank in ranks:
+            if len(rank) != len(ranks[0]):
+                raise ValueError("GradList: every rank needs the same number of tensors")
+            for g, g0 in zip(rank, ranks[0]):
+                if not g.is_cuda or not g.is_contiguous() or g.device != flat[0].device:
+                    raise ValueError("GradList: gradients must be contiguous CUDA tensors on one device")
+                if g.numel() != g0.numel() or g.dtype != g0.dtype:
+                    raise ValueError("GradList: a tensor has different sizes or dtypes on different ranks")
+        codes = [_dtype_code(g.dtype) for g in ranks[0]]
+        if _DTYPE_NAMES["i32"] in codes:
+            raise TypeError("GradList: gradients must be float32, bfloat16 or float16")
+        self._marshal(_ptr_array(flat), [int(g.numel()) for g in ranks[0]], codes, len(ranks))
+        self.device = flat[0].device if flat else None
+        self._keep = ranks  # the tensors must outlive the pointers
+
+    def _marshal(self, ptrs, numels, codes, nranks):
+        n = len(numels)
+        self.nranks = nranks
+        self._arrays = (ptrs, (ctypes.c_size_t * max(n, 1))(*numels), (ctypes.c_int * max(n, 1))(*codes))
+        self._c = TensorList(*[ctypes.cast(a, t) for a, (_, t) in zip(self._arrays, TensorList._fields_)], n, nranks)
+        self._ref = ctypes.byref(self._c)
+        self._scratch_bytes = None
+
+    @classmethod
+    def _of(cls, grads) -> "GradList":
+        """``grads`` as a GradList; a GradSet's is made once and kept with it."""
+        if isinstance(grads, GradList):
+            return grads
+        if not isinstance(grads, GradSet):
+            return cls(grads)
+        if grads._list is None:
+            one = cls.__new__(cls)
+            one._marshal(grads.ptrs, grads.numels, [grads.dtype] * len(grads.numels), grads.nranks)
+            one.device = grads.device
+            one._keep = grads._keep
+            grads._list = one
+        return grads._list
+
+    def _workspace(self) -> int:
+        """Bytes of device workspace that a call on this list needs."""
+        if self._scratch_bytes is None:
+            b = ctypes.c_size_t()
+            check(lib().rr_clip_workspace(None, 0, 0, 0, self._ref, ctypes.byref(b)), "clip_workspace")
+            self._scratch_bytes = b.value
+        return self._scratch_bytes
+
+
+def _on_stream(stream, device):
+    """A context in which the caching allocator serves ``stream`` (None: the
+    device's current stream): scratch memory of a call is taken there, so that
+    its next user on that stream is ordered behind the call."""
+    import contextlib
+
+    import torch
+
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device)
+    return torch.cuda.stream(stream)
+
+
+def _on_device(device):
+    """A context with ``device`` current: kernels are launched from there."""
+    import contextlib
+
+    import torch
+
+    if device.index is None or device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _norm_out(out, device):
+    """The fp32 element that receives a norm."""
+    import torch
+
+    if out is None:
+        return torch.empty((), dtype=torch.float32, device=device)
+    if not out.is_cuda or out.dtype != torch.float32 or out.numel() != 1 or out.device != device:
+        raise ValueError("out must be one float32 element on the gradients' device")
+    return out
+
+
+def _norm_call(what: str, gl: GradList, out, stream, call):
+    """Run ``call(norm pointer, workspace pointer, bytes, stream)`` on a list."""
+    import torch
+
+    device = gl.device if gl.device is not None else out.device if out is not None else \
+        torch.device("cuda", torch.cuda.current_device())
+    with _on_device(device), _on_stream(stream, device):
+        norm = _norm_out(out, device)
+        need = gl._workspace()
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+        check(call(norm.data_ptr(), ws.data_ptr(), need, _stream(stream, device)), what)
+    return norm
+
+
+def grad_norm(grads, out=None, stream=None):
+    """The global 2-norm of rank 0's gradients (``rr_grad_norm``): a float32
+    scalar on the device, ``out`` where it is given.  ``grads``: a list of
+    tensors, one list per rank, a ``GradList`` or a ``GradSet``."""
+    gl = GradList._of(grads)
+    return _norm_call("grad_norm", gl, out, stream, lambda norm, ws, b, s: lib().rr_grad_norm(gl._ref, norm, ws, b, s))
+
+
+def clip_grads(grads, max_norm: float, eps: float = 1e-6, out=None, stream=None):
+    """Scale gradients so that their global norm is at most ``max_norm``
+    (``rr_clip_grads``): in place for one rank; for several, rank 0's
+    gradients, scaled, go to every rank.  Returns the norm before clipping as
+    a float32 scalar on the device (``out`` where it is given); nothing waits
+    for the GPU."""
+    gl = GradList._of(grads)
+    return _norm_call("clip_grads", gl, out, stream,
+                      lambda norm, ws, b, s: lib().rr_clip_grads(gl._ref, float(max_norm), float(eps), norm, ws, b, s))
 
 
 class BucketPlan:
@@ -269,6 +404,7 @@ class BucketPlan:
         self._free = lib().rr_bucket_plan_free  # held: module globals may be gone when __del__ runs at exit
         self.numels = [int(m) for m in numels]
         self.grad_dtype = _dtype_code(grad_dtype)
+        self._clip_bytes = {}  # workspace bytes of all_reduce_clip by bucket range, ranks and synced list
 
     def __del__(self):
         h = getattr(self, "_h", None)
@@ -361,6 +497,38 @@ class BucketPlan:
         g, n, dev = self._grads(grads)
         check(lib().rr_bucket_allreduce_range(self._h, first, count, g, n, _op(op), _stream(stream, dev)),
               "bucket_allreduce_range")
+
+
+    def all_reduce_clip(self, grads, max_norm: float, op="avg", first: int = 0, count: int | None = None, synced=None,
+                        eps: float = 1e-6, out=None, stream=None):
+        """Fused sync of buckets ``first .. first + count - 1`` (default: all)
+        and clipping by the global norm of the result
+        (``rr_bucket_allreduce_clip``): the average (``op``) is formed in
+        fp32, scaled and rounded once.  ``synced`` adds gradients that are
+        already alike on every rank (rank 0's count: a ``GradList`` or one list
+        per rank) to the norm and to the clipping.  Returns the norm before
+        clipping as a float32 scalar on the device (``out`` where it is given)."""
+        import torch
+
+        g, n, dev = self._grads(grads)
+        rest = GradList._of(synced) if synced is not None else None
+        if rest is not None and rest.device not in (None, dev):
+            raise ValueError("the synced gradients must be on the gradients' device")
+        count = self.num_buckets - first if count is None else count
+        ref = rest._ref if rest is not None else None
+        with _on_device(dev), _on_stream(stream, dev):
+            norm = _norm_out(out, dev)
+            key = (first, count, n, rest._workspace() if rest is not None else 0)
+            need = self._clip_bytes.get(key)
+            if need is None:
+                b = ctypes.c_size_t()
+                check(lib().rr_clip_workspace(self._h, first, count, n, ref, ctypes.byref(b)), "clip_workspace")
+                need = self._clip_bytes[key] = b.value
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+            check(lib().rr_bucket_allreduce_clip(self._h, first, count, g, n, _op(op), ref, float(max_norm), float(eps),
+                                                 norm.data_ptr(), ws.data_ptr(), need, _stream(stream, dev)),
+                  "bucket_allreduce_clip")
+        return norm
 
 
 class Reducer:

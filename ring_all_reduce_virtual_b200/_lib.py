@@ -46,6 +46,13 @@ class Cost(ctypes.Structure):
     ]
 
 
+class TensorList(ctypes.Structure):
+    _fields_ = [
+        ("ptrs", ctypes.POINTER(ctypes.c_void_p)), ("numels", ctypes.POINTER(ctypes.c_size_t)),
+        ("dtypes", ctypes.POINTER(ctypes.c_int)), ("ntensors", ctypes.c_int32), ("nranks", ctypes.c_int32),
+    ]
+
+
 _lock = threading.Lock()
 _lib: ctypes.CDLL | None = None
 
@@ -54,6 +61,7 @@ def _declare(lib: ctypes.CDLL) -> None:
     P, PP = ctypes.c_void_p, ctypes.POINTER(ctypes.c_void_p)
     i, sz, d = ctypes.c_int, ctypes.c_size_t, ctypes.c_double
     st = ctypes.c_int
+    f, TL = ctypes.c_float, ctypes.POINTER(TensorList)
     sig = {
         "rr_allreduce": (st, [PP, i, sz, i, i, i, P]),
         "rr_allreduce_host": (st, [PP, PP, i, sz, i, i, i, P]),
@@ -73,6 +81,10 @@ def _declare(lib: ctypes.CDLL) -> None:
         "rr_bucket_unpack": (st, [P, i, PP, PP, i, i, P]),
         "rr_bucket_allreduce": (st, [P, i, PP, i, i, P]),
         "rr_bucket_allreduce_range": (st, [P, i, i, PP, i, i, P]),
+        "rr_clip_workspace": (st, [P, i, i, i, TL, ctypes.POINTER(sz)]),
+        "rr_grad_norm": (st, [TL, P, P, sz, P]),
+        "rr_clip_grads": (st, [TL, f, f, P, P, sz, P]),
+        "rr_bucket_allreduce_clip": (st, [P, i, i, PP, i, i, TL, f, f, P, P, sz, P]),
         "rr_reducer_create": (st, [P, PP, i, i, P, i, ctypes.POINTER(P)]),
         "rr_reducer_ready": (st, [P, i, P]),
         "rr_reducer_finish": (st, [P, P]),
@@ -88,9 +100,9 @@ def _declare(lib: ctypes.CDLL) -> None:
         "rr_binary_version": (st, [ctypes.POINTER(i)]),
     }
     for name, (res, args) in sig.items():
-        f = getattr(lib, name)
-        f.restype = res
-        f.argtypes = args
+        fn = getattr(lib, name)
+        fn.restype = res
+        fn.argtypes = args
 
 
 def lib() -> ctypes.CDLL:

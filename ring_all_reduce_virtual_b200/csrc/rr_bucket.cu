@@ -241,19 +241,6 @@ __device__ __forceinline__ void convert_tile(const typename In::T* src, typename
     else convert_quads_staged<In, Out, OP, Q>(s0, dst, head, nq, tile, d, divisor);
 }
 
-// The segment owning work item w: the last s with prefix[s] <= w (segments
-// without tiles have prefix[s] == prefix[s + 1] and are never returned).
-__device__ __forceinline__ int find_segment(const uint64_t* prefix, int nseg, uint64_t w)
-{
-    int lo = 0, hi = nseg;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (prefix[mid] <= w) lo = mid;
-        else hi = mid;
-    }
-    return lo;
-}
-
 // Work item w of a pack/unpack launch -> (tensor t, rank r, tile).
 __device__ __forceinline__ void copy_item(const BucketCopyParams& p, uint64_t w, uint64_t& t, uint64_t& r,
                                           uint64_t& tile)

@@ -1,0 +1,260 @@
+// rr_bucket_clip.cu -- the first pass of the bucket sync with clipping: every
+// rank's gradients are read once and folded in fp32 in ring order (AVG
+// divided), as in the fused bucket sync, but the result waits for the global
+// norm, so it is parked instead of written to every rank: an fp32 sum whole in
+// rank 0's buffer, for 16-bit gradients its upper half in rank 0's buffer and
+// its lower half in rank 1's -- the same elements the CTA has just read, so no
+// memory beside the gradients is needed and the final value is rounded once.
+// Each tile leaves one fp64 partial sum of squares.
+//
+// Traffic of the whole call for N ranks of S elements of e bytes: N S e read
+// and S e written here (2 S e for 16-bit types), then S e (2 S e) read and N S e
+// written by the scaling pass: 2 (N + 1) S e, or 2 (N + 2) S e for 16-bit types,
+// where a sync, a norm and a scaling one after the other move (4 N + 1) S e.
+#include "rr_bulk.cuh"
+#include "rr_clip.cuh"
+
+namespace rr {
+
+namespace {
+
+struct ParkParams {
+    BucketFoldParams f;  // tile0 counts tiles of park_tile_elems
+    double* partial;     // one per tile
+    unsigned int* waits; // as BulkParams (rr_bulk.cuh)
+    uint32_t hold;
+    uint32_t spin;
+    uint32_t tv;         // vectors per rank per tile
+    uint32_t pad_;
+};
+static_assert(sizeof(ParkParams) <= 32764, "ParkParams too large");
+
+template <class G>
+__device__ __forceinline__ void park_one(typename G::T* p0, typename G::T* p1, uint64_t e, float a)
+{
+    if constexpr (sizeof(typename G::T) == 2) {
+        const uint32_t b = __float_as_uint(a);
+        p0[e] = (uint16_t)(b >> 16);
+        p1[e] = (uint16_t)b;
+    } else {
+        p0[e] = a;
+    }
+}
+
+// Fold of element e: the same operations as the sync's, unrounded.
+template <class G, int OP, class InF>
+__device__ __forceinline__ float fold_value(const InF& in, int n, uint64_t e, float divisor)
+{
+    float a = G::ld1(in(0) + e);
+    for (int j = 1; j < n; ++j) a = apply<OP>(a, G::ld1(in(j) + e));
+    return finish<OP>(a, divisor);
+}
+
+// Ranks whose copies of a tensor share a 16-byte phase: tiles staged by bulk
+// copies as in the fused bucket sync (rr_bucket.cu), the parked halves written
+// by bulk stores from slots 0 and 1.
+template <class G, int OP, int NS>
+__global__ void __launch_bounds__(kThreads) bucket_park_kernel(const __grid_constant__ ParkParams bp)
+{
+    using T = typename G::T;
+    constexpr int L = G::L;
+    constexpr bool kSplit = sizeof(T) == 2;
+    pdl_begin();
+    const BucketFoldParams& p = bp.f;
+    const int n = NS > 0 ? NS : p.n;
+    const uint32_t TV = NS > 0 ? bulk_smem<NS>() / (NS > 0 ? NS : 1) / 16 : bp.tv;
+    extern __shared__ __align__(128) uint4 sm[];  // [n][TV]: slot j holds rank (c + j) mod N
+    __shared__ __align__(8) uint64_t bar;
+    __shared__ double sh[kThreads / 32];
+
+    const uint64_t w = blockIdx.x;
+    const int s = find_segment(p.tile0, p.nseg, w);
+    const uint64_t tile = w - p.tile0[s];
+    const BucketSeg& sg = p.seg[s];
+    const int base = (int)sg.t * n;
+    const int start = (int)sg.c;
+    auto in = [&](int j) {
+        int r = start + j;
+        if (r >= n) r -= n;
+        return static_cast<const T*>(p.grad[base + r]) + sg.off;
+    };
+    T* const p0 = static_cast<T*>(p.grad[base]) + sg.off;
+    T* const p1 = static_cast<T*>(p.grad[base + 1]) + sg.off;
+    const uint64_t len = sg.len;
+    uint64_t head = (uint64_t)((L - phase_of(p0, L)) & (L - 1));
+    if (head > len) head = len;
+    const uint64_t nv = (len - head) / L;
+    const uint64_t tail = len - head - nv * L;
+    double acc = 0.0;
+    if (tile == 0 && (uint64_t)threadIdx.x < head + tail) {
+        const uint64_t e = (uint64_t)threadIdx.x < head ? (uint64_t)threadIdx.x : head + nv * L + (threadIdx.x - head);
+        const float x[1] = {fold_value<G, OP>(in, n, e, p.divisor)};
+        park_one<G>(p0, p1, e, x[0]);
+        acc = sum_squares(x);
+    }
+    const uint64_t v0 = tile * TV;
+    if (v0 < nv) {
+        const uint32_t nvt = (uint32_t)(nv - v0 < TV ? nv - v0 : TV);
+        const uint32_t bytes = nvt * 16u;
+        const uint64_t e0 = head + v0 * L;  // 16-byte aligned in every rank's copy
+        const uint32_t b = bulk_smem_addr(&bar);
+        if (threadIdx.x == 0) bulk_bar_init(b, bp.hold);
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}"
+                         ::"r"(b), "r"(bytes * (uint32_t)n) : "memory");
+#pragma unroll
+            for (int j = 0; j < (NS > 0 ? NS : n); ++j)
+                asm volatile(
+                    "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                    ::"r"(bulk_smem_addr(sm + j * TV)), "l"(in(j) + e0), "r"(bytes), "r"(b)
+                    : "memory");
+        }
+        if (!bulk_tile_landed(b, bp.waits, bp.hold, bp.spin)) {
+            // the whole CTA skips the tile: a NaN norm says that the step is lost
+            if (threadIdx.x == 0) bp.partial[w] = __longlong_as_double(0x7ff8000000000000ll);
+            return;
+        }
+        for (uint32_t v = threadIdx.x; v < nvt; v += kThreads) {
+            float a[L];
+            G::unpack(sm[v], a);
+#pragma unroll 4
+            for (int j = 1; j < (NS > 0 ? NS : n); ++j) {
+                float x[L];
+                G::unpack(sm[j * TV + v], x);
+#pragma unroll
+                for (int l = 0; l < L; ++l) a[l] = apply<OP>(a[l], x[l]);
+            }
+#pragma unroll
+            for (int l = 0; l < L; ++l) a[l] = finish_n<OP, NS>(a[l], p.divisor);
+            acc += sum_squares(a);
+            if constexpr (kSplit) {
+                uint32_t h[4], q[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t b0 = __float_as_uint(a[(2 * k) % L]), b1 = __float_as_uint(a[(2 * k + 1) % L]);
+                    h[k] = __byte_perm(b0, b1, 0x7632);
+                    q[k] = __byte_perm(b0, b1, 0x5410);
+                }
+                sm[v] = make_uint4(h[0], h[1], h[2], h[3]);
+                sm[TV + v] = make_uint4(q[0], q[1], q[2], q[3]);
+            } else {
+                sm[v] = G::pack(a);
+            }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;"
+                         ::"l"(p0 + e0), "r"(bulk_smem_addr(sm)), "r"(bytes)
+                         : "memory");
+            if constexpr (kSplit)
+                asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;"
+                             ::"l"(p1 + e0), "r"(bulk_smem_addr(sm + TV)), "r"(bytes)
+                             : "memory");
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+        acc = cta_sum(acc, sh);
+        if (threadIdx.x == 0) {
+            bp.partial[w] = acc;
+            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            bulk_bar_inval(b);
+        }
+        return;
+    }
+    acc = cta_sum(acc, sh);
+    if (threadIdx.x == 0) bp.partial[w] = acc;
+}
+
+// Any ranks: element by element.
+template <class G, int OP>
+__global__ void __launch_bounds__(kThreads) bucket_park_any_kernel(const __grid_constant__ ParkParams bp)
+{
+    using T = typename G::T;
+    __shared__ double sh[kThreads / 32];
+    pdl_begin();
+    const BucketFoldParams& p = bp.f;
+    const int n = p.n;
+    const uint64_t w = blockIdx.x;
+    const int s = find_segment(p.tile0, p.nseg, w);
+    const BucketSeg& sg = p.seg[s];
+    const int base = (int)sg.t * n, start = (int)sg.c;
+    auto in = [&](int j) {
+        int r = start + j;
+        if (r >= n) r -= n;
+        return static_cast<const T*>(p.grad[base + r]) + sg.off;
+    };
+    T* const p0 = static_cast<T*>(p.grad[base]) + sg.off;
+    T* const p1 = static_cast<T*>(p.grad[base + 1]) + sg.off;
+    const uint64_t te = (uint64_t)bp.tv * G::L, lo = (w - p.tile0[s]) * te;
+    const uint64_t hi = sg.len < lo + te ? sg.len : lo + te;
+    double acc = 0.0;
+    for (uint64_t e = lo + threadIdx.x; e < hi; e += kThreads) {
+        const float x[1] = {fold_value<G, OP>(in, n, e, p.divisor)};
+        park_one<G>(p0, p1, e, x[0]);
+        acc += sum_squares(x);
+    }
+    acc = cta_sum(acc, sh);
+    if (threadIdx.x == 0) bp.partial[w] = acc;
+}
+
+template <class G, int OP>
+cudaError_t park_typed(const ParkParams& bp, cudaStream_t s)
+{
+    const int n = bp.f.n;
+    const unsigned work = (unsigned)bp.f.tile0[bp.f.nseg];
+    auto go = [&](void (*kernel)(ParkParams), uint32_t smem) {
+        cudaLaunchAttribute attr{};
+        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr.val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(work);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = s;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, bp);
+        return e != cudaSuccess ? e : cudaGetLastError();
+    };
+    if (!bp.f.vec_ok || !bp.waits) return go(bucket_park_any_kernel<G, OP>, 0);
+    switch (n) {
+    case 2: return go(bucket_park_kernel<G, OP, 2>, bulk_smem<2>());
+    case 4: return go(bucket_park_kernel<G, OP, 4>, bulk_smem<4>());
+    case 8: return go(bucket_park_kernel<G, OP, 8>, bulk_smem<8>());
+    case 16: return go(bucket_park_kernel<G, OP, 16>, bulk_smem<16>());
+    }
+    return go(bucket_park_kernel<G, OP, 0>, bp.tv * 16u * (uint32_t)n);
+}
+
+}  // namespace
+
+uint64_t park_tile_elems(int grad_dtype, int n)
+{
+    return (uint64_t)bulk_tile_vectors(n) * (grad_dtype == kF32 ? 4u : 8u);
+}
+
+cudaError_t launch_bucket_park(int grad_dtype, int op, const BucketFoldParams& p, double* partial, cudaStream_t s)
+{
+    RankParams rp{};
+    rp.waits = bulk_wait_counters();
+    const BulkParams wait = bulk_params(rp);
+    if (p.tile0[p.nseg] > kMaxGrid || p.n < 2) return cudaErrorInvalidValue;
+    ParkParams bp;
+    bp.f = p;
+    bp.partial = partial;
+    bp.waits = wait.waits;
+    bp.hold = wait.hold;
+    bp.spin = wait.spin;
+    bp.tv = bulk_tile_vectors(p.n);
+    bp.pad_ = 0;
+    const bool avg = op == kAvg;
+    switch (grad_dtype) {
+    case kF32: return avg ? park_typed<F32T, kAvg>(bp, s) : park_typed<F32T, kSum>(bp, s);
+    case kBF16: return avg ? park_typed<BF16T, kAvg>(bp, s) : park_typed<BF16T, kSum>(bp, s);
+    case kF16: return avg ? park_typed<F16T, kAvg>(bp, s) : park_typed<F16T, kSum>(bp, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace rr

@@ -1,0 +1,265 @@
+// rr_clip.cu -- the global gradient norm over many tensors, and clipping by
+// it: one pass that reads every tensor and leaves a few hundred fp64 partial
+// sums of squares, and one that sums those, forms the coefficient and writes
+// the scaled gradients to every rank.
+//
+//   norm    ||g|| = sqrt(sum over tensors t and elements i of g_t[i]^2)
+//   clip    c = 1 if ||g|| + eps <= max_norm else max_norm / (||g|| + eps);
+//           g_r[i] = round(c * g_0[i]) on every rank r
+//
+// Both are bound by HBM.  Partial sums are joined in a fixed order (no
+// atomics), so a call's bits depend only on its tensors.
+#include "rr_clip.cuh"
+
+namespace rr {
+
+namespace {
+
+constexpr int kNormU = 8;   // 16-byte vectors per thread per tile of the norm: 32 KB a tile
+constexpr int kScaleU = 4;  // and of the scaling: 16 KB of one rank's copy
+
+__device__ __forceinline__ uint4 ld_keep(const void* p) { return *reinterpret_cast<const uint4*>(p); }
+
+// The squares of one tile of one tensor, as this thread's share.
+template <class Ty>
+__device__ __forceinline__ double tile_squares(const typename Ty::T* p, uint64_t len, uint64_t tile)
+{
+    constexpr int L = Ty::L;
+    constexpr uint64_t TV = (uint64_t)kThreads * kNormU;
+    const uint64_t tid = threadIdx.x;
+    uint64_t head = (uint64_t)((L - phase_of(p, L)) & (L - 1));
+    if (head > len) head = len;
+    const uint64_t nv = (len - head) / L, tail = len - head - nv * L;
+    double acc = 0.0;
+    if (tile == 0 && tid < head + tail) {
+        const float x[1] = {Ty::ld1(p + (tid < head ? tid : head + nv * L + (tid - head)))};
+        acc = sum_squares(x);
+    }
+    const uint64_t v0 = tile * TV + tid;
+    uint4 raw[kNormU];
+#pragma unroll
+    for (int u = 0; u < kNormU; ++u) {
+        const uint64_t v = v0 + (uint64_t)u * kThreads;
+        raw[u] = v < nv ? ld_keep(p + head + v * L) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    return acc + sum_squares_of<Ty>(raw);
+}
+
+// Every CTA takes one run of consecutive tiles, so it looks its tensor up once.
+template <class Ty, int CAP>
+__global__ void __launch_bounds__(kThreads, 4) norm_kernel(const __grid_constant__ NormParamsT<CAP> p)
+{
+    __shared__ double sh[kThreads / 32];
+    pdl_begin();
+    const uint64_t total = p.tile0[p.nt], G = gridDim.x;
+    const uint64_t lo = total * blockIdx.x / G, hi = total * (blockIdx.x + 1) / G;
+    double acc = 0.0;
+    int t = find_segment(p.tile0, p.nt, lo);
+    for (uint64_t w = lo; w < hi; ++w) {
+        while (w >= p.tile0[t + 1]) ++t;
+        acc += tile_squares<Ty>(static_cast<const typename Ty::T*>(p.ptr[t]), p.len[t], w - p.tile0[t]);
+    }
+    acc = cta_sum(acc, sh);
+    if (threadIdx.x == 0) p.partial[blockIdx.x] = acc;
+}
+
+// Many partials to kJoinCtas: CTA b sums the b-th run of them.
+__global__ void __launch_bounds__(kThreads) norm_join_kernel(const double* in, int64_t count, double* out)
+{
+    __shared__ double sh[kThreads / 32];
+    pdl_begin();
+    const int64_t lo = count * blockIdx.x / gridDim.x, hi = count * (blockIdx.x + 1) / gridDim.x;
+    const double v = partials_sum(in + lo, hi - lo, sh);
+    if (threadIdx.x == 0) out[blockIdx.x] = v;
+}
+
+__global__ void __launch_bounds__(kThreads) norm_finish_kernel(const __grid_constant__ ClipArgs a)
+{
+    __shared__ double sh[kThreads / 32];
+    pdl_begin();
+    clip_coef(a, sh);
+}
+
+// The two fp32 values whose upper halves are the word h and lower halves the
+// word l.
+__device__ __forceinline__ void unpark2(uint32_t h, uint32_t l, float& x, float& y)
+{
+    x = __uint_as_float(__byte_perm(l, h, 0x5410));
+    y = __uint_as_float(__byte_perm(l, h, 0x7632));
+}
+
+// Rank 0's copy, scaled, into every rank's.  PARKED (16-bit types): the value
+// is the fp32 whose upper half rank 0's copy holds and whose lower half rank
+// 1's does.  A thread reads its elements of both before it writes any copy.
+// The tiles run from the last to the first: what the pass before touched last
+// is what L2 still holds.
+template <class Ty, bool PARKED, int CAP, int PTRS>
+__global__ void __launch_bounds__(kThreads, 4) clip_scale_kernel(const __grid_constant__ ScaleParamsT<CAP, PTRS> p)
+{
+    using T = typename Ty::T;
+    constexpr int L = Ty::L;
+    constexpr uint64_t TV = (uint64_t)kThreads * kScaleU;
+    __shared__ double sh[kThreads / 32];
+    pdl_begin();
+    const float c = clip_coef(p.clip, sh);
+    const uint64_t total = p.tile0[p.nt], tid = threadIdx.x;
+    const int n = p.n;
+    for (uint64_t i = blockIdx.x; i < total; i += gridDim.x) {
+        const uint64_t w = total - 1 - i;
+        const int t = find_segment(p.tile0, p.nt, w);
+        const uint64_t tile = w - p.tile0[t], len = p.len[t];
+        T* const* ptr = reinterpret_cast<T* const*>(&p.ptr[(size_t)t * n]);
+        const T* src = ptr[0];
+        const T* low = PARKED ? ptr[1] : ptr[0];
+        auto one = [&](uint64_t e) {
+            float x;
+            if constexpr (PARKED) x = __uint_as_float(((uint32_t)src[e] << 16) | (uint32_t)low[e]);
+            else x = Ty::ld1(src + e);
+            x = __fmul_rn(x, c);
+            for (int o = 0; o < n; ++o) Ty::st1(ptr[o] + e, x);
+        };
+        if (!p.vec[t]) {
+            const uint64_t e0 = tile * TV * L;
+            for (uint64_t e = e0 + tid; e < len && e < e0 + TV * L; e += kThreads) one(e);
+            continue;
+        }
+        uint64_t head = (uint64_t)((L - phase_of(src, L)) & (L - 1));
+        if (head > len) head = len;
+        const uint64_t nv = (len - head) / L, tail = len - head - nv * L;
+        if (tile == 0 && tid < head + tail) one(tid < head ? tid : head + nv * L + (tid - head));
+        const uint64_t v0 = tile * TV + tid;
+        uint4 raw[kScaleU], lo[PARKED ? kScaleU : 1];
+#pragma unroll
+        for (int u = 0; u < kScaleU; ++u) {
+            const uint64_t v = v0 + (uint64_t)u * kThreads;
+            if (v < nv) {
+                raw[u] = ld_keep(src + head + v * L);
+                if constexpr (PARKED) lo[u] = ld_keep(low + head + v * L);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kScaleU; ++u) {
+            float a[L];
+            if constexpr (PARKED) {
+                unpark2(raw[u].x, lo[u].x, a[0], a[1]);
+                unpark2(raw[u].y, lo[u].y, a[2], a[3]);
+                unpark2(raw[u].z, lo[u].z, a[4], a[5]);
+                unpark2(raw[u].w, lo[u].w, a[6], a[7]);
+            } else {
+                Ty::unpack(raw[u], a);
+            }
+#pragma unroll
+            for (int l = 0; l < L; ++l) a[l] = __fmul_rn(a[l], c);
+            raw[u] = Ty::pack(a);
+        }
+        for (int o = 0; o < n; ++o) {
+            T* q = ptr[o] + head;
+#pragma unroll
+            for (int u = 0; u < kScaleU; ++u) {
+                const uint64_t v = v0 + (uint64_t)u * kThreads;
+                if (v < nv) stv(q + v * L, raw[u]);
+            }
+        }
+    }
+}
+
+// A launch as a programmatic dependent of the stream's previous kernel.
+template <class... A>
+cudaError_t launch_pdl(void (*kernel)(A...), unsigned grid, cudaStream_t s, const A&... a)
+{
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a...);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// The same table with fewer entries: a short list's parameter block.
+template <class Small>
+Small shrink(const NormParams& p)
+{
+    Small q{};
+    for (int t = 0; t < p.nt; ++t) {
+        q.ptr[t] = p.ptr[t];
+        q.len[t] = p.len[t];
+        q.tile0[t + 1] = p.tile0[t + 1];
+    }
+    q.partial = p.partial;
+    q.nt = p.nt;
+    return q;
+}
+
+template <class Ty>
+cudaError_t norm_typed(const NormParams& p, unsigned grid, cudaStream_t s)
+{
+    if (p.nt <= kNormTensorsSmall)
+        return launch_pdl(norm_kernel<Ty, kNormTensorsSmall>, grid, s, shrink<NormParamsT<kNormTensorsSmall>>(p));
+    return launch_pdl(norm_kernel<Ty, kNormTensors>, grid, s, p);
+}
+
+template <class Ty, bool PARKED>
+cudaError_t scale_typed(const ScaleParams& p, unsigned grid, cudaStream_t s)
+{
+    if (p.nt <= kScaleTensorsSmall && p.nt * p.n <= kScalePtrsSmall) {
+        ScaleParamsT<kScaleTensorsSmall, kScalePtrsSmall> q{};
+        for (int i = 0; i < p.nt * p.n; ++i) q.ptr[i] = p.ptr[i];
+        for (int t = 0; t < p.nt; ++t) {
+            q.len[t] = p.len[t];
+            q.tile0[t + 1] = p.tile0[t + 1];
+            q.vec[t] = p.vec[t];
+        }
+        q.clip = p.clip;
+        q.n = p.n;
+        q.nt = p.nt;
+        return launch_pdl(clip_scale_kernel<Ty, PARKED, kScaleTensorsSmall, kScalePtrsSmall>, grid, s, q);
+    }
+    return launch_pdl(clip_scale_kernel<Ty, PARKED, kScaleTensors, kScalePtrs>, grid, s, p);
+}
+
+}  // namespace
+
+uint64_t norm_tile_elems(int dtype) { return (uint64_t)kThreads * kNormU * (dtype == kF32 ? 4u : 8u); }
+uint64_t scale_tile_elems(int dtype) { return (uint64_t)kThreads * kScaleU * (dtype == kF32 ? 4u : 8u); }
+
+cudaError_t launch_norm(int dtype, const NormParams& p, int* slots, cudaStream_t s)
+{
+    const uint64_t work = p.tile0[p.nt];
+    const unsigned grid = (unsigned)(work < kNormCtas ? work : kNormCtas);
+    *slots = (int)grid;
+    if (grid == 0) return cudaSuccess;
+    switch (dtype) {
+    case kF32: return norm_typed<F32T>(p, grid, s);
+    case kBF16: return norm_typed<BF16T>(p, grid, s);
+    case kF16: return norm_typed<F16T>(p, grid, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_norm_join(const double* in, int64_t count, double* out, int* slots, cudaStream_t s)
+{
+    *slots = kJoinCtas;
+    return launch_pdl(norm_join_kernel, (unsigned)kJoinCtas, s, in, count, out);
+}
+
+cudaError_t launch_norm_finish(const ClipArgs& a, cudaStream_t s) { return launch_pdl(norm_finish_kernel, 1u, s, a); }
+
+cudaError_t launch_clip_scale(int dtype, bool parked, const ScaleParams& p, cudaStream_t s)
+{
+    const uint64_t work = p.tile0[p.nt];
+    const unsigned grid = (unsigned)(work < kNormCtas ? work : kNormCtas);
+    if (grid == 0) return cudaSuccess;
+    switch (dtype) {
+    case kF32: return scale_typed<F32T, false>(p, grid, s);  // fp32 sums are parked whole, in rank 0's buffers
+    case kBF16: return parked ? scale_typed<BF16T, true>(p, grid, s) : scale_typed<BF16T, false>(p, grid, s);
+    case kF16: return parked ? scale_typed<F16T, true>(p, grid, s) : scale_typed<F16T, false>(p, grid, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace rr

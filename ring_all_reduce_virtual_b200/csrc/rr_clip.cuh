@@ -1,0 +1,122 @@
+// rr_clip.cuh -- device pieces shared by the kernels that sum squares and by
+// those that clip: the exact range of a sum of squares, the CTA's fp64 sum,
+// the coefficient.
+//
+// The norm is sqrt(sum x^2).  Squares of fp32 values leave fp32's range where
+// the norm itself does not (x = 1e30 or 1e-30), so a thread sums a few dozen
+// squares in fp32 -- at most 64 terms, a relative error below 64 * 2^-24 of a
+// term that the next level averages out -- and checks that sum: if it is not
+// finite, or so small that a square could have been lost below fp32's range
+// while some value is not zero, the same values are summed again in fp64.
+// Everything above a thread's few dozen is fp64.
+#pragma once
+
+#include "rr_device.cuh"
+#include "rr_internal.h"
+
+namespace rr {
+
+// Start of a kernel launched as a programmatic dependent of the stream's
+// previous one: wait for it and its memory, then let the next be scheduled.
+// A no-op in a plain launch.
+__device__ __forceinline__ void pdl_begin()
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// A sum of at most 64 squares in fp32 is taken as it is when it is finite and
+// at least 2^-96: a square lost below fp32's smallest normal number is below
+// 2^-126, so 64 of them are below 2^-120, 2^-24 of the sum.
+__device__ __forceinline__ bool squares_in_range(float s)
+{
+    return s >= 0x1p-96f && s <= 0x1.fffffep127f;
+}
+
+// Sum of the squares of N values given in fp32, exact in range.
+template <int N>
+__device__ __forceinline__ double sum_squares(const float (&a)[N])
+{
+    static_assert(N <= 64, "squares_in_range counts at most 64 terms");
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float big = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        s[i & 3] = __fmaf_rn(a[i], a[i], s[i & 3]);
+        big = fmaxf(big, fabsf(a[i]));  // 0 exactly where every value is (or is NaN: then the sum is too)
+    }
+    const float t = (s[0] + s[1]) + (s[2] + s[3]);
+    if (squares_in_range(t) || (t == 0.0f && big == 0.0f)) return (double)t;
+    double d = 0.0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) d = __fma_rn((double)a[i], (double)a[i], d);
+    return d;
+}
+
+// The same for U whole vectors of a type, kept packed until they are summed.
+template <class Ty, int U>
+__device__ __forceinline__ double sum_squares_of(const uint4 (&raw)[U])
+{
+    constexpr int L = Ty::L;
+    static_assert(U * L <= 64, "squares_in_range counts at most 64 terms");
+    constexpr uint32_t kMagnitude = L == 8 ? 0x7fff7fffu : 0x7fffffffu;  // every bit but the signs
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    uint32_t any = 0u;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        float a[L];
+        Ty::unpack(raw[u], a);
+#pragma unroll
+        for (int l = 0; l < L; ++l) s[l & 3] = __fmaf_rn(a[l], a[l], s[l & 3]);
+        any |= raw[u].x | raw[u].y | raw[u].z | raw[u].w;
+    }
+    const float t = (s[0] + s[1]) + (s[2] + s[3]);
+    if (squares_in_range(t) || (any & kMagnitude) == 0u) return (double)t;
+    double d = 0.0;
+#pragma unroll 1
+    for (int u = 0; u < U; ++u) {
+        float a[L];
+        uint4 r = raw[0];
+#pragma unroll
+        for (int k = 1; k < U; ++k)
+            if (k == u) r = raw[k];  // a register array takes no run-time index
+        Ty::unpack(r, a);
+#pragma unroll
+        for (int l = 0; l < L; ++l) d = __fma_rn((double)a[l], (double)a[l], d);
+    }
+    return d;
+}
+
+// The sum of v over the CTA's kThreads threads, in a fixed order, in every
+// thread.  sh: kThreads / 32 doubles; the CTA must not be using them.
+__device__ __forceinline__ double cta_sum(double v, double* sh)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+    __syncthreads();
+    double t = 0.0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) t += sh[w];
+    return t;
+}
+
+// Sum of `count` partial sums, in the same order in every CTA.
+__device__ __forceinline__ double partials_sum(const double* p, int64_t count, double* sh)
+{
+    double v = 0.0;
+    for (int64_t i = threadIdx.x; i < count; i += kThreads) v += p[i];
+    return cta_sum(v, sh);
+}
+
+// The clipping's coefficient, 1 where the norm is within max_norm and
+// max_norm / (norm + eps) otherwise: 0 for an infinite norm, NaN for NaN.
+__device__ __forceinline__ float clip_coef(const ClipArgs& a, double* sh)
+{
+    const double norm = sqrt(partials_sum(a.partial, a.npartial, sh));
+    if (a.norm && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = (float)norm;
+    const double den = norm + (double)a.eps;
+    return den <= (double)a.max_norm ? 1.0f : (float)((double)a.max_norm / den);
+}
+
+}  // namespace rr

@@ -311,6 +311,19 @@ __device__ __forceinline__ uint4 shift_window(const uint4& lo, const uint4& hi, 
     return make_uint4(w0, w1, w2, w3);
 }
 
+// The segment owning work item w: the last s with prefix[s] <= w (segments
+// without tiles have prefix[s] == prefix[s + 1] and are never returned).
+__device__ __forceinline__ int find_segment(const uint64_t* prefix, int nseg, uint64_t w)
+{
+    int lo = 0, hi = nseg;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (prefix[mid] <= w) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
 // --------------------------------------------------------------- the tile
 
 // Scalar fold of element e of a segment.

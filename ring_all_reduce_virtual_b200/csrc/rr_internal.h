@@ -112,6 +112,52 @@ struct BucketFoldParams {
     float divisor;
 };
 
+// Global norm and clipping (rr_clip.cu).  A launch of the norm covers up to
+// CAP tensors of one type and writes one fp64 partial sum of squares per CTA;
+// a small table keeps the parameter block of a short list small.
+constexpr int kNormCtas = 592;        // CTAs of a norm launch: 4 on each of 148 SMs
+constexpr int kNormTensors = 1024;    // tensors per launch
+constexpr int kNormTensorsSmall = 64;
+template <int CAP>
+struct NormParamsT {
+    const void* ptr[CAP];
+    uint64_t len[CAP];
+    uint64_t tile0[CAP + 1];  // first work item (tile) of tensor t
+    double* partial;          // this launch's slots, one per CTA
+    int nt;
+    int pad_;
+};
+using NormParams = NormParamsT<kNormTensors>;
+
+// What a launch that needs the norm reads: the partial sums of squares, and
+// the clipping's arguments.
+struct ClipArgs {
+    const double* partial;
+    int npartial;
+    int pad_;
+    float max_norm;
+    float eps;
+    float* norm;  // where the launch writes the norm (NULL: it does not)
+};
+
+// The clipping's second pass: rank 0's copy of each tensor, scaled, into
+// every rank's (entry t * n + r of ptr is rank r's copy of tensor t).
+constexpr int kScaleTensors = 512;
+constexpr int kScaleTensorsSmall = 64;
+template <int CAP, int PTRS>
+struct ScaleParamsT {
+    void* ptr[PTRS];
+    uint64_t len[CAP];
+    uint64_t tile0[CAP + 1];
+    uint8_t vec[CAP];  // every rank's copy of the tensor at one 16-byte phase
+    ClipArgs clip;
+    int n;
+    int nt;
+};
+constexpr int kScalePtrs = 2048;
+constexpr int kScalePtrsSmall = 256;
+using ScaleParams = ScaleParamsT<kScaleTensors, kScalePtrs>;
+
 enum DType : int { kF32 = 0, kBF16 = 1, kI32 = 2, kF16 = 3 };
 enum Kind : int {
     kOneshotRing = 0,
@@ -176,6 +222,20 @@ cudaError_t launch_bucket_unpack(int grad_dtype, int op, const BucketCopyParams&
 cudaError_t launch_bucket_fold(int grad_dtype, int op, const BucketFoldParams& p, cudaStream_t s,
                                uint64_t max_grid = kMaxGrid, bool pdl = false);
 
+// Global norm and clipping.  parked (16-bit types): the values are fp32 sums
+// whose upper halves lie in rank 0's buffers and lower halves in rank 1's.
+uint64_t norm_tile_elems(int dtype);
+uint64_t scale_tile_elems(int dtype);
+cudaError_t launch_norm(int dtype, const NormParams& p, int* slots, cudaStream_t s);
+cudaError_t launch_norm_join(const double* in, int64_t count, double* out, int* slots, cudaStream_t s);
+cudaError_t launch_norm_finish(const ClipArgs& a, cudaStream_t s);
+cudaError_t launch_clip_scale(int dtype, bool parked, const ScaleParams& p, cudaStream_t s);
+constexpr int kJoinCtas = 128;        // partials that launch_norm_join leaves
+constexpr int kMaxPartials = 2048;    // partials that a launch sums itself
+// The clipped sync's first pass: fold, park the sums, one partial per tile.
+uint64_t park_tile_elems(int grad_dtype, int n);
+cudaError_t launch_bucket_park(int grad_dtype, int op, const BucketFoldParams& p, double* partial, cudaStream_t s);
+
 }  // namespace rr
 
 namespace rr {
@@ -185,4 +245,6 @@ static_assert(sizeof(StepParams) <= 32764, "StepParams too large");
 static_assert(sizeof(ChainParams) <= 32764, "ChainParams too large");
 static_assert(sizeof(BucketCopyParams) <= 32764, "BucketCopyParams too large");
 static_assert(sizeof(BucketFoldParams) <= 32764, "BucketFoldParams too large");
+static_assert(sizeof(NormParams) <= 32764, "NormParams too large");
+static_assert(sizeof(ScaleParams) <= 32764, "ScaleParams too large");
 }  // namespace rr

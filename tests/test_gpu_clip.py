@@ -1,0 +1,341 @@
+"""The global norm, clipping and the clipped bucket sync against their formulas
+in 64 bits.
+
+Tolerances, for values of type t with half a step u_t = torch.finfo(t).eps / 2
+(fp32 2^-24, bf16 2^-8, fp16 2^-11):
+
+* norm: a thread sums at most 64 squares in fp32 in four chains of at most 16
+  fused steps and two joins, each off by at most 2^-24 of a sum of positive
+  terms: 18 * 2^-24 of the sum of squares, half of that of its root, and one
+  rounding to fp32: 10 * 2^-24.
+* coefficient: the norm's 9 * 2^-24 and its own rounding: 10 * 2^-24; the
+  product with an fp32 value one more: 11 * 2^-24; then the rounding to t, u_t
+  (an fp32 result has only the product's), or half the smallest subnormal
+  step where that is more.
+* a fold of N ranks: N - 1 roundings, each at most 2^-24 of the sum of the
+  magnitudes, and AVG's division one of the quotient.
+"""
+import math
+
+import pytest
+import torch
+
+import ring_all_reduce_virtual_b200 as rrv
+
+pytestmark = pytest.mark.gpu
+
+E = 2.0 ** -24
+DT = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+U = {torch.float32: 0.0, torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
+SUB = {torch.float32: 2.0 ** -150, torch.bfloat16: 2.0 ** -134, torch.float16: 2.0 ** -25}
+GUARD = 64
+
+
+class Guarded:
+    """A tensor `off` elements past a 256-byte boundary between canaries."""
+
+    def __init__(self, values, off=0):
+        n = values.numel()
+        self.big = torch.empty(GUARD * 2 + off + n, dtype=values.dtype, device="cuda")
+        self.raw = self.big.view(torch.uint8)
+        self.raw.fill_(0xA5)
+        self.t = self.big[GUARD + off:GUARD + off + n]
+        self.t.copy_(values)
+        es = values.element_size()
+        self.lo, self.hi = (GUARD + off) * es, (GUARD + off + n) * es
+
+    def check(self):
+        assert bool((self.raw[:self.lo] == 0xA5).all()) and bool((self.raw[self.hi:] == 0xA5).all())
+
+
+def values(seed, n, dtype, std=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(n, generator=g, device="cuda") * std).to(dtype)
+
+
+def norm64(ts):
+    return math.sqrt(sum(float(t.double().square().sum()) for t in ts))
+
+
+def near_norm(got, want):
+    assert got.dtype == torch.float32 and abs(float(got) - want) <= 10 * E * want, (float(got), want)
+
+
+def near_scaled(got, want, extra=0.0):
+    """`got` is round(c * a) where want = c * a in 64 bits; extra: bound on c * (a's own error)."""
+    dt = got.dtype
+    tol = want.abs() * (11 * E + U[dt] * (1 + 2.0 ** -10)) + SUB[dt] + extra
+    bad = (got.double() - want).abs() > tol
+    assert not bool(bad.any()), f"{int(bad.sum())} of {bad.numel()} off, worst {float((got.double() - want).abs().max())}"
+
+
+# -------------------------------------------------------------------- norm
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("sizes", [[1], [0], [], [0, 1, 0], [7, 8, 9], [16384], [16385, 3], [70001, 5, 200003]])
+@pytest.mark.parametrize("off", [0, 1, 5])
+def test_norm_sizes_types_phases(dtype, sizes, off):
+    ts = [Guarded(values(i, n, DT[dtype], 0.5), off * (i + 1) % 9) for i, n in enumerate(sizes)]
+    got = rrv.grad_norm([g.t for g in ts], out=torch.full((), 7.0, device="cuda"))
+    near_norm(got, norm64([g.t for g in ts]))
+    for g in ts:
+        g.check()
+
+
+def test_norm_mixed_types_and_many_tensors():
+    sizes = [(i * 37) % 301 for i in range(2500)]
+    ts = [values(i, n, list(DT.values())[i % 3]) for i, n in enumerate(sizes)]
+    got = rrv.grad_norm(ts)
+    near_norm(got, norm64(ts))
+    assert torch.equal(got, rrv.grad_norm(rrv.GradList(ts)))  # the same bits again
+    assert rrv.last_stats()["launches"] == 4  # one per type (833 or 834 tensors each) and the join
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("scale", [1e-36, 1e-30, 1e-20, 1e18, 1e30])
+def test_norm_over_the_whole_range(dtype, scale):
+    t = (values(3, 5000, torch.float32).double() * scale).to(DT[dtype])
+    near_norm(rrv.grad_norm([t]), norm64([t]))
+    mixed = torch.cat([t, values(4, 5000, DT[dtype])])
+    near_norm(rrv.grad_norm([mixed]), norm64([mixed]))
+
+
+def test_norm_of_zeros_infinities_and_nans():
+    z = torch.zeros(100003, device="cuda")
+    assert float(rrv.grad_norm([z, -z])) == 0.0
+    for dt in DT.values():
+        t = values(5, 40000, dt)
+        t[12345] = float("inf")
+        assert float(rrv.grad_norm([t])) == math.inf
+        t[20001] = float("nan")
+        assert math.isnan(float(rrv.grad_norm([t])))
+    huge = torch.full((4,), 3e38, device="cuda")  # the norm itself is above fp32's largest
+    assert float(rrv.grad_norm([huge])) == math.inf
+
+
+def test_norm_counts_repeated_tensors():
+    t = values(6, 1001, torch.float32)
+    near_norm(rrv.grad_norm([t, t]), math.sqrt(2) * norm64([t]))
+
+
+# -------------------------------------------------------------------- clip
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("n", [1, 2, 5])
+@pytest.mark.parametrize("layout", ["aligned", "same", "mixed"])
+def test_clip_scales_rank_0s_copy_into_every_rank(dtype, n, layout):
+    sizes = [1, 40003, 8, 0, 5000]
+    off = {"aligned": lambda r, t: 0, "same": lambda r, t: 3 * t + 1, "mixed": lambda r, t: r + t}[layout]
+    ranks = [[Guarded(values(100 * r + t, m, DT[dtype], 0.1), off(r, t)) for t, m in enumerate(sizes)] for r in range(n)]
+    src = [g.t.clone() for g in ranks[0]]
+    want = norm64(src)
+    got = rrv.clip_grads([[g.t for g in rank] for rank in ranks], 0.3 * want, eps=1e-3)
+    near_norm(got, want)
+    c = 0.3 * want / (want + 1e-3)
+    for rank in ranks:
+        for g, a in zip(rank, src):
+            near_scaled(g.t, a.double() * c)
+            assert torch.equal(g.t, ranks[0][rank.index(g)].t)
+            g.check()
+
+
+def test_clip_below_the_limit_changes_nothing():
+    ts = [values(i, 3001, dt) for i, dt in enumerate(DT.values())]
+    before = [t.clone() for t in ts]
+    want = norm64(ts)
+    for limit in (want * 1.001, math.inf):
+        near_norm(rrv.clip_grads(ts, limit, eps=0.0), want)
+        assert all(torch.equal(a, b) for a, b in zip(ts, before))
+    rrv.clip_grads(ts, 0.0)
+    assert all(not bool(t.any()) for t in ts)
+    near_norm(rrv.clip_grads(ts, 1.0), 0.0)  # all zeros now
+    near_norm(rrv.clip_grads([], 1.0), 0.0)
+
+
+def test_clip_with_infinities_and_nans():
+    t = values(8, 999, torch.float32)
+    t[5] = -math.inf
+    assert float(rrv.clip_grads([t], 1.0)) == math.inf
+    assert math.isnan(float(t[5])) and int(torch.count_nonzero(t)) == 1  # 0 * inf; the finite values are 0
+    t = values(8, 999, torch.bfloat16)
+    t[5] = math.nan
+    assert math.isnan(float(rrv.clip_grads([t], math.inf))) and bool(t.isnan().all())
+
+
+def test_clip_many_tensors_in_several_launches():
+    sizes = [(i * 53) % 97 + 1 for i in range(1200)]
+    ranks = [[values(i + 7 * r, m, torch.bfloat16 if i % 4 else torch.float32) for i, m in enumerate(sizes)] for r in range(3)]
+    src = [t.clone() for t in ranks[0]]
+    want = norm64(src)
+    near_norm(rrv.clip_grads(rrv.GradList(ranks), 0.5 * want, eps=0.0), want)
+    for rank in ranks:
+        for t, a in zip(rank, src):
+            near_scaled(t, a.double() * 0.5)
+
+
+def test_clip_offsets_past_32_bits():
+    n = (1 << 32) + 4099
+    t = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    at = torch.tensor([0, 5, (1 << 31) + 1, (1 << 32) - 1, 1 << 32, n - 1], device="cuda")
+    t[at] = 3.0
+    want = 3.0 * math.sqrt(len(at))
+    near_norm(rrv.clip_grads([t], 0.5 * want, eps=0.0), want)
+    near_scaled(t[at], torch.full((len(at),), 1.5, dtype=torch.float64, device="cuda"))
+    assert int(torch.count_nonzero(t)) == len(at)
+
+
+# ------------------------------------------------------ the clipped bucket sync
+
+SIZES = [100, 5000, 3, 777, 40001, 1, 16, 0, 9000]
+
+
+def rank_grads(n, sizes, dtype, std=0.1, off=lambda r, t: 0):
+    return [[Guarded(values(1000 * r + t, m, dtype, std), off(r, t)) for t, m in enumerate(sizes)] for r in range(n)]
+
+
+def tensors(ranks):
+    return [[g.t for g in rank] for rank in ranks]
+
+
+LAYOUTS = {"aligned": lambda r, t: 0, "same": lambda r, t: t % 8, "mixed": lambda r, t: (r + 2 * t) % 7}
+
+
+@pytest.mark.parametrize("n", [1, 2, 3, 4, 8, 16, 24])
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("op", ["avg", "sum"])
+def test_clipped_sync_without_a_limit_has_the_syncs_bits(n, dtype, op):
+    for layout, off in LAYOUTS.items():
+        a, b = rank_grads(n, SIZES, DT[dtype], off=off), rank_grads(n, SIZES, DT[dtype], off=off)
+        plan = rrv.BucketPlan(SIZES, dtype, 16384)
+        plan.all_reduce_range(0, plan.num_buckets, tensors(a), op)
+        plan.all_reduce_clip(tensors(b), math.inf, op)
+        for r in range(n):
+            for x, y in zip(a[r], b[r]):
+                assert torch.equal(x.t, y.t), (layout, r)
+                y.check()
+    rrv.check_timeouts()
+
+
+@pytest.mark.parametrize("n", [1, 2, 3, 8, 13])
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("op", ["avg", "sum"])
+def test_clipped_sync_against_64_bits(n, dtype, op):
+    for layout, off in LAYOUTS.items():
+        ranks = rank_grads(n, SIZES, DT[dtype], off=off)
+        rest = rank_grads(1, [2000, 33], torch.float32) + rank_grads(n - 1, [2000, 33], torch.float32, std=9.0)
+        div = n if op == "avg" and n > 1 else 1
+        avg = [sum(rank[t].t.double() for rank in ranks) / div for t in range(len(SIZES))]
+        mag = [sum(rank[t].t.double().abs() for rank in ranks) / div for t in range(len(SIZES))]
+        src = [g.t.clone() for g in rest[0]]
+        want = norm64(avg + src)
+        plan = rrv.BucketPlan(SIZES, dtype, 16384)
+        got = plan.all_reduce_clip(rrv.GradSet(tensors(ranks)), 0.6 * want, op, synced=tensors(rest), eps=0.0)
+        # the folds' errors are a share of the magnitudes; the norm's of them at most n * 2^-24 of their norm
+        assert abs(float(got) - want) <= 10 * E * want + n * E * norm64(mag)
+        for rank in ranks:
+            for g, a, m in zip(rank, avg, mag):
+                near_scaled(g.t, 0.6 * a, extra=n * E * (m + a.abs() * norm64(mag) / want))
+                g.check()
+        for rank in rest:
+            for g, a in zip(rank, src):
+                near_scaled(g.t, 0.6 * a.double(), extra=n * E * a.double().abs() * norm64(mag) / want)
+                g.check()
+    rrv.check_timeouts()
+
+
+def test_clipped_sync_of_a_range_and_of_many_tensors():
+    n, sizes = 8, [(i * 31) % 500 + 1 for i in range(700)]
+    ranks = rank_grads(n, sizes, torch.bfloat16)
+    before = [[g.t.clone() for g in rank] for rank in ranks]
+    plan = rrv.BucketPlan(sizes, "bf16", 20000)
+    first, count = 2, plan.num_buckets - 4
+    t0, t1 = plan.info(first)[0], plan.info(first + count)[0]
+    avg = [sum(rank[t].double() for rank in before) / n for t in range(t0, t1)]
+    want = norm64(avg)
+    got = plan.all_reduce_clip(tensors(ranks), 0.5 * want, first=first, count=count, eps=0.0)
+    assert abs(float(got) - want) <= 30 * E * want
+    for r in range(n):
+        for t in range(len(sizes)):
+            if t0 <= t < t1:
+                near_scaled(ranks[r][t].t, 0.5 * avg[t - t0], extra=40 * E * 0.5)
+            else:
+                assert torch.equal(ranks[r][t].t, before[r][t])
+            ranks[r][t].check()
+
+
+def test_clipped_sync_with_a_nan_and_with_a_large_sum():
+    sizes = [500, 60]
+    ranks = tensors(rank_grads(4, sizes, torch.float16))
+    ranks[2][1][7] = math.nan
+    plan = rrv.BucketPlan(sizes, "f16")
+    assert math.isnan(float(plan.all_reduce_clip(ranks, 1.0)))
+    assert all(bool(t.isnan().all()) for rank in ranks for t in rank)
+    big = [[torch.full((m,), 6e4, dtype=torch.float16, device="cuda") for m in sizes] for _ in range(4)]
+    got = plan.all_reduce_clip(big, 100.0, op="sum", eps=0.0)  # the sum leaves fp16's range, its clipped value does not
+    want = 4 * float(torch.tensor(6e4, dtype=torch.float16)) * math.sqrt(560)
+    near_norm(got, want)
+    for rank in big:
+        for t in rank:
+            near_scaled(t, torch.full_like(t, 100.0 / math.sqrt(560), dtype=torch.float64))
+
+
+# ------------------------------------------------- streams, graphs, arguments
+
+def test_calls_on_another_stream_and_with_out():
+    s = torch.cuda.Stream()
+    ts = [values(i, 100003, torch.float32) for i in range(3)]
+    want = norm64(ts)
+    torch.cuda.synchronize()
+    out = torch.zeros(1, device="cuda")
+    torch.cuda.synchronize()
+    assert rrv.grad_norm(ts, out=out, stream=s) is out
+    s.synchronize()
+    near_norm(out[0], want)
+    got = rrv.clip_grads(ts, 0.5 * want, eps=0.0, stream=s.cuda_stream)
+    s.synchronize()
+    near_norm(got, want)
+    assert abs(norm64(ts) - 0.5 * want) <= 30 * E * want
+    with pytest.raises(ValueError, match="out must be"):
+        rrv.grad_norm(ts, out=torch.zeros(2, device="cuda"))
+    with pytest.raises(ValueError, match="out must be"):
+        rrv.clip_grads(ts, 1.0, out=torch.zeros(1, dtype=torch.float64, device="cuda"))
+    with pytest.raises(TypeError):
+        rrv.GradList([torch.zeros(3, dtype=torch.int32, device="cuda")])
+    with pytest.raises(rrv.RRError):
+        rrv.clip_grads([ts[0], ts[0]], 1.0)  # the same tensor twice
+
+
+def test_captured_steps_replay_and_do_not_share_workspaces():
+    n, sizes = 4, [3000, 70001, 12]
+    plan = rrv.BucketPlan(sizes, "bf16", 1 << 20)
+    sets = [tensors(rank_grads(n, sizes, torch.bfloat16)) for _ in range(2)]
+    lists = [rrv.GradSet(s) for s in sets]
+    outs = [torch.zeros((), device="cuda") for _ in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    plan.all_reduce_clip(lists[0], math.inf)  # first use outside of a capture
+    torch.cuda.synchronize()
+    graphs = []
+    for ls, out, s in zip(lists, outs, streams):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            plan.all_reduce_clip(ls, 0.25, out=out, eps=0.0)
+        graphs.append(g)
+    for step in range(3):
+        want = []
+        for k, ranks in enumerate(sets):
+            new = rank_grads(n, sizes, torch.bfloat16, std=0.1 * (1 + step + 3 * k))
+            for rank, src in zip(ranks, new):
+                for t, g in zip(rank, src):
+                    t.copy_(g.t + step)
+            want.append([sum(rank[t].double() for rank in ranks) / n for t in range(len(sizes))])
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for ranks, avg, out in zip(sets, want, outs):
+            norm = norm64(avg)
+            assert abs(float(out) - norm) <= 30 * E * norm
+            for rank in ranks:
+                for t, a in zip(rank, avg):
+                    near_scaled(t, 0.25 / norm * a, extra=40 * E * 0.25 / norm * (step + 3.0))
