@@ -415,6 +415,47 @@ rr_status_t rr_bucket_allreduce_clip(const rr_bucket_plan_t* plan, int first_buc
                                      float eps, float* norm, void* workspace, size_t workspace_bytes,
                                      cudaStream_t stream);
 
+/* ------------------------------------------------------------- embedding -- */
+
+typedef enum rr_id_type { RR_ID_I32 = 0, RR_ID_I64 = 1 } rr_id_type_t;
+
+/* Embedding lookup with scaling, for every rank's tokens in one launch:
+ * outs[r][t, :] = round(scale * tables[r][ids[r][t], :]), one fp32 product and
+ * one rounding.  ids[r]: ntokens ids of id_type; tables[r]: vocab x dim rows of
+ * dtype (RR_F32, RR_BF16 or RR_F16), which ranks may share; outs[r]: ntokens x
+ * dim.  All row-major without gaps.  An id outside [0, vocab) -- a padded
+ * token -- gives a row of zeros.  At most 2^31-1 tokens in all, 2^31-2 rows,
+ * rows of at most 2^20 elements.  outs must overlap nothing.  Rows that are
+ * not whole 16-byte vectors on 16-byte boundaries are copied in the largest
+ * pieces (8, 4 or 2 bytes) that suit the width and every address. */
+rr_status_t rr_embedding(const void* const* ids, rr_id_type_t id_type, const void* const* tables, void* const* outs,
+                         int nranks, size_t ntokens, size_t vocab, size_t dim, rr_dtype_t dtype, float scale,
+                         cudaStream_t stream);
+
+/* The bytes of device workspace rr_embedding_grad needs (host only). */
+rr_status_t rr_embedding_grad_workspace(int nranks, size_t ntokens, size_t vocab, size_t dim, size_t* bytes);
+
+/* The gradient of the table of rr_embedding, summed over the tokens of all
+ * ranks -- the sync of the one gradient that is row-sparse:
+ *     dW[v, :] = f * sum over (r, t) with ids[r][t] == v of grad_out[r][t, :]
+ * with f = scale for SUM and scale / nranks for AVG, written to each of the
+ * ngrads tables grads[] (vocab x dim, grad_dtype: dtype or RR_F32) -- every
+ * rank's replica, or one (rr_bucket_allreduce_clip's synced list carries it to
+ * the others).  accumulate 0: grads = round(dW), zeros in rows that no token
+ * names; accumulate 1: grads = round(grads + dW), each table from its own
+ * values, other rows untouched.  Ids outside [0, vocab) and padding_idx (-1:
+ * none) add nothing.
+ * The rows are summed in fp32, sorted by token and, for one token, in rank and
+ * token order; sums of many rows are joined from sums of runs whose bounds
+ * depend on the ids alone, so the same call gives the same bits.
+ * workspace: 256-byte aligned, at least rr_embedding_grad_workspace's bytes,
+ * contents neither used nor kept, one call at a time (see rr_clip_workspace).
+ * ntokens 0 writes zeros (accumulate 0) or nothing. */
+rr_status_t rr_embedding_grad(const void* const* ids, rr_id_type_t id_type, const void* const* grad_out, int nranks,
+                              size_t ntokens, size_t vocab, size_t dim, rr_dtype_t dtype, rr_op_t op, float scale,
+                              int64_t padding_idx, void* const* grads, int ngrads, rr_dtype_t grad_dtype,
+                              int accumulate, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
 /* ------------------------------------------------ overlapped bucket sync -- */
 
 /* Opaque reducer (host memory and CUDA events owned by the library). */

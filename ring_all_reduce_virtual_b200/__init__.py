@@ -21,7 +21,8 @@ from ._lib import MAX_RANKS, Cost, RingEvent, RRError, Stats, TensorList, check,
 
 __all__ = [
     "all_reduce", "all_reduce_wire", "all_reduce_host", "all_reduce_host_noalloc", "ring_step", "ring_schedule", "reduce_scatter", "all_gather", "all_to_all",
-    "RankSet", "BucketPlan", "GradSet", "Reducer", "GradList", "grad_norm", "clip_grads", "cost_model", "pick_algo", "set_picker_params", "last_stats",
+    "RankSet", "BucketPlan", "GradSet", "Reducer", "GradList", "grad_norm", "clip_grads",
+    "embedding", "embedding_grad", "cost_model", "pick_algo", "set_picker_params", "last_stats",
     "check_timeouts", "RRError",
     "OPS", "ALGOS", "MAX_RANKS",
 ]
@@ -390,6 +391,77 @@ def clip_grads(grads, max_norm: float, eps: float = 1e-6, out=None, stream=None)
     gl = GradList._of(grads)
     return _norm_call("clip_grads", gl, out, stream,
                       lambda norm, ws, b, s: lib().rr_clip_grads(gl._ref, float(max_norm), float(eps), norm, ws, b, s))
+
+
+def _id_set(tokens, what: str):
+    """(pointer array, id type, ranks, tokens per rank, device) of the ranks'
+    token ids: a list of int32 or int64 tensors, or a RankSet (int32)."""
+    import torch
+
+    if isinstance(tokens, RankSet):
+        if tokens.dtype != _DTYPE_NAMES["i32"]:
+            raise TypeError(f"{what}: token ids must be int32 or int64")
+        return tokens.ptrs, 0, tokens.nranks, tokens.count, tokens.device
+    if len(tokens) < 1 or len(tokens) > MAX_RANKS:
+        raise ValueError(f"{what}: need 1..{MAX_RANKS} token tensors, got {len(tokens)}")
+    t0 = tokens[0]
+    if t0.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"{what}: token ids must be int32 or int64")
+    for t in tokens:
+        if not t.is_cuda or not t.is_contiguous() or t.dtype != t0.dtype or t.numel() != t0.numel() \
+                or t.device != t0.device:
+            raise ValueError(f"{what}: token tensors must be contiguous CUDA tensors alike")
+    return _ptr_array(tokens), int(t0.dtype == torch.int64), len(tokens), t0.numel(), t0.device
+
+
+def _row_set(tensors, what: str):
+    """(pointer array, ranks, rows, row width, dtype code, device) of 2-D (or
+    more) tensors whose last axis is a row: a list, or a RankSet."""
+    ptrs, n, count, d, dev = _rank_args(tensors, what)
+    shape = (tensors.tensors if isinstance(tensors, RankSet) else tensors)[0].shape
+    if len(shape) < 2 or shape[-1] == 0:
+        raise ValueError(f"{what}: need tensors of rows (two axes or more, rows not empty)")
+    return ptrs, n, count // shape[-1], shape[-1], d, dev
+
+
+def embedding(tokens, tables, outs, scale: float = 1.0, stream=None) -> None:
+    """``outs[r][t] = scale * tables[r][tokens[r][t]]`` for every rank in one
+    launch (``rr_embedding``).  Lists of one tensor per rank, or RankSets;
+    ids int32 or int64, rows float32, bfloat16 or float16.  An id outside the
+    table gives a row of zeros."""
+    ids, id_type, n, T, dev = _id_set(tokens, "embedding")
+    w, wn, V, D, d, wdev = _row_set(tables, "embedding")
+    o, on, rows, od, odt, odev = _row_set(outs, "embedding")
+    if wn != n or on != n or rows != T or od != D or odt != d or wdev != dev or odev != dev:
+        raise ValueError("embedding: need one table [V, D] and one output [tokens, D] per rank, alike and on the "
+                         "tokens' device")
+    with _on_device(dev):
+        check(lib().rr_embedding(ids, id_type, w, o, n, T, V, D, d, float(scale), _stream(stream, dev)), "embedding")
+
+
+def embedding_grad(tokens, grad_out, grads, op="avg", scale: float = 1.0, accumulate: bool = False,
+                   padding_idx: int | None = None, stream=None) -> None:
+    """The gradient of the embedding table over the tokens of all ranks
+    (``rr_embedding_grad``): ``grads[o][v] = f * sum of grad_out[r][t] over
+    tokens[r][t] == v`` with ``f = scale`` (``op="sum"``) or ``scale / ranks``
+    (``"avg"``), into every tensor of ``grads`` (each rank's replica, or one);
+    with ``accumulate`` added to what is there.  ``grads`` may be float32
+    beside 16-bit rows.  Ids outside the table and ``padding_idx`` add nothing."""
+    import torch
+
+    ids, id_type, n, T, dev = _id_set(tokens, "embedding_grad")
+    g, gn, rows, D, d, gdev = _row_set(grad_out, "embedding_grad")
+    w, wn, V, wd, wdt, wdev = _row_set(grads, "embedding_grad")
+    if gn != n or rows != T or wd != D or gdev != dev or wdev != dev:
+        raise ValueError("embedding_grad: need one output gradient [tokens, D] per rank and table gradients [V, D], on "
+                         "the tokens' device")
+    with _on_device(dev), _on_stream(stream, dev):
+        b = ctypes.c_size_t()
+        check(lib().rr_embedding_grad_workspace(n, T, V, D, ctypes.byref(b)), "embedding_grad_workspace")
+        ws = torch.empty(max(b.value, 256), dtype=torch.uint8, device=dev)
+        check(lib().rr_embedding_grad(ids, id_type, g, n, T, V, D, d, _op(op), float(scale),
+                                      -1 if padding_idx is None else int(padding_idx), w, wn, wdt, int(bool(accumulate)),
+                                      ws.data_ptr(), ws.numel(), _stream(stream, dev)), "embedding_grad")
 
 
 class BucketPlan:

@@ -85,6 +85,9 @@ def _declare(lib: ctypes.CDLL) -> None:
         "rr_grad_norm": (st, [TL, P, P, sz, P]),
         "rr_clip_grads": (st, [TL, f, f, P, P, sz, P]),
         "rr_bucket_allreduce_clip": (st, [P, i, i, PP, i, i, TL, f, f, P, P, sz, P]),
+        "rr_embedding": (st, [PP, i, PP, PP, i, sz, sz, sz, i, f, P]),
+        "rr_embedding_grad_workspace": (st, [i, sz, sz, sz, ctypes.POINTER(sz)]),
+        "rr_embedding_grad": (st, [PP, i, PP, i, sz, sz, sz, i, i, f, ctypes.c_int64, PP, i, i, i, P, sz, P]),
         "rr_reducer_create": (st, [P, PP, i, i, P, i, ctypes.POINTER(P)]),
         "rr_reducer_ready": (st, [P, i, P]),
         "rr_reducer_finish": (st, [P, P]),

@@ -158,6 +158,41 @@ constexpr int kScalePtrs = 2048;
 constexpr int kScalePtrsSmall = 256;
 using ScaleParams = ScaleParamsT<kScaleTensors, kScalePtrs>;
 
+// Embedding lookup and gradient (rr_embed.cu).  ids: int32 or int64 (ids64).
+struct EmbedLookupParams {
+    const void* ids[kMaxRanksH];
+    const void* table[kMaxRanksH];
+    void* out[kMaxRanksH];
+    uint32_t T;     // tokens per rank
+    uint32_t M;     // tokens of all ranks
+    uint64_t V;     // table rows
+    uint32_t D;     // row width
+    int ids64;
+    float scale;
+};
+
+struct EmbedGradParams {
+    const void* ids[kMaxRanksH];
+    const void* dout[kMaxRanksH];
+    void* grad[kMaxRanksH];  // nout of them
+    int64_t padding;         // this id adds nothing
+    uint64_t V;
+    uint32_t T, M, D;
+    int ids64;
+    int nout;
+    int accumulate;
+    float factor;            // scale, over the rank count for AVG
+    // workspace
+    uint32_t* key[2];        // sort buffers: token ids ...
+    uint32_t* pos[2];        // ... and positions (rank * T + token)
+    uint32_t* counts;        // per digit and tile
+    uint32_t* touched;       // one bit per table row
+    float* part;             // partial sums of runs that cross a block: [2][nblk][Dp]
+    int passes, bits;        // of the sort: digits, and bits per digit
+    uint32_t ntiles;
+    uint32_t K, nblk, Dp;    // sorted positions per block, blocks, padded row width
+};
+
 enum DType : int { kF32 = 0, kBF16 = 1, kI32 = 2, kF16 = 3 };
 enum Kind : int {
     kOneshotRing = 0,
@@ -235,6 +270,16 @@ constexpr int kMaxPartials = 2048;    // partials that a launch sums itself
 // The clipped sync's first pass: fold, park the sums, one partial per tile.
 uint64_t park_tile_elems(int grad_dtype, int n);
 cudaError_t launch_bucket_park(int grad_dtype, int op, const BucketFoldParams& p, double* partial, cudaStream_t s);
+
+// Embedding.  vec: elements per access, which divides the row width and
+// suits every address; out_dtype: the gradient's type, dtype or fp32.
+cudaError_t launch_embed_lookup(int dtype, int vec, const EmbedLookupParams& p, cudaStream_t s);
+cudaError_t launch_embed_sort(const EmbedGradParams& p, int* launches, cudaStream_t s);
+cudaError_t launch_embed_reduce(int dtype, int out_dtype, int vec, const EmbedGradParams& p, int* launches,
+                                cudaStream_t s);
+constexpr uint32_t kSortTile = 2048;   // keys per CTA of a sort pass
+constexpr int kSortMaxBits = 9;        // bits per digit, at most
+constexpr uint32_t kEmbedCols = 256;   // columns of a warp's slice of a row
 
 }  // namespace rr
 

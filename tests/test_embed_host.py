@@ -1,0 +1,84 @@
+"""Host-side checks of the embedding calls: every call here fails its argument
+checks before anything is enqueued, or computes on the host only."""
+import ctypes
+
+import pytest
+import torch
+
+import ring_all_reduce_virtual_b200 as rrv
+from ring_all_reduce_virtual_b200 import _lib
+from ring_all_reduce_virtual_b200.build import build
+
+INVALID, UNSUPPORTED = _lib.RR_ERR_INVALID_ARG, _lib.RR_ERR_UNSUPPORTED
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    build()
+
+
+def ptrs(n, base, gap=1 << 30):
+    return (ctypes.c_void_p * n)(*[base + i * gap for i in range(n)])
+
+
+IDS, TABLES, OUTS, WS = 1 << 40, 1 << 42, 1 << 44, 1 << 46
+
+
+def lookup(ids=ptrs(2, IDS), id_type=0, tables=ptrs(2, TABLES), outs=ptrs(2, OUTS), n=2, T=16, V=100, D=32, dtype=0):
+    return _lib.lib().rr_embedding(ids, id_type, tables, outs, n, T, V, D, dtype, 1.0, None)
+
+
+def grad(ids=ptrs(2, IDS), id_type=0, dout=ptrs(2, TABLES), n=2, T=16, V=100, D=32, dtype=1, op=1, grads=ptrs(2, OUTS),
+         nout=2, grad_dtype=1, accumulate=0, ws=WS, size=1 << 30):
+    return _lib.lib().rr_embedding_grad(ids, id_type, dout, n, T, V, D, dtype, op, 1.0, -1, grads, nout, grad_dtype,
+                                        accumulate, ws, size, None)
+
+
+@pytest.mark.parametrize("call", [lookup, grad])
+def test_shapes_types_and_pointers_are_checked(call):
+    for bad in (dict(n=0), dict(n=65), dict(dtype=9), dict(id_type=2), dict(D=0), dict(D=(1 << 20) + 1), dict(V=0),
+                dict(V=(1 << 31) - 1), dict(T=1 << 31), dict(T=1 << 30), dict(T=1 << 63), dict(ids=None),
+                dict(ids=ptrs(2, IDS + 2)), dict(ids=ptrs(2, IDS + 4), id_type=1), dict(ids=(ctypes.c_void_p * 2)(IDS, None))):
+        assert call(**bad) == INVALID, bad
+    assert call(dtype=2) == UNSUPPORTED
+    assert b"bf16, fp16 or fp32" in _lib.lib().rr_last_error()
+
+
+def test_lookup_refuses_bad_buffers():
+    for bad in (dict(tables=None), dict(outs=None), dict(tables=ptrs(2, TABLES + 2)), dict(outs=ptrs(2, OUTS + 1)),
+                dict(outs=ptrs(2, TABLES)), dict(outs=ptrs(2, OUTS, gap=64)), dict(outs=ptrs(2, IDS))):
+        assert lookup(**bad) == INVALID, bad
+    assert lookup(T=0) == 0  # no token: nothing is enqueued
+
+
+def test_grad_refuses_bad_arguments():
+    for bad in (dict(dout=None), dict(grads=None), dict(nout=0), dict(nout=65), dict(dout=ptrs(2, TABLES + 1)),
+                dict(grads=ptrs(2, OUTS + 2), grad_dtype=0), dict(grads=ptrs(2, OUTS, gap=0)), dict(grads=ptrs(2, TABLES)),
+                dict(ws=None), dict(ws=WS + 128), dict(size=1000), dict(ws=OUTS)):
+        assert grad(**bad) == INVALID, bad
+    for bad in (dict(op=2), dict(grad_dtype=3), dict(grad_dtype=2), dict(dtype=0, grad_dtype=1)):
+        assert grad(**bad) == UNSUPPORTED, bad
+    assert grad(T=0, accumulate=1) == 0
+
+
+def test_grad_workspace():
+    lib, b = _lib.lib(), ctypes.c_size_t()
+    assert lib.rr_embedding_grad_workspace(2, 10, 100, 32, None) == INVALID
+    assert lib.rr_embedding_grad_workspace(0, 10, 100, 32, ctypes.byref(b)) == INVALID
+    sizes = []
+    for n, T, V, D in ((1, 0, 1, 1), (1, 1, 1, 1), (2, 10, 100, 32), (8, 8192, 32000, 2048), (8, 65536, 32000, 2048)):
+        assert lib.rr_embedding_grad_workspace(n, T, V, D, ctypes.byref(b)) == 0
+        assert b.value % 256 == 0
+        sizes.append(b.value)
+    assert sizes == sorted(sizes) and sizes[-1] < 200 << 20  # the partial sums do not grow with the tokens
+
+
+def test_python_calls_check_their_tensors():
+    cpu = torch.zeros(2, 4)
+    ids = torch.zeros(2, dtype=torch.int64)
+    with pytest.raises(ValueError, match="alike"):
+        rrv.embedding([ids], [cpu], [cpu])  # not on a GPU
+    with pytest.raises(TypeError, match="int32 or int64"):
+        rrv.embedding([ids.float()], [cpu], [cpu])
+    with pytest.raises(ValueError, match="1..64"):
+        rrv.embedding_grad([], [cpu], [cpu])
