@@ -251,42 +251,212 @@ __global__ void __launch_bounds__(kThreads) embed_place_kernel(const __grid_cons
     }
 }
 
+// The whole sort in one launch, for as many tokens as fit in the shared
+// memory of one cluster: CS CTAs hold `per` consecutive (key, position) pairs
+// each and run every pass between cluster barriers, the pairs moving through
+// distributed shared memory; the last pass writes global memory.  The steps of
+// a pass are those of the kernels above: rank within the warp, stack the
+// warps' counts, then the counts of every digit in every CTA of the cluster
+// give each CTA's first place.
+constexpr int kClusterThreads = 1024;
+constexpr int kClusterWarps = kClusterThreads / 32;
+constexpr int kClusterRounds = (int)((kClusterKeys + kClusterThreads - 1) / kClusterThreads);
+constexpr int kDigits = 1 << kSortMaxBits;
+constexpr uint32_t kClusterSmem =
+    2u * kClusterKeys * 8u + (uint32_t)kClusterWarps * kDigits * 2u + 2u * kDigits * 4u + 32u * 4u;
+static_assert(kClusterSmem <= 232448, "within the shared memory of a CTA");
+static_assert(kDigits <= kClusterThreads, "one thread per digit");
+
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_barrier()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The address in CTA `rank`'s shared memory of the same variable as p here.
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank)
+{
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    return a;
+}
+
+__global__ void __launch_bounds__(kClusterThreads) embed_sort_kernel(const __grid_constant__ EmbedGradParams p)
+{
+    extern __shared__ __align__(16) unsigned char raw[];
+    uint2* buf = reinterpret_cast<uint2*>(raw);                             // [2][kClusterKeys] (key, position)
+    uint16_t* cnt = reinterpret_cast<uint16_t*>(buf + 2 * kClusterKeys);    // [warps][digits]
+    uint32_t* hist = reinterpret_cast<uint32_t*>(cnt + kClusterWarps * kDigits);  // this CTA's keys per digit
+    uint32_t* base = hist + kDigits;                                        // their first places
+    uint32_t* sums = base + kDigits;                                        // of the scan's warps
+    const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u;
+    const uint32_t cs = gridDim.x, me = cs > 1 ? cluster_rank() : 0;  // the grid is one cluster
+    const uint32_t per = (p.M + cs - 1) / cs;                          // <= kClusterKeys
+    const uint32_t i0 = me * per, mine = i0 < p.M ? (p.M - i0 < per ? p.M - i0 : per) : 0;
+    const uint32_t magic = (uint32_t)(((1ull << 32) + per - 1) / per);  // x / per for x < 2^32 / per
+    const uint32_t digits = 1u << p.bits;
+    const uint32_t run = (((mine + kClusterWarps - 1) / kClusterWarps) + 31u) & ~31u;  // keys of a warp, whole rounds
+    auto sync_all = [&] {
+        __syncwarp();  // the cluster barrier is taken by whole warps
+        if (cs > 1) cluster_barrier();
+        else __syncthreads();
+    };
+    pdl_begin();
+    if (!p.accumulate)
+        for (uint64_t w = (uint64_t)me * kClusterThreads + tid; w < (p.V + 31) / 32; w += (uint64_t)cs * kClusterThreads)
+            p.touched[w] = 0u;
+    uint32_t key[kClusterRounds], pos[kClusterRounds], rank[kClusterRounds];
+    for (int pass = 0; pass < p.passes; ++pass) {
+        const uint32_t shift = (uint32_t)(pass * p.bits);
+        const uint2* in = buf + (pass & 1) * kClusterKeys;
+        for (uint32_t i = tid; i < (uint32_t)kClusterWarps << p.bits; i += kClusterThreads)
+            cnt[(i >> p.bits) * kDigits + (i & (digits - 1))] = 0;
+        // the thread's keys, all loads of a pass in flight
+#pragma unroll
+        for (int j = 0; j < kClusterRounds; ++j) {
+            const uint32_t at = (uint32_t)j * 32u + lane, i = warp * run + at;
+            key[j] = 0xffffffffu;
+            if (at < run && i < mine) {
+                if (pass == 0) {
+                    key[j] = position_key(p, i0 + i);
+                    pos[j] = i0 + i;
+                } else {
+                    const uint2 v = in[i];
+                    key[j] = v.x;
+                    pos[j] = v.y;
+                }
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kClusterRounds; ++j) {
+            if ((uint32_t)j * 32u >= run) break;
+            const bool have = key[j] != 0xffffffffu;
+            const uint32_t d = have ? (key[j] >> shift) & (digits - 1) : digits;
+            const uint32_t same = __match_any_sync(0xffffffffu, d);
+            const uint32_t before = __popc(same & ((1u << lane) - 1u));
+            if (have) rank[j] = cnt[warp * kDigits + d] + before;
+            __syncwarp();
+            if (have && before == 0) cnt[warp * kDigits + d] = (uint16_t)(cnt[warp * kDigits + d] + __popc(same));
+            __syncwarp();
+        }
+        __syncthreads();
+        if (tid < digits) {
+            uint32_t at = 0;
+#pragma unroll
+            for (int w = 0; w < kClusterWarps; ++w) {
+                const uint32_t c = cnt[w * kDigits + tid];
+                cnt[w * kDigits + tid] = (uint16_t)at;
+                at += c;
+            }
+            hist[tid] = at;
+        }
+        sync_all();
+        // all keys of a smaller digit, then this digit's keys in earlier CTAs
+        uint32_t total = 0, earlier = 0;
+        if (tid < digits) {
+            if (cs > 1) {
+#pragma unroll
+                for (uint32_t c = 0; c < 8; ++c) {
+                    if (c >= cs) break;
+                    uint32_t h;
+                    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(h) : "r"(cluster_addr(&hist[tid], c)) : "memory");
+                    total += h;
+                    if (c < me) earlier += h;
+                }
+            } else {
+                total = hist[tid];
+            }
+        }
+        uint32_t x = total;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= (uint32_t)o) x += y;
+        }
+        if (lane == 31u) sums[warp] = x;
+        __syncthreads();
+        if (tid < digits) {
+            uint32_t first = x - total + earlier;
+            for (uint32_t w = 0; w < warp; ++w) first += sums[w];
+            base[tid] = first;
+        }
+        __syncthreads();
+        const bool last = pass + 1 == p.passes;
+        const uint32_t out = (uint32_t)((pass + 1) & 1) * kClusterKeys;
+#pragma unroll
+        for (int j = 0; j < kClusterRounds; ++j) {
+            if (key[j] == 0xffffffffu) continue;
+            if (pass == 0 && !p.accumulate && key[j] < p.V) atomicOr(&p.touched[key[j] >> 5], 1u << (key[j] & 31u));
+            const uint32_t d = (key[j] >> shift) & (digits - 1);
+            const uint32_t to = base[d] + cnt[warp * kDigits + d] + rank[j];
+            if (last) {
+                p.key[p.passes & 1][to] = key[j];
+                p.pos[p.passes & 1][to] = pos[j];
+            } else if (cs > 1) {
+                const uint32_t cta = __umulhi(to, magic), at = to - cta * per;
+                asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};"
+                             ::"r"(cluster_addr(&buf[out + at], cta)), "r"(key[j]), "r"(pos[j])
+                             : "memory");
+            } else {
+                buf[out + to] = make_uint2(key[j], pos[j]);
+            }
+        }
+        sync_all();  // the pairs are in place, and no CTA leaves while another reads its counts
+    }
+}
+
 // ------------------------------------------------------------------ reduce
 
 // A lane's columns of a slice: NC chunks of VEC, 32 * VEC apart.
 template <int VEC>
 constexpr int kChunks = (int)kEmbedCols / 32 / VEC;
 
-// The finished sum of row v (the lane's columns) into every replica.
+// The finished sum of row v (the lane's columns) into every replica; old: the
+// first replica's earlier values, where they have been fetched.
 template <class Out, int VEC>
 __device__ __forceinline__ void write_row(const EmbedGradParams& p, uint64_t v, uint32_t c0,
-                                          const float (&acc)[kChunks<VEC>][VEC])
+                                          const float (&acc)[kChunks<VEC>][VEC],
+                                          const Vec<Out, VEC>* old = nullptr)
 {
     using T = typename Out::T;
+    constexpr int NC = kChunks<VEC>;
     for (int o = 0; o < p.nout; ++o) {
         T* q = static_cast<T*>(p.grad[o]) + v * p.D;
+        Vec<Out, VEC> x[NC];
+        if (old && o == 0) {
 #pragma unroll
-        for (int k = 0; k < kChunks<VEC>; ++k) {
-            const uint32_t c = c0 + (uint32_t)k * 32u * VEC;
-            if (c >= p.D) continue;
-            Vec<Out, VEC> x;
+            for (int k = 0; k < NC; ++k) x[k] = old[k];
+        } else if (p.accumulate) {  // every load before the first store
+#pragma unroll
+            for (int k = 0; k < NC; ++k)
+                if (c0 + (uint32_t)k * 32u * VEC < p.D) x[k].load(q + c0 + (uint32_t)k * 32u * VEC);
+        }
+#pragma unroll
+        for (int k = 0; k < NC; ++k) {
             float a[VEC];
             if (p.accumulate) {
-                x.load(q + c);
-                x.to_f(a);
+                x[k].to_f(a);
 #pragma unroll
                 for (int l = 0; l < VEC; ++l) a[l] = __fadd_rn(a[l], __fmul_rn(acc[k][l], p.factor));
             } else {
 #pragma unroll
                 for (int l = 0; l < VEC; ++l) a[l] = __fmul_rn(acc[k][l], p.factor);
             }
-            x.from_f(a);
-            x.store(q + c);
+            x[k].from_f(a);
+            if (c0 + (uint32_t)k * 32u * VEC < p.D) x[k].store(q + c0 + (uint32_t)k * 32u * VEC);
         }
     }
 }
 
-// A run that crosses blocks: its partial sum, in fp32.
+// A run that crosses blocks: its partial sum, in fp32 (rows of Dp floats, on
+// 16-byte boundaries).
 template <int VEC>
 __device__ __forceinline__ void write_part(float* q, uint32_t c0, uint32_t D,
                                            const float (&acc)[kChunks<VEC>][VEC])
@@ -295,8 +465,9 @@ __device__ __forceinline__ void write_part(float* q, uint32_t c0, uint32_t D,
     for (int k = 0; k < kChunks<VEC>; ++k) {
         const uint32_t c = c0 + (uint32_t)k * 32u * VEC;
         if (c >= D) continue;
-#pragma unroll
-        for (int l = 0; l < VEC; ++l) q[c + l] = acc[k][l];
+        Vec<F32T, VEC> x;
+        x.from_f(acc[k]);
+        x.store(q + c);
     }
 }
 
@@ -304,72 +475,225 @@ __device__ __forceinline__ void write_part(float* q, uint32_t c0, uint32_t D,
 __device__ __forceinline__ const uint32_t* sorted_keys(const EmbedGradParams& p) { return p.key[p.passes & 1]; }
 __device__ __forceinline__ const uint32_t* sorted_pos(const EmbedGradParams& p) { return p.pos[p.passes & 1]; }
 
+// The block of K sorted positions that a warp sums, 32 of them at a time: a
+// lane holds one position's id and row address, and three masks say after
+// which of the 32 a run ends, and where its sum goes.
+template <class T>
+struct Chunk {
+    uint32_t n;       // positions with a row: the first n (ids are sorted)
+    uint32_t ends;    // a run's last position (in this chunk, or the block's last)
+    uint32_t first;   // ... whose run began in an earlier block: a partial sum
+    uint32_t on;      // ... whose run goes on in the next block: a partial sum
+    uint32_t key;
+    const T* row;
+};
+
+template <class T>
+__device__ __forceinline__ Chunk<T> load_chunk(const EmbedGradParams& p, uint32_t i0, uint32_t b1, uint32_t before,
+                                               uint32_t after)
+{
+    const uint32_t lane = threadIdx.x & 31u, i = i0 + lane, V = (uint32_t)p.V;
+    Chunk<T> c;
+    c.key = V;
+    c.row = nullptr;
+    uint32_t next = after;
+    if (i < b1) {
+        c.key = sorted_keys(p)[i];
+        const uint32_t at = sorted_pos(p)[i], r = at / p.T;
+        c.row = static_cast<const T*>(p.dout[r]) + (uint64_t)(at - r * p.T) * p.D;
+        if (i + 1 < b1) next = sorted_keys(p)[i + 1];
+    }
+    const bool valid = c.key < V, on = i + 1 == b1 && next == c.key;
+    c.n = __popc(__ballot_sync(0xffffffffu, valid));
+    c.ends = __ballot_sync(0xffffffffu, valid && (next != c.key || on));
+    c.first = __ballot_sync(0xffffffffu, valid && c.key == before);
+    c.on = __ballot_sync(0xffffffffu, valid && on);
+    return c;
+}
+
+// Sum of a run to where it belongs.  old: the row's earlier values (one
+// replica's, fetched ahead) or NULL.
+template <class Out, int VEC, class T>
+__device__ __forceinline__ void close_run(const EmbedGradParams& p, const Chunk<T>& ch, uint32_t j, uint32_t blk,
+                                          uint32_t c0, const float (&acc)[kChunks<VEC>][VEC],
+                                          const Vec<Out, VEC>* old)
+{
+    const uint32_t key = __shfl_sync(0xffffffffu, ch.key, j);
+    if ((ch.first >> j) & 1u) write_part<VEC>(p.part + (uint64_t)blk * p.Dp, c0, p.D, acc);
+    else if ((ch.on >> j) & 1u) write_part<VEC>(p.part + ((uint64_t)p.nblk + blk) * p.Dp, c0, p.D, acc);
+    else write_row<Out, VEC>(p, key, c0, acc, old);
+}
+
 // A warp sums one slice of the columns over one block of K sorted positions:
 // runs that lie inside it go to the table, the first and the last run's sums
 // to the block's partials where they go on outside.
-template <class In, class Out, int VEC>
+//
+// The rows stream through a ring of kRing slots of shared memory per warp by
+// cp.async, one row's slice per slot, and where the call adds to what is there
+// the earlier values of a row follow the last position of its run through the
+// same ring, so the sums never wait for a load that was not issued kRing rows
+// ago.  A lane reads only what it copied itself: no barrier.  Measured on 8 x
+// 8192 tokens of 2048 bf16 into fp32: see the launch.
+#ifndef RR_EMBED_RING
+#define RR_EMBED_RING 8
+#endif
+constexpr int kRing = RR_EMBED_RING;
+
+template <int B>
+__device__ __forceinline__ void copy_async(uint32_t to, const void* from)
+{
+    if constexpr (B == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(B) : "memory");
+}
+
+template <class In, class Out, int VEC, bool ACC>
+constexpr uint32_t kRingSlot =  // bytes of a warp's slot
+    kEmbedCols * (ACC && sizeof(typename Out::T) > sizeof(typename In::T) ? sizeof(typename Out::T) : sizeof(typename In::T));
+
+template <class In, class Out, int VEC, bool ACC>
 __global__ void __launch_bounds__(kThreads) embed_reduce_kernel(const __grid_constant__ EmbedGradParams p)
 {
     using T = typename In::T;
+    using TO = typename Out::T;
     constexpr int NC = kChunks<VEC>;
-    constexpr int G = sizeof(T) * VEC * NC == 16 ? 8 : 4;  // rows whose loads are in flight
+    constexpr uint32_t kSlot = kRingSlot<In, Out, VEC, ACC>;
+    constexpr int BI = VEC * (int)sizeof(T), BO = VEC * (int)sizeof(TO);
+    extern __shared__ __align__(16) unsigned char ring_mem[];
     pdl_begin();
-    const uint32_t* keys = sorted_keys(p);
-    const uint32_t* poss = sorted_pos(p);
-    const uint32_t lane = threadIdx.x & 31u;
-    const uint32_t blk = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
+    const uint32_t blk = blockIdx.x * kWarps + warp;
     if (blk >= p.nblk) return;
+    unsigned char* ring = ring_mem + warp * (kRing * kSlot);
+    const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
     const uint32_t b0 = blk * p.K, b1 = b0 + p.K < p.M ? b0 + p.K : p.M;
     const uint32_t c0 = blockIdx.y * kEmbedCols + lane * VEC;
     const uint32_t V = (uint32_t)p.V;
-    const uint32_t before = b0 > 0 ? keys[b0 - 1] : V, after = b1 < p.M ? keys[b1] : V;
+    const uint32_t before = b0 > 0 ? sorted_keys(p)[b0 - 1] : V, after = b1 < p.M ? sorted_keys(p)[b1] : V;
     float acc[NC][VEC];
-    uint32_t cur = V;      // the run being summed (V: none)
-    bool from = false;     // it began in an earlier block
     auto clear = [&] {
 #pragma unroll
         for (int k = 0; k < NC; ++k)
 #pragma unroll
             for (int l = 0; l < VEC; ++l) acc[k][l] = 0.0f;
     };
-    auto close = [&](bool goes_on) {
-        if (cur >= V) return;
-        if (from) write_part<VEC>(p.part + (uint64_t)blk * p.Dp, c0, p.D, acc);
-        else if (goes_on) write_part<VEC>(p.part + ((uint64_t)p.nblk + blk) * p.Dp, c0, p.D, acc);
-        else write_row<Out, VEC>(p, cur, c0, acc);
-    };
     clear();
     for (uint32_t i0 = b0; i0 < b1; i0 += 32) {
-        const uint32_t mine = i0 + lane;
-        uint32_t key = V;
-        const T* row = nullptr;
-        if (mine < b1) {
-            key = keys[mine];
-            const uint32_t at = poss[mine], r = at / p.T;
-            row = static_cast<const T*>(p.dout[r]) + (uint64_t)(at - r * p.T) * p.D;
-        }
-        const uint32_t n = __popc(__ballot_sync(0xffffffffu, key < V));  // sorted: the valid ones come first
-        for (uint32_t j0 = 0; j0 < n; j0 += G) {
-            Vec<In, VEC> x[G][NC];
-#pragma unroll
-            for (int g = 0; g < G; ++g) {
-                const T* q = reinterpret_cast<const T*>(__shfl_sync(0xffffffffu, (unsigned long long)row, j0 + g));
+        const Chunk<T> ch = load_chunk<T>(p, i0, b1, before, after);
+        const uint32_t fetch = ACC ? ch.ends & ~ch.first & ~ch.on : 0u;  // rows whose earlier values are needed
+        uint32_t made = 0;      // the next position to copy
+        bool old_next = false;  // the earlier values of the one before it come first
+        uint32_t in_slot = 0, out_slot = 0;
+        auto issue = [&] {  // one item into the ring (an empty group where nothing is left)
+            const uint32_t to = ring_at + in_slot * kSlot;
+            if (ACC && old_next) {
+                const TO* q = static_cast<const TO*>(p.grad[0]) + (uint64_t)__shfl_sync(0xffffffffu, ch.key, made - 1) * p.D;
 #pragma unroll
                 for (int k = 0; k < NC; ++k) {
                     const uint32_t c = c0 + (uint32_t)k * 32u * VEC;
-                    if (j0 + g < n && c < p.D) x[g][k].load(q + c);
+                    if (c < p.D) {
+                        constexpr int B = BO > 16 ? 16 : BO;
+#pragma unroll
+                        for (int h = 0; h < BO; h += B)
+                            copy_async<B < 4 ? 4 : B>(to + (uint32_t)(k * 32 + lane) * BO + h,
+                                                      reinterpret_cast<const char*>(q + c) + h);
+                    }
+                }
+                old_next = false;
+            } else if (made < ch.n) {
+                const T* q = reinterpret_cast<const T*>(__shfl_sync(0xffffffffu, (unsigned long long)ch.row, made));
+#pragma unroll
+                for (int k = 0; k < NC; ++k) {
+                    const uint32_t c = c0 + (uint32_t)k * 32u * VEC;
+                    if (c < p.D) copy_async<BI < 4 ? 4 : BI>(to + (uint32_t)(k * 32 + lane) * BI, q + c);
+                }
+                if (ACC) old_next = (fetch >> made) & 1u;
+                ++made;
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            in_slot = in_slot + 1 < kRing ? in_slot + 1 : 0;
+        };
+        auto next_slot = [&]() -> const unsigned char* {  // the oldest item, landed
+            asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+            const unsigned char* q = ring + out_slot * kSlot;
+            out_slot = out_slot + 1 < kRing ? out_slot + 1 : 0;
+            return q;
+        };
+#pragma unroll 1
+        for (int k = 0; k < kRing; ++k) issue();
+#pragma unroll 1
+        for (uint32_t j = 0; j < ch.n; ++j) {
+            const T* x = reinterpret_cast<const T*>(next_slot());
+#pragma unroll
+            for (int k = 0; k < NC; ++k) {
+                if (c0 + (uint32_t)k * 32u * VEC >= p.D) continue;
+                Vec<In, VEC> v;
+                float a[VEC];
+                v.load(x + (k * 32 + lane) * VEC);
+                v.to_f(a);
+#pragma unroll
+                for (int l = 0; l < VEC; ++l) acc[k][l] = __fadd_rn(acc[k][l], a[l]);
+            }
+            issue();
+            if (!((ch.ends >> j) & 1u)) continue;
+            if (ACC && ((fetch >> j) & 1u)) {
+                const TO* y = reinterpret_cast<const TO*>(next_slot());
+                Vec<Out, VEC> old[NC];
+#pragma unroll
+                for (int k = 0; k < NC; ++k)
+                    if (c0 + (uint32_t)k * 32u * VEC < p.D) old[k].load(y + (k * 32 + lane) * VEC);
+                issue();
+                close_run<Out, VEC>(p, ch, j, blk, c0, acc, old);
+            } else {
+                close_run<Out, VEC>(p, ch, j, blk, c0, acc, static_cast<const Vec<Out, VEC>*>(nullptr));
+            }
+            clear();
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");  // the ring is free for the next chunk
+        if (ch.n < 32) break;
+    }
+}
+
+// The same for rows in 2-byte pieces, which cp.async cannot copy: the loads of
+// a few rows in flight in registers.
+template <class In, class Out, int VEC>
+__global__ void __launch_bounds__(kThreads) embed_reduce_narrow_kernel(const __grid_constant__ EmbedGradParams p)
+{
+    using T = typename In::T;
+    constexpr int NC = kChunks<VEC>;
+    constexpr int G = 4;  // rows whose loads are in flight
+    pdl_begin();
+    const uint32_t lane = threadIdx.x & 31u;
+    const uint32_t blk = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    if (blk >= p.nblk) return;
+    const uint32_t b0 = blk * p.K, b1 = b0 + p.K < p.M ? b0 + p.K : p.M;
+    const uint32_t c0 = blockIdx.y * kEmbedCols + lane * VEC;
+    const uint32_t V = (uint32_t)p.V;
+    const uint32_t before = b0 > 0 ? sorted_keys(p)[b0 - 1] : V, after = b1 < p.M ? sorted_keys(p)[b1] : V;
+    float acc[NC][VEC];
+    auto clear = [&] {
+#pragma unroll
+        for (int k = 0; k < NC; ++k)
+#pragma unroll
+            for (int l = 0; l < VEC; ++l) acc[k][l] = 0.0f;
+    };
+    clear();
+    for (uint32_t i0 = b0; i0 < b1; i0 += 32) {
+        const Chunk<T> ch = load_chunk<T>(p, i0, b1, before, after);
+        for (uint32_t j0 = 0; j0 < ch.n; j0 += G) {
+            Vec<In, VEC> x[G][NC];
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const T* q = reinterpret_cast<const T*>(__shfl_sync(0xffffffffu, (unsigned long long)ch.row, j0 + g));
+#pragma unroll
+                for (int k = 0; k < NC; ++k) {
+                    const uint32_t c = c0 + (uint32_t)k * 32u * VEC;
+                    if (j0 + g < ch.n && c < p.D) x[g][k].load(q + c);
                 }
             }
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-                const uint32_t next = __shfl_sync(0xffffffffu, key, j0 + g);
-                if (j0 + g >= n) continue;
-                if (next != cur) {
-                    close(false);
-                    clear();
-                    from = cur >= V && next == before;  // only a block's first run can have begun earlier
-                    cur = next;
-                }
+                const uint32_t j = j0 + g;
+                if (j >= ch.n) break;
 #pragma unroll
                 for (int k = 0; k < NC; ++k) {
                     if (c0 + (uint32_t)k * 32u * VEC >= p.D) continue;
@@ -378,61 +702,58 @@ __global__ void __launch_bounds__(kThreads) embed_reduce_kernel(const __grid_con
 #pragma unroll
                     for (int l = 0; l < VEC; ++l) acc[k][l] = __fadd_rn(acc[k][l], a[l]);
                 }
+                if (!((ch.ends >> j) & 1u)) continue;
+                close_run<Out, VEC>(p, ch, j, blk, c0, acc, static_cast<const Vec<Out, VEC>*>(nullptr));
+                clear();
             }
         }
-        if (n < 32) break;
+        if (ch.n < 32) break;
     }
-    close(cur == after);
 }
 
-// Joins the runs that cross blocks: the block in which such a run begins adds
-// its partial sums in block order and writes the row.
-template <class Out, int VEC>
-__global__ void __launch_bounds__(kThreads) embed_join_kernel(const __grid_constant__ EmbedGradParams p)
+// Adds the partial sums of entries [a, b) of a run to acc, in order: entry 0
+// is the last partial of block blk, entry i the first partial of block blk + i.
+template <int VEC>
+__device__ __forceinline__ void add_parts(const EmbedGradParams& p, uint32_t blk, uint32_t a, uint32_t b, uint32_t c0,
+                                          float (&acc)[kChunks<VEC>][VEC])
 {
-    constexpr int NC = kChunks<VEC>;
-    pdl_begin();
-    const uint32_t* keys = sorted_keys(p);
-    const uint32_t lane = threadIdx.x & 31u;
-    const uint32_t blk = blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (blk + 1 >= p.nblk) return;
-    const uint32_t end = (blk + 1) * p.K;  // < M
-    const uint32_t key = keys[end - 1];
-    if (key >= (uint32_t)p.V || keys[end] != key) return;
-    if (blk > 0 && keys[blk * p.K - 1] == key) return;  // begun earlier (then the whole block is the run's)
-    uint32_t lo = blk + 1, hi = p.nblk - 1;             // the last block whose first key is this one
-    while (lo < hi) {
-        const uint32_t mid = (lo + hi + 1) / 2;
-        if (keys[mid * p.K] == key) lo = mid;
-        else hi = mid - 1;
-    }
-    const uint32_t c0 = blockIdx.y * kEmbedCols + lane * VEC;
-    float acc[NC][VEC];
+    constexpr int NC = kChunks<VEC>, U = 4;  // entries whose loads are in flight
+    for (uint32_t i0 = a; i0 < b; i0 += U) {
+        Vec<F32T, VEC> x[U][NC];
 #pragma unroll
-    for (int k = 0; k < NC; ++k)
+        for (int u = 0; u < U; ++u) {
+            const uint32_t i = i0 + u;
+            const float* q = p.part + (i == 0 ? (uint64_t)p.nblk + blk : (uint64_t)blk + i) * p.Dp;
 #pragma unroll
-        for (int l = 0; l < VEC; ++l) {
-            const uint32_t c = c0 + (uint32_t)k * 32u * VEC + l;
-            if (c >= p.D) continue;
-            float s = p.part[((uint64_t)p.nblk + blk) * p.Dp + c];
-            for (uint32_t b = blk + 1; b <= lo; ++b) s = __fadd_rn(s, p.part[(uint64_t)b * p.Dp + c]);
-            acc[k][l] = s;
+            for (int k = 0; k < NC; ++k) {
+                const uint32_t c = c0 + (uint32_t)k * 32u * VEC;
+                if (i < b && c < p.D) x[u][k].load(q + c);
+            }
         }
-    write_row<Out, VEC>(p, key, c0, acc);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (i0 + u >= b) break;
+#pragma unroll
+            for (int k = 0; k < NC; ++k) {
+                if (c0 + (uint32_t)k * 32u * VEC >= p.D) continue;
+#pragma unroll
+                for (int l = 0; l < VEC; ++l) acc[k][l] = __fadd_rn(acc[k][l], __uint_as_float(x[u][k].r[l]));
+            }
+        }
+    }
 }
 
 // Zeros into the rows that no token touched: a CTA takes 32 rows of one
 // replica, run by run of untouched ones.
 template <class Out>
-__global__ void __launch_bounds__(kThreads) embed_zero_kernel(const __grid_constant__ EmbedGradParams p)
+__device__ __forceinline__ void zero_rows(const EmbedGradParams& p, uint32_t chunk, uint32_t replica)
 {
     using T = typename Out::T;
     constexpr int L = Out::L;
-    pdl_begin();
-    const uint64_t v0 = (uint64_t)blockIdx.x * 32u;
+    const uint64_t v0 = (uint64_t)chunk * 32u;
     const uint32_t rows = (uint32_t)(p.V - v0 < 32 ? p.V - v0 : 32);
-    const uint32_t word = p.touched[blockIdx.x];
-    T* base = static_cast<T*>(p.grad[blockIdx.y]) + v0 * p.D;
+    const uint32_t word = p.touched[chunk];
+    T* base = static_cast<T*>(p.grad[replica]) + v0 * p.D;
     for (uint32_t i = 0; i < rows;) {
         if ((word >> i) & 1u) {
             ++i;
@@ -452,8 +773,88 @@ __global__ void __launch_bounds__(kThreads) embed_zero_kernel(const __grid_const
     }
 }
 
+// Joins the runs that cross blocks -- the block in which such a run begins
+// adds its partial sums in block order and writes the row -- and, in the CTAs
+// behind those (chunks of rows x replicas), clears the untouched rows: the
+// joins wait for memory while the clearing fills it.  A warp joins one run for
+// one slice; a run over many blocks (a frequent token) is shared by the CTA's
+// warps, each an eighth of the entries, and the eighths added in order.
+constexpr uint32_t kLongRun = 32;  // entries from which a run is shared
+
+template <class Out, int VEC>
+__global__ void __launch_bounds__(kThreads) embed_join_kernel(const __grid_constant__ EmbedGradParams p, uint32_t joins,
+                                                              uint32_t slices, uint32_t chunks)
+{
+    constexpr int NC = kChunks<VEC>;
+    __shared__ uint32_t long_run[kWarps];
+    __shared__ __align__(16) float eighth[kWarps][kEmbedCols];
+    pdl_begin();
+    if (blockIdx.x >= joins) {
+        const uint32_t z = blockIdx.x - joins;
+        zero_rows<Out>(p, z % chunks, z / chunks);
+        return;
+    }
+    const uint32_t* keys = sorted_keys(p);
+    const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
+    const uint32_t slice = blockIdx.x % slices, blk0 = blockIdx.x / slices * kWarps;
+    const uint32_t c0 = slice * kEmbedCols + lane * VEC;
+    // the entries of the run that begins in block blk and goes on behind it; 0: none
+    auto entries = [&](uint32_t blk) -> uint32_t {
+        if (blk + 1 >= p.nblk) return 0;
+        const uint32_t end = (blk + 1) * p.K;  // < M
+        const uint32_t key = keys[end - 1];
+        if (key >= (uint32_t)p.V || keys[end] != key) return 0;
+        if (blk > 0 && keys[blk * p.K - 1] == key) return 0;  // begun earlier (then the whole block is the run's)
+        uint32_t lo = blk + 1, hi = p.nblk - 1;               // the last block whose first key is this one
+        if (lo < hi && keys[(lo + 1) * p.K] != key) hi = lo;  // most runs end in the next block
+        while (lo < hi) {
+            const uint32_t mid = (lo + hi + 1) / 2;
+            if (keys[mid * p.K] == key) lo = mid;
+            else hi = mid - 1;
+        }
+        return lo - blk + 1;
+    };
+    float acc[NC][VEC];
+    auto clear = [&] {
+#pragma unroll
+        for (int k = 0; k < NC; ++k)
+#pragma unroll
+            for (int l = 0; l < VEC; ++l) acc[k][l] = 0.0f;
+    };
+    const uint32_t mine = entries(blk0 + warp);
+    if (mine > 0 && mine <= kLongRun) {
+        clear();
+        add_parts<VEC>(p, blk0 + warp, 0, mine, c0, acc);
+        write_row<Out, VEC>(p, keys[(blk0 + warp + 1) * p.K], c0, acc);
+    }
+    if (lane == 0) long_run[warp] = mine > kLongRun ? mine : 0;
+    __syncthreads();
+    for (uint32_t w = 0; w < kWarps; ++w) {
+        const uint32_t n = long_run[w];
+        if (n == 0) continue;
+        clear();
+        add_parts<VEC>(p, blk0 + w, (uint32_t)((uint64_t)n * warp / kWarps), (uint32_t)((uint64_t)n * (warp + 1) / kWarps),
+                       c0, acc);
+#pragma unroll
+        for (int k = 0; k < NC; ++k)
+#pragma unroll
+            for (int l = 0; l < VEC; ++l) eighth[warp][(k * 32 + lane) * VEC + l] = acc[k][l];
+        __syncthreads();
+        if (warp == 0) {
+            for (int e = 1; e < kWarps; ++e)
+#pragma unroll
+                for (int k = 0; k < NC; ++k)
+#pragma unroll
+                    for (int l = 0; l < VEC; ++l)
+                        acc[k][l] = __fadd_rn(acc[k][l], eighth[e][(k * 32 + lane) * VEC + l]);
+            write_row<Out, VEC>(p, keys[(blk0 + w + 1) * p.K], c0, acc);
+        }
+        __syncthreads();
+    }
+}
+
 template <class... A>
-cudaError_t launch_pdl(void (*kernel)(A...), dim3 grid, unsigned threads, cudaStream_t s, const A&... a)
+cudaError_t launch_pdl(void (*kernel)(A...), dim3 grid, unsigned threads, uint32_t smem, cudaStream_t s, const A&... a)
 {
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -461,6 +862,7 @@ cudaError_t launch_pdl(void (*kernel)(A...), dim3 grid, unsigned threads, cudaSt
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
@@ -468,21 +870,40 @@ cudaError_t launch_pdl(void (*kernel)(A...), dim3 grid, unsigned threads, cudaSt
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+// A ring kernel: more shared memory than a launch gets by default.
+cudaError_t launch_ring(void (*kernel)(EmbedGradParams), dim3 grid, uint32_t smem, cudaStream_t s,
+                        const EmbedGradParams& p)
+{
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    return e != cudaSuccess ? e : launch_pdl(kernel, grid, kThreads, smem, s, p);
+}
+
 unsigned blocks_for(uint64_t items, uint64_t per) { return (unsigned)((items + per - 1) / per); }
 
 template <class In, class Out, int VEC>
 cudaError_t reduce_typed(const EmbedGradParams& p, int* launches, cudaStream_t s)
 {
-    const dim3 grid(blocks_for(p.nblk, kWarps), blocks_for(p.D, kEmbedCols));
-    cudaError_t e = launch_pdl(embed_reduce_kernel<In, Out, VEC>, grid, kThreads, s, p);
+    const uint32_t slices = blocks_for(p.D, kEmbedCols);
+    const dim3 grid(blocks_for(p.nblk, kWarps), slices);
+    cudaError_t e;
+    if constexpr (VEC * sizeof(typename In::T) < 4) {
+        e = launch_pdl(embed_reduce_narrow_kernel<In, Out, VEC>, grid, kThreads, 0, s, p);
+    } else if (p.accumulate) {
+        e = launch_ring(embed_reduce_kernel<In, Out, VEC, true>, grid, kWarps * kRing * kRingSlot<In, Out, VEC, true>, s, p);
+    } else {
+        e = launch_ring(embed_reduce_kernel<In, Out, VEC, false>, grid, kWarps * kRing * kRingSlot<In, Out, VEC, false>, s, p);
+    }
     if (e != cudaSuccess) return e;
     *launches += 1;
-    if (p.nblk > 1) {
-        e = launch_pdl(embed_join_kernel<Out, VEC>, grid, kThreads, s, p);
-        if (e != cudaSuccess) return e;
-        *launches += 1;
-    }
-    return cudaSuccess;
+    const uint64_t joins = p.nblk > 1 ? (uint64_t)blocks_for(p.nblk, kWarps) * slices : 0;
+    const uint64_t chunks = p.accumulate ? 0 : (p.V + 31) / 32;
+    const uint64_t work = joins + chunks * (uint64_t)p.nout;
+    if (work == 0) return cudaSuccess;
+    if (work > kMaxGrid) return cudaErrorInvalidValue;
+    e = launch_pdl(embed_join_kernel<Out, VEC>, dim3((unsigned)work), kThreads, 0, s, p, (uint32_t)joins, slices,
+                   (uint32_t)chunks);
+    *launches += e == cudaSuccess;
+    return e;
 }
 
 template <class In, class Out>
@@ -499,26 +920,17 @@ cudaError_t reduce_out(int vec, const EmbedGradParams& p, int* launches, cudaStr
     return cudaErrorInvalidValue;
 }
 
-template <class Out>
-cudaError_t zero_typed(const EmbedGradParams& p, int* launches, cudaStream_t s)
-{
-    const cudaError_t e =
-        launch_pdl(embed_zero_kernel<Out>, dim3(blocks_for(p.V, 32), (unsigned)p.nout), kThreads, s, p);
-    *launches += e == cudaSuccess;
-    return e;
-}
-
 template <class Ty>
 cudaError_t lookup_typed(int vec, const EmbedLookupParams& p, cudaStream_t s)
 {
     const dim3 grid(blocks_for(p.M, kWarps), blocks_for(p.D, (uint64_t)32 * kLookupU * vec));
     switch (vec) {
     case 8:
-        if constexpr (sizeof(typename Ty::T) == 2) return launch_pdl(embed_lookup_kernel<Ty, 8>, grid, kThreads, s, p);
+        if constexpr (sizeof(typename Ty::T) == 2) return launch_pdl(embed_lookup_kernel<Ty, 8>, grid, kThreads, 0, s, p);
         else return cudaErrorInvalidValue;
-    case 4: return launch_pdl(embed_lookup_kernel<Ty, 4>, grid, kThreads, s, p);
-    case 2: return launch_pdl(embed_lookup_kernel<Ty, 2>, grid, kThreads, s, p);
-    case 1: return launch_pdl(embed_lookup_kernel<Ty, 1>, grid, kThreads, s, p);
+    case 4: return launch_pdl(embed_lookup_kernel<Ty, 4>, grid, kThreads, 0, s, p);
+    case 2: return launch_pdl(embed_lookup_kernel<Ty, 2>, grid, kThreads, 0, s, p);
+    case 1: return launch_pdl(embed_lookup_kernel<Ty, 1>, grid, kThreads, 0, s, p);
     }
     return cudaErrorInvalidValue;
 }
@@ -537,10 +949,36 @@ cudaError_t launch_embed_lookup(int dtype, int vec, const EmbedLookupParams& p, 
 
 cudaError_t launch_embed_sort(const EmbedGradParams& p, int* launches, cudaStream_t s)
 {
+    if (p.M <= kClusterMax) {
+        // CTAs of the cluster: enough that each holds at most kClusterShare keys
+        unsigned cs = 1;
+        while (cs < 8 && p.M > cs * kClusterShare) cs *= 2;
+        const cudaError_t set =
+            cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kClusterSmem);
+        if (set != cudaSuccess) return set;
+        cudaLaunchAttribute attr[2]{};
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = cs;
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(cs);
+        cfg.blockDim = dim3(kClusterThreads);
+        cfg.dynamicSmemBytes = kClusterSmem;
+        cfg.stream = s;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, embed_sort_kernel, p);
+        if (e != cudaSuccess) return e;
+        *launches += 1;
+        return cudaGetLastError();
+    }
     for (int pass = 0; pass < p.passes; ++pass) {
-        cudaError_t e = launch_pdl(embed_count_kernel, dim3(p.ntiles), kThreads, s, p, pass);
-        if (e == cudaSuccess) e = launch_pdl(embed_scan_kernel, dim3(1), 1024, s, p.counts, p.ntiles << p.bits);
-        if (e == cudaSuccess) e = launch_pdl(embed_place_kernel, dim3(p.ntiles), kThreads, s, p, pass);
+        cudaError_t e = launch_pdl(embed_count_kernel, dim3(p.ntiles), kThreads, 0, s, p, pass);
+        if (e == cudaSuccess) e = launch_pdl(embed_scan_kernel, dim3(1), 1024, 0, s, p.counts, p.ntiles << p.bits);
+        if (e == cudaSuccess) e = launch_pdl(embed_place_kernel, dim3(p.ntiles), kThreads, 0, s, p, pass);
         if (e != cudaSuccess) return e;
         *launches += 3;
     }
@@ -556,8 +994,7 @@ cudaError_t launch_embed_reduce(int dtype, int out_dtype, int vec, const EmbedGr
     else if (dtype == kBF16 && out_dtype == kF32) e = reduce_out<BF16T, F32T>(vec, p, launches, s);
     else if (dtype == kF16 && out_dtype == kF16) e = reduce_out<F16T, F16T>(vec, p, launches, s);
     else if (dtype == kF16 && out_dtype == kF32) e = reduce_out<F16T, F32T>(vec, p, launches, s);
-    if (e != cudaSuccess || p.accumulate) return e;
-    return out_dtype == kF32 ? zero_typed<F32T>(p, launches, s) : zero_typed<BF16T>(p, launches, s);
+    return e;
 }
 
 }  // namespace rr

@@ -105,6 +105,20 @@ struct Layout {
 
 uint64_t up(uint64_t x, uint64_t to) { return (x + to - 1) / to * to; }
 
+// Sorted positions per block: 32, fewer where that leaves a GPU of 148 SMs
+// short of warps (one per block and slice of the columns), more where the
+// partial sums would need more than 8192 rows.
+uint32_t block_positions(uint64_t M, uint64_t D)
+{
+#ifdef RR_EMBED_K
+    return RR_EMBED_K;
+#endif
+    if (M > 32 * 4096) return (uint32_t)(32 * ceil_div(M, 32 * 4096));
+    uint32_t k = 32;
+    while (k > 8 && ceil_div(M, k) * ceil_div(D, kEmbedCols) < 148 * 32) k /= 2;
+    return k;
+}
+
 Layout layout(uint64_t M, uint64_t V, uint64_t D)
 {
     Layout l{};
@@ -113,9 +127,7 @@ Layout layout(uint64_t M, uint64_t V, uint64_t D)
     l.passes = (total + kSortMaxBits - 1) / kSortMaxBits;
     l.bits = (total + l.passes - 1) / l.passes;
     l.ntiles = (uint32_t)ceil_div(M, kSortTile);
-    // blocks of 32 sorted positions, larger ones where those would be more
-    // than 4096: the partial sums stay below 8192 rows
-    l.K = (uint32_t)(32 * std::max<uint64_t>(1, ceil_div(M, 32 * 4096)));
+    l.K = block_positions(M, D);
     l.nblk = (uint32_t)ceil_div(M, l.K);
     l.Dp = (uint32_t)up(D, 4);
     uint64_t at = 0;

@@ -279,6 +279,12 @@ cudaError_t launch_embed_reduce(int dtype, int out_dtype, int vec, const EmbedGr
                                 cudaStream_t s);
 constexpr uint32_t kSortTile = 2048;   // keys per CTA of a sort pass
 constexpr int kSortMaxBits = 9;        // bits per digit, at most
+constexpr uint32_t kClusterKeys = 12000;         // keys that one CTA of the one-launch sort holds
+constexpr uint32_t kClusterMax = 8 * kClusterKeys;  // and that its largest cluster does
+#ifndef RR_CLUSTER_SHARE
+#define RR_CLUSTER_SHARE 2048
+#endif
+constexpr uint32_t kClusterShare = RR_CLUSTER_SHARE;  // keys per CTA from which the cluster grows
 constexpr uint32_t kEmbedCols = 256;   // columns of a warp's slice of a row
 
 }  // namespace rr
