@@ -145,81 +145,172 @@ __device__ __forceinline__ uint32_t position_key(const EmbedGradParams& p, uint3
 }
 
 constexpr int kWarps = kThreads / 32;
+
+// Up to kRankMax tokens: every position's place is the number of positions
+// with a smaller id, or the same id and an earlier place in the list.  Every
+// CTA reads all the ids; kRankParts threads share a position's comparisons.
+constexpr int kRankThreads = 128, kRankParts = 4;
+
+__global__ void __launch_bounds__(kRankThreads) embed_rank_kernel(const __grid_constant__ EmbedGradParams p)
+{
+    __shared__ __align__(16) uint32_t keys[kRankMax];
+    pdl_begin();
+    const uint32_t M = p.M, padded = (M + 15u) & ~15u;
+#pragma unroll 8
+    for (uint32_t i = threadIdx.x; i < padded; i += kRankThreads) keys[i] = i < M ? position_key(p, i) : 0xffffffffu;
+    __syncthreads();
+    const uint32_t i = blockIdx.x * (kRankThreads / kRankParts) + threadIdx.x / kRankParts;
+    const uint32_t key = i < M ? keys[i] : 0u;
+    uint32_t place = 0;
+    const uint4* v4 = reinterpret_cast<const uint4*>(keys);
+#pragma unroll 4
+    for (uint32_t v = threadIdx.x % kRankParts; v < padded / 4; v += kRankParts) {
+        const uint4 k = v4[v];
+        const uint32_t than = v < i / 4 ? key + 1u : key;  // equal ids in front count, equal ids behind do not
+        place += (k.x < than) + (k.y < than) + (k.z < than) + (k.w < than);
+    }
+    place += __shfl_xor_sync(0xffffffffu, place, 1);
+    place += __shfl_xor_sync(0xffffffffu, place, 2);
+    if (i >= M || threadIdx.x % kRankParts) return;
+    for (uint32_t e = i & ~3u; e < i; ++e) place += keys[e] == key;  // the vector that i is in
+    p.key[0][place] = key;
+    p.pos[0][place] = i;
+}
+
+// More tokens: least-significant-digit radix sort, a launch that counts the
+// first digit and one per digit that places; pass k reads buffer
+// (passes - k) & 1 and writes the other, so the last pass writes buffer 0.  A tile is kSortTile consecutive keys.
+// The first launch counts every tile's keys per digit, tile by tile, writes
+// the keys down, and clears the later digits' counts; each placing adds the
+// next digit's counts of the tiles that it fills (whole numbers: any order of
+// the atomics gives the same).
 constexpr int kSortRounds = (int)kSortTile / kThreads;  // keys per thread
 
-// Least-significant-digit radix sort, one digit per pass; pass k reads buffer
-// k & 1 (pass 0 the ids) and writes the other.  Counting: a tile's keys per
-// digit, digit-major, so one exclusive scan over all counts gives every tile's
-// first place for every digit.  Pass 0 also clears the touched bits.
-__global__ void __launch_bounds__(kThreads) embed_count_kernel(const __grid_constant__ EmbedGradParams p, int pass)
+__global__ void __launch_bounds__(kThreads) embed_count_kernel(const __grid_constant__ EmbedGradParams p)
 {
     __shared__ uint32_t hist[1 << kSortMaxBits];
     pdl_begin();
-    const uint32_t digits = 1u << p.bits, shift = (uint32_t)(pass * p.bits);
+    const uint32_t digits = 1u << p.bits, from = (uint32_t)p.passes & 1u;
+    const uint64_t table = (uint64_t)p.ntiles * digits;
     for (uint32_t d = threadIdx.x; d < digits; d += kThreads) hist[d] = 0;
-    if (pass == 0)
-        for (uint64_t w = (uint64_t)blockIdx.x * kThreads + threadIdx.x; w < (p.V + 31) / 32;
-             w += (uint64_t)gridDim.x * kThreads)
-            p.touched[w] = 0u;
+    const uint32_t i0 = blockIdx.x * kSortTile + threadIdx.x;
+    uint32_t key[kSortRounds];
+#pragma unroll
+    for (int j = 0; j < kSortRounds; ++j) {
+        const uint32_t i = i0 + (uint32_t)j * kThreads;
+        if (i < p.M) key[j] = position_key(p, i);
+    }
+    for (int later = 1; later < p.passes; ++later)
+        for (uint32_t d = threadIdx.x; d < digits; d += kThreads)
+            p.counts[(uint64_t)later * table + (uint64_t)blockIdx.x * digits + d] = 0u;
     __syncthreads();
-    const uint32_t i0 = blockIdx.x * kSortTile;
-    for (uint32_t k = threadIdx.x; k < kSortTile && k < p.M - i0; k += kThreads) {
-        const uint32_t key = pass == 0 ? position_key(p, i0 + k) : p.key[pass & 1][i0 + k];
-        atomicAdd(&hist[(key >> shift) & (digits - 1)], 1u);
+#pragma unroll
+    for (int j = 0; j < kSortRounds; ++j) {
+        const uint32_t i = i0 + (uint32_t)j * kThreads;
+        if (i >= p.M) continue;
+        p.key[from][i] = key[j];
+        atomicAdd(&hist[key[j] & (digits - 1)], 1u);
     }
     __syncthreads();
-    for (uint32_t d = threadIdx.x; d < digits; d += kThreads) p.counts[(uint64_t)d * p.ntiles + blockIdx.x] = hist[d];
+    for (uint32_t d = threadIdx.x; d < digits; d += kThreads) p.counts[(uint64_t)blockIdx.x * digits + d] = hist[d];
 }
 
-// Exclusive scan of count values in place, by one CTA: every thread takes a
-// run of consecutive ones.
-__global__ void __launch_bounds__(1024) embed_scan_kernel(uint32_t* v, uint32_t count)
+// First place of every digit's keys: an exclusive scan over the digits of
+// their totals, one digit per thread (digits <= blockDim.x * 2; a thread has
+// the digits 2t and 2t + 1).
+__device__ __forceinline__ void scan_digits(uint32_t (&v)[2], uint32_t* sums)
 {
-    __shared__ uint32_t sums[32];
-    pdl_begin();
-    const uint32_t per = (count + 1023) / 1024, tid = threadIdx.x, lane = tid & 31u;
-    const uint32_t lo = tid * per < count ? tid * per : count, hi = lo + per < count ? lo + per : count;
-    uint32_t s = 0;
-    for (uint32_t i = lo; i < hi; ++i) s += v[i];
-    uint32_t x = s;
+    const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
+    uint32_t x = v[0] + v[1];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= (uint32_t)o) x += y;
     }
-    if (lane == 31u) sums[tid >> 5] = x;
+    if (lane == 31u) sums[warp] = x;
     __syncthreads();
-    uint32_t before = x - s;
-    for (uint32_t w = 0; w < tid >> 5; ++w) before += sums[w];
-    for (uint32_t i = lo; i < hi; ++i) {
-        const uint32_t c = v[i];
-        v[i] = before;
-        before += c;
-    }
+    uint32_t first = x - v[0] - v[1];
+    for (uint32_t w = 0; w < warp; ++w) first += sums[w];
+    v[1] = first + v[0];
+    v[0] = first;
+}
+
+// Many tiles: one CTA turns the counts into every tile's first places.
+__global__ void __launch_bounds__(kThreads) embed_scan_kernel(const __grid_constant__ EmbedGradParams p, int pass)
+{
+    __shared__ uint32_t sums[kWarps];
+    pdl_begin();
+    const uint32_t digits = 1u << p.bits, d = threadIdx.x * 2;
+    uint32_t* counts = p.counts + (uint64_t)pass * p.ntiles * digits;
+    uint32_t v[2] = {0, 0};
+    if (d < digits)
+#pragma unroll 8
+        for (uint32_t t = 0; t < p.ntiles; ++t) {
+            const uint2 c = *reinterpret_cast<const uint2*>(counts + (uint64_t)t * digits + d);
+            v[0] += c.x;
+            v[1] += c.y;
+        }
+    scan_digits(v, sums);
+    if (d < digits)
+#pragma unroll 8
+        for (uint32_t t = 0; t < p.ntiles; ++t) {
+            uint2* at = reinterpret_cast<uint2*>(counts + (uint64_t)t * digits + d);
+            const uint2 c = *at;
+            *at = make_uint2(v[0], v[1]);
+            v[0] += c.x;
+            v[1] += c.y;
+        }
 }
 
 // Placing, stable: a warp takes consecutive keys, 32 at a time; lanes with
 // the same digit rank themselves by lane, behind the warp's earlier ones, and
-// the warps' counts stack in warp order.  Pass 0 also marks the rows.
+// the warps' counts stack in warp order.  A tile's first places come from the
+// scan, or -- few tiles -- from the counts themselves, which every CTA sums.
+template <bool SCANNED>
 __global__ void __launch_bounds__(kThreads) embed_place_kernel(const __grid_constant__ EmbedGradParams p, int pass)
 {
     __shared__ uint32_t cnt[kWarps][1 << kSortMaxBits];
+    __shared__ uint32_t sums[kWarps];
     pdl_begin();
-    const uint32_t digits = 1u << p.bits, shift = (uint32_t)(pass * p.bits);
+    const uint32_t digits = 1u << p.bits, shift = (uint32_t)(pass * p.bits), from = (uint32_t)(p.passes - pass) & 1u;
+    const uint32_t* counts = p.counts + (uint64_t)pass * p.ntiles * digits;
+    uint32_t* later = p.counts + (uint64_t)(pass + 1) * p.ntiles * digits;
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u;
     for (uint32_t d = threadIdx.x; d < kWarps << p.bits; d += kThreads) cnt[d >> p.bits][d & (digits - 1)] = 0;
-    __syncthreads();
     const uint32_t i0 = blockIdx.x * kSortTile + warp * (kSortTile / kWarps);
     uint32_t key[kSortRounds], pos[kSortRounds], rank[kSortRounds];
 #pragma unroll
     for (int j = 0; j < kSortRounds; ++j) {
         const uint32_t i = i0 + (uint32_t)j * 32u + lane;
         if (i < p.M) {
-            key[j] = pass == 0 ? position_key(p, i) : p.key[pass & 1][i];
-            pos[j] = pass == 0 ? i : p.pos[pass & 1][i];
-            if (pass == 0 && key[j] < p.V) atomicOr(&p.touched[key[j] >> 5], 1u << (key[j] & 31u));
+            key[j] = p.key[from][i];
+            pos[j] = pass == 0 ? i : p.pos[from][i];
         }
     }
+    // this tile's first place of the digits 2t and 2t + 1
+    const uint32_t d2 = threadIdx.x * 2;
+    uint32_t first[2] = {0, 0};
+    if constexpr (SCANNED) {
+        if (d2 < digits) {
+            first[0] = counts[(uint64_t)blockIdx.x * digits + d2];
+            first[1] = counts[(uint64_t)blockIdx.x * digits + d2 + 1];
+        }
+    } else {
+        uint32_t total[2] = {0, 0}, ahead[2] = {0, 0};
+        if (d2 < digits)
+#pragma unroll 8
+            for (uint32_t t = 0; t < p.ntiles; ++t) {
+                const uint2 c = *reinterpret_cast<const uint2*>(counts + (uint64_t)t * digits + d2);
+                total[0] += c.x;
+                total[1] += c.y;
+                ahead[0] += t < blockIdx.x ? c.x : 0;
+                ahead[1] += t < blockIdx.x ? c.y : 0;
+            }
+        scan_digits(total, sums);
+        first[0] = total[0] + ahead[0];
+        first[1] = total[1] + ahead[1];
+    }
+    __syncthreads();
 #pragma unroll
     for (int j = 0; j < kSortRounds; ++j) {
         const bool have = i0 + (uint32_t)j * 32u + lane < p.M;
@@ -232,13 +323,15 @@ __global__ void __launch_bounds__(kThreads) embed_place_kernel(const __grid_cons
         __syncwarp();
     }
     __syncthreads();
-    for (uint32_t d = threadIdx.x; d < digits; d += kThreads) {
-        uint32_t at = p.counts[(uint64_t)d * p.ntiles + blockIdx.x];
+    if (d2 < digits) {
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const uint32_t c = cnt[w][d];
-            cnt[w][d] = at;
-            at += c;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const uint32_t c = cnt[w][d2 + e];
+                cnt[w][d2 + e] = first[e];
+                first[e] += c;
+            }
         }
     }
     __syncthreads();
@@ -246,169 +339,10 @@ __global__ void __launch_bounds__(kThreads) embed_place_kernel(const __grid_cons
     for (int j = 0; j < kSortRounds; ++j) {
         if (i0 + (uint32_t)j * 32u + lane >= p.M) continue;
         const uint32_t to = cnt[warp][(key[j] >> shift) & (digits - 1)] + rank[j];
-        p.key[(pass + 1) & 1][to] = key[j];
-        p.pos[(pass + 1) & 1][to] = pos[j];
-    }
-}
-
-// The whole sort in one launch, for as many tokens as fit in the shared
-// memory of one cluster: CS CTAs hold `per` consecutive (key, position) pairs
-// each and run every pass between cluster barriers, the pairs moving through
-// distributed shared memory; the last pass writes global memory.  The steps of
-// a pass are those of the kernels above: rank within the warp, stack the
-// warps' counts, then the counts of every digit in every CTA of the cluster
-// give each CTA's first place.
-constexpr int kClusterThreads = 1024;
-constexpr int kClusterWarps = kClusterThreads / 32;
-constexpr int kClusterRounds = (int)((kClusterKeys + kClusterThreads - 1) / kClusterThreads);
-constexpr int kDigits = 1 << kSortMaxBits;
-constexpr uint32_t kClusterSmem =
-    2u * kClusterKeys * 8u + (uint32_t)kClusterWarps * kDigits * 2u + 2u * kDigits * 4u + 32u * 4u;
-static_assert(kClusterSmem <= 232448, "within the shared memory of a CTA");
-static_assert(kDigits <= kClusterThreads, "one thread per digit");
-
-__device__ __forceinline__ uint32_t cluster_rank()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-
-__device__ __forceinline__ void cluster_barrier()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// The address in CTA `rank`'s shared memory of the same variable as p here.
-__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank)
-{
-    uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
-    return a;
-}
-
-__global__ void __launch_bounds__(kClusterThreads) embed_sort_kernel(const __grid_constant__ EmbedGradParams p)
-{
-    extern __shared__ __align__(16) unsigned char raw[];
-    uint2* buf = reinterpret_cast<uint2*>(raw);                             // [2][kClusterKeys] (key, position)
-    uint16_t* cnt = reinterpret_cast<uint16_t*>(buf + 2 * kClusterKeys);    // [warps][digits]
-    uint32_t* hist = reinterpret_cast<uint32_t*>(cnt + kClusterWarps * kDigits);  // this CTA's keys per digit
-    uint32_t* base = hist + kDigits;                                        // their first places
-    uint32_t* sums = base + kDigits;                                        // of the scan's warps
-    const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u;
-    const uint32_t cs = gridDim.x, me = cs > 1 ? cluster_rank() : 0;  // the grid is one cluster
-    const uint32_t per = (p.M + cs - 1) / cs;                          // <= kClusterKeys
-    const uint32_t i0 = me * per, mine = i0 < p.M ? (p.M - i0 < per ? p.M - i0 : per) : 0;
-    const uint32_t magic = (uint32_t)(((1ull << 32) + per - 1) / per);  // x / per for x < 2^32 / per
-    const uint32_t digits = 1u << p.bits;
-    const uint32_t run = (((mine + kClusterWarps - 1) / kClusterWarps) + 31u) & ~31u;  // keys of a warp, whole rounds
-    auto sync_all = [&] {
-        __syncwarp();  // the cluster barrier is taken by whole warps
-        if (cs > 1) cluster_barrier();
-        else __syncthreads();
-    };
-    pdl_begin();
-    if (!p.accumulate)
-        for (uint64_t w = (uint64_t)me * kClusterThreads + tid; w < (p.V + 31) / 32; w += (uint64_t)cs * kClusterThreads)
-            p.touched[w] = 0u;
-    uint32_t key[kClusterRounds], pos[kClusterRounds], rank[kClusterRounds];
-    for (int pass = 0; pass < p.passes; ++pass) {
-        const uint32_t shift = (uint32_t)(pass * p.bits);
-        const uint2* in = buf + (pass & 1) * kClusterKeys;
-        for (uint32_t i = tid; i < (uint32_t)kClusterWarps << p.bits; i += kClusterThreads)
-            cnt[(i >> p.bits) * kDigits + (i & (digits - 1))] = 0;
-        // the thread's keys, all loads of a pass in flight
-#pragma unroll
-        for (int j = 0; j < kClusterRounds; ++j) {
-            const uint32_t at = (uint32_t)j * 32u + lane, i = warp * run + at;
-            key[j] = 0xffffffffu;
-            if (at < run && i < mine) {
-                if (pass == 0) {
-                    key[j] = position_key(p, i0 + i);
-                    pos[j] = i0 + i;
-                } else {
-                    const uint2 v = in[i];
-                    key[j] = v.x;
-                    pos[j] = v.y;
-                }
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < kClusterRounds; ++j) {
-            if ((uint32_t)j * 32u >= run) break;
-            const bool have = key[j] != 0xffffffffu;
-            const uint32_t d = have ? (key[j] >> shift) & (digits - 1) : digits;
-            const uint32_t same = __match_any_sync(0xffffffffu, d);
-            const uint32_t before = __popc(same & ((1u << lane) - 1u));
-            if (have) rank[j] = cnt[warp * kDigits + d] + before;
-            __syncwarp();
-            if (have && before == 0) cnt[warp * kDigits + d] = (uint16_t)(cnt[warp * kDigits + d] + __popc(same));
-            __syncwarp();
-        }
-        __syncthreads();
-        if (tid < digits) {
-            uint32_t at = 0;
-#pragma unroll
-            for (int w = 0; w < kClusterWarps; ++w) {
-                const uint32_t c = cnt[w * kDigits + tid];
-                cnt[w * kDigits + tid] = (uint16_t)at;
-                at += c;
-            }
-            hist[tid] = at;
-        }
-        sync_all();
-        // all keys of a smaller digit, then this digit's keys in earlier CTAs
-        uint32_t total = 0, earlier = 0;
-        if (tid < digits) {
-            if (cs > 1) {
-#pragma unroll
-                for (uint32_t c = 0; c < 8; ++c) {
-                    if (c >= cs) break;
-                    uint32_t h;
-                    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(h) : "r"(cluster_addr(&hist[tid], c)) : "memory");
-                    total += h;
-                    if (c < me) earlier += h;
-                }
-            } else {
-                total = hist[tid];
-            }
-        }
-        uint32_t x = total;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= (uint32_t)o) x += y;
-        }
-        if (lane == 31u) sums[warp] = x;
-        __syncthreads();
-        if (tid < digits) {
-            uint32_t first = x - total + earlier;
-            for (uint32_t w = 0; w < warp; ++w) first += sums[w];
-            base[tid] = first;
-        }
-        __syncthreads();
-        const bool last = pass + 1 == p.passes;
-        const uint32_t out = (uint32_t)((pass + 1) & 1) * kClusterKeys;
-#pragma unroll
-        for (int j = 0; j < kClusterRounds; ++j) {
-            if (key[j] == 0xffffffffu) continue;
-            if (pass == 0 && !p.accumulate && key[j] < p.V) atomicOr(&p.touched[key[j] >> 5], 1u << (key[j] & 31u));
-            const uint32_t d = (key[j] >> shift) & (digits - 1);
-            const uint32_t to = base[d] + cnt[warp * kDigits + d] + rank[j];
-            if (last) {
-                p.key[p.passes & 1][to] = key[j];
-                p.pos[p.passes & 1][to] = pos[j];
-            } else if (cs > 1) {
-                const uint32_t cta = __umulhi(to, magic), at = to - cta * per;
-                asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};"
-                             ::"r"(cluster_addr(&buf[out + at], cta)), "r"(key[j]), "r"(pos[j])
-                             : "memory");
-            } else {
-                buf[out + to] = make_uint2(key[j], pos[j]);
-            }
-        }
-        sync_all();  // the pairs are in place, and no CTA leaves while another reads its counts
+        p.key[from ^ 1u][to] = key[j];
+        p.pos[from ^ 1u][to] = pos[j];
+        if (pass + 1 < p.passes)
+            atomicAdd(&later[(uint64_t)(to / kSortTile) * digits + ((key[j] >> (shift + (uint32_t)p.bits)) & (digits - 1))], 1u);
     }
 }
 
@@ -471,43 +405,98 @@ __device__ __forceinline__ void write_part(float* q, uint32_t c0, uint32_t D,
     }
 }
 
-// Where the sorted keys are after the last pass.
-__device__ __forceinline__ const uint32_t* sorted_keys(const EmbedGradParams& p) { return p.key[p.passes & 1]; }
-__device__ __forceinline__ const uint32_t* sorted_pos(const EmbedGradParams& p) { return p.pos[p.passes & 1]; }
+// The sorted list.
+__device__ __forceinline__ const uint32_t* sorted_keys(const EmbedGradParams& p) { return p.key[0]; }
+__device__ __forceinline__ const uint32_t* sorted_pos(const EmbedGradParams& p) { return p.pos[0]; }
 
-// The block of K sorted positions that a warp sums, 32 of them at a time: a
-// lane holds one position's id and row address, and three masks say after
-// which of the 32 a run ends, and where its sum goes.
+// What a warp sums of the sorted list.  Block b covers positions [bK, (b+1)K)
+// and owns the runs of equal ids that begin there: a run that goes on into the
+// next block only is summed to its end by its owner, and that block's warp
+// skips it.  A longer run (a frequent token) is cut at the blocks' ends: the
+// block it begins in leaves its "last" partial sum, the others their "first"
+// one, and the join adds them up.
+struct Span {
+    uint32_t from, to;  // positions
+    uint32_t head;      // the id of a cut run that began earlier (V: none)
+    bool cut;           // the last run goes on: it is cut at `to`
+};
+
+__device__ __forceinline__ Span block_span(const EmbedGradParams& p, uint32_t blk)
+{
+    const uint32_t* keys = sorted_keys(p);
+    const uint32_t V = (uint32_t)p.V, K = p.K, lane = threadIdx.x & 31u;
+    const uint32_t s = blk * K, e = s + K < p.M ? s + K : p.M;
+    // six ids decide, loaded at once: before, first, last, after, one block back, one block on
+    const uint32_t at = lane == 0 ? s - 1 : lane == 1 ? s : lane == 2 ? e - 1 : lane == 3 ? e : lane == 4 ? s - K - 1 : s + 2 * K;
+    const bool there = lane == 0 ? s > 0 : lane == 3 ? e < p.M : lane == 4 ? s > K : lane == 5 ? (uint64_t)s + 2ull * K < p.M : true;
+    const uint32_t k = lane < 6 && there ? keys[at] : 0xffffffffu;
+    const uint32_t before = __shfl_sync(0xffffffffu, k, 0), first = __shfl_sync(0xffffffffu, k, 1);
+    const uint32_t last = __shfl_sync(0xffffffffu, k, 2), after = __shfl_sync(0xffffffffu, k, 3);
+    const uint32_t back = __shfl_sync(0xffffffffu, k, 4), on = __shfl_sync(0xffffffffu, k, 5);
+    Span sp{s, e, V, false};
+    if (first >= V) {  // nothing but ids without a row from here on
+        sp.to = s;
+        return sp;
+    }
+    const bool began_earlier = before == first;
+    if (began_earlier) {
+        if (back == first || after == first) {  // over three blocks or more: cut here
+            sp.head = first;
+        } else {  // the block before sums it: skip to its end
+            for (uint32_t i = s; i < e; i += 32) {
+                const uint32_t same = __ballot_sync(0xffffffffu, i + lane < e && keys[i + lane < e ? i + lane : s] == first);
+                sp.from = i + __popc(same);
+                if (same != 0xffffffffu) break;
+            }
+        }
+    }
+    if (last < V && after == last && !(began_earlier && last == first)) {  // begins here and goes on
+        if (on == last) {
+            sp.cut = true;
+        } else {
+            const uint32_t end = e + K < p.M ? e + K : p.M;
+            for (uint32_t i = e; i < end; i += 32) {
+                const uint32_t same = __ballot_sync(0xffffffffu, i + lane < end && keys[i + lane < end ? i + lane : e] == last);
+                sp.to = i + __popc(same);
+                if (same != 0xffffffffu) break;
+            }
+        }
+    }
+    return sp;
+}
+
+// Up to 32 positions of a span: a lane holds one position's id and row
+// address, and three masks say after which of them a run ends, and where its
+// sum goes.
 template <class T>
 struct Chunk {
     uint32_t n;       // positions with a row: the first n (ids are sorted)
-    uint32_t ends;    // a run's last position (in this chunk, or the block's last)
-    uint32_t first;   // ... whose run began in an earlier block: a partial sum
-    uint32_t on;      // ... whose run goes on in the next block: a partial sum
+    uint32_t ends;    // a run's last position in the span
+    uint32_t first;   // ... of a cut run that began earlier: a partial sum
+    uint32_t cut;     // ... of a cut run that goes on: a partial sum
     uint32_t key;
     const T* row;
 };
 
 template <class T>
-__device__ __forceinline__ Chunk<T> load_chunk(const EmbedGradParams& p, uint32_t i0, uint32_t b1, uint32_t before,
-                                               uint32_t after)
+__device__ __forceinline__ Chunk<T> load_chunk(const EmbedGradParams& p, uint32_t i0, const Span& sp)
 {
     const uint32_t lane = threadIdx.x & 31u, i = i0 + lane, V = (uint32_t)p.V;
     Chunk<T> c;
     c.key = V;
     c.row = nullptr;
-    uint32_t next = after;
-    if (i < b1) {
+    uint32_t next = V;
+    if (i < sp.to) {
         c.key = sorted_keys(p)[i];
         const uint32_t at = sorted_pos(p)[i], r = at / p.T;
         c.row = static_cast<const T*>(p.dout[r]) + (uint64_t)(at - r * p.T) * p.D;
-        if (i + 1 < b1) next = sorted_keys(p)[i + 1];
+        if (i + 1 < sp.to) next = sorted_keys(p)[i + 1];
     }
-    const bool valid = c.key < V, on = i + 1 == b1 && next == c.key;
+    const bool valid = c.key < V, end = valid && next != c.key;
     c.n = __popc(__ballot_sync(0xffffffffu, valid));
-    c.ends = __ballot_sync(0xffffffffu, valid && (next != c.key || on));
-    c.first = __ballot_sync(0xffffffffu, valid && c.key == before);
-    c.on = __ballot_sync(0xffffffffu, valid && on);
+    c.ends = __ballot_sync(0xffffffffu, end);
+    c.first = __ballot_sync(0xffffffffu, valid && c.key == sp.head);
+    c.cut = __ballot_sync(0xffffffffu, end && sp.cut && i + 1 == sp.to);
     return c;
 }
 
@@ -520,13 +509,11 @@ __device__ __forceinline__ void close_run(const EmbedGradParams& p, const Chunk<
 {
     const uint32_t key = __shfl_sync(0xffffffffu, ch.key, j);
     if ((ch.first >> j) & 1u) write_part<VEC>(p.part + (uint64_t)blk * p.Dp, c0, p.D, acc);
-    else if ((ch.on >> j) & 1u) write_part<VEC>(p.part + ((uint64_t)p.nblk + blk) * p.Dp, c0, p.D, acc);
+    else if ((ch.cut >> j) & 1u) write_part<VEC>(p.part + ((uint64_t)p.nblk + blk) * p.Dp, c0, p.D, acc);
     else write_row<Out, VEC>(p, key, c0, acc, old);
 }
 
-// A warp sums one slice of the columns over one block of K sorted positions:
-// runs that lie inside it go to the table, the first and the last run's sums
-// to the block's partials where they go on outside.
+// A warp sums one slice of the columns over one block's span.
 //
 // The rows stream through a ring of kRing slots of shared memory per warp by
 // cp.async, one row's slice per slot, and where the call adds to what is there
@@ -565,10 +552,8 @@ __global__ void __launch_bounds__(kThreads) embed_reduce_kernel(const __grid_con
     if (blk >= p.nblk) return;
     unsigned char* ring = ring_mem + warp * (kRing * kSlot);
     const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
-    const uint32_t b0 = blk * p.K, b1 = b0 + p.K < p.M ? b0 + p.K : p.M;
+    const Span sp = block_span(p, blk);
     const uint32_t c0 = blockIdx.y * kEmbedCols + lane * VEC;
-    const uint32_t V = (uint32_t)p.V;
-    const uint32_t before = b0 > 0 ? sorted_keys(p)[b0 - 1] : V, after = b1 < p.M ? sorted_keys(p)[b1] : V;
     float acc[NC][VEC];
     auto clear = [&] {
 #pragma unroll
@@ -577,9 +562,9 @@ __global__ void __launch_bounds__(kThreads) embed_reduce_kernel(const __grid_con
             for (int l = 0; l < VEC; ++l) acc[k][l] = 0.0f;
     };
     clear();
-    for (uint32_t i0 = b0; i0 < b1; i0 += 32) {
-        const Chunk<T> ch = load_chunk<T>(p, i0, b1, before, after);
-        const uint32_t fetch = ACC ? ch.ends & ~ch.first & ~ch.on : 0u;  // rows whose earlier values are needed
+    for (uint32_t i0 = sp.from; i0 < sp.to; i0 += 32) {
+        const Chunk<T> ch = load_chunk<T>(p, i0, sp);
+        const uint32_t fetch = ACC ? ch.ends & ~ch.first & ~ch.cut : 0u;  // rows whose earlier values are needed
         uint32_t made = 0;      // the next position to copy
         bool old_next = false;  // the earlier values of the one before it come first
         uint32_t in_slot = 0, out_slot = 0;
@@ -665,10 +650,8 @@ __global__ void __launch_bounds__(kThreads) embed_reduce_narrow_kernel(const __g
     const uint32_t lane = threadIdx.x & 31u;
     const uint32_t blk = blockIdx.x * kWarps + (threadIdx.x >> 5);
     if (blk >= p.nblk) return;
-    const uint32_t b0 = blk * p.K, b1 = b0 + p.K < p.M ? b0 + p.K : p.M;
+    const Span sp = block_span(p, blk);
     const uint32_t c0 = blockIdx.y * kEmbedCols + lane * VEC;
-    const uint32_t V = (uint32_t)p.V;
-    const uint32_t before = b0 > 0 ? sorted_keys(p)[b0 - 1] : V, after = b1 < p.M ? sorted_keys(p)[b1] : V;
     float acc[NC][VEC];
     auto clear = [&] {
 #pragma unroll
@@ -677,8 +660,8 @@ __global__ void __launch_bounds__(kThreads) embed_reduce_narrow_kernel(const __g
             for (int l = 0; l < VEC; ++l) acc[k][l] = 0.0f;
     };
     clear();
-    for (uint32_t i0 = b0; i0 < b1; i0 += 32) {
-        const Chunk<T> ch = load_chunk<T>(p, i0, b1, before, after);
+    for (uint32_t i0 = sp.from; i0 < sp.to; i0 += 32) {
+        const Chunk<T> ch = load_chunk<T>(p, i0, sp);
         for (uint32_t j0 = 0; j0 < ch.n; j0 += G) {
             Vec<In, VEC> x[G][NC];
 #pragma unroll
@@ -743,6 +726,34 @@ __device__ __forceinline__ void add_parts(const EmbedGradParams& p, uint32_t blk
     }
 }
 
+// Which of the 32 table rows from v0 on have a token, as bits: every lane
+// looks its row up in the sorted list, the warp's 32 first steps together.
+__device__ __forceinline__ uint32_t touched_rows(const EmbedGradParams& p, uint64_t v0)
+{
+    const uint32_t lane = threadIdx.x & 31u;
+    const uint32_t* keys = sorted_keys(p);
+    const uint64_t v = v0 + lane;
+    // the warp's range [lo, hi): keys before lo are below v0, keys from hi on are at least v0 + 32
+    uint32_t lo = 0, hi = p.M;
+    while (hi - lo > 64) {
+        const uint32_t step = (hi - lo + 31) / 32, at = lo + lane * step;
+        const uint32_t k = at < hi ? keys[at] : 0xffffffffu;
+        const uint32_t below = __popc(__ballot_sync(0xffffffffu, at < hi && k < v0));
+        const uint32_t within = __popc(__ballot_sync(0xffffffffu, at < hi && k < v0 + 32));
+        const uint32_t nlo = below ? lo + (below - 1) * step + 1 : lo;
+        const uint32_t nhi = lo + (uint64_t)within * step < hi ? lo + within * step : hi;
+        if (nlo == lo && nhi == hi) break;  // a frequent token's run: no narrower this way
+        lo = nlo;
+        hi = nhi;
+    }
+    while (lo < hi) {  // the first key that is at least v
+        const uint32_t mid = lo + (hi - lo) / 2;
+        if (keys[mid] < v) lo = mid + 1;
+        else hi = mid;
+    }
+    return __ballot_sync(0xffffffffu, lo < p.M && keys[lo] == v);
+}
+
 // Zeros into the rows that no token touched: a CTA takes 32 rows of one
 // replica, run by run of untouched ones.
 template <class Out>
@@ -752,7 +763,7 @@ __device__ __forceinline__ void zero_rows(const EmbedGradParams& p, uint32_t chu
     constexpr int L = Out::L;
     const uint64_t v0 = (uint64_t)chunk * 32u;
     const uint32_t rows = (uint32_t)(p.V - v0 < 32 ? p.V - v0 : 32);
-    const uint32_t word = p.touched[chunk];
+    const uint32_t word = touched_rows(p, v0);
     T* base = static_cast<T*>(p.grad[replica]) + v0 * p.D;
     for (uint32_t i = 0; i < rows;) {
         if ((word >> i) & 1u) {
@@ -773,20 +784,23 @@ __device__ __forceinline__ void zero_rows(const EmbedGradParams& p, uint32_t chu
     }
 }
 
-// Joins the runs that cross blocks -- the block in which such a run begins
-// adds its partial sums in block order and writes the row -- and, in the CTAs
-// behind those (chunks of rows x replicas), clears the untouched rows: the
-// joins wait for memory while the clearing fills it.  A warp joins one run for
-// one slice; a run over many blocks (a frequent token) is shared by the CTA's
-// warps, each an eighth of the entries, and the eighths added in order.
-constexpr uint32_t kLongRun = 32;  // entries from which a run is shared
+// Joins the cut runs -- the block in which such a run begins adds its partial
+// sums in block order and writes the row -- and, in the CTAs behind those
+// (chunks of rows x replicas), clears the untouched rows: the joins wait for
+// memory while the clearing fills it.  A warp looks at kJoinBlocks blocks, a
+// lane at each, and joins a run for one slice; a run over many blocks is
+// shared by the CTA's warps, each an eighth of the entries, and the eighths
+// added in order.
+constexpr uint32_t kLongRun = 32;    // entries from which a run is shared
+constexpr uint32_t kJoinBlocks = 8;  // blocks per warp: fewer than a shared run's, so a warp meets at most one
 
 template <class Out, int VEC>
 __global__ void __launch_bounds__(kThreads) embed_join_kernel(const __grid_constant__ EmbedGradParams p, uint32_t joins,
                                                               uint32_t slices, uint32_t chunks)
 {
     constexpr int NC = kChunks<VEC>;
-    __shared__ uint32_t long_run[kWarps];
+    static_assert(kJoinBlocks < kLongRun);
+    __shared__ uint32_t long_run[kWarps], long_blk[kWarps];
     __shared__ __align__(16) float eighth[kWarps][kEmbedCols];
     pdl_begin();
     if (blockIdx.x >= joins) {
@@ -796,17 +810,16 @@ __global__ void __launch_bounds__(kThreads) embed_join_kernel(const __grid_const
     }
     const uint32_t* keys = sorted_keys(p);
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
-    const uint32_t slice = blockIdx.x % slices, blk0 = blockIdx.x / slices * kWarps;
+    const uint32_t slice = blockIdx.x % slices, blk0 = (blockIdx.x / slices * kWarps + warp) * kJoinBlocks;
     const uint32_t c0 = slice * kEmbedCols + lane * VEC;
-    // the entries of the run that begins in block blk and goes on behind it; 0: none
+    // the entries of the cut run that begins in block blk; 0: none
     auto entries = [&](uint32_t blk) -> uint32_t {
-        if (blk + 1 >= p.nblk) return 0;
-        const uint32_t end = (blk + 1) * p.K;  // < M
-        const uint32_t key = keys[end - 1];
-        if (key >= (uint32_t)p.V || keys[end] != key) return 0;
-        if (blk > 0 && keys[blk * p.K - 1] == key) return 0;  // begun earlier (then the whole block is the run's)
-        uint32_t lo = blk + 1, hi = p.nblk - 1;               // the last block whose first key is this one
-        if (lo < hi && keys[(lo + 1) * p.K] != key) hi = lo;  // most runs end in the next block
+        const uint64_t on = ((uint64_t)blk + 2) * p.K;
+        if (on >= p.M) return 0;
+        const uint32_t end = (blk + 1) * p.K, key = keys[end - 1];
+        const uint32_t before = blk > 0 ? keys[blk * p.K - 1] : 0xffffffffu;
+        if (key >= (uint32_t)p.V || keys[on] != key || before == key) return 0;
+        uint32_t lo = blk + 2, hi = p.nblk - 1;  // the last block whose first key is this one
         while (lo < hi) {
             const uint32_t mid = (lo + hi + 1) / 2;
             if (keys[mid * p.K] == key) lo = mid;
@@ -821,20 +834,28 @@ __global__ void __launch_bounds__(kThreads) embed_join_kernel(const __grid_const
 #pragma unroll
             for (int l = 0; l < VEC; ++l) acc[k][l] = 0.0f;
     };
-    const uint32_t mine = entries(blk0 + warp);
-    if (mine > 0 && mine <= kLongRun) {
-        clear();
-        add_parts<VEC>(p, blk0 + warp, 0, mine, c0, acc);
-        write_row<Out, VEC>(p, keys[(blk0 + warp + 1) * p.K], c0, acc);
+    const uint32_t mine = lane < kJoinBlocks ? entries(blk0 + lane) : 0;
+    const uint32_t shared_run = __ballot_sync(0xffffffffu, mine > kLongRun);
+    if (lane == 0) long_run[warp] = 0;
+    __syncwarp();
+    if (mine > kLongRun) {
+        long_run[warp] = mine;
+        long_blk[warp] = blk0 + lane;
     }
-    if (lane == 0) long_run[warp] = mine > kLongRun ? mine : 0;
+    for (uint32_t todo = __ballot_sync(0xffffffffu, mine > 0) & ~shared_run; todo; todo &= todo - 1) {
+        const uint32_t l = __ffs(todo) - 1, blk = blk0 + l, n = __shfl_sync(0xffffffffu, mine, l);
+        clear();
+        add_parts<VEC>(p, blk, 0, n, c0, acc);
+        write_row<Out, VEC>(p, keys[(blk + 1) * p.K], c0, acc);
+    }
     __syncthreads();
     for (uint32_t w = 0; w < kWarps; ++w) {
         const uint32_t n = long_run[w];
         if (n == 0) continue;
+        const uint32_t blk = long_blk[w];
         clear();
-        add_parts<VEC>(p, blk0 + w, (uint32_t)((uint64_t)n * warp / kWarps), (uint32_t)((uint64_t)n * (warp + 1) / kWarps),
-                       c0, acc);
+        add_parts<VEC>(p, blk, (uint32_t)((uint64_t)n * warp / kWarps), (uint32_t)((uint64_t)n * (warp + 1) / kWarps), c0,
+                       acc);
 #pragma unroll
         for (int k = 0; k < NC; ++k)
 #pragma unroll
@@ -847,7 +868,7 @@ __global__ void __launch_bounds__(kThreads) embed_join_kernel(const __grid_const
 #pragma unroll
                     for (int l = 0; l < VEC; ++l)
                         acc[k][l] = __fadd_rn(acc[k][l], eighth[e][(k * 32 + lane) * VEC + l]);
-            write_row<Out, VEC>(p, keys[(blk0 + w + 1) * p.K], c0, acc);
+            write_row<Out, VEC>(p, keys[(blk + 1) * p.K], c0, acc);
         }
         __syncthreads();
     }
@@ -895,7 +916,7 @@ cudaError_t reduce_typed(const EmbedGradParams& p, int* launches, cudaStream_t s
     }
     if (e != cudaSuccess) return e;
     *launches += 1;
-    const uint64_t joins = p.nblk > 1 ? (uint64_t)blocks_for(p.nblk, kWarps) * slices : 0;
+    const uint64_t joins = p.nblk > 2 ? (uint64_t)blocks_for(p.nblk, kWarps * kJoinBlocks) * slices : 0;  // a cut run covers three blocks
     const uint64_t chunks = p.accumulate ? 0 : (p.V + 31) / 32;
     const uint64_t work = joins + chunks * (uint64_t)p.nout;
     if (work == 0) return cudaSuccess;
@@ -949,40 +970,21 @@ cudaError_t launch_embed_lookup(int dtype, int vec, const EmbedLookupParams& p, 
 
 cudaError_t launch_embed_sort(const EmbedGradParams& p, int* launches, cudaStream_t s)
 {
-    if (p.M <= kClusterMax) {
-        // CTAs of the cluster: enough that each holds at most kClusterShare keys
-        unsigned cs = 1;
-        while (cs < 8 && p.M > cs * kClusterShare) cs *= 2;
-        const cudaError_t set =
-            cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kClusterSmem);
-        if (set != cudaSuccess) return set;
-        cudaLaunchAttribute attr[2]{};
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        attr[1].id = cudaLaunchAttributeClusterDimension;
-        attr[1].val.clusterDim.x = cs;
-        attr[1].val.clusterDim.y = 1;
-        attr[1].val.clusterDim.z = 1;
-        cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3(cs);
-        cfg.blockDim = dim3(kClusterThreads);
-        cfg.dynamicSmemBytes = kClusterSmem;
-        cfg.stream = s;
-        cfg.attrs = attr;
-        cfg.numAttrs = 2;
-        const cudaError_t e = cudaLaunchKernelEx(&cfg, embed_sort_kernel, p);
-        if (e != cudaSuccess) return e;
+    if (p.M <= kRankMax) {
         *launches += 1;
-        return cudaGetLastError();
+        return launch_pdl(embed_rank_kernel, dim3(blocks_for(p.M, kRankThreads / kRankParts)), kRankThreads, 0, s, p);
     }
-    for (int pass = 0; pass < p.passes; ++pass) {
-        cudaError_t e = launch_pdl(embed_count_kernel, dim3(p.ntiles), kThreads, 0, s, p, pass);
-        if (e == cudaSuccess) e = launch_pdl(embed_scan_kernel, dim3(1), 1024, 0, s, p.counts, p.ntiles << p.bits);
-        if (e == cudaSuccess) e = launch_pdl(embed_place_kernel, dim3(p.ntiles), kThreads, 0, s, p, pass);
-        if (e != cudaSuccess) return e;
-        *launches += 3;
+    const bool scan = p.ntiles > kScanTiles;
+    cudaError_t e = launch_pdl(embed_count_kernel, dim3(p.ntiles), kThreads, 0, s, p);
+    *launches += 1;
+    for (int pass = 0; pass < p.passes && e == cudaSuccess; ++pass) {
+        if (scan) e = launch_pdl(embed_scan_kernel, dim3(1), kThreads, 0, s, p, pass);
+        if (e == cudaSuccess)
+            e = scan ? launch_pdl(embed_place_kernel<true>, dim3(p.ntiles), kThreads, 0, s, p, pass)
+                     : launch_pdl(embed_place_kernel<false>, dim3(p.ntiles), kThreads, 0, s, p, pass);
+        *launches += scan ? 2 : 1;
     }
-    return cudaSuccess;
+    return e;
 }
 
 cudaError_t launch_embed_reduce(int dtype, int out_dtype, int vec, const EmbedGradParams& p, int* launches,

@@ -98,7 +98,7 @@ rr_status_t embedding(const void* const* ids, rr_id_type_t id_type, const void* 
 // The gradient's workspace, in the order in which it is laid out; every part
 // starts on a 256-byte boundary.
 struct Layout {
-    uint64_t key[2], pos[2], counts, touched, part, bytes;
+    uint64_t key[2], pos[2], counts, part, bytes;
     uint32_t ntiles, K, nblk, Dp;
     int passes, bits;
 };
@@ -138,8 +138,7 @@ Layout layout(uint64_t M, uint64_t V, uint64_t D)
     };
     for (int k = 0; k < 2; ++k) l.key[k] = part(M * 4);
     for (int k = 0; k < 2; ++k) l.pos[k] = part(M * 4);
-    l.counts = part(((uint64_t)l.ntiles << l.bits) * 4);
-    l.touched = part((V + 31) / 32 * 4);
+    l.counts = part(((uint64_t)l.passes * l.ntiles << l.bits) * 4);
     l.part = part(2ull * l.nblk * l.Dp * 4);
     l.bytes = at;
     return l;
@@ -204,7 +203,6 @@ rr_status_t embedding_grad(const void* const* ids, rr_id_type_t id_type, const v
         p.pos[k] = reinterpret_cast<uint32_t*>(base + l.pos[k]);
     }
     p.counts = reinterpret_cast<uint32_t*>(base + l.counts);
-    p.touched = reinterpret_cast<uint32_t*>(base + l.touched);
     p.part = reinterpret_cast<float*>(base + l.part);
     p.passes = l.passes;
     p.bits = l.bits;

@@ -185,8 +185,7 @@ struct EmbedGradParams {
     // workspace
     uint32_t* key[2];        // sort buffers: token ids ...
     uint32_t* pos[2];        // ... and positions (rank * T + token)
-    uint32_t* counts;        // per digit and tile
-    uint32_t* touched;       // one bit per table row
+    uint32_t* counts;        // per pass, tile and digit
     float* part;             // partial sums of runs that cross a block: [2][nblk][Dp]
     int passes, bits;        // of the sort: digits, and bits per digit
     uint32_t ntiles;
@@ -277,14 +276,13 @@ cudaError_t launch_embed_lookup(int dtype, int vec, const EmbedLookupParams& p, 
 cudaError_t launch_embed_sort(const EmbedGradParams& p, int* launches, cudaStream_t s);
 cudaError_t launch_embed_reduce(int dtype, int out_dtype, int vec, const EmbedGradParams& p, int* launches,
                                 cudaStream_t s);
-constexpr uint32_t kSortTile = 2048;   // keys per CTA of a sort pass
-constexpr int kSortMaxBits = 9;        // bits per digit, at most
-constexpr uint32_t kClusterKeys = 12000;         // keys that one CTA of the one-launch sort holds
-constexpr uint32_t kClusterMax = 8 * kClusterKeys;  // and that its largest cluster does
-#ifndef RR_CLUSTER_SHARE
-#define RR_CLUSTER_SHARE 2048
+#ifndef RR_SORT_TILE
+#define RR_SORT_TILE 2048
 #endif
-constexpr uint32_t kClusterShare = RR_CLUSTER_SHARE;  // keys per CTA from which the cluster grows
+constexpr uint32_t kSortTile = RR_SORT_TILE;   // keys per CTA of a sort pass
+constexpr int kSortMaxBits = 9;        // bits per digit, at most
+constexpr uint32_t kRankMax = 4096;    // tokens that are sorted by counting smaller ids, in one launch
+constexpr uint32_t kScanTiles = 128;   // tiles from which a pass scans its counts in a launch of its own
 constexpr uint32_t kEmbedCols = 256;   // columns of a warp's slice of a row
 
 }  // namespace rr

@@ -151,6 +151,23 @@ def test_grad_of_many_tokens():
     run_grad(2, 140_001, 5000, 8, torch.bfloat16, "zipf", nout=1)  # blocks of more than 32 positions
     run_grad(1, 200_000, 300_000, 8, torch.float32, "same")
     run_grad(64, 11, 50, 16, torch.float16, "zipf", nout=2)
+    for kind in ("zipf", "runs", "same"):  # blocks of 16 and of 32 positions
+        run_grad(2, 5_003, 2000, 2048, torch.bfloat16, kind, nout=1)
+        run_grad(2, 12_000, 2000, 2048, torch.bfloat16, kind, nout=1, accumulate=True, grad_dtype=torch.float32)
+
+
+@pytest.mark.parametrize("length", [1, 7, 8, 9, 15, 16, 17, 24, 25, 63, 64, 65, 300])
+def test_grad_runs_that_end_at_block_bounds(length):
+    """Runs of one length shifted against the blocks of positions by 0..7."""
+    for shift in range(8):
+        t = length * 5 + shift
+        ids = torch.cat([torch.zeros(shift, dtype=torch.int64), 1 + torch.arange(5).repeat_interleave(length)]).cuda()
+        x = values(length + shift, t * 40, torch.bfloat16).view(t, 40)
+        for accumulate in (False, True):
+            g = values(3, 8 * 40, torch.float32).view(8, 40)
+            old = g.clone()
+            rrv.embedding_grad([ids], [x], [g], "sum", accumulate=accumulate)
+            check_grad([ids], [x], [g], [old], 8, 1.0, accumulate)
 
 
 def test_grad_padding_and_no_tokens():
