@@ -9,6 +9,7 @@
 //
 // Both are bound by HBM.  Partial sums are joined in a fixed order (no
 // atomics), so a call's bits depend only on its tensors.
+#include "rr_bulk.cuh"
 #include "rr_clip.cuh"
 
 namespace rr {
@@ -77,7 +78,8 @@ __global__ void __launch_bounds__(kThreads) norm_finish_kernel(const __grid_cons
 {
     __shared__ double sh[kThreads / 32];
     pdl_begin();
-    clip_coef(a, sh);
+    const float c = clip_coef(a, sh);
+    if (a.coef && threadIdx.x == 0) *a.coef = c;
 }
 
 // The two fp32 values whose upper halves are the word h and lower halves the
@@ -163,9 +165,104 @@ __global__ void __launch_bounds__(kThreads, 4) clip_scale_kernel(const __grid_co
     }
 }
 
+// The scaling of large sets: one CTA per tile, the tile (two of them where the
+// values are parked in halves) brought to shared memory and sent to every
+// rank by bulk copies, as the one-shot all-reduce moves its tiles; the
+// coefficient comes from norm_finish_kernel.  Tensors whose copies are at
+// different 16-byte phases run element by element.
+struct ScaleBulkParams {
+    ScaleParams s;       // tile0 counts tiles of kBulkScaleBytes in all
+    const float* coef;
+    unsigned int* waits; // as BulkParams (rr_bulk.cuh)
+    uint32_t hold;
+    uint32_t spin;
+};
+static_assert(sizeof(ScaleBulkParams) <= 32764, "ScaleBulkParams too large");
+constexpr uint32_t kBulkScaleBytes = 16384;  // of shared memory per CTA
+
+template <class Ty, bool PARKED>
+__global__ void __launch_bounds__(kThreads) clip_bulk_kernel(const __grid_constant__ ScaleBulkParams bp)
+{
+    using T = typename Ty::T;
+    constexpr int L = Ty::L;
+    constexpr uint32_t TV = kBulkScaleBytes / 16 / (PARKED ? 2 : 1);
+    extern __shared__ __align__(128) uint4 sm[];
+    __shared__ __align__(8) uint64_t bar;
+    pdl_begin();
+    const ScaleParams& p = bp.s;
+    const float c = *bp.coef;
+    const int n = p.n;
+    const uint64_t w = p.tile0[p.nt] - 1 - blockIdx.x;  // last tiles first: L2 still holds what was touched last
+    const int t = find_segment(p.tile0, p.nt, w);
+    const uint64_t tile = w - p.tile0[t], len = p.len[t];
+    T* const* ptr = reinterpret_cast<T* const*>(&p.ptr[(size_t)t * n]);
+    const T* src = ptr[0];
+    const T* low = PARKED ? ptr[1] : ptr[0];
+    auto one = [&](uint64_t e) {
+        float x;
+        if constexpr (PARKED) x = __uint_as_float(((uint32_t)src[e] << 16) | (uint32_t)low[e]);
+        else x = Ty::ld1(src + e);
+        x = __fmul_rn(x, c);
+        for (int o = 0; o < n; ++o) Ty::st1(ptr[o] + e, x);
+    };
+    if (!p.vec[t]) {
+        const uint64_t e0 = tile * TV * L;
+        for (uint64_t e = e0 + threadIdx.x; e < len && e < e0 + TV * L; e += kThreads) one(e);
+        return;
+    }
+    uint64_t head = (uint64_t)((L - phase_of(src, L)) & (L - 1));
+    if (head > len) head = len;
+    const uint64_t nv = (len - head) / L, tail = len - head - nv * L;
+    if (tile == 0 && threadIdx.x < head + tail)
+        one(threadIdx.x < head ? threadIdx.x : head + nv * L + (threadIdx.x - head));
+    const uint64_t v0 = tile * TV;
+    if (v0 >= nv) return;
+    const uint32_t nvt = (uint32_t)(nv - v0 < TV ? nv - v0 : TV), bytes = nvt * 16u;
+    const uint64_t e0 = head + v0 * L;
+    const uint32_t b = bulk_smem_addr(&bar);
+    if (threadIdx.x == 0) bulk_bar_init(b, bp.hold);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}"
+                     ::"r"(b), "r"(bytes * (PARKED ? 2u : 1u)) : "memory");
+#pragma unroll
+        for (int k = 0; k < (PARKED ? 2 : 1); ++k)
+            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                         ::"r"(bulk_smem_addr(sm + k * TV)), "l"((k ? low : src) + e0), "r"(bytes), "r"(b)
+                         : "memory");
+    }
+    if (!bulk_tile_landed(b, bp.waits, bp.hold, bp.spin)) return;  // the whole CTA skips the tile
+    for (uint32_t v = threadIdx.x; v < nvt; v += kThreads) {
+        float a[L];
+        if constexpr (PARKED) {
+            const uint4 h = sm[v], q = sm[TV + v];
+            unpark2(h.x, q.x, a[0], a[1]);
+            unpark2(h.y, q.y, a[2], a[3]);
+            unpark2(h.z, q.z, a[4], a[5]);
+            unpark2(h.w, q.w, a[6], a[7]);
+        } else {
+            Ty::unpack(sm[v], a);
+        }
+#pragma unroll
+        for (int l = 0; l < L; ++l) a[l] = __fmul_rn(a[l], c);
+        sm[v] = Ty::pack(a);
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int o = 0; o < n; ++o)
+            asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;"
+                         ::"l"(ptr[o] + e0), "r"(bulk_smem_addr(sm)), "r"(bytes)
+                         : "memory");
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        bulk_bar_inval(b);
+    }
+}
+
 // A launch as a programmatic dependent of the stream's previous kernel.
 template <class... A>
-cudaError_t launch_pdl(void (*kernel)(A...), unsigned grid, cudaStream_t s, const A&... a)
+cudaError_t launch_pdl(void (*kernel)(A...), unsigned grid, uint32_t smem, cudaStream_t s, const A&... a)
 {
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -173,6 +270,7 @@ cudaError_t launch_pdl(void (*kernel)(A...), unsigned grid, cudaStream_t s, cons
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
@@ -199,8 +297,8 @@ template <class Ty>
 cudaError_t norm_typed(const NormParams& p, unsigned grid, cudaStream_t s)
 {
     if (p.nt <= kNormTensorsSmall)
-        return launch_pdl(norm_kernel<Ty, kNormTensorsSmall>, grid, s, shrink<NormParamsT<kNormTensorsSmall>>(p));
-    return launch_pdl(norm_kernel<Ty, kNormTensors>, grid, s, p);
+        return launch_pdl(norm_kernel<Ty, kNormTensorsSmall>, grid, 0, s, shrink<NormParamsT<kNormTensorsSmall>>(p));
+    return launch_pdl(norm_kernel<Ty, kNormTensors>, grid, 0, s, p);
 }
 
 template <class Ty, bool PARKED>
@@ -217,15 +315,35 @@ cudaError_t scale_typed(const ScaleParams& p, unsigned grid, cudaStream_t s)
         q.clip = p.clip;
         q.n = p.n;
         q.nt = p.nt;
-        return launch_pdl(clip_scale_kernel<Ty, PARKED, kScaleTensorsSmall, kScalePtrsSmall>, grid, s, q);
+        return launch_pdl(clip_scale_kernel<Ty, PARKED, kScaleTensorsSmall, kScalePtrsSmall>, grid, 0, s, q);
     }
-    return launch_pdl(clip_scale_kernel<Ty, PARKED, kScaleTensors, kScalePtrs>, grid, s, p);
+    return launch_pdl(clip_scale_kernel<Ty, PARKED, kScaleTensors, kScalePtrs>, grid, 0, s, p);
+}
+
+template <class Ty, bool PARKED>
+cudaError_t bulk_typed(const ScaleParams& p, const float* coef, unsigned grid, cudaStream_t s)
+{
+    RankParams rp{};
+    rp.waits = bulk_wait_counters();
+    if (!rp.waits) return cudaErrorInvalidValue;
+    const BulkParams wait = bulk_params(rp);
+    ScaleBulkParams bp;
+    bp.s = p;
+    bp.coef = coef;
+    bp.waits = wait.waits;
+    bp.hold = wait.hold;
+    bp.spin = wait.spin;
+    return launch_pdl(clip_bulk_kernel<Ty, PARKED>, grid, kBulkScaleBytes, s, bp);
 }
 
 }  // namespace
 
 uint64_t norm_tile_elems(int dtype) { return (uint64_t)kThreads * kNormU * (dtype == kF32 ? 4u : 8u); }
-uint64_t scale_tile_elems(int dtype) { return (uint64_t)kThreads * kScaleU * (dtype == kF32 ? 4u : 8u); }
+uint64_t scale_tile_elems(int dtype, bool parked, bool bulk)
+{
+    const uint64_t vecs = bulk ? kBulkScaleBytes / 16 / (parked && dtype != kF32 ? 2 : 1) : (uint64_t)kThreads * kScaleU;
+    return vecs * (dtype == kF32 ? 4u : 8u);
+}
 
 cudaError_t launch_norm(int dtype, const NormParams& p, int* slots, cudaStream_t s)
 {
@@ -244,16 +362,30 @@ cudaError_t launch_norm(int dtype, const NormParams& p, int* slots, cudaStream_t
 cudaError_t launch_norm_join(const double* in, int64_t count, double* out, int* slots, cudaStream_t s)
 {
     *slots = kJoinCtas;
-    return launch_pdl(norm_join_kernel, (unsigned)kJoinCtas, s, in, count, out);
+    return launch_pdl(norm_join_kernel, (unsigned)kJoinCtas, 0, s, in, count, out);
 }
 
-cudaError_t launch_norm_finish(const ClipArgs& a, cudaStream_t s) { return launch_pdl(norm_finish_kernel, 1u, s, a); }
+cudaError_t launch_norm_finish(const ClipArgs& a, cudaStream_t s) { return launch_pdl(norm_finish_kernel, 1u, 0, s, a); }
 
-cudaError_t launch_clip_scale(int dtype, bool parked, const ScaleParams& p, cudaStream_t s)
+cudaError_t launch_clip_scale(int dtype, bool parked, bool bulk, const ScaleParams& p, cudaStream_t s)
 {
     const uint64_t work = p.tile0[p.nt];
+    if (work == 0) return cudaSuccess;
+    if (bulk) {
+        if (work > kMaxGrid) return cudaErrorInvalidValue;
+        const float* coef = p.clip.coef;
+        switch (dtype) {
+        case kF32: return bulk_typed<F32T, false>(p, coef, (unsigned)work, s);
+        case kBF16:
+            return parked ? bulk_typed<BF16T, true>(p, coef, (unsigned)work, s)
+                          : bulk_typed<BF16T, false>(p, coef, (unsigned)work, s);
+        case kF16:
+            return parked ? bulk_typed<F16T, true>(p, coef, (unsigned)work, s)
+                          : bulk_typed<F16T, false>(p, coef, (unsigned)work, s);
+        }
+        return cudaErrorInvalidValue;
+    }
     const unsigned grid = (unsigned)(work < kNormCtas ? work : kNormCtas);
-    if (grid == 0) return cudaSuccess;
     switch (dtype) {
     case kF32: return scale_typed<F32T, false>(p, grid, s);  // fp32 sums are parked whole, in rank 0's buffers
     case kBF16: return parked ? scale_typed<BF16T, true>(p, grid, s) : scale_typed<BF16T, false>(p, grid, s);

@@ -76,6 +76,7 @@ constexpr rr_dtype_t kGradTypes[] = {RR_F32, RR_BF16, RR_F16};
 struct Passes {
     double* partial;
     cudaStream_t stream;
+    bool bulk = false;  // the scaling runs by bulk copies
     int64_t count = 0;  // partials so far
 
     // The norm's launches over rank 0's tensors, one type at a time.
@@ -105,20 +106,26 @@ struct Passes {
         return RR_OK;
     }
 
-    // The partials as the next launches read them: at most kMaxPartials.
+    // The partials as the next launches read them: at most kMaxPartials; and
+    // for a scaling by bulk copies the coefficient itself.
     rr_status_t join(ClipArgs* a)
     {
         a->partial = partial;
         a->npartial = (int)count;
-        if (count <= kMaxPartials) return RR_OK;
-        int slots = 0;
-        const cudaError_t e =
-            timed_launch([&] { return launch_norm_join(partial, count, partial + count, &slots, stream); });
-        if (e != cudaSuccess) return cuda_fail(e, "norm join launch");
-        t_stats.launches += 1;
-        a->partial = partial + count;
-        a->npartial = slots;
-        return RR_OK;
+        if (count > kMaxPartials) {
+            int slots = 0;
+            const cudaError_t e =
+                timed_launch([&] { return launch_norm_join(partial, count, partial + count, &slots, stream); });
+            if (e != cudaSuccess) return cuda_fail(e, "norm join launch");
+            t_stats.launches += 1;
+            a->partial = partial + count;
+            a->npartial = slots;
+        }
+        if (!bulk) return RR_OK;
+        a->coef = reinterpret_cast<float*>(partial + count + kJoinCtas);
+        const rr_status_t st = finish(*a);
+        a->norm = nullptr;
+        return st;
     }
 
     rr_status_t finish(const ClipArgs& a)
@@ -135,14 +142,14 @@ struct Passes {
     rr_status_t scale(rr_dtype_t d, bool parked, int n, int ntensors, Ptr&& ptr, Len&& numel, ClipArgs& a)
     {
         auto p = std::make_unique<ScaleParams>();
-        const uint64_t te = scale_tile_elems(d);
+        const uint64_t te = scale_tile_elems(d, parked, bulk);
         const int most = std::min(kScaleTensors, kScalePtrs / n);
         for (int t = 0; t <= ntensors; ++t) {
             const bool end = t == ntensors;
             if ((end || p->nt == most) && p->nt > 0) {
                 p->n = n;
                 p->clip = a;
-                const cudaError_t e = timed_launch([&] { return launch_clip_scale(d, parked, *p, stream); });
+                const cudaError_t e = timed_launch([&] { return launch_clip_scale(d, parked, bulk, *p, stream); });
                 if (e != cudaSuccess) return cuda_fail(e, "clip launch");
                 t_stats.launches += 1;
                 a.norm = nullptr;
@@ -196,7 +203,8 @@ uint64_t park_tiles(const rr_bucket_plan_t* plan, int b0, int nb, int n)
     return tiles;
 }
 
-size_t workspace_bytes(uint64_t partials) { return (size_t)(partials + kJoinCtas) * sizeof(double); }
+// Partial sums, the joined ones, the coefficient.
+size_t workspace_bytes(uint64_t partials) { return (size_t)(partials + kJoinCtas + 1) * sizeof(double); }
 
 rr_status_t bucket_range_ok(const rr_bucket_plan_t* plan, int b0, int nb, int nranks)
 {
@@ -286,7 +294,7 @@ rr_status_t clip_grads(const rr_tensor_list_t* grads, float max_norm, float eps,
     add_spans(grads, n, true, spans);
     if ((st = check_scratch(norm, ws, ws_bytes, workspace_bytes(norm_slots(grads)), spans)) != RR_OK) return st;
     if ((st = check_device_ptrs(grads->ptrs, n * grads->ntensors)) != RR_OK) return st;
-    Passes run{static_cast<double*>(ws), stream};
+    Passes run{static_cast<double*>(ws), stream, n * S >= kBulkClipBytes};
     ClipArgs a{};
     a.max_norm = max_norm;
     a.eps = eps;
@@ -335,7 +343,7 @@ rr_status_t bucket_allreduce_clip(const rr_bucket_plan_t* plan, int b0, int nb, 
     if (synced) add_spans(synced, n, true, spans);
     const size_t need = workspace_bytes(clip_partials(plan, b0, nb, n, synced));
     if ((st = check_scratch(norm, ws, ws_bytes, need, spans)) != RR_OK) return st;
-    Passes run{static_cast<double*>(ws), stream};
+    Passes run{static_cast<double*>(ws), stream, n * (S + R) >= kBulkClipBytes};
     ClipArgs a{};
     a.max_norm = max_norm;
     a.eps = eps;

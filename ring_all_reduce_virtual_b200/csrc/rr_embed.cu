@@ -352,22 +352,18 @@ __global__ void __launch_bounds__(kThreads) embed_place_kernel(const __grid_cons
 template <int VEC>
 constexpr int kChunks = (int)kEmbedCols / 32 / VEC;
 
-// The finished sum of row v (the lane's columns) into every replica; old: the
-// first replica's earlier values, where they have been fetched.
+// The finished sum of row v (the lane's columns) into every replica.
 template <class Out, int VEC>
 __device__ __forceinline__ void write_row(const EmbedGradParams& p, uint64_t v, uint32_t c0,
-                                          const float (&acc)[kChunks<VEC>][VEC],
-                                          const Vec<Out, VEC>* old = nullptr)
+                                          const float (&acc)[kChunks<VEC>][VEC])
 {
     using T = typename Out::T;
     constexpr int NC = kChunks<VEC>;
+#pragma unroll 1
     for (int o = 0; o < p.nout; ++o) {
         T* q = static_cast<T*>(p.grad[o]) + v * p.D;
         Vec<Out, VEC> x[NC];
-        if (old && o == 0) {
-#pragma unroll
-            for (int k = 0; k < NC; ++k) x[k] = old[k];
-        } else if (p.accumulate) {  // every load before the first store
+        if (p.accumulate) {  // every load before the first store
 #pragma unroll
             for (int k = 0; k < NC; ++k)
                 if (c0 + (uint32_t)k * 32u * VEC < p.D) x[k].load(q + c0 + (uint32_t)k * 32u * VEC);
@@ -386,6 +382,27 @@ __device__ __forceinline__ void write_row(const EmbedGradParams& p, uint64_t v, 
             x[k].from_f(a);
             if (c0 + (uint32_t)k * 32u * VEC < p.D) x[k].store(q + c0 + (uint32_t)k * 32u * VEC);
         }
+    }
+}
+
+// The same for a call that adds to one table, whose earlier values of the row
+// (the lane's columns) have been brought to shared memory.
+template <class Out, int VEC>
+__device__ __forceinline__ void write_row_onto(const EmbedGradParams& p, uint64_t v, uint32_t c0,
+                                               const float (&acc)[kChunks<VEC>][VEC], const typename Out::T* old)
+{
+    typename Out::T* q = static_cast<typename Out::T*>(p.grad[0]) + v * p.D;
+#pragma unroll
+    for (int k = 0; k < kChunks<VEC>; ++k) {
+        if (kChunks<VEC> > 1 && c0 + (uint32_t)k * 32u * VEC >= p.D) continue;
+        Vec<Out, VEC> x;
+        float a[VEC];
+        x.load(old + (k * 32 + (threadIdx.x & 31u)) * VEC);
+        x.to_f(a);
+#pragma unroll
+        for (int l = 0; l < VEC; ++l) a[l] = __fadd_rn(a[l], __fmul_rn(acc[k][l], p.factor));
+        x.from_f(a);
+        if (c0 + (uint32_t)k * 32u * VEC < p.D) x.store(q + c0 + (uint32_t)k * 32u * VEC);
     }
 }
 
@@ -500,31 +517,27 @@ __device__ __forceinline__ Chunk<T> load_chunk(const EmbedGradParams& p, uint32_
     return c;
 }
 
-// Sum of a run to where it belongs.  old: the row's earlier values (one
-// replica's, fetched ahead) or NULL.
+// Sum of the run that ends at position j of a chunk to where it belongs.
 template <class Out, int VEC, class T>
 __device__ __forceinline__ void close_run(const EmbedGradParams& p, const Chunk<T>& ch, uint32_t j, uint32_t blk,
-                                          uint32_t c0, const float (&acc)[kChunks<VEC>][VEC],
-                                          const Vec<Out, VEC>* old)
+                                          uint32_t c0, const float (&acc)[kChunks<VEC>][VEC])
 {
     const uint32_t key = __shfl_sync(0xffffffffu, ch.key, j);
-    if ((ch.first >> j) & 1u) write_part<VEC>(p.part + (uint64_t)blk * p.Dp, c0, p.D, acc);
-    else if ((ch.cut >> j) & 1u) write_part<VEC>(p.part + ((uint64_t)p.nblk + blk) * p.Dp, c0, p.D, acc);
-    else write_row<Out, VEC>(p, key, c0, acc, old);
+    const bool first = (ch.first >> j) & 1u;
+    if (first || ((ch.cut >> j) & 1u))
+        write_part<VEC>(p.part + ((first ? 0 : (uint64_t)p.nblk) + blk) * p.Dp, c0, p.D, acc);
+    else
+        write_row<Out, VEC>(p, key, c0, acc);
 }
 
 // A warp sums one slice of the columns over one block's span.
 //
-// The rows stream through a ring of kRing slots of shared memory per warp by
-// cp.async, one row's slice per slot, and where the call adds to what is there
+// The rows stream through a ring of slots in shared memory, kRingBytes a warp, by
+// cp.async, one row's slice per slot, and where the call adds to one table
 // the earlier values of a row follow the last position of its run through the
-// same ring, so the sums never wait for a load that was not issued kRing rows
-// ago.  A lane reads only what it copied itself: no barrier.  Measured on 8 x
+// same ring, so the sums wait only for loads that were issued several rows ago.  A lane reads only what it copied itself: no barrier.  Measured on 8 x
 // 8192 tokens of 2048 bf16 into fp32: see the launch.
-#ifndef RR_EMBED_RING
-#define RR_EMBED_RING 8
-#endif
-constexpr int kRing = RR_EMBED_RING;
+constexpr uint32_t kRingBytes = 8192;  // of a warp
 
 template <int B>
 __device__ __forceinline__ void copy_async(uint32_t to, const void* from)
@@ -544,16 +557,23 @@ __global__ void __launch_bounds__(kThreads) embed_reduce_kernel(const __grid_con
     using TO = typename Out::T;
     constexpr int NC = kChunks<VEC>;
     constexpr uint32_t kSlot = kRingSlot<In, Out, VEC, ACC>;
+    constexpr int kRing = (int)(kRingBytes / kSlot);
+    static_assert(kRing >= 2 && (kRing & (kRing - 1)) == 0, "slots are counted modulo a power of two");
     constexpr int BI = VEC * (int)sizeof(T), BO = VEC * (int)sizeof(TO);
     extern __shared__ __align__(16) unsigned char ring_mem[];
     pdl_begin();
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
     const uint32_t blk = blockIdx.x * kWarps + warp;
     if (blk >= p.nblk) return;
-    unsigned char* ring = ring_mem + warp * (kRing * kSlot);
+    unsigned char* ring = ring_mem + warp * kRingBytes;
     const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
     const Span sp = block_span(p, blk);
     const uint32_t c0 = blockIdx.y * kEmbedCols + lane * VEC;
+    // one access per lane: a lane past the row's end copies the row's last
+    // columns (and stores nothing), which saves a branch per row; several: it
+    // copies nothing
+    const uint32_t col = NC == 1 ? min(c0, p.D - VEC) : c0;
+    auto inside = [&](int k) { return NC == 1 || c0 + (uint32_t)k * 32u * VEC < p.D; };
     float acc[NC][VEC];
     auto clear = [&] {
 #pragma unroll
@@ -574,33 +594,29 @@ __global__ void __launch_bounds__(kThreads) embed_reduce_kernel(const __grid_con
                 const TO* q = static_cast<const TO*>(p.grad[0]) + (uint64_t)__shfl_sync(0xffffffffu, ch.key, made - 1) * p.D;
 #pragma unroll
                 for (int k = 0; k < NC; ++k) {
-                    const uint32_t c = c0 + (uint32_t)k * 32u * VEC;
-                    if (c < p.D) {
-                        constexpr int B = BO > 16 ? 16 : BO;
+                    constexpr int B = BO > 16 ? 16 : BO;
+                    if (!inside(k)) continue;
 #pragma unroll
-                        for (int h = 0; h < BO; h += B)
-                            copy_async<B < 4 ? 4 : B>(to + (uint32_t)(k * 32 + lane) * BO + h,
-                                                      reinterpret_cast<const char*>(q + c) + h);
-                    }
+                    for (int h = 0; h < BO; h += B)
+                        copy_async<B < 4 ? 4 : B>(to + (uint32_t)(k * 32 + lane) * BO + h,
+                                                  reinterpret_cast<const char*>(q + col + k * 32 * VEC) + h);
                 }
                 old_next = false;
             } else if (made < ch.n) {
                 const T* q = reinterpret_cast<const T*>(__shfl_sync(0xffffffffu, (unsigned long long)ch.row, made));
 #pragma unroll
-                for (int k = 0; k < NC; ++k) {
-                    const uint32_t c = c0 + (uint32_t)k * 32u * VEC;
-                    if (c < p.D) copy_async<BI < 4 ? 4 : BI>(to + (uint32_t)(k * 32 + lane) * BI, q + c);
-                }
+                for (int k = 0; k < NC; ++k)
+                    if (inside(k)) copy_async<BI < 4 ? 4 : BI>(to + (uint32_t)(k * 32 + lane) * BI, q + col + k * 32 * VEC);
                 if (ACC) old_next = (fetch >> made) & 1u;
                 ++made;
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
-            in_slot = in_slot + 1 < kRing ? in_slot + 1 : 0;
+            in_slot = (in_slot + 1) & (kRing - 1);
         };
         auto next_slot = [&]() -> const unsigned char* {  // the oldest item, landed
             asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
             const unsigned char* q = ring + out_slot * kSlot;
-            out_slot = out_slot + 1 < kRing ? out_slot + 1 : 0;
+            out_slot = (out_slot + 1) & (kRing - 1);
             return q;
         };
 #pragma unroll 1
@@ -610,7 +626,7 @@ __global__ void __launch_bounds__(kThreads) embed_reduce_kernel(const __grid_con
             const T* x = reinterpret_cast<const T*>(next_slot());
 #pragma unroll
             for (int k = 0; k < NC; ++k) {
-                if (c0 + (uint32_t)k * 32u * VEC >= p.D) continue;
+                if (!inside(k)) continue;
                 Vec<In, VEC> v;
                 float a[VEC];
                 v.load(x + (k * 32 + lane) * VEC);
@@ -621,15 +637,11 @@ __global__ void __launch_bounds__(kThreads) embed_reduce_kernel(const __grid_con
             issue();
             if (!((ch.ends >> j) & 1u)) continue;
             if (ACC && ((fetch >> j) & 1u)) {
-                const TO* y = reinterpret_cast<const TO*>(next_slot());
-                Vec<Out, VEC> old[NC];
-#pragma unroll
-                for (int k = 0; k < NC; ++k)
-                    if (c0 + (uint32_t)k * 32u * VEC < p.D) old[k].load(y + (k * 32 + lane) * VEC);
+                write_row_onto<Out, VEC>(p, __shfl_sync(0xffffffffu, ch.key, j), c0, acc,
+                                         reinterpret_cast<const TO*>(next_slot()));
                 issue();
-                close_run<Out, VEC>(p, ch, j, blk, c0, acc, old);
             } else {
-                close_run<Out, VEC>(p, ch, j, blk, c0, acc, static_cast<const Vec<Out, VEC>*>(nullptr));
+                close_run<Out, VEC>(p, ch, j, blk, c0, acc);
             }
             clear();
         }
@@ -686,7 +698,7 @@ __global__ void __launch_bounds__(kThreads) embed_reduce_narrow_kernel(const __g
                     for (int l = 0; l < VEC; ++l) acc[k][l] = __fadd_rn(acc[k][l], a[l]);
                 }
                 if (!((ch.ends >> j) & 1u)) continue;
-                close_run<Out, VEC>(p, ch, j, blk, c0, acc, static_cast<const Vec<Out, VEC>*>(nullptr));
+                close_run<Out, VEC>(p, ch, j, blk, c0, acc);
                 clear();
             }
         }
@@ -700,7 +712,7 @@ template <int VEC>
 __device__ __forceinline__ void add_parts(const EmbedGradParams& p, uint32_t blk, uint32_t a, uint32_t b, uint32_t c0,
                                           float (&acc)[kChunks<VEC>][VEC])
 {
-    constexpr int NC = kChunks<VEC>, U = 4;  // entries whose loads are in flight
+    constexpr int NC = kChunks<VEC>, U = 1024 / (int)kEmbedCols;  // entries whose loads are in flight
     for (uint32_t i0 = a; i0 < b; i0 += U) {
         Vec<F32T, VEC> x[U][NC];
 #pragma unroll
@@ -909,10 +921,10 @@ cudaError_t reduce_typed(const EmbedGradParams& p, int* launches, cudaStream_t s
     cudaError_t e;
     if constexpr (VEC * sizeof(typename In::T) < 4) {
         e = launch_pdl(embed_reduce_narrow_kernel<In, Out, VEC>, grid, kThreads, 0, s, p);
-    } else if (p.accumulate) {
-        e = launch_ring(embed_reduce_kernel<In, Out, VEC, true>, grid, kWarps * kRing * kRingSlot<In, Out, VEC, true>, s, p);
+    } else if (p.accumulate && p.nout == 1) {
+        e = launch_ring(embed_reduce_kernel<In, Out, VEC, true>, grid, kWarps * kRingBytes, s, p);
     } else {
-        e = launch_ring(embed_reduce_kernel<In, Out, VEC, false>, grid, kWarps * kRing * kRingSlot<In, Out, VEC, false>, s, p);
+        e = launch_ring(embed_reduce_kernel<In, Out, VEC, false>, grid, kWarps * kRingBytes, s, p);
     }
     if (e != cudaSuccess) return e;
     *launches += 1;

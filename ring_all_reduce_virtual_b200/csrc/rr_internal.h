@@ -138,6 +138,7 @@ struct ClipArgs {
     float max_norm;
     float eps;
     float* norm;  // where the launch writes the norm (NULL: it does not)
+    float* coef;  // norm_finish: where it writes the coefficient (NULL: it does not); bulk scaling: where it reads it
 };
 
 // The clipping's second pass: rank 0's copy of each tensor, scaled, into
@@ -259,11 +260,15 @@ cudaError_t launch_bucket_fold(int grad_dtype, int op, const BucketFoldParams& p
 // Global norm and clipping.  parked (16-bit types): the values are fp32 sums
 // whose upper halves lie in rank 0's buffers and lower halves in rank 1's.
 uint64_t norm_tile_elems(int dtype);
-uint64_t scale_tile_elems(int dtype);
+uint64_t scale_tile_elems(int dtype, bool parked, bool bulk);
 cudaError_t launch_norm(int dtype, const NormParams& p, int* slots, cudaStream_t s);
 cudaError_t launch_norm_join(const double* in, int64_t count, double* out, int* slots, cudaStream_t s);
 cudaError_t launch_norm_finish(const ClipArgs& a, cudaStream_t s);
-cudaError_t launch_clip_scale(int dtype, bool parked, const ScaleParams& p, cudaStream_t s);
+cudaError_t launch_clip_scale(int dtype, bool parked, bool bulk, const ScaleParams& p, cudaStream_t s);
+#ifndef RR_BULK_CLIP
+#define RR_BULK_CLIP (32ull << 20)
+#endif
+constexpr uint64_t kBulkClipBytes = RR_BULK_CLIP;  // bytes written from which the scaling runs by bulk copies
 constexpr int kJoinCtas = 128;        // partials that launch_norm_join leaves
 constexpr int kMaxPartials = 2048;    // partials that a launch sums itself
 // The clipped sync's first pass: fold, park the sums, one partial per tile.
@@ -276,10 +281,7 @@ cudaError_t launch_embed_lookup(int dtype, int vec, const EmbedLookupParams& p, 
 cudaError_t launch_embed_sort(const EmbedGradParams& p, int* launches, cudaStream_t s);
 cudaError_t launch_embed_reduce(int dtype, int out_dtype, int vec, const EmbedGradParams& p, int* launches,
                                 cudaStream_t s);
-#ifndef RR_SORT_TILE
-#define RR_SORT_TILE 2048
-#endif
-constexpr uint32_t kSortTile = RR_SORT_TILE;   // keys per CTA of a sort pass
+constexpr uint32_t kSortTile = 1024;   // keys per CTA of a sort pass
 constexpr int kSortMaxBits = 9;        // bits per digit, at most
 constexpr uint32_t kRankMax = 4096;    // tokens that are sorted by counting smaller ids, in one launch
 constexpr uint32_t kScanTiles = 128;   // tiles from which a pass scans its counts in a launch of its own

@@ -263,6 +263,45 @@ def test_clipped_sync_of_a_range_and_of_many_tensors():
             ranks[r][t].check()
 
 
+@pytest.mark.parametrize("n", [1, 2, 3, 8])
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("layout", list(LAYOUTS))
+def test_large_sets(n, dtype, layout):
+    """Sets whose scaling runs by bulk copies: bits without a limit, values with one."""
+    sizes = [40_000_003 // n, 17, 70_001, 0, 8192]
+    off = LAYOUTS[layout]
+    plan = rrv.BucketPlan(sizes, dtype)
+    ranks = rank_grads(n, sizes, DT[dtype], off=off)
+    other = [[g.t.clone() for g in rank] for rank in ranks]
+    div = n if n > 1 else 1
+    avg = [sum(rank[t].t.double() for rank in ranks) / div for t in range(len(sizes))]
+    plan.all_reduce_range(0, plan.num_buckets, other, "avg")
+    keep = [[g.t.clone() for g in rank] for rank in ranks]
+    plan.all_reduce_clip(tensors(ranks), math.inf)
+    for rank, want in zip(ranks, other):
+        for g, w in zip(rank, want):
+            assert torch.equal(g.t, w)
+            g.check()
+    for rank, k in zip(ranks, keep):
+        for g, v in zip(rank, k):
+            g.t.copy_(v)
+    norm = norm64(avg)
+    got = plan.all_reduce_clip(tensors(ranks), 0.3 * norm, eps=0.0)
+    assert abs(float(got) - norm) <= (10 + 3 * n) * E * norm
+    for rank in ranks:
+        for g, a in zip(rank, avg):
+            near_scaled(g.t, 0.3 * a, extra=0.3 * 0.1 * 6 * n * E)
+            g.check()
+    src = [g.t.clone() for g in ranks[0]]
+    norm = norm64(src)
+    near_norm(rrv.clip_grads(tensors(ranks), 0.7 * norm, eps=0.0), norm)
+    for rank in ranks:
+        for g, a in zip(rank, src):
+            near_scaled(g.t, 0.7 * a.double())
+            g.check()
+    rrv.check_timeouts()
+
+
 def test_clipped_sync_with_a_nan_and_with_a_large_sum():
     sizes = [500, 60]
     ranks = tensors(rank_grads(4, sizes, torch.float16))
