@@ -14,6 +14,7 @@ semantics with its passage.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import Sequence
 
@@ -111,11 +112,23 @@ def _rank_args(tensors, what: str):
     return _ptr_array(tensors), len(tensors), count, d, dev
 
 
-def _stream(stream, device):
-    import torch
+_raw_stream = None
 
+
+def _current_stream(index: int) -> int:
+    """The handle of a device's current stream, without building a Stream object (2 us) where PyTorch offers that."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda i: torch.cuda.current_stream(i).cuda_stream)
+    return _raw_stream(index)
+
+
+def _stream(stream, device):
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        return ctypes.c_void_p(_current_stream(device.index))
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -323,55 +336,61 @@ class GradList:
         return self._scratch_bytes
 
 
-def _on_stream(stream, device):
-    """A context in which the caching allocator serves ``stream`` (None: the
-    device's current stream): scratch memory of a call is taken there, so that
-    its next user on that stream is ordered behind the call."""
-    import contextlib
-
+@contextlib.contextmanager
+def _placed(stream, device):
+    """Run with ``device`` current (kernels are launched from there) and the
+    caching allocator serving ``stream``: scratch memory of a call is taken
+    there, so that its next user on that stream is ordered behind the call."""
     import torch
 
-    if stream is None:
-        return contextlib.nullcontext()
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device)
-    return torch.cuda.stream(stream)
+    with torch.cuda.device(device):
+        if stream is None:
+            yield
+        else:
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), device)
+            with torch.cuda.stream(stream):
+                yield
 
 
-def _on_device(device):
-    """A context with ``device`` current: kernels are launched from there."""
-    import contextlib
-
+def _in_place(stream, device) -> bool:
+    """Whether a call needs no ``_placed``: the current stream of the current device."""
     import torch
 
-    if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+    return stream is None and device.index == torch.cuda.current_device()
 
 
-def _norm_out(out, device):
-    """The fp32 element that receives a norm."""
+_NORM_BYTES = 256  # in front of a workspace, for the norm
+
+
+def _with_norm(what: str, device, need: int, out, stream, call):
+    """Run ``call(norm pointer, workspace pointer, bytes, stream)``; the norm's tensor."""
     import torch
 
+    if not _in_place(stream, device):
+        with _placed(stream, device):
+            return _with_norm(what, device, need, out, None, call)
     if out is None:
-        return torch.empty((), dtype=torch.float32, device=device)
+        mem = torch.empty((_NORM_BYTES + need) // 4, dtype=torch.float32, device=device)
+        norm, at = mem[0], mem.data_ptr()
+        check(call(at, at + _NORM_BYTES, need, _current_stream(device.index)), what)
+        # a large workspace does not live on with the norm
+        return norm if need <= 1 << 16 else norm.clone()
     if not out.is_cuda or out.dtype != torch.float32 or out.numel() != 1 or out.device != device:
         raise ValueError("out must be one float32 element on the gradients' device")
+    mem = torch.empty(need, dtype=torch.uint8, device=device)
+    check(call(out.data_ptr(), mem.data_ptr(), need, _current_stream(device.index)), what)
     return out
 
 
 def _norm_call(what: str, gl: GradList, out, stream, call):
-    """Run ``call(norm pointer, workspace pointer, bytes, stream)`` on a list."""
+    """``_with_norm`` for a list."""
     import torch
 
-    device = gl.device if gl.device is not None else out.device if out is not None else \
-        torch.device("cuda", torch.cuda.current_device())
-    with _on_device(device), _on_stream(stream, device):
-        norm = _norm_out(out, device)
-        need = gl._workspace()
-        ws = torch.empty(need, dtype=torch.uint8, device=device)
-        check(call(norm.data_ptr(), ws.data_ptr(), need, _stream(stream, device)), what)
-    return norm
+    device = gl.device
+    if device is None:
+        device = out.device if out is not None else torch.device("cuda", torch.cuda.current_device())
+    return _with_norm(what, device, gl._workspace(), out, stream, call)
 
 
 def grad_norm(grads, out=None, stream=None):
@@ -390,7 +409,7 @@ def clip_grads(grads, max_norm: float, eps: float = 1e-6, out=None, stream=None)
     for the GPU."""
     gl = GradList._of(grads)
     return _norm_call("clip_grads", gl, out, stream,
-                      lambda norm, ws, b, s: lib().rr_clip_grads(gl._ref, float(max_norm), float(eps), norm, ws, b, s))
+                      lambda norm, ws, b, s: lib().rr_clip_grads(gl._ref, max_norm, eps, norm, ws, b, s))
 
 
 def _id_set(tokens, what: str):
@@ -435,8 +454,14 @@ def embedding(tokens, tables, outs, scale: float = 1.0, stream=None) -> None:
     if wn != n or on != n or rows != T or od != D or odt != d or wdev != dev or odev != dev:
         raise ValueError("embedding: need one table [V, D] and one output [tokens, D] per rank, alike and on the "
                          "tokens' device")
-    with _on_device(dev):
-        check(lib().rr_embedding(ids, id_type, w, o, n, T, V, D, d, float(scale), _stream(stream, dev)), "embedding")
+    if not _in_place(stream, dev):
+        with _placed(stream, dev):
+            check(lib().rr_embedding(ids, id_type, w, o, n, T, V, D, d, scale, _current_stream(dev.index)), "embedding")
+        return
+    check(lib().rr_embedding(ids, id_type, w, o, n, T, V, D, d, scale, _current_stream(dev.index)), "embedding")
+
+
+_embed_bytes: dict = {}  # workspace bytes of embedding_grad by (ranks, tokens, rows, width)
 
 
 def embedding_grad(tokens, grad_out, grads, op="avg", scale: float = 1.0, accumulate: bool = False,
@@ -455,13 +480,26 @@ def embedding_grad(tokens, grad_out, grads, op="avg", scale: float = 1.0, accumu
     if gn != n or rows != T or wd != D or gdev != dev or wdev != dev:
         raise ValueError("embedding_grad: need one output gradient [tokens, D] per rank and table gradients [V, D], on "
                          "the tokens' device")
-    with _on_device(dev), _on_stream(stream, dev):
+    key = (n, T, V, D)
+    need = _embed_bytes.get(key)
+    if need is None:
         b = ctypes.c_size_t()
         check(lib().rr_embedding_grad_workspace(n, T, V, D, ctypes.byref(b)), "embedding_grad_workspace")
-        ws = torch.empty(max(b.value, 256), dtype=torch.uint8, device=dev)
-        check(lib().rr_embedding_grad(ids, id_type, g, n, T, V, D, d, _op(op), float(scale),
-                                      -1 if padding_idx is None else int(padding_idx), w, wn, wdt, int(bool(accumulate)),
-                                      ws.data_ptr(), ws.numel(), _stream(stream, dev)), "embedding_grad")
+        if len(_embed_bytes) >= 4096:  # token counts that change from call to call
+            _embed_bytes.clear()
+        need = _embed_bytes[key] = max(b.value, 256)
+
+    def call():
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        check(lib().rr_embedding_grad(ids, id_type, g, n, T, V, D, d, _op(op), scale,
+                                      -1 if padding_idx is None else padding_idx, w, wn, wdt, int(bool(accumulate)),
+                                      ws.data_ptr(), need, _current_stream(dev.index)), "embedding_grad")
+
+    if _in_place(stream, dev):
+        call()
+    else:
+        with _placed(stream, dev):
+            call()
 
 
 class BucketPlan:
@@ -580,27 +618,21 @@ class BucketPlan:
         already alike on every rank (rank 0's count: a ``GradList`` or one list
         per rank) to the norm and to the clipping.  Returns the norm before
         clipping as a float32 scalar on the device (``out`` where it is given)."""
-        import torch
-
         g, n, dev = self._grads(grads)
         rest = GradList._of(synced) if synced is not None else None
         if rest is not None and rest.device not in (None, dev):
             raise ValueError("the synced gradients must be on the gradients' device")
         count = self.num_buckets - first if count is None else count
         ref = rest._ref if rest is not None else None
-        with _on_device(dev), _on_stream(stream, dev):
-            norm = _norm_out(out, dev)
-            key = (first, count, n, rest._workspace() if rest is not None else 0)
-            need = self._clip_bytes.get(key)
-            if need is None:
-                b = ctypes.c_size_t()
-                check(lib().rr_clip_workspace(self._h, first, count, n, ref, ctypes.byref(b)), "clip_workspace")
-                need = self._clip_bytes[key] = b.value
-            ws = torch.empty(need, dtype=torch.uint8, device=dev)
-            check(lib().rr_bucket_allreduce_clip(self._h, first, count, g, n, _op(op), ref, float(max_norm), float(eps),
-                                                 norm.data_ptr(), ws.data_ptr(), need, _stream(stream, dev)),
-                  "bucket_allreduce_clip")
-        return norm
+        key = (first, count, n, rest._workspace() if rest is not None else 0)
+        need = self._clip_bytes.get(key)
+        if need is None:
+            b = ctypes.c_size_t()
+            check(lib().rr_clip_workspace(self._h, first, count, n, ref, ctypes.byref(b)), "clip_workspace")
+            need = self._clip_bytes[key] = b.value
+        return _with_norm("bucket_allreduce_clip", dev, need, out, stream,
+                          lambda norm, ws, size, s: lib().rr_bucket_allreduce_clip(
+                              self._h, first, count, g, n, _op(op), ref, max_norm, eps, norm, ws, size, s))
 
 
 class Reducer:

@@ -18,8 +18,9 @@ namespace rr {
 
 namespace {
 
+template <class Fold>
 struct ParkParams {
-    BucketFoldParams f;  // tile0 counts tiles of park_tile_elems
+    Fold f;              // BucketFoldParams or ParkSmallParams; tile0 counts tiles of park_tile_elems
     double* partial;     // one per tile
     unsigned int* waits; // as BulkParams (rr_bulk.cuh)
     uint32_t hold;
@@ -27,7 +28,8 @@ struct ParkParams {
     uint32_t tv;         // vectors per rank per tile
     uint32_t pad_;
 };
-static_assert(sizeof(ParkParams) <= 32764, "ParkParams too large");
+static_assert(sizeof(ParkParams<BucketFoldParams>) <= 32764, "ParkParams too large");
+static_assert(sizeof(ParkParams<ParkSmallParams>) <= 4064, "a small parameter block");
 
 template <class G>
 __device__ __forceinline__ void park_one(typename G::T* p0, typename G::T* p1, uint64_t e, float a)
@@ -53,14 +55,14 @@ __device__ __forceinline__ float fold_value(const InF& in, int n, uint64_t e, fl
 // Ranks whose copies of a tensor share a 16-byte phase: tiles staged by bulk
 // copies as in the fused bucket sync (rr_bucket.cu), the parked halves written
 // by bulk stores from slots 0 and 1.
-template <class G, int OP, int NS>
-__global__ void __launch_bounds__(kThreads) bucket_park_kernel(const __grid_constant__ ParkParams bp)
+template <class G, int OP, int NS, class Fold>
+__global__ void __launch_bounds__(kThreads) bucket_park_kernel(const __grid_constant__ ParkParams<Fold> bp)
 {
     using T = typename G::T;
     constexpr int L = G::L;
     constexpr bool kSplit = sizeof(T) == 2;
     pdl_begin();
-    const BucketFoldParams& p = bp.f;
+    const Fold& p = bp.f;
     const int n = NS > 0 ? NS : p.n;
     const uint32_t TV = NS > 0 ? bulk_smem<NS>() / (NS > 0 ? NS : 1) / 16 : bp.tv;
     extern __shared__ __align__(128) uint4 sm[];  // [n][TV]: slot j holds rank (c + j) mod N
@@ -167,13 +169,13 @@ __global__ void __launch_bounds__(kThreads) bucket_park_kernel(const __grid_cons
 }
 
 // Any ranks: element by element.
-template <class G, int OP>
-__global__ void __launch_bounds__(kThreads) bucket_park_any_kernel(const __grid_constant__ ParkParams bp)
+template <class G, int OP, class Fold>
+__global__ void __launch_bounds__(kThreads) bucket_park_any_kernel(const __grid_constant__ ParkParams<Fold> bp)
 {
     using T = typename G::T;
     __shared__ double sh[kThreads / 32];
     pdl_begin();
-    const BucketFoldParams& p = bp.f;
+    const Fold& p = bp.f;
     const int n = p.n;
     const uint64_t w = blockIdx.x;
     const int s = find_segment(p.tile0, p.nseg, w);
@@ -198,12 +200,12 @@ __global__ void __launch_bounds__(kThreads) bucket_park_any_kernel(const __grid_
     if (threadIdx.x == 0) bp.partial[w] = acc;
 }
 
-template <class G, int OP>
-cudaError_t park_typed(const ParkParams& bp, cudaStream_t s)
+template <class G, int OP, class Fold>
+cudaError_t park_sized(const ParkParams<Fold>& bp, cudaStream_t s)
 {
     const int n = bp.f.n;
     const unsigned work = (unsigned)bp.f.tile0[bp.f.nseg];
-    auto go = [&](void (*kernel)(ParkParams), uint32_t smem) {
+    auto go = [&](void (*kernel)(ParkParams<Fold>), uint32_t smem) {
         cudaLaunchAttribute attr{};
         attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr.val.programmaticStreamSerializationAllowed = 1;
@@ -217,14 +219,37 @@ cudaError_t park_typed(const ParkParams& bp, cudaStream_t s)
         const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, bp);
         return e != cudaSuccess ? e : cudaGetLastError();
     };
-    if (!bp.f.vec_ok || !bp.waits) return go(bucket_park_any_kernel<G, OP>, 0);
+    if (!bp.f.vec_ok || !bp.waits) return go(bucket_park_any_kernel<G, OP, Fold>, 0);
     switch (n) {
-    case 2: return go(bucket_park_kernel<G, OP, 2>, bulk_smem<2>());
-    case 4: return go(bucket_park_kernel<G, OP, 4>, bulk_smem<4>());
-    case 8: return go(bucket_park_kernel<G, OP, 8>, bulk_smem<8>());
-    case 16: return go(bucket_park_kernel<G, OP, 16>, bulk_smem<16>());
+    case 2: return go(bucket_park_kernel<G, OP, 2, Fold>, bulk_smem<2>());
+    case 4: return go(bucket_park_kernel<G, OP, 4, Fold>, bulk_smem<4>());
+    case 8: return go(bucket_park_kernel<G, OP, 8, Fold>, bulk_smem<8>());
+    case 16: return go(bucket_park_kernel<G, OP, 16, Fold>, bulk_smem<16>());
     }
-    return go(bucket_park_kernel<G, OP, 0>, bp.tv * 16u * (uint32_t)n);
+    return go(bucket_park_kernel<G, OP, 0, Fold>, bp.tv * 16u * (uint32_t)n);
+}
+
+template <class G, int OP>
+cudaError_t park_typed(const ParkParams<BucketFoldParams>& bp, int ntensors, cudaStream_t s)
+{
+    const BucketFoldParams& f = bp.f;
+    if (f.nseg > kParkSegsSmall || ntensors * f.n > kParkPtrsSmall) return park_sized<G, OP>(bp, s);
+    ParkParams<ParkSmallParams> q{};
+    for (int i = 0; i < ntensors * f.n; ++i) q.f.grad[i] = f.grad[i];
+    for (int i = 0; i < f.nseg; ++i) {
+        q.f.seg[i] = f.seg[i];
+        q.f.tile0[i + 1] = f.tile0[i + 1];
+    }
+    q.f.n = f.n;
+    q.f.nseg = f.nseg;
+    q.f.vec_ok = f.vec_ok;
+    q.f.divisor = f.divisor;
+    q.partial = bp.partial;
+    q.waits = bp.waits;
+    q.hold = bp.hold;
+    q.spin = bp.spin;
+    q.tv = bp.tv;
+    return park_sized<G, OP>(q, s);
 }
 
 }  // namespace
@@ -234,13 +259,14 @@ uint64_t park_tile_elems(int grad_dtype, int n)
     return (uint64_t)bulk_tile_vectors(n) * (grad_dtype == kF32 ? 4u : 8u);
 }
 
-cudaError_t launch_bucket_park(int grad_dtype, int op, const BucketFoldParams& p, double* partial, cudaStream_t s)
+cudaError_t launch_bucket_park(int grad_dtype, int op, const BucketFoldParams& p, int ntensors, double* partial,
+                               cudaStream_t s)
 {
     RankParams rp{};
     rp.waits = bulk_wait_counters();
     const BulkParams wait = bulk_params(rp);
     if (p.tile0[p.nseg] > kMaxGrid || p.n < 2) return cudaErrorInvalidValue;
-    ParkParams bp;
+    ParkParams<BucketFoldParams> bp;
     bp.f = p;
     bp.partial = partial;
     bp.waits = wait.waits;
@@ -250,9 +276,9 @@ cudaError_t launch_bucket_park(int grad_dtype, int op, const BucketFoldParams& p
     bp.pad_ = 0;
     const bool avg = op == kAvg;
     switch (grad_dtype) {
-    case kF32: return avg ? park_typed<F32T, kAvg>(bp, s) : park_typed<F32T, kSum>(bp, s);
-    case kBF16: return avg ? park_typed<BF16T, kAvg>(bp, s) : park_typed<BF16T, kSum>(bp, s);
-    case kF16: return avg ? park_typed<F16T, kAvg>(bp, s) : park_typed<F16T, kSum>(bp, s);
+    case kF32: return avg ? park_typed<F32T, kAvg>(bp, ntensors, s) : park_typed<F32T, kSum>(bp, ntensors, s);
+    case kBF16: return avg ? park_typed<BF16T, kAvg>(bp, ntensors, s) : park_typed<BF16T, kSum>(bp, ntensors, s);
+    case kF16: return avg ? park_typed<F16T, kAvg>(bp, ntensors, s) : park_typed<F16T, kSum>(bp, ntensors, s);
     }
     return cudaErrorInvalidValue;
 }

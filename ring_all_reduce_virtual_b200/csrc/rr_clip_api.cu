@@ -326,18 +326,12 @@ rr_status_t bucket_allreduce_clip(const rr_bucket_plan_t* plan, int b0, int nb, 
         if (synced->nranks != n) return fail(RR_ERR_INVALID_ARG, "the synced list has another number of ranks");
         list_bytes(synced, &R);
     }
-    if ((st = bucket_range_check(plan, b0, nb, grads, n, &t0, &nt)) != RR_OK) return st;
+    std::vector<Span> spans;
+    if ((st = bucket_range_spans(plan, b0, nb, grads, n, &t0, &nt, spans)) != RR_OK) return st;
     const rr_dtype_t d = (rr_dtype_t)plan->grad_dtype;
     const uint64_t es = esize(d);
-    std::vector<Span> spans;
     uint64_t total = 0;
     for (int t = t0; t < t0 + nt; ++t) total += plan->numel[t];
-    for (int r = 0; r < n; ++r)
-        for (int t = t0; t < t0 + nt; ++t)
-            if (plan->numel[t]) {
-                const uintptr_t g = (uintptr_t)grads[(size_t)r * plan->ntensors + t];
-                spans.push_back({g, g + plan->numel[t] * es, true});
-            }
     S = total * es;
     stats_begin(RR_ALGO_ONESHOT, n, S + R);
     if (synced) add_spans(synced, n, true, spans);
@@ -363,7 +357,7 @@ rr_status_t bucket_allreduce_clip(const rr_bucket_plan_t* plan, int b0, int nb, 
             for (int t = 0; t < ntens; ++t) v = v && same_phase(&p->grad[t * n], n);
             p->vec_ok = v;
             const cudaError_t e =
-                timed_launch([&] { return launch_bucket_park(d, op, *p, run.partial + run.count, stream); });
+                timed_launch([&] { return launch_bucket_park(d, op, *p, ntens, run.partial + run.count, stream); });
             if (e != cudaSuccess) return cuda_fail(e, "bucket all-reduce launch");
             t_stats.launches += 1;
             run.count += (int64_t)p->tile0[p->nseg];

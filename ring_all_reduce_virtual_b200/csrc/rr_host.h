@@ -232,12 +232,11 @@ cudaError_t timed_launch(F&& f)
     return e;
 }
 
-// Checks shared by the bucket calls; fills the bucket's tensor range.
-// Checks buckets [b0, b0 + nb) of a plan and the gradients they cover (every
-// rank's copy of every tensor in the range, pairwise disjoint); *t0 and *nt
-// are the range's first tensor and tensor count.
-inline rr_status_t bucket_range_check(const rr_bucket_plan_t* plan, int b0, int nb, const void* const* grads, int nranks,
-                               int* t0, int* nt)
+// Checks buckets [b0, b0 + nb) of a plan and the gradients they cover, whose
+// spans (every rank's copy of every tensor in the range) are added to
+// `spans`; *t0 and *nt are the range's first tensor and tensor count.
+inline rr_status_t bucket_range_spans(const rr_bucket_plan_t* plan, int b0, int nb, const void* const* grads, int nranks,
+                                      int* t0, int* nt, std::vector<Span>& spans)
 {
     if (!plan) return fail(RR_ERR_INVALID_ARG, "NULL plan");
     if (nranks < 1 || nranks > RR_MAX_RANKS) return fail(RR_ERR_INVALID_ARG, "nranks must be in 1..64");
@@ -247,7 +246,6 @@ inline rr_status_t bucket_range_check(const rr_bucket_plan_t* plan, int b0, int 
     *t0 = plan->first[b0];
     *nt = plan->first[b0 + nb - 1] + plan->count[b0 + nb - 1] - *t0;
     const uint64_t es = esize((rr_dtype_t)plan->grad_dtype);
-    std::vector<Span> spans;
     for (int r = 0; r < nranks; ++r)
         for (int t = *t0; t < *t0 + *nt; ++t) {
             const void* g = grads[(size_t)r * plan->ntensors + t];
@@ -255,7 +253,16 @@ inline rr_status_t bucket_range_check(const rr_bucket_plan_t* plan, int b0, int 
             if ((uintptr_t)g % es != 0) return fail(RR_ERR_INVALID_ARG, "gradient not aligned to its element size");
             spans.push_back({(uintptr_t)g, (uintptr_t)g + plan->numel[t] * es, true});
         }
-    return check_spans(spans);
+    return RR_OK;
+}
+
+// The same for a call without other buffers: the gradients pairwise disjoint.
+inline rr_status_t bucket_range_check(const rr_bucket_plan_t* plan, int b0, int nb, const void* const* grads, int nranks,
+                                      int* t0, int* nt)
+{
+    std::vector<Span> spans;
+    const rr_status_t st = bucket_range_spans(plan, b0, nb, grads, nranks, t0, nt, spans);
+    return st != RR_OK ? st : check_spans(spans);
 }
 
 // The segments of a fused sync of buckets [b0, b0 + nb) as launch tables:

@@ -117,7 +117,7 @@ struct BucketFoldParams {
 // a small table keeps the parameter block of a short list small.
 constexpr int kNormCtas = 592;        // CTAs of a norm launch: 4 on each of 148 SMs
 constexpr int kNormTensors = 1024;    // tensors per launch
-constexpr int kNormTensorsSmall = 64;
+constexpr int kNormTensorsSmall = 160;  // a parameter block below 4 KB: larger ones cost the host 3-5 us per launch
 template <int CAP>
 struct NormParamsT {
     const void* ptr[CAP];
@@ -191,6 +191,20 @@ struct EmbedGradParams {
     int passes, bits;        // of the sort: digits, and bits per digit
     uint32_t ntiles;
     uint32_t K, nblk, Dp;    // sorted positions per block, blocks, padded row width
+};
+
+// The clipped sync's first pass over a short range: BucketFoldParams with a
+// parameter block below 4 KB.
+constexpr int kParkPtrsSmall = 256;
+constexpr int kParkSegsSmall = 48;
+struct ParkSmallParams {
+    void* grad[kParkPtrsSmall];
+    BucketSeg seg[kParkSegsSmall];
+    uint64_t tile0[kParkSegsSmall + 1];
+    int n;
+    int nseg;
+    int vec_ok;
+    float divisor;
 };
 
 enum DType : int { kF32 = 0, kBF16 = 1, kI32 = 2, kF16 = 3 };
@@ -273,7 +287,8 @@ constexpr int kJoinCtas = 128;        // partials that launch_norm_join leaves
 constexpr int kMaxPartials = 2048;    // partials that a launch sums itself
 // The clipped sync's first pass: fold, park the sums, one partial per tile.
 uint64_t park_tile_elems(int grad_dtype, int n);
-cudaError_t launch_bucket_park(int grad_dtype, int op, const BucketFoldParams& p, double* partial, cudaStream_t s);
+cudaError_t launch_bucket_park(int grad_dtype, int op, const BucketFoldParams& p, int ntensors, double* partial,
+                               cudaStream_t s);
 
 // Embedding.  vec: elements per access, which divides the row width and
 // suits every address; out_dtype: the gradient's type, dtype or fp32.
