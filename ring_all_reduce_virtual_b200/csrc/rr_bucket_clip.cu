@@ -1,16 +1,21 @@
-// rr_bucket_clip.cu -- the first pass of the bucket sync with clipping: every
-// rank's gradients are read once and folded in fp32 in ring order (AVG
-// divided), as in the fused bucket sync, but the result waits for the global
-// norm, so it is parked instead of written to every rank: an fp32 sum whole in
-// rank 0's buffer, for 16-bit gradients its upper half in rank 0's buffer and
-// its lower half in rank 1's -- the same elements the CTA has just read, so no
-// memory beside the gradients is needed and the final value is rounded once.
-// Each tile leaves one fp64 partial sum of squares.
+// rr_bucket_clip.cu -- the passes of the bucket sync with clipping.  Every
+// pass reads every rank's gradients and folds them in fp32 in ring order (AVG
+// divided), as the fused bucket sync does; the result a cannot be written
+// before the global norm is known.  Two ways:
 //
-// Traffic of the whole call for N ranks of S elements of e bytes: N S e read
-// and S e written here (2 S e for 16-bit types), then S e (2 S e) read and N S e
-// written by the scaling pass: 2 (N + 1) S e, or 2 (N + 2) S e for 16-bit types,
-// where a sync, a norm and a scaling one after the other move (4 N + 1) S e.
+//   parked      the first pass parks a: an fp32 sum whole in rank 0's buffer,
+//               for 16-bit gradients its upper half in rank 0's buffer and its
+//               lower half in rank 1's -- the same elements the CTA has just
+//               read, so no memory beside the gradients is needed and the
+//               final value is rounded once; the scaling (rr_clip.cu) reads
+//               the halves and writes every rank.  Traffic for N ranks of S
+//               elements of e bytes: 2 (N + 1) S e, 16-bit types 2 (N + 2) S e.
+//   folded      the first pass only sums the squares, the second folds again
+//   twice       and writes round(c a) to every rank: 3 N S e, of which the
+//               second reading hits L2 for what the first touched last.
+//
+// A sync, a norm and a scaling one after the other move (4 N + 1) S e.  Each
+// tile of a first pass leaves one fp64 partial sum of squares.
 #include "rr_bulk.cuh"
 #include "rr_clip.cuh"
 
@@ -18,10 +23,19 @@ namespace rr {
 
 namespace {
 
+// Bytes of shared memory per CTA: the tiles of all ranks.  Measured against
+// 16, 24 and 40 KB: 144 MB of 3 / 5 / 8 bf16 ranks 85.6 / 78.1 / 66.1 us with 16 KB,
+// 76.3 / 68.2 / 60.9 with 32 KB (fewer, longer CTAs: short sets are bound by a
+// CTA's latency), 40 KB as 32; 1 GB of 8 ranks 393 and 388 us.
+constexpr uint32_t kParkBytes = 32768;
+
+enum FoldMode : int { kPark = 0, kSquares = 1, kScaled = 2 };
+
 template <class Fold>
 struct ParkParams {
     Fold f;              // BucketFoldParams or ParkSmallParams; tile0 counts tiles of park_tile_elems
-    double* partial;     // one per tile
+    double* partial;     // kPark, kSquares: one per tile
+    ClipArgs clip;       // kScaled: the coefficient, or the partial sums it comes from
     unsigned int* waits; // as BulkParams (rr_bulk.cuh)
     uint32_t hold;
     uint32_t spin;
@@ -52,10 +66,29 @@ __device__ __forceinline__ float fold_value(const InF& in, int n, uint64_t e, fl
     return finish<OP>(a, divisor);
 }
 
+// One element's result to where the pass puts it; its square.
+template <class G, int MODE, class OutF>
+__device__ __forceinline__ double settle_one(const OutF& out, int n, uint64_t e, float a, float c)
+{
+    if constexpr (MODE == kScaled) {
+        const float x = __fmul_rn(a, c);
+        for (int o = 0; o < n; ++o) G::st1(out(o) + e, x);
+        return 0.0;
+    } else {
+        if constexpr (MODE == kPark) park_one<G>(out(0), out(1), e, a);
+        const float x[1] = {a};
+        return sum_squares(x);
+    }
+}
+
+// kScaled: the coefficient.
+__device__ __forceinline__ float pass_coef(const ClipArgs& a, double* sh) { return a.coef ? *a.coef : clip_coef(a, sh); }
+
 // Ranks whose copies of a tensor share a 16-byte phase: tiles staged by bulk
-// copies as in the fused bucket sync (rr_bucket.cu), the parked halves written
-// by bulk stores from slots 0 and 1.
-template <class G, int OP, int NS, class Fold>
+// copies as in the fused bucket sync (rr_bucket.cu); results leave by bulk
+// stores from slot 0, parked lower halves from slot 1.  The second pass takes
+// the tiles from the last to the first: L2 still holds what was touched last.
+template <class G, int OP, int NS, int MODE, class Fold>
 __global__ void __launch_bounds__(kThreads) bucket_park_kernel(const __grid_constant__ ParkParams<Fold> bp)
 {
     using T = typename G::T;
@@ -64,12 +97,13 @@ __global__ void __launch_bounds__(kThreads) bucket_park_kernel(const __grid_cons
     pdl_begin();
     const Fold& p = bp.f;
     const int n = NS > 0 ? NS : p.n;
-    const uint32_t TV = NS > 0 ? bulk_smem<NS>() / (NS > 0 ? NS : 1) / 16 : bp.tv;
+    const uint32_t TV = NS > 0 ? kParkBytes / (NS > 0 ? NS : 1) / 16 : bp.tv;
     extern __shared__ __align__(128) uint4 sm[];  // [n][TV]: slot j holds rank (c + j) mod N
     __shared__ __align__(8) uint64_t bar;
     __shared__ double sh[kThreads / 32];
 
-    const uint64_t w = blockIdx.x;
+    const float c = MODE == kScaled ? pass_coef(bp.clip, sh) : 1.0f;
+    const uint64_t w = MODE == kScaled ? p.tile0[p.nseg] - 1 - blockIdx.x : blockIdx.x;
     const int s = find_segment(p.tile0, p.nseg, w);
     const uint64_t tile = w - p.tile0[s];
     const BucketSeg& sg = p.seg[s];
@@ -80,19 +114,16 @@ __global__ void __launch_bounds__(kThreads) bucket_park_kernel(const __grid_cons
         if (r >= n) r -= n;
         return static_cast<const T*>(p.grad[base + r]) + sg.off;
     };
-    T* const p0 = static_cast<T*>(p.grad[base]) + sg.off;
-    T* const p1 = static_cast<T*>(p.grad[base + 1]) + sg.off;
+    auto out = [&](int o) { return static_cast<T*>(p.grad[base + o]) + sg.off; };
     const uint64_t len = sg.len;
-    uint64_t head = (uint64_t)((L - phase_of(p0, L)) & (L - 1));
+    uint64_t head = (uint64_t)((L - phase_of(in(0), L)) & (L - 1));
     if (head > len) head = len;
     const uint64_t nv = (len - head) / L;
     const uint64_t tail = len - head - nv * L;
     double acc = 0.0;
     if (tile == 0 && (uint64_t)threadIdx.x < head + tail) {
         const uint64_t e = (uint64_t)threadIdx.x < head ? (uint64_t)threadIdx.x : head + nv * L + (threadIdx.x - head);
-        const float x[1] = {fold_value<G, OP>(in, n, e, p.divisor)};
-        park_one<G>(p0, p1, e, x[0]);
-        acc = sum_squares(x);
+        acc = settle_one<G, MODE>(out, n, e, fold_value<G, OP>(in, n, e, p.divisor), c);
     }
     const uint64_t v0 = tile * TV;
     if (v0 < nv) {
@@ -114,7 +145,7 @@ __global__ void __launch_bounds__(kThreads) bucket_park_kernel(const __grid_cons
         }
         if (!bulk_tile_landed(b, bp.waits, bp.hold, bp.spin)) {
             // the whole CTA skips the tile: a NaN norm says that the step is lost
-            if (threadIdx.x == 0) bp.partial[w] = __longlong_as_double(0x7ff8000000000000ll);
+            if (MODE != kScaled && threadIdx.x == 0) bp.partial[w] = __longlong_as_double(0x7ff8000000000000ll);
             return;
         }
         for (uint32_t v = threadIdx.x; v < nvt; v += kThreads) {
@@ -129,7 +160,14 @@ __global__ void __launch_bounds__(kThreads) bucket_park_kernel(const __grid_cons
             }
 #pragma unroll
             for (int l = 0; l < L; ++l) a[l] = finish_n<OP, NS>(a[l], p.divisor);
+            if constexpr (MODE == kScaled) {
+#pragma unroll
+                for (int l = 0; l < L; ++l) a[l] = __fmul_rn(a[l], c);
+                sm[v] = G::pack(a);
+                continue;
+            }
             acc += sum_squares(a);
+            if constexpr (MODE == kSquares) continue;
             if constexpr (kSplit) {
                 uint32_t h[4], q[4];
 #pragma unroll
@@ -144,32 +182,34 @@ __global__ void __launch_bounds__(kThreads) bucket_park_kernel(const __grid_cons
                 sm[v] = G::pack(a);
             }
         }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;"
-                         ::"l"(p0 + e0), "r"(bulk_smem_addr(sm)), "r"(bytes)
-                         : "memory");
-            if constexpr (kSplit)
-                asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;"
-                             ::"l"(p1 + e0), "r"(bulk_smem_addr(sm + TV)), "r"(bytes)
-                             : "memory");
-            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        if constexpr (MODE != kSquares) {
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                const int nout = MODE == kScaled ? n : kSplit ? 2 : 1;
+                for (int o = 0; o < nout; ++o)
+                    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;"
+                                 ::"l"(out(o) + e0), "r"(bulk_smem_addr(sm + (MODE == kPark ? o * TV : 0))), "r"(bytes)
+                                 : "memory");
+                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
         }
-        acc = cta_sum(acc, sh);
+        if constexpr (MODE != kScaled) acc = cta_sum(acc, sh);
         if (threadIdx.x == 0) {
-            bp.partial[w] = acc;
-            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            if constexpr (MODE != kScaled) bp.partial[w] = acc;
+            if constexpr (MODE != kSquares) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
             bulk_bar_inval(b);
         }
         return;
     }
-    acc = cta_sum(acc, sh);
-    if (threadIdx.x == 0) bp.partial[w] = acc;
+    if constexpr (MODE != kScaled) {
+        acc = cta_sum(acc, sh);
+        if (threadIdx.x == 0) bp.partial[w] = acc;
+    }
 }
 
 // Any ranks: element by element.
-template <class G, int OP, class Fold>
+template <class G, int OP, int MODE, class Fold>
 __global__ void __launch_bounds__(kThreads) bucket_park_any_kernel(const __grid_constant__ ParkParams<Fold> bp)
 {
     using T = typename G::T;
@@ -177,7 +217,8 @@ __global__ void __launch_bounds__(kThreads) bucket_park_any_kernel(const __grid_
     pdl_begin();
     const Fold& p = bp.f;
     const int n = p.n;
-    const uint64_t w = blockIdx.x;
+    const float c = MODE == kScaled ? pass_coef(bp.clip, sh) : 1.0f;
+    const uint64_t w = MODE == kScaled ? p.tile0[p.nseg] - 1 - blockIdx.x : blockIdx.x;
     const int s = find_segment(p.tile0, p.nseg, w);
     const BucketSeg& sg = p.seg[s];
     const int base = (int)sg.t * n, start = (int)sg.c;
@@ -186,21 +227,20 @@ __global__ void __launch_bounds__(kThreads) bucket_park_any_kernel(const __grid_
         if (r >= n) r -= n;
         return static_cast<const T*>(p.grad[base + r]) + sg.off;
     };
-    T* const p0 = static_cast<T*>(p.grad[base]) + sg.off;
-    T* const p1 = static_cast<T*>(p.grad[base + 1]) + sg.off;
+    auto out = [&](int o) { return static_cast<T*>(p.grad[base + o]) + sg.off; };
     const uint64_t te = (uint64_t)bp.tv * G::L, lo = (w - p.tile0[s]) * te;
     const uint64_t hi = sg.len < lo + te ? sg.len : lo + te;
     double acc = 0.0;
     for (uint64_t e = lo + threadIdx.x; e < hi; e += kThreads) {
-        const float x[1] = {fold_value<G, OP>(in, n, e, p.divisor)};
-        park_one<G>(p0, p1, e, x[0]);
-        acc += sum_squares(x);
+        acc += settle_one<G, MODE>(out, n, e, fold_value<G, OP>(in, n, e, p.divisor), c);
     }
-    acc = cta_sum(acc, sh);
-    if (threadIdx.x == 0) bp.partial[w] = acc;
+    if constexpr (MODE != kScaled) {
+        acc = cta_sum(acc, sh);
+        if (threadIdx.x == 0) bp.partial[w] = acc;
+    }
 }
 
-template <class G, int OP, class Fold>
+template <class G, int OP, int MODE, class Fold>
 cudaError_t park_sized(const ParkParams<Fold>& bp, cudaStream_t s)
 {
     const int n = bp.f.n;
@@ -219,21 +259,30 @@ cudaError_t park_sized(const ParkParams<Fold>& bp, cudaStream_t s)
         const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, bp);
         return e != cudaSuccess ? e : cudaGetLastError();
     };
-    if (!bp.f.vec_ok || !bp.waits) return go(bucket_park_any_kernel<G, OP, Fold>, 0);
-    switch (n) {
-    case 2: return go(bucket_park_kernel<G, OP, 2, Fold>, bulk_smem<2>());
-    case 4: return go(bucket_park_kernel<G, OP, 4, Fold>, bulk_smem<4>());
-    case 8: return go(bucket_park_kernel<G, OP, 8, Fold>, bulk_smem<8>());
-    case 16: return go(bucket_park_kernel<G, OP, 16, Fold>, bulk_smem<16>());
+    if (!bp.f.vec_ok || !bp.waits) return go(bucket_park_any_kernel<G, OP, MODE, Fold>, 0);
+    // compiled rank counts of the calls that get here (clip_folds_twice)
+    if constexpr (MODE != kPark) {
+        if (n == 2) return go(bucket_park_kernel<G, OP, 2, MODE, Fold>, kParkBytes);
+        if (n == 3) return go(bucket_park_kernel<G, OP, 3, MODE, Fold>, bp.tv * 16u * 3u);
+        return cudaErrorInvalidValue;
+    } else {
+        switch (n) {
+        case 2:
+            if constexpr (sizeof(typename G::T) == 4) return go(bucket_park_kernel<G, OP, 2, MODE, Fold>, kParkBytes);
+            break;
+        case 4: return go(bucket_park_kernel<G, OP, 4, MODE, Fold>, kParkBytes);
+        case 8: return go(bucket_park_kernel<G, OP, 8, MODE, Fold>, kParkBytes);
+        case 16: return go(bucket_park_kernel<G, OP, 16, MODE, Fold>, kParkBytes);
+        }
+        return go(bucket_park_kernel<G, OP, 0, MODE, Fold>, bp.tv * 16u * (uint32_t)n);
     }
-    return go(bucket_park_kernel<G, OP, 0, Fold>, bp.tv * 16u * (uint32_t)n);
 }
 
-template <class G, int OP>
+template <class G, int OP, int MODE>
 cudaError_t park_typed(const ParkParams<BucketFoldParams>& bp, int ntensors, cudaStream_t s)
 {
     const BucketFoldParams& f = bp.f;
-    if (f.nseg > kParkSegsSmall || ntensors * f.n > kParkPtrsSmall) return park_sized<G, OP>(bp, s);
+    if (f.nseg > kParkSegsSmall || ntensors * f.n > kParkPtrsSmall) return park_sized<G, OP, MODE>(bp, s);
     ParkParams<ParkSmallParams> q{};
     for (int i = 0; i < ntensors * f.n; ++i) q.f.grad[i] = f.grad[i];
     for (int i = 0; i < f.nseg; ++i) {
@@ -245,22 +294,26 @@ cudaError_t park_typed(const ParkParams<BucketFoldParams>& bp, int ntensors, cud
     q.f.vec_ok = f.vec_ok;
     q.f.divisor = f.divisor;
     q.partial = bp.partial;
+    q.clip = bp.clip;
     q.waits = bp.waits;
     q.hold = bp.hold;
     q.spin = bp.spin;
     q.tv = bp.tv;
-    return park_sized<G, OP>(q, s);
+    return park_sized<G, OP, MODE>(q, s);
 }
 
 }  // namespace
 
 uint64_t park_tile_elems(int grad_dtype, int n)
 {
-    return (uint64_t)bulk_tile_vectors(n) * (grad_dtype == kF32 ? 4u : 8u);
+    return (uint64_t)(kParkBytes / (uint32_t)n / 16u) * (grad_dtype == kF32 ? 4u : 8u);
 }
 
-cudaError_t launch_bucket_park(int grad_dtype, int op, const BucketFoldParams& p, int ntensors, double* partial,
-                               cudaStream_t s)
+bool clip_folds_twice(int n, int grad_dtype) { return n <= 3 && grad_dtype != kF32; }
+
+template <int MODE>
+static cudaError_t launch_pass(int grad_dtype, int op, const BucketFoldParams& p, int ntensors, double* partial,
+                               const ClipArgs* clip, cudaStream_t s)
 {
     RankParams rp{};
     rp.waits = bulk_wait_counters();
@@ -269,18 +322,39 @@ cudaError_t launch_bucket_park(int grad_dtype, int op, const BucketFoldParams& p
     ParkParams<BucketFoldParams> bp;
     bp.f = p;
     bp.partial = partial;
+    bp.clip = clip ? *clip : ClipArgs{};
     bp.waits = wait.waits;
     bp.hold = wait.hold;
     bp.spin = wait.spin;
-    bp.tv = bulk_tile_vectors(p.n);
+    bp.tv = kParkBytes / (uint32_t)p.n / 16u;
     bp.pad_ = 0;
     const bool avg = op == kAvg;
     switch (grad_dtype) {
-    case kF32: return avg ? park_typed<F32T, kAvg>(bp, ntensors, s) : park_typed<F32T, kSum>(bp, ntensors, s);
-    case kBF16: return avg ? park_typed<BF16T, kAvg>(bp, ntensors, s) : park_typed<BF16T, kSum>(bp, ntensors, s);
-    case kF16: return avg ? park_typed<F16T, kAvg>(bp, ntensors, s) : park_typed<F16T, kSum>(bp, ntensors, s);
+    case kF32:
+        if constexpr (MODE != kPark) return cudaErrorInvalidValue;  // fp32 is parked
+        else return avg ? park_typed<F32T, kAvg, MODE>(bp, ntensors, s) : park_typed<F32T, kSum, MODE>(bp, ntensors, s);
+    case kBF16: return avg ? park_typed<BF16T, kAvg, MODE>(bp, ntensors, s) : park_typed<BF16T, kSum, MODE>(bp, ntensors, s);
+    case kF16: return avg ? park_typed<F16T, kAvg, MODE>(bp, ntensors, s) : park_typed<F16T, kSum, MODE>(bp, ntensors, s);
     }
     return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_bucket_park(int grad_dtype, int op, const BucketFoldParams& p, int ntensors, double* partial,
+                               cudaStream_t s)
+{
+    return launch_pass<kPark>(grad_dtype, op, p, ntensors, partial, nullptr, s);
+}
+
+cudaError_t launch_bucket_squares(int grad_dtype, int op, const BucketFoldParams& p, int ntensors, double* partial,
+                                  cudaStream_t s)
+{
+    return launch_pass<kSquares>(grad_dtype, op, p, ntensors, partial, nullptr, s);
+}
+
+cudaError_t launch_bucket_scaled(int grad_dtype, int op, const BucketFoldParams& p, int ntensors, const ClipArgs& clip,
+                                 cudaStream_t s)
+{
+    return launch_pass<kScaled>(grad_dtype, op, p, ntensors, nullptr, &clip, s);
 }
 
 }  // namespace rr

@@ -343,11 +343,11 @@ rr_status_t bucket_allreduce_clip(const rr_bucket_plan_t* plan, int b0, int nb, 
     a.eps = eps;
     a.norm = norm;
     const RangeList own(plan, t0, nt, grads);
-    if (n == 1) {
-        st = run.norm(&own.list);  // one rank: nothing to fold
-    } else {
-        auto p = std::make_unique<BucketFoldParams>();
-        st = for_each_fold_launch(plan, b0, nb, grads, n, *p, [&](int ntens) -> rr_status_t {
+    const bool twice = n > 1 && clip_folds_twice(n, d);
+    // the range's launches, a pass at a time
+    auto p = std::make_unique<BucketFoldParams>();
+    auto pass = [&](auto&& launch) {
+        return for_each_fold_launch(plan, b0, nb, grads, n, *p, [&](int ntens) -> rr_status_t {
             const uint64_t te = park_tile_elems(d, n);
             p->tile0[0] = 0;
             for (int s = 0; s < p->nseg; ++s) p->tile0[s + 1] = p->tile0[s] + ceil_div(p->seg[s].len, te);
@@ -356,20 +356,35 @@ rr_status_t bucket_allreduce_clip(const rr_bucket_plan_t* plan, int b0, int nb, 
             bool v = true;
             for (int t = 0; t < ntens; ++t) v = v && same_phase(&p->grad[t * n], n);
             p->vec_ok = v;
-            const cudaError_t e =
-                timed_launch([&] { return launch_bucket_park(d, op, *p, ntens, run.partial + run.count, stream); });
+            const cudaError_t e = timed_launch([&] { return launch(ntens); });
             if (e != cudaSuccess) return cuda_fail(e, "bucket all-reduce launch");
             t_stats.launches += 1;
-            run.count += (int64_t)p->tile0[p->nseg];
             return RR_OK;
+        });
+    };
+    if (n == 1) {
+        st = run.norm(&own.list);  // one rank: nothing to fold
+    } else {
+        st = pass([&](int ntens) {
+            double* slots = run.partial + run.count;
+            run.count += (int64_t)p->tile0[p->nseg];
+            return twice ? launch_bucket_squares(d, op, *p, ntens, slots, stream)
+                         : launch_bucket_park(d, op, *p, ntens, slots, stream);
         });
     }
     if (st != RR_OK) return st;
     if (synced && (st = run.norm(synced)) != RR_OK) return st;
     if ((st = run.join(&a)) != RR_OK) return st;
-    st = run.scale(
-        d, n > 1, n, nt, [&](int t, int r) { return grads[(size_t)r * plan->ntensors + t0 + t]; },
-        [&](int t) { return plan->numel[t0 + t]; }, a);
+    if (twice)
+        st = pass([&](int ntens) {
+            const ClipArgs now = a;
+            a.norm = nullptr;
+            return launch_bucket_scaled(d, op, *p, ntens, now, stream);
+        });
+    else
+        st = run.scale(
+            d, n > 1, n, nt, [&](int t, int r) { return grads[(size_t)r * plan->ntensors + t0 + t]; },
+            [&](int t) { return plan->numel[t0 + t]; }, a);
     if (st != RR_OK) return st;
     if (synced && (st = run.scale_list(synced, a)) != RR_OK) return st;
     if (a.norm && (st = run.finish(a)) != RR_OK) return st;
@@ -377,7 +392,7 @@ rr_status_t bucket_allreduce_clip(const rr_bucket_plan_t* plan, int b0, int nb, 
     t_stats.bytes_sent_max = (uint64_t)(n - 1) * (S + R);
     t_stats.bytes_sent_total = (uint64_t)n * (uint64_t)(n - 1) * S + (uint64_t)(n - 1) * R;
     const uint64_t parked = d == RR_F32 || n == 1 ? S : 2 * S;
-    t_stats.hbm_bytes = n == 1 ? 3 * S : 2 * (uint64_t)n * S + 2 * parked;
+    t_stats.hbm_bytes = n == 1 ? 3 * S : twice ? 3 * (uint64_t)n * S : 2 * (uint64_t)n * S + 2 * parked;
     t_stats.hbm_bytes += (uint64_t)(2 + n) * R;
     log_call("bucket_allreduce_clip", n, total, d, op, RR_ALGO_ONESHOT);
     return debug_check(st, stream);

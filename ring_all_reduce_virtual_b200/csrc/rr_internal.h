@@ -289,6 +289,14 @@ constexpr int kMaxPartials = 2048;    // partials that a launch sums itself
 uint64_t park_tile_elems(int grad_dtype, int n);
 cudaError_t launch_bucket_park(int grad_dtype, int op, const BucketFoldParams& p, int ntensors, double* partial,
                                cudaStream_t s);
+// The other way: a first pass that only sums the squares, and a second that
+// folds again and writes the scaled values to every rank; which one a call
+// takes.
+bool clip_folds_twice(int n, int grad_dtype);
+cudaError_t launch_bucket_squares(int grad_dtype, int op, const BucketFoldParams& p, int ntensors, double* partial,
+                                  cudaStream_t s);
+cudaError_t launch_bucket_scaled(int grad_dtype, int op, const BucketFoldParams& p, int ntensors, const ClipArgs& clip,
+                                 cudaStream_t s);
 
 // Embedding.  vec: elements per access, which divides the row width and
 // suits every address; out_dtype: the gradient's type, dtype or fp32.
