@@ -250,10 +250,14 @@ __global__ void __launch_bounds__(kThreads) clip_bulk_kernel(const __grid_consta
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();
     if (threadIdx.x == 0) {
-        for (int o = 0; o < n; ++o)
-            asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;"
-                         ::"l"(ptr[o] + e0), "r"(bulk_smem_addr(sm)), "r"(bytes)
-                         : "memory");
+        const uint64_t pol = evict_first_policy();
+        for (int o = 0; o < n; ++o) {
+            if (!PARKED && p.clip.in_l2) bulk_store_last(ptr[o] + e0, bulk_smem_addr(sm), bytes, pol);
+            else
+                asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;"
+                             ::"l"(ptr[o] + e0), "r"(bulk_smem_addr(sm)), "r"(bytes)
+                             : "memory");
+        }
         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
         asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
         bulk_bar_inval(b);

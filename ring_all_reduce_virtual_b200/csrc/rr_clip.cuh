@@ -25,6 +25,21 @@ __device__ __forceinline__ void pdl_begin()
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// Bulk store (a multiple of 16 bytes, shared to global, in the thread's bulk
+// group) of bytes that L2 should evict before those the pass will still read.
+__device__ __forceinline__ uint64_t evict_first_policy()
+{
+    uint64_t pol;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(pol));
+    return pol;
+}
+
+__device__ __forceinline__ void bulk_store_last(void* to, uint32_t from, uint32_t bytes, uint64_t pol)
+{
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group.L2::cache_hint [%0], [%1], %2, %3;"
+                 ::"l"(to), "r"(from), "r"(bytes), "l"(pol) : "memory");
+}
+
 // A sum of at most 64 squares in fp32 is taken as it is when it is finite and
 // at least 2^-96: a square lost below fp32's smallest normal number is below
 // 2^-126, so 64 of them are below 2^-120, 2^-24 of the sum.
@@ -109,14 +124,20 @@ __device__ __forceinline__ double partials_sum(const double* p, int64_t count, d
     return cta_sum(v, sh);
 }
 
-// The clipping's coefficient, 1 where the norm is within max_norm and
-// max_norm / (norm + eps) otherwise: 0 for an infinite norm, NaN for NaN.
-__device__ __forceinline__ float clip_coef(const ClipArgs& a, double* sh)
+// The clipping's coefficient for a sum of squares, 1 where the norm is within
+// max_norm and max_norm / (norm + eps) otherwise: 0 for an infinite norm, NaN
+// for NaN.  One thread writes the norm, where the launch is asked to.
+__device__ __forceinline__ float coef_of(const ClipArgs& a, double squares)
 {
-    const double norm = sqrt(partials_sum(a.partial, a.npartial, sh));
+    const double norm = sqrt(squares);
     if (a.norm && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = (float)norm;
     const double den = norm + (double)a.eps;
     return den <= (double)a.max_norm ? 1.0f : (float)((double)a.max_norm / den);
+}
+
+__device__ __forceinline__ float clip_coef(const ClipArgs& a, double* sh)
+{
+    return coef_of(a, partials_sum(a.partial, a.npartial, sh));
 }
 
 }  // namespace rr

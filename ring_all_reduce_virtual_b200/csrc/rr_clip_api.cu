@@ -69,6 +69,10 @@ rr_status_t check_clip(float max_norm, float eps)
     return RR_OK;
 }
 
+// Elements up to which a call tries the one launch of a small set (its
+// vectors have to fit the cluster's registers too).
+constexpr uint64_t kSmallElems = 8 * 1024 * 32;
+
 constexpr rr_dtype_t kGradTypes[] = {RR_F32, RR_BF16, RR_F16};
 
 // One call's passes: launches on its stream, and the fp64 partial sums they
@@ -178,6 +182,34 @@ struct Passes {
     }
 };
 
+// The first `ranks` ranks' tensors of a list in the one launch of a small set:
+// *done says whether it was one (tensors of one type, few enough).
+rr_status_t small_list(const rr_tensor_list_t* l, uint64_t total, int ranks, bool scale, const ClipArgs& a,
+                       cudaStream_t stream, bool* done)
+{
+    *done = false;
+    if (total == 0 || total > kSmallElems) return RR_OK;
+    ParkSmallParams p{};
+    p.n = ranks;
+    p.divisor = 1.0f;
+    rr_dtype_t d = RR_F32;
+    for (int t = 0; t < l->ntensors; ++t) {
+        if (l->numels[t] == 0) continue;
+        if (p.nseg > 0 && l->dtypes[t] != d) return RR_OK;
+        if (p.nseg == kParkSegsSmall || (p.nseg + 1) * ranks > kParkPtrsSmall) return RR_OK;
+        d = l->dtypes[t];
+        for (int r = 0; r < ranks; ++r) p.grad[p.nseg * ranks + r] = l->ptrs[(size_t)r * l->ntensors + t];
+        p.seg[p.nseg] = BucketSeg{(uint32_t)p.nseg, 0, 0, l->numels[t]};
+        ++p.nseg;
+    }
+    if (!clip_small_plan(d, p, p.nseg)) return RR_OK;
+    const cudaError_t e = timed_launch([&] { return launch_clip_small(d, scale, p, a, stream); });
+    if (e != cudaSuccess) return cuda_fail(e, "clip launch");
+    t_stats.launches += 1;
+    *done = true;
+    return RR_OK;
+}
+
 // Partial sums that the norm's launches over a list leave, at most.
 uint64_t norm_slots(const rr_tensor_list_t* l)
 {
@@ -274,7 +306,10 @@ rr_status_t grad_norm(const rr_tensor_list_t* grads, float* norm, void* ws, size
     Passes run{static_cast<double*>(ws), stream};
     ClipArgs a{};
     a.norm = norm;
-    if ((st = run.norm(grads)) != RR_OK || (st = run.join(&a)) != RR_OK || (st = run.finish(a)) != RR_OK) return st;
+    bool done = false;
+    if ((st = small_list(grads, total, 1, false, a, stream, &done)) != RR_OK) return st;
+    if (!done && ((st = run.norm(grads)) != RR_OK || (st = run.join(&a)) != RR_OK || (st = run.finish(a)) != RR_OK))
+        return st;
     t_stats.hbm_bytes = S;
     log_call("grad_norm", grads->nranks, total, RR_F32, RR_SUM, RR_ALGO_ONESHOT);
     return debug_check(st, stream);
@@ -296,16 +331,21 @@ rr_status_t clip_grads(const rr_tensor_list_t* grads, float max_norm, float eps,
     if ((st = check_device_ptrs(grads->ptrs, n * grads->ntensors)) != RR_OK) return st;
     Passes run{static_cast<double*>(ws), stream, n * S >= kBulkClipBytes};
     ClipArgs a{};
+    a.in_l2 = S <= kKeepBytes;
     a.max_norm = max_norm;
     a.eps = eps;
     a.norm = norm;
-    if ((st = run.norm(grads)) != RR_OK || (st = run.join(&a)) != RR_OK) return st;
-    if ((st = run.scale_list(grads, a)) != RR_OK) return st;
-    if (a.norm && (st = run.finish(a)) != RR_OK) return st;  // nothing to scale: the norm alone
+    bool done = false;
+    if ((st = small_list(grads, total, n, true, a, stream, &done)) != RR_OK) return st;
+    if (!done) {
+        if ((st = run.norm(grads)) != RR_OK || (st = run.join(&a)) != RR_OK) return st;
+        if ((st = run.scale_list(grads, a)) != RR_OK) return st;
+        if (a.norm && (st = run.finish(a)) != RR_OK) return st;  // nothing to scale: the norm alone
+    }
     t_stats.steps = n > 1 ? 1 : 0;
     t_stats.bytes_sent_max = (uint64_t)(n - 1) * S;  // rank 0 sends its copy to every other
     t_stats.bytes_sent_total = t_stats.bytes_sent_max;
-    t_stats.hbm_bytes = (uint64_t)(2 + n) * S;
+    t_stats.hbm_bytes = (uint64_t)((done ? 1 : 2) + n) * S;
     log_call("clip_grads", n, total, RR_F32, RR_SUM, RR_ALGO_ONESHOT);
     return debug_check(st, stream);
 }

@@ -134,7 +134,7 @@ using NormParams = NormParamsT<kNormTensors>;
 struct ClipArgs {
     const double* partial;
     int npartial;
-    int pad_;
+    int in_l2;    // the set is small enough for L2 to hold much of it between the passes
     float max_norm;
     float eps;
     float* norm;  // where the launch writes the norm (NULL: it does not)
@@ -279,16 +279,25 @@ cudaError_t launch_norm(int dtype, const NormParams& p, int* slots, cudaStream_t
 cudaError_t launch_norm_join(const double* in, int64_t count, double* out, int* slots, cudaStream_t s);
 cudaError_t launch_norm_finish(const ClipArgs& a, cudaStream_t s);
 cudaError_t launch_clip_scale(int dtype, bool parked, bool bulk, const ScaleParams& p, cudaStream_t s);
-#ifndef RR_BULK_CLIP
-#define RR_BULK_CLIP (32ull << 20)
-#endif
-constexpr uint64_t kBulkClipBytes = RR_BULK_CLIP;  // bytes written from which the scaling runs by bulk copies
+// Bytes written from which the scaling runs by bulk copies: 4 x 104 MB 117 us by
+// the threads, 105 by bulk copies; 8 x 666 MB 1984 and 1816; below, the bulk
+// form's launch for the coefficient costs what its copies gain (50 MB: 26.4
+// and 26.6).
+constexpr uint64_t kBulkClipBytes = 32ull << 20;
+// One rank's bytes up to which the scaling stores with an evict-first hint, so
+// that the values the norm left in L2 are read there: 4 x 104 MB 104.6 -> 99.9
+// us; above L2's 126 MB the hint costs (8 x 666 MB: 1773 -> 1794).
+constexpr uint64_t kKeepBytes = 126ull << 20;
 constexpr int kJoinCtas = 128;        // partials that launch_norm_join leaves
 constexpr int kMaxPartials = 2048;    // partials that a launch sums itself
 // The clipped sync's first pass: fold, park the sums, one partial per tile.
 uint64_t park_tile_elems(int grad_dtype, int n);
 cudaError_t launch_bucket_park(int grad_dtype, int op, const BucketFoldParams& p, int ntensors, double* partial,
                                cudaStream_t s);
+// Norm (scale false) or clipping of a small set in one launch: whether it is
+// one (the tensors' prefix sums are filled in), and the launch.
+bool clip_small_plan(int dtype, ParkSmallParams& p, int ntensors);
+cudaError_t launch_clip_small(int dtype, bool scale, const ParkSmallParams& f, const ClipArgs& clip, cudaStream_t s);
 // The other way: a first pass that only sums the squares, and a second that
 // folds again and writes the scaled values to every rank; which one a call
 // takes.

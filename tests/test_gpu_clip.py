@@ -123,8 +123,8 @@ def test_norm_counts_repeated_tensors():
 @pytest.mark.parametrize("dtype", list(DT))
 @pytest.mark.parametrize("n", [1, 2, 5])
 @pytest.mark.parametrize("layout", ["aligned", "same", "mixed"])
-def test_clip_scales_rank_0s_copy_into_every_rank(dtype, n, layout):
-    sizes = [1, 40003, 8, 0, 5000]
+@pytest.mark.parametrize("sizes", [[1, 40003, 8, 0, 5000], [260_000, 3, 2100], [1, 40003, 8, 0, 300_011], [5] * 49])
+def test_clip_scales_rank_0s_copy_into_every_rank(dtype, n, layout, sizes):
     off = {"aligned": lambda r, t: 0, "same": lambda r, t: 3 * t + 1, "mixed": lambda r, t: r + t}[layout]
     ranks = [[Guarded(values(100 * r + t, m, DT[dtype], 0.1), off(r, t)) for t, m in enumerate(sizes)] for r in range(n)]
     src = [g.t.clone() for g in ranks[0]]
@@ -186,7 +186,8 @@ def test_clip_offsets_past_32_bits():
 
 # ------------------------------------------------------ the clipped bucket sync
 
-SIZES = [100, 5000, 3, 777, 40001, 1, 16, 0, 9000]
+SIZES = [100, 5000, 3, 777, 40001, 1, 16, 0, 9000]  # a small set: one launch where the phases allow it
+MORE = SIZES + [300_007]  # above what one launch holds
 
 
 def rank_grads(n, sizes, dtype, std=0.1, off=lambda r, t: 0):
@@ -203,10 +204,11 @@ LAYOUTS = {"aligned": lambda r, t: 0, "same": lambda r, t: t % 8, "mixed": lambd
 @pytest.mark.parametrize("n", [1, 2, 3, 4, 8, 16, 24])
 @pytest.mark.parametrize("dtype", list(DT))
 @pytest.mark.parametrize("op", ["avg", "sum"])
-def test_clipped_sync_without_a_limit_has_the_syncs_bits(n, dtype, op):
+@pytest.mark.parametrize("sizes", [SIZES, MORE])
+def test_clipped_sync_without_a_limit_has_the_syncs_bits(n, dtype, op, sizes):
     for layout, off in LAYOUTS.items():
-        a, b = rank_grads(n, SIZES, DT[dtype], off=off), rank_grads(n, SIZES, DT[dtype], off=off)
-        plan = rrv.BucketPlan(SIZES, dtype, 16384)
+        a, b = rank_grads(n, sizes, DT[dtype], off=off), rank_grads(n, sizes, DT[dtype], off=off)
+        plan = rrv.BucketPlan(sizes, dtype, 16384)
         plan.all_reduce_range(0, plan.num_buckets, tensors(a), op)
         plan.all_reduce_clip(tensors(b), math.inf, op)
         for r in range(n):
@@ -219,17 +221,19 @@ def test_clipped_sync_without_a_limit_has_the_syncs_bits(n, dtype, op):
 @pytest.mark.parametrize("n", [1, 2, 3, 8, 13])
 @pytest.mark.parametrize("dtype", list(DT))
 @pytest.mark.parametrize("op", ["avg", "sum"])
-def test_clipped_sync_against_64_bits(n, dtype, op):
+@pytest.mark.parametrize("sizes,synced", [(SIZES, True), (SIZES, False), (MORE, True), (MORE, False)])
+def test_clipped_sync_against_64_bits(n, dtype, op, sizes, synced):
     for layout, off in LAYOUTS.items():
-        ranks = rank_grads(n, SIZES, DT[dtype], off=off)
-        rest = rank_grads(1, [2000, 33], torch.float32) + rank_grads(n - 1, [2000, 33], torch.float32, std=9.0)
+        ranks = rank_grads(n, sizes, DT[dtype], off=off)
+        rest = [[]] * n if not synced else rank_grads(1, [2000, 33], torch.float32) + rank_grads(n - 1, [2000, 33], torch.float32, std=9.0)
         div = n if op == "avg" and n > 1 else 1
-        avg = [sum(rank[t].t.double() for rank in ranks) / div for t in range(len(SIZES))]
-        mag = [sum(rank[t].t.double().abs() for rank in ranks) / div for t in range(len(SIZES))]
+        avg = [sum(rank[t].t.double() for rank in ranks) / div for t in range(len(sizes))]
+        mag = [sum(rank[t].t.double().abs() for rank in ranks) / div for t in range(len(sizes))]
         src = [g.t.clone() for g in rest[0]]
         want = norm64(avg + src)
-        plan = rrv.BucketPlan(SIZES, dtype, 16384)
-        got = plan.all_reduce_clip(rrv.GradSet(tensors(ranks)), 0.6 * want, op, synced=tensors(rest), eps=0.0)
+        plan = rrv.BucketPlan(sizes, dtype, 16384)
+        got = plan.all_reduce_clip(rrv.GradSet(tensors(ranks)), 0.6 * want, op, synced=tensors(rest) if synced else None,
+                                   eps=0.0)
         # the folds' errors are a share of the magnitudes; the norm's of them at most n * 2^-24 of their norm
         assert abs(float(got) - want) <= 10 * E * want + n * E * norm64(mag)
         for rank in ranks:
