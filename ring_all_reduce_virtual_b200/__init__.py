@@ -370,12 +370,13 @@ def _with_norm(what: str, device, need: int, out, stream, call):
     if not _in_place(stream, device):
         with _placed(stream, device):
             return _with_norm(what, device, need, out, None, call)
-    if out is None:
+    if out is None and need <= 1 << 16:  # one piece of memory for both, which lives on with the norm
         mem = torch.empty((_NORM_BYTES + need) // 4, dtype=torch.float32, device=device)
         norm, at = mem[0], mem.data_ptr()
         check(call(at, at + _NORM_BYTES, need, _current_stream(device.index)), what)
-        # a large workspace does not live on with the norm
-        return norm if need <= 1 << 16 else norm.clone()
+        return norm
+    if out is None:
+        out = torch.empty((), dtype=torch.float32, device=device)
     if not out.is_cuda or out.dtype != torch.float32 or out.numel() != 1 or out.device != device:
         raise ValueError("out must be one float32 element on the gradients' device")
     mem = torch.empty(need, dtype=torch.uint8, device=device)

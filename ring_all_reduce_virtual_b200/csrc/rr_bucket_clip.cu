@@ -35,7 +35,7 @@ template <class Fold>
 struct ParkParams {
     Fold f;              // BucketFoldParams or ParkSmallParams; tile0 counts tiles of park_tile_elems
     double* partial;     // kPark, kSquares: one per tile
-    ClipArgs clip;       // kScaled: the coefficient, or the partial sums it comes from
+    ClipArgs clip;       // kScaled: what the coefficient comes from
     unsigned int* waits; // as BulkParams (rr_bulk.cuh)
     uint32_t hold;
     uint32_t spin;
@@ -81,9 +81,6 @@ __device__ __forceinline__ double settle_one(const OutF& out, int n, uint64_t e,
     }
 }
 
-// kScaled: the coefficient.
-__device__ __forceinline__ float pass_coef(const ClipArgs& a, double* sh) { return a.coef ? *a.coef : clip_coef(a, sh); }
-
 // Ranks whose copies of a tensor share a 16-byte phase: tiles staged by bulk
 // copies as in the fused bucket sync (rr_bucket.cu); results leave by bulk
 // stores from slot 0, parked lower halves from slot 1.  The second pass takes
@@ -102,7 +99,6 @@ __global__ void __launch_bounds__(kThreads) bucket_park_kernel(const __grid_cons
     __shared__ __align__(8) uint64_t bar;
     __shared__ double sh[kThreads / 32];
 
-    const float c = MODE == kScaled ? pass_coef(bp.clip, sh) : 1.0f;
     const uint64_t w = MODE == kScaled ? p.tile0[p.nseg] - 1 - blockIdx.x : blockIdx.x;
     const int s = find_segment(p.tile0, p.nseg, w);
     const uint64_t tile = w - p.tile0[s];
@@ -120,29 +116,34 @@ __global__ void __launch_bounds__(kThreads) bucket_park_kernel(const __grid_cons
     if (head > len) head = len;
     const uint64_t nv = (len - head) / L;
     const uint64_t tail = len - head - nv * L;
+    const uint64_t v0 = tile * TV;
+    const bool staged = v0 < nv;
+    const uint32_t nvt = (uint32_t)(nv - v0 < TV ? nv - v0 : TV);
+    const uint32_t bytes = nvt * 16u;
+    const uint64_t e0 = head + v0 * L;  // 16-byte aligned in every rank's copy
+    const uint32_t b = bulk_smem_addr(&bar);
+    if (threadIdx.x == 0 && staged) {
+        bulk_bar_init(b, bp.hold);
+        asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}"
+                     ::"r"(b), "r"(bytes * (uint32_t)n) : "memory");
+#pragma unroll
+        for (int j = 0; j < (NS > 0 ? NS : n); ++j)
+            asm volatile(
+                "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                ::"r"(bulk_smem_addr(sm + j * TV)), "l"(in(j) + e0), "r"(bytes), "r"(b)
+                : "memory");
+    }
+    // the barrier is set up before the other threads wait on it; the second
+    // pass forms the coefficient meanwhile
+    float c = 1.0f;
+    if constexpr (MODE == kScaled) c = clip_coef(bp.clip, sh);
+    else __syncthreads();
     double acc = 0.0;
     if (tile == 0 && (uint64_t)threadIdx.x < head + tail) {
         const uint64_t e = (uint64_t)threadIdx.x < head ? (uint64_t)threadIdx.x : head + nv * L + (threadIdx.x - head);
         acc = settle_one<G, MODE>(out, n, e, fold_value<G, OP>(in, n, e, p.divisor), c);
     }
-    const uint64_t v0 = tile * TV;
-    if (v0 < nv) {
-        const uint32_t nvt = (uint32_t)(nv - v0 < TV ? nv - v0 : TV);
-        const uint32_t bytes = nvt * 16u;
-        const uint64_t e0 = head + v0 * L;  // 16-byte aligned in every rank's copy
-        const uint32_t b = bulk_smem_addr(&bar);
-        if (threadIdx.x == 0) bulk_bar_init(b, bp.hold);
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}"
-                         ::"r"(b), "r"(bytes * (uint32_t)n) : "memory");
-#pragma unroll
-            for (int j = 0; j < (NS > 0 ? NS : n); ++j)
-                asm volatile(
-                    "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                    ::"r"(bulk_smem_addr(sm + j * TV)), "l"(in(j) + e0), "r"(bytes), "r"(b)
-                    : "memory");
-        }
+    if (staged) {
         if (!bulk_tile_landed(b, bp.waits, bp.hold, bp.spin)) {
             // the whole CTA skips the tile: a NaN norm says that the step is lost
             if (MODE != kScaled && threadIdx.x == 0) bp.partial[w] = __longlong_as_double(0x7ff8000000000000ll);
@@ -217,7 +218,7 @@ __global__ void __launch_bounds__(kThreads) bucket_park_any_kernel(const __grid_
     pdl_begin();
     const Fold& p = bp.f;
     const int n = p.n;
-    const float c = MODE == kScaled ? pass_coef(bp.clip, sh) : 1.0f;
+    const float c = MODE == kScaled ? clip_coef(bp.clip, sh) : 1.0f;
     const uint64_t w = MODE == kScaled ? p.tile0[p.nseg] - 1 - blockIdx.x : blockIdx.x;
     const int s = find_segment(p.tile0, p.nseg, w);
     const BucketSeg& sg = p.seg[s];

@@ -78,8 +78,7 @@ __global__ void __launch_bounds__(kThreads) norm_finish_kernel(const __grid_cons
 {
     __shared__ double sh[kThreads / 32];
     pdl_begin();
-    const float c = clip_coef(a, sh);
-    if (a.coef && threadIdx.x == 0) *a.coef = c;
+    clip_coef(a, sh);
 }
 
 // The two fp32 values whose upper halves are the word h and lower halves the
@@ -167,12 +166,11 @@ __global__ void __launch_bounds__(kThreads, 4) clip_scale_kernel(const __grid_co
 
 // The scaling of large sets: one CTA per tile, the tile (two of them where the
 // values are parked in halves) brought to shared memory and sent to every
-// rank by bulk copies, as the one-shot all-reduce moves its tiles; the
-// coefficient comes from norm_finish_kernel.  Tensors whose copies are at
-// different 16-byte phases run element by element.
+// rank by bulk copies, as the one-shot all-reduce moves its tiles.  Every CTA
+// forms the coefficient while its tile is on the way.  Tensors whose copies are
+// at different 16-byte phases run element by element.
 struct ScaleBulkParams {
     ScaleParams s;       // tile0 counts tiles of kBulkScaleBytes in all
-    const float* coef;
     unsigned int* waits; // as BulkParams (rr_bulk.cuh)
     uint32_t hold;
     uint32_t spin;
@@ -188,9 +186,9 @@ __global__ void __launch_bounds__(kThreads) clip_bulk_kernel(const __grid_consta
     constexpr uint32_t TV = kBulkScaleBytes / 16 / (PARKED ? 2 : 1);
     extern __shared__ __align__(128) uint4 sm[];
     __shared__ __align__(8) uint64_t bar;
+    __shared__ double sh[kThreads / 32];
     pdl_begin();
     const ScaleParams& p = bp.s;
-    const float c = *bp.coef;
     const int n = p.n;
     const uint64_t w = p.tile0[p.nt] - 1 - blockIdx.x;  // last tiles first: L2 still holds what was touched last
     const int t = find_segment(p.tile0, p.nt, w);
@@ -198,31 +196,16 @@ __global__ void __launch_bounds__(kThreads) clip_bulk_kernel(const __grid_consta
     T* const* ptr = reinterpret_cast<T* const*>(&p.ptr[(size_t)t * n]);
     const T* src = ptr[0];
     const T* low = PARKED ? ptr[1] : ptr[0];
-    auto one = [&](uint64_t e) {
-        float x;
-        if constexpr (PARKED) x = __uint_as_float(((uint32_t)src[e] << 16) | (uint32_t)low[e]);
-        else x = Ty::ld1(src + e);
-        x = __fmul_rn(x, c);
-        for (int o = 0; o < n; ++o) Ty::st1(ptr[o] + e, x);
-    };
-    if (!p.vec[t]) {
-        const uint64_t e0 = tile * TV * L;
-        for (uint64_t e = e0 + threadIdx.x; e < len && e < e0 + TV * L; e += kThreads) one(e);
-        return;
-    }
     uint64_t head = (uint64_t)((L - phase_of(src, L)) & (L - 1));
     if (head > len) head = len;
     const uint64_t nv = (len - head) / L, tail = len - head - nv * L;
-    if (tile == 0 && threadIdx.x < head + tail)
-        one(threadIdx.x < head ? threadIdx.x : head + nv * L + (threadIdx.x - head));
     const uint64_t v0 = tile * TV;
-    if (v0 >= nv) return;
+    const bool staged = p.vec[t] && v0 < nv;
     const uint32_t nvt = (uint32_t)(nv - v0 < TV ? nv - v0 : TV), bytes = nvt * 16u;
     const uint64_t e0 = head + v0 * L;
     const uint32_t b = bulk_smem_addr(&bar);
-    if (threadIdx.x == 0) bulk_bar_init(b, bp.hold);
-    __syncthreads();
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 0 && staged) {
+        bulk_bar_init(b, bp.hold);  // the others wait on it only after clip_coef's barrier
         asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}"
                      ::"r"(b), "r"(bytes * (PARKED ? 2u : 1u)) : "memory");
 #pragma unroll
@@ -231,6 +214,22 @@ __global__ void __launch_bounds__(kThreads) clip_bulk_kernel(const __grid_consta
                          ::"r"(bulk_smem_addr(sm + k * TV)), "l"((k ? low : src) + e0), "r"(bytes), "r"(b)
                          : "memory");
     }
+    const float c = clip_coef(p.clip, sh);
+    auto one = [&](uint64_t e) {
+        float x;
+        if constexpr (PARKED) x = __uint_as_float(((uint32_t)src[e] << 16) | (uint32_t)low[e]);
+        else x = Ty::ld1(src + e);
+        x = __fmul_rn(x, c);
+        for (int o = 0; o < n; ++o) Ty::st1(ptr[o] + e, x);
+    };
+    if (!p.vec[t]) {
+        const uint64_t at = tile * TV * L;
+        for (uint64_t e = at + threadIdx.x; e < len && e < at + TV * L; e += kThreads) one(e);
+        return;
+    }
+    if (tile == 0 && threadIdx.x < head + tail)
+        one(threadIdx.x < head ? threadIdx.x : head + nv * L + (threadIdx.x - head));
+    if (!staged) return;
     if (!bulk_tile_landed(b, bp.waits, bp.hold, bp.spin)) return;  // the whole CTA skips the tile
     for (uint32_t v = threadIdx.x; v < nvt; v += kThreads) {
         float a[L];
@@ -325,7 +324,7 @@ cudaError_t scale_typed(const ScaleParams& p, unsigned grid, cudaStream_t s)
 }
 
 template <class Ty, bool PARKED>
-cudaError_t bulk_typed(const ScaleParams& p, const float* coef, unsigned grid, cudaStream_t s)
+cudaError_t bulk_typed(const ScaleParams& p, unsigned grid, cudaStream_t s)
 {
     RankParams rp{};
     rp.waits = bulk_wait_counters();
@@ -333,7 +332,6 @@ cudaError_t bulk_typed(const ScaleParams& p, const float* coef, unsigned grid, c
     const BulkParams wait = bulk_params(rp);
     ScaleBulkParams bp;
     bp.s = p;
-    bp.coef = coef;
     bp.waits = wait.waits;
     bp.hold = wait.hold;
     bp.spin = wait.spin;
@@ -377,15 +375,14 @@ cudaError_t launch_clip_scale(int dtype, bool parked, bool bulk, const ScalePara
     if (work == 0) return cudaSuccess;
     if (bulk) {
         if (work > kMaxGrid) return cudaErrorInvalidValue;
-        const float* coef = p.clip.coef;
         switch (dtype) {
-        case kF32: return bulk_typed<F32T, false>(p, coef, (unsigned)work, s);
+        case kF32: return bulk_typed<F32T, false>(p, (unsigned)work, s);
         case kBF16:
-            return parked ? bulk_typed<BF16T, true>(p, coef, (unsigned)work, s)
-                          : bulk_typed<BF16T, false>(p, coef, (unsigned)work, s);
+            return parked ? bulk_typed<BF16T, true>(p, (unsigned)work, s)
+                          : bulk_typed<BF16T, false>(p, (unsigned)work, s);
         case kF16:
-            return parked ? bulk_typed<F16T, true>(p, coef, (unsigned)work, s)
-                          : bulk_typed<F16T, false>(p, coef, (unsigned)work, s);
+            return parked ? bulk_typed<F16T, true>(p, (unsigned)work, s)
+                          : bulk_typed<F16T, false>(p, (unsigned)work, s);
         }
         return cudaErrorInvalidValue;
     }

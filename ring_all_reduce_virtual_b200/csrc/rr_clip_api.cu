@@ -110,26 +110,20 @@ struct Passes {
         return RR_OK;
     }
 
-    // The partials as the next launches read them: at most kMaxPartials; and
-    // for a scaling by bulk copies the coefficient itself.
+    // The partials as the next launches read them: at most kMaxPartials.
     rr_status_t join(ClipArgs* a)
     {
         a->partial = partial;
         a->npartial = (int)count;
-        if (count > kMaxPartials) {
-            int slots = 0;
-            const cudaError_t e =
-                timed_launch([&] { return launch_norm_join(partial, count, partial + count, &slots, stream); });
-            if (e != cudaSuccess) return cuda_fail(e, "norm join launch");
-            t_stats.launches += 1;
-            a->partial = partial + count;
-            a->npartial = slots;
-        }
-        if (!bulk) return RR_OK;
-        a->coef = reinterpret_cast<float*>(partial + count + kJoinCtas);
-        const rr_status_t st = finish(*a);
-        a->norm = nullptr;
-        return st;
+        if (count <= kMaxPartials) return RR_OK;
+        int slots = 0;
+        const cudaError_t e =
+            timed_launch([&] { return launch_norm_join(partial, count, partial + count, &slots, stream); });
+        if (e != cudaSuccess) return cuda_fail(e, "norm join launch");
+        t_stats.launches += 1;
+        a->partial = partial + count;
+        a->npartial = slots;
+        return RR_OK;
     }
 
     rr_status_t finish(const ClipArgs& a)
@@ -235,8 +229,8 @@ uint64_t park_tiles(const rr_bucket_plan_t* plan, int b0, int nb, int n)
     return tiles;
 }
 
-// Partial sums, the joined ones, the coefficient.
-size_t workspace_bytes(uint64_t partials) { return (size_t)(partials + kJoinCtas + 1) * sizeof(double); }
+// Partial sums, and the joined ones.
+size_t workspace_bytes(uint64_t partials) { return (size_t)(partials + kJoinCtas) * sizeof(double); }
 
 rr_status_t bucket_range_ok(const rr_bucket_plan_t* plan, int b0, int nb, int nranks)
 {

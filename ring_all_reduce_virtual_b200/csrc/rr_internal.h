@@ -138,7 +138,6 @@ struct ClipArgs {
     float max_norm;
     float eps;
     float* norm;  // where the launch writes the norm (NULL: it does not)
-    float* coef;  // norm_finish: where it writes the coefficient (NULL: it does not); bulk scaling: where it reads it
 };
 
 // The clipping's second pass: rank 0's copy of each tensor, scaled, into
@@ -289,7 +288,7 @@ constexpr uint64_t kBulkClipBytes = 32ull << 20;
 // us; above L2's 126 MB the hint costs (8 x 666 MB: 1773 -> 1794).
 constexpr uint64_t kKeepBytes = 126ull << 20;
 constexpr int kJoinCtas = 128;        // partials that launch_norm_join leaves
-constexpr int kMaxPartials = 2048;    // partials that a launch sums itself
+constexpr int kMaxPartials = 1280;    // partials that a launch sums itself
 // The clipped sync's first pass: fold, park the sums, one partial per tile.
 uint64_t park_tile_elems(int grad_dtype, int n);
 cudaError_t launch_bucket_park(int grad_dtype, int op, const BucketFoldParams& p, int ntensors, double* partial,

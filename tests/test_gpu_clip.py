@@ -88,7 +88,6 @@ def test_norm_mixed_types_and_many_tensors():
     got = rrv.grad_norm(ts)
     near_norm(got, norm64(ts))
     assert torch.equal(got, rrv.grad_norm(rrv.GradList(ts)))  # the same bits again
-    assert rrv.last_stats()["launches"] == 4  # one per type (833 or 834 tensors each) and the join
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
