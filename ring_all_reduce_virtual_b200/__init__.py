@@ -410,7 +410,7 @@ def clip_grads(grads, max_norm: float, eps: float = 1e-6, out=None, stream=None)
     for the GPU."""
     gl = GradList._of(grads)
     return _norm_call("clip_grads", gl, out, stream,
-                      lambda norm, ws, b, s: lib().rr_clip_grads(gl._ref, max_norm, eps, norm, ws, b, s))
+                      lambda norm, ws, b, s: lib().rr_clip_grads(gl._ref, float(max_norm), float(eps), norm, ws, b, s))
 
 
 def _id_set(tokens, what: str):
@@ -455,11 +455,15 @@ def embedding(tokens, tables, outs, scale: float = 1.0, stream=None) -> None:
     if wn != n or on != n or rows != T or od != D or odt != d or wdev != dev or odev != dev:
         raise ValueError("embedding: need one table [V, D] and one output [tokens, D] per rank, alike and on the "
                          "tokens' device")
-    if not _in_place(stream, dev):
+
+    def call():
+        check(lib().rr_embedding(ids, id_type, w, o, n, T, V, D, d, float(scale), _current_stream(dev.index)), "embedding")
+
+    if _in_place(stream, dev):
+        call()
+    else:
         with _placed(stream, dev):
-            check(lib().rr_embedding(ids, id_type, w, o, n, T, V, D, d, scale, _current_stream(dev.index)), "embedding")
-        return
-    check(lib().rr_embedding(ids, id_type, w, o, n, T, V, D, d, scale, _current_stream(dev.index)), "embedding")
+            call()
 
 
 _embed_bytes: dict = {}  # workspace bytes of embedding_grad by (ranks, tokens, rows, width)
@@ -492,8 +496,8 @@ def embedding_grad(tokens, grad_out, grads, op="avg", scale: float = 1.0, accumu
 
     def call():
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
-        check(lib().rr_embedding_grad(ids, id_type, g, n, T, V, D, d, _op(op), scale,
-                                      -1 if padding_idx is None else padding_idx, w, wn, wdt, int(bool(accumulate)),
+        check(lib().rr_embedding_grad(ids, id_type, g, n, T, V, D, d, _op(op), float(scale),
+                                      -1 if padding_idx is None else int(padding_idx), w, wn, wdt, int(bool(accumulate)),
                                       ws.data_ptr(), need, _current_stream(dev.index)), "embedding_grad")
 
     if _in_place(stream, dev):
@@ -633,7 +637,7 @@ class BucketPlan:
             need = self._clip_bytes[key] = b.value
         return _with_norm("bucket_allreduce_clip", dev, need, out, stream,
                           lambda norm, ws, size, s: lib().rr_bucket_allreduce_clip(
-                              self._h, first, count, g, n, _op(op), ref, max_norm, eps, norm, ws, size, s))
+                              self._h, first, count, g, n, _op(op), ref, float(max_norm), float(eps), norm, ws, size, s))
 
 
 class Reducer:
@@ -666,8 +670,13 @@ class Reducer:
     def ready(self, tensor: int, stream=None) -> None:
         check(lib().rr_reducer_ready(self._h, tensor, _stream(stream, self._device)), "reducer_ready")
 
-    def finish(self, stream=None) -> None:
+    def finish(self, stream=None, max_norm: float | None = None, eps: float = 1e-6):
+        """Join the step on ``stream``; with ``max_norm``, then clip the synced
+        gradients there (``clip_grads``) and return their norm."""
         check(lib().rr_reducer_finish(self._h, _stream(stream, self._device)), "reducer_finish")
+        if max_norm is not None:
+            return clip_grads(self._grads, max_norm, eps, stream=stream)
+        return None
 
 
 def cost_model(algo, nranks: int, bytes_per_rank: float, alpha_s: float, beta_bytes_per_s: float) -> dict:

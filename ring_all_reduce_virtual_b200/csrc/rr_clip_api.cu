@@ -2,7 +2,6 @@
 // (rr_grad_norm, rr_clip_grads, rr_bucket_allreduce_clip in include/rr.h):
 // argument checks, launch tables, the order of the passes.
 #include <cmath>
-#include <exception>
 #include <memory>
 
 #include "rr_host.h"
@@ -430,17 +429,6 @@ rr_status_t bucket_allreduce_clip(const rr_bucket_plan_t* plan, int b0, int nb, 
     t_stats.hbm_bytes += (uint64_t)(2 + n) * R;
     log_call("bucket_allreduce_clip", n, total, d, op, RR_ALGO_ONESHOT);
     return debug_check(st, stream);
-}
-
-// A C entry lets no C++ exception out (the host's memory may be exhausted).
-template <class F>
-rr_status_t guarded(F&& f)
-{
-    try {
-        return f();
-    } catch (const std::exception&) {
-        return RR_ERR_CUDA;
-    }
 }
 
 }  // namespace

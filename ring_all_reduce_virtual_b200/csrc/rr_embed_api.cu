@@ -2,7 +2,6 @@
 // rr_embedding_grad in include/rr.h): argument checks, the access width, the
 // workspace's layout.
 #include <cmath>
-#include <exception>
 
 #include "rr_host.h"
 
@@ -222,16 +221,6 @@ rr_status_t embedding_grad(const void* const* ids, rr_id_type_t id_type, const v
     t_stats.hbm_bytes = M * (ib + D * es) + (accumulate ? 2 * std::min(M, (uint64_t)V) : (uint64_t)V) * D * gs * nout;
     log_call("embedding_grad", n, T * D, dtype, op, RR_ALGO_ONESHOT);
     return debug_check(st, stream);
-}
-
-template <class F>
-rr_status_t guarded(F&& f)
-{
-    try {
-        return f();
-    } catch (const std::exception&) {
-        return RR_ERR_CUDA;
-    }
 }
 
 }  // namespace

@@ -9,6 +9,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <exception>
 #include <string>
 #include <vector>
 
@@ -301,6 +302,18 @@ rr_status_t for_each_fold_launch(const rr_bucket_plan_t* plan, int b0, int nb, v
     }
     if (st == RR_OK && p.nseg > 0) st = flush(lt);
     return st;
+}
+
+// A C entry that lets no C++ exception out: the host's memory may be
+// exhausted (the message fits a std::string's own storage).
+template <class F>
+rr_status_t guarded(F&& f)
+{
+    try {
+        return f();
+    } catch (const std::exception&) {
+        return fail(RR_ERR_CUDA, "no host memory");
+    }
 }
 
 }  // namespace rr

@@ -381,3 +381,95 @@ def test_captured_steps_replay_and_do_not_share_workspaces():
             for rank in ranks:
                 for t, a in zip(rank, avg):
                     near_scaled(t, 0.25 / norm * a, extra=40 * E * 0.25 / norm * (step + 3.0))
+
+
+def test_reducer_clips_when_its_step_ends():
+    n, sizes = 4, [4096, 5, 30000, 64]
+    plan = rrv.BucketPlan(sizes, "bf16", 8192)
+    ranks = tensors(rank_grads(n, sizes, torch.bfloat16))
+    synced = [[t.clone() for t in rank] for rank in ranks]
+    plan.all_reduce_range(0, plan.num_buckets, synced, "avg")
+    red = rrv.Reducer(plan, ranks, "avg")
+    for limit in (None, 0.5):
+        for rank, s in zip(ranks, synced):  # alike on every rank: their average is what they are
+            for t, v in zip(rank, s):
+                t.copy_(v)
+        for t in range(len(sizes)):
+            red.ready(t)
+        got = red.finish() if limit is None else red.finish(max_norm=limit, eps=0.0)
+        if limit is None:
+            assert got is None
+            continue
+        want = norm64(synced[0])
+        near_norm(got, want)
+        for rank in ranks:
+            for t, v in zip(rank, synced[0]):
+                near_scaled(t, v.double() * (limit / want))
+
+
+def run_child(script, **env):
+    import os
+    import subprocess
+    import sys
+
+    out = subprocess.run([sys.executable, "-c", script], env=dict(os.environ, **env), capture_output=True, text=True,
+                         timeout=300)
+    assert out.returncode == 0, out.stderr[-2000:]
+    return out.stdout
+
+
+def test_first_calls_of_a_process_may_be_captured():
+    """A fresh process whose first calls of these operators are captured into a graph."""
+    out = run_child(r"""
+import torch
+import ring_all_reduce_virtual_b200 as rrv
+g = [[torch.full((m,), float(r + 1), device="cuda").bfloat16() for m in (300_000, 7)] for r in range(4)]
+plan = rrv.BucketPlan([300_000, 7], "bf16")
+ids = [torch.tensor([1, 3, 1], dtype=torch.int32, device="cuda")]
+w, o, dw = torch.ones(5, 64, device="cuda"), torch.zeros(3, 64, device="cuda"), torch.zeros(5, 64, device="cuda")
+norm = torch.zeros((), device="cuda")
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    rrv.embedding(ids, [w], [o], 2.0)
+    rrv.embedding_grad(ids, [o], [dw], "sum")
+    rrv.grad_norm([dw], out=norm)
+    plan.all_reduce_clip(g, 1.0)
+    rrv.clip_grads([dw], 1.0)
+graph.replay()
+torch.cuda.synchronize()
+want = (64 * (4.0 ** 2 + 2.0 ** 2)) ** 0.5
+assert abs(float(norm) - want) < 1e-5 * want, float(norm)
+assert abs(float(dw.double().norm()) - 1.0) < 1e-5
+total = sum(float(t.double().square().sum()) for t in g[0]) ** 0.5
+assert abs(total - 1.0) < 1e-2, total
+rrv.check_timeouts()
+print("CAPTURED")
+""")
+    assert "CAPTURED" in out
+
+
+def test_timeouts_of_the_clipping_are_reported_and_the_context_survives():
+    """RR_DEBUG_BULK_TIMEOUT=1 makes every first bounded wait run out: the tiles are skipped, the norm is NaN, the status
+    says so, nothing partly folded is stored (a scaling without such waits makes every value NaN, as a NaN norm does),
+    and the context still runs a call."""
+    out = run_child(r"""
+import torch
+import ring_all_reduce_virtual_b200 as rrv
+def report():
+    try:
+        rrv.check_timeouts()
+        print("NO TIMEOUT")
+    except rrv.RRError as e:
+        print("TIMEOUT", e.status, "not seen to land: 0" in str(e))
+for n, m in ((8, 1 << 20), (2, 1 << 23)):  # parked and folded twice, scaled by bulk copies
+    plan = rrv.BucketPlan([m], "bf16")
+    g = [[torch.full((m,), float(r + 1), device="cuda").bfloat16()] for r in range(n)]
+    norm = plan.all_reduce_clip(g, 1.0)
+    report()
+    assert bool(norm.isnan())
+    assert all(bool(((t[0] == r + 1) | t[0].isnan()).all()) for r, t in enumerate(g)), "a skipped tile was stored"
+x = [torch.ones(1000, device="cuda")]
+print("CONTEXT OK", float(rrv.grad_norm(x)) == 1000 ** 0.5 or abs(float(rrv.grad_norm(x)) - 1000 ** 0.5) < 1e-4)
+""", RR_DEBUG_BULK_TIMEOUT="1")
+    assert out.count("TIMEOUT 4 True") == 2 and "CONTEXT OK True" in out, out
