@@ -31,7 +31,7 @@ rr_status_t check_list(const rr_tensor_list_t* l, uint64_t* total)
         for (int r = 0; r < l->nranks; ++r) {
             const uintptr_t a = (uintptr_t)l->ptrs[(size_t)r * l->ntensors + t];
             if (a == 0) return fail(RR_ERR_INVALID_ARG, "NULL buffer pointer");
-            if (a % esize(l->dtypes[t]) != 0)
+            if ((a & (esize(l->dtypes[t]) - 1)) != 0)
                 return fail(RR_ERR_INVALID_ARG, "gradient not aligned to its element size");
         }
     }
@@ -49,6 +49,19 @@ void add_spans(const rr_tensor_list_t* l, int ranks, bool out, std::vector<Span>
             }
 }
 
+// Whether [lo, hi) meets one of the spans, which are sorted and disjoint where
+// they are written (check_spans has passed).
+bool meets(const std::vector<Span>& spans, uintptr_t lo, uintptr_t hi)
+{
+    // read-only spans may nest, so every span that begins before hi counts
+    auto it = std::lower_bound(spans.begin(), spans.end(), hi, [](const Span& s, uintptr_t x) { return s.lo < x; });
+    if (it == spans.begin()) return false;
+    if (std::prev(it)->out) return std::prev(it)->hi > lo;
+    return std::any_of(spans.begin(), it, [lo](const Span& s) { return s.hi > lo; });
+}
+
+// The gradients' spans, then the norm and the workspace against them: two
+// more spans at the end of a sorted list would have it sorted anew.
 rr_status_t check_scratch(float* norm, void* ws, size_t have, size_t need, std::vector<Span>& spans)
 {
     if (!norm) return fail(RR_ERR_INVALID_ARG, "NULL norm pointer");
@@ -56,9 +69,12 @@ rr_status_t check_scratch(float* norm, void* ws, size_t have, size_t need, std::
     if (!ws || (uintptr_t)ws % 8 != 0) return fail(RR_ERR_INVALID_ARG, "workspace NULL or not aligned to 8 bytes");
     if (have < need)
         return fail(RR_ERR_INVALID_ARG, "workspace too small: " + std::to_string(need) + " bytes are needed");
-    spans.push_back({(uintptr_t)norm, (uintptr_t)norm + 4, true});
-    spans.push_back({(uintptr_t)ws, (uintptr_t)ws + need, true});
-    return check_spans(spans);
+    const rr_status_t st = check_spans(spans);
+    if (st != RR_OK) return st;
+    const uintptr_t a = (uintptr_t)norm, b = (uintptr_t)ws;
+    if (meets(spans, a, a + 4) || meets(spans, b, b + need) || (a < b + need && b < a + 4))
+        return fail(RR_ERR_INVALID_ARG, "buffers overlap (or repeat): the norm or the workspace");
+    return RR_OK;
 }
 
 rr_status_t check_clip(float max_norm, float eps)
@@ -85,7 +101,9 @@ struct Passes {
     // The norm's launches over rank 0's tensors, one type at a time.
     rr_status_t norm(const rr_tensor_list_t* l)
     {
-        NormParams p{};
+        NormParams p;  // as it comes: every field that counts is set
+        p.nt = 0;
+        p.tile0[0] = 0;
         for (rr_dtype_t d : kGradTypes) {
             const uint64_t te = norm_tile_elems(d);
             for (int t = 0; t <= l->ntensors; ++t) {
@@ -138,7 +156,9 @@ struct Passes {
     template <class Ptr, class Len>
     rr_status_t scale(rr_dtype_t d, bool parked, int n, int ntensors, Ptr&& ptr, Len&& numel, ClipArgs& a)
     {
-        auto p = std::make_unique<ScaleParams>();
+        std::unique_ptr<ScaleParams> p(new ScaleParams);  // as it comes: every field that counts is set
+        p->nt = 0;
+        p->tile0[0] = 0;
         const uint64_t te = scale_tile_elems(d, parked, bulk);
         const int most = std::min(kScaleTensors, kScalePtrs / n);
         for (int t = 0; t <= ntensors; ++t) {
@@ -215,16 +235,23 @@ uint64_t norm_slots(const rr_tensor_list_t* l)
     return slots;
 }
 
-// Tiles of the first pass over a bucket range, one partial sum each.
+// Tiles of the first pass over a bucket range, one partial sum each: the tiles
+// of every run of a tensor inside one of its bucket's chunks.
 uint64_t park_tiles(const rr_bucket_plan_t* plan, int b0, int nb, int n)
 {
     uint64_t tiles = 0;
     const uint64_t te = park_tile_elems(plan->grad_dtype, n);
-    auto p = std::make_unique<BucketFoldParams>();
-    for_each_fold_launch(plan, b0, nb, nullptr, n, *p, [&](int) {
-        for (int s = 0; s < p->nseg; ++s) tiles += ceil_div(p->seg[s].len, te);
-        return RR_OK;
-    });
+    for (int b = b0; b < b0 + nb; ++b) {
+        const uint64_t C = ceil_div(plan->bnumel[b], (uint64_t)n);
+        for (int t = plan->first[b]; t < plan->first[b] + plan->count[b]; ++t) {
+            const uint64_t hi = plan->offset[t] + plan->numel[t];
+            for (uint64_t pos = plan->offset[t]; pos < hi;) {
+                const uint64_t end = std::min(hi, (pos / C + 1) * C);
+                tiles += ceil_div(end - pos, te);
+                pos = end;
+            }
+        }
+    }
     return tiles;
 }
 
@@ -378,7 +405,7 @@ rr_status_t bucket_allreduce_clip(const rr_bucket_plan_t* plan, int b0, int nb, 
     const RangeList own(plan, t0, nt, grads);
     const bool twice = n > 1 && clip_folds_twice(n, d);
     // the range's launches, a pass at a time
-    auto p = std::make_unique<BucketFoldParams>();
+    std::unique_ptr<BucketFoldParams> p(new BucketFoldParams);  // as it comes: every field that counts is set
     auto pass = [&](auto&& launch) {
         return for_each_fold_launch(plan, b0, nb, grads, n, *p, [&](int ntens) -> rr_status_t {
             const uint64_t te = park_tile_elems(d, n);

@@ -117,7 +117,8 @@ inline rr_status_t check_spans(Spans& s)
 {
     for (const Span& a : s)
         if (a.lo == 0) return fail(RR_ERR_INVALID_ARG, "NULL buffer pointer");
-    std::sort(s.begin(), s.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });
+    const auto before = [](const Span& a, const Span& b) { return a.lo < b.lo; };
+    if (!std::is_sorted(s.begin(), s.end(), before)) std::sort(s.begin(), s.end(), before);
     for (size_t i = 0; i < s.size(); ++i)
         for (size_t j = i + 1; j < s.size() && s[j].lo < s[i].hi; ++j)
             if (s[i].out || s[j].out) return fail(RR_ERR_INVALID_ARG, "buffers overlap (or repeat)");
@@ -247,11 +248,12 @@ inline rr_status_t bucket_range_spans(const rr_bucket_plan_t* plan, int b0, int 
     *t0 = plan->first[b0];
     *nt = plan->first[b0 + nb - 1] + plan->count[b0 + nb - 1] - *t0;
     const uint64_t es = esize((rr_dtype_t)plan->grad_dtype);
+    spans.reserve(spans.size() + (size_t)nranks * *nt);
     for (int r = 0; r < nranks; ++r)
         for (int t = *t0; t < *t0 + *nt; ++t) {
             const void* g = grads[(size_t)r * plan->ntensors + t];
             if (plan->numel[t] == 0) continue;
-            if ((uintptr_t)g % es != 0) return fail(RR_ERR_INVALID_ARG, "gradient not aligned to its element size");
+            if (((uintptr_t)g & (es - 1)) != 0) return fail(RR_ERR_INVALID_ARG, "gradient not aligned to its element size");
             spans.push_back({(uintptr_t)g, (uintptr_t)g + plan->numel[t] * es, true});
         }
     return RR_OK;
@@ -280,7 +282,7 @@ rr_status_t for_each_fold_launch(const rr_bucket_plan_t* plan, int b0, int nb, v
 {
     rr_status_t st = RR_OK;
     int lt = 0;  // tensors in the current launch
-    p = BucketFoldParams{};
+    p.nseg = 0;
     for (int b = b0; b < b0 + nb && st == RR_OK; ++b) {
         const uint64_t C = ceil_div(plan->bnumel[b], (uint64_t)n);  // this bucket's chunk size
         for (int t = plan->first[b]; t < plan->first[b] + plan->count[b] && st == RR_OK; ++t) {
@@ -288,7 +290,7 @@ rr_status_t for_each_fold_launch(const rr_bucket_plan_t* plan, int b0, int nb, v
             const int nsegs_t = hi > lo ? (int)((hi - 1) / C - lo / C + 1) : 0;
             if (lt + 1 > kMaxBucketTensors || (lt + 1) * n > kMaxBucketPtrs || p.nseg + nsegs_t > kMaxBucketSegs) {
                 if (p.nseg > 0) st = flush(lt);
-                p = BucketFoldParams{};
+                p.nseg = 0;
                 lt = 0;
             }
             for (int r = 0; grads && r < n; ++r) p.grad[lt * n + r] = grads[(size_t)r * plan->ntensors + t];
