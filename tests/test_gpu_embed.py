@@ -150,6 +150,7 @@ def test_grad_tokens_and_table_rows(t, v):
 def test_grad_of_many_tokens():
     run_grad(2, 140_001, 5000, 8, torch.bfloat16, "zipf", nout=1)  # blocks of more than 32 positions
     run_grad(1, 200_000, 300_000, 8, torch.float32, "same")
+    run_grad(3, 400_001, 40_000, 4, torch.float32, "zipf", nout=1)  # more tiles than a CTA sums
     run_grad(64, 11, 50, 16, torch.float16, "zipf", nout=2)
     for kind in ("zipf", "runs", "same"):  # blocks of 16 and of 32 positions
         run_grad(2, 5_003, 2000, 2048, torch.bfloat16, kind, nout=1)
