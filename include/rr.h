@@ -406,8 +406,9 @@ rr_status_t rr_clip_grads(const rr_tensor_list_t* grads, float max_norm, float e
  * lists tensors whose gradients are already alike on every rank -- an
  * embedding's, say (rr_embedding_grad) -- with the same nranks: they count
  * into the norm and are clipped as rr_clip_grads does, from rank 0's copy.
- * Between its two passes the call keeps the fp32 sums in the gradients' own
- * buffers (ranks 0 and 1).  op: SUM or AVG.  With nranks 1 it is the clipping
+ * Between its two passes the call may keep the fp32 sums in the gradients' own
+ * buffers (ranks 0 and 1), so a call that ends with RR_ERR_CUDA leaves the
+ * gradients undefined.  op: SUM or AVG.  With nranks 1 it is the clipping
  * alone.  Other arguments and errors as rr_bucket_allreduce_range and
  * rr_clip_grads. */
 rr_status_t rr_bucket_allreduce_clip(const rr_bucket_plan_t* plan, int first_bucket, int nbuckets, void* const* grads,
@@ -526,8 +527,9 @@ rr_status_t rr_set_picker_params(double launch_s, double hbm_bytes_per_s);
 rr_status_t rr_get_stats(rr_stats_t* out); /* last call on this host thread */
 
 /* Bounded waits.  The one-shot all-reduce (2-64 ranks), the reduce-scatter
- * (2-16 ranks), the tree-order one-shot (2-8, 12 and 16 ranks) and the fused
- * bucket sync (2-64 ranks) stage their tiles in shared memory with bulk async
+ * (2-16 ranks), the tree-order one-shot (2-8, 12 and 16 ranks), the fused
+ * bucket sync (2-64 ranks), the clipped bucket sync and the clipping of large
+ * sets stage their tiles in shared memory with bulk async
  * copies when every rank's buffer sits at one 16-byte phase (on element
  * boundaries); their threads wait on an mbarrier for those
  * copies with an iteration limit instead of forever.  A wait that runs out --
@@ -537,8 +539,9 @@ rr_status_t rr_get_stats(rr_stats_t* out); /* last call on this host thread */
  * the tile a second time if they were not seen to land.  This call
  * synchronises the current device, takes both counts (atomically exchanged
  * for zero on the device) and returns RR_ERR_TIMEOUT if either is not zero
- * (rr_last_error() gives both), RR_OK otherwise.  No other kernel of the
- * library waits on anything. */
+ * (rr_last_error() gives both), RR_OK otherwise.  (A clipped sync that
+ * skipped a tile also reports a NaN norm.)  No other kernel of the library
+ * waits on anything but the hardware's barriers of its own CTA or cluster. */
 rr_status_t rr_check_timeouts(void);
 const char* rr_status_string(rr_status_t status);
 const char* rr_last_error(void); /* detail of the last failure on this thread */

@@ -278,11 +278,11 @@ cudaError_t launch_norm(int dtype, const NormParams& p, int* slots, cudaStream_t
 cudaError_t launch_norm_join(const double* in, int64_t count, double* out, int* slots, cudaStream_t s);
 cudaError_t launch_norm_finish(const ClipArgs& a, cudaStream_t s);
 cudaError_t launch_clip_scale(int dtype, bool parked, bool bulk, const ScaleParams& p, cudaStream_t s);
-// Bytes written from which the scaling runs by bulk copies: 4 x 104 MB 117 us by
-// the threads, 105 by bulk copies; 8 x 666 MB 1984 and 1816; below, the bulk
-// form's launch for the coefficient costs what its copies gain (50 MB: 26.4
-// and 26.6).
-constexpr uint64_t kBulkClipBytes = 32ull << 20;
+// Bytes written from which the scaling runs by bulk copies, against by the
+// threads: 4 x 64 MB 60.4 and 68.9 us, 4 x 32 MB 31.2 and 33.7, 4 x 16 MB 20.0 and
+// 20.4, 1 x 32 MB 18.1 and 18.3, 1 x 16 MB 13.6 and 12.5 (its CTAs are short, and
+// each sums the partials).
+constexpr uint64_t kBulkClipBytes = 64ull << 20;
 // One rank's bytes up to which the scaling stores with an evict-first hint, so
 // that the values the norm left in L2 are read there: 4 x 104 MB 104.6 -> 99.9
 // us; above L2's 126 MB the hint costs (8 x 666 MB: 1773 -> 1794).
