@@ -84,6 +84,7 @@ class RankSet:
         self.nranks = len(tensors)
         self.ptrs = _ptr_array(tensors)
         self.tensors = list(tensors)
+        self._rows = None  # what the embedding calls make of it, kept by the first
 
     def __len__(self) -> int:
         return self.nranks
@@ -112,23 +113,26 @@ def _rank_args(tensors, what: str):
     return _ptr_array(tensors), len(tensors), count, d, dev
 
 
-_raw_stream = None
+_torch_calls = None  # (torch, current stream's handle by device index, current device's index), at first use
 
 
-def _current_stream(index: int) -> int:
-    """The handle of a device's current stream, without building a Stream object (2 us) where PyTorch offers that."""
-    global _raw_stream
-    if _raw_stream is None:
+def _calls():
+    """PyTorch's calls that every norm, clipping and embedding call makes: a
+    stream's handle without building a Stream object (2 us) where PyTorch
+    offers that, the current device's index without its initialisation check."""
+    global _torch_calls
+    if _torch_calls is None:
         import torch
 
-        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
-            (lambda i: torch.cuda.current_stream(i).cuda_stream)
-    return _raw_stream(index)
+        torch.cuda.current_device()  # initialises CUDA, once
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+        _torch_calls = torch, raw, getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    return _torch_calls
 
 
 def _stream(stream, device):
     if stream is None:
-        return ctypes.c_void_p(_current_stream(device.index))
+        return ctypes.c_void_p(_calls()[1](device.index))
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -353,45 +357,39 @@ def _placed(stream, device):
                 yield
 
 
-def _in_place(stream, device) -> bool:
-    """Whether a call needs no ``_placed``: the current stream of the current device."""
-    import torch
-
-    return stream is None and device.index == torch.cuda.current_device()
-
-
 _NORM_BYTES = 256  # in front of a workspace, for the norm
 
 
-def _with_norm(what: str, device, need: int, out, stream, call):
-    """Run ``call(norm pointer, workspace pointer, bytes, stream)``; the norm's tensor."""
-    import torch
-
-    if not _in_place(stream, device):
+def _with_norm(what: str, fn, args: tuple, device, need: int, out, stream):
+    """Run ``fn(*args, norm pointer, workspace pointer, bytes, stream)``; the norm's tensor."""
+    torch, raw, current = _calls()
+    index = device.index
+    if stream is not None or index != current():
         with _placed(stream, device):
-            return _with_norm(what, device, need, out, None, call)
+            return _with_norm(what, fn, args, device, need, out, None)
     if out is None and need <= 1 << 16:  # one piece of memory for both, which lives on with the norm
         mem = torch.empty((_NORM_BYTES + need) // 4, dtype=torch.float32, device=device)
-        norm, at = mem[0], mem.data_ptr()
-        check(call(at, at + _NORM_BYTES, need, _current_stream(device.index)), what)
-        return norm
+        at = mem.data_ptr()
+        st = fn(*args, at, at + _NORM_BYTES, need, raw(index))
+        if st:
+            check(st, what)
+        return mem[0]
     if out is None:
         out = torch.empty((), dtype=torch.float32, device=device)
     if not out.is_cuda or out.dtype != torch.float32 or out.numel() != 1 or out.device != device:
         raise ValueError("out must be one float32 element on the gradients' device")
     mem = torch.empty(need, dtype=torch.uint8, device=device)
-    check(call(out.data_ptr(), mem.data_ptr(), need, _current_stream(device.index)), what)
+    check(fn(*args, out.data_ptr(), mem.data_ptr(), need, raw(index)), what)
     return out
 
 
-def _norm_call(what: str, gl: GradList, out, stream, call):
+def _norm_call(what: str, fn, args: tuple, gl: GradList, out, stream):
     """``_with_norm`` for a list."""
-    import torch
-
     device = gl.device
     if device is None:
+        torch = _calls()[0]
         device = out.device if out is not None else torch.device("cuda", torch.cuda.current_device())
-    return _with_norm(what, device, gl._workspace(), out, stream, call)
+    return _with_norm(what, fn, args, device, gl._workspace(), out, stream)
 
 
 def grad_norm(grads, out=None, stream=None):
@@ -399,7 +397,7 @@ def grad_norm(grads, out=None, stream=None):
     scalar on the device, ``out`` where it is given.  ``grads``: a list of
     tensors, one list per rank, a ``GradList`` or a ``GradSet``."""
     gl = GradList._of(grads)
-    return _norm_call("grad_norm", gl, out, stream, lambda norm, ws, b, s: lib().rr_grad_norm(gl._ref, norm, ws, b, s))
+    return _norm_call("grad_norm", lib().rr_grad_norm, (gl._ref,), gl, out, stream)
 
 
 def clip_grads(grads, max_norm: float, eps: float = 1e-6, out=None, stream=None):
@@ -409,39 +407,48 @@ def clip_grads(grads, max_norm: float, eps: float = 1e-6, out=None, stream=None)
     a float32 scalar on the device (``out`` where it is given); nothing waits
     for the GPU."""
     gl = GradList._of(grads)
-    return _norm_call("clip_grads", gl, out, stream,
-                      lambda norm, ws, b, s: lib().rr_clip_grads(gl._ref, float(max_norm), float(eps), norm, ws, b, s))
+    return _norm_call("clip_grads", lib().rr_clip_grads, (gl._ref, float(max_norm), float(eps)), gl, out, stream)
 
 
 def _id_set(tokens, what: str):
     """(pointer array, id type, ranks, tokens per rank, device) of the ranks'
     token ids: a list of int32 or int64 tensors, or a RankSet (int32)."""
-    import torch
-
     if isinstance(tokens, RankSet):
-        if tokens.dtype != _DTYPE_NAMES["i32"]:
+        if tokens.dtype != 2:
             raise TypeError(f"{what}: token ids must be int32 or int64")
         return tokens.ptrs, 0, tokens.nranks, tokens.count, tokens.device
-    if len(tokens) < 1 or len(tokens) > MAX_RANKS:
-        raise ValueError(f"{what}: need 1..{MAX_RANKS} token tensors, got {len(tokens)}")
+    n = len(tokens)
+    if n < 1 or n > MAX_RANKS:
+        raise ValueError(f"{what}: need 1..{MAX_RANKS} token tensors, got {n}")
     t0 = tokens[0]
-    if t0.dtype not in (torch.int32, torch.int64):
+    dtype, count, device = t0.dtype, t0.numel(), t0.device
+    id_type = _ID_TYPES.get(str(dtype))
+    if id_type is None:
         raise TypeError(f"{what}: token ids must be int32 or int64")
     for t in tokens:
-        if not t.is_cuda or not t.is_contiguous() or t.dtype != t0.dtype or t.numel() != t0.numel() \
-                or t.device != t0.device:
+        if not t.is_cuda or not t.is_contiguous() or t.dtype != dtype or t.numel() != count or t.device != device:
             raise ValueError(f"{what}: token tensors must be contiguous CUDA tensors alike")
-    return _ptr_array(tokens), int(t0.dtype == torch.int64), len(tokens), t0.numel(), t0.device
+    return _ptr_array(tokens), id_type, n, count, device
+
+
+_ID_TYPES = {"torch.int32": 0, "torch.int64": 1}
 
 
 def _row_set(tensors, what: str):
     """(pointer array, ranks, rows, row width, dtype code, device) of 2-D (or
-    more) tensors whose last axis is a row: a list, or a RankSet."""
+    more) tensors whose last axis is a row: a list, or a RankSet (which keeps
+    the answer)."""
+    is_set = isinstance(tensors, RankSet)
+    if is_set and tensors._rows is not None:
+        return tensors._rows
     ptrs, n, count, d, dev = _rank_args(tensors, what)
-    shape = (tensors.tensors if isinstance(tensors, RankSet) else tensors)[0].shape
+    shape = (tensors.tensors if is_set else tensors)[0].shape
     if len(shape) < 2 or shape[-1] == 0:
         raise ValueError(f"{what}: need tensors of rows (two axes or more, rows not empty)")
-    return ptrs, n, count // shape[-1], shape[-1], d, dev
+    rows = ptrs, n, count // shape[-1], shape[-1], d, dev
+    if is_set:
+        tensors._rows = rows
+    return rows
 
 
 def embedding(tokens, tables, outs, scale: float = 1.0, stream=None) -> None:
@@ -455,15 +462,15 @@ def embedding(tokens, tables, outs, scale: float = 1.0, stream=None) -> None:
     if wn != n or on != n or rows != T or od != D or odt != d or wdev != dev or odev != dev:
         raise ValueError("embedding: need one table [V, D] and one output [tokens, D] per rank, alike and on the "
                          "tokens' device")
-
-    def call():
-        check(lib().rr_embedding(ids, id_type, w, o, n, T, V, D, d, float(scale), _current_stream(dev.index)), "embedding")
-
-    if _in_place(stream, dev):
-        call()
-    else:
-        with _placed(stream, dev):
-            call()
+    args = (ids, id_type, w, o, n, T, V, D, d, float(scale))
+    _, raw, current = _calls()
+    if stream is None and dev.index == current():
+        st = lib().rr_embedding(*args, raw(dev.index))
+        if st:
+            check(st, "embedding")
+        return
+    with _placed(stream, dev):
+        check(lib().rr_embedding(*args, raw(dev.index)), "embedding")
 
 
 _embed_bytes: dict = {}  # workspace bytes of embedding_grad by (ranks, tokens, rows, width)
@@ -477,8 +484,6 @@ def embedding_grad(tokens, grad_out, grads, op="avg", scale: float = 1.0, accumu
     (``"avg"``), into every tensor of ``grads`` (each rank's replica, or one);
     with ``accumulate`` added to what is there.  ``grads`` may be float32
     beside 16-bit rows.  Ids outside the table and ``padding_idx`` add nothing."""
-    import torch
-
     ids, id_type, n, T, dev = _id_set(tokens, "embedding_grad")
     g, gn, rows, D, d, gdev = _row_set(grad_out, "embedding_grad")
     w, wn, V, wd, wdt, wdev = _row_set(grads, "embedding_grad")
@@ -494,17 +499,12 @@ def embedding_grad(tokens, grad_out, grads, op="avg", scale: float = 1.0, accumu
             _embed_bytes.clear()
         need = _embed_bytes[key] = max(b.value, 256)
 
-    def call():
+    args = (ids, id_type, g, n, T, V, D, d, _op(op), float(scale), -1 if padding_idx is None else int(padding_idx), w, wn,
+            wdt, 1 if accumulate else 0)
+    torch, raw, current = _calls()
+    with contextlib.nullcontext() if stream is None and dev.index == current() else _placed(stream, dev):
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
-        check(lib().rr_embedding_grad(ids, id_type, g, n, T, V, D, d, _op(op), float(scale),
-                                      -1 if padding_idx is None else int(padding_idx), w, wn, wdt, int(bool(accumulate)),
-                                      ws.data_ptr(), need, _current_stream(dev.index)), "embedding_grad")
-
-    if _in_place(stream, dev):
-        call()
-    else:
-        with _placed(stream, dev):
-            call()
+        check(lib().rr_embedding_grad(*args, ws.data_ptr(), need, raw(dev.index)), "embedding_grad")
 
 
 class BucketPlan:
@@ -635,9 +635,8 @@ class BucketPlan:
             b = ctypes.c_size_t()
             check(lib().rr_clip_workspace(self._h, first, count, n, ref, ctypes.byref(b)), "clip_workspace")
             need = self._clip_bytes[key] = b.value
-        return _with_norm("bucket_allreduce_clip", dev, need, out, stream,
-                          lambda norm, ws, size, s: lib().rr_bucket_allreduce_clip(
-                              self._h, first, count, g, n, _op(op), ref, float(max_norm), float(eps), norm, ws, size, s))
+        args = (self._h, first, count, g, n, _op(op), ref, float(max_norm), float(eps))
+        return _with_norm("bucket_allreduce_clip", lib().rr_bucket_allreduce_clip, args, dev, need, out, stream)
 
 
 class Reducer:

@@ -111,6 +111,8 @@ def _declare(lib: ctypes.CDLL) -> None:
 def lib() -> ctypes.CDLL:
     """The loaded library (loaded on first use)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):

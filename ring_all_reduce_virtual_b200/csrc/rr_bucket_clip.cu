@@ -283,28 +283,58 @@ cudaError_t park_sized(const ParkParams<Fold>& bp, cudaStream_t s)
     }
 }
 
-template <class G, int OP, int MODE>
-cudaError_t park_typed(const ParkParams<BucketFoldParams>& bp, int ntensors, cudaStream_t s)
+// The launch's table, as it is or as a small one.
+inline void copy_table(BucketFoldParams& to, const BucketFoldParams& f, int) { to = f; }
+
+inline void copy_table(ParkSmallParams& to, const BucketFoldParams& f, int ntensors)
 {
-    const BucketFoldParams& f = bp.f;
-    if (f.nseg > kParkSegsSmall || ntensors * f.n > kParkPtrsSmall) return park_sized<G, OP, MODE>(bp, s);
-    ParkParams<ParkSmallParams> q{};
-    for (int i = 0; i < ntensors * f.n; ++i) q.f.grad[i] = f.grad[i];
+    for (int i = 0; i < ntensors * f.n; ++i) to.grad[i] = f.grad[i];
+    to.tile0[0] = 0;
     for (int i = 0; i < f.nseg; ++i) {
-        q.f.seg[i] = f.seg[i];
-        q.f.tile0[i + 1] = f.tile0[i + 1];
+        to.seg[i] = f.seg[i];
+        to.tile0[i + 1] = f.tile0[i + 1];
     }
-    q.f.n = f.n;
-    q.f.nseg = f.nseg;
-    q.f.vec_ok = f.vec_ok;
-    q.f.divisor = f.divisor;
-    q.partial = bp.partial;
-    q.clip = bp.clip;
-    q.waits = bp.waits;
-    q.hold = bp.hold;
-    q.spin = bp.spin;
-    q.tv = bp.tv;
-    return park_sized<G, OP, MODE>(q, s);
+    to.n = f.n;
+    to.nseg = f.nseg;
+    to.vec_ok = f.vec_ok;
+    to.divisor = f.divisor;
+}
+
+template <int MODE, class Fold>
+cudaError_t launch_table(int grad_dtype, int op, const BucketFoldParams& f, int ntensors, double* partial,
+                         const ClipArgs* clip, cudaStream_t s)
+{
+    RankParams rp{};
+    rp.waits = bulk_wait_counters();
+    const BulkParams wait = bulk_params(rp);
+    ParkParams<Fold> bp;
+    copy_table(bp.f, f, ntensors);
+    bp.partial = partial;
+    bp.clip = clip ? *clip : ClipArgs{};
+    bp.waits = wait.waits;
+    bp.hold = wait.hold;
+    bp.spin = wait.spin;
+    bp.tv = kParkBytes / (uint32_t)f.n / 16u;
+    bp.pad_ = 0;
+    const bool avg = op == kAvg;
+    switch (grad_dtype) {
+    case kF32:
+        if constexpr (MODE != kPark) return cudaErrorInvalidValue;  // fp32 is parked
+        else return avg ? park_sized<F32T, kAvg, MODE>(bp, s) : park_sized<F32T, kSum, MODE>(bp, s);
+    case kBF16: return avg ? park_sized<BF16T, kAvg, MODE>(bp, s) : park_sized<BF16T, kSum, MODE>(bp, s);
+    case kF16: return avg ? park_sized<F16T, kAvg, MODE>(bp, s) : park_sized<F16T, kSum, MODE>(bp, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
+template <int MODE>
+cudaError_t launch_pass(int grad_dtype, int op, const BucketFoldParams& p, int ntensors, double* partial,
+                        const ClipArgs* clip, cudaStream_t s)
+{
+    if (p.tile0[p.nseg] > kMaxGrid || p.n < 2) return cudaErrorInvalidValue;
+    if (p.nseg <= kParkSegsSmall && ntensors * p.n <= kParkPtrsSmall)
+        return launch_table<MODE, ParkSmallParams>(grad_dtype, op, p, ntensors, partial, clip, s);
+    return launch_table<MODE, BucketFoldParams>(grad_dtype, op, p, ntensors, partial, clip, s);
 }
 
 }  // namespace
@@ -315,34 +345,6 @@ uint64_t park_tile_elems(int grad_dtype, int n)
 }
 
 bool clip_folds_twice(int n, int grad_dtype) { return n <= 3 && grad_dtype != kF32; }
-
-template <int MODE>
-static cudaError_t launch_pass(int grad_dtype, int op, const BucketFoldParams& p, int ntensors, double* partial,
-                               const ClipArgs* clip, cudaStream_t s)
-{
-    RankParams rp{};
-    rp.waits = bulk_wait_counters();
-    const BulkParams wait = bulk_params(rp);
-    if (p.tile0[p.nseg] > kMaxGrid || p.n < 2) return cudaErrorInvalidValue;
-    ParkParams<BucketFoldParams> bp;
-    bp.f = p;
-    bp.partial = partial;
-    bp.clip = clip ? *clip : ClipArgs{};
-    bp.waits = wait.waits;
-    bp.hold = wait.hold;
-    bp.spin = wait.spin;
-    bp.tv = kParkBytes / (uint32_t)p.n / 16u;
-    bp.pad_ = 0;
-    const bool avg = op == kAvg;
-    switch (grad_dtype) {
-    case kF32:
-        if constexpr (MODE != kPark) return cudaErrorInvalidValue;  // fp32 is parked
-        else return avg ? park_typed<F32T, kAvg, MODE>(bp, ntensors, s) : park_typed<F32T, kSum, MODE>(bp, ntensors, s);
-    case kBF16: return avg ? park_typed<BF16T, kAvg, MODE>(bp, ntensors, s) : park_typed<BF16T, kSum, MODE>(bp, ntensors, s);
-    case kF16: return avg ? park_typed<F16T, kAvg, MODE>(bp, ntensors, s) : park_typed<F16T, kSum, MODE>(bp, ntensors, s);
-    }
-    return cudaErrorInvalidValue;
-}
 
 cudaError_t launch_bucket_park(int grad_dtype, int op, const BucketFoldParams& p, int ntensors, double* partial,
                                cudaStream_t s)
