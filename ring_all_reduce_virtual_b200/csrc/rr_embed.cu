@@ -23,6 +23,8 @@
 // us: 21, 83 and 12 for the joins.  A sort by a cluster of 8 CTAs in one launch,
 // the keys in distributed shared memory, took 18 us for 16384 tokens and 37 for
 // 65536, where the three launches take 16 and 21.
+#include <atomic>
+
 #include "rr_device.cuh"
 #include "rr_internal.h"
 
@@ -921,12 +923,22 @@ cudaError_t launch_pdl(void (*kernel)(A...), dim3 grid, unsigned threads, uint32
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// A ring kernel: more shared memory than a launch gets by default.
-cudaError_t launch_ring(void (*kernel)(EmbedGradParams), dim3 grid, uint32_t smem, cudaStream_t s,
-                        const EmbedGradParams& p)
+// A ring kernel: more shared memory than a launch gets by default, which is
+// asked for once per kernel and device.
+template <void (*KERNEL)(EmbedGradParams)>
+cudaError_t launch_ring(dim3 grid, cudaStream_t s, const EmbedGradParams& p)
 {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    return e != cudaSuccess ? e : launch_pdl(kernel, grid, kThreads, smem, s, p);
+    static std::atomic<uint64_t> asked{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (!(asked.load(std::memory_order_relaxed) & bit) || bit == 0) {
+        e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kWarps * kRingBytes));
+        if (e != cudaSuccess) return e;
+        asked.fetch_or(bit, std::memory_order_relaxed);
+    }
+    return launch_pdl(KERNEL, grid, kThreads, kWarps * kRingBytes, s, p);
 }
 
 unsigned blocks_for(uint64_t items, uint64_t per) { return (unsigned)((items + per - 1) / per); }
@@ -940,9 +952,9 @@ cudaError_t reduce_typed(const EmbedGradParams& p, int* launches, cudaStream_t s
     if constexpr (VEC * sizeof(typename In::T) < 4) {
         e = launch_pdl(embed_reduce_narrow_kernel<In, Out, VEC>, grid, kThreads, 0, s, p);
     } else if (p.accumulate && p.nout == 1) {
-        e = launch_ring(embed_reduce_kernel<In, Out, VEC, true>, grid, kWarps * kRingBytes, s, p);
+        e = launch_ring<embed_reduce_kernel<In, Out, VEC, true>>(grid, s, p);
     } else {
-        e = launch_ring(embed_reduce_kernel<In, Out, VEC, false>, grid, kWarps * kRingBytes, s, p);
+        e = launch_ring<embed_reduce_kernel<In, Out, VEC, false>>(grid, s, p);
     }
     if (e != cudaSuccess) return e;
     *launches += 1;
