@@ -349,7 +349,7 @@ rr_status_t clip_grads(const rr_tensor_list_t* grads, float max_norm, float eps,
     add_spans(grads, n, true, spans);
     if ((st = check_scratch(norm, ws, ws_bytes, workspace_bytes(norm_slots(grads)), spans)) != RR_OK) return st;
     if ((st = check_device_ptrs(grads->ptrs, n * grads->ntensors)) != RR_OK) return st;
-    Passes run{static_cast<double*>(ws), stream, n * S >= kBulkClipBytes};
+    Passes run{static_cast<double*>(ws), stream, n * S >= kBulkClipBytes && bulk_wait_counters()};
     ClipArgs a{};
     a.in_l2 = S <= kKeepBytes;
     a.max_norm = max_norm;
@@ -397,7 +397,7 @@ rr_status_t bucket_allreduce_clip(const rr_bucket_plan_t* plan, int b0, int nb, 
     if (synced) add_spans(synced, n, true, spans);
     const size_t need = workspace_bytes(clip_partials(plan, b0, nb, n, synced));
     if ((st = check_scratch(norm, ws, ws_bytes, need, spans)) != RR_OK) return st;
-    Passes run{static_cast<double*>(ws), stream, n * (S + R) >= kBulkClipBytes};
+    Passes run{static_cast<double*>(ws), stream, n * (S + R) >= kBulkClipBytes && bulk_wait_counters()};
     ClipArgs a{};
     a.max_norm = max_norm;
     a.eps = eps;

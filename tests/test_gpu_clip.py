@@ -246,6 +246,22 @@ def test_clipped_sync_against_64_bits(n, dtype, op, sizes, synced):
     rrv.check_timeouts()
 
 
+@pytest.mark.parametrize("n", [48, 64])
+@pytest.mark.parametrize("dtype", list(DT))
+def test_clipped_sync_of_many_ranks(n, dtype):
+    sizes = [9000, 70_001, 5]
+    a, b = rank_grads(n, sizes, DT[dtype]), rank_grads(n, sizes, DT[dtype])
+    plan = rrv.BucketPlan(sizes, dtype, 16384)
+    plan.all_reduce_range(0, plan.num_buckets, tensors(a), "avg")
+    got = plan.all_reduce_clip(tensors(b), math.inf, "avg")
+    assert abs(float(got) - norm64([g.t for g in a[0]])) <= 2.0 ** -8 * float(got)  # a is rounded to its type
+    for ra, rb in zip(a, b):
+        for x, y in zip(ra, rb):
+            assert torch.equal(x.t, y.t)
+            y.check()
+    rrv.check_timeouts()
+
+
 def test_clipped_sync_of_a_range_and_of_many_tensors():
     n, sizes = 8, [(i * 31) % 500 + 1 for i in range(700)]
     ranks = rank_grads(n, sizes, torch.bfloat16)

@@ -264,6 +264,40 @@ def test_embed_refusals_on_the_gpu():
         rrv.embedding_grad(ids, [o], [w, w])  # the same replica twice
 
 
+def test_wide_rows_many_ranks_and_far_ids():
+    run_grad(2, 5, 3, 1 << 20, torch.bfloat16, "zipf", nout=1)
+    run_grad(1, 40, 3, (1 << 18) + 1, torch.float16, "runs", accumulate=True)
+    far = torch.tensor([1 << 40, -(1 << 40), 2, (1 << 31) - 1, 1 << 31, -1, 2, (1 << 63) - 1, -(1 << 63)], device="cuda")
+    n, v, d = 64, 5, 24
+    tables = [values(r, v * d, torch.float32).view(v, d) for r in range(n)]
+    outs = [torch.full((len(far), d), 7.0, device="cuda") for _ in range(n)]
+    rrv.embedding([far] * n, tables, outs, 3.0)
+    for w, o in zip(tables, outs):
+        want = torch.zeros(len(far), d, device="cuda")
+        want[[2, 6]] = w[2] * 3.0
+        assert torch.equal(o, want)
+    g = [torch.full((v, d), 7.0, device="cuda") for _ in range(n)]
+    rrv.embedding_grad([far] * n, outs, g, "sum")
+    check_grad([far] * n, outs, g, g, v, 1.0, False)
+
+
+def test_calls_on_two_streams_at_once():
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    n, t, v, d = 2, 3000, 900, 136
+    work = []
+    for k in range(2):
+        ids = [draw_ids(9 * k + r, t, v, torch.int32) for r in range(n)]
+        x = [values(50 * k + r, t * d, torch.bfloat16).view(t, d) for r in range(n)]
+        work.append((ids, x, [torch.empty(v, d, dtype=torch.bfloat16, device="cuda") for _ in range(n)]))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for (ids, x, g), s in zip(work, streams):
+            rrv.embedding_grad(ids, x, g, "avg", stream=s)
+    torch.cuda.synchronize()
+    for ids, x, g in work:
+        check_grad(ids, x, g, g, v, 1.0 / n, False)
+
+
 # ------------------------------------------------------- a step, as it is used
 
 def step_inputs(n=4, t=300, v=700, d=72):
