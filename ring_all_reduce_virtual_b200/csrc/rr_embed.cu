@@ -18,9 +18,9 @@
 //
 // Both are bound by HBM.  Lookup: 8 x 2048 bf16 rows of 2048 (101 MB) in 17.9 us, 5.6
 // TB/s.  Gradient: 8 x 2048 tokens into eight bf16 tables of 32000 x 2048 (1.11 GB)
-// in 193 us, 5.8 TB/s: 16 for the sort, 49 for the sums, 128 (at 6.6 TB/s) for
-// the rows without a token; 8 x 8192 tokens onto one fp32 table (470 MB) in 116
-// us: 21, 83 and 12 for the joins.  A sort by a cluster of 8 CTAs in one launch,
+// in 191 us, 5.8 TB/s: 16 for the sort, 49 for the sums, 127 (at 6.6 TB/s) for
+// the rows without a token; 8 x 8192 tokens onto one fp32 table (470 MB) in 110
+// us: 21, 78 and 11 for the joins.  A sort by a cluster of 8 CTAs in one launch,
 // the keys in distributed shared memory, took 18 us for 16384 tokens and 37 for
 // 65536, where the three launches take 16 and 21.
 #include <atomic>
@@ -550,13 +550,16 @@ __device__ __forceinline__ void close_run(const EmbedGradParams& p, const Chunk<
 // same ring, so the sums wait only for loads that were issued several rows
 // ago.  A lane reads only what it copied itself: no barrier.
 //
-// Bound by HBM, with instructions close behind (66 % of the issue slots taken):
-// 8 x 8192 tokens of 2048 bf16 onto one fp32 table move 452 MB in 83 us (5.4
+// Bound by HBM, with instructions close behind (59 % of the issue slots taken):
+// 8 x 8192 tokens of 2048 bf16 onto one fp32 table move 450 MB in 78 us (5.8
 // TB/s).  With the loads of 8 rows held in registers instead (100 registers, 2
 // CTAs per SM, 63 % of the warps' time waiting for memory) the kernel took 150
-// us.  Slices of 512 columns halve the work per row but leave fewer warps and 2
-// CTAs per SM: the call 121 us against 117, and 205 against 194 for 8 x 2048
-// tokens into eight bf16 tables.
+// us.  Slices of 512 columns halve the work per row but leave fewer warps (at 8
+// warps per CTA the call took 121 us against 117, and 205 against 194 for 8 x 2048
+// tokens into eight bf16 tables).
+// Warps per CTA of the sums: with 8 / 4 / 2 / 1 that call takes 116.5 / 114.4 / 112.6 /
+// 110.8 us, because a CTA keeps its shared memory until its slowest span ends.
+constexpr int kReduceWarps = 1;
 constexpr uint32_t kRingBytes = 8192;  // of a warp
 
 template <int B>
@@ -571,7 +574,7 @@ constexpr uint32_t kRingSlot =  // bytes of a warp's slot
     kEmbedCols * (ACC && sizeof(typename Out::T) > sizeof(typename In::T) ? sizeof(typename Out::T) : sizeof(typename In::T));
 
 template <class In, class Out, int VEC, bool ACC>
-__global__ void __launch_bounds__(kThreads) embed_reduce_kernel(const __grid_constant__ EmbedGradParams p)
+__global__ void __launch_bounds__(kReduceWarps * 32) embed_reduce_kernel(const __grid_constant__ EmbedGradParams p)
 {
     using T = typename In::T;
     using TO = typename Out::T;
@@ -583,7 +586,7 @@ __global__ void __launch_bounds__(kThreads) embed_reduce_kernel(const __grid_con
     extern __shared__ __align__(16) unsigned char ring_mem[];
     pdl_begin();
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
-    const uint32_t blk = blockIdx.x * kWarps + warp;
+    const uint32_t blk = blockIdx.x * kReduceWarps + warp;
     if (blk >= p.nblk) return;
     unsigned char* ring = ring_mem + warp * kRingBytes;
     const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
@@ -673,14 +676,14 @@ __global__ void __launch_bounds__(kThreads) embed_reduce_kernel(const __grid_con
 // The same for rows in 2-byte pieces, which cp.async cannot copy: the loads of
 // a few rows in flight in registers.
 template <class In, class Out, int VEC>
-__global__ void __launch_bounds__(kThreads) embed_reduce_narrow_kernel(const __grid_constant__ EmbedGradParams p)
+__global__ void __launch_bounds__(kReduceWarps * 32) embed_reduce_narrow_kernel(const __grid_constant__ EmbedGradParams p)
 {
     using T = typename In::T;
     constexpr int NC = kChunks<VEC>;
     constexpr int G = 4;  // rows whose loads are in flight
     pdl_begin();
     const uint32_t lane = threadIdx.x & 31u;
-    const uint32_t blk = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const uint32_t blk = blockIdx.x * kReduceWarps + (threadIdx.x >> 5);
     if (blk >= p.nblk) return;
     const Span sp = block_span(p, blk);
     const uint32_t c0 = blockIdx.y * kEmbedCols + lane * VEC;
@@ -823,8 +826,8 @@ __device__ __forceinline__ void zero_rows(const EmbedGradParams& p, uint32_t chu
 // lane at each, and joins a run for one slice; a run over many blocks is
 // shared by the CTA's warps, each an eighth of the entries, and the eighths
 // added in order.
-constexpr uint32_t kLongRun = 32;    // entries from which a run is shared: below, an eighth is less than one access deep
-constexpr uint32_t kJoinBlocks = 8;  // blocks per warp: fewer than a shared run's, so a warp meets at most one
+constexpr uint32_t kLongRun = 8;     // entries from which a run is shared (32, with 8 blocks per warp: 1 us more)
+constexpr uint32_t kJoinBlocks = 4;  // blocks per warp: fewer than a shared run's, so a warp meets at most one
 
 template <class Out, int VEC>
 __global__ void __launch_bounds__(kThreads) embed_join_kernel(const __grid_constant__ EmbedGradParams p, uint32_t joins,
@@ -934,11 +937,11 @@ cudaError_t launch_ring(dim3 grid, cudaStream_t s, const EmbedGradParams& p)
     if (e != cudaSuccess) return e;
     const uint64_t bit = dev < 64 ? 1ull << dev : 0;
     if (!(asked.load(std::memory_order_relaxed) & bit) || bit == 0) {
-        e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kWarps * kRingBytes));
+        e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kReduceWarps * kRingBytes));
         if (e != cudaSuccess) return e;
         asked.fetch_or(bit, std::memory_order_relaxed);
     }
-    return launch_pdl(KERNEL, grid, kThreads, kWarps * kRingBytes, s, p);
+    return launch_pdl(KERNEL, grid, kReduceWarps * 32, kReduceWarps * kRingBytes, s, p);
 }
 
 unsigned blocks_for(uint64_t items, uint64_t per) { return (unsigned)((items + per - 1) / per); }
@@ -947,10 +950,10 @@ template <class In, class Out, int VEC>
 cudaError_t reduce_typed(const EmbedGradParams& p, int* launches, cudaStream_t s)
 {
     const uint32_t slices = blocks_for(p.D, kEmbedCols);
-    const dim3 grid(blocks_for(p.nblk, kWarps), slices);
+    const dim3 grid(blocks_for(p.nblk, kReduceWarps), slices);
     cudaError_t e;
     if constexpr (VEC * sizeof(typename In::T) < 4) {
-        e = launch_pdl(embed_reduce_narrow_kernel<In, Out, VEC>, grid, kThreads, 0, s, p);
+        e = launch_pdl(embed_reduce_narrow_kernel<In, Out, VEC>, grid, kReduceWarps * 32, 0, s, p);
     } else if (p.accumulate && p.nout == 1) {
         e = launch_ring<embed_reduce_kernel<In, Out, VEC, true>>(grid, s, p);
     } else {
