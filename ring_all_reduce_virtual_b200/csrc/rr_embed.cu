@@ -18,11 +18,11 @@
 //
 // Both are bound by HBM.  Lookup: 8 x 2048 bf16 rows of 2048 (101 MB) in 17.9 us, 5.6
 // TB/s.  Gradient: 8 x 2048 tokens into eight bf16 tables of 32000 x 2048 (1.11 GB)
-// in 191 us, 5.8 TB/s: 16 for the sort, 49 for the sums, 127 (at 6.6 TB/s) for
-// the rows without a token; 8 x 8192 tokens onto one fp32 table (470 MB) in 110
-// us: 21, 78 and 11 for the joins.  A sort by a cluster of 8 CTAs in one launch,
+// in 191 us, 5.8 TB/s: 14 for the sort, 48 for the sums, 127 (at 6.6 TB/s) for
+// the rows without a token; 8 x 8192 tokens onto one fp32 table (470 MB) in 105
+// us: 16, 77 and 11 for the joins.  A sort by a cluster of 8 CTAs in one launch,
 // the keys in distributed shared memory, took 18 us for 16384 tokens and 37 for
-// 65536, where the three launches take 16 and 21.
+// 65536, where the three launches take 14 and 16.
 #include <atomic>
 
 #include "rr_device.cuh"
@@ -281,14 +281,14 @@ __global__ void __launch_bounds__(kThreads) embed_scan_kernel(const __grid_const
 template <bool SCANNED>
 __global__ void __launch_bounds__(kThreads) embed_place_kernel(const __grid_constant__ EmbedGradParams p, int pass)
 {
-    __shared__ uint32_t cnt[kWarps][1 << kSortMaxBits];
+    __shared__ __align__(16) uint32_t cnt[kWarps][1 << kSortMaxBits];
+    __shared__ __align__(16) uint32_t ahead_of[SCANNED ? 1 : kWarps][1 << kSortMaxBits];
     __shared__ uint32_t sums[kWarps];
     pdl_begin();
     const uint32_t digits = 1u << p.bits, shift = (uint32_t)(pass * p.bits), from = (uint32_t)(p.passes - pass) & 1u;
     const uint32_t* counts = p.counts + (uint64_t)pass * p.ntiles * digits;
     uint32_t* later = p.counts + (uint64_t)(pass + 1) * p.ntiles * digits;
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u;
-    for (uint32_t d = threadIdx.x; d < kWarps << p.bits; d += kThreads) cnt[d >> p.bits][d & (digits - 1)] = 0;
     const uint32_t i0 = blockIdx.x * kSortTile + warp * (kSortTile / kWarps);
     uint32_t key[kSortRounds], pos[kSortRounds], rank[kSortRounds];
 #pragma unroll
@@ -308,20 +308,60 @@ __global__ void __launch_bounds__(kThreads) embed_place_kernel(const __grid_cons
             first[1] = counts[(uint64_t)blockIdx.x * digits + d2 + 1];
         }
     } else {
+        // a warp adds up every eighth tile's counts, four digits per lane and
+        // access, four tiles in flight; the warps' sums meet in shared memory
+        // (cnt is not in use yet)
+        constexpr int Q = (1 << kSortMaxBits) / 128, U = 4;
+        const uint32_t dl = min(lane * 4u, digits - 4u);  // fewer than 128 digits: the last lanes repeat and are not kept
+        uint4 tot[Q], bef[Q];
+#pragma unroll
+        for (int q = 0; q < Q; ++q) tot[q] = bef[q] = make_uint4(0u, 0u, 0u, 0u);
+        for (uint32_t t0 = warp; t0 < p.ntiles; t0 += kWarps * U) {
+            uint4 c[U][Q];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const uint32_t t = min(t0 + (uint32_t)u * kWarps, p.ntiles - 1u);
+#pragma unroll
+                for (int q = 0; q < Q; ++q)
+                    if ((uint32_t)q * 128u < digits)
+                        c[u][q] = *reinterpret_cast<const uint4*>(counts + (uint64_t)t * digits + (uint32_t)q * 128u + dl);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const uint32_t t = t0 + (uint32_t)u * kWarps;
+                if (t >= p.ntiles) break;
+                const bool before = t < blockIdx.x;
+#pragma unroll
+                for (int q = 0; q < Q; ++q) {
+                    if ((uint32_t)q * 128u >= digits) break;
+                    const uint4 v = c[u][q];
+                    tot[q] = make_uint4(tot[q].x + v.x, tot[q].y + v.y, tot[q].z + v.z, tot[q].w + v.w);
+                    if (before) bef[q] = make_uint4(bef[q].x + v.x, bef[q].y + v.y, bef[q].z + v.z, bef[q].w + v.w);
+                }
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            const uint32_t d = (uint32_t)q * 128u + lane * 4u;
+            if (d >= digits) continue;
+            *reinterpret_cast<uint4*>(&cnt[warp][d]) = tot[q];
+            *reinterpret_cast<uint4*>(&ahead_of[warp][d]) = bef[q];
+        }
+        __syncthreads();
         uint32_t total[2] = {0, 0}, ahead[2] = {0, 0};
         if (d2 < digits)
-#pragma unroll 8
-            for (uint32_t t = 0; t < p.ntiles; ++t) {
-                const uint2 c = *reinterpret_cast<const uint2*>(counts + (uint64_t)t * digits + d2);
-                total[0] += c.x;
-                total[1] += c.y;
-                ahead[0] += t < blockIdx.x ? c.x : 0;
-                ahead[1] += t < blockIdx.x ? c.y : 0;
-            }
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    total[e] += cnt[w][d2 + e];
+                    ahead[e] += ahead_of[w][d2 + e];
+                }
         scan_digits(total, sums);
         first[0] = total[0] + ahead[0];
         first[1] = total[1] + ahead[1];
     }
+    for (uint32_t d = threadIdx.x; d < kWarps << p.bits; d += kThreads) cnt[d >> p.bits][d & (digits - 1)] = 0;
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < kSortRounds; ++j) {

@@ -108,7 +108,7 @@ uint64_t up(uint64_t x, uint64_t to) { return (x + to - 1) / to * to; }
 // short of warps (one per block and slice of the columns), more where the
 // partial sums would need more than 8192 rows.  With 8 / 16 / 32: 300 tokens of
 // width 515 44 / 48 / 54 us waited for, 16384 of 2048 (16 here) 197 / 194 / 196;
-// with 16 / 32 / 64, 65536 of 2048 119 / 116 / 139.
+// with 16 / 32 / 64, 65536 of 2048 111 / 105 / 108.
 uint32_t block_positions(uint64_t M, uint64_t D)
 {
     if (M > 32 * 4096) return (uint32_t)(32 * ceil_div(M, 32 * 4096));
@@ -123,7 +123,7 @@ Layout layout(uint64_t M, uint64_t V, uint64_t D)
     int total = 1;  // bits of the largest key, V
     while (V >> total) ++total;
     l.passes = (total + kSortMaxBits - 1) / kSortMaxBits;
-    l.bits = (total + l.passes - 1) / l.passes;
+    l.bits = std::max(2, (total + l.passes - 1) / l.passes);  // counts are read four digits at a time
     l.ntiles = (uint32_t)ceil_div(M, kSortTile);
     l.K = block_positions(M, D);
     l.nblk = (uint32_t)ceil_div(M, l.K);

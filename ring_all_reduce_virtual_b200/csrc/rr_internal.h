@@ -312,9 +312,9 @@ cudaError_t launch_embed_lookup(int dtype, int vec, const EmbedLookupParams& p, 
 cudaError_t launch_embed_sort(const EmbedGradParams& p, int* launches, cudaStream_t s);
 cudaError_t launch_embed_reduce(int dtype, int out_dtype, int vec, const EmbedGradParams& p, int* launches,
                                 cudaStream_t s);
-// Keys per CTA of a sort pass: 65536 tokens' gradient 137.7 / 133.0 / 142.3 us
-// with 2048 / 1024 / 512 (more tiles spread a pass over more SMs, and each CTA
-// reads more tiles' counts).
+// Keys per CTA of a sort pass: 65536 tokens' gradient 109.7 / 104.6 / 105.4 us with
+// 2048 / 1024 / 512, 16384 tokens' 196.9 / 191.5 / 188.5 (more tiles spread a pass
+// over more SMs; each CTA reads every tile's counts, so many tokens want few).
 constexpr uint32_t kSortTile = 1024;
 constexpr int kSortMaxBits = 9;        // bits per digit, at most
 // Tokens that are sorted by counting smaller ids, in one launch: against the
@@ -323,7 +323,7 @@ constexpr int kSortMaxBits = 9;        // bits per digit, at most
 constexpr uint32_t kRankMax = 2048;
 // Tiles from which a sort pass scans its counts in a launch of its own instead
 // of every CTA summing all of them, which grows with the square of the tiles:
-// at 512 tiles still 203 us for the call against 266.
+// at 512 tiles 152 us for the call against 266.
 constexpr uint32_t kScanTiles = 1024;
 constexpr uint32_t kEmbedCols = 256;   // columns of a warp's slice of a row
 
