@@ -22,6 +22,7 @@
 // and 800 for the scaling (6.7), where the copy peak is 6.55 TB/s.
 #include "rr_bulk.cuh"
 #include "rr_clip.cuh"
+#include "rr_launch.cuh"
 
 namespace rr {
 
@@ -251,18 +252,7 @@ cudaError_t park_sized(const ParkParams<Fold>& bp, cudaStream_t s)
     const int n = bp.f.n;
     const unsigned work = (unsigned)bp.f.tile0[bp.f.nseg];
     auto go = [&](void (*kernel)(ParkParams<Fold>), uint32_t smem) {
-        cudaLaunchAttribute attr{};
-        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr.val.programmaticStreamSerializationAllowed = 1;
-        cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3(work);
-        cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = smem;
-        cfg.stream = s;
-        cfg.attrs = &attr;
-        cfg.numAttrs = 1;
-        const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, bp);
-        return e != cudaSuccess ? e : cudaGetLastError();
+        return launch_pdl(kernel, dim3(work), kThreads, smem, s, bp);
     };
     if (!bp.f.vec_ok || !bp.waits) return go(bucket_park_any_kernel<G, OP, MODE, Fold>, 0);
     // compiled rank counts of the calls that get here (clip_folds_twice)

@@ -15,6 +15,7 @@
 // atomics), so a call's bits depend only on its tensors.
 #include "rr_bulk.cuh"
 #include "rr_clip.cuh"
+#include "rr_launch.cuh"
 
 namespace rr {
 
@@ -273,24 +274,6 @@ __global__ void __launch_bounds__(kThreads) clip_bulk_kernel(const __grid_consta
     }
 }
 
-// A launch as a programmatic dependent of the stream's previous kernel.
-template <class... A>
-cudaError_t launch_pdl(void (*kernel)(A...), unsigned grid, uint32_t smem, cudaStream_t s, const A&... a)
-{
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a...);
-    return e != cudaSuccess ? e : cudaGetLastError();
-}
-
 // The same table with fewer entries: a short list's parameter block.
 template <class Small>
 Small shrink(const NormParams& p)
@@ -310,8 +293,8 @@ template <class Ty>
 cudaError_t norm_typed(const NormParams& p, unsigned grid, cudaStream_t s)
 {
     if (p.nt <= kNormTensorsSmall)
-        return launch_pdl(norm_kernel<Ty, kNormTensorsSmall>, grid, 0, s, shrink<NormParamsT<kNormTensorsSmall>>(p));
-    return launch_pdl(norm_kernel<Ty, kNormTensors>, grid, 0, s, p);
+        return launch_pdl(norm_kernel<Ty, kNormTensorsSmall>, dim3(grid), kThreads, 0, s, shrink<NormParamsT<kNormTensorsSmall>>(p));
+    return launch_pdl(norm_kernel<Ty, kNormTensors>, dim3(grid), kThreads, 0, s, p);
 }
 
 template <class Ty, bool PARKED>
@@ -328,9 +311,9 @@ cudaError_t scale_typed(const ScaleParams& p, unsigned grid, cudaStream_t s)
         q.clip = p.clip;
         q.n = p.n;
         q.nt = p.nt;
-        return launch_pdl(clip_scale_kernel<Ty, PARKED, kScaleTensorsSmall, kScalePtrsSmall>, grid, 0, s, q);
+        return launch_pdl(clip_scale_kernel<Ty, PARKED, kScaleTensorsSmall, kScalePtrsSmall>, dim3(grid), kThreads, 0, s, q);
     }
-    return launch_pdl(clip_scale_kernel<Ty, PARKED, kScaleTensors, kScalePtrs>, grid, 0, s, p);
+    return launch_pdl(clip_scale_kernel<Ty, PARKED, kScaleTensors, kScalePtrs>, dim3(grid), kThreads, 0, s, p);
 }
 
 template <class Ty, bool PARKED>
@@ -345,7 +328,7 @@ cudaError_t bulk_typed(const ScaleParams& p, unsigned grid, cudaStream_t s)
     bp.waits = wait.waits;
     bp.hold = wait.hold;
     bp.spin = wait.spin;
-    return launch_pdl(clip_bulk_kernel<Ty, PARKED>, grid, kBulkScaleBytes, s, bp);
+    return launch_pdl(clip_bulk_kernel<Ty, PARKED>, dim3(grid), kThreads, kBulkScaleBytes, s, bp);
 }
 
 }  // namespace
@@ -374,10 +357,10 @@ cudaError_t launch_norm(int dtype, const NormParams& p, int* slots, cudaStream_t
 cudaError_t launch_norm_join(const double* in, int64_t count, double* out, int* slots, cudaStream_t s)
 {
     *slots = kJoinCtas;
-    return launch_pdl(norm_join_kernel, (unsigned)kJoinCtas, 0, s, in, count, out);
+    return launch_pdl(norm_join_kernel, dim3(kJoinCtas), kThreads, 0, s, in, count, out);
 }
 
-cudaError_t launch_norm_finish(const ClipArgs& a, cudaStream_t s) { return launch_pdl(norm_finish_kernel, 1u, 0, s, a); }
+cudaError_t launch_norm_finish(const ClipArgs& a, cudaStream_t s) { return launch_pdl(norm_finish_kernel, dim3(1), kThreads, 0, s, a); }
 
 cudaError_t launch_clip_scale(int dtype, bool parked, bool bulk, const ScaleParams& p, cudaStream_t s)
 {

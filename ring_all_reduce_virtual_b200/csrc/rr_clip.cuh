@@ -16,15 +16,6 @@
 
 namespace rr {
 
-// Start of a kernel launched as a programmatic dependent of the stream's
-// previous one: wait for it and its memory, then let the next be scheduled.
-// A no-op in a plain launch.
-__device__ __forceinline__ void pdl_begin()
-{
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
 // Bulk store (a multiple of 16 bytes, shared to global, in the thread's bulk
 // group) of bytes that L2 should evict before those the pass will still read.
 __device__ __forceinline__ uint64_t evict_first_policy()

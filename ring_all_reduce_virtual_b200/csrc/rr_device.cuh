@@ -311,6 +311,15 @@ __device__ __forceinline__ uint4 shift_window(const uint4& lo, const uint4& hi, 
     return make_uint4(w0, w1, w2, w3);
 }
 
+// Start of a kernel launched as a programmatic dependent of the stream's
+// previous one (launch_pdl): wait for it and its memory, then let the next be
+// scheduled.  A no-op in a plain launch.
+__device__ __forceinline__ void pdl_begin()
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // The segment owning work item w: the last s with prefix[s] <= w (segments
 // without tiles have prefix[s] == prefix[s + 1] and are never returned).
 __device__ __forceinline__ int find_segment(const uint64_t* prefix, int nseg, uint64_t w)

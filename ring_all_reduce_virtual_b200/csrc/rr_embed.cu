@@ -25,18 +25,11 @@
 // 65536, where the three launches take 14 and 16.
 #include <atomic>
 
-#include "rr_device.cuh"
-#include "rr_internal.h"
+#include "rr_launch.cuh"
 
 namespace rr {
 
 namespace {
-
-__device__ __forceinline__ void pdl_begin()
-{
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
 
 // VEC consecutive elements of a type as one access (two for 32 bytes).
 template <class Ty, int VEC>
@@ -168,6 +161,8 @@ __global__ void __launch_bounds__(kRankThreads) embed_rank_kernel(const __grid_c
     __shared__ __align__(16) uint32_t keys[kRankMax];
     pdl_begin();
     const uint32_t M = p.M, padded = (M + 15u) & ~15u;
+    if (blockIdx.x == 0)
+        for (uint32_t c = threadIdx.x; c * kEmbedCols < p.D; c += kRankThreads) p.arrived[c] = 0u;
 #pragma unroll 8
     for (uint32_t i = threadIdx.x; i < padded; i += kRankThreads) keys[i] = i < M ? position_key(p, i) : 0xffffffffu;
     __syncthreads();
@@ -582,6 +577,86 @@ __device__ __forceinline__ void close_run(const EmbedGradParams& p, const Chunk<
         write_row<Out, VEC>(p, key, c0, acc);
 }
 
+// The entries of the cut run that begins in block blk (its partial sums); 0:
+// none begins there.
+__device__ __forceinline__ uint32_t cut_entries(const EmbedGradParams& p, uint32_t blk)
+{
+    const uint32_t* keys = sorted_keys(p);
+    const uint64_t on = ((uint64_t)blk + 2) * p.K;
+    if (on >= p.M) return 0;
+    const uint32_t end = (blk + 1) * p.K, key = keys[end - 1];
+    const uint32_t before = blk > 0 ? keys[blk * p.K - 1] : 0xffffffffu;
+    if (key >= (uint32_t)p.V || keys[on] != key || before == key) return 0;
+    uint32_t lo = blk + 2, hi = p.nblk - 1;  // the last block whose first key is this one
+    while (lo < hi) {
+        const uint32_t mid = (lo + hi + 1) / 2;
+        if (keys[mid * p.K] == key) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo - blk + 1;
+}
+
+// Adds the partial sums of entries [a, b) of a run to acc, in order: entry 0
+// is the last partial of block blk, entry i the first partial of block blk + i.
+template <int VEC>
+__device__ __forceinline__ void add_parts(const EmbedGradParams& p, uint32_t blk, uint32_t a, uint32_t b, uint32_t c0,
+                                          float (&acc)[kChunks<VEC>][VEC])
+{
+    constexpr int NC = kChunks<VEC>, U = 1024 / (int)kEmbedCols;  // entries whose loads are in flight
+    for (uint32_t i0 = a; i0 < b; i0 += U) {
+        Vec<F32T, VEC> x[U][NC];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t i = i0 + u;
+            const float* q = p.part + (i == 0 ? (uint64_t)p.nblk + blk : (uint64_t)blk + i) * p.Dp;
+#pragma unroll
+            for (int k = 0; k < NC; ++k) {
+                const uint32_t c = c0 + (uint32_t)k * 32u * VEC;
+                if (i < b && c < p.D) x[u][k].load(q + c);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (i0 + u >= b) break;
+#pragma unroll
+            for (int k = 0; k < NC; ++k) {
+                if (c0 + (uint32_t)k * 32u * VEC >= p.D) continue;
+#pragma unroll
+                for (int l = 0; l < VEC; ++l) acc[k][l] = __fadd_rn(acc[k][l], __uint_as_float(x[u][k].r[l]));
+            }
+        }
+    }
+}
+
+// Few blocks (kJoinHere): the warp that comes last at a slice joins its cut runs
+// itself, which saves the join's launch.  The count of those that came starts
+// at zero with the sort's launch; a partial sum is in memory before its warp
+// counts itself.
+template <class Out, int VEC>
+__device__ __forceinline__ void join_when_last(const EmbedGradParams& p, uint32_t slice, uint32_t c0)
+{
+    const uint32_t lane = threadIdx.x & 31u;
+    __threadfence();
+    __syncwarp();
+    uint32_t came = 0;
+    if (lane == 0) came = atomicAdd(&p.arrived[slice], 1u);
+    if (__shfl_sync(0xffffffffu, came, 0) + 1 != p.nblk) return;
+    __threadfence();
+    for (uint32_t b0 = 0; b0 < p.nblk; b0 += 32) {
+        const uint32_t mine = b0 + lane < p.nblk ? cut_entries(p, b0 + lane) : 0;
+        for (uint32_t todo = __ballot_sync(0xffffffffu, mine > 0); todo; todo &= todo - 1) {
+            const uint32_t l = __ffs(todo) - 1, n = __shfl_sync(0xffffffffu, mine, l);
+            float acc[kChunks<VEC>][VEC];
+#pragma unroll
+            for (int k = 0; k < kChunks<VEC>; ++k)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) acc[k][e] = 0.0f;
+            add_parts<VEC>(p, b0 + l, 0, n, c0, acc);
+            write_row<Out, VEC>(p, sorted_keys(p)[(b0 + l + 1) * p.K], c0, acc);
+        }
+    }
+}
+
 // A warp sums one slice of the columns over one block's span.
 //
 // The rows stream through a ring of slots in shared memory, kRingBytes a warp,
@@ -600,6 +675,7 @@ __device__ __forceinline__ void close_run(const EmbedGradParams& p, const Chunk<
 // Warps per CTA of the sums: with 8 / 4 / 2 / 1 that call takes 116.5 / 114.4 / 112.6 /
 // 110.8 us, because a CTA keeps its shared memory until its slowest span ends.
 constexpr int kReduceWarps = 1;
+static_assert(kReduceWarps == 1, "join_when_last counts a warp per block");
 constexpr uint32_t kRingBytes = 8192;  // of a warp
 
 template <int B>
@@ -613,7 +689,7 @@ template <class In, class Out, int VEC, bool ACC>
 constexpr uint32_t kRingSlot =  // bytes of a warp's slot
     kEmbedCols * (ACC && sizeof(typename Out::T) > sizeof(typename In::T) ? sizeof(typename Out::T) : sizeof(typename In::T));
 
-template <class In, class Out, int VEC, bool ACC>
+template <class In, class Out, int VEC, bool ACC, bool JOIN>
 __global__ void __launch_bounds__(kReduceWarps * 32) embed_reduce_kernel(const __grid_constant__ EmbedGradParams p)
 {
     using T = typename In::T;
@@ -711,6 +787,7 @@ __global__ void __launch_bounds__(kReduceWarps * 32) embed_reduce_kernel(const _
         asm volatile("cp.async.wait_group 0;" ::: "memory");  // the ring is free for the next chunk
         if (ch.n < 32) break;
     }
+    if constexpr (JOIN) join_when_last<Out, VEC>(p, blockIdx.y, c0);
 }
 
 // The same for rows in 2-byte pieces, which cp.async cannot copy: the loads of
@@ -766,38 +843,6 @@ __global__ void __launch_bounds__(kReduceWarps * 32) embed_reduce_narrow_kernel(
             }
         }
         if (ch.n < 32) break;
-    }
-}
-
-// Adds the partial sums of entries [a, b) of a run to acc, in order: entry 0
-// is the last partial of block blk, entry i the first partial of block blk + i.
-template <int VEC>
-__device__ __forceinline__ void add_parts(const EmbedGradParams& p, uint32_t blk, uint32_t a, uint32_t b, uint32_t c0,
-                                          float (&acc)[kChunks<VEC>][VEC])
-{
-    constexpr int NC = kChunks<VEC>, U = 1024 / (int)kEmbedCols;  // entries whose loads are in flight
-    for (uint32_t i0 = a; i0 < b; i0 += U) {
-        Vec<F32T, VEC> x[U][NC];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const uint32_t i = i0 + u;
-            const float* q = p.part + (i == 0 ? (uint64_t)p.nblk + blk : (uint64_t)blk + i) * p.Dp;
-#pragma unroll
-            for (int k = 0; k < NC; ++k) {
-                const uint32_t c = c0 + (uint32_t)k * 32u * VEC;
-                if (i < b && c < p.D) x[u][k].load(q + c);
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (i0 + u >= b) break;
-#pragma unroll
-            for (int k = 0; k < NC; ++k) {
-                if (c0 + (uint32_t)k * 32u * VEC >= p.D) continue;
-#pragma unroll
-                for (int l = 0; l < VEC; ++l) acc[k][l] = __fadd_rn(acc[k][l], __uint_as_float(x[u][k].r[l]));
-            }
-        }
     }
 }
 
@@ -887,21 +932,6 @@ __global__ void __launch_bounds__(kThreads) embed_join_kernel(const __grid_const
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
     const uint32_t slice = blockIdx.x % slices, blk0 = (blockIdx.x / slices * kWarps + warp) * kJoinBlocks;
     const uint32_t c0 = slice * kEmbedCols + lane * VEC;
-    // the entries of the cut run that begins in block blk; 0: none
-    auto entries = [&](uint32_t blk) -> uint32_t {
-        const uint64_t on = ((uint64_t)blk + 2) * p.K;
-        if (on >= p.M) return 0;
-        const uint32_t end = (blk + 1) * p.K, key = keys[end - 1];
-        const uint32_t before = blk > 0 ? keys[blk * p.K - 1] : 0xffffffffu;
-        if (key >= (uint32_t)p.V || keys[on] != key || before == key) return 0;
-        uint32_t lo = blk + 2, hi = p.nblk - 1;  // the last block whose first key is this one
-        while (lo < hi) {
-            const uint32_t mid = (lo + hi + 1) / 2;
-            if (keys[mid * p.K] == key) lo = mid;
-            else hi = mid - 1;
-        }
-        return lo - blk + 1;
-    };
     float acc[NC][VEC];
     auto clear = [&] {
 #pragma unroll
@@ -909,7 +939,7 @@ __global__ void __launch_bounds__(kThreads) embed_join_kernel(const __grid_const
 #pragma unroll
             for (int l = 0; l < VEC; ++l) acc[k][l] = 0.0f;
     };
-    const uint32_t mine = lane < kJoinBlocks ? entries(blk0 + lane) : 0;
+    const uint32_t mine = lane < kJoinBlocks ? cut_entries(p, blk0 + lane) : 0;
     const uint32_t shared_run = __ballot_sync(0xffffffffu, mine > kLongRun);
     if (lane == 0) long_run[warp] = 0;
     __syncwarp();
@@ -949,23 +979,6 @@ __global__ void __launch_bounds__(kThreads) embed_join_kernel(const __grid_const
     }
 }
 
-template <class... A>
-cudaError_t launch_pdl(void (*kernel)(A...), dim3 grid, unsigned threads, uint32_t smem, cudaStream_t s, const A&... a)
-{
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a...);
-    return e != cudaSuccess ? e : cudaGetLastError();
-}
-
 // A ring kernel: more shared memory than a launch gets by default, which is
 // asked for once per kernel and device.
 template <void (*KERNEL)(EmbedGradParams)>
@@ -995,9 +1008,13 @@ cudaError_t reduce_typed(const EmbedGradParams& p, int* launches, cudaStream_t s
     if constexpr (VEC * sizeof(typename In::T) < 4) {
         e = launch_pdl(embed_reduce_narrow_kernel<In, Out, VEC>, grid, kReduceWarps * 32, 0, s, p);
     } else if (p.accumulate && p.nout == 1) {
-        e = launch_ring<embed_reduce_kernel<In, Out, VEC, true>>(grid, s, p);
+        if (p.nblk > 2 && p.nblk <= kJoinHere && p.M <= kRankMax) {
+            *launches += 1;
+            return launch_ring<embed_reduce_kernel<In, Out, VEC, true, true>>(grid, s, p);
+        }
+        e = launch_ring<embed_reduce_kernel<In, Out, VEC, true, false>>(grid, s, p);
     } else {
-        e = launch_ring<embed_reduce_kernel<In, Out, VEC, false>>(grid, s, p);
+        e = launch_ring<embed_reduce_kernel<In, Out, VEC, false, false>>(grid, s, p);
     }
     if (e != cudaSuccess) return e;
     *launches += 1;

@@ -97,7 +97,7 @@ rr_status_t embedding(const void* const* ids, rr_id_type_t id_type, const void* 
 // The gradient's workspace, in the order in which it is laid out; every part
 // starts on a 256-byte boundary.
 struct Layout {
-    uint64_t key[2], pos[2], counts, part, bytes;
+    uint64_t key[2], pos[2], counts, part, arrived, bytes;
     uint32_t ntiles, K, nblk, Dp;
     int passes, bits;
 };
@@ -138,6 +138,7 @@ Layout layout(uint64_t M, uint64_t V, uint64_t D)
     for (int k = 0; k < 2; ++k) l.pos[k] = part(M * 4);
     l.counts = part(((uint64_t)l.passes * l.ntiles << l.bits) * 4);
     l.part = part(2ull * l.nblk * l.Dp * 4);
+    l.arrived = part(ceil_div(D, kEmbedCols) * 4);
     l.bytes = at;
     return l;
 }
@@ -202,6 +203,7 @@ rr_status_t embedding_grad(const void* const* ids, rr_id_type_t id_type, const v
     }
     p.counts = reinterpret_cast<uint32_t*>(base + l.counts);
     p.part = reinterpret_cast<float*>(base + l.part);
+    p.arrived = reinterpret_cast<uint32_t*>(base + l.arrived);
     p.passes = l.passes;
     p.bits = l.bits;
     p.ntiles = l.ntiles;

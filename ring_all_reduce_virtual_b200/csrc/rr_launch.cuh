@@ -21,6 +21,26 @@ inline cudaError_t launch_all(void (*kernel)(P), const P& p, uint64_t work, cuda
     return cudaGetLastError();
 }
 
+// A launch as a programmatic dependent of the stream's previous kernel: its
+// CTAs are scheduled while that one drains and start with pdl_begin.
+template <class... A>
+inline cudaError_t launch_pdl(void (*kernel)(A...), dim3 grid, unsigned threads, uint32_t smem, cudaStream_t s,
+                              const A&... a)
+{
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a...);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 template <class F>
 inline cudaError_t with_type(int dtype, int op, F&& f)
 {
