@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kThreads, 4) clip_scale_kernel(const __grid_co
     constexpr uint64_t TV = (uint64_t)kThreads * kScaleU;
     __shared__ double sh[kThreads / 32];
     pdl_begin();
-    const float c = clip_coef(p.clip, sh);
+    float c = 0.0f;
     const uint64_t total = p.tile0[p.nt], tid = threadIdx.x;
     const int n = p.n;
     for (uint64_t i = blockIdx.x; i < total; i += gridDim.x) {
@@ -121,6 +121,20 @@ __global__ void __launch_bounds__(kThreads, 4) clip_scale_kernel(const __grid_co
         T* const* ptr = reinterpret_cast<T* const*>(&p.ptr[(size_t)t * n]);
         const T* src = ptr[0];
         const T* low = PARKED ? ptr[1] : ptr[0];
+        uint64_t head = (uint64_t)((L - phase_of(src, L)) & (L - 1));
+        if (head > len) head = len;
+        const uint64_t nv = p.vec[t] ? (len - head) / L : 0, tail = len - head - nv * L;
+        const uint64_t v0 = tile * TV + tid;
+        uint4 raw[kScaleU], lo[PARKED ? kScaleU : 1];
+#pragma unroll
+        for (int u = 0; u < kScaleU; ++u) {
+            const uint64_t v = v0 + (uint64_t)u * kThreads;
+            if (v < nv) {
+                raw[u] = ld_keep(src + head + v * L);
+                if constexpr (PARKED) lo[u] = ld_keep(low + head + v * L);
+            }
+        }
+        if (i == blockIdx.x) c = clip_coef(p.clip, sh);  // while the first tile is on the way
         auto one = [&](uint64_t e) {
             float x;
             if constexpr (PARKED) x = __uint_as_float(((uint32_t)src[e] << 16) | (uint32_t)low[e]);
@@ -133,20 +147,7 @@ __global__ void __launch_bounds__(kThreads, 4) clip_scale_kernel(const __grid_co
             for (uint64_t e = e0 + tid; e < len && e < e0 + TV * L; e += kThreads) one(e);
             continue;
         }
-        uint64_t head = (uint64_t)((L - phase_of(src, L)) & (L - 1));
-        if (head > len) head = len;
-        const uint64_t nv = (len - head) / L, tail = len - head - nv * L;
         if (tile == 0 && tid < head + tail) one(tid < head ? tid : head + nv * L + (tid - head));
-        const uint64_t v0 = tile * TV + tid;
-        uint4 raw[kScaleU], lo[PARKED ? kScaleU : 1];
-#pragma unroll
-        for (int u = 0; u < kScaleU; ++u) {
-            const uint64_t v = v0 + (uint64_t)u * kThreads;
-            if (v < nv) {
-                raw[u] = ld_keep(src + head + v * L);
-                if constexpr (PARKED) lo[u] = ld_keep(low + head + v * L);
-            }
-        }
 #pragma unroll
         for (int u = 0; u < kScaleU; ++u) {
             float a[L];
