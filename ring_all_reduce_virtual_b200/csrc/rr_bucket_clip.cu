@@ -33,6 +33,9 @@ namespace {
 // 76.3 / 68.2 / 60.9 with 32 KB (fewer, longer CTAs: short sets are bound by a
 // CTA's latency), 40 KB as 32; 1 GB of 8 ranks 393 and 388 us.
 constexpr uint32_t kParkBytes = 32768;
+// And of the passes that fold twice: 48 / 144 MB / 1 GB of 3 bf16 ranks 31.2 / 77.1 /
+// 473 us with 32 KB, 29.5 / 74.0 / 469 with 24; 2 ranks alike with both.
+constexpr uint32_t kTwiceBytes = 24576;
 
 enum FoldMode : int { kPark = 0, kSquares = 1, kScaled = 2 };
 
@@ -99,7 +102,7 @@ __global__ void __launch_bounds__(kThreads) bucket_park_kernel(const __grid_cons
     pdl_begin();
     const Fold& p = bp.f;
     const int n = NS > 0 ? NS : p.n;
-    const uint32_t TV = NS > 0 ? kParkBytes / (NS > 0 ? NS : 1) / 16 : bp.tv;
+    const uint32_t TV = NS > 0 ? (MODE == kPark ? kParkBytes : kTwiceBytes) / (NS > 0 ? NS : 1) / 16 : bp.tv;
     extern __shared__ __align__(128) uint4 sm[];  // [n][TV]: slot j holds rank (c + j) mod N
     __shared__ __align__(8) uint64_t bar;
     __shared__ double sh[kThreads / 32];
@@ -257,8 +260,8 @@ cudaError_t park_sized(const ParkParams<Fold>& bp, cudaStream_t s)
     if (!bp.f.vec_ok || !bp.waits) return go(bucket_park_any_kernel<G, OP, MODE, Fold>, 0);
     // compiled rank counts of the calls that get here (clip_folds_twice)
     if constexpr (MODE != kPark) {
-        if (n == 2) return go(bucket_park_kernel<G, OP, 2, MODE, Fold>, kParkBytes);
-        if (n == 3) return go(bucket_park_kernel<G, OP, 3, MODE, Fold>, bp.tv * 16u * 3u);
+        if (n == 2) return go(bucket_park_kernel<G, OP, 2, MODE, Fold>, kTwiceBytes);
+        if (n == 3) return go(bucket_park_kernel<G, OP, 3, MODE, Fold>, kTwiceBytes);
         return cudaErrorInvalidValue;
     } else {
         switch (n) {
@@ -304,7 +307,7 @@ cudaError_t launch_table(int grad_dtype, int op, const BucketFoldParams& f, int 
     bp.waits = wait.waits;
     bp.hold = wait.hold;
     bp.spin = wait.spin;
-    bp.tv = kParkBytes / (uint32_t)f.n / 16u;
+    bp.tv = (MODE == kPark ? kParkBytes : kTwiceBytes) / (uint32_t)f.n / 16u;
     bp.pad_ = 0;
     const bool avg = op == kAvg;
     switch (grad_dtype) {
@@ -331,7 +334,8 @@ cudaError_t launch_pass(int grad_dtype, int op, const BucketFoldParams& p, int n
 
 uint64_t park_tile_elems(int grad_dtype, int n)
 {
-    return (uint64_t)(kParkBytes / (uint32_t)n / 16u) * (grad_dtype == kF32 ? 4u : 8u);
+    const uint32_t bytes = clip_folds_twice(n, grad_dtype) ? kTwiceBytes : kParkBytes;
+    return (uint64_t)(bytes / (uint32_t)n / 16u) * (grad_dtype == kF32 ? 4u : 8u);
 }
 
 bool clip_folds_twice(int n, int grad_dtype) { return n <= 3 && grad_dtype != kF32; }

@@ -9,7 +9,7 @@
 //
 // Both are bound by HBM.  The norm of 735 MB of bf16 takes 107 us, 6.9 TB/s (a copy
 // moves 6.55).  Clipping 4 replicas of 104 MB of fp16 (519 MB written and read
-// once) takes 97 us, of one rank's 50 MB of fp32 26 us: the second pass finds part
+// once) takes 97 us, of one rank's 50 MB of fp32 25 us: the second pass finds part
 // of the values in L2, but the first one shares HBM with the write-back of what
 // the program wrote before.  Partial sums are joined in a fixed order (no
 // atomics), so a call's bits depend only on its tensors.
