@@ -657,23 +657,8 @@ __device__ __forceinline__ void join_when_last(const EmbedGradParams& p, uint32_
     }
 }
 
-// A warp sums one slice of the columns over one block's span.
-//
-// The rows stream through a ring of slots in shared memory, kRingBytes a warp,
-// by cp.async, one row's slice per slot, and where the call adds to one table
-// the earlier values of a row follow the last position of its run through the
-// same ring, so the sums wait only for loads that were issued several rows
-// ago.  A lane reads only what it copied itself: no barrier.
-//
-// Bound by HBM, with instructions close behind (59 % of the issue slots taken):
-// 8 x 8192 tokens of 2048 bf16 onto one fp32 table move 450 MB in 78 us (5.8
-// TB/s).  With the loads of 8 rows held in registers instead (100 registers, 2
-// CTAs per SM, 63 % of the warps' time waiting for memory) the kernel took 150
-// us.  Slices of 512 columns halve the work per row but leave fewer warps (at 8
-// warps per CTA the call took 121 us against 117, and 205 against 194 for 8 x 2048
-// tokens into eight bf16 tables).
-// Warps per CTA of the sums: with 8 / 4 / 2 / 1 that call takes 116.5 / 114.4 / 112.6 /
-// 110.8 us, because a CTA keeps its shared memory until its slowest span ends.
+// Warps per CTA of the sums: with 8 / 4 / 2 / 1, 8 x 8192 tokens take 116.5 / 114.4 /
+// 112.6 / 110.8 us, because a CTA keeps its shared memory until its slowest span ends.
 constexpr int kReduceWarps = 1;
 static_assert(kReduceWarps == 1, "join_when_last counts a warp per block");
 constexpr uint32_t kRingBytes = 8192;  // of a warp
@@ -689,6 +674,21 @@ template <class In, class Out, int VEC, bool ACC>
 constexpr uint32_t kRingSlot =  // bytes of a warp's slot
     kEmbedCols * (ACC && sizeof(typename Out::T) > sizeof(typename In::T) ? sizeof(typename Out::T) : sizeof(typename In::T));
 
+// A warp sums one slice of the columns over one block's span.
+//
+// The rows stream through a ring of slots in shared memory, kRingBytes a warp,
+// by cp.async, one row's slice per slot, and where the call adds to one table
+// the earlier values of a row follow the last position of its run through the
+// same ring, so the sums wait only for loads that were issued several rows
+// ago.  A lane reads only what it copied itself: no barrier.
+//
+// Bound by HBM, with instructions close behind (59 % of the issue slots taken):
+// 8 x 8192 tokens of 2048 bf16 onto one fp32 table move 450 MB in 78 us (5.8
+// TB/s).  With the loads of 8 rows held in registers instead (100 registers, 2
+// CTAs per SM, 63 % of the warps' time waiting for memory) the kernel took 150
+// us.  Slices of 512 columns halve the work per row but leave fewer warps (at 8
+// warps per CTA the call took 121 us against 117, and 205 against 194 for 8 x 2048
+// tokens into eight bf16 tables).
 template <class In, class Out, int VEC, bool ACC, bool JOIN>
 __global__ void __launch_bounds__(kReduceWarps * 32) embed_reduce_kernel(const __grid_constant__ EmbedGradParams p)
 {
