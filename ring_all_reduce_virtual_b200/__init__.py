@@ -344,9 +344,12 @@ class GradList:
 def _placed(stream, device):
     """Run with ``device`` current (kernels are launched from there) and the
     caching allocator serving ``stream``: scratch memory of a call is taken
-    there, so that its next user on that stream is ordered behind the call."""
+    there, so that its next user on that stream is ordered behind the call.
+    A stream of another device is refused: making it current would leave it."""
     import torch
 
+    if isinstance(stream, torch.cuda.Stream) and stream.device != device:
+        raise ValueError(f"the stream belongs to {stream.device}, the tensors to {device}")
     with torch.cuda.device(device):
         if stream is None:
             yield

@@ -82,3 +82,14 @@ def test_python_calls_check_their_tensors():
         rrv.embedding([ids.float()], [cpu], [cpu])
     with pytest.raises(ValueError, match="1..64"):
         rrv.embedding_grad([], [cpu], [cpu])
+
+
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    class OnDevice1:  # what a stream of a second GPU is to the check, without one
+        device = torch.device("cuda", 1)
+        cuda_stream = 0
+
+    monkeypatch.setattr(torch.cuda, "Stream", OnDevice1)
+    with pytest.raises(ValueError, match="cuda:1, the tensors to cuda:0"):
+        with rrv._placed(OnDevice1(), torch.device("cuda", 0)):
+            pass
