@@ -393,8 +393,10 @@ rr_status_t rr_grad_norm(const rr_tensor_list_t* grads, float* norm, void* works
  * one rounding to nearest even.  With nranks 1 the tensors are clipped in
  * place; with more, the other ranks' copies are only written (so rank 0 alone
  * need hold the gradients).  *norm receives ||g||.  A NaN norm makes every
- * value NaN, an infinite one zeroes the finite values (c is 0).  max_norm may
- * be 0 or infinite.  Buffers must not overlap. */
+ * value NaN, an infinite gradient zeroes the finite values (c is 0).  A norm of
+ * finite gradients that is above fp32's largest number reads as infinite in
+ * *norm and still counts as it is in c.  max_norm may be 0 or infinite.
+ * Buffers must not overlap. */
 rr_status_t rr_clip_grads(const rr_tensor_list_t* grads, float max_norm, float eps, float* norm, void* workspace,
                           size_t workspace_bytes, cudaStream_t stream);
 

@@ -76,10 +76,10 @@ __device__ __forceinline__ float fold_value(const InF& in, int n, uint64_t e, fl
 
 // One element's result to where the pass puts it; its square.
 template <class G, int MODE, class OutF>
-__device__ __forceinline__ double settle_one(const OutF& out, int n, uint64_t e, float a, float c)
+__device__ __forceinline__ double settle_one(const OutF& out, int n, uint64_t e, float a, const Coef& c)
 {
     if constexpr (MODE == kScaled) {
-        const float x = __fmul_rn(a, c);
+        const float x = scaled(a, c);
         for (int o = 0; o < n; ++o) G::st1(out(o) + e, x);
         return 0.0;
     } else {
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kThreads) bucket_park_kernel(const __grid_cons
     }
     // the barrier is set up before the other threads wait on it; the second
     // pass forms the coefficient meanwhile
-    float c = 1.0f;
+    Coef c{};
     if constexpr (MODE == kScaled) c = clip_coef(bp.clip, sh);
     else __syncthreads();
     double acc = 0.0;
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kThreads) bucket_park_kernel(const __grid_cons
             for (int l = 0; l < L; ++l) a[l] = finish_n<OP, NS>(a[l], p.divisor);
             if constexpr (MODE == kScaled) {
 #pragma unroll
-                for (int l = 0; l < L; ++l) a[l] = __fmul_rn(a[l], c);
+                for (int l = 0; l < L; ++l) a[l] = scaled(a[l], c);
                 sm[v] = G::pack(a);
                 continue;
             }
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kThreads) bucket_park_any_kernel(const __grid_
     pdl_begin();
     const Fold& p = bp.f;
     const int n = p.n;
-    const float c = MODE == kScaled ? clip_coef(bp.clip, sh) : 1.0f;
+    const Coef c = MODE == kScaled ? clip_coef(bp.clip, sh) : Coef{};
     const uint64_t w = MODE == kScaled ? p.tile0[p.nseg] - 1 - blockIdx.x : blockIdx.x;
     const int s = find_segment(p.tile0, p.nseg, w);
     const BucketSeg& sg = p.seg[s];

@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kThreads, 4) clip_scale_kernel(const __grid_co
     constexpr uint64_t TV = (uint64_t)kThreads * kScaleU;
     __shared__ double sh[kThreads / 32];
     pdl_begin();
-    float c = 0.0f;
+    Coef c{};
     const uint64_t total = p.tile0[p.nt], tid = threadIdx.x;
     const int n = p.n;
     for (uint64_t i = blockIdx.x; i < total; i += gridDim.x) {
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, 4) clip_scale_kernel(const __grid_co
             float x;
             if constexpr (PARKED) x = __uint_as_float(((uint32_t)src[e] << 16) | (uint32_t)low[e]);
             else x = Ty::ld1(src + e);
-            x = __fmul_rn(x, c);
+            x = scaled(x, c);
             for (int o = 0; o < n; ++o) Ty::st1(ptr[o] + e, x);
         };
         if (!p.vec[t]) {
@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 4) clip_scale_kernel(const __grid_co
                 Ty::unpack(raw[u], a);
             }
 #pragma unroll
-            for (int l = 0; l < L; ++l) a[l] = __fmul_rn(a[l], c);
+            for (int l = 0; l < L; ++l) a[l] = scaled(a[l], c);
             raw[u] = Ty::pack(a);
         }
         for (int o = 0; o < n; ++o) {
@@ -226,12 +226,12 @@ __global__ void __launch_bounds__(kThreads) clip_bulk_kernel(const __grid_consta
                          ::"r"(bulk_smem_addr(sm + k * TV)), "l"((k ? low : src) + e0), "r"(bytes), "r"(b)
                          : "memory");
     }
-    const float c = clip_coef(p.clip, sh);
+    const Coef c = clip_coef(p.clip, sh);
     auto one = [&](uint64_t e) {
         float x;
         if constexpr (PARKED) x = __uint_as_float(((uint32_t)src[e] << 16) | (uint32_t)low[e]);
         else x = Ty::ld1(src + e);
-        x = __fmul_rn(x, c);
+        x = scaled(x, c);
         for (int o = 0; o < n; ++o) Ty::st1(ptr[o] + e, x);
     };
     if (!p.vec[t]) {
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kThreads) clip_bulk_kernel(const __grid_consta
             Ty::unpack(sm[v], a);
         }
 #pragma unroll
-        for (int l = 0; l < L; ++l) a[l] = __fmul_rn(a[l], c);
+        for (int l = 0; l < L; ++l) a[l] = scaled(a[l], c);
         sm[v] = Ty::pack(a);
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");

@@ -115,18 +115,35 @@ __device__ __forceinline__ double partials_sum(const double* p, int64_t count, d
     return cta_sum(v, sh);
 }
 
-// The clipping's coefficient for a sum of squares, 1 where the norm is within
-// max_norm and max_norm / (norm + eps) otherwise: 0 for an infinite norm, NaN
-// for NaN.  One thread writes the norm, where the launch is asked to.
-__device__ __forceinline__ float coef_of(const ClipArgs& a, double squares)
+// The clipping's coefficient: the product of two factors, of which the second
+// is 1 unless the coefficient is below fp32's smallest normal number (a norm
+// above 2^126 clipped to 1, say).  There one fp32 would keep few of its bits;
+// the first factor keeps 24 and the second is the power of two.
+struct Coef {
+    float a, b;
+};
+
+__device__ __forceinline__ float scaled(float x, const Coef& c)
+{
+    return __fmul_rn(__fmul_rn(x, c.a), c.b);
+}
+
+// The coefficient for a sum of squares, 1 where the norm is within max_norm
+// and max_norm / (norm + eps) otherwise: 0 for an infinite norm, NaN for NaN.
+// The norm counts in fp64, also where it is above fp32's largest number.  One
+// thread writes it, where the launch is asked to.
+__device__ __forceinline__ Coef coef_of(const ClipArgs& a, double squares)
 {
     const double norm = sqrt(squares);
     if (a.norm && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = (float)norm;
     const double den = norm + (double)a.eps;
-    return den <= (double)a.max_norm ? 1.0f : (float)((double)a.max_norm / den);
+    if (den <= (double)a.max_norm) return {1.0f, 1.0f};
+    const double c = (double)a.max_norm / den;
+    if (c < 0x1p-126) return {(float)(c * 0x1p126), 0x1p-126f};
+    return {(float)c, 1.0f};
 }
 
-__device__ __forceinline__ float clip_coef(const ClipArgs& a, double* sh)
+__device__ __forceinline__ Coef clip_coef(const ClipArgs& a, double* sh)
 {
     return coef_of(a, partials_sum(a.partial, a.npartial, sh));
 }

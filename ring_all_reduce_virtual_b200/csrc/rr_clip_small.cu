@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kSmallThreads) clip_small_kernel(const __grid_
         sum += x;
     }
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // this CTA has read the others' sums
-    const float c = coef_of(sp.clip, sum);
+    const Coef c = coef_of(sp.clip, sum);
     if (sp.scale) {
 #pragma unroll
         for (int j = 0; j < R; ++j) {
@@ -123,12 +123,12 @@ __global__ void __launch_bounds__(kSmallThreads) clip_small_kernel(const __grid_
             uint64_t e;
             if (!locate(j, s, e)) continue;
 #pragma unroll
-            for (int l = 0; l < L; ++l) a[j][l] = __fmul_rn(a[j][l], c);
+            for (int l = 0; l < L; ++l) a[j][l] = scaled(a[j][l], c);
             const uint4 out = Ty::pack(a[j]);
             for (int r = 0; r < n; ++r) *reinterpret_cast<uint4*>(copy(s, r) + e) = out;
         }
         if (has_edge)
-            for (int r = 0; r < n; ++r) Ty::st1(copy(es, r) + edge, __fmul_rn(b[0], c));
+            for (int r = 0; r < n; ++r) Ty::st1(copy(es, r) + edge, scaled(b[0], c));
     }
     __syncwarp();
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // no CTA leaves before its sum was read

@@ -161,6 +161,42 @@ def test_clip_with_infinities_and_nans():
     assert math.isnan(float(rrv.clip_grads([t], math.inf))) and bool(t.isnan().all())
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("sizes", [[7, 1000], [300_001], [20_000_003]])  # one launch, two, by bulk copies
+@pytest.mark.parametrize("limit", [1.0, 1e-3])
+def test_clip_of_norms_near_and_above_the_largest_fp32(dtype, sizes, limit):
+    """The coefficient is then below fp32's smallest normal number, where one
+    fp32 would keep 2^-149 of it; the clipped values are ordinary ones."""
+    ts = [(values(i, m, torch.float32).clamp(-3, 3).double() * 1e38).to(DT[dtype]) for i, m in enumerate(sizes)]
+    src = [t.clone() for t in ts]
+    want = norm64(src)
+    got = rrv.clip_grads(ts, limit, eps=0.0)
+    assert limit / want < 2.0 ** -126
+    assert float(got) == math.inf if want > 1.01 * torch.finfo(torch.float32).max else abs(float(got) - want) <= 10 * E * want
+    c = float(torch.tensor(limit)) / want
+    for t, a in zip(ts, src):
+        near_scaled(t, a.double() * c)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [2, 3, 4])
+def test_clipped_sync_of_a_norm_above_the_largest_fp32(n, dtype):
+    sizes = [5003, 900]
+    ranks = [[(values(10 * r + t, m, torch.float32).clamp(-3, 3).double() * 2e37).to(DT[dtype]) for t, m in enumerate(sizes)]
+             for r in range(n)]
+    terms = [[rank[t].double() for rank in ranks] for t in range(len(sizes))]
+    avg = [sum(x) / n for x in terms]
+    mag = [sum(v.abs() for v in x) / n for x in terms]
+    want = norm64(avg)
+    assert want > torch.finfo(torch.float32).max
+    assert float(rrv.BucketPlan(sizes, dtype).all_reduce_clip(ranks, 1.0, eps=0.0)) == math.inf
+    # the norm's own error through the folds: at most the folds' share of the values
+    fold = math.sqrt(sum(float((n * E * v).square().sum()) for v in mag)) / want
+    for rank in ranks:
+        for t, a, m in zip(rank, avg, mag):
+            near_scaled(t, a / want, extra=m / want * n * E + a.abs() / want * fold)
+
+
 def test_clip_many_tensors_in_several_launches():
     sizes = [(i * 53) % 97 + 1 for i in range(1200)]
     ranks = [[values(i + 7 * r, m, torch.bfloat16 if i % 4 else torch.float32) for i, m in enumerate(sizes)] for r in range(3)]
