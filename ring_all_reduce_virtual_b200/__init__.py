@@ -445,10 +445,13 @@ def _row_set(tensors, what: str):
     if is_set and tensors._rows is not None:
         return tensors._rows
     ptrs, n, count, d, dev = _rank_args(tensors, what)
-    shape = (tensors.tensors if is_set else tensors)[0].shape
-    if len(shape) < 2 or shape[-1] == 0:
-        raise ValueError(f"{what}: need tensors of rows (two axes or more, rows not empty)")
-    rows = ptrs, n, count // shape[-1], shape[-1], d, dev
+    width = 0
+    for t in tensors.tensors if is_set else tensors:
+        shape = t.shape
+        if len(shape) < 2 or shape[-1] == 0 or shape[-1] != (width or shape[-1]):
+            raise ValueError(f"{what}: need tensors of rows (two axes or more, rows not empty, of one width on every rank)")
+        width = shape[-1]
+    rows = ptrs, n, count // width, width, d, dev
     if is_set:
         tensors._rows = rows
     return rows

@@ -93,3 +93,42 @@ def test_a_stream_of_another_device_is_refused(monkeypatch):
     with pytest.raises(ValueError, match="cuda:1, the tensors to cuda:0"):
         with rrv._placed(OnDevice1(), torch.device("cuda", 0)):
             pass
+
+
+class Fake:
+    """What the argument checks read of a CUDA tensor, without a GPU; its address is never used."""
+
+    is_cuda = True
+    device = torch.device("cuda", 0)
+
+    def __init__(self, *shape, dtype=torch.float32):
+        self.shape, self.dtype = torch.Size(shape), dtype
+
+    def numel(self):
+        return self.shape.numel()
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 1 << 40
+
+
+@pytest.mark.parametrize("as_set", [False, True])
+@pytest.mark.parametrize("bad", ["tables", "outs", "grad_out", "grads"])
+@pytest.mark.parametrize("shape", [(8, 6), (2, 24), (48,), (48, 1)])
+def test_rows_of_another_width_on_another_rank_are_refused(as_set, bad, shape):
+    """Rank 1's tensor has rank 0's element count (6 rows of 8) but not its rows."""
+    ids = [Fake(6, dtype=torch.int32), Fake(6, dtype=torch.int32)]
+    wrap = rrv.RankSet if as_set else list
+    good, mixed = wrap([Fake(6, 8), Fake(6, 8)]), wrap([Fake(6, 8), Fake(*shape)])
+    with pytest.raises(ValueError, match="one width on every rank"):
+        if bad in ("tables", "outs"):
+            rrv.embedding(ids, mixed if bad == "tables" else good, mixed if bad == "outs" else good)
+        else:
+            rrv.embedding_grad(ids, mixed if bad == "grad_out" else good, mixed if bad == "grads" else good)
+
+
+def test_rows_may_be_grouped_differently():
+    """Leading axes only group the rows: the same rows and width count as alike."""
+    assert rrv._row_set([Fake(6, 8), Fake(2, 3, 8)], "rows")[1:4] == (2, 6, 8)
