@@ -409,8 +409,9 @@ rr_status_t rr_clip_grads(const rr_tensor_list_t* grads, float max_norm, float e
  * embedding's, say (rr_embedding_grad) -- with the same nranks: they count
  * into the norm and are clipped as rr_clip_grads does, from rank 0's copy.
  * Between its two passes the call may keep the fp32 sums in the gradients' own
- * buffers (ranks 0 and 1), so a call that ends with RR_ERR_CUDA leaves the
- * gradients undefined.  op: SUM or AVG.  With nranks 1 it is the clipping
+ * buffers (ranks 0 and 1), so a call that ends with RR_ERR_CUDA, or one of
+ * whose bounded waits ran out (rr_check_timeouts), leaves the gradients
+ * undefined.  op: SUM or AVG.  With nranks 1 it is the clipping
  * alone.  Other arguments and errors as rr_bucket_allreduce_range and
  * rr_clip_grads. */
 rr_status_t rr_bucket_allreduce_clip(const rr_bucket_plan_t* plan, int first_bucket, int nbuckets, void* const* grads,
@@ -541,8 +542,9 @@ rr_status_t rr_get_stats(rr_stats_t* out); /* last call on this host thread */
  * the tile a second time if they were not seen to land.  This call
  * synchronises the current device, takes both counts (atomically exchanged
  * for zero on the device) and returns RR_ERR_TIMEOUT if either is not zero
- * (rr_last_error() gives both), RR_OK otherwise.  (A clipped sync that
- * skipped a tile also reports a NaN norm.)  No other kernel of the library
+ * (rr_last_error() gives both), RR_OK otherwise.  (A clipped sync or a
+ * clipping that skipped a tile, in any of its passes, also reports a NaN norm;
+ * its gradients are then undefined.)  No other kernel of the library
  * waits on anything but the hardware's barriers of its own CTA or cluster. */
 rr_status_t rr_check_timeouts(void);
 const char* rr_status_string(rr_status_t status);

@@ -43,7 +43,7 @@ template <class Fold>
 struct ParkParams {
     Fold f;              // BucketFoldParams or ParkSmallParams; tile0 counts tiles of park_tile_elems
     double* partial;     // kPark, kSquares: one per tile
-    ClipArgs clip;       // kScaled: what the coefficient comes from
+    ClipArgs clip;       // kScaled: what the coefficient comes from; else norm: the word to zero, or NULL
     unsigned int* waits; // as BulkParams (rr_bulk.cuh)
     uint32_t hold;
     uint32_t spin;
@@ -63,6 +63,12 @@ __device__ __forceinline__ void park_one(typename G::T* p0, typename G::T* p1, u
     } else {
         p0[e] = a;
     }
+}
+
+// A first pass zeroes the norm's word where it is given (ClipArgs::lost).
+__device__ __forceinline__ void zero_norm(const ClipArgs& a)
+{
+    if (a.norm && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = 0.0f;
 }
 
 // Fold of element e: the same operations as the sync's, unrounded.
@@ -103,6 +109,7 @@ __global__ void __launch_bounds__(kThreads) bucket_park_kernel(const __grid_cons
     const Fold& p = bp.f;
     const int n = NS > 0 ? NS : p.n;
     const uint32_t TV = NS > 0 ? (MODE == kPark ? kParkBytes : kTwiceBytes) / (NS > 0 ? NS : 1) / 16 : bp.tv;
+    if constexpr (MODE != kScaled) zero_norm(bp.clip);
     extern __shared__ __align__(128) uint4 sm[];  // [n][TV]: slot j holds rank (c + j) mod N
     __shared__ __align__(8) uint64_t bar;
     __shared__ double sh[kThreads / 32];
@@ -154,7 +161,10 @@ __global__ void __launch_bounds__(kThreads) bucket_park_kernel(const __grid_cons
     if (staged) {
         if (!bulk_tile_landed(b, bp.waits, bp.hold, bp.spin)) {
             // the whole CTA skips the tile: a NaN norm says that the step is lost
-            if (MODE != kScaled && threadIdx.x == 0) bp.partial[w] = __longlong_as_double(0x7ff8000000000000ll);
+            if (threadIdx.x == 0) {
+                if constexpr (MODE == kScaled) tile_lost(bp.clip);
+                else bp.partial[w] = __longlong_as_double(0x7ff8000000000000ll);
+            }
             return;
         }
         for (uint32_t v = threadIdx.x; v < nvt; v += kThreads) {
@@ -224,6 +234,7 @@ __global__ void __launch_bounds__(kThreads) bucket_park_any_kernel(const __grid_
     using T = typename G::T;
     __shared__ double sh[kThreads / 32];
     pdl_begin();
+    if constexpr (MODE != kScaled) zero_norm(bp.clip);
     const Fold& p = bp.f;
     const int n = p.n;
     const Coef c = MODE == kScaled ? clip_coef(bp.clip, sh) : Coef{};
@@ -295,15 +306,15 @@ inline void copy_table(ParkSmallParams& to, const BucketFoldParams& f, int ntens
 
 template <int MODE, class Fold>
 cudaError_t launch_table(int grad_dtype, int op, const BucketFoldParams& f, int ntensors, double* partial,
-                         const ClipArgs* clip, cudaStream_t s)
+                         const ClipArgs& clip, cudaStream_t s)
 {
     RankParams rp{};
     rp.waits = bulk_wait_counters();
-    const BulkParams wait = bulk_params(rp);
+    const BulkParams wait = bulk_params(rp, MODE == kScaled);
     ParkParams<Fold> bp;
     copy_table(bp.f, f, ntensors);
     bp.partial = partial;
-    bp.clip = clip ? *clip : ClipArgs{};
+    bp.clip = clip;
     bp.waits = wait.waits;
     bp.hold = wait.hold;
     bp.spin = wait.spin;
@@ -322,7 +333,7 @@ cudaError_t launch_table(int grad_dtype, int op, const BucketFoldParams& f, int 
 
 template <int MODE>
 cudaError_t launch_pass(int grad_dtype, int op, const BucketFoldParams& p, int ntensors, double* partial,
-                        const ClipArgs* clip, cudaStream_t s)
+                        const ClipArgs& clip, cudaStream_t s)
 {
     if (p.tile0[p.nseg] > kMaxGrid || p.n < 2) return cudaErrorInvalidValue;
     if (p.nseg <= kParkSegsSmall && ntensors * p.n <= kParkPtrsSmall)
@@ -341,21 +352,25 @@ uint64_t park_tile_elems(int grad_dtype, int n)
 bool clip_folds_twice(int n, int grad_dtype) { return n <= 3 && grad_dtype != kF32; }
 
 cudaError_t launch_bucket_park(int grad_dtype, int op, const BucketFoldParams& p, int ntensors, double* partial,
-                               cudaStream_t s)
+                               float* clear, cudaStream_t s)
 {
-    return launch_pass<kPark>(grad_dtype, op, p, ntensors, partial, nullptr, s);
+    ClipArgs a{};
+    a.norm = clear;
+    return launch_pass<kPark>(grad_dtype, op, p, ntensors, partial, a, s);
 }
 
 cudaError_t launch_bucket_squares(int grad_dtype, int op, const BucketFoldParams& p, int ntensors, double* partial,
-                                  cudaStream_t s)
+                                  float* clear, cudaStream_t s)
 {
-    return launch_pass<kSquares>(grad_dtype, op, p, ntensors, partial, nullptr, s);
+    ClipArgs a{};
+    a.norm = clear;
+    return launch_pass<kSquares>(grad_dtype, op, p, ntensors, partial, a, s);
 }
 
 cudaError_t launch_bucket_scaled(int grad_dtype, int op, const BucketFoldParams& p, int ntensors, const ClipArgs& clip,
                                  cudaStream_t s)
 {
-    return launch_pass<kScaled>(grad_dtype, op, p, ntensors, nullptr, &clip, s);
+    return launch_pass<kScaled>(grad_dtype, op, p, ntensors, nullptr, clip, s);
 }
 
 }  // namespace rr

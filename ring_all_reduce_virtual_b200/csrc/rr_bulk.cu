@@ -35,17 +35,15 @@ __global__ void take_waits_kernel()
 // barrier expect one arrival more than the copying thread makes, and bounds
 // each wait at 2^16 rounds, so that every first wait runs out; the missing
 // arrival is then made, and the second wait ends when the tile's copies have
-// landed -- the path a real timeout takes.
+// landed -- the path a real timeout takes.  RR_DEBUG_BULK_TIMEOUT=2 does so to
+// the second passes of the clipping calls alone.
 struct BulkDebug {
-    uint32_t hold = 0;
-    uint32_t spin = 1u << 22;  // try_wait rounds, each of which may suspend the thread briefly
+    bool all = false, scaling = false;
     BulkDebug()
     {
         const char* v = std::getenv("RR_DEBUG_BULK_TIMEOUT");
-        if (v && std::strcmp(v, "1") == 0) {
-            hold = 1;
-            spin = 1u << 16;
-        }
+        all = v && std::strcmp(v, "1") == 0;
+        scaling = all || (v && std::strcmp(v, "2") == 0);
     }
 };
 
@@ -97,13 +95,14 @@ unsigned int* bulk_wait_counters()
     return static_cast<unsigned int*>(q);
 }
 
-BulkParams bulk_params(const RankParams& p)
+BulkParams bulk_params(const RankParams& p, bool scaling)
 {
+    const bool hold = scaling ? bulk_debug().scaling : bulk_debug().all;
     BulkParams bp{};
     bp.r = p;
     bp.waits = p.waits;
-    bp.hold = bulk_debug().hold;
-    bp.spin = bulk_debug().spin;
+    bp.hold = hold ? 1 : 0;
+    bp.spin = hold ? 1u << 16 : 1u << 22;  // try_wait rounds, each of which may suspend the thread briefly
     return bp;
 }
 

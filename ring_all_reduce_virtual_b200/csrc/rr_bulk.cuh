@@ -83,8 +83,8 @@ __host__ __device__ constexpr uint32_t bulk_smem()
 }
 
 // The parameter block of a launch: p, the counters' address (p.waits) and
-// the wait bounds (rr_bulk.cu).
-BulkParams bulk_params(const RankParams& p);
+// the wait bounds (rr_bulk.cu); scaling: of a clipping's second pass.
+BulkParams bulk_params(const RankParams& p, bool scaling = false);
 
 // Whether a call can take the aligned bulk kernels (scatter and tree modes):
 // the wait counters are known (p.waits), 2..nmax ranks (powers of two only

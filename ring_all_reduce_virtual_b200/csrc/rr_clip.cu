@@ -62,6 +62,7 @@ __global__ void __launch_bounds__(kThreads, 4) norm_kernel(const __grid_constant
 {
     __shared__ double sh[kThreads / 32];
     pdl_begin();
+    if (p.clear && blockIdx.x == 0 && threadIdx.x == 0) *p.clear = 0.0f;
     const uint64_t total = p.tile0[p.nt];
     double acc = 0.0;
     int t = find_segment(p.tile0, p.nt, blockIdx.x);
@@ -242,7 +243,10 @@ __global__ void __launch_bounds__(kThreads) clip_bulk_kernel(const __grid_consta
     if (tile == 0 && threadIdx.x < head + tail)
         one(threadIdx.x < head ? threadIdx.x : head + nv * L + (threadIdx.x - head));
     if (!staged) return;
-    if (!bulk_tile_landed(b, bp.waits, bp.hold, bp.spin)) return;  // the whole CTA skips the tile
+    if (!bulk_tile_landed(b, bp.waits, bp.hold, bp.spin)) {  // the whole CTA skips the tile
+        if (threadIdx.x == 0) tile_lost(p.clip);
+        return;
+    }
     for (uint32_t v = threadIdx.x; v < nvt; v += kThreads) {
         float a[L];
         if constexpr (PARKED) {
@@ -286,6 +290,7 @@ Small shrink(const NormParams& p)
         q.tile0[t + 1] = p.tile0[t + 1];
     }
     q.partial = p.partial;
+    q.clear = p.clear;
     q.nt = p.nt;
     return q;
 }
@@ -323,7 +328,7 @@ cudaError_t bulk_typed(const ScaleParams& p, unsigned grid, cudaStream_t s)
     RankParams rp{};
     rp.waits = bulk_wait_counters();
     if (!rp.waits) return cudaErrorInvalidValue;
-    const BulkParams wait = bulk_params(rp);
+    const BulkParams wait = bulk_params(rp, true);
     ScaleBulkParams bp;
     bp.s = p;
     bp.waits = wait.waits;

@@ -128,6 +128,19 @@ __device__ __forceinline__ float scaled(float x, const Coef& c)
     return __fmul_rn(__fmul_rn(x, c.a), c.b);
 }
 
+// The norm into its word: see ClipArgs::lost.
+__device__ __forceinline__ void write_norm(const ClipArgs& a, float norm)
+{
+    if (a.lost) atomicMax(reinterpret_cast<unsigned int*>(a.norm), __float_as_uint(norm) & 0x7fffffffu);
+    else *a.norm = norm;
+}
+
+// A tile of the scaling was skipped: the norm says that the step is lost.
+__device__ __forceinline__ void tile_lost(const ClipArgs& a)
+{
+    if (a.lost) atomicMax(reinterpret_cast<unsigned int*>(a.lost), 0x7fffffffu);
+}
+
 // The coefficient for a sum of squares, 1 where the norm is within max_norm
 // and max_norm / (norm + eps) otherwise: 0 for an infinite norm, NaN for NaN.
 // The norm counts in fp64, also where it is above fp32's largest number.  One
@@ -135,7 +148,7 @@ __device__ __forceinline__ float scaled(float x, const Coef& c)
 __device__ __forceinline__ Coef coef_of(const ClipArgs& a, double squares)
 {
     const double norm = sqrt(squares);
-    if (a.norm && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = (float)norm;
+    if (a.norm && blockIdx.x == 0 && threadIdx.x == 0) write_norm(a, (float)norm);
     const double den = norm + (double)a.eps;
     if (den <= (double)a.max_norm) return {1.0f, 1.0f};
     const double c = (double)a.max_norm / den;

@@ -96,7 +96,15 @@ struct Passes {
     double* partial;
     cudaStream_t stream;
     bool bulk = false;  // the scaling runs by bulk copies
+    float* clear = nullptr;  // the norm's word where the first launch is to zero it (ClipArgs::lost)
     int64_t count = 0;  // partials so far
+
+    float* take_clear()  // once: the first launch zeroes the word
+    {
+        float* w = clear;
+        clear = nullptr;
+        return w;
+    }
 
     // The norm's launches over rank 0's tensors, one type at a time.
     rr_status_t norm(const rr_tensor_list_t* l)
@@ -111,6 +119,7 @@ struct Passes {
                 if ((end || p.nt == kNormTensors) && p.nt > 0) {
                     int slots = 0;
                     p.partial = partial + count;
+                    p.clear = take_clear();
                     const cudaError_t e = timed_launch([&] { return launch_norm(d, p, &slots, stream); });
                     if (e != cudaSuccess) return cuda_fail(e, "norm launch");
                     t_stats.launches += 1;
@@ -143,8 +152,10 @@ struct Passes {
         return RR_OK;
     }
 
-    rr_status_t finish(const ClipArgs& a)
+    // The norm alone, of a call that had nothing to scale.
+    rr_status_t finish(ClipArgs a)
     {
+        a.lost = nullptr;
         const cudaError_t e = timed_launch([&] { return launch_norm_finish(a, stream); });
         if (e != cudaSuccess) return cuda_fail(e, "norm launch");
         t_stats.launches += 1;
@@ -355,6 +366,7 @@ rr_status_t clip_grads(const rr_tensor_list_t* grads, float max_norm, float eps,
     a.max_norm = max_norm;
     a.eps = eps;
     a.norm = norm;
+    a.lost = run.clear = run.bulk ? norm : nullptr;
     bool done = false;
     if ((st = small_list(grads, total, n, true, a, stream, &done)) != RR_OK) return st;
     if (!done) {
@@ -404,6 +416,7 @@ rr_status_t bucket_allreduce_clip(const rr_bucket_plan_t* plan, int b0, int nb, 
     a.norm = norm;
     const RangeList own(plan, t0, nt, grads);
     const bool twice = n > 1 && clip_folds_twice(n, d);
+    a.lost = run.clear = run.bulk || twice ? norm : nullptr;
     // the range's launches, a pass at a time
     std::unique_ptr<BucketFoldParams> p(new BucketFoldParams);  // as it comes: every field that counts is set
     auto pass = [&](auto&& launch) {
@@ -428,8 +441,8 @@ rr_status_t bucket_allreduce_clip(const rr_bucket_plan_t* plan, int b0, int nb, 
         st = pass([&](int ntens) {
             double* slots = run.partial + run.count;
             run.count += (int64_t)p->tile0[p->nseg];
-            return twice ? launch_bucket_squares(d, op, *p, ntens, slots, stream)
-                         : launch_bucket_park(d, op, *p, ntens, slots, stream);
+            return twice ? launch_bucket_squares(d, op, *p, ntens, slots, run.take_clear(), stream)
+                         : launch_bucket_park(d, op, *p, ntens, slots, run.take_clear(), stream);
         });
     }
     if (st != RR_OK) return st;

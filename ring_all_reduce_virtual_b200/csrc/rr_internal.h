@@ -124,6 +124,7 @@ struct NormParamsT {
     uint64_t len[CAP];
     uint64_t tile0[CAP + 1];  // first work item (tile) of tensor t
     double* partial;          // this launch's slots, one per CTA
+    float* clear;             // the launch zeroes this word (NULL: it does not); see ClipArgs::lost
     int nt;
     int pad_;
 };
@@ -138,6 +139,11 @@ struct ClipArgs {
     float max_norm;
     float eps;
     float* norm;  // where the launch writes the norm (NULL: it does not)
+    // The norm's word in a call whose scaling waits for copies (NULL: none does).
+    // A tile that a wait gave up on makes it NaN, before or after the norm is
+    // written: a launch of the pass before zeroes it, and both go through
+    // atomicMax, by whose order a NaN's bits are above every norm's.
+    float* lost;
 };
 
 // The clipping's second pass: rank 0's copy of each tensor, scaled, into
@@ -290,10 +296,11 @@ constexpr uint64_t kBulkClipBytes = 64ull << 20;
 constexpr uint64_t kKeepBytes = 126ull << 20;
 constexpr int kJoinCtas = 128;        // partials that launch_norm_join leaves
 constexpr int kMaxPartials = 1280;    // partials that a launch sums itself
-// The clipped sync's first pass: fold, park the sums, one partial per tile.
+// The clipped sync's first pass: fold, park the sums, one partial per tile;
+// clear (or NULL): a word that the launch zeroes (ClipArgs::lost).
 uint64_t park_tile_elems(int grad_dtype, int n);
 cudaError_t launch_bucket_park(int grad_dtype, int op, const BucketFoldParams& p, int ntensors, double* partial,
-                               cudaStream_t s);
+                               float* clear, cudaStream_t s);
 // Norm (scale false) or clipping of a small set in one launch: whether it is
 // one (the tensors' prefix sums are filled in), and the launch.
 bool clip_small_plan(int dtype, ParkSmallParams& p, int ntensors);
@@ -303,7 +310,7 @@ cudaError_t launch_clip_small(int dtype, bool scale, const ParkSmallParams& f, c
 // takes.
 bool clip_folds_twice(int n, int grad_dtype);
 cudaError_t launch_bucket_squares(int grad_dtype, int op, const BucketFoldParams& p, int ntensors, double* partial,
-                                  cudaStream_t s);
+                                  float* clear, cudaStream_t s);
 cudaError_t launch_bucket_scaled(int grad_dtype, int op, const BucketFoldParams& p, int ntensors, const ClipArgs& clip,
                                  cudaStream_t s);
 

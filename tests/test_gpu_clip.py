@@ -525,3 +525,40 @@ x = [torch.ones(1000, device="cuda")]
 print("CONTEXT OK", float(rrv.grad_norm(x)) == 1000 ** 0.5 or abs(float(rrv.grad_norm(x)) - 1000 ** 0.5) < 1e-4)
 """, RR_DEBUG_BULK_TIMEOUT="1")
     assert out.count("TIMEOUT 4 True") == 2 and "CONTEXT OK True" in out, out
+
+
+def test_timeouts_of_the_second_pass_alone_make_the_norm_nan():
+    """RR_DEBUG_BULK_TIMEOUT=2 makes only the scaling's bounded waits run out: every partial sum is whole, and the norm says
+    all the same that the step is lost, also where a later launch of the call skips the tile; a call without such waits
+    (the norm, a small clipping, a scaling by the threads) is as ever."""
+    out = run_child(r"""
+import torch
+import ring_all_reduce_virtual_b200 as rrv
+def report():
+    try:
+        rrv.check_timeouts()
+        print("NO TIMEOUT")
+    except rrv.RRError as e:
+        print("RAN OUT", e.status, "not seen to land: 0" in str(e))
+def ranks(n, m, dtype=torch.bfloat16):
+    return [[torch.full((m,), float(r + 1), device="cuda").to(dtype)] for r in range(n)]
+for n, m, d in ((8, 1 << 23, "bf16"), (2, 1 << 23, "bf16"), (3, 1 << 12, "f16"), (4, 1 << 23, "f32")):
+    g = ranks(n, m, {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}[d])
+    norm = rrv.BucketPlan([m], d).all_reduce_clip(g, 1.0)  # parked, folded twice, the same with one tile's few, fp32
+    assert bool(norm.isnan()), (n, m, float(norm))
+    report()
+big = ranks(2, 1 << 24, torch.float32)
+assert bool(rrv.clip_grads(big, 1.0).isnan())
+report()
+# the buckets' scaling runs by the threads, or not at all; the synced list's by bulk copies
+big = ranks(4, 1 << 24, torch.float32)
+norm = rrv.BucketPlan([0], "f32").all_reduce_clip([[torch.empty(0, device="cuda")] for _ in range(4)], 1.0, synced=big)
+assert bool(norm.isnan())
+report()
+one = [torch.ones(1000, device="cuda")]
+assert abs(float(rrv.grad_norm(one)) - 1000 ** 0.5) < 1e-4 and abs(float(rrv.clip_grads(one, 1.0)) - 1000 ** 0.5) < 1e-4
+g = ranks(4, 1 << 19, torch.float32)
+assert abs(float(rrv.BucketPlan([1 << 19], "f32").all_reduce_clip(g, 1.0)) - 2.5 * 2 ** 9.5) < 1e-2
+report()
+""", RR_DEBUG_BULK_TIMEOUT="2")
+    assert out.count("RAN OUT 4 True") == 6 and out.count("NO TIMEOUT") == 1, out
