@@ -406,14 +406,14 @@ rr_status_t rr_clip_grads(const rr_tensor_list_t* grads, float max_norm, float e
  * rounding), ||g|| = the norm of all a and of the synced list's tensors, and
  * every rank's gradients become round(c * a), rounded once.  synced (or NULL)
  * lists tensors whose gradients are already alike on every rank -- an
- * embedding's, say (rr_embedding_grad) -- with the same nranks: they count
- * into the norm and are clipped as rr_clip_grads does, from rank 0's copy.
- * Between its two passes the call may keep the fp32 sums in the gradients' own
- * buffers (ranks 0 and 1), so a call that ends with RR_ERR_CUDA, or one of
- * whose bounded waits ran out (rr_check_timeouts), leaves the gradients
- * undefined.  op: SUM or AVG.  With nranks 1 it is the clipping
- * alone.  Other arguments and errors as rr_bucket_allreduce_range and
- * rr_clip_grads. */
+ * embedding's, say (rr_embedding_grad) -- with the same nranks (a list of no
+ * tensors counts as NULL, whatever its nranks): they count into the norm and
+ * are clipped as rr_clip_grads does, from rank 0's copy.  Between its two
+ * passes the call may keep the fp32 sums in the gradients' own buffers (ranks
+ * 0 and 1), so a call that ends with RR_ERR_CUDA, or one of whose bounded
+ * waits ran out (rr_check_timeouts), leaves the gradients undefined.  op: SUM
+ * or AVG.  With nranks 1 it is the clipping alone.  Other arguments and errors
+ * as rr_bucket_allreduce_range and rr_clip_grads. */
 rr_status_t rr_bucket_allreduce_clip(const rr_bucket_plan_t* plan, int first_bucket, int nbuckets, void* const* grads,
                                      int nranks, rr_op_t op, const rr_tensor_list_t* synced, float max_norm,
                                      float eps, float* norm, void* workspace, size_t workspace_bytes,

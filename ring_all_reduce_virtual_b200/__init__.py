@@ -627,7 +627,7 @@ class BucketPlan:
         (``rr_bucket_allreduce_clip``): the average (``op``) is formed in
         fp32, scaled and rounded once.  ``synced`` adds gradients that are
         already alike on every rank (rank 0's count: a ``GradList`` or one list
-        per rank) to the norm and to the clipping.  Returns the norm before
+        per rank; ``[]`` is none) to the norm and to the clipping.  Returns the norm before
         clipping as a float32 scalar on the device (``out`` where it is given)."""
         g, n, dev = self._grads(grads)
         rest = GradList._of(synced) if synced is not None else None

@@ -395,6 +395,9 @@ rr_status_t bucket_allreduce_clip(const rr_bucket_plan_t* plan, int b0, int nb, 
     uint64_t rest = 0, S = 0, R = 0;
     if (synced) {
         if ((st = check_list(synced, &rest)) != RR_OK) return st;
+        if (synced->ntensors == 0) synced = nullptr;  // no tensors: any rank count
+    }
+    if (synced) {
         if (synced->nranks != n) return fail(RR_ERR_INVALID_ARG, "the synced list has another number of ranks");
         list_bytes(synced, &R);
     }

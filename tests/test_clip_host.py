@@ -139,3 +139,13 @@ def test_grad_list_checks_its_tensors():
         rrv.grad_norm([cpu])
     with pytest.raises(ValueError, match="CUDA"):
         rrv.clip_grads([cpu], 1.0)
+
+
+@pytest.mark.parametrize("nranks", [1, 2, 3])
+def test_an_empty_synced_list_is_none(nranks):
+    """Whatever its rank count: the call goes on to its later checks (here the workspace's) and is refused there."""
+    plan = rrv.BucketPlan([1000, 20], "bf16", 1 << 20)
+    grads = (ctypes.c_void_p * 4)(*[BASE + (i << 24) for i in range(4)])
+    st = _lib.lib().rr_bucket_allreduce_clip(plan._h, 0, 1, grads, 2, 1, List([], [], nranks=nranks).ref, 1.0, 1e-6, NORM,
+                                             WS, 8, None)
+    assert st == INVALID and b"workspace too small" in _lib.lib().rr_last_error()

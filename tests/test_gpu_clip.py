@@ -562,3 +562,13 @@ assert abs(float(rrv.BucketPlan([1 << 19], "f32").all_reduce_clip(g, 1.0)) - 2.5
 report()
 """, RR_DEBUG_BULK_TIMEOUT="2")
     assert out.count("RAN OUT 4 True") == 6 and out.count("NO TIMEOUT") == 1, out
+
+
+@pytest.mark.parametrize("n", [1, 2, 4])
+def test_clipped_sync_with_an_empty_synced_list(n):
+    plan = rrv.BucketPlan([5000, 3], "bf16")
+    for empty in ([], [[]] * n, rrv.GradList([])):
+        a = [[values(10 * r + t, m, torch.bfloat16) for t, m in enumerate((5000, 3))] for r in range(n)]
+        b = [[t.clone() for t in rank] for rank in a]
+        want, got = plan.all_reduce_clip(a, 0.5), plan.all_reduce_clip(b, 0.5, synced=empty)
+        assert torch.equal(want, got) and all(torch.equal(x, y) for p, q in zip(a, b) for x, y in zip(p, q))
