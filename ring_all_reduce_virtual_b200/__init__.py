@@ -275,6 +275,15 @@ class GradSet:
         self._plans = weakref.WeakSet()  # plans this set was checked against
         self._list = None  # this set as a GradList, made when a norm or a clipping first asks for it
 
+    @classmethod
+    def _of(cls, grads) -> "GradSet":
+        """``grads`` as a GradSet; a GradList's is made once and kept with it."""
+        if not isinstance(grads, GradList):
+            return cls([grads] if len(grads) and hasattr(grads[0], "data_ptr") else grads)
+        if grads._set is None:
+            grads._set = cls(grads._keep)
+        return grads._set
+
 
 class GradList:
     """The gradient tensors whose global norm is taken and that are clipped,
@@ -282,8 +291,9 @@ class GradList:
     (one rank), or one list per rank (``grads[r][t]``) whose ranks hold the
     same sizes and types.  Unlike a ``GradSet`` a list may mix float32,
     bfloat16 and float16 tensors.  ``grad_norm``, ``clip_grads`` and
-    ``BucketPlan.all_reduce_clip`` accept this, a ``GradSet`` or the lists; it
-    keeps the tensors alive and stays valid while they keep their storage."""
+    ``BucketPlan.all_reduce_clip`` (for its gradients, which are of one type,
+    and for ``synced``) accept this, a ``GradSet`` or the lists; it keeps the
+    tensors alive and stays valid while they keep their storage."""
 
     def __init__(self, grads):
         grads = list(grads)
@@ -307,6 +317,7 @@ class GradList:
         self._marshal(_ptr_array(flat), [int(g.numel()) for g in ranks[0]], codes, len(ranks))
         self.device = flat[0].device if flat else None
         self._keep = ranks  # the tensors must outlive the pointers
+        self._set = None  # this list as a GradSet, made when a bucket call first asks for it
 
     def _marshal(self, ptrs, numels, codes, nranks):
         n = len(numels)
@@ -327,7 +338,7 @@ class GradList:
             one = cls.__new__(cls)
             one._marshal(grads.ptrs, grads.numels, [grads.dtype] * len(grads.numels), grads.nranks)
             one.device = grads.device
-            one._keep = grads._keep
+            one._keep, one._set = grads._keep, None
             grads._list = one
         return grads._list
 
@@ -553,7 +564,7 @@ class BucketPlan:
     def _grads(self, grads):
         """(pointers, nranks, device) of gradients that match this plan's
         tensor sizes and dtype (checked once per GradSet and plan)."""
-        gs = grads if isinstance(grads, GradSet) else GradSet(grads)
+        gs = grads if isinstance(grads, GradSet) else GradSet._of(grads)
         if self not in gs._plans:
             if gs.numels != self.numels or gs.dtype != self.grad_dtype:
                 raise ValueError("gradients do not match the bucket plan (tensor count, sizes or dtype)")

@@ -149,3 +149,38 @@ def test_an_empty_synced_list_is_none(nranks):
     st = _lib.lib().rr_bucket_allreduce_clip(plan._h, 0, 1, grads, 2, 1, List([], [], nranks=nranks).ref, 1.0, 1e-6, NORM,
                                              WS, 8, None)
     assert st == INVALID and b"workspace too small" in _lib.lib().rr_last_error()
+
+
+class Fake:
+    """What the argument checks read of a CUDA tensor, without a GPU; its address is never used."""
+
+    is_cuda = True
+    device = torch.device("cuda", 0)
+
+    def __init__(self, n, dtype=torch.bfloat16, at=BASE):
+        self.n, self.dtype, self.at = n, dtype, at
+
+    def numel(self):
+        return self.n
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return self.at
+
+
+def test_bucket_calls_take_a_grad_list():
+    plan = rrv.BucketPlan([1000, 20], "bf16", 1 << 20)
+    for n in (1, 3):
+        ranks = [[Fake(m, at=BASE + ((2 * r + t) << 24)) for t, m in enumerate((1000, 20))] for r in range(n)]
+        want = plan._grads(rrv.GradSet(ranks))
+        gl = rrv.GradList(ranks if n > 1 else ranks[0])
+        got = plan._grads(gl)
+        assert list(got[0]) == list(want[0]) and got[1:] == want[1:]
+        assert plan._grads(gl)[0] is got[0]  # marshalled once
+    assert list(plan._grads(ranks[0])[0]) == list(want[0])[:2]  # one rank's tensors as they are
+    for wrong in (rrv.GradList([Fake(1000), Fake(21)]), rrv.GradList([Fake(1000), Fake(20, torch.float32)]),
+                  rrv.GradList([])):
+        with pytest.raises(ValueError):
+            plan._grads(wrong)

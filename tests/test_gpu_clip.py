@@ -572,3 +572,15 @@ def test_clipped_sync_with_an_empty_synced_list(n):
         b = [[t.clone() for t in rank] for rank in a]
         want, got = plan.all_reduce_clip(a, 0.5), plan.all_reduce_clip(b, 0.5, synced=empty)
         assert torch.equal(want, got) and all(torch.equal(x, y) for p, q in zip(a, b) for x, y in zip(p, q))
+
+
+@pytest.mark.parametrize("n", [1, 2, 4])
+def test_clipped_sync_of_a_grad_list(n):
+    plan = rrv.BucketPlan([5000, 3], "bf16")
+    a = [[values(10 * r + t, m, torch.bfloat16) for t, m in enumerate((5000, 3))] for r in range(n)]
+    b = [[t.clone() for t in rank] for rank in a]
+    gl = rrv.GradList(b if n > 1 else b[0])
+    for limit in (0.5, 0.25):
+        want, got = plan.all_reduce_clip(a, limit, "avg"), plan.all_reduce_clip(gl, limit, "avg")
+        assert torch.equal(want, got) and all(torch.equal(x, y) for p, q in zip(a, b) for x, y in zip(p, q))
+    assert torch.equal(rrv.grad_norm(gl), rrv.grad_norm(b))
