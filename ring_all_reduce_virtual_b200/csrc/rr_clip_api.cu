@@ -74,7 +74,7 @@ rr_status_t check_scratch(float* norm, void* ws, size_t have, size_t need, std::
     const uintptr_t a = (uintptr_t)norm, b = (uintptr_t)ws;
     if (meets(spans, a, a + 4) || meets(spans, b, b + need) || (a < b + need && b < a + 4))
         return fail(RR_ERR_INVALID_ARG, "buffers overlap (or repeat): the norm or the workspace");
-    return RR_OK;
+    return check_device_spans(spans);
 }
 
 rr_status_t check_clip(float max_norm, float eps)
@@ -333,7 +333,6 @@ rr_status_t grad_norm(const rr_tensor_list_t* grads, float* norm, void* ws, size
     std::vector<Span> spans;
     add_spans(grads, 1, false, spans);
     if ((st = check_scratch(norm, ws, ws_bytes, workspace_bytes(norm_slots(grads)), spans)) != RR_OK) return st;
-    if ((st = check_device_ptrs(grads->ptrs, grads->ntensors)) != RR_OK) return st;
     Passes run{static_cast<double*>(ws), stream};
     ClipArgs a{};
     a.norm = norm;
@@ -359,7 +358,6 @@ rr_status_t clip_grads(const rr_tensor_list_t* grads, float max_norm, float eps,
     std::vector<Span> spans;
     add_spans(grads, n, true, spans);
     if ((st = check_scratch(norm, ws, ws_bytes, workspace_bytes(norm_slots(grads)), spans)) != RR_OK) return st;
-    if ((st = check_device_ptrs(grads->ptrs, n * grads->ntensors)) != RR_OK) return st;
     Passes run{static_cast<double*>(ws), stream, n * S >= kBulkClipBytes && bulk_wait_counters()};
     ClipArgs a{};
     a.in_l2 = S <= kKeepBytes;

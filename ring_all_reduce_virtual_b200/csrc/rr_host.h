@@ -159,6 +159,17 @@ inline rr_status_t check_device_ptrs(const void* const* p, int n)
     return RR_OK;
 }
 
+// The same for a call's spans, which leave out tensors without elements.
+inline rr_status_t check_device_spans(const std::vector<Span>& spans)
+{
+    for (const Span& s : spans) {
+        const void* p = reinterpret_cast<const void*>(s.lo);
+        const rr_status_t st = check_device_ptrs(&p, 1);
+        if (st != RR_OK) return st;
+    }
+    return RR_OK;
+}
+
 // Optional (RR_DEBUG=1): after a call that enqueued work, synchronise its
 // stream (unless the stream is being captured into a graph) and report a
 // kernel fault, or a bounded device wait that ran out, at the call that

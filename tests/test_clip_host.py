@@ -184,3 +184,35 @@ def test_bucket_calls_take_a_grad_list():
                   rrv.GradList([])):
         with pytest.raises(ValueError):
             plan._grads(wrong)
+
+
+def test_debug_mode_checks_the_pointers_of_tensors_with_elements():
+    """RR_DEBUG=1: an empty tensor's NULL passes as it does without it (the call gets as far as a launch, which fails where
+    no GPU is), and every gradient of every call is looked up."""
+    import os
+    import subprocess
+    import sys
+
+    script = """
+import sys
+sys.path[:0] = sys.argv[1:]
+from test_clip_host import *
+from ring_all_reduce_virtual_b200 import _lib
+lib = _lib.lib()
+empty = List([0, 0], [0, 1], nranks=2, ptrs=[None] * 4)
+made_up = List([0, 8], [0, 1], nranks=2, ptrs=[None, BASE] * 2)
+for call in (norm, clip):
+    print("EMPTY", call(empty) == _lib.RR_ERR_CUDA, b"not device memory" not in lib.rr_last_error())
+print("MADE UP", norm(made_up) == INVALID, b"not device memory" in lib.rr_last_error())
+two = List([0, 8], [0, 1], nranks=2, ptrs=[None, BASE, None, BASE + 64])
+print("MADE UP", clip(two) == INVALID, b"not device memory" in lib.rr_last_error())
+plan = rrv.BucketPlan([1000, 0], "bf16", 1 << 20)
+grads = (ctypes.c_void_p * 4)(BASE, None, BASE + (1 << 20), None)
+st = lib.rr_bucket_allreduce_clip(plan._h, 0, plan.num_buckets, grads, 2, 1, None, 1.0, 1e-6, NORM, WS, BIG, None)
+print("MADE UP", st == INVALID, b"not device memory" in lib.rr_last_error())
+"""
+    here = os.path.dirname(os.path.abspath(__file__))
+    out = subprocess.run([sys.executable, "-c", script, here, os.path.dirname(here)], capture_output=True, text=True,
+                         env=dict(os.environ, RR_DEBUG="1", CUDA_VISIBLE_DEVICES=""), timeout=300)
+    assert out.returncode == 0, out.stderr[-2000:]
+    assert out.stdout.count("EMPTY True True") == 2 and out.stdout.count("MADE UP True True") == 3, out.stdout

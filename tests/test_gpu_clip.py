@@ -584,3 +584,22 @@ def test_clipped_sync_of_a_grad_list(n):
         want, got = plan.all_reduce_clip(a, limit, "avg"), plan.all_reduce_clip(gl, limit, "avg")
         assert torch.equal(want, got) and all(torch.equal(x, y) for p, q in zip(a, b) for x, y in zip(p, q))
     assert torch.equal(rrv.grad_norm(gl), rrv.grad_norm(b))
+
+
+def test_debug_mode_takes_lists_with_empty_tensors():
+    """RR_DEBUG=1 with tensors whose own pointer is NULL, in every call."""
+    out = run_child(r"""
+import torch
+import ring_all_reduce_virtual_b200 as rrv
+def grads(n):
+    return [[torch.empty(0, device="cuda"), torch.full((500,), 2.0, device="cuda"), torch.empty(0, device="cuda")] for _ in range(n)]
+assert grads(1)[0][0].data_ptr() == 0
+want = 2.0 * 500 ** 0.5
+print("NORM", abs(float(rrv.grad_norm(grads(1))) - want) < 1e-5 * want)
+g = grads(2)
+print("CLIP", abs(float(rrv.clip_grads(g, 1.0)) - want) < 1e-5 * want, abs(float(g[1][1].norm()) - 1.0) < 1e-5)
+g, s = grads(3), grads(3)
+norm = rrv.BucketPlan([0, 500, 0], "f32").all_reduce_clip(g, 1.0, synced=s)
+print("SYNC", abs(float(norm) - want * 2 ** 0.5) < 1e-5 * want, abs(float(g[2][1].norm()) - 0.5 ** 0.5) < 1e-5)
+""", RR_DEBUG="1")
+    assert "NORM True" in out and "CLIP True True" in out and "SYNC True True" in out, out
