@@ -132,3 +132,81 @@ def test_rows_of_another_width_on_another_rank_are_refused(as_set, bad, shape):
 def test_rows_may_be_grouped_differently():
     """Leading axes only group the rows: the same rows and width count as alike."""
     assert rrv._row_set([Fake(6, 8), Fake(2, 3, 8)], "rows")[1:4] == (2, 6, 8)
+
+
+SEARCH = r"""
+#include <cmath>
+#include <cstdio>
+#include <random>
+#include <vector>
+#include <algorithm>
+#include "rr_search.h"
+
+// A warp's search for the rows [v0, v0 + 32): its rounds, and the range that it leaves.
+static int follow(const std::vector<uint32_t>& keys, uint64_t v0, uint32_t& lo, uint32_t& hi)
+{
+    int rounds = 0;
+    lo = 0;
+    hi = (uint32_t)keys.size();
+    while (hi - lo > 64) {
+        uint32_t below = 0, within = 0;
+        for (uint32_t lane = 0; lane < 32; ++lane) {
+            const uint64_t at = lo + (uint64_t)lane * rr::search_step(lo, hi);
+            if (at >= hi) continue;
+            below += keys[at] < v0;
+            within += keys[at] < v0 + 32;
+        }
+        ++rounds;
+        if (rounds > 1000000 || !rr::search_narrow(lo, hi, below, within)) break;
+    }
+    return rounds;
+}
+
+int main()
+{
+    std::mt19937_64 gen(1);
+    std::uniform_real_distribution<double> unit(0.0, 1.0);
+    int bad = 0;
+    for (const uint32_t V : {1u, 40u, 5000u})
+        for (const uint32_t M : {1u, 64u, 65u, 2049u, 65536u, 1000003u})
+            for (int kind = 0; kind < 5; ++kind) {
+                std::vector<uint32_t> keys(M);
+                for (uint32_t i = 0; i < M; ++i) {
+                    const double u = unit(gen);
+                    const uint32_t zipf = std::min(V, (uint32_t)(std::exp(u * std::log(V + 1.0)) - 1.0));
+                    keys[i] = kind == 0 ? zipf                              // frequent tokens, first rows
+                              : kind == 1 ? (zipf * 2654435761u) % V        // ... anywhere
+                              : kind == 2 ? V / 2                           // one token
+                              : kind == 3 ? (u < 0.9 ? V : (uint32_t)(unit(gen) * V))  // ids without a row behind
+                                          : (uint32_t)(unit(gen) * V);
+                }
+                std::sort(keys.begin(), keys.end());
+                const double most = std::ceil(std::log2((double)M)) + 3;
+                for (uint64_t v0 = 0; v0 < V; v0 += 32) {
+                    uint32_t lo, hi;
+                    const int rounds = follow(keys, v0, lo, hi);
+                    const double steps = rounds + std::ceil(std::log2(hi - lo + 1.0));
+                    const bool lost = lo > hi || hi > M || (lo > 0 && keys[lo - 1] >= v0) || (hi < M && keys[hi] < v0 + 32);
+                    if ((lost || steps > most) && bad++ < 5)
+                        std::printf("V %u M %u kind %d v0 %llu: %d rounds to [%u, %u)\n", V, M, kind, (unsigned long long)v0,
+                                    rounds, lo, hi);
+                }
+            }
+    std::printf("bad %d\n", bad);
+    return bad != 0;
+}
+"""
+
+
+def test_a_frequent_token_does_not_lengthen_the_search_for_rows_without_one(tmp_path):
+    """Every round but the last halves the range, so r rounds leave at most M / 2^(r - 1) positions, and the rounds and the
+    binary search behind them are at most log2(M) + 3 steps; the range keeps all that a lane looks for."""
+    import os
+    import subprocess
+
+    src, exe = tmp_path / "search.cpp", tmp_path / "search"
+    src.write_text(SEARCH)
+    csrc = os.path.join(os.path.dirname(os.path.abspath(rrv.__file__)), "csrc")
+    subprocess.run(["g++", "-std=c++17", "-O2", "-Wall", "-Werror", "-I", csrc, "-o", str(exe), str(src)], check=True)
+    out = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
+    assert out.returncode == 0 and "bad 0" in out.stdout, out.stdout
