@@ -23,8 +23,6 @@
 // us: 16, 77 and 11 for the joins.  A sort by a cluster of 8 CTAs in one launch,
 // the keys in distributed shared memory, took 18 us for 16384 tokens and 37 for
 // 65536, where the three launches take 14 and 16.
-#include <atomic>
-
 #include "rr_launch.cuh"
 #include "rr_search.h"
 
@@ -980,24 +978,6 @@ __global__ void __launch_bounds__(kThreads) embed_join_kernel(const __grid_const
     }
 }
 
-// A ring kernel: more shared memory than a launch gets by default, which is
-// asked for once per kernel and device.
-template <void (*KERNEL)(EmbedGradParams)>
-cudaError_t launch_ring(dim3 grid, cudaStream_t s, const EmbedGradParams& p)
-{
-    static std::atomic<uint64_t> asked{0};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-    if (!(asked.load(std::memory_order_relaxed) & bit) || bit == 0) {
-        e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kReduceWarps * kRingBytes));
-        if (e != cudaSuccess) return e;
-        asked.fetch_or(bit, std::memory_order_relaxed);
-    }
-    return launch_pdl(KERNEL, grid, kReduceWarps * 32, kReduceWarps * kRingBytes, s, p);
-}
-
 unsigned blocks_for(uint64_t items, uint64_t per) { return (unsigned)((items + per - 1) / per); }
 
 template <class In, class Out, int VEC>
@@ -1005,17 +985,19 @@ cudaError_t reduce_typed(const EmbedGradParams& p, int* launches, cudaStream_t s
 {
     const uint32_t slices = blocks_for(p.D, kEmbedCols);
     const dim3 grid(blocks_for(p.nblk, kReduceWarps), slices);
+    constexpr uint32_t kRings = kReduceWarps * kRingBytes;
+    static_assert(kRings <= 48 * 1024, "within the default dynamic shared memory of a CTA");
     cudaError_t e;
     if constexpr (VEC * sizeof(typename In::T) < 4) {
         e = launch_pdl(embed_reduce_narrow_kernel<In, Out, VEC>, grid, kReduceWarps * 32, 0, s, p);
     } else if (p.accumulate && p.nout == 1) {
         if (p.nblk > 2 && p.nblk <= kJoinHere && p.M <= kRankMax) {
             *launches += 1;
-            return launch_ring<embed_reduce_kernel<In, Out, VEC, true, true>>(grid, s, p);
+            return launch_pdl(embed_reduce_kernel<In, Out, VEC, true, true>, grid, kReduceWarps * 32, kRings, s, p);
         }
-        e = launch_ring<embed_reduce_kernel<In, Out, VEC, true, false>>(grid, s, p);
+        e = launch_pdl(embed_reduce_kernel<In, Out, VEC, true, false>, grid, kReduceWarps * 32, kRings, s, p);
     } else {
-        e = launch_ring<embed_reduce_kernel<In, Out, VEC, false, false>>(grid, s, p);
+        e = launch_pdl(embed_reduce_kernel<In, Out, VEC, false, false>, grid, kReduceWarps * 32, kRings, s, p);
     }
     if (e != cudaSuccess) return e;
     *launches += 1;
