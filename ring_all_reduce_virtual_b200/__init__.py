@@ -371,9 +371,6 @@ def _placed(stream, device):
                 yield
 
 
-_NORM_BYTES = 256  # in front of a workspace, for the norm
-
-
 def _with_norm(what: str, fn, args: tuple, device, need: int, out, stream):
     """Run ``fn(*args, norm pointer, workspace pointer, bytes, stream)``; the norm's tensor."""
     torch, raw, current = _calls()
@@ -381,19 +378,14 @@ def _with_norm(what: str, fn, args: tuple, device, need: int, out, stream):
     if stream is not None or index != current():
         with _placed(stream, device):
             return _with_norm(what, fn, args, device, need, out, None)
-    if out is None and need <= 1 << 16:  # one piece of memory for both, which lives on with the norm
-        mem = torch.empty((_NORM_BYTES + need) // 4, dtype=torch.float32, device=device)
-        at = mem.data_ptr()
-        st = fn(*args, at, at + _NORM_BYTES, need, raw(index))
-        if st:
-            check(st, what)
-        return mem[0]
-    if out is None:
-        out = torch.empty((), dtype=torch.float32, device=device)
-    if not out.is_cuda or out.dtype != torch.float32 or out.numel() != 1 or out.device != device:
+    if out is None:  # memory of its own: a norm that is kept, in a log say, does not keep the workspace
+        out = torch.empty_strided((), (), dtype=torch.float32, device=device)  # 0.9 us less than empty(())
+    elif not out.is_cuda or out.dtype != torch.float32 or out.numel() != 1 or out.device != device:
         raise ValueError("out must be one float32 element on the gradients' device")
-    mem = torch.empty(need, dtype=torch.uint8, device=device)
-    check(fn(*args, out.data_ptr(), mem.data_ptr(), need, raw(index)), what)
+    mem = torch.empty_strided((need,), (1,), dtype=torch.uint8, device=device)
+    st = fn(*args, out.data_ptr(), mem.data_ptr(), need, raw(index))
+    if st:
+        check(st, what)
     return out
 
 

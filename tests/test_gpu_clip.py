@@ -603,3 +603,13 @@ norm = rrv.BucketPlan([0, 500, 0], "f32").all_reduce_clip(g, 1.0, synced=s)
 print("SYNC", abs(float(norm) - want * 2 ** 0.5) < 1e-5 * want, abs(float(g[2][1].norm()) - 0.5 ** 0.5) < 1e-5)
 """, RR_DEBUG="1")
     assert "NORM True" in out and "CLIP True True" in out and "SYNC True True" in out, out
+
+
+def test_a_kept_norm_keeps_four_bytes():
+    """Norms of calls without `out` have a storage of their own, not a piece of the call's workspace."""
+    g = [[torch.ones(5000, device="cuda")] for _ in range(2)]
+    kept = [rrv.grad_norm(g), rrv.clip_grads(g, 1.0), rrv.BucketPlan([5000], "f32").all_reduce_clip(g, 1.0)]
+    for norm in kept:
+        assert norm.shape == () and norm.dtype == torch.float32 and norm.untyped_storage().nbytes() == 4
+    near_norm(kept[0], 5000 ** 0.5)  # as they were, with later calls' workspaces beside them
+    near_norm(kept[1], 5000 ** 0.5)
