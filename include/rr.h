@@ -389,14 +389,15 @@ rr_status_t rr_grad_norm(const rr_tensor_list_t* grads, float* norm, void* works
 /* Clips gradients that are alike on every rank (the data-parallel step after
  * its sync): ||g|| is the global norm of rank 0's tensors, c = 1 where
  * ||g|| + eps <= max_norm and max_norm / (||g|| + eps) elsewhere, and
- * afterwards every rank's copy of every tensor holds round(c * rank 0's value),
- * one rounding to nearest even.  With nranks 1 the tensors are clipped in
- * place; with more, the other ranks' copies are only written (so rank 0 alone
- * need hold the gradients).  *norm receives ||g||.  A NaN norm makes every
- * value NaN, an infinite gradient zeroes the finite values (c is 0).  A norm of
- * finite gradients that is above fp32's largest number reads as infinite in
- * *norm and still counts as it is in c.  max_norm may be 0 or infinite.
- * Buffers must not overlap. */
+ * afterwards every rank's copy of every tensor holds round(c * rank 0's value):
+ * c to fp32's 24 bits, the product in fp32, then rounded to the tensor's type,
+ * each to nearest even.  With nranks 1 the tensors are clipped in place; with
+ * more, the other ranks' copies are only written (so rank 0 alone need hold the
+ * gradients).  *norm receives ||g||.  A NaN norm makes every value NaN, an
+ * infinite gradient zeroes the finite values (c is 0; under an infinite max_norm
+ * it is 1).  A norm of finite gradients that is above fp32's largest number reads
+ * as infinite in *norm and still counts as it is in c.  max_norm may be 0 or
+ * infinite.  Buffers must not overlap. */
 rr_status_t rr_clip_grads(const rr_tensor_list_t* grads, float max_norm, float eps, float* norm, void* workspace,
                           size_t workspace_bytes, cudaStream_t stream);
 
@@ -404,16 +405,17 @@ rr_status_t rr_clip_grads(const rr_tensor_list_t* grads, float max_norm, float e
  * clipping by the global norm of what was synced, in one call: a = the fold of
  * rr_bucket_allreduce_range in fp32 (the same operations, before its
  * rounding), ||g|| = the norm of all a and of the synced list's tensors, and
- * every rank's gradients become round(c * a), rounded once.  synced (or NULL)
- * lists tensors whose gradients are already alike on every rank -- an
- * embedding's, say (rr_embedding_grad) -- with the same nranks (a list of no
- * tensors counts as NULL, whatever its nranks): they count into the norm and
- * are clipped as rr_clip_grads does, from rank 0's copy.  Between its two
- * passes the call may keep the fp32 sums in the gradients' own buffers (ranks
- * 0 and 1), so a call that ends with RR_ERR_CUDA, or one of whose bounded
- * waits ran out (rr_check_timeouts), leaves the gradients undefined.  op: SUM
- * or AVG.  With nranks 1 it is the clipping alone.  Other arguments and errors
- * as rr_bucket_allreduce_range and rr_clip_grads. */
+ * every rank's gradients become round(c * a), the product formed in fp32 and
+ * rounded to their type as rr_clip_grads does.  synced (or NULL) lists tensors
+ * whose gradients are already alike on every rank -- an embedding's, say
+ * (rr_embedding_grad) -- with the same nranks (a list of no tensors counts as
+ * NULL, whatever its nranks): they count into the norm and are clipped as
+ * rr_clip_grads does, from rank 0's copy.  Between its two passes the call may
+ * keep the fp32 sums in the gradients' own buffers (ranks 0 and 1), so a call
+ * that ends with RR_ERR_CUDA, or one of whose bounded waits ran out
+ * (rr_check_timeouts), leaves the gradients undefined.  op: SUM or AVG.  With
+ * nranks 1 it is the clipping alone.  Other arguments and errors as
+ * rr_bucket_allreduce_range and rr_clip_grads. */
 rr_status_t rr_bucket_allreduce_clip(const rr_bucket_plan_t* plan, int first_bucket, int nbuckets, void* const* grads,
                                      int nranks, rr_op_t op, const rr_tensor_list_t* synced, float max_norm,
                                      float eps, float* norm, void* workspace, size_t workspace_bytes,

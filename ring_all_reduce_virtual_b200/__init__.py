@@ -628,7 +628,7 @@ class BucketPlan:
         """Fused sync of buckets ``first .. first + count - 1`` (default: all)
         and clipping by the global norm of the result
         (``rr_bucket_allreduce_clip``): the average (``op``) is formed in
-        fp32, scaled and rounded once.  ``synced`` adds gradients that are
+        fp32, scaled there and then rounded.  ``synced`` adds gradients that are
         already alike on every rank (rank 0's count: a ``GradList`` or one list
         per rank; ``[]`` is none) to the norm and to the clipping.  Returns the norm before
         clipping as a float32 scalar on the device (``out`` where it is given)."""

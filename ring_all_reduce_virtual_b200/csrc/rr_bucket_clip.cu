@@ -6,8 +6,8 @@
 //   parked      the first pass parks a: an fp32 sum whole in rank 0's buffer,
 //               for 16-bit gradients its upper half in rank 0's buffer and its
 //               lower half in rank 1's -- the same elements the CTA has just
-//               read, so no memory beside the gradients is needed and the
-//               final value is rounded once; the scaling (rr_clip.cu) reads
+//               read, so no memory beside the gradients is needed and a is
+//               not rounded to 16 bits before it is scaled; the scaling (rr_clip.cu) reads
 //               the halves and writes every rank.  Traffic for N ranks of S
 //               elements of e bytes: 2 (N + 1) S e, 16-bit types 2 (N + 2) S e.
 //   folded      the first pass only sums the squares, the second folds again

@@ -5,7 +5,8 @@
 //
 //   norm    ||g|| = sqrt(sum over tensors t and elements i of g_t[i]^2)
 //   clip    c = 1 if ||g|| + eps <= max_norm else max_norm / (||g|| + eps);
-//           g_r[i] = round(c * g_0[i]) on every rank r
+//           g_r[i] = round(c * g_0[i]) on every rank r: c and the product in
+//           fp32, then the rounding to the tensor's type
 //
 // Both are bound by HBM.  The norm of 735 MB of bf16 takes 107 us, 6.9 TB/s (a copy
 // moves 6.55).  Clipping 4 replicas of 104 MB of fp16 (519 MB written and read

@@ -18,7 +18,7 @@
 //
 // Both are bound by HBM.  Lookup: 8 x 2048 bf16 rows of 2048 (101 MB) in 17.9 us, 5.6
 // TB/s.  Gradient: 8 x 2048 tokens into eight bf16 tables of 32000 x 2048 (1.11 GB)
-// in 191 us, 5.8 TB/s: 14 for the sort, 48 for the sums, 127 (at 6.6 TB/s) for
+// in 188 us, 5.9 TB/s: 14 for the sort, 47 for the sums, 127 (at 6.6 TB/s) for
 // the rows without a token; 8 x 8192 tokens onto one fp32 table (470 MB) in 105
 // us: 16, 77 and 11 for the joins.  A sort by a cluster of 8 CTAs in one launch,
 // the keys in distributed shared memory, took 18 us for 16384 tokens and 37 for
