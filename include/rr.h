@@ -462,6 +462,49 @@ rr_status_t rr_embedding_grad(const void* const* ids, rr_id_type_t id_type, cons
                               int64_t padding_idx, void* const* grads, int ngrads, rr_dtype_t grad_dtype,
                               int accumulate, void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/* ------------------------------------------- token log probabilities -- */
+
+/* What a model's logits say of given tokens, for every rank's rows in one
+ * launch and one pass over them.  logits[r]: ntokens rows of vocab values of
+ * dtype (RR_F32, RR_BF16 or RR_F16), row_stride elements from row to row (a
+ * padded LM head's further columns are not read); ids[r]: the ntokens given
+ * tokens, of id_type.  With z = scale * x (scale: 1 / temperature, finite and
+ * above 0), for row i = r * ntokens + t of the outputs:
+ *     lse[i]         = ln sum_j e^z_j
+ *     logprob[i]     = z_id - lse, 0 for an id outside [0, vocab) (a padded token)
+ *     entropy[i]     = - sum_j p_j ln p_j, p = e^(z - lse)     (NULL: not wanted)
+ *     top_id, top_logprob [i * top_k + j]: the j-th most likely id and its log
+ *                      probability, equal logits with the lowest id first, NaN
+ *                      above all; top_k 0..32, at most vocab (0: not wanted,
+ *                      the pointers are not looked at)
+ * all fp32 (top_id int32), sums in fp32.  Entries of -inf have probability 0.
+ * A row whose every z is -inf has no distribution: lse and every log
+ * probability of it are -inf, its entropy 0, its top ids the lowest.  A row
+ * with a NaN or whose largest z is +inf has NaN for all of them but its top
+ * ids (and the 0 of a padded token).  Rows may start on any element.  At most 2^31-1 rows in all,
+ * vocab and row_stride up to 2^31-2.  Outputs must overlap nothing; a logits
+ * buffer counts from its first row's first to its last row's last element. */
+rr_status_t rr_token_logprobs(const void* const* logits, size_t row_stride, const void* const* ids, rr_id_type_t id_type,
+                              int nranks, size_t ntokens, size_t vocab, rr_dtype_t dtype, float scale, float* logprob,
+                              float* lse, float* entropy, int top_k, float* top_logprob, int32_t* top_id,
+                              cudaStream_t stream);
+
+/* The gradient of rr_token_logprobs with respect to the logits, from the lse
+ * (and entropy) it gave: with g = dlogprob[i] (0 where the id is outside the
+ * vocabulary) and h = dentropy[i] (NULL: 0, entropy is not looked at),
+ *     dlogits[r][t, j] = round(scale * (g * ((j == id) - p_j) - h * p_j * (ln p_j + entropy[i])))
+ * in fp32, rounded once to dtype.  dlogits[r]: rows of vocab values,
+ * grad_stride elements apart, whose further columns are left as they are; it
+ * may be logits[r] itself with the same stride (each logit is read before its
+ * gradient is written), and otherwise overlaps nothing.  Rows whose lse is
+ * -inf, and rows with g = h = 0 (padded tokens), get zeros, whatever they hold.
+ * p is e^(z - lse), so lse must be this row's; where |lse| is above 2^24 it no
+ * longer holds the sum's logarithm and p is 1 for every logit at the maximum. */
+rr_status_t rr_token_logprobs_grad(const void* const* logits, size_t row_stride, const void* const* ids,
+                                   rr_id_type_t id_type, int nranks, size_t ntokens, size_t vocab, rr_dtype_t dtype,
+                                   float scale, const float* lse, const float* entropy, const float* dlogprob,
+                                   const float* dentropy, void* const* dlogits, size_t grad_stride, cudaStream_t stream);
+
 /* ------------------------------------------------ overlapped bucket sync -- */
 
 /* Opaque reducer (host memory and CUDA events owned by the library). */

@@ -16,14 +16,14 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
-from typing import Sequence
+from typing import Any, NamedTuple, Sequence
 
 from ._lib import MAX_RANKS, Cost, RingEvent, RRError, Stats, TensorList, check, lib
 
 __all__ = [
     "all_reduce", "all_reduce_wire", "all_reduce_host", "all_reduce_host_noalloc", "ring_step", "ring_schedule", "reduce_scatter", "all_gather", "all_to_all",
     "RankSet", "BucketPlan", "GradSet", "Reducer", "GradList", "grad_norm", "clip_grads",
-    "embedding", "embedding_grad", "cost_model", "pick_algo", "set_picker_params", "last_stats",
+    "embedding", "embedding_grad", "TokenLogprobs", "token_logprobs", "token_logprobs_grad", "cost_model", "pick_algo", "set_picker_params", "last_stats",
     "check_timeouts", "RRError",
     "OPS", "ALGOS", "MAX_RANKS",
 ]
@@ -514,6 +514,114 @@ def embedding_grad(tokens, grad_out, grads, op="avg", scale: float = 1.0, accumu
     with contextlib.nullcontext() if stream is None and dev.index == current() else _placed(stream, dev):
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
         check(lib().rr_embedding_grad(*args, ws.data_ptr(), need, raw(dev.index)), "embedding_grad")
+
+
+class TokenLogprobs(NamedTuple):
+    """What ``token_logprobs`` gives: float32 tensors [ranks, tokens] (``top_id``
+    int32 and ``top_logprob`` [ranks, tokens, top_k]); ``None`` for what was
+    not asked for."""
+
+    logprob: Any
+    lse: Any
+    entropy: Any = None
+    top_id: Any = None
+    top_logprob: Any = None
+
+
+def _logit_set(tensors, what: str):
+    """(pointer array, ranks, rows, vocabulary, elements from row to row, dtype
+    code, device) of the ranks' logits: contiguous tensors whose last axis is
+    the vocabulary (or a RankSet of them), or 2-D views with any row stride."""
+    if isinstance(tensors, RankSet):
+        ptrs, n, rows, width, d, dev = _row_set(tensors, what)
+        return ptrs, n, rows, width, width, d, dev
+    n = len(tensors)
+    if n < 1 or n > MAX_RANKS:
+        raise ValueError(f"{what}: need 1..{MAX_RANKS} logit tensors, got {n}")
+    t0 = tensors[0]
+    shape, dtype, device = t0.shape, t0.dtype, t0.device
+    if len(shape) < 2 or shape[-1] == 0:
+        raise ValueError(f"{what}: logits need two axes or more, the last not empty")
+    V = shape[-1]
+    rows = t0.numel() // V
+    stride = V if t0.is_contiguous() else t0.stride(0) if len(shape) == 2 and t0.stride(1) == 1 and rows > 1 else 0
+    for t in tensors:
+        if not t.is_cuda or t.shape != shape or t.dtype != dtype or t.device != device:
+            raise ValueError(f"{what}: logit tensors must be CUDA tensors of one shape, dtype and device")
+        if stride < V or not (t.is_contiguous() if stride == V else t.stride() == (stride, 1)):
+            raise ValueError(f"{what}: logits must be contiguous, or 2-D with contiguous rows and one row stride")
+    return _ptr_array(tensors), n, rows, V, stride, _dtype_code(dtype), device
+
+
+def token_logprobs(logits, tokens, scale: float = 1.0, entropy: bool = False, top_k: int = 0, stream=None) -> TokenLogprobs:
+    """Log probabilities of given tokens under ``softmax(scale * logits)``,
+    every rank's rows in one launch and one pass (``rr_token_logprobs``).
+    ``logits``: one tensor [tokens, vocabulary] per rank (float32, bfloat16 or
+    float16; any row stride); ``tokens``: one int32 or int64 tensor per rank, or
+    a RankSet.  A token outside the vocabulary (padding) has log probability 0.
+    ``entropy`` adds each row's entropy, ``top_k`` (up to 32) its most likely
+    ids, equal logits with the lowest id first, and their log probabilities."""
+    ids, id_type, n, T, dev = _id_set(tokens, "token_logprobs")
+    x, xn, rows, V, stride, d, xdev = _logit_set(logits, "token_logprobs")
+    if xn != n or rows != T or xdev != dev:
+        raise ValueError("token_logprobs: need one logit tensor [tokens, V] per rank, on the tokens' device")
+    k = int(top_k)
+    if not 0 <= k <= min(32, V):
+        raise ValueError("token_logprobs: top_k must be in 0..32 and at most the vocabulary")
+    torch, raw, current = _calls()
+    with contextlib.nullcontext() if stream is None and dev.index == current() else _placed(stream, dev):
+        def empty(*shape, dtype=torch.float32):
+            return torch.empty(shape, dtype=dtype, device=dev)
+        out = TokenLogprobs(empty(n, T), empty(n, T), empty(n, T) if entropy else None,
+                            empty(n, T, k, dtype=torch.int32) if k else None, empty(n, T, k) if k else None)
+        ptrs = [t.data_ptr() if t is not None else None for t in out]
+        st = lib().rr_token_logprobs(x, stride, ids, id_type, n, T, V, d, float(scale), *ptrs[:3], k, ptrs[4], ptrs[3],
+                                     raw(dev.index))
+        if st:
+            check(st, "token_logprobs")
+    return out
+
+
+def _row_values(t, n: int, T: int, dev, what: str):
+    """Pointer of one float32 value per row of every rank; None for None."""
+    if t is None:
+        return None
+    if not t.is_cuda or not t.is_contiguous() or str(t.dtype) != "torch.float32" or t.numel() != n * T or t.device != dev:
+        raise ValueError(f"token_logprobs_grad: {what} must be a contiguous float32 tensor [ranks, tokens] on the tokens' device")
+    return t.data_ptr()
+
+
+def token_logprobs_grad(logits, tokens, lse, dlogprob, entropy=None, dentropy=None, scale: float = 1.0, outs=None,
+                        stream=None):
+    """The gradient of ``token_logprobs`` with respect to the logits
+    (``rr_token_logprobs_grad``), from the ``lse`` (and the ``entropy``, where
+    ``dentropy`` is given) it returned for the same logits and scale.
+    ``dlogprob``, ``dentropy``: float32 [ranks, tokens], the loss's gradients
+    with respect to each log probability and entropy (-1 / tokens for a mean
+    cross entropy).  ``outs``: one tensor per rank like its logits -- the
+    logits themselves, say -- or None for new ones.  Returns ``outs``."""
+    ids, id_type, n, T, dev = _id_set(tokens, "token_logprobs_grad")
+    x, xn, rows, V, stride, d, xdev = _logit_set(logits, "token_logprobs_grad")
+    if xn != n or rows != T or xdev != dev:
+        raise ValueError("token_logprobs_grad: need one logit tensor [tokens, V] per rank, on the tokens' device")
+    if dentropy is not None and entropy is None:
+        raise ValueError("token_logprobs_grad: the entropy's gradient needs the entropy")
+    values = [_row_values(t, n, T, dev, what) for t, what in
+              ((lse, "lse"), (entropy if dentropy is not None else None, "entropy"), (dlogprob, "dlogprob"), (dentropy, "dentropy"))]
+    if lse is None or dlogprob is None:
+        raise ValueError("token_logprobs_grad: lse and dlogprob are needed")
+    torch, raw, current = _calls()
+    with contextlib.nullcontext() if stream is None and dev.index == current() else _placed(stream, dev):
+        if outs is None:
+            ranks = logits.tensors if isinstance(logits, RankSet) else logits
+            outs = [torch.empty(t.shape, dtype=t.dtype, device=dev) for t in ranks]
+        o, on, orows, oV, ostride, od, odev = _logit_set(outs, "token_logprobs_grad")
+        if on != n or orows != T or oV != V or od != d or odev != dev:
+            raise ValueError("token_logprobs_grad: need one gradient tensor per rank, like its logits")
+        st = lib().rr_token_logprobs_grad(x, stride, ids, id_type, n, T, V, d, float(scale), *values, o, ostride, raw(dev.index))
+        if st:
+            check(st, "token_logprobs_grad")
+    return outs
 
 
 class BucketPlan:

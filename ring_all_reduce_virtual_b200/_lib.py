@@ -88,6 +88,8 @@ def _declare(lib: ctypes.CDLL) -> None:
         "rr_embedding": (st, [PP, i, PP, PP, i, sz, sz, sz, i, f, P]),
         "rr_embedding_grad_workspace": (st, [i, sz, sz, sz, ctypes.POINTER(sz)]),
         "rr_embedding_grad": (st, [PP, i, PP, i, sz, sz, sz, i, i, f, ctypes.c_int64, PP, i, i, i, P, sz, P]),
+        "rr_token_logprobs": (st, [PP, sz, PP, i, i, sz, sz, i, f, P, P, P, i, P, P, P]),
+        "rr_token_logprobs_grad": (st, [PP, sz, PP, i, i, sz, sz, i, f, P, P, P, P, PP, sz, P]),
         "rr_reducer_create": (st, [P, PP, i, i, P, i, ctypes.POINTER(P)]),
         "rr_reducer_ready": (st, [P, i, P]),
         "rr_reducer_finish": (st, [P, P]),

@@ -1,0 +1,660 @@
+// rr_logprob.cu -- log probabilities of given tokens over all ranks' logits,
+// with entropy and top alternatives, and their gradient.
+//
+// For a row x of V logits, z = scale * x, m = max x, y_j = scale * (x_j - m):
+//     s = sum e^y_j       lse = scale * m + ln s       logprob = y_t - ln s
+//     t = sum e^y_j y_j   entropy = ln s - t / s
+// in one pass over the row: a thread keeps the running maximum of what it has
+// read with s and t relative to it, and rescales them when the maximum grows
+// (t / s shifts by the difference).  x_j - m is exact in sign and 0 at the
+// maximum, so a row whose every value is the type's lowest is uniform, as it
+// should be.  Exponentials are powers of two (y in units of ln 2).
+//
+// Bound by HBM: 2 or 4 bytes an element against about 5 issue slots (packed
+// fp32 pairs: one subtraction, one product, one sum) and one exponential, of
+// which an SM does 16 a clock -- bf16 logits at full bandwidth need 12.
+//
+// The top alternatives cost the pass nothing but the maxima it has anyway.  A
+// thread's maximum is an element of its own, so at least k elements are at or
+// above tau, the k-th largest of the threads' maxima, and every element that
+// is at or above tau belongs to a thread whose maximum is: k threads of 256
+// (more on ties).  Their elements alone are read once more, from L2, and go
+// through a sorted list of 32 per warp; the lists are merged.  Elements are
+// ordered by (value, lowest id first), so the outcome does not depend on who
+// saw them first.
+#include <type_traits>
+
+#include "rr_device.cuh"
+#include "rr_launch.cuh"
+#include "rr_logprob.h"
+
+namespace rr {
+
+namespace {
+
+constexpr int kU = 4;              // vectors a thread has on the way
+constexpr int kMaxSplit = 8;       // portable cluster size
+constexpr uint32_t kFull = 0xffffffffu;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// ------------------------------------------------------------- small pieces
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi)
+{
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void un2(F2 a, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v)); }
+__device__ __forceinline__ F2 add2(F2 a, F2 b)
+{
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b)
+{
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
+{
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+
+// The largest of a vector's values, NaN where one is.
+template <class Ty>
+__device__ __forceinline__ uint32_t max_words(uint32_t a, uint32_t b)
+{
+    uint32_t y;
+    if constexpr (std::is_same_v<Ty, BF16T>) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+    else if constexpr (std::is_same_v<Ty, F16T>) asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+    else y = __float_as_uint(max_nan(__uint_as_float(a), __uint_as_float(b)));
+    return y;
+}
+
+template <class Ty, int N>
+__device__ __forceinline__ float max_of(const uint4 (&raw)[N])
+{
+    uint32_t w = max_words<Ty>(max_words<Ty>(raw[0].x, raw[0].y), max_words<Ty>(raw[0].z, raw[0].w));
+#pragma unroll
+    for (int u = 1; u < N; ++u)
+        w = max_words<Ty>(w, max_words<Ty>(max_words<Ty>(raw[u].x, raw[u].y), max_words<Ty>(raw[u].z, raw[u].w)));
+    if constexpr (Ty::L == 8) {
+        float lo, hi;
+        Ty::unpack2(w, lo, hi);
+        return max_nan(lo, hi);
+    } else {
+        return __uint_as_float(w);
+    }
+}
+
+// Every element -inf.
+template <class Ty>
+__device__ __forceinline__ uint4 lowest_vector()
+{
+    const uint32_t w = std::is_same_v<Ty, BF16T> ? 0xff80ff80u : std::is_same_v<Ty, F16T> ? 0xfc00fc00u : 0xff800000u;
+    return make_uint4(w, w, w, w);
+}
+
+__device__ __forceinline__ int64_t id_at(const void* ids, int ids64, uint64_t t)
+{
+    return ids64 ? static_cast<const int64_t*>(ids)[t] : (int64_t)static_cast<const int32_t*>(ids)[t];
+}
+
+// ------------------------------------------------------- softmax statistics
+
+// The statistics of some elements: their maximum, and relative to it the sums
+// s of 2^y and t of 2^y y.
+struct Stat {
+    float m, s, t;
+};
+
+// a and b together.  c = scale * log2 e.
+__device__ __forceinline__ Stat joined(const Stat& a, const Stat& b, float c)
+{
+    Stat r;
+    r.m = max_nan(a.m, b.m);
+    const float ref = r.m == -INFINITY ? 0.0f : r.m;
+    // no element at all, or none above -inf: its sums are zeros, and 2^-2000 is
+    const float da = fmaxf((a.m - ref) * c, -2000.0f), db = fmaxf((b.m - ref) * c, -2000.0f);
+    const float fa = ex2(da), fb = ex2(db);
+    r.s = a.s * fa + b.s * fb;
+    r.t = (a.t + da * a.s) * fa + (b.t + db * b.s) * fb;
+    if (r.m != r.m || r.m == INFINITY) r.s = r.t = NAN;  // fmaxf drops the NaN of inf - inf
+    return r;
+}
+
+template <bool ENT>
+__device__ __forceinline__ void add_one(Stat& st, float x, float c)
+{
+    const Stat one{x, x == -INFINITY ? 0.0f : 1.0f, 0.0f};
+    st = joined(st, one, c);
+}
+
+// The running statistics of a thread's vectors.
+template <class Ty, bool ENT>
+struct Running {
+    float m = -INFINITY;
+    F2 s = f2(0.0f, 0.0f), t = f2(0.0f, 0.0f);
+
+    __device__ __forceinline__ void take(const uint4 (&raw)[kU], float c)
+    {
+        const float b = max_of<Ty, kU>(raw);
+        if (!(b <= m)) {  // NaN comes in here too
+            const float now = max_nan(m, b);
+            const float d = fmaxf((m - now) * c, -2000.0f), f = ex2(d);
+            if (ENT) t = mul2(fma2(s, f2(d, d), t), f2(f, f));
+            s = mul2(s, f2(f, f));
+            m = now;
+        }
+        const float ref = m == -INFINITY ? 0.0f : m;
+        const F2 neg = f2(-ref, -ref), cc = f2(c, c);
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            float a[Ty::L];
+            Ty::unpack(raw[u], a);
+#pragma unroll
+            for (int l = 0; l < Ty::L; l += 2) {
+                float lo, hi;
+                un2(mul2(add2(f2(a[l], a[l + 1]), neg), cc), lo, hi);
+                const F2 e = f2(ex2(lo), ex2(hi));
+                s = add2(s, e);
+                if (ENT) t = fma2(e, f2(fmaxf(lo, -2000.0f), fmaxf(hi, -2000.0f)), t);  // 0 * -inf is no 0
+            }
+        }
+    }
+    __device__ __forceinline__ Stat stat() const
+    {
+        float a, b, x, y;
+        un2(s, a, b);
+        un2(t, x, y);
+        Stat r{m, a + b, x + y};
+        if (m != m || m == INFINITY) r.s = r.t = NAN;
+        return r;
+    }
+};
+
+__device__ __forceinline__ Stat warp_joined(Stat st, float c)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const Stat other{__shfl_xor_sync(kFull, st.m, o), __shfl_xor_sync(kFull, st.s, o), __shfl_xor_sync(kFull, st.t, o)};
+        st = joined(st, other, c);
+    }
+    return st;
+}
+
+// --------------------------------------------------------- top alternatives
+
+// A whole number that orders fp32 values, NaN above all, both zeros alike.
+__device__ __forceinline__ uint32_t order_of(float x)
+{
+    if (x != x) return 0xffffffffu;
+    const uint32_t u = __float_as_uint(x + 0.0f);
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+__device__ __forceinline__ float value_of(uint32_t order)
+{
+    return __uint_as_float(order & 0x80000000u ? order & 0x7fffffffu : ~order);  // NaN's order gives a NaN
+}
+
+// An element's rank among all: the value above, the lowest id first.  0: none.
+__device__ __forceinline__ uint64_t entry_of(uint32_t order, uint32_t id) { return (uint64_t)order << 32 | (uint32_t)~id; }
+
+template <class K>
+__device__ __forceinline__ K larger(K a, K b) { return a > b ? a : b; }
+template <class K>
+__device__ __forceinline__ K smaller(K a, K b) { return a < b ? a : b; }
+
+// The warp's values, largest in lane 0 (a bitonic network).
+template <class K>
+__device__ __forceinline__ K warp_sorted(K v)
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int size = 2; size <= 32; size *= 2)
+#pragma unroll
+        for (int o = size / 2; o > 0; o /= 2) {
+            const K other = __shfl_xor_sync(kFull, v, o);
+            const bool keep_large = ((lane & o) == 0) == ((lane & size) == 0);
+            v = keep_large ? larger(v, other) : smaller(v, other);
+        }
+    return v;
+}
+
+// The 32 largest of two sorted lists, sorted.
+template <class K>
+__device__ __forceinline__ K warp_merged(K a, K b)
+{
+    const int lane = threadIdx.x & 31;
+    a = larger(a, __shfl_sync(kFull, b, 31 - lane));  // the larger half, bitonic
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) {
+        const K other = __shfl_xor_sync(kFull, a, o);
+        a = (lane & o) == 0 ? larger(a, other) : smaller(a, other);
+    }
+    return a;
+}
+
+// A warp's sorted list of the largest entries it has been offered.
+struct TopList {
+    uint64_t mine = 0;   // lane i: the i-th largest
+    uint64_t least = 0;  // entries must exceed it: the k-th of the list
+
+    __device__ __forceinline__ void offer(uint64_t e, int k)
+    {
+        uint32_t want = __ballot_sync(kFull, e > least);
+        if (want == 0) return;
+        if (__popc(want) > 5) {
+            mine = warp_merged(mine, warp_sorted(e > least ? e : 0));
+        } else {
+            const int lane = threadIdx.x & 31;
+            while (want) {
+                const uint64_t v = __shfl_sync(kFull, e, __ffs(want) - 1);
+                want &= want - 1;
+                const uint64_t up = __shfl_up_sync(kFull, mine, 1);
+                if (mine < v) mine = lane > 0 && up < v ? up : v;
+            }
+        }
+        least = __shfl_sync(kFull, mine, k - 1);
+    }
+};
+
+// ---------------------------------------------------------------- the pass
+
+template <class T>
+__device__ __forceinline__ T* cluster_at(T* p, uint32_t rank)
+{
+    uint64_t r;
+    asm("mapa.u64 %0, %1, %2;" : "=l"(r) : "l"(p), "r"(rank));
+    return reinterpret_cast<T*>(r);
+}
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }  // release
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }      // acquire
+
+struct Shared {
+    Stat part[kThreads / 32];
+    uint32_t order[kThreads / 32][32];
+    uint64_t list[kThreads / 32][32];
+    uint8_t who[kThreads];
+    uint32_t count[kThreads / 32 + 1];
+    uint32_t tau;
+    Stat all[kMaxSplit];               // cluster rank 0: of every CTA of the row
+    uint64_t lists[kMaxSplit][32];
+};
+
+// TEAM threads (a CTA of kThreads, or a warp) of each of `split` CTAs read a
+// row.  A warp per row is for short rows, whose sums a CTA would spend more
+// time joining than reading.
+template <class Ty, int TEAM, bool ENT, bool TOP>
+__global__ void __launch_bounds__(kThreads) logprob_kernel(const __grid_constant__ LogprobParams p)
+{
+    using T = typename Ty::T;
+    constexpr int L = Ty::L;
+    constexpr bool kWarp = TEAM == 32;
+    __shared__ Shared sh;
+    const int tid = kWarp ? threadIdx.x & 31 : threadIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t split = kWarp ? 1u : (uint32_t)p.split;
+    const uint32_t part = kWarp ? 0u : blockIdx.x % split;
+    const uint64_t row = kWarp ? (uint64_t)blockIdx.x * (kThreads / 32) + warp : blockIdx.x / split;
+    pdl_begin();
+    if (row >= p.M) return;  // a whole warp, of a kernel without barriers then
+    if (!kWarp && split > 1) cluster_arrive();  // this CTA runs: its shared memory may be written
+    const uint32_t r = (uint32_t)row / p.T, tok = (uint32_t)row % p.T;
+    const T* x = static_cast<const T*>(p.x[r]) + (uint64_t)tok * p.ld;
+    const float c = p.scale * kLog2e;
+
+    // head up to the first 16-byte boundary, whole vectors, tail
+    uint32_t head = (uint32_t)((L - phase_of(x, L)) & (L - 1));
+    if (head > p.V) head = p.V;
+    const uint32_t nv = (p.V - head) / L, tail = p.V - head - nv * L;
+    const uint32_t v0 = (uint32_t)((uint64_t)nv * part / split), v1 = (uint32_t)((uint64_t)nv * (part + 1) / split);
+    const uint4* xv = reinterpret_cast<const uint4*>(x + head);
+
+    Running<Ty, ENT> run;
+    for (uint32_t v = v0 + tid; v < v1; v += TEAM * kU) {
+        uint4 raw[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const uint64_t at = (uint64_t)v + u * TEAM;
+            raw[u] = lowest_vector<Ty>();
+            if (at < v1) raw[u] = TOP ? xv[at] : __ldcs(xv + at);  // read again by the alternatives
+        }
+        run.take(raw, c);
+    }
+    const float mine = run.m;
+    Stat st = run.stat();
+    const bool edge = part == 0 && (uint32_t)tid < head + tail;
+    const uint32_t edge_id = (uint32_t)tid < head ? (uint32_t)tid : head + nv * L + ((uint32_t)tid - head);
+    float edge_x = -INFINITY;
+    if (edge) {
+        edge_x = Ty::ld1(x + edge_id);
+        add_one<ENT>(st, edge_x, c);
+    }
+
+    st = warp_joined(st, c);
+    if constexpr (!kWarp) {
+        if (lane == 0) sh.part[warp] = st;
+        __syncthreads();
+        st = sh.part[0];
+#pragma unroll
+        for (int w = 1; w < kThreads / 32; ++w) st = joined(st, sh.part[w], c);
+    }
+
+    uint64_t best = 0;  // lane i of the team's first warp: the i-th largest entry
+    if constexpr (TOP) {
+        uint32_t order = v0 + tid < v1 ? order_of(mine) : 0u;  // 0: a thread without elements
+        const uint32_t sorted = warp_sorted(order);
+        uint32_t tau;
+        if constexpr (kWarp) {
+            tau = __shfl_sync(kFull, sorted, p.k - 1);
+        } else {
+            sh.order[warp][lane] = sorted;
+            __syncthreads();
+            if (warp == 0) {
+                uint32_t top = sorted;
+                for (int w = 1; w < kThreads / 32; ++w) top = warp_merged(top, sh.order[w][lane]);
+                if (lane == p.k - 1) sh.tau = top;
+            }
+            __syncthreads();
+            tau = sh.tau;
+        }
+        TopList list;
+        // the head's and the tail's elements first
+        if (warp == 0 || kWarp) list.offer(edge ? entry_of(order_of(edge_x), edge_id) : 0, p.k);
+        const bool in = order != 0 && order >= tau;
+        const uint32_t votes = __ballot_sync(kFull, in);
+        uint32_t nwho;
+        if constexpr (kWarp) {
+            nwho = __popc(votes);
+        } else {
+            if (lane == 0) sh.count[warp] = __popc(votes);
+            __syncthreads();
+            uint32_t before = 0;
+            nwho = 0;
+#pragma unroll
+            for (int w = 0; w < kThreads / 32; ++w) {
+                before += w < warp ? sh.count[w] : 0;
+                nwho += sh.count[w];
+            }
+            if (in) sh.who[before + __popc(votes & ((1u << lane) - 1))] = (uint8_t)tid;
+            __syncthreads();
+        }
+        // Every vector of the threads in question, one a lane: the i-th of
+        // each, then the next of each, so that ids rise and a tie is refused by
+        // the list at once.
+        const uint32_t each = (v1 - v0 + TEAM - 1) / TEAM;
+        const uint64_t items = (uint64_t)each * nwho;
+        for (uint64_t base = kWarp ? 0 : (uint64_t)warp * 32; base < items; base += TEAM) {
+            const uint64_t item = base + lane;
+            const uint32_t i = (uint32_t)(item / nwho), j = (uint32_t)(item % nwho);
+            const uint32_t who = kWarp ? __fns(votes, 0, (int)j + 1) : sh.who[item < items ? j : 0];
+            const uint64_t at = (uint64_t)v0 + (uint64_t)i * TEAM + who;
+            uint32_t ord[L];
+            uint32_t any = 0;
+            if (item < items && at < v1) {
+                float a[L];
+                Ty::unpack(xv[at], a);
+#pragma unroll
+                for (int l = 0; l < L; ++l) {
+                    ord[l] = order_of(a[l]);
+                    any |= (ord[l] >= tau ? 1u : 0u) << l;
+                }
+            }
+            uint32_t which = __reduce_or_sync(kFull, any);
+#pragma unroll
+            for (int l = 0; l < L; ++l)
+                if (which >> l & 1)
+                    list.offer(any >> l & 1 ? entry_of(ord[l], head + (uint32_t)at * L + l) : 0, p.k);
+        }
+        best = list.mine;
+        if constexpr (!kWarp) {
+            sh.list[warp][lane] = best;
+            __syncthreads();
+            if (warp == 0)
+                for (int w = 1; w < kThreads / 32; ++w) best = warp_merged(best, sh.list[w][lane]);
+        }
+    }
+
+    if (!kWarp && split > 1) {  // the other CTAs' results to the cluster's first
+        cluster_wait();
+        if (threadIdx.x == 0) *cluster_at(&sh.all[part], 0) = st;
+        if (TOP && warp == 0) *cluster_at(&sh.lists[part][lane], 0) = best;
+        cluster_arrive();
+        cluster_wait();
+        if (part != 0) return;
+        st = sh.all[0];
+        for (uint32_t q = 1; q < split; ++q) st = joined(st, sh.all[q], c);
+        if (TOP && warp == 0)
+            for (uint32_t q = 1; q < split; ++q) best = warp_merged(best, sh.lists[q][lane]);
+    }
+    if (!kWarp && warp != 0) return;
+
+    // the row's results; a row whose every scaled value is -inf has no
+    // distribution: lse and its log probabilities are -inf, its entropy 0.  One
+    // whose largest is +inf, or with a NaN, is NaN.
+    const float peak = st.m * p.scale;
+    const bool empty = peak == -INFINITY;
+    const float ln_s = peak == INFINITY ? NAN : logf(st.s);
+    if (lane == 0) {
+        const int64_t id = id_at(p.ids[r], p.ids64, tok);
+        float lp = 0.0f;
+        if (id >= 0 && id < (int64_t)p.V) lp = empty ? -INFINITY : (Ty::ld1(x + id) - st.m) * p.scale - ln_s;
+        p.logprob[row] = lp;
+        p.lse[row] = empty ? -INFINITY : __fmaf_rn(st.m, p.scale, ln_s);
+        if (ENT) p.entropy[row] = empty ? 0.0f : ln_s - kLn2 * (st.t / st.s);
+    }
+    if (TOP && lane < p.k) {
+        const float v = value_of((uint32_t)(best >> 32));
+        p.top_logprob[row * p.k + lane] = empty ? -INFINITY : (v - st.m) * p.scale - ln_s;
+        p.top_id[row * p.k + lane] = (int32_t)~(uint32_t)best;
+    }
+}
+
+// --------------------------------------------------------------- gradient
+//
+// dx_j = scale * (g (d_jt - p_j) - h p_j (ln p_j + H)), p_j = e^(z_j - lse):
+// one pass, each logit read once, each gradient written once.  A warp takes
+// kU vectors a lane of one row.  Rows of zero gradients (ignored tokens) and
+// rows without a distribution are written as zeros without being read.
+
+template <class Ty, bool ENT>
+struct GradRow {
+    float scale, lse, g, h, H, at_target;
+    uint32_t target;
+
+    // z - lse rounds once, at its own size: an error of p of half a step of ln p
+    __device__ __forceinline__ float at(float x) const
+    {
+        const float lp = __fmaf_rn(x, scale, -lse);
+        const float e = ex2(lp * kLog2e);
+        float d = g * e;
+        if (ENT) d += h * e * (fmaxf(lp, -2000.0f) + H);  // 0 * -inf is no 0
+        return d;
+    }
+};
+
+template <class Ty, bool ENT>
+__global__ void __launch_bounds__(kThreads) logprob_grad_kernel(const __grid_constant__ LogprobGradParams p)
+{
+    using T = typename Ty::T;
+    constexpr int L = Ty::L;
+    constexpr uint32_t TV = 32 * kU;
+    const int lane = threadIdx.x & 31;
+    pdl_begin();
+    const uint64_t w = p.first + (uint64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    const uint64_t row = w / p.tiles;
+    const uint32_t tile = (uint32_t)(w % p.tiles);
+    if (row >= p.M) return;
+    const uint32_t r = (uint32_t)row / p.T, tok = (uint32_t)row % p.T;
+    const T* x = static_cast<const T*>(p.x[r]) + (uint64_t)tok * p.ld;
+    T* dx = static_cast<T*>(p.dx[r]) + (uint64_t)tok * p.gld;
+    const int64_t id = id_at(p.ids[r], p.ids64, tok);
+    const bool known = id >= 0 && id < (int64_t)p.V;
+    const float lse = p.lse[row], dl = known ? p.dlogprob[row] : 0.0f;
+    GradRow<Ty, ENT> q;
+    q.scale = p.scale;
+    q.lse = lse;
+    q.g = -dl * p.scale;
+    q.h = ENT ? -p.dentropy[row] * p.scale : 0.0f;
+    q.H = ENT ? p.entropy[row] : 0.0f;
+    q.at_target = dl * p.scale;
+    q.target = known ? (uint32_t)id : 0xffffffffu;
+    const bool zeros = lse == -INFINITY || (q.g == 0.0f && q.h == 0.0f);
+
+    const bool same = phase_of(x, L) == phase_of(dx, L);
+    if (!same) {  // the gradient's rows lie at another phase: element by element
+        const uint32_t e0 = tile * TV * L;
+#pragma unroll 4
+        for (uint32_t k = 0; k < (uint32_t)kU * L; ++k) {
+            const uint32_t e = e0 + k * 32 + lane;
+            if (e >= p.V) break;
+            float d = 0.0f;
+            if (!zeros) {
+                d = q.at(Ty::ld1(x + e));
+                if (e == q.target) d += q.at_target;
+            }
+            Ty::st1(dx + e, d);
+        }
+        return;
+    }
+    uint32_t head = (uint32_t)((L - phase_of(x, L)) & (L - 1));
+    if (head > p.V) head = p.V;
+    const uint32_t nv = (p.V - head) / L, tail = p.V - head - nv * L;
+    if (tile == 0 && (uint32_t)lane < head + tail) {
+        const uint32_t e = (uint32_t)lane < head ? (uint32_t)lane : head + nv * L + ((uint32_t)lane - head);
+        float d = 0.0f;
+        if (!zeros) {
+            d = q.at(Ty::ld1(x + e));
+            if (e == q.target) d += q.at_target;
+        }
+        Ty::st1(dx + e, d);
+    }
+    uint4 raw[kU];
+    uint32_t v[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+        v[u] = tile * TV + u * 32 + lane;
+        raw[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (v[u] < nv && !zeros) raw[u] = ldv(x + head + (uint64_t)v[u] * L);
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+        if (v[u] >= nv) continue;
+        const uint32_t e0 = head + v[u] * L;
+        uint4 res = make_uint4(0u, 0u, 0u, 0u);
+        if (!zeros) {
+            float a[L];
+            Ty::unpack(raw[u], a);
+#pragma unroll
+            for (int l = 0; l < L; ++l) a[l] = q.at(a[l]);
+            if (q.target - e0 < (uint32_t)L) {
+#pragma unroll
+                for (int l = 0; l < L; ++l)
+                    if (e0 + l == q.target) a[l] += q.at_target;
+            }
+            res = Ty::pack(a);
+        }
+        stv(dx + e0, res);
+    }
+}
+
+template <class Ty, bool ENT, bool TOP>
+cudaError_t launch_logprob_as(const LogprobParams& p, bool warp, cudaStream_t s)
+{
+    if (warp)
+        return launch_pdl(logprob_kernel<Ty, 32, ENT, TOP>, dim3((unsigned)((p.M + kThreads / 32 - 1) / (kThreads / 32))), kThreads, 0, s, p);
+    if (p.split == 1) return launch_pdl(logprob_kernel<Ty, kThreads, ENT, TOP>, dim3(p.M), kThreads, 0, s, p);
+    cudaLaunchAttribute attr[2]{};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)p.split;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(p.M * (unsigned)p.split);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, logprob_kernel<Ty, kThreads, ENT, TOP>, p);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <class F>
+cudaError_t with_float(int dtype, F&& f)
+{
+    switch (dtype) {
+    case kF32: return f.template operator()<F32T>();
+    case kBF16: return f.template operator()<BF16T>();
+    case kF16: return f.template operator()<F16T>();
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+// A row of at most 8 KB goes to a warp; longer ones to a CTA, or to a cluster
+// of up to 8 while that leaves SMs without a CTA and each part 8 KB.
+int logprob_split(uint64_t M, uint64_t V, int dtype)
+{
+    const uint64_t bytes = V * (dtype == kF32 ? 4 : 2);
+    int split = 1;
+    while (split < kMaxSplit && M * (uint64_t)split * 2 <= 148 * 2 && bytes / (uint64_t)(2 * split) >= 8192) split *= 2;
+    return split;
+}
+
+cudaError_t launch_logprob(int dtype, const LogprobParams& p, cudaStream_t s)
+{
+    const uint64_t bytes = (uint64_t)p.V * (dtype == kF32 ? 4 : 2);
+    const bool warp = p.split == 1 && bytes <= 8192 && p.M > 8 * 148;
+    return with_float(dtype, [&]<class Ty>() -> cudaError_t {
+        if (p.entropy) return p.k ? launch_logprob_as<Ty, true, true>(p, warp, s) : launch_logprob_as<Ty, true, false>(p, warp, s);
+        return p.k ? launch_logprob_as<Ty, false, true>(p, warp, s) : launch_logprob_as<Ty, false, false>(p, warp, s);
+    });
+}
+
+cudaError_t launch_logprob_grad(int dtype, LogprobGradParams p, int* launches, cudaStream_t s)
+{
+    const uint32_t L = dtype == kF32 ? 4 : 8;
+    const uint32_t per = 32 * kU * L;
+    p.tiles = (uint32_t)(((uint64_t)p.V + per - 1) / per);
+    const uint64_t work = ((uint64_t)p.M * p.tiles + kThreads / 32 - 1) / (kThreads / 32);
+    for (uint64_t at = 0; at < work; at += kMaxGrid) {
+        p.first = at * (kThreads / 32);
+        const dim3 grid((unsigned)(work - at < kMaxGrid ? work - at : kMaxGrid));
+        const cudaError_t e = with_float(dtype, [&]<class Ty>() -> cudaError_t {
+            if (p.dentropy) return launch_pdl(logprob_grad_kernel<Ty, true>, grid, kThreads, 0, s, p);
+            return launch_pdl(logprob_grad_kernel<Ty, false>, grid, kThreads, 0, s, p);
+        });
+        if (e != cudaSuccess) return e;
+        *launches += 1;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace rr
