@@ -505,6 +505,74 @@ rr_status_t rr_token_logprobs_grad(const void* const* logits, size_t row_stride,
                                    float scale, const float* lse, const float* entropy, const float* dlogprob,
                                    const float* dentropy, void* const* dlogits, size_t grad_stride, cudaStream_t stream);
 
+/* --------------------------------------- orthogonalisation, Muon step -- */
+
+/* Matrices on one or more ranks: matrix t is rows[t] x cols[t], row-major
+ * without gaps, of type dtypes[t] (RR_F32, RR_BF16 or RR_F16; a list may mix
+ * them and shapes) on every rank; ptrs as in rr_tensor_list_t.  At most 2^20
+ * rows and columns; a matrix without elements is passed over. */
+typedef struct rr_matrix_list {
+    void* const* ptrs;
+    const size_t* rows;
+    const size_t* cols;
+    const rr_dtype_t* dtypes;
+    int32_t nmatrices;
+    int32_t nranks;
+} rr_matrix_list_t;
+
+/* The Newton-Schulz iteration: X = G / (||G||_F + eps), then `steps` times
+ * X = a X + (b A + c A^2) X with A = X X^T (for more rows than columns the same
+ * on X^T), which takes every singular value s of X to a s + b s^3 + c s^5.  Five
+ * steps of (3.4445, -4.7750, 2.0315) take all that are not tiny to 0.7 .. 1.2:
+ * the matrix is nearly orthogonal.  steps 0..64; eps finite and above 0; a
+ * singular value must not be able to pass 1024 on the way (RR_ERR_UNSUPPORTED). */
+typedef struct rr_newton_schulz {
+    int32_t steps;
+    float a, b, c;
+    float eps;
+} rr_newton_schulz_t;
+
+/* The bytes of device workspace the calls below need for a list (host only):
+ * 256-byte aligned, contents neither used nor kept, one call at a time (see
+ * rr_clip_workspace).  Matrices run in groups of up to 24 and 2 GiB of it. */
+rr_status_t rr_muon_workspace(const rr_matrix_list_t* matrices, const rr_newton_schulz_t* ns, size_t* bytes);
+
+/* Orthogonalises every matrix of `matrices` (its rank 0) into every rank's
+ * matrix of `results` (the same shapes, any of the types), which may be the
+ * matrix itself where the types agree; other buffers must not overlap.  The
+ * products run on the tensor cores with operands of 22 bits and fp32 sums; the
+ * result is rounded once to its type.  Of fp32 matrices it is as near to the
+ * exact polynomial as the same steps in fp32 are.  A matrix of zeros stays
+ * zero; one with a NaN or an infinity gives NaN.  The same call gives the same
+ * bits. */
+rr_status_t rr_orthogonalize(const rr_matrix_list_t* matrices, const rr_matrix_list_t* results, const rr_newton_schulz_t* ns,
+                             void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* How a Muon step's length goes by a matrix's shape: sqrt(max(1, rows / cols)),
+ * or 0.2 sqrt(max(rows, cols)) (an update about as large as AdamW's). */
+typedef enum rr_muon_adjust { RR_MUON_SPECTRAL = 0, RR_MUON_RMS = 1 } rr_muon_adjust_t;
+
+typedef struct rr_muon {
+    float lr, momentum, weight_decay;
+    int32_t nesterov;
+    int32_t adjust; /* rr_muon_adjust_t */
+    rr_newton_schulz_t ns;
+} rr_muon_t;
+
+/* The Muon step on synced gradients, for every replica of the weights:
+ *     M = momentum * M + G
+ *     U = G + momentum * M (nesterov) or M
+ *     W_r = round((1 - lr * weight_decay) * W_0 - lr * f * O)   on every rank r
+ * with O = U orthogonalised (rr_orthogonalize, the momentum in fp32, not
+ * rounded on the way) and f the shape's factor.  params: nranks replicas, of
+ * which rank 0's is read and all are written; grads: rank 0's are read;
+ * momenta: one rank, fp32, kept by the caller from step to step (zeros at
+ * first).  All three list the same shapes; types may differ from list to list.
+ * momentum finite and 0 or more.  Buffers must not overlap.  What is no matrix
+ * (biases, norms, usually the embedding) takes another optimiser. */
+rr_status_t rr_muon_step(const rr_matrix_list_t* params, const rr_matrix_list_t* grads, const rr_matrix_list_t* momenta,
+                         const rr_muon_t* config, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
 /* ------------------------------------------------ overlapped bucket sync -- */
 
 /* Opaque reducer (host memory and CUDA events owned by the library). */

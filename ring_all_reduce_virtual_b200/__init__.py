@@ -18,12 +18,14 @@ import contextlib
 import ctypes
 from typing import Any, NamedTuple, Sequence
 
-from ._lib import MAX_RANKS, Cost, RingEvent, RRError, Stats, TensorList, check, lib
+from ._lib import (MAX_RANKS, Cost, MatrixListC, Muon, NewtonSchulz, RingEvent, RRError, Stats, TensorList, check,
+                   lib)
 
 __all__ = [
     "all_reduce", "all_reduce_wire", "all_reduce_host", "all_reduce_host_noalloc", "ring_step", "ring_schedule", "reduce_scatter", "all_gather", "all_to_all",
     "RankSet", "BucketPlan", "GradSet", "Reducer", "GradList", "grad_norm", "clip_grads",
-    "embedding", "embedding_grad", "TokenLogprobs", "token_logprobs", "token_logprobs_grad", "cost_model", "pick_algo", "set_picker_params", "last_stats",
+    "embedding", "embedding_grad", "TokenLogprobs", "token_logprobs", "token_logprobs_grad", "MatrixList",
+    "orthogonalize", "muon_step", "cost_model", "pick_algo", "set_picker_params", "last_stats",
     "check_timeouts", "RRError",
     "OPS", "ALGOS", "MAX_RANKS",
 ]
@@ -622,6 +624,121 @@ def token_logprobs_grad(logits, tokens, lse, dlogprob, entropy=None, dentropy=No
         if st:
             check(st, "token_logprobs_grad")
     return outs
+
+
+class MatrixList:
+    """Matrices checked and with their pointers and shapes marshalled once: a
+    list of 2-D tensors (one rank), or one list per rank (``m[r][t]``) whose
+    ranks hold the same shapes and types.  Contiguous float32, bfloat16 or
+    float16 CUDA tensors on one device, mixed as they come.  ``orthogonalize``
+    and ``muon_step`` accept this or the lists; it keeps the tensors alive and
+    stays valid while they keep their storage."""
+
+    def __init__(self, matrices):
+        matrices = list(matrices)
+        if matrices and hasattr(matrices[0], "data_ptr"):
+            matrices = [matrices]
+        ranks = [list(rank) for rank in matrices] or [[]]
+        if len(ranks) > MAX_RANKS:
+            raise ValueError(f"MatrixList: need 1..{MAX_RANKS} ranks, got {len(ranks)}")
+        flat = [m for rank in ranks for m in rank]
+        for rank in ranks:
+            if len(rank) != len(ranks[0]):
+                raise ValueError("MatrixList: every rank needs the same number of matrices")
+            for m, m0 in zip(rank, ranks[0]):
+                if not m.is_cuda or not m.is_contiguous() or m.dim() != 2 or m.device != flat[0].device:
+                    raise ValueError("MatrixList: matrices must be contiguous 2-D CUDA tensors on one device")
+                if m.shape != m0.shape or m.dtype != m0.dtype:
+                    raise ValueError("MatrixList: a matrix has different shapes or dtypes on different ranks")
+        codes = [_dtype_code(m.dtype) for m in ranks[0]]
+        if _DTYPE_NAMES["i32"] in codes:
+            raise TypeError("MatrixList: matrices must be float32, bfloat16 or float16")
+        n = len(ranks[0])
+        self.nranks, self.shapes, self.dtypes = len(ranks), [tuple(m.shape) for m in ranks[0]], codes
+        self.device = flat[0].device if flat else None
+        self._keep = ranks  # the tensors must outlive the pointers
+        self._arrays = (_ptr_array(flat), (ctypes.c_size_t * max(n, 1))(*[s[0] for s in self.shapes]),
+                        (ctypes.c_size_t * max(n, 1))(*[s[1] for s in self.shapes]), (ctypes.c_int * max(n, 1))(*codes))
+        self._c = MatrixListC(*[ctypes.cast(a, t) for a, (_, t) in zip(self._arrays, MatrixListC._fields_)], n, self.nranks)
+        self._ref = ctypes.byref(self._c)
+        self._bytes = {}  # workspace bytes by number of steps > 0 or not
+
+    @classmethod
+    def _of(cls, matrices) -> "MatrixList":
+        return matrices if isinstance(matrices, MatrixList) else cls(matrices)
+
+    def _workspace(self, ns) -> int:
+        key = ns.steps > 0
+        need = self._bytes.get(key)
+        if need is None:
+            b = ctypes.c_size_t()
+            check(lib().rr_muon_workspace(self._ref, ctypes.byref(ns), ctypes.byref(b)), "muon_workspace")
+            need = self._bytes[key] = b.value
+        return need
+
+
+NEWTON_SCHULZ = (3.4445, -4.7750, 2.0315)
+MUON_ADJUST = {"spectral": 0, "rms": 1}
+
+
+def _newton_schulz(steps, coefficients, eps) -> NewtonSchulz:
+    a, b, c = coefficients
+    return NewtonSchulz(int(steps), float(a), float(b), float(c), float(eps))
+
+
+def _with_workspace(what: str, fn, args: tuple, device, need: int, stream) -> None:
+    """Run ``fn(*args, workspace pointer, bytes, stream)`` on ``device``."""
+    torch, raw, current = _calls()
+    with contextlib.nullcontext() if stream is None and device.index == current() else _placed(stream, device):
+        mem = torch.empty_strided((need,), (1,), dtype=torch.uint8, device=device)
+        st = fn(*args, mem.data_ptr(), need, raw(device.index))
+        if st:
+            check(st, what)
+
+
+def orthogonalize(matrices, outs=None, steps: int = 5, coefficients=NEWTON_SCHULZ, eps: float = 1e-7, stream=None):
+    """Every matrix nearly orthogonal, by ``steps`` Newton-Schulz products
+    (``rr_orthogonalize``): its singular values s go to a s + b s^3 + c s^5 a
+    step, from s / (the Frobenius norm + eps).  ``matrices``: a list of 2-D
+    tensors or a ``MatrixList``; ``outs``: the same shapes (any float type,
+    one list per rank where every rank is to have the results; the matrices
+    themselves, say), or None for new tensors.  Returns ``outs``."""
+    src = MatrixList._of(matrices)
+    ns = _newton_schulz(steps, coefficients, eps)
+    if outs is None:
+        if src.device is None:
+            return []
+        with contextlib.nullcontext() if stream is None else _placed(stream, src.device):
+            outs = [m.new_empty(m.shape) for m in src._keep[0]]
+    dst = MatrixList._of(outs)
+    if dst.shapes != src.shapes or dst.device != src.device:
+        raise ValueError("orthogonalize: need one result per matrix, of its shape and on its device")
+    if src.device is not None:
+        _with_workspace("orthogonalize", lib().rr_orthogonalize, (src._ref, dst._ref, ctypes.byref(ns)), src.device,
+                        src._workspace(ns), stream)
+    return outs
+
+
+def muon_step(params, grads, momenta, lr: float, momentum: float = 0.95, nesterov: bool = True, weight_decay: float = 0.0,
+              adjust="spectral", steps: int = 5, coefficients=NEWTON_SCHULZ, eps: float = 1e-7, stream=None) -> None:
+    """The Muon step on synced gradients, for every replica (``rr_muon_step``):
+    ``M = momentum M + G``; the update is ``G + momentum M`` (``nesterov``) or
+    ``M``, orthogonalised; ``W = (1 - lr weight_decay) W - lr f O`` from rank
+    0's weights into every rank's.  ``f`` is sqrt(max(1, rows / columns))
+    (``adjust="spectral"``) or 0.2 sqrt(max(rows, columns)) (``"rms"``).
+    ``params``: 2-D tensors (one list, or one per rank); ``grads``: alike in
+    shape, rank 0's are read; ``momenta``: float32, kept once.  Lists or
+    ``MatrixList``s."""
+    w, g, m = MatrixList._of(params), MatrixList._of(grads), MatrixList._of(momenta)
+    if g.shapes != w.shapes or m.shapes != w.shapes or g.device != w.device or m.device != w.device:
+        raise ValueError("muon_step: weights, gradients and momenta must agree in shapes and device")
+    if w.device is None:
+        return
+    ns = _newton_schulz(steps, coefficients, eps)
+    cfg = Muon(float(lr), float(momentum), float(weight_decay), 1 if nesterov else 0,
+               MUON_ADJUST[adjust] if isinstance(adjust, str) else int(adjust), ns)
+    _with_workspace("muon_step", lib().rr_muon_step, (w._ref, g._ref, m._ref, ctypes.byref(cfg)), w.device,
+                    w._workspace(ns), stream)
 
 
 class BucketPlan:

@@ -53,6 +53,28 @@ class TensorList(ctypes.Structure):
     ]
 
 
+class MatrixListC(ctypes.Structure):
+    _fields_ = [
+        ("ptrs", ctypes.POINTER(ctypes.c_void_p)), ("rows", ctypes.POINTER(ctypes.c_size_t)),
+        ("cols", ctypes.POINTER(ctypes.c_size_t)), ("dtypes", ctypes.POINTER(ctypes.c_int)),
+        ("nmatrices", ctypes.c_int32), ("nranks", ctypes.c_int32),
+    ]
+
+
+class NewtonSchulz(ctypes.Structure):
+    _fields_ = [
+        ("steps", ctypes.c_int32), ("a", ctypes.c_float), ("b", ctypes.c_float), ("c", ctypes.c_float),
+        ("eps", ctypes.c_float),
+    ]
+
+
+class Muon(ctypes.Structure):
+    _fields_ = [
+        ("lr", ctypes.c_float), ("momentum", ctypes.c_float), ("weight_decay", ctypes.c_float),
+        ("nesterov", ctypes.c_int32), ("adjust", ctypes.c_int32), ("ns", NewtonSchulz),
+    ]
+
+
 _lock = threading.Lock()
 _lib: ctypes.CDLL | None = None
 
@@ -62,6 +84,7 @@ def _declare(lib: ctypes.CDLL) -> None:
     i, sz, d = ctypes.c_int, ctypes.c_size_t, ctypes.c_double
     st = ctypes.c_int
     f, TL = ctypes.c_float, ctypes.POINTER(TensorList)
+    ML, NS = ctypes.POINTER(MatrixListC), ctypes.POINTER(NewtonSchulz)
     sig = {
         "rr_allreduce": (st, [PP, i, sz, i, i, i, P]),
         "rr_allreduce_host": (st, [PP, PP, i, sz, i, i, i, P]),
@@ -90,6 +113,9 @@ def _declare(lib: ctypes.CDLL) -> None:
         "rr_embedding_grad": (st, [PP, i, PP, i, sz, sz, sz, i, i, f, ctypes.c_int64, PP, i, i, i, P, sz, P]),
         "rr_token_logprobs": (st, [PP, sz, PP, i, i, sz, sz, i, f, P, P, P, i, P, P, P]),
         "rr_token_logprobs_grad": (st, [PP, sz, PP, i, i, sz, sz, i, f, P, P, P, P, PP, sz, P]),
+        "rr_muon_workspace": (st, [ML, NS, ctypes.POINTER(sz)]),
+        "rr_orthogonalize": (st, [ML, ML, NS, P, sz, P]),
+        "rr_muon_step": (st, [ML, ML, ML, ctypes.POINTER(Muon), P, sz, P]),
         "rr_reducer_create": (st, [P, PP, i, i, P, i, ctypes.POINTER(P)]),
         "rr_reducer_ready": (st, [P, i, P]),
         "rr_reducer_finish": (st, [P, P]),
