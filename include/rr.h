@@ -532,17 +532,21 @@ typedef struct rr_newton_schulz {
     float eps;
 } rr_newton_schulz_t;
 
-/* The bytes of device workspace the calls below need for a list (host only):
+/* The bytes of device workspace the calls below need (host only) for their
+ * list of results (weights 0: rr_orthogonalize) or weights (1: rr_muon_step):
  * 256-byte aligned, contents neither used nor kept, one call at a time (see
  * rr_clip_workspace).  Matrices run in groups of up to 24 and 2 GiB of it. */
-rr_status_t rr_muon_workspace(const rr_matrix_list_t* matrices, const rr_newton_schulz_t* ns, size_t* bytes);
+rr_status_t rr_muon_workspace(const rr_matrix_list_t* results, int weights, const rr_newton_schulz_t* ns, size_t* bytes);
 
 /* Orthogonalises every matrix of `matrices` (its rank 0) into every rank's
  * matrix of `results` (the same shapes, any of the types), which may be the
  * matrix itself where the types agree; other buffers must not overlap.  The
  * products run on the tensor cores with operands of 22 bits and fp32 sums; the
- * result is rounded once to its type.  Of fp32 matrices it is as near to the
- * exact polynomial as the same steps in fp32 are.  A matrix of zeros stays
+ * result is rounded once to its type.  fp32 results are as near to the exact
+ * polynomial as the same steps in fp32 are (about 1e-6 to 1e-5 of the matrix's
+ * norm); for bf16 and fp16 results of matrices that are not square several
+ * steps share one A, whose roundings then count up to 4e-4 and 2e-5 of it (the
+ * types' own: 1.7e-3 and 2e-4).  A matrix of zeros stays
  * zero; one with a NaN or an infinity gives NaN.  The same call gives the same
  * bits. */
 rr_status_t rr_orthogonalize(const rr_matrix_list_t* matrices, const rr_matrix_list_t* results, const rr_newton_schulz_t* ns,
@@ -563,8 +567,8 @@ typedef struct rr_muon {
  *     M = momentum * M + G
  *     U = G + momentum * M (nesterov) or M
  *     W_r = round((1 - lr * weight_decay) * W_0 - lr * f * O)   on every rank r
- * with O = U orthogonalised (rr_orthogonalize, the momentum in fp32, not
- * rounded on the way) and f the shape's factor.  params: nranks replicas, of
+ * with O = U orthogonalised (rr_orthogonalize; U in fp32, O not rounded on the
+ * way, for fp32 weights as for fp16 results) and f the shape's factor.  params: nranks replicas, of
  * which rank 0's is read and all are written; grads: rank 0's are read;
  * momenta: one rank, fp32, kept by the caller from step to step (zeros at
  * first).  All three list the same shapes; types may differ from list to list.

@@ -661,18 +661,19 @@ class MatrixList:
                         (ctypes.c_size_t * max(n, 1))(*[s[1] for s in self.shapes]), (ctypes.c_int * max(n, 1))(*codes))
         self._c = MatrixListC(*[ctypes.cast(a, t) for a, (_, t) in zip(self._arrays, MatrixListC._fields_)], n, self.nranks)
         self._ref = ctypes.byref(self._c)
-        self._bytes = {}  # workspace bytes by number of steps > 0 or not
+        self._bytes = {}  # workspace bytes of calls that write this list, by iteration
 
     @classmethod
     def _of(cls, matrices) -> "MatrixList":
         return matrices if isinstance(matrices, MatrixList) else cls(matrices)
 
-    def _workspace(self, ns) -> int:
-        key = ns.steps > 0
+    def _workspace(self, weights: bool, ns) -> int:
+        """Bytes of device workspace that a call whose results (or weights) these are needs."""
+        key = (weights, ns.steps, ns.a, ns.b, ns.c)
         need = self._bytes.get(key)
         if need is None:
             b = ctypes.c_size_t()
-            check(lib().rr_muon_workspace(self._ref, ctypes.byref(ns), ctypes.byref(b)), "muon_workspace")
+            check(lib().rr_muon_workspace(self._ref, 1 if weights else 0, ctypes.byref(ns), ctypes.byref(b)), "muon_workspace")
             need = self._bytes[key] = b.value
         return need
 
@@ -715,7 +716,7 @@ def orthogonalize(matrices, outs=None, steps: int = 5, coefficients=NEWTON_SCHUL
         raise ValueError("orthogonalize: need one result per matrix, of its shape and on its device")
     if src.device is not None:
         _with_workspace("orthogonalize", lib().rr_orthogonalize, (src._ref, dst._ref, ctypes.byref(ns)), src.device,
-                        src._workspace(ns), stream)
+                        dst._workspace(False, ns), stream)
     return outs
 
 
@@ -738,7 +739,7 @@ def muon_step(params, grads, momenta, lr: float, momentum: float = 0.95, nestero
     cfg = Muon(float(lr), float(momentum), float(weight_decay), 1 if nesterov else 0,
                MUON_ADJUST[adjust] if isinstance(adjust, str) else int(adjust), ns)
     _with_workspace("muon_step", lib().rr_muon_step, (w._ref, g._ref, m._ref, ctypes.byref(cfg)), w.device,
-                    w._workspace(ns), stream)
+                    w._workspace(True, ns), stream)
 
 
 class BucketPlan:

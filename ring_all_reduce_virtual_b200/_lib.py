@@ -113,7 +113,7 @@ def _declare(lib: ctypes.CDLL) -> None:
         "rr_embedding_grad": (st, [PP, i, PP, i, sz, sz, sz, i, i, f, ctypes.c_int64, PP, i, i, i, P, sz, P]),
         "rr_token_logprobs": (st, [PP, sz, PP, i, i, sz, sz, i, f, P, P, P, i, P, P, P]),
         "rr_token_logprobs_grad": (st, [PP, sz, PP, i, i, sz, sz, i, f, P, P, P, P, PP, sz, P]),
-        "rr_muon_workspace": (st, [ML, NS, ctypes.POINTER(sz)]),
+        "rr_muon_workspace": (st, [ML, i, NS, ctypes.POINTER(sz)]),
         "rr_orthogonalize": (st, [ML, ML, NS, P, sz, P]),
         "rr_muon_step": (st, [ML, ML, ML, ctypes.POINTER(Muon), P, sz, P]),
         "rr_reducer_create": (st, [P, PP, i, i, P, i, ctypes.POINTER(P)]),

@@ -46,25 +46,29 @@ struct Halves {
     uint16_t* lo;
 };
 
-// One product of a launch: out = alpha * op(a) op(b)^T + beta * c, on tiles of
-// 128 rows and `tile_n` columns.
+// One product of a launch: out = alpha * op(a) op(b)^T + beta * c + diag * 1,
+// on tiles of 256 rows and `tile_n` columns.  A symmetric matrix is formed and
+// kept on and below the diagonal of its 256 x 256 tiles; an operand's block
+// above it is read as the transpose of the one below.
 struct MuonProduct {
     Halves a, b, c, out;   // c.hi NULL: none
     uint32_t a_nbj, b_nbj, o_nbj;  // columns of blocks: operands, out (and c)
-    uint32_t mt, nu, kb;   // tiles of 128 rows, units of 128 columns, blocks along K
+    uint32_t mt, nu, kb;   // units of 128 rows, of 128 columns, blocks along K
     uint32_t tile0;        // the launch's first tile of this product
     uint8_t a_mn, b_mn;    // the operand's rows run along K (not its columns)
-    uint8_t sym;           // the result is symmetric: tiles on and below the diagonal, mirrored
-    uint8_t pad_;
-    float alpha, beta;
+    uint8_t a_low, b_low;  // the operand is symmetric, kept on and below the diagonal
+    uint32_t side;         // diag goes to the first `side` elements of the diagonal
+    uint8_t sym, pad_[3];  // the result is symmetric
+    float alpha, beta, diag;
 };
 
-constexpr int kMuonMats = 24;   // matrices per launch: parameter blocks below 4 KB
+constexpr int kMuonMats = 24;     // matrices per launch: parameter blocks below 4 KB,
+constexpr int kMuonProducts = 30; // which larger ones cost the host 3-5 us more
 constexpr uint32_t kNormParts = 256;  // partial sums of squares per matrix, at most
 constexpr uint32_t kPrepTile = 8192;  // elements of a tile of the first pass
 
 struct MuonGemmParams {
-    MuonProduct q[kMuonMats];
+    MuonProduct q[kMuonProducts];
     int n;
     uint32_t tile_n;       // 128 or 256
     uint32_t tiles;
@@ -108,7 +112,7 @@ struct MuonFinishParams {
 cudaError_t launch_muon_squares(const MuonPrepParams& p, uint32_t parts, cudaStream_t s);
 cudaError_t launch_muon_pack(const MuonPrepParams& p, uint32_t tiles, cudaStream_t s);
 cudaError_t launch_muon_finish(const MuonFinishParams& p, uint32_t tiles, cudaStream_t s);
-// Fills in the tiles and the waits and launches; steps: the K steps of all tiles.
+// Fills in the tiles and the waits and launches.
 cudaError_t launch_muon_gemm(MuonGemmParams& p, cudaStream_t s);
 
 }  // namespace rr

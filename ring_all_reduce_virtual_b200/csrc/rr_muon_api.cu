@@ -65,16 +65,17 @@ rr_status_t add_spans(const rr_matrix_list_t* l, int ranks, bool out, std::vecto
     return RR_OK;
 }
 
-// The scales of the halves, a power of two for every step's X, A = X X^T and
-// B = b A + c A^2.  No element exceeds the largest singular value, which starts
-// at 1 at most (the Frobenius norm is 1) and is carried through the
-// polynomials' extrema; the scale puts that just below fp16's largest.
+// What the iteration's values are bounded by.  No element exceeds the largest
+// singular value, which starts at 1 at most (the Frobenius norm is 1) and is
+// carried through the polynomials' extrema.
 struct Plan {
     int steps;
     float a, b, c;
-    double x[kMaxSteps + 1], gram[kMaxSteps], poly[kMaxSteps];
+    double rho[kMaxSteps + 1];   // of X before step k
+    double poly[kMaxSteps];      // of D = a + b A + c A^2
 };
 
+// The halves' scale, a power of two: the bound comes just below fp16's largest.
 double scale_for(double bound)
 {
     if (!(bound > 0x1p-12)) bound = 0x1p-12;
@@ -97,18 +98,15 @@ rr_status_t make_plan(const rr_newton_schulz_t* ns, Plan* p)
     for (int k = 0; k <= ns->steps; ++k) {
         if (rho > 1024.0)
             return fail(RR_ERR_UNSUPPORTED, "with these coefficients a step can take a singular value above 1024");
-        p->x[k] = scale_for(rho);
+        p->rho[k] = rho;
         if (k == ns->steps) break;
+        // the extrema of |d(l)| and of |d(l)| sqrt(l), d = a + b l + c l^2, on 0 <= l <= rho^2
         const double top = rho * rho;
-        p->gram[k] = scale_for(top);
-        const auto poly = [&](double l) { return std::fabs(b * l + c * l * l); };
-        double most = poly(top);
-        if (c != 0.0 && -b / (2 * c) > 0.0 && -b / (2 * c) < top) most = std::max(most, poly(-b / (2 * c)));
-        p->poly[k] = scale_for(most);
-        // extrema of |a s + b s^3 + c s^5| on [0, rho]: a + 3 b l + 5 c l^2 = 0, l = s^2
-        const auto step = [&](double l) { return std::fabs(a + b * l + c * l * l) * std::sqrt(l); };
-        double next = step(top);
-        double roots[2] = {-1.0, -1.0};
+        const auto d = [&](double l) { return std::fabs(a + b * l + c * l * l); };
+        double most = std::max(d(0.0), d(top)), next = d(top) * rho;
+        const double vertex = c != 0.0 ? -b / (2 * c) : -1.0;
+        if (vertex > 0.0 && vertex < top) most = std::max(most, d(vertex));
+        double roots[2] = {-1.0, -1.0};  // of a + 3 b l + 5 c l^2
         if (c != 0.0) {
             const double disc = 9 * b * b - 20 * a * c;
             if (disc >= 0.0) {
@@ -119,38 +117,76 @@ rr_status_t make_plan(const rr_newton_schulz_t* ns, Plan* p)
             roots[0] = -a / (3 * b);
         }
         for (double l : roots)
-            if (l > 0.0 && l < top) next = std::max(next, step(l));
+            if (l > 0.0 && l < top) next = std::max(next, d(l) * std::sqrt(l));
+        p->poly[k] = most * (1.0 + 0x1p-10);
         rho = next * (1.0 + 0x1p-10);
     }
     return RR_OK;
 }
 
-uint64_t up256(uint64_t x) { return (x + 255) / 256 * 256; }
+// The steps of a matrix run in segments.  A segment of s steps forms A = X X^T
+// once and carries on in the smaller side's m x m space,
+//     D = a + b A + c A^2    Q <- D Q    A <- D (D A)
+// and ends with X <- Q X; with n = r m the longer side its products cost
+// 1.5 r + 2 s - 1.5 times 2 m^3 operations (symmetric ones count half), the
+// whole 1.5 (r - 1) a segment and 2 a step: the fewer segments the better, the
+// more so the longer the matrix, and none for a square one.  But D (D A)
+// multiplies what A was rounded by, up to a^2 a step, where its eigenvalues are
+// small.  Measured error of five steps against 64 bits, segments of 5 / 3 + 2 /
+// 1 each, from noise to few directions in little noise (rank 1/16 of the side):
+// 2e-6..4e-4 / 2e-6..2e-5 / 1e-6..2e-5 (fp32's own: the last).  So a result of
+// fp32 has a segment per step; bf16's, which are rounded by 1.7e-3, have A's
+// errors grow by 3e4 at most (5 steps of the usual coefficients); fp16's (2e-4)
+// and fp32 weights, of which the result is a small part, by 200 (3 steps).
+enum Exactness { kExact = 0, kClose = 1, kCoarse = 2 };
 
-// One matrix's part of the workspace: X twice (a product reads one and writes
-// the other), A and B, two halves each.
+std::vector<int> segments_of(const Plan& plan, uint32_t m, uint32_t n, Exactness exact)
+{
+    const double limit = exact == kExact ? 0.0 : exact == kClose ? 200.0 : 3e4;
+    const double grow = std::max(1.0, (double)plan.a * plan.a);
+    int most = 1;
+    for (double g = grow; g <= limit && most < plan.steps; g *= grow) ++most;
+    // nearly square matrices would gain less than a twentieth
+    if (1.5 * ((double)n / m - 1.0) * (plan.steps - 1) < 0.05 * 2.0 * plan.steps) most = 1;
+    std::vector<int> parts;
+    for (int left = plan.steps; left > 0; left -= most) parts.push_back(std::min(most, left));
+    return parts;
+}
+
+// One matrix's part of the workspace: X twice (a segment reads one and writes
+// the other) and up to five m x m matrices, two halves each.
 struct Room {
-    uint64_t x[2], gram, poly;  // bytes of one half
-    uint64_t bytes() const { return 2 * (x[0] + x[1] + gram + poly); }
+    uint64_t x, square;  // bytes of one half
+    int xs, squares;
+    uint64_t bytes() const { return 2 * (x * xs + square * squares); }
 };
 
-Room room_of(const Shape& s, int steps)
+Room room_of(const Shape& s, const std::vector<int>& segments)
 {
-    Room r{};
-    r.x[0] = (uint64_t)pad_up(s.rows) * pad_up(s.cols) * 2;
-    if (steps > 0) {
-        r.x[1] = r.x[0];
-        r.gram = r.poly = (uint64_t)pad_up(s.small()) * pad_up(s.small()) * 2;
-    }
-    return r;
+    const int most = segments.empty() ? 0 : *std::max_element(segments.begin(), segments.end());
+    return {(uint64_t)pad_up(s.rows) * pad_up(s.cols) * 2, (uint64_t)pad_up(s.small()) * pad_up(s.small()) * 2,
+            most > 0 ? 2 : 1, most > 1 ? 5 : most > 0 ? 2 : 0};
 }
 
 uint32_t parts_of(const Shape& s) { return (uint32_t)std::min<uint64_t>(kNormParts, ceil_div(s.numel(), kPrepTile)); }
 
 constexpr uint64_t kPartialBytes = (uint64_t)kMuonMats * kNormParts * sizeof(double);
 
+// How exactly a list's matrix t has to come out.
+Exactness exactness(const rr_matrix_list_t* out, int t, bool weights)
+{
+    if (out->dtypes[t] == RR_BF16) return kCoarse;
+    return out->dtypes[t] == RR_F16 || weights ? kClose : kExact;
+}
+
+std::vector<int> segments_for(const Plan& plan, const rr_matrix_list_t* out, int t, bool weights)
+{
+    const uint32_t r = (uint32_t)out->rows[t], c = (uint32_t)out->cols[t];
+    return segments_of(plan, std::min(r, c), std::max(r, c), exactness(out, t, weights));
+}
+
 // The groups of a list's matrices (those with elements), in order.
-std::vector<std::vector<int>> groups_of(const rr_matrix_list_t* l, int steps, uint64_t* bytes)
+std::vector<std::vector<int>> groups_of(const rr_matrix_list_t* l, const Plan& plan, bool weights, uint64_t* bytes)
 {
     std::vector<std::vector<int>> groups;
     uint64_t used = 0;
@@ -158,7 +194,7 @@ std::vector<std::vector<int>> groups_of(const rr_matrix_list_t* l, int steps, ui
     for (int t = 0; t < l->nmatrices; ++t) {
         const Shape s{(uint32_t)l->rows[t], (uint32_t)l->cols[t]};
         if (s.numel() == 0) continue;
-        const uint64_t need = room_of(s, steps).bytes();
+        const uint64_t need = room_of(s, segments_for(plan, l, t, weights)).bytes();
         if (groups.empty() || groups.back().size() == kMuonMats || used + need > kGroupBytes) {
             groups.emplace_back();
             used = kPartialBytes;
@@ -187,14 +223,120 @@ float shape_factor(const Shape& s, int adjust)
 
 bool on16(const void* p) { return (uintptr_t)p % 16 == 0; }
 
+// The products of one matrix, level by level: what a level reads was written in
+// an earlier one.  x[0] holds the first X; *last is the result's buffer.
+void products_of(const Plan& plan, const Shape& s, const std::vector<int>& segments, const Halves (&x)[2],
+                 const Halves (&sq)[5], std::vector<std::vector<MuonProduct>>& levels, int* last)
+{
+    const bool wide = s.rows <= s.cols;
+    const uint32_t m = s.small(), n = std::max(s.rows, s.cols);
+    const uint32_t xb = pad_up(s.cols) / kBlk, mb = pad_up(m) / kBlk, mu = pad_up(m) / 128;
+    size_t level = 0;
+    const auto add = [&](size_t at, const MuonProduct& q) {
+        if (levels.size() <= at) levels.resize(at + 1);
+        levels[at].push_back(q);
+    };
+    // a product of two symmetric m x m matrices that commute
+    const auto square = [&](const Halves& a, const Halves& b, const Halves& out, double alpha) {
+        MuonProduct q{};
+        q.a = a;
+        q.b = b;
+        q.out = out;
+        q.a_nbj = q.b_nbj = q.o_nbj = mb;
+        q.a_low = q.b_low = q.sym = 1;
+        q.mt = q.nu = mu;
+        q.kb = (uint32_t)ceil_div(m, kBlk);
+        q.alpha = (float)alpha;
+        return q;
+    };
+    const Halves A = sq[0], Y = sq[1], D = sq[2];
+    int cur = 0, step = 0;
+    for (int len : segments) {
+        const double sx = scale_for(plan.rho[step]);
+        double top = plan.rho[step] * plan.rho[step], sa = scale_for(top);
+        MuonProduct g{};  // A = X X^T, or X^T X
+        g.a = g.b = x[cur];
+        g.out = A;
+        g.a_nbj = g.b_nbj = xb;
+        g.o_nbj = mb;
+        g.a_mn = g.b_mn = !wide;
+        g.sym = 1;
+        g.mt = g.nu = mu;
+        g.kb = (uint32_t)ceil_div(n, kBlk);
+        g.alpha = (float)(sa / (sx * sx));
+        add(level++, g);
+        // A segment of one step keeps a X out of the products, X <- a X + (D - a) X:
+        // as a term of the tensor cores' sums it would be cut off with them
+        // (a step's error 4e-7 instead of 8e-8).
+        const bool alone = len == 1;
+        Halves Q = alone ? sq[1] : sq[3], Q2 = sq[4];
+        double bound = 1.0, sq_scale = 1.0;  // of Q
+        for (int k = 0; k < len; ++k) {
+            const double most = plan.poly[step + k] + (alone ? std::fabs(plan.a) : 0.0), sd = scale_for(most);
+            const Halves d = k == 0 ? Q : D;
+            MuonProduct q = square(A, A, d, plan.c * sd / (sa * sa));
+            q.c = A;
+            q.beta = (float)(plan.b * sd / sa);
+            if (!alone) {
+                q.diag = (float)(plan.a * sd);
+                q.side = m;
+            }
+            add(level++, q);
+            if (k == 0) {
+                bound = most;
+                sq_scale = sd;
+            }
+            size_t end = level;
+            if (k + 1 < len) {  // A <- D (D A)
+                const double sy = scale_for(most * top);
+                add(level, square(d, A, Y, sy / (sd * sa)));
+                top = plan.rho[step + k + 1] * plan.rho[step + k + 1];
+                sa = scale_for(top);
+                add(level + 1, square(d, Y, A, sa / (sd * sy)));
+                end = level + 2;
+            }
+            if (k > 0) {
+                bound *= most;
+                const double to = scale_for(bound);
+                add(level, square(d, Q, Q2, to / (sd * sq_scale)));
+                sq_scale = to;
+                std::swap(Q, Q2);
+                end = std::max(end, level + 1);
+            }
+            level = end;
+        }
+        step += len;
+        MuonProduct q{};  // X = Q X, or X Q
+        q.a = wide ? Q : x[cur];
+        q.b = wide ? x[cur] : Q;
+        q.out = x[cur ^ 1];
+        q.a_nbj = wide ? mb : xb;
+        q.b_nbj = wide ? xb : mb;
+        q.o_nbj = xb;
+        q.a_low = wide;
+        q.b_low = !wide;
+        q.b_mn = wide;
+        q.mt = pad_up(s.rows) / 128;
+        q.nu = pad_up(s.cols) / 128;
+        q.kb = (uint32_t)ceil_div(m, kBlk);
+        const double to = scale_for(plan.rho[step]);
+        q.alpha = (float)(to / (sq_scale * sx));
+        if (alone) {
+            q.c = x[cur];
+            q.beta = (float)(plan.a * to / sx);
+        }
+        add(level++, q);
+        cur ^= 1;
+    }
+    *last = cur;
+}
+
 rr_status_t run_group(const Job& job, const Plan& plan, const std::vector<int>& group, char* ws, cudaStream_t stream)
 {
     const int n = (int)group.size();
     std::unique_ptr<MuonPrepParams> prep(new MuonPrepParams{});
-    std::unique_ptr<MuonGemmParams> gemm(new MuonGemmParams{});
-    std::vector<Halves> x[2], gram(n), poly(n);
-    x[0].resize(n);
-    x[1].resize(n);
+    std::vector<std::vector<MuonProduct>> levels;
+    std::vector<Halves> result(n);
     uint64_t at = kPartialBytes;
     const auto take = [&](uint64_t half) {
         Halves h;
@@ -208,17 +350,20 @@ rr_status_t run_group(const Job& job, const Plan& plan, const std::vector<int>& 
     prep->momentum = job.momentum;
     prep->nesterov = job.nesterov;
     prep->eps = job.eps;
-    prep->scale = (float)plan.x[0];
+    prep->scale = (float)scale_for(plan.rho[0]);
     uint32_t parts = 0, tiles = 0;
     std::vector<Shape> shape(n);
     for (int k = 0; k < n; ++k) {
         const int t = group[k];
         const Shape s = shape[k] = {(uint32_t)job.in->rows[t], (uint32_t)job.in->cols[t]};
-        const Room room = room_of(s, plan.steps);
-        x[0][k] = take(room.x[0]);
-        x[1][k] = plan.steps > 0 ? take(room.x[1]) : x[0][k];
-        gram[k] = take(room.gram);
-        poly[k] = take(room.poly);
+        const std::vector<int> segments = segments_for(plan, job.out, t, job.mom != nullptr);
+        const Room room = room_of(s, segments);
+        Halves x[2], sq[5]{};
+        for (int i = 0; i < room.xs; ++i) x[i] = take(room.x);
+        for (int i = 0; i < room.squares; ++i) sq[i] = take(room.square);
+        int last = 0;
+        products_of(plan, s, segments, x, sq, levels, &last);
+        result[k] = x[last];
         MuonMat& m = prep->mat[k];
         m.g = job.in->ptrs[t];
         m.m = job.mom ? static_cast<float*>(job.mom->ptrs[t]) : nullptr;
@@ -226,7 +371,7 @@ rr_status_t run_group(const Job& job, const Plan& plan, const std::vector<int>& 
         m.cols = s.cols;
         m.part0 = parts;
         m.parts = parts_of(s);
-        m.x = x[0][k];
+        m.x = x[0];
         m.tile0 = tiles;
         m.dtype = (uint8_t)job.in->dtypes[t];
         m.vec = s.cols % 8 == 0 && on16(m.g) && (!m.m || on16(m.m));
@@ -239,53 +384,13 @@ rr_status_t run_group(const Job& job, const Plan& plan, const std::vector<int>& 
     if (e != cudaSuccess) return cuda_fail(e, "Muon pack launch");
     t_stats.launches += 2;
 
-    gemm->n = n;
-    for (int step = 0; step < plan.steps; ++step) {
-        const std::vector<Halves>& from = x[step & 1];
-        const std::vector<Halves>& to = x[(step + 1) & 1];
-        const double sx = plan.x[step], sg = plan.gram[step], sp = plan.poly[step];
-        for (int product = 0; product < 3; ++product) {
-            for (int k = 0; k < n; ++k) {
-                const Shape& s = shape[k];
-                const bool wide = s.rows <= s.cols;
-                const uint32_t xb = pad_up(s.cols) / kBlk, mb = pad_up(s.small()) / kBlk;
-                MuonProduct q{};
-                if (product == 0) {  // A = X X^T, or X^T X
-                    q.a = q.b = from[k];
-                    q.out = gram[k];
-                    q.a_nbj = q.b_nbj = xb;
-                    q.o_nbj = mb;
-                    q.a_mn = q.b_mn = !wide;
-                    q.mt = q.nu = pad_up(s.small()) / 128;
-                    q.kb = (uint32_t)ceil_div(std::max(s.rows, s.cols), kBlk);
-                    q.sym = 1;
-                    q.alpha = (float)(sg / (sx * sx));
-                } else if (product == 1) {  // B = b A + c A A
-                    q.a = q.b = q.c = gram[k];
-                    q.out = poly[k];
-                    q.a_nbj = q.b_nbj = q.o_nbj = mb;
-                    q.mt = q.nu = pad_up(s.small()) / 128;
-                    q.kb = (uint32_t)ceil_div(s.small(), kBlk);
-                    q.sym = 1;
-                    q.alpha = (float)(plan.c * sp / (sg * sg));
-                    q.beta = (float)(plan.b * sp / sg);
-                } else {  // X' = a X + B X, or a X + X B (B is symmetric)
-                    q.a = wide ? poly[k] : from[k];
-                    q.b = wide ? from[k] : poly[k];
-                    q.c = from[k];
-                    q.out = to[k];
-                    q.a_nbj = wide ? mb : xb;
-                    q.b_nbj = wide ? xb : mb;
-                    q.o_nbj = xb;
-                    q.b_mn = wide;
-                    q.mt = pad_up(s.rows) / 128;
-                    q.nu = pad_up(s.cols) / 128;
-                    q.kb = (uint32_t)ceil_div(s.small(), kBlk);
-                    q.alpha = (float)(plan.x[step + 1] / (sp * sx));
-                    q.beta = (float)(plan.a * plan.x[step + 1] / sx);
-                }
-                gemm->q[k] = q;
-            }
+    std::unique_ptr<MuonGemmParams> gemm(new MuonGemmParams);  // as it comes: every field that counts is set
+    for (auto& level : levels) {
+        // long products first: a launch ends with its shortest tiles
+        std::stable_sort(level.begin(), level.end(), [](const MuonProduct& a, const MuonProduct& b) { return a.kb > b.kb; });
+        for (size_t q0 = 0; q0 < level.size(); q0 += kMuonProducts) {
+            gemm->n = (int)std::min<size_t>(kMuonProducts, level.size() - q0);
+            std::copy_n(level.begin() + q0, gemm->n, gemm->q);
             e = timed_launch([&] { return launch_muon_gemm(*gemm, stream); });
             if (e != cudaSuccess) return cuda_fail(e, "Newton-Schulz product launch");
             t_stats.launches += 1;
@@ -295,7 +400,7 @@ rr_status_t run_group(const Job& job, const Plan& plan, const std::vector<int>& 
     std::unique_ptr<MuonFinishParams> fin(new MuonFinishParams{});
     const int nr = job.out->nranks, most = std::max(1, kMuonPtrs / nr);
     fin->nranks = nr;
-    fin->inv = (float)(1.0 / plan.x[plan.steps]);
+    fin->inv = (float)(1.0 / scale_for(plan.rho[plan.steps]));
     fin->keep = job.keep;
     for (int k0 = 0; k0 < n; k0 += most) {
         fin->n = std::min(most, n - k0);
@@ -304,7 +409,7 @@ rr_status_t run_group(const Job& job, const Plan& plan, const std::vector<int>& 
             const int t = group[k0 + k];
             MuonMat& m = fin->mat[k];
             m = prep->mat[k0 + k];
-            m.x = x[plan.steps & 1][k0 + k];
+            m.x = result[k0 + k];
             m.tile0 = todo;
             todo += pad_up(m.rows) / 128 * (pad_up(m.cols) / kBlk);
             m.out_dtype = (uint8_t)job.out->dtypes[t];
@@ -326,7 +431,7 @@ rr_status_t run_group(const Job& job, const Plan& plan, const std::vector<int>& 
 rr_status_t run(const Job& job, const Plan& plan, std::vector<Span>& spans, void* ws, size_t ws_bytes, cudaStream_t stream)
 {
     uint64_t need = 0, S = 0, total = 0;
-    const auto groups = groups_of(job.in, plan.steps, &need);
+    const auto groups = groups_of(job.out, plan, job.mom != nullptr, &need);
     for (int t = 0; t < job.in->nmatrices; ++t) {
         const uint64_t numel = job.in->rows[t] * job.in->cols[t];
         S += numel * esize(job.out->dtypes[t]);
@@ -422,16 +527,16 @@ rr_status_t muon_step(const rr_matrix_list_t* params, const rr_matrix_list_t* gr
 
 extern "C" {
 
-rr_status_t rr_muon_workspace(const rr_matrix_list_t* matrices, const rr_newton_schulz_t* ns, size_t* bytes)
+rr_status_t rr_muon_workspace(const rr_matrix_list_t* results, int weights, const rr_newton_schulz_t* ns, size_t* bytes)
 {
     return guarded([&]() -> rr_status_t {
         if (!bytes) return fail(RR_ERR_INVALID_ARG, "NULL workspace size output");
         Plan plan;
         rr_status_t st = make_plan(ns, &plan);
-        if (st == RR_OK) st = check_list(matrices, "matrices");
+        if (st == RR_OK) st = check_list(results, "results");
         if (st != RR_OK) return st;
         uint64_t need = 0;
-        groups_of(matrices, plan.steps, &need);
+        groups_of(results, plan, weights != 0, &need);
         *bytes = (size_t)need;
         return RR_OK;
     });

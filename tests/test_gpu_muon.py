@@ -208,7 +208,7 @@ def test_groups_that_share_the_workspace():
     xs = [gradient(r, c, torch.bfloat16, seed=i) for i, (r, c) in enumerate(shapes)]
     ml = rrv.MatrixList(xs)
     ns = _lib.NewtonSchulz(2, *COEF, 1e-7)
-    assert ml._workspace(ns) <= (2 << 30)
+    assert ml._workspace(False, ns) <= (2 << 30)
     got = rrv.orthogonalize(ml, steps=2)
     for g, x in zip(got, xs):
         check(g, x, steps=2)
