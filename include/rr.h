@@ -524,7 +524,7 @@ typedef struct rr_matrix_list {
  * X = a X + (b A + c A^2) X with A = X X^T (for more rows than columns the same
  * on X^T), which takes every singular value s of X to a s + b s^3 + c s^5.  Five
  * steps of (3.4445, -4.7750, 2.0315) take all that are not tiny to 0.7 .. 1.2:
- * the matrix is nearly orthogonal.  steps 0..64; eps finite and above 0; a
+ * the matrix is nearly orthogonal.  steps 0..50; eps finite and above 0; a
  * singular value must not be able to pass 1024 on the way (RR_ERR_UNSUPPORTED). */
 typedef struct rr_newton_schulz {
     int32_t steps;
@@ -535,7 +535,7 @@ typedef struct rr_newton_schulz {
 /* The bytes of device workspace the calls below need (host only) for their
  * list of results (weights 0: rr_orthogonalize) or weights (1: rr_muon_step):
  * 256-byte aligned, contents neither used nor kept, one call at a time (see
- * rr_clip_workspace).  Matrices run in groups of up to 24 and 2 GiB of it. */
+ * rr_clip_workspace).  Matrices run in groups of up to 24 and 5 GiB of it. */
 rr_status_t rr_muon_workspace(const rr_matrix_list_t* results, int weights, const rr_newton_schulz_t* ns, size_t* bytes);
 
 /* Orthogonalises every matrix of `matrices` (its rank 0) into every rank's

@@ -92,6 +92,7 @@ __global__ void __launch_bounds__(kThreads) muon_squares_kernel(const __grid_con
 {
     __shared__ double sh[kThreads / 32];
     pdl_begin();
+    if (blockIdx.x == 0 && threadIdx.x < kMuonCounters) p.counters[threadIdx.x] = 0;
     const MuonMat& t = p.mat[mat_of_part(p, blockIdx.x)];
     const uint64_t len = (uint64_t)t.rows * t.cols;
     double acc = 0.0;

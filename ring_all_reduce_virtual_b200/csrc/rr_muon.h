@@ -46,35 +46,85 @@ struct Halves {
     uint16_t* lo;
 };
 
-// One product of a launch: out = alpha * op(a) op(b)^T + beta * c + diag * 1,
-// on tiles of 256 rows and `tile_n` columns.  A symmetric matrix is formed and
-// kept on and below the diagonal of its 256 x 256 tiles; an operand's block
-// above it is read as the transpose of the one below.
-struct MuonProduct {
-    Halves a, b, c, out;   // c.hi NULL: none
-    uint32_t a_nbj, b_nbj, o_nbj;  // columns of blocks: operands, out (and c)
-    uint32_t mt, nu, kb;   // units of 128 rows, of 128 columns, blocks along K
-    uint32_t tile0;        // the launch's first tile of this product
-    uint8_t a_mn, b_mn;    // the operand's rows run along K (not its columns)
-    uint8_t a_low, b_low;  // the operand is symmetric, kept on and below the diagonal
-    uint32_t side;         // diag goes to the first `side` elements of the diagonal
-    uint8_t sym, pad_[3];  // the result is symmetric
+// The products of all matrices of a call's group run in one launch, as a list
+// of tiles of 256 rows and `tile_n` columns that pairs of CTAs take in order.
+//
+// A product: out = alpha * a b^T + beta * c + diag * 1.  Of a matrix with
+// m <= n sides, X is rows x cols and the others m x m:
+//   kGram    X X^T, or X^T X of a tall matrix (symmetric)
+//   kSquare  two symmetric m x m matrices that commute (symmetric)
+//   kApply   Q X, or X Q of a tall matrix
+// A symmetric matrix is formed and kept on and below the diagonal of its
+// 256 x 256 tiles; an operand's block above it is read as the transpose of the
+// one below.
+enum MuonKind : int { kGram = 0, kSquare = 1, kApply = 2 };
+
+// Buffers of a matrix: 0 and 1 are X's, kSquares and up the m x m ones.
+constexpr uint8_t kSquares = 2, kNoBuffer = 255;
+
+struct MuonOp {
     float alpha, beta, diag;
+    uint8_t kind, a, b, c, out;  // buffers; c kNoBuffer: none.  kApply: a is Q, b is X
+    uint8_t level;               // reads what its matrix's earlier levels wrote
+    uint8_t pad_[2];
 };
 
-constexpr int kMuonMats = 24;     // matrices per launch: parameter blocks below 4 KB,
-constexpr int kMuonProducts = 30; // which larger ones cost the host 3-5 us more
+struct MuonWork {
+    uint16_t* x[2];
+    uint16_t* squares;
+    uint32_t rows, cols;
+    uint16_t op0, ops;           // its products in MuonGemmParams::op, in the order of their levels
+};
+
+constexpr int kMuonMats = 24;         // matrices per group
+constexpr int kMuonOps = 200;         // different products of a launch, at most
+constexpr int kMuonOpsSmall = 60;     // a parameter block below 4 KB: larger ones cost the host 3-5 us
+constexpr int kMuonSeq = 768;         // products of a launch in all
+constexpr int kMuonSeqSmall = 512;
+constexpr uint32_t kMuonCounters = 32;  // words of the workspace: the next tile, each matrix's finished parts
 constexpr uint32_t kNormParts = 256;  // partial sums of squares per matrix, at most
 constexpr uint32_t kPrepTile = 8192;  // elements of a tile of the first pass
 
-struct MuonGemmParams {
-    MuonProduct q[kMuonProducts];
-    int n;
-    uint32_t tile_n;       // 128 or 256
-    uint32_t tiles;
+template <int OPS, int SEQ>
+struct MuonGemmParamsT {
+    MuonWork work[kMuonMats];
+    MuonOp op[OPS];
+    uint16_t seq[SEQ];     // the products in order: matrix | (its product's number) << 5
+    uint32_t nseq;
+    uint32_t tile_n[3];    // of each kind of product: 128 or 256
+    uint32_t* counters;
     unsigned int* waits;   // bulk_wait_counters()
     uint32_t hold, spin;   // as in BulkParams
 };
+using MuonGemmParams = MuonGemmParamsT<kMuonOps, kMuonSeq>;
+
+// Sides of a matrix's product, in units of 128 rows and columns, and its tiles.
+struct MuonSides {
+    uint32_t mt, nu;
+};
+
+__host__ __device__ inline MuonSides muon_sides(uint32_t rows, uint32_t cols, int kind)
+{
+    const uint32_t mu = pad_up(rows < cols ? rows : cols) / 128;
+    if (kind == kApply) return {pad_up(rows) / 128, pad_up(cols) / 128};
+    return {mu, mu};
+}
+
+// Column tiles of row tile i of a symmetric result.
+__host__ __device__ inline uint32_t muon_sym_tiles(uint32_t i, uint32_t nu, uint32_t per)
+{
+    const uint32_t units = 2 * i + 2 < nu ? 2 * i + 2 : nu;
+    return (units + per - 1) / per;
+}
+
+__host__ __device__ inline uint32_t muon_tiles(uint32_t rows, uint32_t cols, int kind, uint32_t tile_n)
+{
+    const MuonSides s = muon_sides(rows, cols, kind);
+    const uint32_t per = tile_n / 128, r = (s.mt + 1) / 2;
+    if (kind == kApply) return r * ((s.nu + per - 1) / per);
+    // the sum of muon_sym_tiles over the row tiles
+    return per == 2 ? r * (r + 1) / 2 : r * (r + 1) - (s.mt & 1);
+}
 
 // What the elementwise passes need of a matrix.
 struct MuonMat {
@@ -93,6 +143,7 @@ struct MuonPrepParams {
     MuonMat mat[kMuonMats];
     int n;
     double* partial;
+    uint32_t* counters;    // zeroed by the first pass
     float momentum;
     int nesterov;
     float eps;
@@ -112,7 +163,7 @@ struct MuonFinishParams {
 cudaError_t launch_muon_squares(const MuonPrepParams& p, uint32_t parts, cudaStream_t s);
 cudaError_t launch_muon_pack(const MuonPrepParams& p, uint32_t tiles, cudaStream_t s);
 cudaError_t launch_muon_finish(const MuonFinishParams& p, uint32_t tiles, cudaStream_t s);
-// Fills in the tiles and the waits and launches.
-cudaError_t launch_muon_gemm(MuonGemmParams& p, cudaStream_t s);
+// The products of a group: tile_n, waits, hold and spin are filled in here.
+cudaError_t launch_muon_gemm(MuonGemmParams& p, int nops, cudaStream_t s);
 
 }  // namespace rr

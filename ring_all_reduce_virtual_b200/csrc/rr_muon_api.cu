@@ -12,10 +12,10 @@ using namespace rr;
 namespace {
 
 constexpr uint64_t kMaxSide = 1ull << 20;    // rows and columns
-constexpr int kMaxSteps = 64;
+constexpr int kMaxSteps = 50;
 // Workspace of a group of matrices that run in the same launches, unless one
 // alone needs more.
-constexpr uint64_t kGroupBytes = 2ull << 30;
+constexpr uint64_t kGroupBytes = 5ull << 30;
 
 bool real_dtype(rr_dtype_t d) { return d == RR_F32 || d == RR_BF16 || d == RR_F16; }
 
@@ -85,7 +85,7 @@ double scale_for(double bound)
 rr_status_t make_plan(const rr_newton_schulz_t* ns, Plan* p)
 {
     if (!ns) return fail(RR_ERR_INVALID_ARG, "NULL Newton-Schulz parameters");
-    if (ns->steps < 0 || ns->steps > kMaxSteps) return fail(RR_ERR_INVALID_ARG, "steps must be in 0..64");
+    if (ns->steps < 0 || ns->steps > kMaxSteps) return fail(RR_ERR_INVALID_ARG, "steps must be in 0..50");
     if (!(ns->eps > 0.0f) || std::isinf(ns->eps)) return fail(RR_ERR_INVALID_ARG, "eps must be finite and above 0");
     if (!std::isfinite(ns->a) || !std::isfinite(ns->b) || !std::isfinite(ns->c))
         return fail(RR_ERR_INVALID_ARG, "the coefficients must be finite");
@@ -171,6 +171,16 @@ Room room_of(const Shape& s, const std::vector<int>& segments)
 uint32_t parts_of(const Shape& s) { return (uint32_t)std::min<uint64_t>(kNormParts, ceil_div(s.numel(), kPrepTile)); }
 
 constexpr uint64_t kPartialBytes = (uint64_t)kMuonMats * kNormParts * sizeof(double);
+constexpr uint64_t kHeadBytes = kPartialBytes + 256;  // and the counters
+static_assert(kMuonCounters * 4 <= 256 && kMuonMats < (int)kMuonCounters && kMuonMats <= 32, "a counter per matrix and one more");
+
+// Products of a matrix.
+int products_in(const std::vector<int>& segments)
+{
+    int n = 0;
+    for (int len : segments) n += 2 + len + (len - 1) * 3;
+    return n;
+}
 
 // How exactly a list's matrix t has to come out.
 Exactness exactness(const rr_matrix_list_t* out, int t, bool weights)
@@ -188,16 +198,28 @@ std::vector<int> segments_for(const Plan& plan, const rr_matrix_list_t* out, int
 // The groups of a list's matrices (those with elements), in order.
 std::vector<std::vector<int>> groups_of(const rr_matrix_list_t* l, const Plan& plan, bool weights, uint64_t* bytes)
 {
-    std::vector<std::vector<int>> groups;
+    std::vector<std::vector<int>> groups, kinds;
     uint64_t used = 0;
+    int listed = 0, ops = 0;
     *bytes = 256;
     for (int t = 0; t < l->nmatrices; ++t) {
         const Shape s{(uint32_t)l->rows[t], (uint32_t)l->cols[t]};
         if (s.numel() == 0) continue;
-        const uint64_t need = room_of(s, segments_for(plan, l, t, weights)).bytes();
-        if (groups.empty() || groups.back().size() == kMuonMats || used + need > kGroupBytes) {
+        const std::vector<int> segments = segments_for(plan, l, t, weights);
+        const uint64_t need = room_of(s, segments).bytes();
+        const int products = products_in(segments);
+        const bool seen = std::find(kinds.begin(), kinds.end(), segments) != kinds.end();
+        if (groups.empty() || groups.back().size() == kMuonMats || used + need > kGroupBytes ||
+            listed + products > kMuonSeq || (!seen && ops + products > kMuonOps)) {
             groups.emplace_back();
-            used = kPartialBytes;
+            used = kHeadBytes;
+            listed = ops = 0;
+            kinds.clear();
+        }
+        listed += products;
+        if (std::find(kinds.begin(), kinds.end(), segments) == kinds.end()) {
+            kinds.push_back(segments);
+            ops += products;
         }
         groups.back().push_back(t);
         used += need;
@@ -223,130 +245,94 @@ float shape_factor(const Shape& s, int adjust)
 
 bool on16(const void* p) { return (uintptr_t)p % 16 == 0; }
 
-// The products of one matrix, level by level: what a level reads was written in
-// an earlier one.  x[0] holds the first X; *last is the result's buffer.
-void products_of(const Plan& plan, const Shape& s, const std::vector<int>& segments, const Halves (&x)[2],
-                 const Halves (&sq)[5], std::vector<std::vector<MuonProduct>>& levels, int* last)
+// The products of a matrix of m <= n sides, in the order of their levels; X
+// begins in buffer 0.  *last: the result's buffer.
+std::vector<MuonOp> products_of(const Plan& plan, const std::vector<int>& segments, int* last)
 {
-    const bool wide = s.rows <= s.cols;
-    const uint32_t m = s.small(), n = std::max(s.rows, s.cols);
-    const uint32_t xb = pad_up(s.cols) / kBlk, mb = pad_up(m) / kBlk, mu = pad_up(m) / 128;
-    size_t level = 0;
-    const auto add = [&](size_t at, const MuonProduct& q) {
-        if (levels.size() <= at) levels.resize(at + 1);
-        levels[at].push_back(q);
-    };
-    // a product of two symmetric m x m matrices that commute
-    const auto square = [&](const Halves& a, const Halves& b, const Halves& out, double alpha) {
-        MuonProduct q{};
+    std::vector<MuonOp> ops;
+    const uint8_t A = kSquares, Y = kSquares + 1, D = kSquares + 2;
+    uint8_t cur = 0;
+    int step = 0, level = 0;
+    const auto add = [&](int kind, uint8_t a, uint8_t b, uint8_t out, int at, double alpha) -> MuonOp& {
+        MuonOp q{};
+        q.kind = (uint8_t)kind;
         q.a = a;
         q.b = b;
+        q.c = kNoBuffer;
         q.out = out;
-        q.a_nbj = q.b_nbj = q.o_nbj = mb;
-        q.a_low = q.b_low = q.sym = 1;
-        q.mt = q.nu = mu;
-        q.kb = (uint32_t)ceil_div(m, kBlk);
+        q.level = (uint8_t)at;
         q.alpha = (float)alpha;
-        return q;
+        ops.push_back(q);
+        return ops.back();
     };
-    const Halves A = sq[0], Y = sq[1], D = sq[2];
-    int cur = 0, step = 0;
     for (int len : segments) {
         const double sx = scale_for(plan.rho[step]);
         double top = plan.rho[step] * plan.rho[step], sa = scale_for(top);
-        MuonProduct g{};  // A = X X^T, or X^T X
-        g.a = g.b = x[cur];
-        g.out = A;
-        g.a_nbj = g.b_nbj = xb;
-        g.o_nbj = mb;
-        g.a_mn = g.b_mn = !wide;
-        g.sym = 1;
-        g.mt = g.nu = mu;
-        g.kb = (uint32_t)ceil_div(n, kBlk);
-        g.alpha = (float)(sa / (sx * sx));
-        add(level++, g);
+        add(kGram, cur, cur, A, level++, sa / (sx * sx));
         // A segment of one step keeps a X out of the products, X <- a X + (D - a) X:
         // as a term of the tensor cores' sums it would be cut off with them
         // (a step's error 4e-7 instead of 8e-8).
         const bool alone = len == 1;
-        Halves Q = alone ? sq[1] : sq[3], Q2 = sq[4];
-        double bound = 1.0, sq_scale = 1.0;  // of Q
+        uint8_t Q = alone ? Y : kSquares + 3, Q2 = kSquares + 4;
+        double bound = 1.0, scale_q = 1.0;  // of Q
         for (int k = 0; k < len; ++k) {
             const double most = plan.poly[step + k] + (alone ? std::fabs(plan.a) : 0.0), sd = scale_for(most);
-            const Halves d = k == 0 ? Q : D;
-            MuonProduct q = square(A, A, d, plan.c * sd / (sa * sa));
+            const uint8_t d = k == 0 ? Q : D;
+            MuonOp& q = add(kSquare, A, A, d, level++, plan.c * sd / (sa * sa));
             q.c = A;
             q.beta = (float)(plan.b * sd / sa);
-            if (!alone) {
-                q.diag = (float)(plan.a * sd);
-                q.side = m;
-            }
-            add(level++, q);
+            q.diag = alone ? 0.0f : (float)(plan.a * sd);
             if (k == 0) {
                 bound = most;
-                sq_scale = sd;
+                scale_q = sd;
             }
-            size_t end = level;
-            if (k + 1 < len) {  // A <- D (D A)
-                const double sy = scale_for(most * top);
-                add(level, square(d, A, Y, sy / (sd * sa)));
-                top = plan.rho[step + k + 1] * plan.rho[step + k + 1];
-                sa = scale_for(top);
-                add(level + 1, square(d, Y, A, sa / (sd * sy)));
-                end = level + 2;
-            }
-            if (k > 0) {
+            if (k > 0) {  // Q <- D Q, beside D A
                 bound *= most;
                 const double to = scale_for(bound);
-                add(level, square(d, Q, Q2, to / (sd * sq_scale)));
-                sq_scale = to;
+                add(kSquare, d, Q, Q2, level, to / (sd * scale_q));
+                scale_q = to;
                 std::swap(Q, Q2);
-                end = std::max(end, level + 1);
             }
-            level = end;
+            if (k + 1 < len) {  // A <- D (D A)
+                const double sy = scale_for(most * top);
+                add(kSquare, d, A, Y, level++, sy / (sd * sa));
+                top = plan.rho[step + k + 1] * plan.rho[step + k + 1];
+                sa = scale_for(top);
+                add(kSquare, d, Y, A, level++, sa / (sd * sy));
+            } else if (k > 0) {
+                ++level;
+            }
         }
         step += len;
-        MuonProduct q{};  // X = Q X, or X Q
-        q.a = wide ? Q : x[cur];
-        q.b = wide ? x[cur] : Q;
-        q.out = x[cur ^ 1];
-        q.a_nbj = wide ? mb : xb;
-        q.b_nbj = wide ? xb : mb;
-        q.o_nbj = xb;
-        q.a_low = wide;
-        q.b_low = !wide;
-        q.b_mn = wide;
-        q.mt = pad_up(s.rows) / 128;
-        q.nu = pad_up(s.cols) / 128;
-        q.kb = (uint32_t)ceil_div(m, kBlk);
         const double to = scale_for(plan.rho[step]);
-        q.alpha = (float)(to / (sq_scale * sx));
+        MuonOp& q = add(kApply, Q, cur, cur ^ 1, level++, to / (scale_q * sx));
         if (alone) {
-            q.c = x[cur];
+            q.c = cur;
             q.beta = (float)(plan.a * to / sx);
         }
-        add(level++, q);
         cur ^= 1;
     }
     *last = cur;
+    return ops;
 }
 
 rr_status_t run_group(const Job& job, const Plan& plan, const std::vector<int>& group, char* ws, cudaStream_t stream)
 {
     const int n = (int)group.size();
     std::unique_ptr<MuonPrepParams> prep(new MuonPrepParams{});
-    std::vector<std::vector<MuonProduct>> levels;
+    std::unique_ptr<MuonGemmParams> gemm(new MuonGemmParams);  // as it comes: every field that counts is set
     std::vector<Halves> result(n);
-    uint64_t at = kPartialBytes;
-    const auto take = [&](uint64_t half) {
-        Halves h;
-        h.hi = reinterpret_cast<uint16_t*>(ws + at);
-        h.lo = reinterpret_cast<uint16_t*>(ws + at + half);
-        at += 2 * half;
-        return h;
+    std::vector<std::pair<std::vector<int>, std::pair<int, int>>> known;  // segments: first product, result's buffer
+    int nops = 0;
+    uint64_t at = kHeadBytes;
+    const auto take = [&](uint64_t bytes) {
+        uint16_t* const p = reinterpret_cast<uint16_t*>(ws + at);
+        at += bytes;
+        return p;
     };
     prep->n = n;
     prep->partial = reinterpret_cast<double*>(ws);
+    prep->counters = gemm->counters = reinterpret_cast<uint32_t*>(ws + kPartialBytes);
     prep->momentum = job.momentum;
     prep->nesterov = job.nesterov;
     prep->eps = job.eps;
@@ -358,12 +344,25 @@ rr_status_t run_group(const Job& job, const Plan& plan, const std::vector<int>& 
         const Shape s = shape[k] = {(uint32_t)job.in->rows[t], (uint32_t)job.in->cols[t]};
         const std::vector<int> segments = segments_for(plan, job.out, t, job.mom != nullptr);
         const Room room = room_of(s, segments);
-        Halves x[2], sq[5]{};
-        for (int i = 0; i < room.xs; ++i) x[i] = take(room.x);
-        for (int i = 0; i < room.squares; ++i) sq[i] = take(room.square);
-        int last = 0;
-        products_of(plan, s, segments, x, sq, levels, &last);
-        result[k] = x[last];
+        auto same = std::find_if(known.begin(), known.end(), [&](const auto& e) { return e.first == segments; });
+        if (same == known.end()) {
+            int last = 0;
+            const std::vector<MuonOp> ops = products_of(plan, segments, &last);
+            std::copy(ops.begin(), ops.end(), gemm->op + nops);
+            known.push_back({segments, {nops, last}});
+            same = known.end() - 1;
+            nops += (int)ops.size();
+        }
+        MuonWork& w = gemm->work[k];
+        for (int i = 0; i < 2; ++i) w.x[i] = i < room.xs ? take(2 * room.x) : nullptr;
+        w.squares = take(2 * room.square * room.squares);
+        w.rows = s.rows;
+        w.cols = s.cols;
+        w.op0 = (uint16_t)same->second.first;
+        w.ops = (uint16_t)products_in(segments);
+        uint16_t* const last = w.x[same->second.second];
+        result[k] = {last, last + room.x / 2};
+        const Halves first{w.x[0], w.x[0] + room.x / 2};
         MuonMat& m = prep->mat[k];
         m.g = job.in->ptrs[t];
         m.m = job.mom ? static_cast<float*>(job.mom->ptrs[t]) : nullptr;
@@ -371,7 +370,7 @@ rr_status_t run_group(const Job& job, const Plan& plan, const std::vector<int>& 
         m.cols = s.cols;
         m.part0 = parts;
         m.parts = parts_of(s);
-        m.x = x[0];
+        m.x = first;
         m.tile0 = tiles;
         m.dtype = (uint8_t)job.in->dtypes[t];
         m.vec = s.cols % 8 == 0 && on16(m.g) && (!m.m || on16(m.m));
@@ -384,18 +383,28 @@ rr_status_t run_group(const Job& job, const Plan& plan, const std::vector<int>& 
     if (e != cudaSuccess) return cuda_fail(e, "Muon pack launch");
     t_stats.launches += 2;
 
-    std::unique_ptr<MuonGemmParams> gemm(new MuonGemmParams);  // as it comes: every field that counts is set
-    for (auto& level : levels) {
-        // long products first: a launch ends with its shortest tiles
-        std::stable_sort(level.begin(), level.end(), [](const MuonProduct& a, const MuonProduct& b) { return a.kb > b.kb; });
-        for (size_t q0 = 0; q0 < level.size(); q0 += kMuonProducts) {
-            gemm->n = (int)std::min<size_t>(kMuonProducts, level.size() - q0);
-            std::copy_n(level.begin() + q0, gemm->n, gemm->q);
-            e = timed_launch([&] { return launch_muon_gemm(*gemm, stream); });
-            if (e != cudaSuccess) return cuda_fail(e, "Newton-Schulz product launch");
-            t_stats.launches += 1;
+    // The list of products: level by level, in each the longest first, so that the
+    // end of a level is short tiles.
+    struct Item {
+        int level;
+        uint32_t depth, at;
+    };
+    std::vector<Item> list;
+    for (int k = 0; k < n; ++k) {
+        const MuonWork& w = gemm->work[k];
+        for (int o = 0; o < w.ops; ++o) {
+            const MuonOp& q = gemm->op[w.op0 + o];
+            const uint32_t depth = q.kind == kGram ? std::max(w.rows, w.cols) : shape[k].small();
+            list.push_back({q.level, depth, (uint32_t)(k | o << 5)});
         }
     }
+    std::stable_sort(list.begin(), list.end(),
+                     [](const Item& a, const Item& b) { return a.level != b.level ? a.level < b.level : a.depth > b.depth; });
+    gemm->nseq = (uint32_t)list.size();
+    for (size_t k = 0; k < list.size(); ++k) gemm->seq[k] = (uint16_t)list[k].at;
+    e = timed_launch([&] { return launch_muon_gemm(*gemm, nops, stream); });
+    if (e != cudaSuccess) return cuda_fail(e, "Newton-Schulz product launch");
+    t_stats.launches += gemm->nseq > 0 ? 1 : 0;
 
     std::unique_ptr<MuonFinishParams> fin(new MuonFinishParams{});
     const int nr = job.out->nranks, most = std::max(1, kMuonPtrs / nr);

@@ -1,36 +1,40 @@
 // rr_muon_gemm.cu -- the products of the Newton-Schulz iteration on the fifth
-// generation tensor cores: a group of matrices in one launch,
-//     out = alpha * op(A) op(B)^T + beta * C
-// for operands and results held as two fp16 halves (rr_muon.h).  A product of
+// generation tensor cores: all steps of a group of matrices in one launch
+// (rr_muon.h), for operands and results held as two fp16 halves.  A product of
 // two such values is three products of halves, lo hi + hi lo + hi hi (lo lo is
 // below 2^-22), in one fp32 accumulator.
 //
 // Two CTAs on neighbouring SMs share a tile of 256 x 256 (or 256 x 128): each
 // copies its 128 rows of A and its half of B's (cp.async.bulk, both halves of 64
 // of K a stage, 64 KB, three stages), and the first one's instructions multiply
-// out of both.  That is what the L2 cache can feed: 196 operations a byte,
-// against 85 of one CTA's tile of 128 x 256 with K gone through three times
-// (796 TFLOP/s at 16 matrices of width 2048, all of it waiting for L2).
-// Of a CTA's warps one copies, one issues the products (in the second CTA: tells
-// the first that a stage has landed), eight take accumulators out of tensor
-// memory.
+// out of both: 196 operations a byte from L2, against 85 of one CTA's tile of
+// 128 x 256 with K gone through three times.  Of a CTA's warps two copy, one
+// issues the products (in the second CTA: tells the first that a stage has
+// landed), eight take accumulators out of tensor memory.
 //
 // The tensor cores' sums are cut off, not rounded: a long one comes out low by
 // 2^-25 and more a term (a sum of 8192 positive products by 1.5e-5).  So an
 // accumulator collects kChunk stages only; the eight warps add it to sums in
 // their registers, rounded to nearest, while the other accumulator fills.
 //
+// A pair takes the next tile of the list from a counter, and begins it once its
+// matrix's earlier levels are finished, which another counter says.  A tile
+// waits only for tiles before it in the list, which are then in the hands of
+// pairs that run, so the waits end whatever the number of pairs that run at a
+// time.  Against a launch per level, SMs do not idle at the end of each level
+// while another matrix has work, and a level of a small matrix does not cost a
+// launch.
+//
 // Results leave through shared memory, 4 KB a warp: a thread has a row of the
 // tile, whose 16-byte pieces lie 128 bytes from the next row's; written to L2
-// from there they took the warps longer than the products (8 x 2048 x 2048, one
-// step: 803 us against 633 without them).  Laid into 32 rows of a block they go
-// out as one copy.
+// from there they took the warps longer than the products took.
 //
 // Every wait is bounded (rr_bulk.cuh): one that runs out is counted, the CTA's
 // warps stop, wait (bounded) for copies and products in flight, give their
 // tensor memory back and leave; what the call writes is then undefined.
 #include <algorithm>
 #include <atomic>
+#include <cstddef>
 
 #include <cuda_fp16.h>
 
@@ -56,17 +60,33 @@ constexpr int kGemmThreads = 128 + 32 * kTakers;
 constexpr int kFewRegs = 56, kManyRegs = 224;
 static_assert(128 * kFewRegs + 32 * kTakers * kManyRegs <= 168 * kGemmThreads, "more than the launch has");
 constexpr uint32_t kOutBytes = 32 * kBlk * 2;  // a warp's 32 rows of a block
-constexpr uint32_t kSmem = kStages * kStageBytes + kTakers * kOutBytes + 1024 + 256;  // from a 1024-byte boundary; barriers
+constexpr int kSlots = 4;                      // tiles handed on to the CTA's other warps
+constexpr uint32_t kSmem = kStages * kStageBytes + kTakers * kOutBytes + 1024 + 512;  // from a 1024-byte boundary; the rest
+constexpr uint32_t kEnd = 0xffffffffu;
+constexpr uint32_t kFull = 0xffffffffu;
+
+struct Slot {
+    uint32_t seq;   // in the list of products; kEnd: no more tiles
+    uint32_t i, j;  // the tile: 256 rows, tile_n columns
+    uint32_t pad_;
+};
 
 struct Bars {
     uint64_t full[kStages], empty[kStages];  // of a stage: its copies have landed; its products are done
     uint64_t other[kStages];                 // first CTA: the second's copies have landed
     uint64_t ready[2], taken[2];             // of an accumulator: finished; read out by both CTAs (in the first)
-    uint64_t added[kTakers];                 // a taker's piece of C has landed
+    uint64_t told[kSlots], heard[kSlots];    // of a slot: filled; read by all of both CTAs (in the first)
     uint64_t drained;
+    Slot slot[kSlots];
     uint32_t tmem;
     uint32_t stop;
+    uint32_t begun_b;                        // stages that copies of B were begun for
 };
+static_assert(sizeof(Bars) <= 512 && offsetof(Bars, slot) % 16 == 0, "kSmem counts 512 bytes; slots are written whole");
+// Who reads a slot: the first CTA's copies of B, products and takers, the second's copies, messages and takers.
+constexpr uint32_t kHearers = 2 + kTakers + 3 + kTakers;
+
+// ---------------------------------------------------------------- barriers
 
 __device__ __forceinline__ uint32_t smem_of(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
@@ -83,6 +103,11 @@ __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity)
     return done != 0;
 }
 
+__device__ __forceinline__ void give_up(Bars* b, unsigned int* waits)
+{
+    if (atomicExch(&b->stop, 1u) == 0) atomicAdd(&waits[0], 1u);
+}
+
 // Bounded; false as well once another warp of the CTA has given up.
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, Bars* b, unsigned int* waits, uint32_t spin)
 {
@@ -91,17 +116,16 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, Bars* b
         if (try_wait(at, parity)) return true;
         if (*(volatile uint32_t*)&b->stop) return false;
     }
-    if (atomicExch(&b->stop, 1u) == 0) atomicAdd(&waits[0], 1u);
+    give_up(b, waits);
     return false;
 }
 
-// The same for a whole warp, one lane of which looks: 32 that do keep the shared
-// memory busy for the warps that copy and multiply.
+// The same for a whole warp, one lane of which looks.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Bars* b, unsigned int* waits, uint32_t spin)
 {
     uint32_t ok = 0;
     if ((threadIdx.x & 31) == 0) ok = wait_for(bar, parity, b, waits, spin);
-    return __shfl_sync(0xffffffffu, ok, 0) != 0;
+    return __shfl_sync(kFull, ok, 0) != 0;
 }
 
 __device__ __forceinline__ void bar_init(uint64_t* bar, uint32_t count)
@@ -130,44 +154,156 @@ __device__ __forceinline__ void copy_block(uint32_t to, const uint16_t* from, ui
                  : "memory");
 }
 
-// Where the launch's tile `w` lies: 256 rows, tile_n columns.
+// ------------------------------------------------------------------- tiles
+
+// A buffer of a matrix, and its columns of blocks.
+__device__ __forceinline__ Halves buffer_of(const MuonWork& w, uint32_t id, uint32_t* nbj)
+{
+    const uint32_t m = pad_up(min(w.rows, w.cols));
+    if (id < kSquares) {
+        *nbj = pad_up(w.cols) / kBlk;
+        return {w.x[id], w.x[id] + (uint64_t)pad_up(w.rows) * pad_up(w.cols)};
+    }
+    *nbj = m / kBlk;
+    const uint64_t half = (uint64_t)m * m;
+    uint16_t* hi = w.squares + (id - kSquares) * 2 * half;
+    return {hi, hi + half};
+}
+
+// Blocks along K.
+__device__ __forceinline__ uint32_t depth_of(const MuonWork& w, int kind)
+{
+    const uint32_t k = kind == kGram ? max(w.rows, w.cols) : min(w.rows, w.cols);
+    return (k + kBlk - 1) / kBlk;
+}
+
+// Tile t of a product.
+__device__ __forceinline__ void place_of(const MuonWork& w, int kind, uint32_t tile_n, uint32_t t, uint32_t* i, uint32_t* j)
+{
+    const MuonSides s = muon_sides(w.rows, w.cols, kind);
+    if (kind == kApply) {
+        const uint32_t r = (s.mt + 1) / 2;
+        *i = t % r;
+        *j = t / r;
+        return;
+    }
+    uint32_t row = 0;
+    for (uint32_t n; t >= (n = muon_sym_tiles(row, s.nu, tile_n / 128)); ++row) t -= n;
+    *i = row;
+    *j = t;
+}
+
+// What every warp knows of its tile.
 struct Tile {
-    const MuonProduct* q;
-    uint32_t i, j;
-    uint32_t units;  // of 128 columns: 1 or 2
+    const MuonWork* w;
+    const MuonOp* op;
+    uint32_t i, j, per, units, mt, kb, mat;  // per: units of 128 columns of a whole tile
 };
 
-// Column tiles of a row tile of a symmetric result.
-__host__ __device__ __forceinline__ uint32_t sym_tiles(uint32_t i, uint32_t nu, uint32_t per)
+template <class P>
+__device__ __forceinline__ Tile tile_at(const P& p, const Slot& s)
 {
-    const uint32_t units = 2 * i + 2 < nu ? 2 * i + 2 : nu;
-    return (units + per - 1) / per;
-}
-
-__device__ __forceinline__ Tile tile_of(const MuonGemmParams& p, uint32_t w)
-{
-    int lo = 0, hi = p.n;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (p.q[mid].tile0 <= w) lo = mid;
-        else hi = mid;
-    }
     Tile t;
-    t.q = &p.q[lo];
-    uint32_t k = w - t.q->tile0;
-    const uint32_t per = p.tile_n / 128, rows = (t.q->mt + 1) / 2;
-    if (t.q->sym) {
-        uint32_t i = 0;
-        while (k >= sym_tiles(i, t.q->nu, per)) k -= sym_tiles(i++, t.q->nu, per);
-        t.i = i;
-        t.j = k;
-    } else {
-        t.i = k % rows;
-        t.j = k / rows;
-    }
-    t.units = min(per, t.q->nu - t.j * per);
+    const uint32_t e = p.seq[s.seq];
+    t.mat = e & 31u;
+    t.w = &p.work[t.mat];
+    t.op = &p.op[t.w->op0 + (e >> 5)];
+    const MuonSides sides = muon_sides(t.w->rows, t.w->cols, t.op->kind);
+    t.i = s.i;
+    t.j = s.j;
+    t.per = p.tile_n[t.op->kind] / 128;
+    t.units = min(t.per, sides.nu - s.j * t.per);
+    t.mt = sides.mt;
+    t.kb = depth_of(*t.w, t.op->kind);
     return t;
 }
+
+// Tiles of product k of the list.
+template <class P>
+__device__ __forceinline__ uint32_t tiles_of(const P& p, uint32_t k)
+{
+    const uint32_t e = p.seq[k];
+    const MuonWork& w = p.work[e & 31u];
+    const int kind = p.op[w.op0 + (e >> 5)].kind;
+    return muon_tiles(w.rows, w.cols, kind, p.tile_n[kind]);
+}
+
+// What the matrix's counter shows when the levels before op's are finished:
+// every taker of both CTAs counts each tile.
+template <class P>
+__device__ __forceinline__ uint32_t parts_before(const P& p, const Tile& t)
+{
+    uint32_t tiles[3], sum = 0;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) tiles[k] = muon_tiles(t.w->rows, t.w->cols, k, p.tile_n[k]);
+    for (uint32_t o = 0; o < t.w->ops; ++o) {
+        const MuonOp& op = p.op[t.w->op0 + o];
+        if (op.level >= t.op->level) break;
+        sum += op.kind == kGram ? tiles[kGram] : op.kind == kSquare ? tiles[kSquare] : tiles[kApply];
+    }
+    return sum * 2 * kTakers;
+}
+
+__device__ __forceinline__ bool parts_done(const uint32_t* counter, uint32_t need, Bars* b, unsigned int* waits, uint32_t spin)
+{
+    for (uint32_t i = 0; i < spin; ++i) {
+        uint32_t have;
+        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(have) : "l"(counter) : "memory");
+        if (have >= need) return true;
+        if (*(volatile uint32_t*)&b->stop) return false;
+    }
+    give_up(b, waits);
+    return false;
+}
+
+// A tile into both CTAs' slot.
+__device__ __forceinline__ void tell(const Slot& s, uint32_t n, Bars* b)
+{
+    const uint32_t k = n % kSlots, at = smem_of(&b->slot[k]), bar = smem_of(&b->told[k]);
+    asm volatile(
+        "{\n\t.reg .b32 a, r;\n\t"
+        "st.shared.v4.b32 [%0], {%2, %3, %4, %2};\n\t"
+        "mapa.shared::cluster.u32 r, %1, 0;\n\t"
+        "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [r];\n\t"
+        "mapa.shared::cluster.u32 a, %0, 1;\n\t"
+        "st.shared::cluster.v4.b32 [a], {%2, %3, %4, %2};\n\t"
+        "mapa.shared::cluster.u32 r, %1, 1;\n\t"
+        "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [r];\n\t}" ::"r"(at),
+        "r"(bar), "r"(s.seq), "r"(s.i), "r"(s.j)
+        : "memory");
+}
+
+// The next tile as it was told, for one thread; it says that it has read it.
+__device__ __forceinline__ bool hear(Slot& s, uint32_t n, Bars* b, unsigned int* waits, uint32_t spin)
+{
+    const uint32_t k = n % kSlots;
+    s.seq = kEnd;
+    s.i = s.j = 0;
+    if (!wait_for(&b->told[k], (n / kSlots) & 1, b, waits, spin)) return false;
+    volatile Slot* v = &b->slot[k];
+    s.seq = v->seq;
+    s.i = v->i;
+    s.j = v->j;
+    first_arrive(&b->heard[k]);
+    return s.seq != kEnd;
+}
+
+__device__ __forceinline__ void share(Slot& s)
+{
+    s.seq = __shfl_sync(kFull, s.seq, 0);
+    s.i = __shfl_sync(kFull, s.i, 0);
+    s.j = __shfl_sync(kFull, s.j, 0);
+}
+
+// The same for a whole warp.
+__device__ __forceinline__ bool warp_hear(Slot& s, uint32_t n, Bars* b, unsigned int* waits, uint32_t spin)
+{
+    if ((threadIdx.x & 31) == 0) hear(s, n, b, waits, spin);
+    share(s);
+    return s.seq != kEnd;
+}
+
+// ---------------------------------------------------------------- products
 
 // Shared-memory descriptor of an operand in 128-byte-swizzled blocks: K along a
 // block's columns (groups of 8 rows are 1024 bytes apart), or along its rows
@@ -213,80 +349,64 @@ __device__ __forceinline__ void load_acc(uint32_t addr, uint32_t (&r)[32])
           "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]),
           "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(addr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
-// A taker's 4 KB of shared memory, 32 rows of one half of a block.
+__device__ __forceinline__ void acc_landed() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// ----------------------------------------------------------------- results
+
+// A taker's 4 KB of shared memory, 32 rows of one half of a block, in which a
+// lane has its row's pieces and the warp moves whole lines.
 struct OutRows {
     uint8_t* mem;
-    uint64_t* bar;    // of copies into it
-    uint32_t parity;  // of the next one
 
     __device__ __forceinline__ uint4* piece(int lane, int g) const
     {
         return reinterpret_cast<uint4*>(mem + lane * (kBlk * 2) + ((g ^ (lane & 7)) << 4));
     }
-    // Free again: the copy out of it has read it.
-    __device__ __forceinline__ void reuse(int lane) const
-    {
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-        __syncwarp();
-    }
-    __device__ __forceinline__ void send(uint16_t* to, int lane) const
-    {
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) {
-            asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(to), "r"(smem_of(mem)), "r"(kOutBytes)
-                         : "memory");
-            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-        }
-    }
+    __device__ __forceinline__ uint4* line(int lane, int g) const { return reinterpret_cast<uint4*>(mem) + g * 32 + lane; }
 };
 
-// 64 columns of this thread's row: to out's block, `at` halves into it.
-__device__ __forceinline__ bool put_block(const MuonProduct& q, uint64_t at, uint32_t row, uint32_t col, float (&v)[64], OutRows& o,
-                                          int lane, Bars* b, const MuonGemmParams& p)
+__device__ __forceinline__ void fetch(uint4 (&r)[8], const uint16_t* from, int lane)
 {
 #pragma unroll
-    for (int l = 0; l < 64; ++l) v[l] *= q.alpha;
-    if (q.c.hi) {
-#pragma unroll 1
+    for (int g = 0; g < 8; ++g) r[g] = __ldcg(reinterpret_cast<const uint4*>(from) + g * 32 + lane);
+}
+
+// 64 columns of this thread's row of the sums: v[l] is column col + l.  The
+// warp's part of the blocks begins at c and out.
+__device__ __forceinline__ void put_block(float (&v)[64], const MuonOp& op, const Halves& c, const Halves& out, uint32_t row,
+                                          uint32_t col, uint32_t side, const OutRows& o, int lane)
+{
+    const float alpha = op.alpha, beta = op.beta, diag = op.diag;
+#pragma unroll
+    for (int l = 0; l < 64; ++l) v[l] *= alpha;
+    if (c.hi) {
+        uint4 r[8];
+        fetch(r, c.hi, lane);
+#pragma unroll
         for (int half = 0; half < 2; ++half) {
-            o.reuse(lane);
-            if (lane == 0) {
-                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_of(o.bar)), "r"(kOutBytes) : "memory");
-                copy_block(smem_of(o.mem), (half ? q.c.lo : q.c.hi) + at, kOutBytes, o.bar);
-            }
-            const bool landed = warp_wait(o.bar, o.parity, b, p.waits, p.spin);
-            o.parity ^= 1;
-            if (!landed) {  // given up: the copy lands before the CTA leaves
-                if (lane == 0) {
-                    bool late = false;
-                    for (uint32_t i = 0; i < p.spin && !late; ++i) late = try_wait(smem_of(o.bar), o.parity ^ 1);
-                    if (!late) atomicAdd(&p.waits[1], 1u);
-                }
-                __syncwarp();
-                return false;
-            }
+#pragma unroll
+            for (int g = 0; g < 8; ++g) *o.line(lane, g) = r[g];
+            __syncwarp();
+            if (half == 0) fetch(r, c.lo, lane);
 #pragma unroll
             for (int g = 0; g < 8; ++g) {
                 float a[8];
                 F16T::unpack(*o.piece(lane, g), a);
 #pragma unroll
-                for (int l = 0; l < 8; ++l) v[g * 8 + l] = __fmaf_rn(q.beta, a[l], v[g * 8 + l]);
+                for (int l = 0; l < 8; ++l) v[g * 8 + l] = __fmaf_rn(beta, a[l], v[g * 8 + l]);
             }
             __syncwarp();
         }
     }
-    if (q.diag != 0.0f && row < q.side) {
+    if (diag != 0.0f && row < side && row / 64 == col / 64) {
 #pragma unroll
         for (int l = 0; l < 64; ++l)
-            if (col + l == row) v[l] += q.diag;
+            if (col + l == row) v[l] += diag;
     }
-#pragma unroll 1
+#pragma unroll
     for (int half = 0; half < 2; ++half) {
-        o.reuse(lane);
 #pragma unroll
         for (int g = 0; g < 8; ++g) {
             float a[8];
@@ -294,27 +414,260 @@ __device__ __forceinline__ bool put_block(const MuonProduct& q, uint64_t at, uin
             for (int l = 0; l < 8; ++l) a[l] = v[g * 8 + l];
             const uint4 w = F16T::pack(a);
             *o.piece(lane, g) = w;
-            float r[8];
-            F16T::unpack(w, r);  // what is left, for the second half (unread after it)
+            if (half == 0) {  // what is left
+                float r[8];
+                F16T::unpack(w, r);
 #pragma unroll
-            for (int l = 0; l < 8; ++l) v[g * 8 + l] = a[l] - r[l];
+                for (int l = 0; l < 8; ++l) v[g * 8 + l] = a[l] - r[l];
+            }
         }
-        o.send((half ? q.out.lo : q.out.hi) + at, lane);
+        __syncwarp();
+        uint4* to = reinterpret_cast<uint4*>(half ? out.lo : out.hi);
+#pragma unroll
+        for (int g = 0; g < 8; ++g) __stcg(to + g * 32 + lane, *o.line(lane, g));
+        __syncwarp();
+    }
+}
+
+// ------------------------------------------------------------- the warps
+
+// The first CTA's lane that takes tiles off the list: the next one's number, and
+// where in the list it is.
+template <class P>
+struct Source {
+    uint32_t next, at_seq = 0, at_tile = 0, in_seq;
+
+    __device__ __forceinline__ Source() : next(0), in_seq(0) {}
+    __device__ __forceinline__ explicit Source(const P& p) : next(atomicAdd(p.counters, 1u)), in_seq(tiles_of(p, 0)) {}
+
+    // The n-th tile of the pair, told to all that wait for it.
+    __device__ __forceinline__ void take(const P& p, Slot& s, uint32_t n, Bars* b)
+    {
+        while (at_seq < p.nseq && next - at_tile >= in_seq) {
+            at_tile += in_seq;
+            if (++at_seq < p.nseq) in_seq = tiles_of(p, at_seq);
+        }
+        if (at_seq < p.nseq) {
+            const uint32_t e = p.seq[at_seq];
+            const MuonWork& w = p.work[e & 31u];
+            s.seq = at_seq;
+            const int kind = p.op[w.op0 + (e >> 5)].kind;
+            place_of(w, kind, p.tile_n[kind], next - at_tile, &s.i, &s.j);
+        }
+        if (n < kSlots || wait_for(&b->heard[n % kSlots], ((n / kSlots) - 1) & 1, b, p.waits, p.spin)) {
+            tell(s, n, b);
+            if (s.seq != kEnd) next = atomicAdd(p.counters, 1u);  // on its way while this tile is copied
+        } else {
+            s.seq = kEnd;
+        }
+    }
+};
+
+// Copies of A's stages (IS_B 0) or B's by a warp: four blocks of 8 KB by a lane
+// each, the pairs that follow one another in memory as one copy of 16 KB.  A
+// copy takes its warp about 100 clocks to issue, so that one warp's four or
+// eight a stage took longer than the products of a tile of 128 columns.
+// Returns the stages begun.
+template <bool IS_B, class P>
+__device__ __forceinline__ uint32_t copy_tiles(const P& p, Bars* b, uint32_t ops, uint32_t rank, int lane)
+{
+    const uint32_t half = lane & 1, second = lane >> 1 & 1;  // of the pair; the low halves
+    const bool source = !IS_B && rank == 0;
+    uint32_t it = 0;
+    Source<P> from = source && lane == 0 ? Source<P>(p) : Source<P>();
+    uint32_t last = kEnd;  // the product whose earlier levels are known to be finished
+    for (uint32_t n = 0;; ++n) {
+        Slot s{kEnd, 0, 0, 0};
+        if (source) {
+            if (lane == 0) from.take(p, s, n, b);
+            share(s);
+            if (s.seq == kEnd) return it;
+        } else if (!warp_hear(s, n, b, p.waits, p.spin)) {
+            return it;
+        }
+        const Tile t = tile_at(p, s);
+        const bool wide = t.w->rows <= t.w->cols;
+        const int kind = t.op->kind;
+        const bool rows = 2 * t.i + rank < t.mt;  // else this CTA's part of the products is of no use
+        // kApply: Q X, or X Q
+        const uint32_t id = kind == kApply ? (IS_B == wide ? t.op->b : t.op->a) : IS_B ? t.op->b : t.op->a;
+        uint32_t nbj;
+        const Halves op = buffer_of(*t.w, id, &nbj);
+        const bool low = id >= kSquares;
+        const bool mn = !low && (kind == kGram ? !wide : wide);
+        // the first of this CTA's blocks along M or N, and how many there are
+        const uint32_t at = IS_B ? t.j * t.per * 2 + t.units * rank : 2 * (2 * t.i + rank);
+        const uint32_t blocks = IS_B ? t.units : rows ? 2 : 0;
+        const uint16_t* src = second ? op.lo : op.hi;
+        const uint16_t* by_row = src + block_at(at + half, 0, nbj);  // + k * 2 blocks
+        const uint16_t* by_col = src + block_at(0, at + half, nbj);  // + k / 2 * 2 nbj blocks + k % 2
+        const uint32_t to = ops + (IS_B ? 2 * kPlane : 0) + second * kPlane + half * (kPlane / 2);
+        const uint32_t kb = t.kb, limit = low ? (at >> 2) * 4 + 4 : mn ? 0 : kb;  // K's blocks that lie by rows
+        const uint64_t pair = (uint64_t)nbj * 2 * kBlkElems;
+        if (s.seq != last) {  // what the operands come from is finished
+            uint32_t fine = 1;
+            if (lane == 0 && t.op->level > 0) fine = parts_done(p.counters + 1 + t.mat, parts_before(p, t), b, p.waits, p.spin);
+            if (!__shfl_sync(kFull, fine, 0)) return it;
+            last = s.seq;
+            asm volatile("fence.proxy.async;" ::: "memory");  // it was written by ordinary stores
+        }
+        for (uint32_t k = 0; k < kb; ++k, ++it) {
+            const uint32_t st = it % kStages, use = it / kStages;
+            if (use > 0 && !warp_wait(&b->empty[st], (use - 1) & 1, b, p.waits, p.spin)) return it;
+            uint64_t* full = &b->full[st];
+            if (lane == 0)
+                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_of(full)), "r"(blocks * kPlane) : "memory");
+            __syncwarp();
+            const bool whole = k < limit && blocks == 2;  // both blocks, one after the other
+            if (lane < 4 && half < (whole ? 1 : blocks))
+                copy_block(to + st * kStageBytes,
+                           k < limit ? by_row + (uint64_t)k * 2 * kBlkElems : by_col + (k >> 1) * pair + (k & 1) * kBlkElems,
+                           whole ? kPlane : kPlane / 2, full);
+        }
+    }
+}
+
+// The second CTA, one thread: the first one learns of its copies.
+template <class P>
+__device__ __forceinline__ void report_copies(const P& p, Bars* b)
+{
+    uint32_t stages = 0;
+    Slot slot;
+    for (uint32_t n = 0; hear(slot, n, b, p.waits, p.spin); ++n) {
+        const uint32_t kb = tile_at(p, slot).kb;
+        for (uint32_t k = 0; k < kb; ++k, ++stages) {
+            const uint32_t s = stages % kStages;
+            if (!wait_for(&b->full[s], (stages / kStages) & 1, b, p.waits, p.spin)) return;
+            first_arrive(&b->other[s]);
+        }
+    }
+}
+
+// The first CTA, one thread: the products of both.
+template <class P>
+__device__ __forceinline__ void multiply(const P& p, Bars* b, uint32_t ops, uint32_t tmem)
+{
+    uint32_t stages = 0, sums = 0;
+    Slot slot;
+    for (uint32_t n = 0; hear(slot, n, b, p.waits, p.spin); ++n) {
+        const Tile t = tile_at(p, slot);
+        const bool wide = t.w->rows <= t.w->cols;
+        const int kind = t.op->kind;
+        // K's blocks that lie by rows; both CTAs' blocks lie in one tile of 256
+        const uint32_t kb = t.kb, n128 = t.units * 128;
+        const uint32_t low_a = t.i * 4 + 4, low_b = (t.j * t.per / 2) * 4 + 4;
+        const uint32_t a_rows = kind == kSquare || (kind == kApply && wide) ? low_a : kind == kGram && !wide ? 0 : kb;
+        const uint32_t b_rows = kind == kSquare || (kind == kApply && !wide) ? low_b : kind == kGram && wide ? kb : 0;
+        for (uint32_t k0 = 0; k0 < kb; k0 += kChunk, ++sums) {
+            const uint32_t acc = tmem + (sums & 1) * kTileN, k1 = min(kb, k0 + kChunk);
+            if (sums >= 2 && !wait_for(&b->taken[sums & 1], ((sums >> 1) - 1) & 1, b, p.waits, p.spin)) return;
+            for (uint32_t k = k0; k < k1; ++k, ++stages) {
+                const uint32_t s = stages % kStages, parity = (stages / kStages) & 1;
+                if (!wait_for(&b->full[s], parity, b, p.waits, p.spin)) return;
+                if (!wait_for(&b->other[s], parity, b, p.waits, p.spin)) return;
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                const uint32_t sa = ops + s * kStageBytes;
+                const bool a_mn = k >= a_rows, b_mn = k >= b_rows;
+                const uint32_t inst = instruction(n128, a_mn, b_mn);
+                const uint32_t astep = (a_mn ? 2048u : 32u) >> 4, bstep = (b_mn ? 2048u : 32u) >> 4;  // 16 of K
+                const uint64_t ah = operand(sa, a_mn), al = operand(sa + kPlane, a_mn);
+                const uint64_t bh = operand(sa + 2 * kPlane, b_mn), bl = operand(sa + 3 * kPlane, b_mn);
+#pragma unroll
+                for (uint32_t c = 0; c < kBlk / 16; ++c) mma(acc, al + c * astep, bh + c * bstep, inst, k > k0 || c > 0);
+#pragma unroll
+                for (uint32_t c = 0; c < kBlk / 16; ++c) mma(acc, ah + c * astep, bl + c * bstep, inst, true);
+#pragma unroll
+                for (uint32_t c = 0; c < kBlk / 16; ++c) mma(acc, ah + c * astep, bh + c * bstep, inst, true);
+                commit(&b->empty[s]);
+            }
+            commit(&b->ready[sums & 1]);
+        }
+    }
+}
+
+// One tile's results: a warp reads the quarter of the accumulator's rows that is
+// its own, and COLS columns, half of them.  False: a wait ran out.
+template <int COLS, class P>
+__device__ __forceinline__ bool take_tile(const P& p, Bars* b, uint32_t tmem, const OutRows& o, uint32_t rank, int warp, int lane,
+                                          const Tile& t, uint32_t& sums)
+{
+    const uint32_t quarter = warp & 3, col0 = ((warp - 4) >> 2) * COLS;
+    const uint32_t unit = 2 * t.i + rank;  // of 128 rows
+    const uint32_t row0 = unit * 128 + quarter * 32, col = t.j * t.per * 128 + col0;
+    const bool mine = unit < t.mt;
+    float sum[COLS];
+#pragma unroll
+    for (int l = 0; l < COLS; ++l) sum[l] = 0.0f;
+    for (uint32_t k0 = 0; k0 < t.kb; k0 += kChunk, ++sums) {
+        if (!warp_wait(&b->ready[sums & 1], (sums >> 1) & 1, b, p.waits, p.spin)) return false;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint32_t acc = tmem + (quarter * 32 << 16) + (sums & 1) * kTileN + col0;
+        constexpr int kAtOnce = COLS == 64 ? 2 : 1;  // as the registers allow
+#pragma unroll
+        for (int h = 0; h < COLS / 32; h += kAtOnce) {
+            uint32_t bits[kAtOnce][32];
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) load_acc(acc + (h + u) * 32, bits[u]);
+            acc_landed();
+#pragma unroll
+            for (int l = 0; l < 32 * kAtOnce; ++l) sum[h * 32 + l] += __uint_as_float(bits[l / 32][l % 32]);
+        }
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) first_arrive(&b->taken[sums & 1]);
+    }
+    if (mine) {
+        uint32_t nbj;
+        Halves out = buffer_of(*t.w, t.op->out, &nbj), c{nullptr, nullptr};
+        const uint64_t at = block_at(row0 / kBlk, col / kBlk, nbj) + row0 % kBlk * kBlk;
+        out = {out.hi + at, out.lo + at};
+        if (t.op->c != kNoBuffer) {
+            c = buffer_of(*t.w, t.op->c, &nbj);  // of out's shape
+            c = {c.hi + at, c.lo + at};
+        }
+        const uint32_t side = min(t.w->rows, t.w->cols);
+#pragma unroll
+        for (int h = 0; h < COLS / 64; ++h) {
+            float v[64];
+#pragma unroll
+            for (int l = 0; l < 64; ++l) v[l] = sum[h * 64 + l];
+            constexpr uint64_t next = 2 * kBlkElems;  // the block beside it
+            put_block(v, *t.op, {c.hi ? c.hi + h * next : nullptr, c.lo + h * next}, {out.hi + h * next, out.lo + h * next}, row0 + lane,
+                      col + h * 64, side, o, lane);
+        }
     }
     return true;
 }
 
-__global__ void __launch_bounds__(kGemmThreads, 1) muon_gemm_kernel(const __grid_constant__ MuonGemmParams p)
+template <class P>
+__device__ __forceinline__ void take_tiles(const P& p, Bars* b, uint32_t tmem, const OutRows& o, uint32_t rank, int warp, int lane)
+{
+    uint32_t sums = 0;
+    Slot slot;
+    for (uint32_t n = 0; warp_hear(slot, n, b, p.waits, p.spin); ++n) {
+        const Tile t = tile_at(p, slot);
+        if (!(t.units == 2 ? take_tile<128>(p, b, tmem, o, rank, warp, lane, t, sums)
+                           : take_tile<64>(p, b, tmem, o, rank, warp, lane, t, sums)))
+            return;
+        __syncwarp();
+        if (lane == 0)  // this part is there, of every lane's stores
+            asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p.counters + 1 + t.mat) : "memory");
+    }
+}
+
+template <int OPS, int SEQ>
+__global__ void __launch_bounds__(kGemmThreads, 1) muon_gemm_kernel(const __grid_constant__ MuonGemmParamsT<OPS, SEQ> p)
 {
     extern __shared__ uint8_t raw_smem[];
     uint8_t* base = raw_smem + ((1024u - (smem_of(raw_smem) & 1023u)) & 1023u);
-    Bars* b = reinterpret_cast<Bars*>(base + kStages * kStageBytes + kTakers * kOutBytes);
+    uint8_t* out_rows = base + kStages * kStageBytes;
+    Bars* b = reinterpret_cast<Bars*>(out_rows + kTakers * kOutBytes);
     const uint32_t ops = smem_of(base);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = blockIdx.x & 1;  // in its pair
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            bar_init(&b->full[s], 1 + p.hold);
+            bar_init(&b->full[s], 2 + p.hold);
             bar_init(&b->empty[s], 1);
             bar_init(&b->other[s], 1);
         }
@@ -322,7 +675,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1) muon_gemm_kernel(const __grid
             bar_init(&b->ready[s], 1);
             bar_init(&b->taken[s], 2 * kTakers);
         }
-        for (int k = 0; k < kTakers; ++k) bar_init(&b->added[k], 1);
+        for (int s = 0; s < kSlots; ++s) {
+            bar_init(&b->told[s], 1);
+            bar_init(&b->heard[s], kHearers);
+        }
         bar_init(&b->drained, 1);
         b->stop = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -339,158 +695,39 @@ __global__ void __launch_bounds__(kGemmThreads, 1) muon_gemm_kernel(const __grid
     const uint32_t tmem = b->tmem;
     pdl_begin();
 
-    const uint32_t first = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-    uint32_t it = 0;  // the copying warp's: stages begun
+    uint32_t begun = 0;  // stages, of a copying warp
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
         if (warp == 0) {
-                // Copies: a stage's eight blocks of 8 KB by a lane each, the pairs that
-            // follow one another in memory as one copy of 16 KB.  (One thread that
-            // worked out and issued them all took 2600 clocks a stage, which the
-            // products need for 1536.)
-            asm volatile("fence.proxy.async;" ::: "memory");  // the operands were written by ordinary stores
-            const uint32_t half = lane & 1, second = lane >> 1 & 1;  // of the pair; the low halves
-            const bool is_b = lane >> 2 & 1;
-            bool ok = true;
-            for (uint32_t w = first; w < p.tiles && ok; w += pairs) {
-                const Tile t = tile_of(p, w);
-                const MuonProduct& q = *t.q;
-                const bool rows = 2 * t.i + rank < q.mt;  // else this CTA's part of the products is of no use
-                // the first of this CTA's blocks along M or N, and how many there are
-                const uint32_t at = is_b ? t.j * (p.tile_n / kBlk) + t.units * rank : 2 * (2 * t.i + rank);
-                const uint32_t blocks = is_b ? t.units : rows ? 2 : 0;
-                const Halves& op = is_b ? q.b : q.a;
-                const uint16_t* src = second ? op.lo : op.hi;
-                const uint32_t nbj = is_b ? q.b_nbj : q.a_nbj;
-                const bool mn = is_b ? q.b_mn : q.a_mn, low = is_b ? q.b_low : q.a_low;
-                const uint16_t* by_row = src + block_at(at + half, 0, nbj);  // + k * 2 blocks
-                const uint16_t* by_col = src + block_at(0, at + half, nbj);  // + k / 2 * 2 nbj blocks + k % 2
-                const uint32_t to = ops + (is_b ? 2 * kPlane : 0) + second * kPlane + half * (kPlane / 2);
-                const uint32_t bytes = (rows ? 2 * kPlane : 0) + t.units * kPlane;
-                const uint32_t kb = q.kb, limit = low ? (at >> 2) * 4 + 4 : mn ? 0 : kb;  // K's blocks that lie by rows
-                const uint64_t pair = (uint64_t)nbj * 2 * kBlkElems;
-                for (uint32_t k = 0; k < kb; ++k, ++it) {
-                    const uint32_t s = it % kStages, use = it / kStages;
-                    if (use > 0) ok = warp_wait(&b->empty[s], (use - 1) & 1, b, p.waits, p.spin);
-                    if (!ok) break;
-                    uint64_t* full = &b->full[s];
-                    if (lane == 0)
-                        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_of(full)), "r"(bytes) : "memory");
-                    __syncwarp();
-                    const bool whole = k < limit && blocks == 2;  // both blocks, one after the other
-                    if (lane < 8 && half < (whole ? 1 : blocks))
-                        copy_block(to + s * kStageBytes, k < limit ? by_row + (uint64_t)k * 2 * kBlkElems : by_col + (k >> 1) * pair + (k & 1) * kBlkElems,
-                                   whole ? kPlane : kPlane / 2, full);
-                }
-            }
+            begun = copy_tiles<false>(p, b, ops, rank, lane);
+            __syncwarp();
+        } else if (warp == 2) {
+            begun = copy_tiles<true>(p, b, ops, rank, lane);
+            if (lane == 0) b->begun_b = begun;
             __syncwarp();
         } else if (warp == 1) {
-            if (lane == 0 && rank != 0) {  // the first CTA learns of this one's copies
-                uint32_t done = 0;
-                bool ok = true;
-                for (uint32_t w = first; w < p.tiles && ok; w += pairs) {
-                    const uint32_t kb = tile_of(p, w).q->kb;
-                    for (uint32_t k = 0; k < kb; ++k, ++done) {
-                        const uint32_t s = done % kStages;
-                        if (!(ok = wait_for(&b->full[s], (done / kStages) & 1, b, p.waits, p.spin))) break;
-                        first_arrive(&b->other[s]);
-                    }
-                }
-            } else if (lane == 0) {  // products
-                uint32_t done = 0, n = 0;  // stages, accumulators
-                bool ok = true;
-                for (uint32_t w = first; w < p.tiles && ok; w += pairs) {
-                    const Tile t = tile_of(p, w);
-                    const MuonProduct& q = *t.q;
-                    // K's blocks that lie by rows; both CTAs' blocks lie in one tile of 256
-                    const uint32_t kb = q.kb, n128 = t.units * 128;
-                    const uint32_t a_rows = q.a_low ? t.i * 4 + 4 : q.a_mn ? 0 : kb;
-                    const uint32_t b_rows = q.b_low ? (t.j * p.tile_n / 256) * 4 + 4 : q.b_mn ? 0 : kb;
-                    for (uint32_t k0 = 0; k0 < kb && ok; k0 += kChunk, ++n) {
-                        const uint32_t acc = tmem + (n & 1) * kTileN, k1 = min(kb, k0 + kChunk);
-                        if (n >= 2 && !(ok = wait_for(&b->taken[n & 1], ((n >> 1) - 1) & 1, b, p.waits, p.spin))) break;
-                        for (uint32_t k = k0; k < k1; ++k, ++done) {
-                            const uint32_t s = done % kStages, parity = (done / kStages) & 1;
-                            if (!(ok = wait_for(&b->full[s], parity, b, p.waits, p.spin) &&
-                                       wait_for(&b->other[s], parity, b, p.waits, p.spin)))
-                                break;
-                            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                            const uint32_t sa = ops + s * kStageBytes;
-                            const bool a_mn = k >= a_rows, b_mn = k >= b_rows;
-                            const uint32_t inst = instruction(n128, a_mn, b_mn);
-                            const uint32_t astep = (a_mn ? 2048u : 32u) >> 4, bstep = (b_mn ? 2048u : 32u) >> 4;
-                            const uint64_t ah = operand(sa, a_mn), al = operand(sa + kPlane, a_mn);
-                            const uint64_t bh = operand(sa + 2 * kPlane, b_mn), bl = operand(sa + 3 * kPlane, b_mn);
-    #pragma unroll
-                            for (uint32_t c = 0; c < kBlk / 16; ++c) mma(acc, al + c * astep, bh + c * bstep, inst, k > k0 || c > 0);
-#pragma unroll
-                            for (uint32_t c = 0; c < kBlk / 16; ++c) mma(acc, ah + c * astep, bl + c * bstep, inst, true);
-#pragma unroll
-                            for (uint32_t c = 0; c < kBlk / 16; ++c) mma(acc, ah + c * astep, bh + c * bstep, inst, true);
-                            commit(&b->empty[s]);
-                        }
-                        if (ok) commit(&b->ready[n & 1]);
-                    }
-                }
+            if (lane == 0) {
+                if (rank != 0) report_copies(p, b);
+                else multiply(p, b, ops, tmem);
             }
             __syncwarp();
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
-        // results: a warp reads the quarter of the accumulator's rows that is its
-        // own, and one of its units of 128 columns
-        const uint32_t quarter = warp & 3, side = (warp - 4) >> 2;
-        OutRows o{base + kStages * kStageBytes + (warp - 4) * kOutBytes, &b->added[warp - 4], 0};
-        uint32_t n = 0;
-        bool ok = true;
-        for (uint32_t w = first; w < p.tiles && ok; w += pairs) {
-            const Tile t = tile_of(p, w);
-            const MuonProduct& q = *t.q;
-            const bool mine = side < t.units;
-            float sum[128];
-#pragma unroll
-            for (int l = 0; l < 128; ++l) sum[l] = 0.0f;
-            for (uint32_t k0 = 0; k0 < q.kb && ok; k0 += kChunk, ++n) {
-                ok = warp_wait(&b->ready[n & 1], (n >> 1) & 1, b, p.waits, p.spin);
-                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                const uint32_t acc = tmem + (quarter * 32 << 16) + (n & 1) * kTileN + side * 128;
-                if (mine && ok) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t r[32];
-                        load_acc(acc + c * 32, r);
-#pragma unroll
-                        for (int l = 0; l < 32; ++l) sum[c * 32 + l] += __uint_as_float(r[l]);
-                    }
-                }
-                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-                __syncwarp();
-                if (lane == 0 && ok) first_arrive(&b->taken[n & 1]);
-            }
-            const uint32_t unit = 2 * t.i + rank;  // of 128 rows
-            if (!ok || !mine || unit >= q.mt) continue;
-            const uint32_t row0 = unit * 128 + quarter * 32, col = t.j * p.tile_n + side * 128;
-            const uint64_t at = block_at(row0 / kBlk, col / kBlk, q.o_nbj) + row0 % kBlk * kBlk;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float v[64];
-#pragma unroll
-                for (int l = 0; l < 64; ++l) v[l] = sum[h * 64 + l];
-                ok = ok && put_block(q, at + (uint64_t)h * 2 * kBlkElems, row0 + lane, col + h * 64, v, o, lane, b, p);
-            }
-        }
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-        __syncwarp();
+        take_tiles(p, b, tmem, OutRows{out_rows + (warp - 4) * kOutBytes}, rank, warp, lane);
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     if (b->stop) {  // a wait ran out: what is in flight ends before the CTA's memory goes
         if (threadIdx.x == 0) {
+            const uint32_t least = min(begun, b->begun_b);
+            begun = max(begun, b->begun_b);
+            for (uint32_t k = least; k < begun; ++k) bar_arrive(&b->full[k % kStages]);  // for the warp that got less far
             if (p.hold)
-                for (uint32_t k = 0; k < kStages && k < it; ++k) bar_arrive(&b->full[k]);
-            for (uint32_t back = 1; back <= kStages && back <= it; ++back) {
-                const uint32_t last = it - back;
+                for (uint32_t k = 0; k < kStages && k < begun; ++k) bar_arrive(&b->full[k]);
+            for (uint32_t back = 1; back <= kStages && back <= begun; ++back) {
+                const uint32_t last = begun - back;
                 bool landed = false;
                 for (uint32_t i = 0; i < p.spin && !landed; ++i)
                     landed = try_wait(smem_of(&b->full[last % kStages]), (last / kStages) & 1);
@@ -511,18 +748,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) muon_gemm_kernel(const __grid
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
-uint32_t tiles_of(const MuonProduct& q, uint32_t tile_n)
-{
-    const uint32_t per = tile_n / 128, rows = (q.mt + 1) / 2;
-    if (!q.sym) return rows * ((q.nu + per - 1) / per);
-    uint32_t t = 0;
-    for (uint32_t i = 0; i < rows; ++i) t += sym_tiles(i, q.nu, per);
-    return t;
-}
-
-}  // namespace
-
-cudaError_t launch_muon_gemm(MuonGemmParams& p, cudaStream_t s)
+template <int OPS, int SEQ>
+cudaError_t launch_as(const MuonGemmParamsT<OPS, SEQ>& p, uint32_t pairs, cudaStream_t s)
 {
     constexpr int kMaxDevices = 64;
     static std::atomic<bool> asked[kMaxDevices];
@@ -530,10 +757,45 @@ cudaError_t launch_muon_gemm(MuonGemmParams& p, cudaStream_t s)
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= kMaxDevices || !asked[dev].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(muon_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+        e = cudaFuncSetAttribute(muon_gemm_kernel<OPS, SEQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
         if (e != cudaSuccess) return e;
         if (dev < kMaxDevices) asked[dev].store(true, std::memory_order_release);
     }
+    cudaLaunchAttribute attr[2]{};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(2 * pairs);
+    cfg.blockDim = dim3(kGemmThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, muon_gemm_kernel<OPS, SEQ>, p);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// Tiles of one product of each matrix.
+uint32_t tiles_of_all(const MuonGemmParams& p, int kind, uint32_t tile_n)
+{
+    uint32_t sum = 0, seen = 0;
+    for (uint32_t k = 0; k < p.nseq; ++k) {
+        const uint32_t mat = p.seq[k] & 31u;
+        if (seen >> mat & 1u) continue;
+        seen |= 1u << mat;
+        sum += muon_tiles(p.work[mat].rows, p.work[mat].cols, kind, tile_n);
+    }
+    return sum;
+}
+
+}  // namespace
+
+cudaError_t launch_muon_gemm(MuonGemmParams& p, int nops, cudaStream_t s)
+{
+    if (p.nseq == 0) return cudaSuccess;
     RankParams rp{};
     rp.waits = bulk_wait_counters();
     if (!rp.waits) return cudaErrorSymbolNotFound;
@@ -542,30 +804,24 @@ cudaError_t launch_muon_gemm(MuonGemmParams& p, cudaStream_t s)
     p.hold = bp.hold;
     p.spin = bp.spin;
     // tiles of 256 columns where every pair of SMs has one; narrower ones are done sooner
-    for (p.tile_n = 256;; p.tile_n = 128) {
-        p.tiles = 0;
-        for (int i = 0; i < p.n; ++i) {
-            p.q[i].tile0 = p.tiles;
-            p.tiles += tiles_of(p.q[i], p.tile_n);
-        }
-        if (p.tiles >= kPairs || p.tile_n == 128) break;
+    uint32_t widest = 0;
+    for (int kind = 0; kind < 3; ++kind) {
+        p.tile_n[kind] = tiles_of_all(p, kind, 256) >= kPairs ? 256 : 128;
+        widest = std::max(widest, tiles_of_all(p, kind, p.tile_n[kind]));
     }
-    if (p.tiles == 0) return cudaSuccess;
-    cudaLaunchAttribute attr[2]{};
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 2;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(2 * std::min(p.tiles, kPairs));
-    cfg.blockDim = dim3(kGemmThreads);
-    cfg.dynamicSmemBytes = kSmem;
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, muon_gemm_kernel, p);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    const uint32_t pairs = std::min(kPairs, 2 * widest);  // two products of a matrix may run side by side
+    if (nops > kMuonOpsSmall || p.nseq > kMuonSeqSmall) return launch_as(p, pairs, s);
+    MuonGemmParamsT<kMuonOpsSmall, kMuonSeqSmall> q;
+    std::copy_n(p.work, kMuonMats, q.work);
+    std::copy_n(p.op, nops, q.op);
+    std::copy_n(p.seq, p.nseq, q.seq);
+    q.nseq = p.nseq;
+    std::copy_n(p.tile_n, 3, q.tile_n);
+    q.counters = p.counters;
+    q.waits = p.waits;
+    q.hold = p.hold;
+    q.spin = p.spin;
+    return launch_as(q, pairs, s);
 }
 
 }  // namespace rr

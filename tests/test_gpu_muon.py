@@ -204,11 +204,11 @@ def test_large_matrices():
 def test_groups_that_share_the_workspace():
     """Matrices whose workspace passes what one group takes: one after the other in the same memory."""
     from ring_all_reduce_virtual_b200 import _lib
-    shapes = [(4096, 4096)] * 6 + [(64, 64)]
+    shapes = [(4096, 4096)] * 16 + [(64, 64)]
     xs = [gradient(r, c, torch.bfloat16, seed=i) for i, (r, c) in enumerate(shapes)]
     ml = rrv.MatrixList(xs)
     ns = _lib.NewtonSchulz(2, *COEF, 1e-7)
-    assert ml._workspace(False, ns) <= (2 << 30)
+    assert ml._workspace(False, ns) <= (5 << 30)
     got = rrv.orthogonalize(ml, steps=2)
     for g, x in zip(got, xs):
         check(g, x, steps=2)
@@ -286,7 +286,7 @@ def test_refused_tensors():
             bad()
     with pytest.raises(TypeError):
         rrv.orthogonalize([x.int()])
-    for bad in (dict(steps=-1), dict(steps=65), dict(eps=0.0), dict(eps=math.nan), dict(coefficients=(math.nan, 0, 0)),
+    for bad in (dict(steps=-1), dict(steps=51), dict(eps=0.0), dict(eps=math.nan), dict(coefficients=(math.nan, 0, 0)),
                 dict(steps=40, coefficients=(3.0, 1.0, 1.0))):
         with pytest.raises(rrv.RRError):
             rrv.orthogonalize([x], **bad)
