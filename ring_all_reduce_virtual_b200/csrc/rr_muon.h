@@ -66,7 +66,8 @@ struct MuonOp {
     float alpha, beta, diag;
     uint8_t kind, a, b, c, out;  // buffers; c kNoBuffer: none.  kApply: a is Q, b is X
     uint8_t level;               // reads what its matrix's earlier levels wrote
-    uint8_t pad_[2];
+    uint8_t chunk;               // stages of 64 of K that an accumulator collects
+    uint8_t pad_;
 };
 
 struct MuonWork {

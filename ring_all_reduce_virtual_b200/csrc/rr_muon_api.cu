@@ -198,7 +198,8 @@ std::vector<int> segments_for(const Plan& plan, const rr_matrix_list_t* out, int
 // The groups of a list's matrices (those with elements), in order.
 std::vector<std::vector<int>> groups_of(const rr_matrix_list_t* l, const Plan& plan, bool weights, uint64_t* bytes)
 {
-    std::vector<std::vector<int>> groups, kinds;
+    std::vector<std::vector<int>> groups;
+    std::vector<std::pair<std::vector<int>, bool>> kinds;
     uint64_t used = 0;
     int listed = 0, ops = 0;
     *bytes = 256;
@@ -208,7 +209,8 @@ std::vector<std::vector<int>> groups_of(const rr_matrix_list_t* l, const Plan& p
         const std::vector<int> segments = segments_for(plan, l, t, weights);
         const uint64_t need = room_of(s, segments).bytes();
         const int products = products_in(segments);
-        const bool seen = std::find(kinds.begin(), kinds.end(), segments) != kinds.end();
+        const std::pair<std::vector<int>, bool> kind{segments, exactness(l, t, weights) == kExact};
+        const bool seen = std::find(kinds.begin(), kinds.end(), kind) != kinds.end();
         if (groups.empty() || groups.back().size() == kMuonMats || used + need > kGroupBytes ||
             listed + products > kMuonSeq || (!seen && ops + products > kMuonOps)) {
             groups.emplace_back();
@@ -217,8 +219,8 @@ std::vector<std::vector<int>> groups_of(const rr_matrix_list_t* l, const Plan& p
             kinds.clear();
         }
         listed += products;
-        if (std::find(kinds.begin(), kinds.end(), segments) == kinds.end()) {
-            kinds.push_back(segments);
+        if (std::find(kinds.begin(), kinds.end(), kind) == kinds.end()) {
+            kinds.push_back(kind);
             ops += products;
         }
         groups.back().push_back(t);
@@ -245,9 +247,15 @@ float shape_factor(const Shape& s, int adjust)
 
 bool on16(const void* p) { return (uintptr_t)p % 16 == 0; }
 
+// Stages of 64 of K between the roundings of a sum.  Error of five steps in
+// fp32, chunks of 1 / 2 / 4, from 128 x 128 to 8192 x 2048: 0.7e-6..2.0e-6 /
+// 1.2e-6..3.4e-6 / 1.3e-6..4.5e-6 (the same steps in plain fp32: 1.3e-6..6e-6);
+// time of 8 x 2048 x 2048, one step: 860 / 759 / 723 us.
+constexpr uint8_t kExactChunk = 1, kChunk = 4;
+
 // The products of a matrix of m <= n sides, in the order of their levels; X
 // begins in buffer 0.  *last: the result's buffer.
-std::vector<MuonOp> products_of(const Plan& plan, const std::vector<int>& segments, int* last)
+std::vector<MuonOp> products_of(const Plan& plan, const std::vector<int>& segments, bool exact, int* last)
 {
     std::vector<MuonOp> ops;
     const uint8_t A = kSquares, Y = kSquares + 1, D = kSquares + 2;
@@ -261,6 +269,7 @@ std::vector<MuonOp> products_of(const Plan& plan, const std::vector<int>& segmen
         q.c = kNoBuffer;
         q.out = out;
         q.level = (uint8_t)at;
+        q.chunk = exact ? kExactChunk : kChunk;
         q.alpha = (float)alpha;
         ops.push_back(q);
         return ops.back();
@@ -322,7 +331,8 @@ rr_status_t run_group(const Job& job, const Plan& plan, const std::vector<int>& 
     std::unique_ptr<MuonPrepParams> prep(new MuonPrepParams{});
     std::unique_ptr<MuonGemmParams> gemm(new MuonGemmParams);  // as it comes: every field that counts is set
     std::vector<Halves> result(n);
-    std::vector<std::pair<std::vector<int>, std::pair<int, int>>> known;  // segments: first product, result's buffer
+    using Kind = std::pair<std::vector<int>, bool>;  // segments, exactly or not
+    std::vector<std::pair<Kind, std::pair<int, int>>> known;  // first product, result's buffer
     int nops = 0;
     uint64_t at = kHeadBytes;
     const auto take = [&](uint64_t bytes) {
@@ -344,12 +354,13 @@ rr_status_t run_group(const Job& job, const Plan& plan, const std::vector<int>& 
         const Shape s = shape[k] = {(uint32_t)job.in->rows[t], (uint32_t)job.in->cols[t]};
         const std::vector<int> segments = segments_for(plan, job.out, t, job.mom != nullptr);
         const Room room = room_of(s, segments);
-        auto same = std::find_if(known.begin(), known.end(), [&](const auto& e) { return e.first == segments; });
+        const Kind kind{segments, exactness(job.out, t, job.mom != nullptr) == kExact};
+        auto same = std::find_if(known.begin(), known.end(), [&](const auto& e) { return e.first == kind; });
         if (same == known.end()) {
             int last = 0;
-            const std::vector<MuonOp> ops = products_of(plan, segments, &last);
+            const std::vector<MuonOp> ops = products_of(plan, segments, kind.second, &last);
             std::copy(ops.begin(), ops.end(), gemm->op + nops);
-            known.push_back({segments, {nops, last}});
+            known.push_back({kind, {nops, last}});
             same = known.end() - 1;
             nops += (int)ops.size();
         }

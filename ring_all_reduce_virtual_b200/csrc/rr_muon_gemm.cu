@@ -14,7 +14,7 @@
 //
 // The tensor cores' sums are cut off, not rounded: a long one comes out low by
 // 2^-25 and more a term (a sum of 8192 positive products by 1.5e-5).  So an
-// accumulator collects kChunk stages only; the eight warps add it to sums in
+// accumulator collects a few stages only (MuonOp::chunk); the eight warps add it to sums in
 // their registers, rounded to nearest, while the other accumulator fills.
 //
 // A pair takes the next tile of the list from a counter, and begins it once its
@@ -48,7 +48,6 @@ namespace {
 
 constexpr int kStages = 3;
 constexpr uint32_t kPairs = 74;                // pairs of SMs
-constexpr uint32_t kChunk = 4;                 // stages an accumulator collects
 constexpr uint32_t kTileN = 256;
 constexpr uint32_t kPlane = 128 * kBlk * 2;    // one half of 128 rows (or columns) of an operand's stage
 constexpr uint32_t kStageBytes = 4 * kPlane;   // A's hi and lo, B's hi and lo
@@ -197,7 +196,7 @@ __device__ __forceinline__ void place_of(const MuonWork& w, int kind, uint32_t t
 struct Tile {
     const MuonWork* w;
     const MuonOp* op;
-    uint32_t i, j, per, units, mt, kb, mat;  // per: units of 128 columns of a whole tile
+    uint32_t i, j, per, units, mt, kb, chunk, mat;  // per: units of 128 columns of a whole tile
 };
 
 template <class P>
@@ -215,6 +214,7 @@ __device__ __forceinline__ Tile tile_at(const P& p, const Slot& s)
     t.units = min(t.per, sides.nu - s.j * t.per);
     t.mt = sides.mt;
     t.kb = depth_of(*t.w, t.op->kind);
+    t.chunk = t.op->chunk;
     return t;
 }
 
@@ -558,8 +558,8 @@ __device__ __forceinline__ void multiply(const P& p, Bars* b, uint32_t ops, uint
         const uint32_t low_a = t.i * 4 + 4, low_b = (t.j * t.per / 2) * 4 + 4;
         const uint32_t a_rows = kind == kSquare || (kind == kApply && wide) ? low_a : kind == kGram && !wide ? 0 : kb;
         const uint32_t b_rows = kind == kSquare || (kind == kApply && !wide) ? low_b : kind == kGram && wide ? kb : 0;
-        for (uint32_t k0 = 0; k0 < kb; k0 += kChunk, ++sums) {
-            const uint32_t acc = tmem + (sums & 1) * kTileN, k1 = min(kb, k0 + kChunk);
+        for (uint32_t k0 = 0; k0 < kb; k0 += t.chunk, ++sums) {
+            const uint32_t acc = tmem + (sums & 1) * kTileN, k1 = min(kb, k0 + t.chunk);
             if (sums >= 2 && !wait_for(&b->taken[sums & 1], ((sums >> 1) - 1) & 1, b, p.waits, p.spin)) return;
             for (uint32_t k = k0; k < k1; ++k, ++stages) {
                 const uint32_t s = stages % kStages, parity = (stages / kStages) & 1;
@@ -598,7 +598,7 @@ __device__ __forceinline__ bool take_tile(const P& p, Bars* b, uint32_t tmem, co
     float sum[COLS];
 #pragma unroll
     for (int l = 0; l < COLS; ++l) sum[l] = 0.0f;
-    for (uint32_t k0 = 0; k0 < t.kb; k0 += kChunk, ++sums) {
+    for (uint32_t k0 = 0; k0 < t.kb; k0 += t.chunk, ++sums) {
         if (!warp_wait(&b->ready[sums & 1], (sums >> 1) & 1, b, p.waits, p.spin)) return false;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         const uint32_t acc = tmem + (quarter * 32 << 16) + (sums & 1) * kTileN + col0;
