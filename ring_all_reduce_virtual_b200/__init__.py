@@ -37,15 +37,21 @@ PHASES = {"reduce_scatter": 0, "all_gather": 1}
 _DTYPE_NAMES = {"f32": 0, "bf16": 1, "i32": 2, "f16": 3}
 
 
-def _dtype_code(dtype) -> int:
-    import torch
+_dtype_codes: dict = {}  # code by torch dtype, at first use
 
-    codes = {torch.float32: 0, torch.bfloat16: 1, torch.int32: 2, torch.float16: 3}
+
+def _dtype_code(dtype) -> int:
+    code = _dtype_codes.get(dtype)
+    if code is not None:
+        return code
     if isinstance(dtype, str):
         return _DTYPE_NAMES[dtype]
-    if dtype not in codes:
+    import torch
+
+    _dtype_codes.update({torch.float32: 0, torch.bfloat16: 1, torch.int32: 2, torch.float16: 3})
+    if dtype not in _dtype_codes:
         raise TypeError(f"unsupported dtype {dtype}; use float32, bfloat16, float16 or int32")
-    return codes[dtype]
+    return _dtype_codes[dtype]
 
 
 def _ptr_array(tensors: Sequence) -> ctypes.Array:
@@ -430,16 +436,26 @@ def _id_set(tokens, what: str):
         raise ValueError(f"{what}: need 1..{MAX_RANKS} token tensors, got {n}")
     t0 = tokens[0]
     dtype, count, device = t0.dtype, t0.numel(), t0.device
-    id_type = _ID_TYPES.get(str(dtype))
+    id_type = _ID_TYPES.get(dtype) if _ID_TYPES else _id_types().get(dtype)
     if id_type is None:
         raise TypeError(f"{what}: token ids must be int32 or int64")
-    for t in tokens:
-        if not t.is_cuda or not t.is_contiguous() or t.dtype != dtype or t.numel() != count or t.device != device:
+    arr = (ctypes.c_void_p * n)()
+    for i, t in enumerate(tokens):
+        if (not t.is_cuda or not t.is_contiguous()
+                or t is not t0 and (t.dtype != dtype or t.numel() != count or t.device != device)):
             raise ValueError(f"{what}: token tensors must be contiguous CUDA tensors alike")
-    return _ptr_array(tokens), id_type, n, count, device
+        arr[i] = t.data_ptr()
+    return arr, id_type, n, count, device
 
 
-_ID_TYPES = {"torch.int32": 0, "torch.int64": 1}
+_ID_TYPES: dict = {}  # id type by dtype, at first use
+
+
+def _id_types() -> dict:
+    import torch
+
+    _ID_TYPES.update({torch.int32: 0, torch.int64: 1})
+    return _ID_TYPES
 
 
 def _row_set(tensors, what: str):
@@ -546,13 +562,16 @@ def _logit_set(tensors, what: str):
         raise ValueError(f"{what}: logits need two axes or more, the last not empty")
     V = shape[-1]
     rows = t0.numel() // V
-    stride = V if t0.is_contiguous() else t0.stride(0) if len(shape) == 2 and t0.stride(1) == 1 and rows > 1 else 0
-    for t in tensors:
-        if not t.is_cuda or t.shape != shape or t.dtype != dtype or t.device != device:
+    packed = t0.is_contiguous()
+    stride = V if packed else t0.stride(0) if len(shape) == 2 and t0.stride(1) == 1 and rows > 1 else 0
+    arr = (ctypes.c_void_p * n)()
+    for i, t in enumerate(tensors):
+        if not t.is_cuda or t is not t0 and (t.shape != shape or t.dtype != dtype or t.device != device):
             raise ValueError(f"{what}: logit tensors must be CUDA tensors of one shape, dtype and device")
-        if stride < V or not (t.is_contiguous() if stride == V else t.stride() == (stride, 1)):
+        if stride < V or (not t.is_contiguous() if packed else t.stride() != (stride, 1)):
             raise ValueError(f"{what}: logits must be contiguous, or 2-D with contiguous rows and one row stride")
-    return _ptr_array(tensors), n, rows, V, stride, _dtype_code(dtype), device
+        arr[i] = t.data_ptr()
+    return arr, n, rows, V, stride, _dtype_code(dtype), device
 
 
 def token_logprobs(logits, tokens, scale: float = 1.0, entropy: bool = False, top_k: int = 0, stream=None) -> TokenLogprobs:
@@ -562,7 +581,8 @@ def token_logprobs(logits, tokens, scale: float = 1.0, entropy: bool = False, to
     float16; any row stride); ``tokens``: one int32 or int64 tensor per rank, or
     a RankSet.  A token outside the vocabulary (padding) has log probability 0.
     ``entropy`` adds each row's entropy, ``top_k`` (up to 32) its most likely
-    ids, equal logits with the lowest id first, and their log probabilities."""
+    ids, equal logits with the lowest id first, and their log probabilities.
+    The values of a call share one storage, its top ids another."""
     ids, id_type, n, T, dev = _id_set(tokens, "token_logprobs")
     x, xn, rows, V, stride, d, xdev = _logit_set(logits, "token_logprobs")
     if xn != n or rows != T or xdev != dev:
@@ -571,24 +591,36 @@ def token_logprobs(logits, tokens, scale: float = 1.0, entropy: bool = False, to
     if not 0 <= k <= min(32, V):
         raise ValueError("token_logprobs: top_k must be in 0..32 and at most the vocabulary")
     torch, raw, current = _calls()
-    with contextlib.nullcontext() if stream is None and dev.index == current() else _placed(stream, dev):
-        def empty(*shape, dtype=torch.float32):
-            return torch.empty(shape, dtype=dtype, device=dev)
-        out = TokenLogprobs(empty(n, T), empty(n, T), empty(n, T) if entropy else None,
-                            empty(n, T, k, dtype=torch.int32) if k else None, empty(n, T, k) if k else None)
-        ptrs = [t.data_ptr() if t is not None else None for t in out]
-        st = lib().rr_token_logprobs(x, stride, ids, id_type, n, T, V, d, float(scale), *ptrs[:3], k, ptrs[4], ptrs[3],
-                                     raw(dev.index))
-        if st:
-            check(st, "token_logprobs")
-    return out
+    index = dev.index
+    if stream is not None or index != current():
+        with _placed(stream, dev):
+            return token_logprobs(logits, tokens, scale, entropy, top_k)
+    # one allocation for the values: each costs a microsecond, a small call's kernel ten
+    M = n * T
+    count = 3 if entropy else 2
+    values = torch.empty_strided((count, n, T), (M, T, 1), dtype=torch.float32, device=dev)
+    at = values.data_ptr()
+    ent = at + 8 * M if entropy else None
+    if k:
+        shape, strides = (n, T, k), (T * k, k, 1)
+        tops = torch.empty_strided(shape, strides, dtype=torch.float32, device=dev)
+        ids_out = torch.empty_strided(shape, strides, dtype=torch.int32, device=dev)
+        st = lib().rr_token_logprobs(x, stride, ids, id_type, n, T, V, d, float(scale), at, at + 4 * M, ent, k, tops.data_ptr(),
+                                     ids_out.data_ptr(), raw(index))
+    else:
+        tops = ids_out = None
+        st = lib().rr_token_logprobs(x, stride, ids, id_type, n, T, V, d, float(scale), at, at + 4 * M, ent, 0, None, None, raw(index))
+    if st:
+        check(st, "token_logprobs")
+    out = values.unbind(0)
+    return TokenLogprobs(out[0], out[1], out[2] if entropy else None, ids_out, tops)
 
 
-def _row_values(t, n: int, T: int, dev, what: str):
+def _row_values(t, count: int, dev, what: str):
     """Pointer of one float32 value per row of every rank; None for None."""
     if t is None:
         return None
-    if not t.is_cuda or not t.is_contiguous() or str(t.dtype) != "torch.float32" or t.numel() != n * T or t.device != dev:
+    if not t.is_cuda or _dtype_codes.get(t.dtype) != 0 or t.numel() != count or not t.is_contiguous() or t.device != dev:
         raise ValueError(f"token_logprobs_grad: {what} must be a contiguous float32 tensor [ranks, tokens] on the tokens' device")
     return t.data_ptr()
 
@@ -606,23 +638,29 @@ def token_logprobs_grad(logits, tokens, lse, dlogprob, entropy=None, dentropy=No
     x, xn, rows, V, stride, d, xdev = _logit_set(logits, "token_logprobs_grad")
     if xn != n or rows != T or xdev != dev:
         raise ValueError("token_logprobs_grad: need one logit tensor [tokens, V] per rank, on the tokens' device")
-    if dentropy is not None and entropy is None:
-        raise ValueError("token_logprobs_grad: the entropy's gradient needs the entropy")
-    values = [_row_values(t, n, T, dev, what) for t, what in
-              ((lse, "lse"), (entropy if dentropy is not None else None, "entropy"), (dlogprob, "dlogprob"), (dentropy, "dentropy"))]
     if lse is None or dlogprob is None:
         raise ValueError("token_logprobs_grad: lse and dlogprob are needed")
+    if dentropy is None:
+        entropy = None
+    elif entropy is None:
+        raise ValueError("token_logprobs_grad: the entropy's gradient needs the entropy")
     torch, raw, current = _calls()
-    with contextlib.nullcontext() if stream is None and dev.index == current() else _placed(stream, dev):
-        if outs is None:
-            ranks = logits.tensors if isinstance(logits, RankSet) else logits
-            outs = [torch.empty(t.shape, dtype=t.dtype, device=dev) for t in ranks]
-        o, on, orows, oV, ostride, od, odev = _logit_set(outs, "token_logprobs_grad")
-        if on != n or orows != T or oV != V or od != d or odev != dev:
-            raise ValueError("token_logprobs_grad: need one gradient tensor per rank, like its logits")
-        st = lib().rr_token_logprobs_grad(x, stride, ids, id_type, n, T, V, d, float(scale), *values, o, ostride, raw(dev.index))
-        if st:
-            check(st, "token_logprobs_grad")
+    index = dev.index
+    if stream is not None or index != current():
+        with _placed(stream, dev):
+            return token_logprobs_grad(logits, tokens, lse, dlogprob, entropy, dentropy, scale, outs)
+    if outs is None:
+        ranks = logits.tensors if isinstance(logits, RankSet) else logits
+        outs = [torch.empty(t.shape, dtype=t.dtype, device=dev) for t in ranks]
+    o, on, orows, oV, ostride, od, odev = _logit_set(outs, "token_logprobs_grad")
+    if on != n or orows != T or oV != V or od != d or odev != dev:
+        raise ValueError("token_logprobs_grad: need one gradient tensor per rank, like its logits")
+    M = n * T
+    st = lib().rr_token_logprobs_grad(x, stride, ids, id_type, n, T, V, d, float(scale), _row_values(lse, M, dev, "lse"),
+                                      _row_values(entropy, M, dev, "entropy"), _row_values(dlogprob, M, dev, "dlogprob"),
+                                      _row_values(dentropy, M, dev, "dentropy"), o, ostride, raw(index))
+    if st:
+        check(st, "token_logprobs_grad")
     return outs
 
 

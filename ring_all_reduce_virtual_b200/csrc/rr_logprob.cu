@@ -6,22 +6,23 @@
 //     t = sum e^y_j y_j   entropy = ln s - t / s
 // in one pass over the row: a thread keeps the running maximum of what it has
 // read with s and t relative to it, and rescales them when the maximum grows
-// (t / s shifts by the difference).  x_j - m is exact in sign and 0 at the
-// maximum, so a row whose every value is the type's lowest is uniform, as it
-// should be.  Exponentials are powers of two (y in units of ln 2).
+// (t / s shifts by the difference).  x_j - m is 0 at the maximum, so a row with
+// one value left has the log probability 0 exactly, and a row whose every value
+// is the type's lowest is uniform, as it should be.  Exponentials are powers of
+// two (y in units of ln 2).
 //
 // Bound by HBM: 2 or 4 bytes an element against about 5 issue slots (packed
 // fp32 pairs: one subtraction, one product, one sum) and one exponential, of
 // which an SM does 16 a clock -- bf16 logits at full bandwidth need 12.
 //
 // The top alternatives cost the pass nothing but the maxima it has anyway.  A
-// thread's maximum is an element of its own, so at least k elements are at or
-// above tau, the k-th largest of the threads' maxima, and every element that
-// is at or above tau belongs to a thread whose maximum is: k threads of 256
-// (more on ties).  Their elements alone are read once more, from L2, and go
-// through a sorted list of 32 per warp; the lists are merged.  Elements are
-// ordered by (value, lowest id first), so the outcome does not depend on who
-// saw them first.
+// thread's maximum is an element of its own.  With tau the smallest of the
+// eight warps' ceil(k / 8)-th largest maxima, at least k elements are at or
+// above tau, and every element that is belongs to a thread whose maximum is:
+// 20 to 40 threads of 256 for k up to 20 (more on ties).  Their elements alone
+// are read once more, from L2, and go through a sorted list of 32 per warp; the
+// lists are merged.  Elements are ordered by (value, lowest id first), so the
+// outcome does not depend on who saw them first.
 #include <type_traits>
 
 #include "rr_device.cuh"
@@ -123,52 +124,41 @@ __device__ __forceinline__ int64_t id_at(const void* ids, int ids64, uint64_t t)
     return ids64 ? static_cast<const int64_t*>(ids)[t] : (int64_t)static_cast<const int32_t*>(ids)[t];
 }
 
+// A whole number that orders fp32 values, NaN above all, both zeros alike.
+__device__ __forceinline__ uint32_t order_of(float x)
+{
+    if (x != x) return 0xffffffffu;
+    const uint32_t u = __float_as_uint(x + 0.0f);
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+__device__ __forceinline__ float value_of(uint32_t order)
+{
+    return __uint_as_float(order & 0x80000000u ? order & 0x7fffffffu : ~order);  // NaN's order gives a NaN
+}
+
 // ------------------------------------------------------- softmax statistics
 
-// The statistics of some elements: their maximum, and relative to it the sums
-// s of 2^y and t of 2^y y.
-struct Stat {
-    float m, s, t;
-};
-
-// a and b together.  c = scale * log2 e.
-__device__ __forceinline__ Stat joined(const Stat& a, const Stat& b, float c)
-{
-    Stat r;
-    r.m = max_nan(a.m, b.m);
-    const float ref = r.m == -INFINITY ? 0.0f : r.m;
-    // no element at all, or none above -inf: its sums are zeros, and 2^-2000 is
-    const float da = fmaxf((a.m - ref) * c, -2000.0f), db = fmaxf((b.m - ref) * c, -2000.0f);
-    const float fa = ex2(da), fb = ex2(db);
-    r.s = a.s * fa + b.s * fb;
-    r.t = (a.t + da * a.s) * fa + (b.t + db * b.s) * fb;
-    if (r.m != r.m || r.m == INFINITY) r.s = r.t = NAN;  // fmaxf drops the NaN of inf - inf
-    return r;
-}
-
-template <bool ENT>
-__device__ __forceinline__ void add_one(Stat& st, float x, float c)
-{
-    const Stat one{x, x == -INFINITY ? 0.0f : 1.0f, 0.0f};
-    st = joined(st, one, c);
-}
-
-// The running statistics of a thread's vectors.
+// A thread's sums relative to the largest value m that it has read: s of 2^y, t
+// of 2^y y, y = (x - m) c with c = scale log2 e.  y is 0 at the maximum and never
+// above, also for rows of the type's lowest value.
 template <class Ty, bool ENT>
 struct Running {
     float m = -INFINITY;
     F2 s = f2(0.0f, 0.0f), t = f2(0.0f, 0.0f);
 
+    // Relative to a larger value.  -inf - -inf counts as -2000: no sums are there.
+    __device__ __forceinline__ void move(float to, float c)
+    {
+        const float d = fmaxf((m - to) * c, -2000.0f), f = ex2(d);
+        if (ENT) t = mul2(fma2(s, f2(d, d), t), f2(f, f));
+        s = mul2(s, f2(f, f));
+        m = to;
+    }
     __device__ __forceinline__ void take(const uint4 (&raw)[kU], float c)
     {
         const float b = max_of<Ty, kU>(raw);
-        if (!(b <= m)) {  // NaN comes in here too
-            const float now = max_nan(m, b);
-            const float d = fmaxf((m - now) * c, -2000.0f), f = ex2(d);
-            if (ENT) t = mul2(fma2(s, f2(d, d), t), f2(f, f));
-            s = mul2(s, f2(f, f));
-            m = now;
-        }
+        if (!(b <= m)) move(max_nan(m, b), c);  // NaN comes in here too
         const float ref = m == -INFINITY ? 0.0f : m;
         const F2 neg = f2(-ref, -ref), cc = f2(c, c);
 #pragma unroll
@@ -185,41 +175,38 @@ struct Running {
             }
         }
     }
-    __device__ __forceinline__ Stat stat() const
+    __device__ __forceinline__ void take_one(float x, float c)
     {
-        float a, b, x, y;
-        un2(s, a, b);
-        un2(t, x, y);
-        Stat r{m, a + b, x + y};
-        if (m != m || m == INFINITY) r.s = r.t = NAN;
-        return r;
+        if (!(x <= m)) move(max_nan(m, x), c);
+        const float y = x == -INFINITY ? -2000.0f : (x - m) * c, e = ex2(y);
+        s = add2(s, f2(e, 0.0f));
+        if (ENT) t = add2(t, f2(e * fmaxf(y, -2000.0f), 0.0f));
     }
 };
 
-__device__ __forceinline__ Stat warp_joined(Stat st, float c)
+template <int N>
+__device__ __forceinline__ float lanes_sum(float v)
 {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const Stat other{__shfl_xor_sync(kFull, st.m, o), __shfl_xor_sync(kFull, st.s, o), __shfl_xor_sync(kFull, st.t, o)};
-        st = joined(st, other, c);
-    }
-    return st;
+    for (int o = N / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    return v;
+}
+
+// The sums of some threads relative to their largest value.
+struct Stat {
+    uint32_t order;  // of that value
+    float s, t;
+};
+
+// Of N neighbouring lanes' Stats; o: the largest order.
+template <int N>
+__device__ __forceinline__ Stat lanes_joined(const Stat& st, uint32_t o, float c)
+{
+    const float d = st.order ? fmaxf((value_of(st.order) - value_of(o)) * c, -2000.0f) : -2000.0f, f = ex2(d);
+    return {o, lanes_sum<N>(st.s * f), lanes_sum<N>((st.t + d * st.s) * f)};
 }
 
 // --------------------------------------------------------- top alternatives
-
-// A whole number that orders fp32 values, NaN above all, both zeros alike.
-__device__ __forceinline__ uint32_t order_of(float x)
-{
-    if (x != x) return 0xffffffffu;
-    const uint32_t u = __float_as_uint(x + 0.0f);
-    return u & 0x80000000u ? ~u : u | 0x80000000u;
-}
-
-__device__ __forceinline__ float value_of(uint32_t order)
-{
-    return __uint_as_float(order & 0x80000000u ? order & 0x7fffffffu : ~order);  // NaN's order gives a NaN
-}
 
 // An element's rank among all: the value above, the lowest id first.  0: none.
 __device__ __forceinline__ uint64_t entry_of(uint32_t order, uint32_t id) { return (uint64_t)order << 32 | (uint32_t)~id; }
@@ -297,12 +284,11 @@ __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }      // acquire
 
 struct Shared {
-    Stat part[kThreads / 32];
-    uint32_t order[kThreads / 32][32];
+    uint32_t order[kThreads / 32], tau[kThreads / 32];
+    float2 sums[kThreads / 32];
     uint64_t list[kThreads / 32][32];
     uint8_t who[kThreads];
-    uint32_t count[kThreads / 32 + 1];
-    uint32_t tau;
+    uint32_t count[kThreads / 32];
     Stat all[kMaxSplit];               // cluster rank 0: of every CTA of the row
     uint64_t lists[kMaxSplit][32];
 };
@@ -346,43 +332,48 @@ __global__ void __launch_bounds__(kThreads) logprob_kernel(const __grid_constant
         }
         run.take(raw, c);
     }
-    const float mine = run.m;
-    Stat st = run.stat();
+    const uint32_t order = v0 + tid < v1 ? order_of(run.m) : 0u;  // 0: a thread without vectors
     const bool edge = part == 0 && (uint32_t)tid < head + tail;
     const uint32_t edge_id = (uint32_t)tid < head ? (uint32_t)tid : head + nv * L + ((uint32_t)tid - head);
     float edge_x = -INFINITY;
     if (edge) {
         edge_x = Ty::ld1(x + edge_id);
-        add_one<ENT>(st, edge_x, c);
+        run.take_one(edge_x, c);
     }
 
-    st = warp_joined(st, c);
+    // the team's largest value, then its sums relative to that
+    Stat st;
+    st.order = __reduce_max_sync(kFull, edge || order ? order_of(run.m) : 0u);
+    uint32_t tau = 0;
+    if constexpr (TOP) tau = __shfl_sync(kFull, warp_sorted(order), kWarp ? p.k - 1 : (p.k - 1) / (kThreads / 32));
     if constexpr (!kWarp) {
-        if (lane == 0) sh.part[warp] = st;
+        if (lane == 0) {
+            sh.order[warp] = st.order;
+            sh.tau[warp] = tau;
+        }
         __syncthreads();
-        st = sh.part[0];
-#pragma unroll
-        for (int w = 1; w < kThreads / 32; ++w) st = joined(st, sh.part[w], c);
+        st.order = __reduce_max_sync(kFull, sh.order[lane % (kThreads / 32)]);
+        if constexpr (TOP) tau = __reduce_min_sync(kFull, sh.tau[lane % (kThreads / 32)]);
+    }
+    run.move(value_of(st.order), c);
+    float a, b;
+    un2(run.s, a, b);
+    st.s = lanes_sum<32>(a + b);
+    st.t = 0.0f;
+    if constexpr (ENT) {
+        un2(run.t, a, b);
+        st.t = lanes_sum<32>(a + b);
+    }
+    if constexpr (!kWarp) {
+        if (lane == 0) sh.sums[warp] = make_float2(st.s, st.t);
+        __syncthreads();
+        const float2 of_warp = sh.sums[lane % (kThreads / 32)];
+        st.s = lanes_sum<kThreads / 32>(of_warp.x);
+        if constexpr (ENT) st.t = lanes_sum<kThreads / 32>(of_warp.y);
     }
 
     uint64_t best = 0;  // lane i of the team's first warp: the i-th largest entry
     if constexpr (TOP) {
-        uint32_t order = v0 + tid < v1 ? order_of(mine) : 0u;  // 0: a thread without elements
-        const uint32_t sorted = warp_sorted(order);
-        uint32_t tau;
-        if constexpr (kWarp) {
-            tau = __shfl_sync(kFull, sorted, p.k - 1);
-        } else {
-            sh.order[warp][lane] = sorted;
-            __syncthreads();
-            if (warp == 0) {
-                uint32_t top = sorted;
-                for (int w = 1; w < kThreads / 32; ++w) top = warp_merged(top, sh.order[w][lane]);
-                if (lane == p.k - 1) sh.tau = top;
-            }
-            __syncthreads();
-            tau = sh.tau;
-        }
         TopList list;
         // the head's and the tail's elements first
         if (warp == 0 || kWarp) list.offer(edge ? entry_of(order_of(edge_x), edge_id) : 0, p.k);
@@ -434,9 +425,14 @@ __global__ void __launch_bounds__(kThreads) logprob_kernel(const __grid_constant
         best = list.mine;
         if constexpr (!kWarp) {
             sh.list[warp][lane] = best;
-            __syncthreads();
-            if (warp == 0)
-                for (int w = 1; w < kThreads / 32; ++w) best = warp_merged(best, sh.list[w][lane]);
+#pragma unroll
+            for (int n = kThreads / 64; n > 0; n /= 2) {  // half of the lists into the other half
+                __syncthreads();
+                if (warp < n && sh.list[warp + n][0] != 0) {
+                    best = warp_merged(best, sh.list[warp + n][lane]);
+                    sh.list[warp][lane] = best;
+                }
+            }
         }
     }
 
@@ -447,30 +443,32 @@ __global__ void __launch_bounds__(kThreads) logprob_kernel(const __grid_constant
         cluster_arrive();
         cluster_wait();
         if (part != 0) return;
-        st = sh.all[0];
-        for (uint32_t q = 1; q < split; ++q) st = joined(st, sh.all[q], c);
-        if (TOP && warp == 0)
-            for (uint32_t q = 1; q < split; ++q) best = warp_merged(best, sh.lists[q][lane]);
+        if (warp != 0) return;
+        st = lane % kMaxSplit < split ? sh.all[lane % kMaxSplit] : Stat{0u, 0.0f, 0.0f};
+        st = lanes_joined<kMaxSplit>(st, __reduce_max_sync(kFull, st.order), c);
+        if (TOP)
+            for (uint32_t q = 1; q < split; ++q)
+                if (sh.lists[q][0] > __shfl_sync(kFull, best, p.k - 1)) best = warp_merged(best, sh.lists[q][lane]);
     }
     if (!kWarp && warp != 0) return;
 
     // the row's results; a row whose every scaled value is -inf has no
     // distribution: lse and its log probabilities are -inf, its entropy 0.  One
     // whose largest is +inf, or with a NaN, is NaN.
-    const float peak = st.m * p.scale;
+    const float top = value_of(st.order), peak = top * p.scale;
     const bool empty = peak == -INFINITY;
     const float ln_s = peak == INFINITY ? NAN : logf(st.s);
     if (lane == 0) {
         const int64_t id = id_at(p.ids[r], p.ids64, tok);
         float lp = 0.0f;
-        if (id >= 0 && id < (int64_t)p.V) lp = empty ? -INFINITY : (Ty::ld1(x + id) - st.m) * p.scale - ln_s;
+        if (id >= 0 && id < (int64_t)p.V) lp = empty ? -INFINITY : (Ty::ld1(x + id) - top) * p.scale - ln_s;
         p.logprob[row] = lp;
-        p.lse[row] = empty ? -INFINITY : __fmaf_rn(st.m, p.scale, ln_s);
+        p.lse[row] = empty ? -INFINITY : __fmaf_rn(top, p.scale, ln_s);
         if (ENT) p.entropy[row] = empty ? 0.0f : ln_s - kLn2 * (st.t / st.s);
     }
     if (TOP && lane < p.k) {
         const float v = value_of((uint32_t)(best >> 32));
-        p.top_logprob[row * p.k + lane] = empty ? -INFINITY : (v - st.m) * p.scale - ln_s;
+        p.top_logprob[row * p.k + lane] = empty ? -INFINITY : (v - top) * p.scale - ln_s;
         p.top_id[row * p.k + lane] = (int32_t)~(uint32_t)best;
     }
 }
