@@ -16,13 +16,13 @@
 // which an SM does 16 a clock -- bf16 logits at full bandwidth need 12.
 //
 // The top alternatives cost the pass nothing but the maxima it has anyway.  A
-// thread's maximum is an element of its own.  With tau the smallest of the
-// eight warps' ceil(k / 8)-th largest maxima, at least k elements are at or
-// above tau, and every element that is belongs to a thread whose maximum is:
-// 20 to 40 threads of 256 for k up to 20 (more on ties).  Their elements alone
-// are read once more, from L2, and go through a sorted list of 32 per warp; the
-// lists are merged.  Elements are ordered by (value, lowest id first), so the
-// outcome does not depend on who saw them first.
+// thread's maximum is an element of its own.  With tau the k-th largest of the
+// eight warps' four largest maxima each, at least k elements are at or above
+// tau, and every element that is belongs to a thread whose maximum is: a few
+// more than k threads of 256 (more on ties).  Their elements alone are read
+// once more, from L2, and go through a sorted list of 32 per warp; the lists are
+// merged.  Elements are ordered by (value, lowest id first), so the outcome does
+// not depend on who saw them first.
 #include <type_traits>
 
 #include "rr_device.cuh"
@@ -284,7 +284,7 @@ __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }      // acquire
 
 struct Shared {
-    uint32_t order[kThreads / 32], tau[kThreads / 32];
+    uint32_t order[kThreads / 32], best[32];
     float2 sums[kThreads / 32];
     uint64_t list[kThreads / 32][32];
     uint8_t who[kThreads];
@@ -345,16 +345,16 @@ __global__ void __launch_bounds__(kThreads) logprob_kernel(const __grid_constant
     Stat st;
     st.order = __reduce_max_sync(kFull, edge || order ? order_of(run.m) : 0u);
     uint32_t tau = 0;
-    if constexpr (TOP) tau = __shfl_sync(kFull, warp_sorted(order), kWarp ? p.k - 1 : (p.k - 1) / (kThreads / 32));
+    if constexpr (TOP) tau = warp_sorted(order);
     if constexpr (!kWarp) {
-        if (lane == 0) {
-            sh.order[warp] = st.order;
-            sh.tau[warp] = tau;
-        }
+        constexpr int kBest = 32 / (kThreads / 32);
+        if (lane == 0) sh.order[warp] = st.order;
+        if (TOP && lane < kBest) sh.best[warp * kBest + lane] = tau;
         __syncthreads();
         st.order = __reduce_max_sync(kFull, sh.order[lane % (kThreads / 32)]);
-        if constexpr (TOP) tau = __reduce_min_sync(kFull, sh.tau[lane % (kThreads / 32)]);
+        if constexpr (TOP) tau = warp_sorted(sh.best[lane]);  // every warp for itself
     }
+    if constexpr (TOP) tau = __shfl_sync(kFull, tau, p.k - 1);
     run.move(value_of(st.order), c);
     float a, b;
     un2(run.s, a, b);
@@ -616,14 +616,22 @@ cudaError_t with_float(int dtype, F&& f)
 
 }  // namespace
 
-// A row of at most 8 KB goes to a warp; longer ones to a CTA, or to a cluster
-// of up to 8 while that leaves SMs without a CTA and each part 8 KB.
+// CTAs per row.  Parts of a row want a cluster's barriers and merges, 2 us and
+// more: a few rows are split as long as the parts of all still find an idle SM
+// and have 8 KB (1 row of 256 KB with 20 alternatives in 1 / 2 / 4 / 8 parts: 21.3
+// / 14.3 / 10.0 / 9.0 us, 64 rows of it 25.0 / 15.6 / 13.5 / 15.6), then as long
+// as they find a free slot and have 64 KB (150 rows of 512 KB: 41.4 / 27.2 / 24.6 /
+// 29.5); more rows are not (1500 of 64 KB: 34 / 46 / 73 / 141).
 int logprob_split(uint64_t M, uint64_t V, int dtype)
 {
     const uint64_t bytes = V * (dtype == kF32 ? 4 : 2);
-    int split = 1;
-    while (split < kMaxSplit && M * (uint64_t)split * 2 <= 148 * 2 && bytes / (uint64_t)(2 * split) >= 8192) split *= 2;
-    return split;
+    uint64_t split = 1;
+    while (split < kMaxSplit) {
+        const uint64_t ctas = 2 * split * M, part = bytes / (2 * split);
+        if (!(ctas <= 148 * 2 && part >= 8192) && !(ctas <= 148 * 5 && part >= 65536)) break;
+        split *= 2;
+    }
+    return (int)split;
 }
 
 cudaError_t launch_logprob(int dtype, const LogprobParams& p, cudaStream_t s)
