@@ -15,57 +15,11 @@
 #include "rr_clip.cuh"
 #include "rr_launch.cuh"
 #include "rr_muon.h"
+#include "rr_muon_device.cuh"
 
 namespace rr {
 
 namespace {
-
-template <class F>
-__device__ __forceinline__ void with_device_type(int dtype, F&& f)
-{
-    switch (dtype) {
-    case 0: f.template operator()<F32T>(); break;   // RR_F32
-    case 1: f.template operator()<BF16T>(); break;  // RR_BF16
-    default: f.template operator()<F16T>(); break;  // RR_F16
-    }
-}
-
-// Eight neighbouring values, whole vectors where vec says that every piece of
-// eight lies on 16 bytes; `left` of them exist.
-template <class Ty>
-__device__ __forceinline__ void load8(const typename Ty::T* p, bool vec, uint32_t left, float (&v)[8])
-{
-    if (vec && left >= 8) {
-#pragma unroll
-        for (int h = 0; h < 8 / Ty::L; ++h) {
-            float a[Ty::L];
-            Ty::unpack(*reinterpret_cast<const uint4*>(p + h * Ty::L), a);
-#pragma unroll
-            for (int l = 0; l < Ty::L; ++l) v[h * Ty::L + l] = a[l];
-        }
-    } else {
-#pragma unroll
-        for (int l = 0; l < 8; ++l) v[l] = (uint32_t)l < left ? Ty::ld1(p + l) : 0.0f;
-    }
-}
-
-template <class Ty>
-__device__ __forceinline__ void store8(typename Ty::T* p, bool vec, uint32_t left, const float (&v)[8])
-{
-    if (vec && left >= 8) {
-#pragma unroll
-        for (int h = 0; h < 8 / Ty::L; ++h) {
-            float a[Ty::L];
-#pragma unroll
-            for (int l = 0; l < Ty::L; ++l) a[l] = v[h * Ty::L + l];
-            stv(p + h * Ty::L, Ty::pack(a));
-        }
-    } else {
-#pragma unroll
-        for (int l = 0; l < 8; ++l)
-            if ((uint32_t)l < left) Ty::st1(p + l, v[l]);
-    }
-}
 
 __device__ __forceinline__ int mat_of_part(const MuonPrepParams& p, uint32_t part)
 {
@@ -96,7 +50,7 @@ __global__ void __launch_bounds__(kThreads) muon_squares_kernel(const __grid_con
     const MuonMat& t = p.mat[mat_of_part(p, blockIdx.x)];
     const uint64_t len = (uint64_t)t.rows * t.cols;
     double acc = 0.0;
-    with_device_type(t.dtype, [&]<class Ty>() {
+    muon_with_type(t.dtype, [&]<class Ty>() {
         const auto* g = static_cast<const typename Ty::T*>(t.g);
         for (uint64_t at = (uint64_t)(blockIdx.x - t.part0) * kPrepTile; at < len; at += (uint64_t)t.parts * kPrepTile) {
 #pragma unroll 1
@@ -105,16 +59,16 @@ __global__ void __launch_bounds__(kThreads) muon_squares_kernel(const __grid_con
                 if (e >= len) break;
                 const uint32_t left = (uint32_t)min((uint64_t)8, len - e);
                 float v[8];
-                load8<Ty>(g + e, t.vec, left, v);
+                muon_load8<Ty>(g + e, t.vec, left, v);
                 if (t.m) {
                     float m[8];
-                    load8<F32T>(t.m + e, t.vec, left, m);
+                    muon_load8<F32T>(t.m + e, t.vec, left, m);
 #pragma unroll
                     for (int l = 0; l < 8; ++l) {
                         m[l] = __fmaf_rn(p.momentum, m[l], v[l]);
                         v[l] = updated(v[l], m[l], p);
                     }
-                    store8<F32T>(t.m + e, t.vec, left, m);
+                    muon_store8<F32T>(t.m + e, t.vec, left, m);
                 }
                 acc += sum_squares(v);
             }
@@ -132,15 +86,8 @@ __global__ void __launch_bounds__(kThreads) muon_pack_kernel(const __grid_consta
     const MuonMat& t = p.mat[mat_of_tile(p, blockIdx.x)];
     const uint32_t nbj = pad_up(t.cols) / kBlk;
     const uint32_t tile = blockIdx.x - t.tile0, ti = tile / nbj, tj = tile % nbj;
-    // 1 / (norm + eps) as a power of two times a factor of 1..2, so that neither
-    // leaves fp32's range where their product with u does not
-    const double den = sqrt(partials_sum(p.partial + t.part0, t.parts, sh)) + (double)p.eps;
-    int ex = 0;
-    const double frac = isfinite(den) ? frexp(den, &ex) : den;  // den = frac * 2^ex, frac in [0.5, 1)
-    const bool plain = ex > -100 && ex < 100;
-    const float f1 = plain ? ldexpf(1.0f, -ex) * p.scale : ldexpf(1.0f, -ex / 2);
-    const float f2 = plain ? (float)(1.0 / frac) : ldexpf((float)(1.0 / frac), -(ex - ex / 2)) * p.scale;
-    with_device_type(t.dtype, [&]<class Ty>() {
+    const MuonScale f = muon_scale(sqrt(partials_sum(p.partial + t.part0, t.parts, sh)) + (double)p.eps, p.scale);
+    muon_with_type(t.dtype, [&]<class Ty>() {
         const auto* g = static_cast<const typename Ty::T*>(t.g);
 #pragma unroll 1
         for (uint32_t u = 0; u < 128 * 8 / kThreads; ++u) {
@@ -150,10 +97,10 @@ __global__ void __launch_bounds__(kThreads) muon_pack_kernel(const __grid_consta
             if (r < t.rows && c < t.cols) {
                 const uint64_t e = (uint64_t)r * t.cols + c;
                 const uint32_t left = min(8u, t.cols - c);
-                load8<Ty>(g + e, t.vec, left, v);
+                muon_load8<Ty>(g + e, t.vec, left, v);
                 if (t.m) {
                     float m[8];
-                    load8<F32T>(t.m + e, t.vec, left, m);
+                    muon_load8<F32T>(t.m + e, t.vec, left, m);
 #pragma unroll
                     for (int l = 0; l < 8; ++l) v[l] = (uint32_t)l < left ? updated(v[l], m[l], p) : 0.0f;
                 }
@@ -161,7 +108,7 @@ __global__ void __launch_bounds__(kThreads) muon_pack_kernel(const __grid_consta
             uint32_t hw[4], lw[4];
 #pragma unroll
             for (int l = 0; l < 4; ++l) {
-                const float a = v[2 * l] * f1 * f2, b = v[2 * l + 1] * f1 * f2;
+                const float a = v[2 * l] * f.a * f.b, b = v[2 * l + 1] * f.a * f.b;
                 const __half ah = __float2half_rn(a), bh = __float2half_rn(b);
                 hw[l] = F16T::pack2(a, b);
                 lw[l] = F16T::pack2(a - __half2float(ah), b - __half2float(bh));
@@ -180,7 +127,7 @@ __global__ void __launch_bounds__(kThreads) muon_finish_kernel(const __grid_cons
     const MuonMat& t = p.mat[mat_of_tile(p, blockIdx.x)];
     const uint32_t nbj = pad_up(t.cols) / kBlk;
     const uint32_t tile = blockIdx.x - t.tile0, ti = tile / nbj, tj = tile % nbj;
-    with_device_type(t.out_dtype, [&]<class Ty>() {
+    muon_with_type(t.out_dtype, [&]<class Ty>() {
         using T = typename Ty::T;
 #pragma unroll 1
         for (uint32_t u = 0; u < 128 * 8 / kThreads; ++u) {
@@ -196,11 +143,11 @@ __global__ void __launch_bounds__(kThreads) muon_finish_kernel(const __grid_cons
             for (int l = 0; l < 8; ++l) h[l] = (h[l] + l8[l]) * p.inv;
             if (t.m) {  // weights: rank 0's, updated, to every rank
                 float w[8];
-                load8<Ty>(static_cast<const T*>(p.out[t.out]) + e, t.vec, left, w);
+                muon_load8<Ty>(static_cast<const T*>(p.out[t.out]) + e, t.out_vec, left, w);
 #pragma unroll
                 for (int l = 0; l < 8; ++l) h[l] = __fmaf_rn(-t.factor, h[l], p.keep * w[l]);
             }
-            for (int o = 0; o < p.nranks; ++o) store8<Ty>(static_cast<T*>(p.out[t.out + o]) + e, t.vec, left, h);
+            for (int o = 0; o < p.nranks; ++o) muon_store8<Ty>(static_cast<T*>(p.out[t.out + o]) + e, t.out_vec, left, h);
         }
     });
 }

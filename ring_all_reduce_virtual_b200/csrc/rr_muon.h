@@ -135,7 +135,8 @@ struct MuonMat {
     uint32_t part0, parts; // its partial sums
     Halves x;
     uint32_t tile0;        // first tile of the launch, 128 rows x 64 columns
-    uint8_t dtype, out_dtype, vec, pad_;
+    uint8_t dtype, out_dtype;
+    uint8_t vec, out_vec;  // whole vectors: gradient and momentum, outputs
     uint32_t out;          // muon: index of its first pointer in MuonFinishParams::out
     float factor;          // muon: lr * the shape's factor
 };
@@ -161,10 +162,36 @@ struct MuonFinishParams {
     void* out[kMuonPtrs];  // matrix-major
 };
 
+// Matrices that one launch takes whole (rr_muon_small.cu): a cluster each.
+constexpr uint32_t kMuonSmallSide = 128, kMuonSmallCtas = 8;
+constexpr int kMuonMaxSteps = 50;
+
+// A step's factors: A = gram P, B = poly_a A + poly A A, X = apply_x X + apply B X.
+struct MuonSmallStep {
+    float gram, poly, poly_a, apply, apply_x;
+};
+
+struct MuonSmallParams {
+    MuonMat mat[kMuonMats];  // x, part0, parts and tile0 unused
+    int n;
+    uint32_t ctas;           // per cluster: of the longest matrix
+    int nranks;
+    int steps, nesterov;
+    float momentum, eps, keep;
+    float scale, inv;        // of the first X; 1 / that of the last
+    unsigned int* waits;     // bulk_wait_counters()
+    uint32_t hold, spin;     // as in BulkParams
+    MuonSmallStep step[kMuonMaxSteps];
+    void* out[kMuonPtrs];    // matrix-major
+};
+
 cudaError_t launch_muon_squares(const MuonPrepParams& p, uint32_t parts, cudaStream_t s);
 cudaError_t launch_muon_pack(const MuonPrepParams& p, uint32_t tiles, cudaStream_t s);
 cudaError_t launch_muon_finish(const MuonFinishParams& p, uint32_t tiles, cudaStream_t s);
 // The products of a group: tile_n, waits, hold and spin are filled in here.
 cudaError_t launch_muon_gemm(MuonGemmParams& p, int nops, cudaStream_t s);
+
+// waits, hold and spin are filled in here.
+cudaError_t launch_muon_small(MuonSmallParams& p, cudaStream_t s);
 
 }  // namespace rr

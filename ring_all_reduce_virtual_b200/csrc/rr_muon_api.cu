@@ -12,7 +12,7 @@ using namespace rr;
 namespace {
 
 constexpr uint64_t kMaxSide = 1ull << 20;    // rows and columns
-constexpr int kMaxSteps = 50;
+constexpr int kMaxSteps = kMuonMaxSteps;
 // Workspace of a group of matrices that run in the same launches, unless one
 // alone needs more.
 constexpr uint64_t kGroupBytes = 5ull << 30;
@@ -195,7 +195,13 @@ std::vector<int> segments_for(const Plan& plan, const rr_matrix_list_t* out, int
     return segments_of(plan, std::min(r, c), std::max(r, c), exactness(out, t, weights));
 }
 
-// The groups of a list's matrices (those with elements), in order.
+// Whether a cluster takes the matrix whole (rr_muon_small.cu).
+bool is_small(uint64_t rows, uint64_t cols)
+{
+    return std::min(rows, cols) <= kMuonSmallSide && std::max(rows, cols) <= kMuonSmallSide * kMuonSmallCtas;
+}
+
+// The groups of a list's other matrices (those with elements), in order.
 std::vector<std::vector<int>> groups_of(const rr_matrix_list_t* l, const Plan& plan, bool weights, uint64_t* bytes)
 {
     std::vector<std::vector<int>> groups;
@@ -205,7 +211,7 @@ std::vector<std::vector<int>> groups_of(const rr_matrix_list_t* l, const Plan& p
     *bytes = 256;
     for (int t = 0; t < l->nmatrices; ++t) {
         const Shape s{(uint32_t)l->rows[t], (uint32_t)l->cols[t]};
-        if (s.numel() == 0) continue;
+        if (s.numel() == 0 || is_small(s.rows, s.cols)) continue;
         const std::vector<int> segments = segments_for(plan, l, t, weights);
         const uint64_t need = room_of(s, segments).bytes();
         const int products = products_in(segments);
@@ -325,6 +331,60 @@ std::vector<MuonOp> products_of(const Plan& plan, const std::vector<int>& segmen
     return ops;
 }
 
+// A matrix's gradient and momentum, and its outputs from out[at] on.
+void place_matrix(const Job& job, int t, MuonMat& m, void** out, uint32_t at)
+{
+    const Shape s{(uint32_t)job.in->rows[t], (uint32_t)job.in->cols[t]};
+    m.g = job.in->ptrs[t];
+    m.m = job.mom ? static_cast<float*>(job.mom->ptrs[t]) : nullptr;
+    m.rows = s.rows;
+    m.cols = s.cols;
+    m.dtype = (uint8_t)job.in->dtypes[t];
+    m.out_dtype = (uint8_t)job.out->dtypes[t];
+    m.factor = job.lr * shape_factor(s, job.adjust);
+    m.vec = s.cols % 8 == 0 && on16(m.g) && (!m.m || on16(m.m));
+    m.out_vec = s.cols % 8 == 0;
+    m.out = at;
+    for (int r = 0; out && r < job.out->nranks; ++r) {
+        out[at + r] = job.out->ptrs[(size_t)r * job.out->nmatrices + t];
+        m.out_vec = m.out_vec && on16(out[at + r]);
+    }
+}
+
+// Matrices that a cluster takes whole.
+rr_status_t run_small(const Job& job, const Plan& plan, const std::vector<int>& list, cudaStream_t stream)
+{
+    std::unique_ptr<MuonSmallParams> p(new MuonSmallParams{});
+    const int nr = job.out->nranks, most = std::min(kMuonMats, std::max(1, kMuonPtrs / nr));
+    p->nranks = nr;
+    p->steps = plan.steps;
+    p->nesterov = job.nesterov;
+    p->momentum = job.momentum;
+    p->eps = job.eps;
+    p->keep = job.keep;
+    p->scale = (float)scale_for(plan.rho[0]);
+    p->inv = (float)(1.0 / scale_for(plan.rho[plan.steps]));
+    for (int k = 0; k < plan.steps; ++k) {
+        const double top = plan.rho[k] * plan.rho[k], sx = scale_for(plan.rho[k]), sa = scale_for(top);
+        const double sb = scale_for(plan.poly[k] + std::fabs(plan.a)), to = scale_for(plan.rho[k + 1]);
+        p->step[k] = {(float)(sa / (sx * sx)), (float)(plan.c * sb / (sa * sa)), (float)(plan.b * sb / sa), (float)(to / (sb * sx)),
+                      (float)(plan.a * to / sx)};
+    }
+    for (size_t k0 = 0; k0 < list.size(); k0 += most) {
+        p->n = (int)std::min<size_t>(most, list.size() - k0);
+        p->ctas = 1;
+        for (int k = 0; k < p->n; ++k) {
+            MuonMat& m = p->mat[k];
+            place_matrix(job, list[k0 + k], m, p->out, (uint32_t)(k * nr));
+            p->ctas = std::max(p->ctas, (uint32_t)ceil_div(std::max(m.rows, m.cols), kMuonSmallSide));
+        }
+        const cudaError_t e = timed_launch([&] { return launch_muon_small(*p, stream); });
+        if (e != cudaSuccess) return cuda_fail(e, "Muon launch of small matrices");
+        t_stats.launches += 1;
+    }
+    return RR_OK;
+}
+
 rr_status_t run_group(const Job& job, const Plan& plan, const std::vector<int>& group, char* ws, cudaStream_t stream)
 {
     const int n = (int)group.size();
@@ -375,16 +435,11 @@ rr_status_t run_group(const Job& job, const Plan& plan, const std::vector<int>& 
         result[k] = {last, last + room.x / 2};
         const Halves first{w.x[0], w.x[0] + room.x / 2};
         MuonMat& m = prep->mat[k];
-        m.g = job.in->ptrs[t];
-        m.m = job.mom ? static_cast<float*>(job.mom->ptrs[t]) : nullptr;
-        m.rows = s.rows;
-        m.cols = s.cols;
+        place_matrix(job, t, m, nullptr, 0);
         m.part0 = parts;
         m.parts = parts_of(s);
         m.x = first;
         m.tile0 = tiles;
-        m.dtype = (uint8_t)job.in->dtypes[t];
-        m.vec = s.cols % 8 == 0 && on16(m.g) && (!m.m || on16(m.m));
         parts += m.parts;
         tiles += pad_up(s.rows) / 128 * (pad_up(s.cols) / kBlk);
     }
@@ -428,18 +483,10 @@ rr_status_t run_group(const Job& job, const Plan& plan, const std::vector<int>& 
         for (int k = 0; k < fin->n; ++k) {
             const int t = group[k0 + k];
             MuonMat& m = fin->mat[k];
-            m = prep->mat[k0 + k];
+            place_matrix(job, t, m, fin->out, (uint32_t)(k * nr));
             m.x = result[k0 + k];
             m.tile0 = todo;
             todo += pad_up(m.rows) / 128 * (pad_up(m.cols) / kBlk);
-            m.out_dtype = (uint8_t)job.out->dtypes[t];
-            m.out = (uint32_t)(k * nr);
-            m.factor = job.lr * shape_factor(shape[k0 + k], job.adjust);
-            m.vec = m.cols % 8 == 0;
-            for (int r = 0; r < nr; ++r) {
-                fin->out[k * nr + r] = job.out->ptrs[(size_t)r * job.out->nmatrices + t];
-                m.vec = m.vec && on16(fin->out[k * nr + r]);
-            }
         }
         e = timed_launch([&] { return launch_muon_finish(*fin, todo, stream); });
         if (e != cudaSuccess) return cuda_fail(e, "Muon update launch");
@@ -458,7 +505,10 @@ rr_status_t run(const Job& job, const Plan& plan, std::vector<Span>& spans, void
         total += numel;
     }
     stats_begin(RR_ALGO_ONESHOT, job.out->nranks, S);
-    if (groups.empty()) return RR_OK;
+    std::vector<int> small;
+    for (int t = 0; t < job.in->nmatrices; ++t)
+        if (job.in->rows[t] * job.in->cols[t] != 0 && is_small(job.in->rows[t], job.in->cols[t])) small.push_back(t);
+    if (groups.empty() && small.empty()) return RR_OK;
     if (!ws || (uintptr_t)ws % 256 != 0) return fail(RR_ERR_INVALID_ARG, "workspace NULL or not aligned to 256 bytes");
     if (ws_bytes < need)
         return fail(RR_ERR_INVALID_ARG, "workspace too small: " + std::to_string(need) + " bytes are needed");
@@ -466,6 +516,11 @@ rr_status_t run(const Job& job, const Plan& plan, std::vector<Span>& spans, void
     rr_status_t st = check_spans(spans);
     if (st != RR_OK) return st;
     if ((st = check_device_spans(spans)) != RR_OK) return st;
+    // long matrices of a group share a cluster size with long ones
+    std::stable_sort(small.begin(), small.end(), [&](int a, int b) {
+        return std::max(job.in->rows[a], job.in->cols[a]) > std::max(job.in->rows[b], job.in->cols[b]);
+    });
+    if ((st = run_small(job, plan, small, stream)) != RR_OK) return st;
     for (const auto& group : groups)
         if ((st = run_group(job, plan, group, static_cast<char*>(ws), stream)) != RR_OK) return st;
     t_stats.steps = plan.steps;

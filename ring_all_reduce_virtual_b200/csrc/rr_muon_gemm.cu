@@ -41,6 +41,7 @@
 #include "rr_bulk.cuh"
 #include "rr_launch.cuh"
 #include "rr_muon.h"
+#include "rr_muon_device.cuh"
 
 namespace rr {
 
@@ -87,21 +88,6 @@ constexpr uint32_t kHearers = 2 + kTakers + 3 + kTakers;
 
 // ---------------------------------------------------------------- barriers
 
-__device__ __forceinline__ uint32_t smem_of(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-
-__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity)
-{
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return done != 0;
-}
-
 __device__ __forceinline__ void give_up(Bars* b, unsigned int* waits)
 {
     if (atomicExch(&b->stop, 1u) == 0) atomicAdd(&waits[0], 1u);
@@ -110,9 +96,9 @@ __device__ __forceinline__ void give_up(Bars* b, unsigned int* waits)
 // Bounded; false as well once another warp of the CTA has given up.
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, Bars* b, unsigned int* waits, uint32_t spin)
 {
-    const uint32_t at = smem_of(bar);
+    const uint32_t at = muon_smem(bar);
     for (uint32_t i = 0; i < spin; ++i) {
-        if (try_wait(at, parity)) return true;
+        if (muon_try_wait(at, parity)) return true;
         if (*(volatile uint32_t*)&b->stop) return false;
     }
     give_up(b, waits);
@@ -129,12 +115,12 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Bars* 
 
 __device__ __forceinline__ void bar_init(uint64_t* bar, uint32_t count)
 {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_of(bar)), "r"(count) : "memory");
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(muon_smem(bar)), "r"(count) : "memory");
 }
 
 __device__ __forceinline__ void bar_arrive(uint64_t* bar)
 {
-    asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0];\n\t}" ::"r"(smem_of(bar)) : "memory");
+    asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0];\n\t}" ::"r"(muon_smem(bar)) : "memory");
 }
 
 // An arrival on the first CTA's barrier, from either CTA.
@@ -142,14 +128,14 @@ __device__ __forceinline__ void first_arrive(uint64_t* bar)
 {
     asm volatile(
         "{\n\t.reg .b32 at;\n\tmapa.shared::cluster.u32 at, %0, 0;\n\t"
-        "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [at];\n\t}" ::"r"(smem_of(bar))
+        "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [at];\n\t}" ::"r"(muon_smem(bar))
         : "memory");
 }
 
 __device__ __forceinline__ void copy_block(uint32_t to, const uint16_t* from, uint32_t bytes, uint64_t* bar)
 {
     asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to), "l"(from),
-                 "r"(bytes), "r"(smem_of(bar))
+                 "r"(bytes), "r"(muon_smem(bar))
                  : "memory");
 }
 
@@ -259,7 +245,7 @@ __device__ __forceinline__ bool parts_done(const uint32_t* counter, uint32_t nee
 // A tile into both CTAs' slot.
 __device__ __forceinline__ void tell(const Slot& s, uint32_t n, Bars* b)
 {
-    const uint32_t k = n % kSlots, at = smem_of(&b->slot[k]), bar = smem_of(&b->told[k]);
+    const uint32_t k = n % kSlots, at = muon_smem(&b->slot[k]), bar = muon_smem(&b->told[k]);
     asm volatile(
         "{\n\t.reg .b32 a, r;\n\t"
         "st.shared.v4.b32 [%0], {%2, %3, %4, %2};\n\t"
@@ -305,53 +291,14 @@ __device__ __forceinline__ bool warp_hear(Slot& s, uint32_t n, Bars* b, unsigned
 
 // ---------------------------------------------------------------- products
 
-// Shared-memory descriptor of an operand in 128-byte-swizzled blocks: K along a
-// block's columns (groups of 8 rows are 1024 bytes apart), or along its rows
-// (groups of 8 of K 1024 bytes apart, of 64 of M or N 8192).
-__device__ __forceinline__ uint64_t operand(uint32_t addr, bool mn)
-{
-    return (uint64_t)((addr & 0x3ffffu) >> 4) | (uint64_t)(mn ? 8192u >> 4 : 1u) << 16 | (uint64_t)(1024u >> 4) << 32 |
-           (uint64_t)1 << 46 | (uint64_t)2 << 61;
-}
-
-// Instruction descriptor: fp16 operands, fp32 accumulator, 256 x n over two CTAs.
-__device__ __forceinline__ uint32_t instruction(uint32_t n, bool a_mn, bool b_mn)
-{
-    return 1u << 4 | (uint32_t)a_mn << 15 | (uint32_t)b_mn << 16 | (n >> 3) << 17 | (256u >> 4) << 24;
-}
-
-__device__ __forceinline__ void mma(uint32_t acc, uint64_t a, uint64_t b, uint32_t inst, bool add)
-{
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(acc),
-        "l"(a), "l"(b), "r"(inst), "r"((uint32_t)add)
-        : "memory");
-}
-
 // An arrival on the barrier of both CTAs once the products issued so far are done.
 __device__ __forceinline__ void commit(uint64_t* bar)
 {
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-                     smem_of(bar)),
+                     muon_smem(bar)),
                  "h"((uint16_t)3)
                  : "memory");
 }
-
-__device__ __forceinline__ void load_acc(uint32_t addr, uint32_t (&r)[32])
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
-          "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]),
-          "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(addr));
-}
-
-__device__ __forceinline__ void acc_landed() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 // ----------------------------------------------------------------- results
 
@@ -516,7 +463,7 @@ __device__ __forceinline__ uint32_t copy_tiles(const P& p, Bars* b, uint32_t ops
             if (use > 0 && !warp_wait(&b->empty[st], (use - 1) & 1, b, p.waits, p.spin)) return it;
             uint64_t* full = &b->full[st];
             if (lane == 0)
-                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_of(full)), "r"(blocks * kPlane) : "memory");
+                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(muon_smem(full)), "r"(blocks * kPlane) : "memory");
             __syncwarp();
             const bool whole = k < limit && blocks == 2;  // both blocks, one after the other
             if (lane < 4 && half < (whole ? 1 : blocks))
@@ -568,16 +515,16 @@ __device__ __forceinline__ void multiply(const P& p, Bars* b, uint32_t ops, uint
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 const uint32_t sa = ops + s * kStageBytes;
                 const bool a_mn = k >= a_rows, b_mn = k >= b_rows;
-                const uint32_t inst = instruction(n128, a_mn, b_mn);
+                const uint32_t inst = muon_instruction(256, n128, a_mn, b_mn);
                 const uint32_t astep = (a_mn ? 2048u : 32u) >> 4, bstep = (b_mn ? 2048u : 32u) >> 4;  // 16 of K
-                const uint64_t ah = operand(sa, a_mn), al = operand(sa + kPlane, a_mn);
-                const uint64_t bh = operand(sa + 2 * kPlane, b_mn), bl = operand(sa + 3 * kPlane, b_mn);
+                const uint64_t ah = muon_operand(sa, a_mn, 8192), al = muon_operand(sa + kPlane, a_mn, 8192);
+                const uint64_t bh = muon_operand(sa + 2 * kPlane, b_mn, 8192), bl = muon_operand(sa + 3 * kPlane, b_mn, 8192);
 #pragma unroll
-                for (uint32_t c = 0; c < kBlk / 16; ++c) mma(acc, al + c * astep, bh + c * bstep, inst, k > k0 || c > 0);
+                for (uint32_t c = 0; c < kBlk / 16; ++c) muon_mma<2>(acc, al + c * astep, bh + c * bstep, inst, k > k0 || c > 0);
 #pragma unroll
-                for (uint32_t c = 0; c < kBlk / 16; ++c) mma(acc, ah + c * astep, bl + c * bstep, inst, true);
+                for (uint32_t c = 0; c < kBlk / 16; ++c) muon_mma<2>(acc, ah + c * astep, bl + c * bstep, inst, true);
 #pragma unroll
-                for (uint32_t c = 0; c < kBlk / 16; ++c) mma(acc, ah + c * astep, bh + c * bstep, inst, true);
+                for (uint32_t c = 0; c < kBlk / 16; ++c) muon_mma<2>(acc, ah + c * astep, bh + c * bstep, inst, true);
                 commit(&b->empty[s]);
             }
             commit(&b->ready[sums & 1]);
@@ -607,8 +554,8 @@ __device__ __forceinline__ bool take_tile(const P& p, Bars* b, uint32_t tmem, co
         for (int h = 0; h < COLS / 32; h += kAtOnce) {
             uint32_t bits[kAtOnce][32];
 #pragma unroll
-            for (int u = 0; u < kAtOnce; ++u) load_acc(acc + (h + u) * 32, bits[u]);
-            acc_landed();
+            for (int u = 0; u < kAtOnce; ++u) muon_load_acc(acc + (h + u) * 32, bits[u]);
+            muon_acc_landed();
 #pragma unroll
             for (int l = 0; l < 32 * kAtOnce; ++l) sum[h * 32 + l] += __uint_as_float(bits[l / 32][l % 32]);
         }
@@ -659,10 +606,10 @@ template <int OPS, int SEQ>
 __global__ void __launch_bounds__(kGemmThreads, 1) muon_gemm_kernel(const __grid_constant__ MuonGemmParamsT<OPS, SEQ> p)
 {
     extern __shared__ uint8_t raw_smem[];
-    uint8_t* base = raw_smem + ((1024u - (smem_of(raw_smem) & 1023u)) & 1023u);
+    uint8_t* base = raw_smem + ((1024u - (muon_smem(raw_smem) & 1023u)) & 1023u);
     uint8_t* out_rows = base + kStages * kStageBytes;
     Bars* b = reinterpret_cast<Bars*>(out_rows + kTakers * kOutBytes);
-    const uint32_t ops = smem_of(base);
+    const uint32_t ops = muon_smem(base);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = blockIdx.x & 1;  // in its pair
     if (threadIdx.x == 0) {
@@ -684,7 +631,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) muon_gemm_kernel(const __grid
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_of(&b->tmem)), "r"(512u)
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(muon_smem(&b->tmem)), "r"(512u)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -730,13 +677,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1) muon_gemm_kernel(const __grid
                 const uint32_t last = begun - back;
                 bool landed = false;
                 for (uint32_t i = 0; i < p.spin && !landed; ++i)
-                    landed = try_wait(smem_of(&b->full[last % kStages]), (last / kStages) & 1);
+                    landed = muon_try_wait(muon_smem(&b->full[last % kStages]), (last / kStages) & 1);
                 if (!landed) atomicAdd(&p.waits[1], 1u);
             }
         }
         if (threadIdx.x == 32 && rank == 0) {
             commit(&b->drained);
-            for (uint32_t i = 0; i < p.spin && !try_wait(smem_of(&b->drained), 0); ++i) {
+            for (uint32_t i = 0; i < p.spin && !muon_try_wait(muon_smem(&b->drained), 0); ++i) {
             }
         }
         __syncwarp();
