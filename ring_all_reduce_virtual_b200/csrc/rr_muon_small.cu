@@ -15,7 +15,7 @@
 // every 64 of K (rr_muon_gemm.cu says why), and its result goes back to shared
 // memory: nothing of an iteration leaves the chip, and a step costs two cluster
 // barriers.  As tiles of rr_muon_gemm.cu a level of such a matrix takes 8 us, most
-// of it the way through L2: one layer of width 128 (fp32) 155 us against 72.
+// of it the way through L2: one layer of width 128 (fp32) 155 us against 70.
 #include <algorithm>
 #include <atomic>
 
@@ -194,33 +194,47 @@ __global__ void __launch_bounds__(kThreads, 1) muon_small_kernel(const __grid_co
     const uint32_t prows = wide ? m : width, pcols = wide ? width : m;  // its part of the matrix as it lies
     const uint64_t first = wide ? n0 : (uint64_t)n0 * t.cols;
     const uint32_t per = (pcols + 7) / 8;
-    for (uint32_t k = tid; k < kSide * kSide / 4; k += kThreads) reinterpret_cast<float4*>(S)[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    __syncthreads();
+    if (m < kSide || width < kSide) {  // what is beyond the matrix is zero
+        for (uint32_t k = tid; k < kSide * kSide / 4; k += kThreads) reinterpret_cast<float4*>(S)[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        __syncthreads();
+    }
+    constexpr uint32_t kAtOnce = 4;  // pieces of eight a thread has on the way
     double squares = 0.0;
     muon_with_type(t.dtype, [&]<class Ty>() {
         const auto* g = static_cast<const typename Ty::T*>(t.g);
-        for (uint32_t k = tid; k < prows * per; k += kThreads) {
-            const uint32_t r = k / per, c = k % per * 8, left = min(8u, pcols - c);
-            const uint64_t e = first + (uint64_t)r * t.cols + c;
-            float v[8];
-            muon_load8<Ty>(g + e, t.vec, left, v);
-            if (t.m) {
-                float mo[8];
-                muon_load8<F32T>(t.m + e, t.vec, left, mo);
+#pragma unroll 1
+        for (uint32_t k0 = tid; k0 < prows * per; k0 += kAtOnce * kThreads) {
+            float v[kAtOnce][8], mo[kAtOnce][8];
+            uint32_t r[kAtOnce], c[kAtOnce], left[kAtOnce];
 #pragma unroll
-                for (int l = 0; l < 8; ++l) {
-                    mo[l] = __fmaf_rn(p.momentum, mo[l], v[l]);
-                    v[l] = p.nesterov ? __fmaf_rn(p.momentum, mo[l], v[l]) : mo[l];
-                }
-                muon_store8<F32T>(t.m + e, t.vec, left, mo);
+            for (uint32_t u = 0; u < kAtOnce; ++u) {
+                const uint32_t k = k0 + u * kThreads;
+                r[u] = k / per;
+                c[u] = (k - r[u] * per) * 8;
+                left[u] = r[u] < prows ? min(8u, pcols - c[u]) : 0;
+                const uint64_t e = first + (uint64_t)r[u] * t.cols + c[u];
+                muon_load8<Ty>(g + e, t.vec, left[u], v[u]);
+                if (t.m) muon_load8<F32T>(t.m + e, t.vec, left[u], mo[u]);
             }
 #pragma unroll
-            for (int l = 0; l < 8; ++l)
-                if ((uint32_t)l >= left) v[l] = 0.0f;
-            squares += sum_squares(v);
+            for (uint32_t u = 0; u < kAtOnce; ++u) {
+                if (left[u] == 0) continue;
+                if (t.m) {
 #pragma unroll
-            for (int l = 0; l < 8; ++l)
-                if ((uint32_t)l < left) *(wide ? word(S, r, c + l) : word(S, c + l, r)) = v[l];
+                    for (int l = 0; l < 8; ++l) {
+                        mo[u][l] = __fmaf_rn(p.momentum, mo[u][l], v[u][l]);
+                        v[u][l] = p.nesterov ? __fmaf_rn(p.momentum, mo[u][l], v[u][l]) : mo[u][l];
+                    }
+                    muon_store8<F32T>(t.m + first + (uint64_t)r[u] * t.cols + c[u], t.vec, left[u], mo[u]);
+                }
+#pragma unroll
+                for (int l = 0; l < 8; ++l)
+                    if ((uint32_t)l >= left[u]) v[u][l] = 0.0f;
+                squares += sum_squares(v[u]);
+#pragma unroll
+                for (int l = 0; l < 8; ++l)
+                    if ((uint32_t)l < left[u]) *(wide ? word(S, r[u], c[u] + l) : word(S, c[u] + l, r[u])) = v[u][l];
+            }
         }
     });
     squares = cta_sum(squares, sh.sums);
@@ -262,27 +276,56 @@ __global__ void __launch_bounds__(kThreads, 1) muon_small_kernel(const __grid_co
             for (int g = 0; g < 8; ++g) *quad(B, arow, c / 4 + g) = make_float4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
         }
         cluster_sync();
-        // 16 rows at a time, of every CTA's sums, in the order of the CTAs
-        for (uint32_t group = rank; group < kSide / 16; group += used) {
-            const uint32_t r = group * 16 + tid / 16, c = tid % 16 * 8;
-            float v[8] = {};
-            for (uint32_t k = 0; k < used; ++k) {
-                uint8_t* const of = in_cta(B, k);
-                const float4 x = *quad(of, r, c / 4), y = *quad(of, r, c / 4 + 1);
-                v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w, v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
+        // 16 rows at a time, of every CTA's sums, in the order of the CTAs: two
+        // groups, four CTAs' values on the way (the summing and handing out takes 5 us of a step's 14 in four CTAs: 112 KB a CTA between SMs)
+#pragma unroll 1
+        for (uint32_t group = rank; group < kSide / 16; group += 2 * used) {
+            const uint32_t c = tid % 16 * 8;
+            float v[2][8] = {};
+#pragma unroll 1
+            for (uint32_t k0 = 0; k0 < used; k0 += 4) {
+                float4 x[2][4][2];
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (uint32_t k = 0; k < 4; ++k) {
+                        const uint32_t r = (group + u * used) * 16 + tid / 16;
+                        x[u][k][0] = x[u][k][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        if (k0 + k < used && r < kSide) {
+                            uint8_t* const of = in_cta(B, k0 + k);
+                            x[u][k][0] = *quad(of, r, c / 4);
+                            x[u][k][1] = *quad(of, r, c / 4 + 1);
+                        }
+                    }
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            v[u][4 * h] += x[u][k][h].x;
+                            v[u][4 * h + 1] += x[u][k][h].y;
+                            v[u][4 * h + 2] += x[u][k][h].z;
+                            v[u][4 * h + 3] += x[u][k][h].w;
+                        }
             }
-            float w[8];
 #pragma unroll
-            for (int l = 0; l < 8; ++l) v[l] *= s.gram;
-            const uint4 hi = F16T::pack(v);
-            F16T::unpack(hi, w);
+            for (int u = 0; u < 2; ++u) {
+                const uint32_t r = (group + u * used) * 16 + tid / 16;
+                if (r >= kSide) continue;
+                float w[8];
 #pragma unroll
-            for (int l = 0; l < 8; ++l) w[l] = v[l] - w[l];
-            const uint4 lo = F16T::pack(w);
-            for (uint32_t k = 0; k < used; ++k) {
-                uint8_t* const of = in_cta(A, k);
-                *piece(of, r, c) = hi;
-                *piece(of + kPlaneBytes, r, c) = lo;
+                for (int l = 0; l < 8; ++l) v[u][l] *= s.gram;
+                const uint4 hi = F16T::pack(v[u]);
+                F16T::unpack(hi, w);
+#pragma unroll
+                for (int l = 0; l < 8; ++l) w[l] = v[u][l] - w[l];
+                const uint4 lo = F16T::pack(w);
+                for (uint32_t k = 0; k < used; ++k) {
+                    uint8_t* const of = in_cta(A, k);
+                    *piece(of, r, c) = hi;
+                    *piece(of + kPlaneBytes, r, c) = lo;
+                }
             }
         }
         cluster_sync();
@@ -312,19 +355,33 @@ __global__ void __launch_bounds__(kThreads, 1) muon_small_kernel(const __grid_co
 
     muon_with_type(t.out_dtype, [&]<class Ty>() {
         using T = typename Ty::T;
-        for (uint32_t k = tid; k < prows * per; k += kThreads) {
-            const uint32_t r = k / per, c = k % per * 8, left = min(8u, pcols - c);
-            const uint64_t e = first + (uint64_t)r * t.cols + c;
-            float v[8];
+#pragma unroll 1
+        for (uint32_t k0 = tid; k0 < prows * per; k0 += kAtOnce * kThreads) {
+            float w[kAtOnce][8];
+            uint32_t r[kAtOnce], c[kAtOnce], left[kAtOnce];
 #pragma unroll
-            for (int l = 0; l < 8; ++l) v[l] = (uint32_t)l < left ? *(wide ? word(S, r, c + l) : word(S, c + l, r)) * p.inv : 0.0f;
-            if (t.m) {  // weights: rank 0's, updated, to every rank
-                float w[8];
-                muon_load8<Ty>(static_cast<const T*>(p.out[t.out]) + e, t.out_vec, left, w);
-#pragma unroll
-                for (int l = 0; l < 8; ++l) v[l] = __fmaf_rn(-t.factor, v[l], p.keep * w[l]);
+            for (uint32_t u = 0; u < kAtOnce; ++u) {
+                const uint32_t k = k0 + u * kThreads;
+                r[u] = k / per;
+                c[u] = (k - r[u] * per) * 8;
+                left[u] = r[u] < prows ? min(8u, pcols - c[u]) : 0;
+                if (t.m)  // weights: rank 0's, updated, to every rank
+                    muon_load8<Ty>(static_cast<const T*>(p.out[t.out]) + first + (uint64_t)r[u] * t.cols + c[u], t.out_vec, left[u], w[u]);
             }
-            for (int o = 0; o < p.nranks; ++o) muon_store8<Ty>(static_cast<T*>(p.out[t.out + o]) + e, t.out_vec, left, v);
+#pragma unroll
+            for (uint32_t u = 0; u < kAtOnce; ++u) {
+                if (left[u] == 0) continue;
+                float v[8];
+#pragma unroll
+                for (int l = 0; l < 8; ++l)
+                    v[l] = (uint32_t)l < left[u] ? *(wide ? word(S, r[u], c[u] + l) : word(S, c[u] + l, r[u])) * p.inv : 0.0f;
+                if (t.m) {
+#pragma unroll
+                    for (int l = 0; l < 8; ++l) v[l] = __fmaf_rn(-t.factor, v[l], p.keep * w[u][l]);
+                }
+                const uint64_t e = first + (uint64_t)r[u] * t.cols + c[u];
+                for (int o = 0; o < p.nranks; ++o) muon_store8<Ty>(static_cast<T*>(p.out[t.out + o]) + e, t.out_vec, left[u], v);
+            }
         }
     });
 
