@@ -47,11 +47,22 @@ namespace rr {
 
 namespace {
 
-constexpr int kStages = 3;
+constexpr int kMaxStages = 4;
 constexpr uint32_t kPairs = 74;                // pairs of SMs
 constexpr uint32_t kTileN = 256;
 constexpr uint32_t kPlane = 128 * kBlk * 2;    // one half of 128 rows (or columns) of an operand's stage
-constexpr uint32_t kStageBytes = 4 * kPlane;   // A's hi and lo, B's hi and lo
+// A's hi and lo, B's hi and lo: three stages where tiles may have 256 columns, four
+// where all have 128 -- a stage's way round (copies from L2, the other CTA's word,
+// products, the word back) takes 2.3 us, which the products of 128 columns do not
+// fill otherwise.
+template <bool WIDE>
+struct Ring {
+    static constexpr int kStages = WIDE ? 3 : 4;
+    static constexpr uint32_t kPlaneB = WIDE ? kPlane : kPlane / 2;
+    static constexpr uint32_t kBytes = 2 * kPlane + 2 * kPlaneB;
+};
+constexpr uint32_t kRingBytes = 3 * 4 * kPlane;
+static_assert(Ring<true>::kStages * Ring<true>::kBytes == kRingBytes && Ring<false>::kStages * Ring<false>::kBytes == kRingBytes);
 constexpr int kTakers = 8;                     // warps that take accumulators out
 constexpr int kGemmThreads = 128 + 32 * kTakers;
 // Registers a thread: 168 at the launch (65536 over 384 threads), of which the
@@ -61,7 +72,7 @@ constexpr int kFewRegs = 56, kManyRegs = 224;
 static_assert(128 * kFewRegs + 32 * kTakers * kManyRegs <= 168 * kGemmThreads, "more than the launch has");
 constexpr uint32_t kOutBytes = 32 * kBlk * 2;  // a warp's 32 rows of a block
 constexpr int kSlots = 4;                      // tiles handed on to the CTA's other warps
-constexpr uint32_t kSmem = kStages * kStageBytes + kTakers * kOutBytes + 1024 + 512;  // from a 1024-byte boundary; the rest
+constexpr uint32_t kSmem = kRingBytes + kTakers * kOutBytes + 1024 + 512;  // from a 1024-byte boundary; the rest
 constexpr uint32_t kEnd = 0xffffffffu;
 constexpr uint32_t kFull = 0xffffffffu;
 
@@ -72,12 +83,12 @@ struct Slot {
 };
 
 struct Bars {
-    uint64_t full[kStages], empty[kStages];  // of a stage: its copies have landed; its products are done
-    uint64_t other[kStages];                 // first CTA: the second's copies have landed
+    uint64_t full[kMaxStages], empty[kMaxStages];  // of a stage: its copies have landed; its products are done
+    uint64_t other[kMaxStages];                // first CTA: the second's copies have landed
     uint64_t ready[2], taken[2];             // of an accumulator: finished; read out by both CTAs (in the first)
     uint64_t told[kSlots], heard[kSlots];    // of a slot: filled; read by all of both CTAs (in the first)
     uint64_t drained;
-    Slot slot[kSlots];
+    alignas(16) Slot slot[kSlots];
     uint32_t tmem;
     uint32_t stop;
     uint32_t begun_b;                        // stages that copies of B were begun for
@@ -415,7 +426,7 @@ struct Source {
 // copy takes its warp about 100 clocks to issue, so that one warp's four or
 // eight a stage took longer than the products of a tile of 128 columns.
 // Returns the stages begun.
-template <bool IS_B, class P>
+template <bool IS_B, bool WIDE, class P>
 __device__ __forceinline__ uint32_t copy_tiles(const P& p, Bars* b, uint32_t ops, uint32_t rank, int lane)
 {
     const uint32_t half = lane & 1, second = lane >> 1 & 1;  // of the pair; the low halves
@@ -448,7 +459,7 @@ __device__ __forceinline__ uint32_t copy_tiles(const P& p, Bars* b, uint32_t ops
         const uint16_t* src = second ? op.lo : op.hi;
         const uint16_t* by_row = src + block_at(at + half, 0, nbj);  // + k * 2 blocks
         const uint16_t* by_col = src + block_at(0, at + half, nbj);  // + k / 2 * 2 nbj blocks + k % 2
-        const uint32_t to = ops + (IS_B ? 2 * kPlane : 0) + second * kPlane + half * (kPlane / 2);
+        const uint32_t to = ops + (IS_B ? 2 * kPlane + second * Ring<WIDE>::kPlaneB : second * kPlane) + half * (kPlane / 2);
         const uint32_t kb = t.kb, limit = low ? (at >> 2) * 4 + 4 : mn ? 0 : kb;  // K's blocks that lie by rows
         const uint64_t pair = (uint64_t)nbj * 2 * kBlkElems;
         if (s.seq != last) {  // what the operands come from is finished
@@ -459,6 +470,7 @@ __device__ __forceinline__ uint32_t copy_tiles(const P& p, Bars* b, uint32_t ops
             asm volatile("fence.proxy.async;" ::: "memory");  // it was written by ordinary stores
         }
         for (uint32_t k = 0; k < kb; ++k, ++it) {
+            constexpr int kStages = Ring<WIDE>::kStages;
             const uint32_t st = it % kStages, use = it / kStages;
             if (use > 0 && !warp_wait(&b->empty[st], (use - 1) & 1, b, p.waits, p.spin)) return it;
             uint64_t* full = &b->full[st];
@@ -467,7 +479,7 @@ __device__ __forceinline__ uint32_t copy_tiles(const P& p, Bars* b, uint32_t ops
             __syncwarp();
             const bool whole = k < limit && blocks == 2;  // both blocks, one after the other
             if (lane < 4 && half < (whole ? 1 : blocks))
-                copy_block(to + st * kStageBytes,
+                copy_block(to + st * Ring<WIDE>::kBytes,
                            k < limit ? by_row + (uint64_t)k * 2 * kBlkElems : by_col + (k >> 1) * pair + (k & 1) * kBlkElems,
                            whole ? kPlane : kPlane / 2, full);
         }
@@ -475,9 +487,10 @@ __device__ __forceinline__ uint32_t copy_tiles(const P& p, Bars* b, uint32_t ops
 }
 
 // The second CTA, one thread: the first one learns of its copies.
-template <class P>
+template <bool WIDE, class P>
 __device__ __forceinline__ void report_copies(const P& p, Bars* b)
 {
+    constexpr int kStages = Ring<WIDE>::kStages;
     uint32_t stages = 0;
     Slot slot;
     for (uint32_t n = 0; hear(slot, n, b, p.waits, p.spin); ++n) {
@@ -491,9 +504,11 @@ __device__ __forceinline__ void report_copies(const P& p, Bars* b)
 }
 
 // The first CTA, one thread: the products of both.
-template <class P>
+template <bool WIDE, class P>
 __device__ __forceinline__ void multiply(const P& p, Bars* b, uint32_t ops, uint32_t tmem)
 {
+    constexpr int kStages = Ring<WIDE>::kStages;
+    constexpr uint32_t kPlaneB = Ring<WIDE>::kPlaneB;
     uint32_t stages = 0, sums = 0;
     Slot slot;
     for (uint32_t n = 0; hear(slot, n, b, p.waits, p.spin); ++n) {
@@ -513,12 +528,12 @@ __device__ __forceinline__ void multiply(const P& p, Bars* b, uint32_t ops, uint
                 if (!wait_for(&b->full[s], parity, b, p.waits, p.spin)) return;
                 if (!wait_for(&b->other[s], parity, b, p.waits, p.spin)) return;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                const uint32_t sa = ops + s * kStageBytes;
+                const uint32_t sa = ops + s * Ring<WIDE>::kBytes;
                 const bool a_mn = k >= a_rows, b_mn = k >= b_rows;
                 const uint32_t inst = muon_instruction(256, n128, a_mn, b_mn);
                 const uint32_t astep = (a_mn ? 2048u : 32u) >> 4, bstep = (b_mn ? 2048u : 32u) >> 4;  // 16 of K
                 const uint64_t ah = muon_operand(sa, a_mn, 8192), al = muon_operand(sa + kPlane, a_mn, 8192);
-                const uint64_t bh = muon_operand(sa + 2 * kPlane, b_mn, 8192), bl = muon_operand(sa + 3 * kPlane, b_mn, 8192);
+                const uint64_t bh = muon_operand(sa + 2 * kPlane, b_mn, 8192), bl = muon_operand(sa + 2 * kPlane + kPlaneB, b_mn, 8192);
 #pragma unroll
                 for (uint32_t c = 0; c < kBlk / 16; ++c) muon_mma<2>(acc, al + c * astep, bh + c * bstep, inst, k > k0 || c > 0);
 #pragma unroll
@@ -586,15 +601,15 @@ __device__ __forceinline__ bool take_tile(const P& p, Bars* b, uint32_t tmem, co
     return true;
 }
 
-template <class P>
+template <bool WIDE, class P>
 __device__ __forceinline__ void take_tiles(const P& p, Bars* b, uint32_t tmem, const OutRows& o, uint32_t rank, int warp, int lane)
 {
     uint32_t sums = 0;
     Slot slot;
     for (uint32_t n = 0; warp_hear(slot, n, b, p.waits, p.spin); ++n) {
         const Tile t = tile_at(p, slot);
-        if (!(t.units == 2 ? take_tile<128>(p, b, tmem, o, rank, warp, lane, t, sums)
-                           : take_tile<64>(p, b, tmem, o, rank, warp, lane, t, sums)))
+        if (!(WIDE && t.units == 2 ? take_tile<WIDE ? 128 : 64>(p, b, tmem, o, rank, warp, lane, t, sums)
+                                   : take_tile<64>(p, b, tmem, o, rank, warp, lane, t, sums)))
             return;
         __syncwarp();
         if (lane == 0)  // this part is there, of every lane's stores
@@ -602,18 +617,18 @@ __device__ __forceinline__ void take_tiles(const P& p, Bars* b, uint32_t tmem, c
     }
 }
 
-template <int OPS, int SEQ>
+template <bool WIDE, int OPS, int SEQ>
 __global__ void __launch_bounds__(kGemmThreads, 1) muon_gemm_kernel(const __grid_constant__ MuonGemmParamsT<OPS, SEQ> p)
 {
     extern __shared__ uint8_t raw_smem[];
     uint8_t* base = raw_smem + ((1024u - (muon_smem(raw_smem) & 1023u)) & 1023u);
-    uint8_t* out_rows = base + kStages * kStageBytes;
+    uint8_t* out_rows = base + kRingBytes;
     Bars* b = reinterpret_cast<Bars*>(out_rows + kTakers * kOutBytes);
     const uint32_t ops = muon_smem(base);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = blockIdx.x & 1;  // in its pair
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
+        for (int s = 0; s < kMaxStages; ++s) {
             bar_init(&b->full[s], 2 + p.hold);
             bar_init(&b->empty[s], 1);
             bar_init(&b->other[s], 1);
@@ -646,28 +661,29 @@ __global__ void __launch_bounds__(kGemmThreads, 1) muon_gemm_kernel(const __grid
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
         if (warp == 0) {
-            begun = copy_tiles<false>(p, b, ops, rank, lane);
+            begun = copy_tiles<false, WIDE>(p, b, ops, rank, lane);
             __syncwarp();
         } else if (warp == 2) {
-            begun = copy_tiles<true>(p, b, ops, rank, lane);
+            begun = copy_tiles<true, WIDE>(p, b, ops, rank, lane);
             if (lane == 0) b->begun_b = begun;
             __syncwarp();
         } else if (warp == 1) {
             if (lane == 0) {
-                if (rank != 0) report_copies(p, b);
-                else multiply(p, b, ops, tmem);
+                if (rank != 0) report_copies<WIDE>(p, b);
+                else multiply<WIDE>(p, b, ops, tmem);
             }
             __syncwarp();
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
-        take_tiles(p, b, tmem, OutRows{out_rows + (warp - 4) * kOutBytes}, rank, warp, lane);
+        take_tiles<WIDE>(p, b, tmem, OutRows{out_rows + (warp - 4) * kOutBytes}, rank, warp, lane);
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     if (b->stop) {  // a wait ran out: what is in flight ends before the CTA's memory goes
         if (threadIdx.x == 0) {
+            constexpr int kStages = Ring<WIDE>::kStages;
             const uint32_t least = min(begun, b->begun_b);
             begun = max(begun, b->begun_b);
             for (uint32_t k = least; k < begun; ++k) bar_arrive(&b->full[k % kStages]);  // for the warp that got less far
@@ -695,7 +711,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) muon_gemm_kernel(const __grid
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
-template <int OPS, int SEQ>
+template <bool WIDE, int OPS, int SEQ>
 cudaError_t launch_as(const MuonGemmParamsT<OPS, SEQ>& p, uint32_t pairs, cudaStream_t s)
 {
     constexpr int kMaxDevices = 64;
@@ -704,7 +720,7 @@ cudaError_t launch_as(const MuonGemmParamsT<OPS, SEQ>& p, uint32_t pairs, cudaSt
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= kMaxDevices || !asked[dev].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(muon_gemm_kernel<OPS, SEQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+        e = cudaFuncSetAttribute(muon_gemm_kernel<WIDE, OPS, SEQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
         if (e != cudaSuccess) return e;
         if (dev < kMaxDevices) asked[dev].store(true, std::memory_order_release);
     }
@@ -721,7 +737,7 @@ cudaError_t launch_as(const MuonGemmParamsT<OPS, SEQ>& p, uint32_t pairs, cudaSt
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, muon_gemm_kernel<OPS, SEQ>, p);
+    e = cudaLaunchKernelEx(&cfg, muon_gemm_kernel<WIDE, OPS, SEQ>, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -750,14 +766,17 @@ cudaError_t launch_muon_gemm(MuonGemmParams& p, int nops, cudaStream_t s)
     p.waits = rp.waits;
     p.hold = bp.hold;
     p.spin = bp.spin;
-    // tiles of 256 columns where every pair of SMs has one; narrower ones are done sooner
+    // Tiles of 256 columns where every pair of SMs has one (of a level's squares,
+    // most of the levels; then of each other kind for itself); narrower ones, twice
+    // as many, are done sooner.
+    const bool wide = tiles_of_all(p, kSquare, 256) >= kPairs;
     uint32_t widest = 0;
     for (int kind = 0; kind < 3; ++kind) {
-        p.tile_n[kind] = tiles_of_all(p, kind, 256) >= kPairs ? 256 : 128;
+        p.tile_n[kind] = wide && tiles_of_all(p, kind, 256) >= kPairs ? 256 : 128;
         widest = std::max(widest, tiles_of_all(p, kind, p.tile_n[kind]));
     }
     const uint32_t pairs = std::min(kPairs, 2 * widest);  // two products of a matrix may run side by side
-    if (nops > kMuonOpsSmall || p.nseq > kMuonSeqSmall) return launch_as(p, pairs, s);
+    if (nops > kMuonOpsSmall || p.nseq > kMuonSeqSmall) return wide ? launch_as<true>(p, pairs, s) : launch_as<false>(p, pairs, s);
     MuonGemmParamsT<kMuonOpsSmall, kMuonSeqSmall> q;
     std::copy_n(p.work, kMuonMats, q.work);
     std::copy_n(p.op, nops, q.op);
@@ -768,7 +787,7 @@ cudaError_t launch_muon_gemm(MuonGemmParams& p, int nops, cudaStream_t s)
     q.waits = p.waits;
     q.hold = p.hold;
     q.spin = p.spin;
-    return launch_as(q, pairs, s);
+    return wide ? launch_as<true>(q, pairs, s) : launch_as<false>(q, pairs, s);
 }
 
 }  // namespace rr
