@@ -298,3 +298,51 @@ def test_refused_tensors():
         rrv.token_logprobs([x], [t], scale=0.0)
     with pytest.raises(TypeError):
         rrv.token_logprobs([x.double()], [t])
+
+
+def test_no_rows_and_first_calls_under_capture():
+    x, t = torch.empty(0, 50, device="cuda"), torch.empty(0, dtype=torch.int64, device="cuda")
+    got = rrv.token_logprobs([x, x], [t, t], entropy=True, top_k=3)
+    assert got.logprob.shape == (2, 0) and got.top_id.shape == (2, 0, 3)
+    assert rrv.token_logprobs_grad([x], [t], torch.empty(1, 0, device="cuda"), torch.empty(1, 0, device="cuda"))[0].shape == (0, 50)
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = r"""
+import torch
+import ring_all_reduce_virtual_b200 as rrv
+x = torch.randn(5, 40000, device="cuda")
+t = torch.arange(5, device="cuda")
+small, large = torch.randn(70, 200, device="cuda"), torch.randn(300, 200, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    a = rrv.token_logprobs([x], [t], entropy=True, top_k=4)
+    d = rrv.token_logprobs_grad([x], [t], a.lse, a.lse)
+    o = rrv.orthogonalize([small, large])
+g.replay()
+torch.cuda.synchronize()
+b = rrv.token_logprobs([x], [t], entropy=True, top_k=4)
+e = rrv.token_logprobs_grad([x], [t], b.lse, b.lse)
+p = rrv.orthogonalize([small, large])
+print("SAME", all(torch.equal(u, v) for u, v in zip((*a, *d, *o), (*b, *e, *p))))
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "SAME True" in r.stdout, r.stdout + r.stderr
+
+
+def test_gradient_rows_at_every_phase_beside_the_logits():
+    """Logits and gradients at all pairs of offsets, row strides that change the phase from row to row; neighbours left alone."""
+    for dt in (torch.bfloat16, torch.float32):
+        L = 16 // torch.tensor([], dtype=dt).element_size()
+        for off in range(L):
+            xs, ids = make(1, 5, 333, dt, seed=off, pitch=off % 3, offset=off)
+            got = rrv.token_logprobs(xs, ids, entropy=True)
+            base = torch.full((6 * 340 + 16,), 7.0, dtype=dt, device="cuda")
+            out = base[3:3 + 5 * 336].view(5, 336)[:, :333]
+            check_backward(xs, ids, 1.0, got, True, outs=[out])
+            keep = torch.ones_like(base, dtype=torch.bool)
+            keep[3:3 + 5 * 336].view(5, 336)[:, :333] = False
+            assert (base[keep] == 7).all()

@@ -297,3 +297,67 @@ def test_refused_tensors():
         rrv.muon_step([x], [x], [torch.zeros(4, 6, device="cuda")], lr=0.1)  # the gradient in the weights' place
     with pytest.raises(rrv.RRError):
         rrv.muon_step([x], [x.clone()], [torch.zeros(4, 6, device="cuda").half()], lr=0.1)
+
+
+def test_waits_that_run_out():
+    """RR_DEBUG_BULK_TIMEOUT=1 makes the products' waits run out, in the launch of many tiles and in a cluster's own: the
+    status says so, copies and products are seen to end, and the context still runs a call."""
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = r"""
+import torch
+import ring_all_reduce_virtual_b200 as rrv
+for shapes in ([(64, 64), (128, 500), (100, 700)], [(300, 300)], [(1024, 512), (512, 2048), (100, 100), (700, 700)]):
+    for dt in (torch.float32, torch.bfloat16):
+        rrv.orthogonalize([torch.randn(s, device="cuda").to(dt) for s in shapes])
+        try:
+            rrv.check_timeouts()
+            print("NO TIMEOUT")
+        except rrv.RRError as e:
+            print("RAN OUT", e.status, "not seen to land: 0" in str(e))
+x = torch.randn(3, 500, device="cuda")
+got = rrv.token_logprobs([x], [torch.zeros(3, dtype=torch.int64, device="cuda")])
+print("CONTEXT OK", bool((got.lse[0] - torch.logsumexp(x, -1)).abs().max() < 1e-5))
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, env=dict(os.environ, RR_DEBUG_BULK_TIMEOUT="1"),
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.count("RAN OUT 4 True") == 6 and "CONTEXT OK True" in r.stdout, r.stdout + r.stderr
+
+
+def test_more_steps_and_mixed_kinds_than_a_small_block_holds():
+    """Fifty steps of a polynomial that keeps singular values where they are, lists whose kinds of iteration differ."""
+    coef = (1.5, -0.5, 0.0)
+    xs = [gradient(300, 200, torch.float32, 1), gradient(200, 300, torch.bfloat16, 2), gradient(256, 520, torch.float16, 3),
+          gradient(90, 90, torch.float32, 4)]
+    for g, x in zip(rrv.orthogonalize(xs, steps=50, coefficients=coef), xs):
+        check(g, x, steps=50, coef=coef)
+
+
+def test_statistics_of_a_call():
+    rrv.orthogonalize([gradient(64, 64, torch.float32)])
+    assert rrv.last_stats()["launches"] == 1
+    rrv.orthogonalize([gradient(300, 300, torch.float32)])
+    s = rrv.last_stats()
+    assert s["launches"] == 4 and s["steps"] == 5 and s["hbm_bytes"] == 2 * 300 * 300 * 4
+
+
+@pytest.mark.parametrize("r,c", [(128, 1024), (1024, 128), (129, 129), (128, 1025), (1025, 100), (1, 1024), (64, 65), (100, 129)])
+def test_shapes_around_what_a_cluster_takes(r, c):
+    for dt in TYPES.values():
+        x = gradient(r, c, dt, seed=r)
+        check(rrv.orthogonalize([x])[0], x)
+
+
+def test_offset_views_beside_aligned_ones():
+    """Matrices whose rows are whole vectors but whose addresses are not."""
+    for r, c in ((64, 64), (264, 512)):
+        base = torch.zeros(r * c + 8, device="cuda")
+        x = base[1:1 + r * c].view(r, c)
+        x.copy_(gradient(r, c, torch.float32))
+        outs = [[torch.empty(r, c, device="cuda")], [torch.empty(r * c + 4, device="cuda")[3:3 + r * c].view(r, c)]]
+        rrv.orthogonalize([x], outs)
+        check(outs[0][0], x)
+        assert torch.equal(outs[0][0], outs[1][0])
