@@ -333,12 +333,15 @@ __device__ __forceinline__ void fetch(uint4 (&r)[8], const uint16_t* from, int l
 
 // 64 columns of this thread's row of the sums: v[l] is column col + l.  The
 // warp's part of the blocks begins at c and out.
-__device__ __forceinline__ void put_block(float (&v)[64], const MuonOp& op, const Halves& c, const Halves& out, uint32_t row,
+struct Factors {
+    float alpha, beta, diag;
+};
+
+__device__ __forceinline__ void put_block(float (&v)[64], const Factors& f, const Halves& c, const Halves& out, uint32_t row,
                                           uint32_t col, uint32_t side, const OutRows& o, int lane)
 {
-    const float alpha = op.alpha, beta = op.beta, diag = op.diag;
 #pragma unroll
-    for (int l = 0; l < 64; ++l) v[l] *= alpha;
+    for (int l = 0; l < 64; ++l) v[l] *= f.alpha;
     if (c.hi) {
         uint4 r[8];
         fetch(r, c.hi, lane);
@@ -353,15 +356,15 @@ __device__ __forceinline__ void put_block(float (&v)[64], const MuonOp& op, cons
                 float a[8];
                 F16T::unpack(*o.piece(lane, g), a);
 #pragma unroll
-                for (int l = 0; l < 8; ++l) v[g * 8 + l] = __fmaf_rn(beta, a[l], v[g * 8 + l]);
+                for (int l = 0; l < 8; ++l) v[g * 8 + l] = __fmaf_rn(f.beta, a[l], v[g * 8 + l]);
             }
             __syncwarp();
         }
     }
-    if (diag != 0.0f && row < side && row / 64 == col / 64) {
+    if (f.diag != 0.0f && row < side && row / 64 == col / 64) {
 #pragma unroll
         for (int l = 0; l < 64; ++l)
-            if (col + l == row) v[l] += diag;
+            if (col + l == row) v[l] += f.diag;
     }
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
@@ -557,6 +560,17 @@ __device__ __forceinline__ bool take_tile(const P& p, Bars* b, uint32_t tmem, co
     const uint32_t unit = 2 * t.i + rank;  // of 128 rows
     const uint32_t row0 = unit * 128 + quarter * 32, col = t.j * t.per * 128 + col0;
     const bool mine = unit < t.mt;
+    // where the results go and what of, looked up while the products run
+    uint32_t nbj;
+    Halves out = buffer_of(*t.w, t.op->out, &nbj), c{nullptr, nullptr};
+    const uint64_t at = block_at(row0 / kBlk, col / kBlk, nbj) + row0 % kBlk * kBlk;
+    out = {out.hi + at, out.lo + at};
+    if (t.op->c != kNoBuffer) {
+        c = buffer_of(*t.w, t.op->c, &nbj);  // of out's shape
+        c = {c.hi + at, c.lo + at};
+    }
+    const uint32_t side = min(t.w->rows, t.w->cols);
+    const Factors f{t.op->alpha, t.op->beta, t.op->diag};
     float sum[COLS];
 #pragma unroll
     for (int l = 0; l < COLS; ++l) sum[l] = 0.0f;
@@ -579,22 +593,13 @@ __device__ __forceinline__ bool take_tile(const P& p, Bars* b, uint32_t tmem, co
         if (lane == 0) first_arrive(&b->taken[sums & 1]);
     }
     if (mine) {
-        uint32_t nbj;
-        Halves out = buffer_of(*t.w, t.op->out, &nbj), c{nullptr, nullptr};
-        const uint64_t at = block_at(row0 / kBlk, col / kBlk, nbj) + row0 % kBlk * kBlk;
-        out = {out.hi + at, out.lo + at};
-        if (t.op->c != kNoBuffer) {
-            c = buffer_of(*t.w, t.op->c, &nbj);  // of out's shape
-            c = {c.hi + at, c.lo + at};
-        }
-        const uint32_t side = min(t.w->rows, t.w->cols);
 #pragma unroll
         for (int h = 0; h < COLS / 64; ++h) {
             float v[64];
 #pragma unroll
             for (int l = 0; l < 64; ++l) v[l] = sum[h * 64 + l];
             constexpr uint64_t next = 2 * kBlkElems;  // the block beside it
-            put_block(v, *t.op, {c.hi ? c.hi + h * next : nullptr, c.lo + h * next}, {out.hi + h * next, out.lo + h * next}, row0 + lane,
+            put_block(v, f, {c.hi ? c.hi + h * next : nullptr, c.lo + h * next}, {out.hi + h * next, out.lo + h * next}, row0 + lane,
                       col + h * 64, side, o, lane);
         }
     }
