@@ -345,11 +345,19 @@ __global__ void __launch_bounds__(kThreads) logprob_kernel(const __grid_constant
     Stat st;
     st.order = __reduce_max_sync(kFull, edge || order ? order_of(run.m) : 0u);
     uint32_t tau = 0;
-    if constexpr (TOP) tau = warp_sorted(order);
+    if constexpr (TOP && kWarp) tau = warp_sorted(order);
     if constexpr (!kWarp) {
-        constexpr int kBest = 32 / (kThreads / 32);
         if (lane == 0) sh.order[warp] = st.order;
-        if (TOP && lane < kBest) sh.best[warp * kBest + lane] = tau;
+        if constexpr (TOP) {  // the warp's four largest, one after the other
+            constexpr int kBest = 32 / (kThreads / 32);
+            uint32_t rest = order;
+#pragma unroll
+            for (int i = 0; i < kBest; ++i) {
+                const uint32_t o = __reduce_max_sync(kFull, rest);
+                if (lane == 0) sh.best[warp * kBest + i] = o;
+                if (lane == __ffs(__ballot_sync(kFull, rest == o)) - 1) rest = 0;
+            }
+        }
         __syncthreads();
         st.order = __reduce_max_sync(kFull, sh.order[lane % (kThreads / 32)]);
         if constexpr (TOP) tau = warp_sorted(sh.best[lane]);  // every warp for itself
@@ -405,22 +413,29 @@ __global__ void __launch_bounds__(kThreads) logprob_kernel(const __grid_constant
             const uint32_t i = (uint32_t)(item / nwho), j = (uint32_t)(item % nwho);
             const uint32_t who = kWarp ? __fns(votes, 0, (int)j + 1) : sh.who[item < items ? j : 0];
             const uint64_t at = (uint64_t)v0 + (uint64_t)i * TEAM + who;
-            uint32_t ord[L];
-            uint32_t any = 0;
+            uint4 raw[1] = {};
+            bool hot = false;
             if (item < items && at < v1) {
-                float a[L];
-                Ty::unpack(xv[at], a);
-#pragma unroll
-                for (int l = 0; l < L; ++l) {
-                    ord[l] = order_of(a[l]);
-                    any |= (ord[l] >= tau ? 1u : 0u) << l;
-                }
+                raw[0] = xv[at];
+                hot = order_of(max_of<Ty, 1>(raw)) >= tau;
             }
-            uint32_t which = __reduce_or_sync(kFull, any);
-#pragma unroll
-            for (int l = 0; l < L; ++l)
-                if (which >> l & 1)
-                    list.offer(any >> l & 1 ? entry_of(ord[l], head + (uint32_t)at * L + l) : 0, p.k);
+            // a vector with one at or above tau: an element a lane
+            for (uint32_t hots = __ballot_sync(kFull, hot); hots; hots &= hots - 1) {
+                const int src = __ffs(hots) - 1;
+                const uint4 v = make_uint4(__shfl_sync(kFull, raw[0].x, src), __shfl_sync(kFull, raw[0].y, src),
+                                           __shfl_sync(kFull, raw[0].z, src), __shfl_sync(kFull, raw[0].w, src));
+                const uint32_t id = __shfl_sync(kFull, head + (uint32_t)at * L, src) + lane;
+                const int word = lane / (L / 4) & 3;
+                const uint32_t w = word == 0 ? v.x : word == 1 ? v.y : word == 2 ? v.z : v.w;
+                float a = __uint_as_float(w);
+                if constexpr (L == 8) {
+                    float lo, hi;
+                    Ty::unpack2(w, lo, hi);
+                    a = lane & 1 ? hi : lo;
+                }
+                const uint32_t o = order_of(a);
+                list.offer(lane < L && o >= tau ? entry_of(o, id) : 0, p.k);
+            }
         }
         best = list.mine;
         if constexpr (!kWarp) {
