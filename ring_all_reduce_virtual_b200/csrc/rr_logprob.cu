@@ -322,15 +322,23 @@ __global__ void __launch_bounds__(kThreads) logprob_kernel(const __grid_constant
     const uint4* xv = reinterpret_cast<const uint4*>(x + head);
 
     Running<Ty, ENT> run;
-    for (uint32_t v = v0 + tid; v < v1; v += TEAM * kU) {
-        uint4 raw[kU];
+    const auto load = [&](uint4 (&raw)[kU], uint32_t v) {
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
             const uint64_t at = (uint64_t)v + u * TEAM;
             raw[u] = lowest_vector<Ty>();
             if (at < v1) raw[u] = TOP ? xv[at] : __ldcs(xv + at);  // read again by the alternatives
         }
+    };
+    // the next vectors are on their way while these are summed (16384 rows of 32000
+    // bf16 with entropy: 181 -> 174 us; 20000 of 2000: 19.3 -> 17.7)
+    uint4 raw[kU], next[kU];
+    load(raw, v0 + tid);
+    for (uint32_t v = v0 + tid; v < v1; v += TEAM * kU) {
+        load(next, v + TEAM * kU);
         run.take(raw, c);
+#pragma unroll
+        for (int u = 0; u < kU; ++u) raw[u] = next[u];
     }
     const uint32_t order = v0 + tid < v1 ? order_of(run.m) : 0u;  // 0: a thread without vectors
     const bool edge = part == 0 && (uint32_t)tid < head + tail;
