@@ -414,13 +414,12 @@ __global__ void __launch_bounds__(kThreads) logprob_kernel(const __grid_constant
         // Every vector of the threads in question, one a lane: the i-th of
         // each, then the next of each, so that ids rise and a tie is refused by
         // the list at once.
-        const uint32_t each = (v1 - v0 + TEAM - 1) / TEAM;
-        const uint64_t items = (uint64_t)each * nwho;
-        for (uint64_t base = kWarp ? 0 : (uint64_t)warp * 32; base < items; base += TEAM) {
-            const uint64_t item = base + lane;
-            const uint32_t i = (uint32_t)(item / nwho), j = (uint32_t)(item % nwho);
-            const uint32_t who = kWarp ? __fns(votes, 0, (int)j + 1) : sh.who[item < items ? j : 0];
-            const uint64_t at = (uint64_t)v0 + (uint64_t)i * TEAM + who;
+        const uint32_t items = (v1 - v0 + TEAM - 1) / TEAM * nwho;  // at most 2^29 + 2^8
+        for (uint32_t base = kWarp ? 0 : warp * 32; base < items; base += TEAM) {
+            const uint32_t item = base + lane;
+            const uint32_t i = item / nwho, j = item - i * nwho;
+            const uint32_t who = kWarp ? __fns(votes, 0, (int)j + 1) : sh.who[j];
+            const uint32_t at = v0 + i * TEAM + who;
             uint4 raw[1] = {};
             bool hot = false;
             if (item < items && at < v1) {
@@ -432,7 +431,7 @@ __global__ void __launch_bounds__(kThreads) logprob_kernel(const __grid_constant
                 const int src = __ffs(hots) - 1;
                 const uint4 v = make_uint4(__shfl_sync(kFull, raw[0].x, src), __shfl_sync(kFull, raw[0].y, src),
                                            __shfl_sync(kFull, raw[0].z, src), __shfl_sync(kFull, raw[0].w, src));
-                const uint32_t id = __shfl_sync(kFull, head + (uint32_t)at * L, src) + lane;
+                const uint32_t id = __shfl_sync(kFull, head + at * L, src) + lane;
                 const int word = lane / (L / 4) & 3;
                 const uint32_t w = word == 0 ? v.x : word == 1 ? v.y : word == 2 ? v.z : v.w;
                 float a = __uint_as_float(w);
