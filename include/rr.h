@@ -652,7 +652,9 @@ rr_status_t rr_get_stats(rr_stats_t* out); /* last call on this host thread */
  * sets stage their tiles in shared memory with bulk async
  * copies when every rank's buffer sits at one 16-byte phase (on element
  * boundaries); their threads wait on an mbarrier for those
- * copies with an iteration limit instead of forever.  A wait that runs out --
+ * copies with an iteration limit instead of forever.  So do the threads of the
+ * orthogonalisation and the Muon step for copies and tensor core products, and
+ * for the tiles that a tile is made of.  A wait that runs out --
  * no working device lets it -- makes the whole CTA skip its tile (nothing of
  * that tile's result is written) and is counted on the device; one thread
  * then waits once more, bounded, for the tile's copies to land, and counts
@@ -661,8 +663,10 @@ rr_status_t rr_get_stats(rr_stats_t* out); /* last call on this host thread */
  * for zero on the device) and returns RR_ERR_TIMEOUT if either is not zero
  * (rr_last_error() gives both), RR_OK otherwise.  (A clipped sync or a
  * clipping that skipped a tile, in any of its passes, also reports a NaN norm;
- * its gradients are then undefined.)  No other kernel of the library
- * waits on anything but the hardware's barriers of its own CTA or cluster. */
+ * its gradients are then undefined.  An orthogonalisation or a Muon step counts
+ * each CTA that gave up as a tile; its results, weights and workspace are then
+ * undefined.)  No other kernel of the library waits on anything but the
+ * hardware's barriers of its own CTA or cluster. */
 rr_status_t rr_check_timeouts(void);
 const char* rr_status_string(rr_status_t status);
 const char* rr_last_error(void); /* detail of the last failure on this thread */

@@ -770,7 +770,9 @@ cudaError_t launch_muon_gemm(MuonGemmParams& p, int nops, cudaStream_t s)
     const BulkParams bp = bulk_params(rp);
     p.waits = rp.waits;
     p.hold = bp.hold;
-    p.spin = bp.spin;
+    // A tile may wait for a whole level of its matrix, which of the largest that fit
+    // the memory takes a second or two.
+    p.spin = bp.hold ? bp.spin : 1u << 26;
     // Tiles of 256 columns where every pair of SMs has one (of a level's squares,
     // most of the levels; then of each other kind for itself); narrower ones, twice
     // as many, are done sooner.
