@@ -133,16 +133,18 @@ rr_status_t make_plan(const rr_newton_schulz_t* ns, Plan* p)
 // more so the longer the matrix, and none for a square one.  But D (D A)
 // multiplies what A was rounded by, up to a^2 a step, where its eigenvalues are
 // small.  Measured error of five steps against 64 bits, segments of 5 / 3 + 2 /
-// 1 each, from noise to few directions in little noise (rank 1/16 of the side):
-// 2e-6..4e-4 / 2e-6..2e-5 / 1e-6..2e-5 (fp32's own: the last).  So a result of
-// fp32 has a segment per step; bf16's, which are rounded by 1.7e-3, have A's
-// errors grow by 3e4 at most (5 steps of the usual coefficients); fp16's (2e-4)
-// and fp32 weights, of which the result is a small part, by 200 (3 steps).
+// 2 + 2 + 1 / 1 each, from noise to few directions in little noise (rank 1/16 of
+// the side): 2e-6..4e-4 / 2e-6..2e-5 / 2e-6..1e-5 / 1e-6..7e-6, the same steps in
+// plain fp32 2e-6..2e-5.  So A's errors may grow by 3e4 (5 steps of the usual
+// coefficients) for bf16 results, which are rounded by 1.7e-3; by 200 (3 steps) for
+// fp16's (2e-4) and for fp32 weights, of which the result is a small part; and by
+// 12.5 (2 steps: 4 layers of width 2048 in 17.3 ms instead of 22.7) for results of
+// fp32 from 192 rows on, below which plain fp32 errs less than that.
 enum Exactness { kExact = 0, kClose = 1, kCoarse = 2 };
 
 std::vector<int> segments_of(const Plan& plan, uint32_t m, uint32_t n, Exactness exact)
 {
-    const double limit = exact == kExact ? 0.0 : exact == kClose ? 200.0 : 3e4;
+    const double limit = exact == kExact ? (m < 192 ? 0.0 : 12.5) : exact == kClose ? 200.0 : 3e4;
     const double grow = std::max(1.0, (double)plan.a * plan.a);
     int most = 1;
     for (double g = grow; g <= limit && most < plan.steps; g *= grow) ++most;

@@ -96,7 +96,7 @@ def test_workspace():
     one = need(((2048, 2048),), (0,))
     assert one >= 4 * 2 * 2 * 2048 * 2048  # X twice, A and B
     # several steps on one A keep three more m x m matrices
-    assert need(((2048, 8192),), (1,)) - need(((2048, 8192),), (0,)) == 3 * 2 * 2 * 2048 * 2048
+    assert need(((150, 8192),), (1,)) - need(((150, 8192),), (0,)) == 3 * 2 * 2 * 256 * 256
     assert need(((2048, 8192),), (0,), weights=1) == need(((2048, 8192),), (1,))
     assert need(((2048, 2048),), (1,), n=ns(steps=0)) < one / 3
     # the workspace does not grow with the list beyond a group's
