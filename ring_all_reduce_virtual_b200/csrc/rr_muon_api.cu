@@ -137,14 +137,20 @@ rr_status_t make_plan(const rr_newton_schulz_t* ns, Plan* p)
 // the side): 2e-6..4e-4 / 2e-6..2e-5 / 2e-6..1e-5 / 1e-6..7e-6, the same steps in
 // plain fp32 2e-6..2e-5.  So A's errors may grow by 3e4 (5 steps of the usual
 // coefficients) for bf16 results, which are rounded by 1.7e-3; by 200 (3 steps) for
-// fp16's (2e-4) and for fp32 weights, of which the result is a small part; and by
-// 12.5 (2 steps: 4 layers of width 2048 in 17.3 ms instead of 22.7) for results of
-// fp32 from 192 rows on, below which plain fp32 errs less than that.
-enum Exactness { kExact = 0, kClose = 1, kCoarse = 2 };
+// fp16's (2e-4) and for fp32 weights of 512 rows and more, of which the result is a
+// small part (three layers of width 512 / 1024: 442 / 1466 us, with 2 steps 490 /
+// 1686); by 12.5 (2 steps) for smaller ones, whose part is larger (width 230: the
+// weights 6.6e-7 off in 269 us, with 3 steps 1.8e-6 in 261), and for results of fp32
+// from 192 rows on (4 layers of width 2048 in 17.3 ms instead of 22.7), below which
+// plain fp32 errs less than that.
+enum Exactness { kExact, kWeight, kClose, kCoarse };
 
 std::vector<int> segments_of(const Plan& plan, uint32_t m, uint32_t n, Exactness exact)
 {
-    const double limit = exact == kExact ? (m < 192 ? 0.0 : 12.5) : exact == kClose ? 200.0 : 3e4;
+    const double limit = exact == kExact    ? (m < 192 ? 0.0 : 12.5)
+                         : exact == kWeight ? (m < 512 ? 12.5 : 200.0)
+                         : exact == kClose  ? 200.0
+                                            : 3e4;
     const double grow = std::max(1.0, (double)plan.a * plan.a);
     int most = 1;
     for (double g = grow; g <= limit && most < plan.steps; g *= grow) ++most;
@@ -188,7 +194,8 @@ int products_in(const std::vector<int>& segments)
 Exactness exactness(const rr_matrix_list_t* out, int t, bool weights)
 {
     if (out->dtypes[t] == RR_BF16) return kCoarse;
-    return out->dtypes[t] == RR_F16 || weights ? kClose : kExact;
+    if (out->dtypes[t] == RR_F16) return kClose;
+    return weights ? kWeight : kExact;
 }
 
 std::vector<int> segments_for(const Plan& plan, const rr_matrix_list_t* out, int t, bool weights)
