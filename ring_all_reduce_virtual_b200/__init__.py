@@ -557,7 +557,7 @@ def _logit_set(tensors, what: str):
     if n < 1 or n > MAX_RANKS:
         raise ValueError(f"{what}: need 1..{MAX_RANKS} logit tensors, got {n}")
     t0 = tensors[0]
-    shape, dtype, device = t0.shape, t0.dtype, t0.device
+    shape, dtype, index = t0.shape, t0.dtype, t0.get_device()  # -1 off the GPUs
     if len(shape) < 2 or shape[-1] == 0:
         raise ValueError(f"{what}: logits need two axes or more, the last not empty")
     V = shape[-1]
@@ -566,12 +566,12 @@ def _logit_set(tensors, what: str):
     stride = V if packed else t0.stride(0) if len(shape) == 2 and t0.stride(1) == 1 and rows > 1 else 0
     arr = (ctypes.c_void_p * n)()
     for i, t in enumerate(tensors):
-        if not t.is_cuda or t is not t0 and (t.shape != shape or t.dtype != dtype or t.device != device):
+        if index < 0 or t is not t0 and (t.get_device() != index or t.shape != shape or t.dtype != dtype):
             raise ValueError(f"{what}: logit tensors must be CUDA tensors of one shape, dtype and device")
         if stride < V or (not t.is_contiguous() if packed else t.stride() != (stride, 1)):
             raise ValueError(f"{what}: logits must be contiguous, or 2-D with contiguous rows and one row stride")
         arr[i] = t.data_ptr()
-    return arr, n, rows, V, stride, _dtype_code(dtype), device
+    return arr, n, rows, V, stride, _dtype_code(dtype), t0.device
 
 
 def token_logprobs(logits, tokens, scale: float = 1.0, entropy: bool = False, top_k: int = 0, stream=None) -> TokenLogprobs:
@@ -598,7 +598,7 @@ def token_logprobs(logits, tokens, scale: float = 1.0, entropy: bool = False, to
     # one allocation for the values: each costs a microsecond, a small call's kernel ten
     M = n * T
     count = 3 if entropy else 2
-    values = torch.empty_strided((count, n, T), (M, T, 1), dtype=torch.float32, device=dev)
+    values = torch.empty_strided((count * n, T), (T, 1), dtype=torch.float32, device=dev)
     at = values.data_ptr()
     ent = at + 8 * M if entropy else None
     if k:
@@ -612,7 +612,7 @@ def token_logprobs(logits, tokens, scale: float = 1.0, entropy: bool = False, to
         st = lib().rr_token_logprobs(x, stride, ids, id_type, n, T, V, d, float(scale), at, at + 4 * M, ent, 0, None, None, raw(index))
     if st:
         check(st, "token_logprobs")
-    out = values.unbind(0)
+    out = torch.unsafe_split_with_sizes(values, (n,) * count)  # a little cheaper than unbind
     return TokenLogprobs(out[0], out[1], out[2] if entropy else None, ids_out, tops)
 
 
