@@ -568,7 +568,8 @@ typedef struct rr_muon {
  *     U = G + momentum * M (nesterov) or M
  *     W_r = round((1 - lr * weight_decay) * W_0 - lr * f * O)   on every rank r
  * with O = U orthogonalised (rr_orthogonalize; U in fp32, O not rounded on the
- * way, for fp32 weights as for fp16 results) and f the shape's factor.  params: nranks replicas, of
+ * way, and as near as for fp16 results or nearer for fp32 weights) and f the
+ * shape's factor.  params: nranks replicas, of
  * which rank 0's is read and all are written; grads: rank 0's are read;
  * momenta: one rank, fp32, kept by the caller from step to step (zeros at
  * first).  All three list the same shapes; types may differ from list to list.

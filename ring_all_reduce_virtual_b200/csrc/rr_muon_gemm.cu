@@ -773,11 +773,11 @@ cudaError_t launch_muon_gemm(MuonGemmParams& p, int nops, cudaStream_t s)
     // A tile may wait for a whole level of its matrix, which of the largest that fit
     // the memory takes a second or two.
     p.spin = bp.hold ? bp.spin : 1u << 26;
-    // Tiles of 256 columns where they keep half of the pairs of SMs busy (with a
-    // level's squares, most of the levels; then for each other kind where every pair
-    // has one); narrower ones, twice as many, are done sooner.  One / four layers of
-    // width 512, bf16, in tiles of 256: 302 / 377 us, of 128: 245 / 408; two of 1000,
-    // fp16: 924 and 1108.
+    // Tiles of 256 columns where those of a square product, which most levels are,
+    // keep half of the pairs of SMs busy, and for Q X where every pair has one;
+    // narrower ones, twice as many, are done sooner.  One / four layers of width 512,
+    // bf16, in tiles of 256: 302 / 377 us, of 128: 245 / 408; two of 1000, fp16: 924
+    // and 1108.
     const bool wide = tiles_of_all(p, kSquare, 256) >= kPairs / 2;
     uint32_t widest = 0;
     for (int kind = 0; kind < 3; ++kind) {

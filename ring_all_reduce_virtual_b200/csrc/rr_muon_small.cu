@@ -277,7 +277,8 @@ __global__ void __launch_bounds__(kThreads, 1) muon_small_kernel(const __grid_co
         }
         cluster_sync();
         // 16 rows at a time, of every CTA's sums, in the order of the CTAs: two
-        // groups, four CTAs' values on the way (the summing and handing out takes 5 us of a step's 14 in four CTAs: 112 KB a CTA between SMs)
+        // groups, four CTAs' values on the way (the summing and handing out takes 5 us
+        // of a step's 14 in four CTAs: 112 KB a CTA between SMs)
 #pragma unroll 1
         for (uint32_t group = rank; group < kSide / 16; group += 2 * used) {
             const uint32_t c = tid % 16 * 8;

@@ -361,3 +361,22 @@ def test_offset_views_beside_aligned_ones():
         rrv.orthogonalize([x], outs)
         check(outs[0][0], x)
         assert torch.equal(outs[0][0], outs[1][0])
+
+
+@pytest.mark.parametrize("r,c", [(230, 920), (690, 230), (920, 230), (511, 1500), (512, 1500)])
+def test_small_fp32_weights_keep_their_precision(r, c):
+    """The result's share of a small weight is large: O errs by 2e-5 of its norm at
+    most, and the update's two roundings are half a step of fp32 each."""
+    gen = torch.Generator(device="cuda").manual_seed(r + c)
+    k = min(r, c) // 16
+    noise = torch.randn(r, c, generator=gen, device="cuda")
+    strong = torch.randn(r, k, generator=gen, device="cuda") @ torch.randn(k, c, generator=gen, device="cuda")
+    g = (noise + strong / math.sqrt(k)) * 1e-3
+    w = torch.randn(r, c, generator=gen, device="cuda") * 0.02
+    m = torch.zeros(r, c, device="cuda")
+    o, _ = iterate(g.double() * 1.95)
+    f = 0.02 * math.sqrt(max(1.0, r / c))
+    want = w.double() * (1.0 - 0.02 * 0.01) - f * o
+    rrv.muon_step([w], [g], [m], lr=0.02, weight_decay=0.01)
+    err = float((w.double() - want).norm())
+    assert err <= f * 2e-5 * float(o.norm()) + 2.0 ** -23 * float(want.norm()), (err, float(o.norm()), float(want.norm()))
