@@ -535,7 +535,7 @@ typedef struct rr_newton_schulz {
 /* The bytes of device workspace the calls below need (host only) for their
  * list of results (weights 0: rr_orthogonalize) or weights (1: rr_muon_step):
  * 256-byte aligned, contents neither used nor kept, one call at a time (see
- * rr_clip_workspace).  Matrices run in groups of up to 24 and 5 GiB of it. */
+ * rr_clip_workspace).  Matrices run in groups of up to 128 and 5 GiB of it. */
 rr_status_t rr_muon_workspace(const rr_matrix_list_t* results, int weights, const rr_newton_schulz_t* ns, size_t* bytes);
 
 /* Orthogonalises every matrix of `matrices` (its rank 0) into every rank's

@@ -10,6 +10,8 @@
 // (201 M elements) they move 12 + 4 bytes and more an element.  The norm is
 // summed as the gradient norm is (rr_clip.cuh: right over fp32's range, fp64
 // partial sums joined in a fixed order).
+#include <algorithm>
+
 #include <cuda_fp16.h>
 
 #include "rr_clip.cuh"
@@ -21,33 +23,32 @@ namespace rr {
 
 namespace {
 
-__device__ __forceinline__ int mat_of_part(const MuonPrepParams& p, uint32_t part)
-{
-    int k = 0;
-    while (k + 1 < p.n && p.mat[k + 1].part0 <= part) ++k;
-    return k;
-}
-
+// The last matrix that begins (a partial sum, or a tile) at `at` or before.
 template <class P>
-__device__ __forceinline__ int mat_of_tile(const P& p, uint32_t tile)
+__device__ __forceinline__ int mat_at(const P& p, uint32_t MuonMat::*begin, uint32_t at)
 {
-    int k = 0;
-    while (k + 1 < p.n && p.mat[k + 1].tile0 <= tile) ++k;
-    return k;
+    int low = 0, high = p.n;
+    while (high - low > 1) {
+        const int mid = (low + high) / 2;
+        if (p.mat[mid].*begin <= at) low = mid;
+        else high = mid;
+    }
+    return low;
 }
 
-__device__ __forceinline__ float updated(float g, float m, const MuonPrepParams& p)
+__device__ __forceinline__ float updated(float g, float m, const MuonPrepHead& p)
 {
     return p.nesterov ? __fmaf_rn(p.momentum, m, g) : m;
 }
 
 // One CTA per partial sum: the tiles of its matrix part, part + parts, ...
-__global__ void __launch_bounds__(kThreads) muon_squares_kernel(const __grid_constant__ MuonPrepParams p)
+template <class P>
+__global__ void __launch_bounds__(kThreads) muon_squares_kernel(const __grid_constant__ P p)
 {
     __shared__ double sh[kThreads / 32];
     pdl_begin();
     if (blockIdx.x == 0 && threadIdx.x < kMuonCounters) p.counters[threadIdx.x] = 0;
-    const MuonMat& t = p.mat[mat_of_part(p, blockIdx.x)];
+    const MuonMat& t = p.mat[mat_at(p, &MuonMat::part0, blockIdx.x)];
     const uint64_t len = (uint64_t)t.rows * t.cols;
     double acc = 0.0;
     muon_with_type(t.dtype, [&]<class Ty>() {
@@ -79,11 +80,12 @@ __global__ void __launch_bounds__(kThreads) muon_squares_kernel(const __grid_con
 }
 
 // 128 rows x 64 columns of X, split into halves.
-__global__ void __launch_bounds__(kThreads) muon_pack_kernel(const __grid_constant__ MuonPrepParams p)
+template <class P>
+__global__ void __launch_bounds__(kThreads) muon_pack_kernel(const __grid_constant__ P p)
 {
     __shared__ double sh[kThreads / 32];
     pdl_begin();
-    const MuonMat& t = p.mat[mat_of_tile(p, blockIdx.x)];
+    const MuonMat& t = p.mat[mat_at(p, &MuonMat::tile0, blockIdx.x)];
     const uint32_t nbj = pad_up(t.cols) / kBlk;
     const uint32_t tile = blockIdx.x - t.tile0, ti = tile / nbj, tj = tile % nbj;
     const MuonScale f = muon_scale(sqrt(partials_sum(p.partial + t.part0, t.parts, sh)) + (double)p.eps, p.scale);
@@ -121,10 +123,11 @@ __global__ void __launch_bounds__(kThreads) muon_pack_kernel(const __grid_consta
 }
 
 // 128 rows x 64 columns of the result.
-__global__ void __launch_bounds__(kThreads) muon_finish_kernel(const __grid_constant__ MuonFinishParams p)
+template <class P>
+__global__ void __launch_bounds__(kThreads) muon_finish_kernel(const __grid_constant__ P p)
 {
     pdl_begin();
-    const MuonMat& t = p.mat[mat_of_tile(p, blockIdx.x)];
+    const MuonMat& t = p.mat[mat_at(p, &MuonMat::tile0, blockIdx.x)];
     const uint32_t nbj = pad_up(t.cols) / kBlk;
     const uint32_t tile = blockIdx.x - t.tile0, ti = tile / nbj, tj = tile % nbj;
     muon_with_type(t.out_dtype, [&]<class Ty>() {
@@ -152,21 +155,39 @@ __global__ void __launch_bounds__(kThreads) muon_finish_kernel(const __grid_cons
     });
 }
 
+// f on the parameters of few matrices, or on all.
+template <class F>
+cudaError_t with_prep(const MuonPrepParams& p, F&& f)
+{
+    if (p.n > kMuonMatsSmall) return f(p);
+    MuonPrepParamsT<kMuonMatsSmall> q;
+    static_cast<MuonPrepHead&>(q) = p;
+    std::copy_n(p.mat, p.n, q.mat);
+    return f(q);
+}
+
 }  // namespace
 
 cudaError_t launch_muon_squares(const MuonPrepParams& p, uint32_t parts, cudaStream_t s)
 {
-    return launch_pdl(muon_squares_kernel, dim3(parts), kThreads, 0, s, p);
+    return with_prep(p, [&]<class P>(const P& q) { return launch_pdl(muon_squares_kernel<P>, dim3(parts), kThreads, 0, s, q); });
 }
 
 cudaError_t launch_muon_pack(const MuonPrepParams& p, uint32_t tiles, cudaStream_t s)
 {
-    return launch_pdl(muon_pack_kernel, dim3(tiles), kThreads, 0, s, p);
+    return with_prep(p, [&]<class P>(const P& q) { return launch_pdl(muon_pack_kernel<P>, dim3(tiles), kThreads, 0, s, q); });
 }
 
 cudaError_t launch_muon_finish(const MuonFinishParams& p, uint32_t tiles, cudaStream_t s)
 {
-    return launch_pdl(muon_finish_kernel, dim3(tiles), kThreads, 0, s, p);
+    if (p.n > kMuonMatsSmall || p.n * p.nranks > kMuonPtrsSmall)
+        return launch_pdl(muon_finish_kernel<MuonFinishParams>, dim3(tiles), kThreads, 0, s, p);
+    using Few = MuonFinishParamsT<kMuonMatsSmall, kMuonPtrsSmall>;
+    Few q;
+    static_cast<MuonFinishHead&>(q) = p;
+    std::copy_n(p.mat, p.n, q.mat);
+    std::copy_n(p.out, p.n * p.nranks, q.out);
+    return launch_pdl(muon_finish_kernel<Few>, dim3(tiles), kThreads, 0, s, q);
 }
 
 }  // namespace rr

@@ -77,27 +77,32 @@ struct MuonWork {
     uint16_t op0, ops;           // its products in MuonGemmParams::op, in the order of their levels
 };
 
-constexpr int kMuonMats = 24;         // matrices per group
+// Matrices per group, and per launch that takes them whole.  While one waits for a
+// level of its own, others have tiles: 24 layers of width 256, bf16, in groups of 24
+// / 128: 907 / 442 us, 12 of 1024: 4448 / 4398.
+constexpr int kMuonMats = 128;
 constexpr int kMuonOps = 200;         // different products of a launch, at most
-constexpr int kMuonOpsSmall = 60;     // a parameter block below 4 KB: larger ones cost the host 3-5 us
-constexpr int kMuonSeq = 768;         // products of a launch in all
-constexpr int kMuonSeqSmall = 512;
-constexpr uint32_t kMuonCounters = 32;  // words of the workspace: the next tile, each matrix's finished parts
+constexpr int kMuonSeq = 768;         // products of a launch, those of like matrices counted once
+// Of parameter blocks below 4 KB: larger ones cost the host 3-5 us.
+constexpr int kMuonMatsSmall = 24, kMuonOpsSmall = 60, kMuonSeqSmall = 400;
+constexpr uint32_t kMuonCounters = 160;  // words of the workspace: the next tile, each matrix's finished parts
 constexpr uint32_t kNormParts = 256;  // partial sums of squares per matrix, at most
 constexpr uint32_t kPrepTile = 8192;  // elements of a tile of the first pass
 
-template <int OPS, int SEQ>
-struct MuonGemmParamsT {
-    MuonWork work[kMuonMats];
-    MuonOp op[OPS];
-    uint16_t seq[SEQ];     // the products in order: matrix | (its product's number) << 5
-    uint32_t nseq;
+struct MuonGemmHead {
+    uint32_t n, nseq;
     uint32_t tile_n[3];    // of each kind of product: 128 or 256
     uint32_t* counters;
     unsigned int* waits;   // bulk_wait_counters()
     uint32_t hold, spin;   // as in BulkParams
 };
-using MuonGemmParams = MuonGemmParamsT<kMuonOps, kMuonSeq>;
+template <int MATS, int OPS, int SEQ>
+struct MuonGemmParamsT : MuonGemmHead {
+    MuonWork work[MATS];
+    MuonOp op[OPS];
+    uint32_t seq[SEQ];     // the products in order, of neighbouring matrices of one shape: first | how many << 8 | number << 16
+};
+using MuonGemmParams = MuonGemmParamsT<kMuonMats, kMuonOps, kMuonSeq>;
 
 // Sides of a matrix's product, in units of 128 rows and columns, and its tiles.
 struct MuonSides {
@@ -141,8 +146,7 @@ struct MuonMat {
     float factor;          // muon: lr * the shape's factor
 };
 
-struct MuonPrepParams {
-    MuonMat mat[kMuonMats];
+struct MuonPrepHead {
     int n;
     double* partial;
     uint32_t* counters;    // zeroed by the first pass
@@ -151,16 +155,25 @@ struct MuonPrepParams {
     float eps;
     float scale;           // of the first X
 };
+template <int MATS>
+struct MuonPrepParamsT : MuonPrepHead {
+    MuonMat mat[MATS];
+};
+using MuonPrepParams = MuonPrepParamsT<kMuonMats>;
 
-constexpr int kMuonPtrs = 128;
-struct MuonFinishParams {
-    MuonMat mat[kMuonMats];
+constexpr int kMuonPtrs = 1024, kMuonPtrsSmall = 128;  // outputs of a launch
+struct MuonFinishHead {
     int n;
     int nranks;            // outputs per matrix
     float inv;             // 1 / the scale of X
     float keep;            // muon: 1 - lr * weight decay
-    void* out[kMuonPtrs];  // matrix-major
 };
+template <int MATS, int PTRS>
+struct MuonFinishParamsT : MuonFinishHead {
+    MuonMat mat[MATS];
+    void* out[PTRS];       // matrix-major
+};
+using MuonFinishParams = MuonFinishParamsT<kMuonMats, kMuonPtrs>;
 
 // Matrices that one launch takes whole (rr_muon_small.cu): a cluster each.
 constexpr uint32_t kMuonSmallSide = 128, kMuonSmallCtas = 8;
@@ -171,8 +184,7 @@ struct MuonSmallStep {
     float gram, poly, poly_a, apply, apply_x;
 };
 
-struct MuonSmallParams {
-    MuonMat mat[kMuonMats];  // x, part0, parts and tile0 unused
+struct MuonSmallHead {
     int n;
     uint32_t ctas;           // per cluster: of the longest matrix
     int nranks;
@@ -182,8 +194,13 @@ struct MuonSmallParams {
     unsigned int* waits;     // bulk_wait_counters()
     uint32_t hold, spin;     // as in BulkParams
     MuonSmallStep step[kMuonMaxSteps];
-    void* out[kMuonPtrs];    // matrix-major
 };
+template <int MATS, int PTRS>
+struct MuonSmallParamsT : MuonSmallHead {
+    MuonMat mat[MATS];       // x, part0, parts and tile0 unused
+    void* out[PTRS];         // matrix-major
+};
+using MuonSmallParams = MuonSmallParamsT<kMuonMats, kMuonPtrs>;
 
 cudaError_t launch_muon_squares(const MuonPrepParams& p, uint32_t parts, cudaStream_t s);
 cudaError_t launch_muon_pack(const MuonPrepParams& p, uint32_t tiles, cudaStream_t s);

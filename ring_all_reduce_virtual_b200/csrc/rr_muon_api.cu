@@ -3,6 +3,7 @@
 // iteration's scales, the order of the products, groups of matrices.
 #include <cmath>
 #include <memory>
+#include <tuple>
 
 #include "rr_host.h"
 #include "rr_muon.h"
@@ -179,8 +180,9 @@ Room room_of(const Shape& s, const std::vector<int>& segments)
 uint32_t parts_of(const Shape& s) { return (uint32_t)std::min<uint64_t>(kNormParts, ceil_div(s.numel(), kPrepTile)); }
 
 constexpr uint64_t kPartialBytes = (uint64_t)kMuonMats * kNormParts * sizeof(double);
-constexpr uint64_t kHeadBytes = kPartialBytes + 256;  // and the counters
-static_assert(kMuonCounters * 4 <= 256 && kMuonMats < (int)kMuonCounters && kMuonMats <= 32, "a counter per matrix and one more");
+constexpr uint64_t kHeadBytes = kPartialBytes + 1024;  // and the counters
+static_assert(kMuonCounters * 4 <= 1024 && kMuonMats < (int)kMuonCounters, "a counter per matrix and one more");
+static_assert(kMuonMats < 256 && kMuonOps <= 256, "fields of MuonGemmParams::seq");
 
 // Products of a matrix.
 int products_in(const std::vector<int>& segments)
@@ -215,6 +217,7 @@ std::vector<std::vector<int>> groups_of(const rr_matrix_list_t* l, const Plan& p
 {
     std::vector<std::vector<int>> groups;
     std::vector<std::pair<std::vector<int>, bool>> kinds;
+    std::vector<std::pair<Shape, size_t>> classes;  // and kind
     uint64_t used = 0;
     int listed = 0, ops = 0;
     *bytes = 256;
@@ -225,16 +228,24 @@ std::vector<std::vector<int>> groups_of(const rr_matrix_list_t* l, const Plan& p
         const uint64_t need = room_of(s, segments).bytes();
         const int products = products_in(segments);
         const std::pair<std::vector<int>, bool> kind{segments, exactness(l, t, weights) == kExact};
-        const bool seen = std::find(kinds.begin(), kinds.end(), kind) != kinds.end();
+        const auto number = [&] { return (size_t)(std::find(kinds.begin(), kinds.end(), kind) - kinds.begin()); };
+        const auto like = [&] {
+            return std::any_of(classes.begin(), classes.end(),
+                               [&](const auto& e) { return e.first.rows == s.rows && e.first.cols == s.cols && e.second == number(); });
+        };
         if (groups.empty() || groups.back().size() == kMuonMats || used + need > kGroupBytes ||
-            listed + products > kMuonSeq || (!seen && ops + products > kMuonOps)) {
+            (!like() && listed + products > kMuonSeq) || (number() == kinds.size() && ops + products > kMuonOps)) {
             groups.emplace_back();
             used = kHeadBytes;
             listed = ops = 0;
             kinds.clear();
+            classes.clear();
         }
-        listed += products;
-        if (std::find(kinds.begin(), kinds.end(), kind) == kinds.end()) {
+        if (!like()) {
+            listed += products;
+            classes.push_back({s, number()});
+        }
+        if (number() == kinds.size()) {
             kinds.push_back(kind);
             ops += products;
         }
@@ -394,9 +405,14 @@ rr_status_t run_small(const Job& job, const Plan& plan, const std::vector<int>& 
     return RR_OK;
 }
 
-rr_status_t run_group(const Job& job, const Plan& plan, const std::vector<int>& group, char* ws, cudaStream_t stream)
+rr_status_t run_group(const Job& job, const Plan& plan, std::vector<int> group, char* ws, cudaStream_t stream)
 {
     const int n = (int)group.size();
+    // matrices alike follow one another, and are listed as one
+    std::stable_sort(group.begin(), group.end(), [&](int a, int b) {
+        const rr_matrix_list_t& l = *job.out;
+        return std::tie(l.rows[a], l.cols[a], l.dtypes[a]) < std::tie(l.rows[b], l.cols[b], l.dtypes[b]);
+    });
     std::unique_ptr<MuonPrepParams> prep(new MuonPrepParams{});
     std::unique_ptr<MuonGemmParams> gemm(new MuonGemmParams);  // as it comes: every field that counts is set
     std::vector<Halves> result(n);
@@ -465,18 +481,21 @@ rr_status_t run_group(const Job& job, const Plan& plan, const std::vector<int>& 
         uint32_t depth, at;
     };
     std::vector<Item> list;
-    for (int k = 0; k < n; ++k) {
+    for (int k = 0, next; k < n; k = next) {
         const MuonWork& w = gemm->work[k];
+        for (next = k + 1; next < n && gemm->work[next].rows == w.rows && gemm->work[next].cols == w.cols && gemm->work[next].op0 == w.op0;)
+            ++next;
         for (int o = 0; o < w.ops; ++o) {
             const MuonOp& q = gemm->op[w.op0 + o];
             const uint32_t depth = q.kind == kGram ? std::max(w.rows, w.cols) : shape[k].small();
-            list.push_back({q.level, depth, (uint32_t)(k | o << 5)});
+            list.push_back({q.level, depth, (uint32_t)(k | (next - k) << 8 | o << 16)});
         }
     }
     std::stable_sort(list.begin(), list.end(),
                      [](const Item& a, const Item& b) { return a.level != b.level ? a.level < b.level : a.depth > b.depth; });
+    gemm->n = (uint32_t)n;
     gemm->nseq = (uint32_t)list.size();
-    for (size_t k = 0; k < list.size(); ++k) gemm->seq[k] = (uint16_t)list[k].at;
+    for (size_t k = 0; k < list.size(); ++k) gemm->seq[k] = list[k].at;
     e = timed_launch([&] { return launch_muon_gemm(*gemm, nops, stream); });
     if (e != cudaSuccess) return cuda_fail(e, "Newton-Schulz product launch");
     t_stats.launches += gemm->nseq > 0 ? 1 : 0;

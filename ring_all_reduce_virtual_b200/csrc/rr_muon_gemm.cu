@@ -79,7 +79,7 @@ constexpr uint32_t kFull = 0xffffffffu;
 struct Slot {
     uint32_t seq;   // in the list of products; kEnd: no more tiles
     uint32_t i, j;  // the tile: 256 rows, tile_n columns
-    uint32_t pad_;
+    uint32_t mat;
 };
 
 struct Bars {
@@ -200,10 +200,9 @@ template <class P>
 __device__ __forceinline__ Tile tile_at(const P& p, const Slot& s)
 {
     Tile t;
-    const uint32_t e = p.seq[s.seq];
-    t.mat = e & 31u;
-    t.w = &p.work[t.mat];
-    t.op = &p.op[t.w->op0 + (e >> 5)];
+    t.mat = s.mat;
+    t.w = &p.work[s.mat];
+    t.op = &p.op[t.w->op0 + (p.seq[s.seq] >> 16)];
     const MuonSides sides = muon_sides(t.w->rows, t.w->cols, t.op->kind);
     t.i = s.i;
     t.j = s.j;
@@ -215,13 +214,13 @@ __device__ __forceinline__ Tile tile_at(const P& p, const Slot& s)
     return t;
 }
 
-// Tiles of product k of the list.
+// Tiles of product k of the list, of one matrix.
 template <class P>
 __device__ __forceinline__ uint32_t tiles_of(const P& p, uint32_t k)
 {
     const uint32_t e = p.seq[k];
-    const MuonWork& w = p.work[e & 31u];
-    const int kind = p.op[w.op0 + (e >> 5)].kind;
+    const MuonWork& w = p.work[e & 255u];
+    const int kind = p.op[w.op0 + (e >> 16)].kind;
     return muon_tiles(w.rows, w.cols, kind, p.tile_n[kind]);
 }
 
@@ -259,14 +258,14 @@ __device__ __forceinline__ void tell(const Slot& s, uint32_t n, Bars* b)
     const uint32_t k = n % kSlots, at = muon_smem(&b->slot[k]), bar = muon_smem(&b->told[k]);
     asm volatile(
         "{\n\t.reg .b32 a, r;\n\t"
-        "st.shared.v4.b32 [%0], {%2, %3, %4, %2};\n\t"
+        "st.shared.v4.b32 [%0], {%2, %3, %4, %5};\n\t"
         "mapa.shared::cluster.u32 r, %1, 0;\n\t"
         "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [r];\n\t"
         "mapa.shared::cluster.u32 a, %0, 1;\n\t"
-        "st.shared::cluster.v4.b32 [a], {%2, %3, %4, %2};\n\t"
+        "st.shared::cluster.v4.b32 [a], {%2, %3, %4, %5};\n\t"
         "mapa.shared::cluster.u32 r, %1, 1;\n\t"
         "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [r];\n\t}" ::"r"(at),
-        "r"(bar), "r"(s.seq), "r"(s.i), "r"(s.j)
+        "r"(bar), "r"(s.seq), "r"(s.i), "r"(s.j), "r"(s.mat)
         : "memory");
 }
 
@@ -275,12 +274,13 @@ __device__ __forceinline__ bool hear(Slot& s, uint32_t n, Bars* b, unsigned int*
 {
     const uint32_t k = n % kSlots;
     s.seq = kEnd;
-    s.i = s.j = 0;
+    s.i = s.j = s.mat = 0;
     if (!wait_for(&b->told[k], (n / kSlots) & 1, b, waits, spin)) return false;
     volatile Slot* v = &b->slot[k];
     s.seq = v->seq;
     s.i = v->i;
     s.j = v->j;
+    s.mat = v->mat;
     first_arrive(&b->heard[k]);
     return s.seq != kEnd;
 }
@@ -290,6 +290,7 @@ __device__ __forceinline__ void share(Slot& s)
     s.seq = __shfl_sync(kFull, s.seq, 0);
     s.i = __shfl_sync(kFull, s.i, 0);
     s.j = __shfl_sync(kFull, s.j, 0);
+    s.mat = __shfl_sync(kFull, s.mat, 0);
 }
 
 // The same for a whole warp.
@@ -396,24 +397,25 @@ __device__ __forceinline__ void put_block(float (&v)[64], const Factors& f, cons
 // where in the list it is.
 template <class P>
 struct Source {
-    uint32_t next, at_seq = 0, at_tile = 0, in_seq;
+    uint32_t next, at_seq = 0, at_tile = 0, each;  // each: tiles of one matrix of at_seq's
 
-    __device__ __forceinline__ Source() : next(0), in_seq(0) {}
-    __device__ __forceinline__ explicit Source(const P& p) : next(atomicAdd(p.counters, 1u)), in_seq(tiles_of(p, 0)) {}
+    __device__ __forceinline__ Source() : next(0), each(0) {}
+    __device__ __forceinline__ explicit Source(const P& p) : next(atomicAdd(p.counters, 1u)), each(tiles_of(p, 0)) {}
 
     // The n-th tile of the pair, told to all that wait for it.
     __device__ __forceinline__ void take(const P& p, Slot& s, uint32_t n, Bars* b)
     {
-        while (at_seq < p.nseq && next - at_tile >= in_seq) {
-            at_tile += in_seq;
-            if (++at_seq < p.nseq) in_seq = tiles_of(p, at_seq);
+        for (uint32_t all; at_seq < p.nseq && next - at_tile >= (all = each * (p.seq[at_seq] >> 8 & 255u));) {
+            at_tile += all;
+            if (++at_seq < p.nseq) each = tiles_of(p, at_seq);
         }
         if (at_seq < p.nseq) {
-            const uint32_t e = p.seq[at_seq];
-            const MuonWork& w = p.work[e & 31u];
+            const uint32_t e = p.seq[at_seq], t = next - at_tile;
             s.seq = at_seq;
-            const int kind = p.op[w.op0 + (e >> 5)].kind;
-            place_of(w, kind, p.tile_n[kind], next - at_tile, &s.i, &s.j);
+            s.mat = (e & 255u) + t / each;
+            const MuonWork& w = p.work[s.mat];
+            const int kind = p.op[w.op0 + (e >> 16)].kind;
+            place_of(w, kind, p.tile_n[kind], t % each, &s.i, &s.j);
         }
         if (n < kSlots || wait_for(&b->heard[n % kSlots], ((n / kSlots) - 1) & 1, b, p.waits, p.spin)) {
             tell(s, n, b);
@@ -436,7 +438,7 @@ __device__ __forceinline__ uint32_t copy_tiles(const P& p, Bars* b, uint32_t ops
     const bool source = !IS_B && rank == 0;
     uint32_t it = 0;
     Source<P> from = source && lane == 0 ? Source<P>(p) : Source<P>();
-    uint32_t last = kEnd;  // the product whose earlier levels are known to be finished
+    uint32_t last = kEnd, of = 0;  // the product and the matrix whose earlier levels are known to be finished
     for (uint32_t n = 0;; ++n) {
         Slot s{kEnd, 0, 0, 0};
         if (source) {
@@ -465,11 +467,12 @@ __device__ __forceinline__ uint32_t copy_tiles(const P& p, Bars* b, uint32_t ops
         const uint32_t to = ops + (IS_B ? 2 * kPlane + second * Ring<WIDE>::kPlaneB : second * kPlane) + half * (kPlane / 2);
         const uint32_t kb = t.kb, limit = low ? (at >> 2) * 4 + 4 : mn ? 0 : kb;  // K's blocks that lie by rows
         const uint64_t pair = (uint64_t)nbj * 2 * kBlkElems;
-        if (s.seq != last) {  // what the operands come from is finished
+        if (s.seq != last || s.mat != of) {  // what the operands come from is finished
             uint32_t fine = 1;
             if (lane == 0 && t.op->level > 0) fine = parts_done(p.counters + 1 + t.mat, parts_before(p, t), b, p.waits, p.spin);
             if (!__shfl_sync(kFull, fine, 0)) return it;
             last = s.seq;
+            of = s.mat;
             asm volatile("fence.proxy.async;" ::: "memory");  // it was written by ordinary stores
         }
         for (uint32_t k = 0; k < kb; ++k, ++it) {
@@ -622,8 +625,8 @@ __device__ __forceinline__ void take_tiles(const P& p, Bars* b, uint32_t tmem, c
     }
 }
 
-template <bool WIDE, int OPS, int SEQ>
-__global__ void __launch_bounds__(kGemmThreads, 1) muon_gemm_kernel(const __grid_constant__ MuonGemmParamsT<OPS, SEQ> p)
+template <bool WIDE, class P>
+__global__ void __launch_bounds__(kGemmThreads, 1) muon_gemm_kernel(const __grid_constant__ P p)
 {
     extern __shared__ uint8_t raw_smem[];
     uint8_t* base = raw_smem + ((1024u - (muon_smem(raw_smem) & 1023u)) & 1023u);
@@ -716,8 +719,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) muon_gemm_kernel(const __grid
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
-template <bool WIDE, int OPS, int SEQ>
-cudaError_t launch_as(const MuonGemmParamsT<OPS, SEQ>& p, uint32_t pairs, cudaStream_t s)
+template <bool WIDE, class P>
+cudaError_t launch_as(const P& p, uint32_t pairs, cudaStream_t s)
 {
     constexpr int kMaxDevices = 64;
     static std::atomic<bool> asked[kMaxDevices];
@@ -725,7 +728,7 @@ cudaError_t launch_as(const MuonGemmParamsT<OPS, SEQ>& p, uint32_t pairs, cudaSt
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= kMaxDevices || !asked[dev].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(muon_gemm_kernel<WIDE, OPS, SEQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+        e = cudaFuncSetAttribute(muon_gemm_kernel<WIDE, P>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
         if (e != cudaSuccess) return e;
         if (dev < kMaxDevices) asked[dev].store(true, std::memory_order_release);
     }
@@ -742,20 +745,15 @@ cudaError_t launch_as(const MuonGemmParamsT<OPS, SEQ>& p, uint32_t pairs, cudaSt
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, muon_gemm_kernel<WIDE, OPS, SEQ>, p);
+    e = cudaLaunchKernelEx(&cfg, muon_gemm_kernel<WIDE, P>, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 // Tiles of one product of each matrix.
 uint32_t tiles_of_all(const MuonGemmParams& p, int kind, uint32_t tile_n)
 {
-    uint32_t sum = 0, seen = 0;
-    for (uint32_t k = 0; k < p.nseq; ++k) {
-        const uint32_t mat = p.seq[k] & 31u;
-        if (seen >> mat & 1u) continue;
-        seen |= 1u << mat;
-        sum += muon_tiles(p.work[mat].rows, p.work[mat].cols, kind, tile_n);
-    }
+    uint32_t sum = 0;
+    for (uint32_t k = 0; k < p.n; ++k) sum += muon_tiles(p.work[k].rows, p.work[k].cols, kind, tile_n);
     return sum;
 }
 
@@ -785,17 +783,13 @@ cudaError_t launch_muon_gemm(MuonGemmParams& p, int nops, cudaStream_t s)
         widest = std::max(widest, tiles_of_all(p, kind, p.tile_n[kind]));
     }
     const uint32_t pairs = std::min(kPairs, 2 * widest);  // two products of a matrix may run side by side
-    if (nops > kMuonOpsSmall || p.nseq > kMuonSeqSmall) return wide ? launch_as<true>(p, pairs, s) : launch_as<false>(p, pairs, s);
-    MuonGemmParamsT<kMuonOpsSmall, kMuonSeqSmall> q;
-    std::copy_n(p.work, kMuonMats, q.work);
+    if (p.n > kMuonMatsSmall || nops > kMuonOpsSmall || p.nseq > kMuonSeqSmall)
+        return wide ? launch_as<true>(p, pairs, s) : launch_as<false>(p, pairs, s);
+    MuonGemmParamsT<kMuonMatsSmall, kMuonOpsSmall, kMuonSeqSmall> q;
+    static_cast<MuonGemmHead&>(q) = p;
+    std::copy_n(p.work, p.n, q.work);
     std::copy_n(p.op, nops, q.op);
     std::copy_n(p.seq, p.nseq, q.seq);
-    q.nseq = p.nseq;
-    std::copy_n(p.tile_n, 3, q.tile_n);
-    q.counters = p.counters;
-    q.waits = p.waits;
-    q.hold = p.hold;
-    q.spin = p.spin;
     return wide ? launch_as<true>(q, pairs, s) : launch_as<false>(q, pairs, s);
 }
 

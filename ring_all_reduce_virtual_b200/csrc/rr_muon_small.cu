@@ -163,7 +163,8 @@ __device__ __forceinline__ void add_halves(uint8_t* mat, uint32_t row, uint32_t 
     }
 }
 
-__global__ void __launch_bounds__(kThreads, 1) muon_small_kernel(const __grid_constant__ MuonSmallParams p)
+template <class P>
+__global__ void __launch_bounds__(kThreads, 1) muon_small_kernel(const __grid_constant__ P p)
 {
     extern __shared__ uint8_t raw_smem[];
     __shared__ SmallShared sh;
@@ -399,9 +400,8 @@ __global__ void __launch_bounds__(kThreads, 1) muon_small_kernel(const __grid_co
     if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(sh.tmem), "r"(256u) : "memory");
 }
 
-}  // namespace
-
-cudaError_t launch_muon_small(MuonSmallParams& p, cudaStream_t s)
+template <class P>
+cudaError_t launch_as(const P& p, cudaStream_t s)
 {
     constexpr int kMaxDevices = 64;
     static std::atomic<bool> asked[kMaxDevices];
@@ -409,17 +409,10 @@ cudaError_t launch_muon_small(MuonSmallParams& p, cudaStream_t s)
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= kMaxDevices || !asked[dev].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(muon_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmallSmem);
+        e = cudaFuncSetAttribute(muon_small_kernel<P>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmallSmem);
         if (e != cudaSuccess) return e;
         if (dev < kMaxDevices) asked[dev].store(true, std::memory_order_release);
     }
-    RankParams rp{};
-    rp.waits = bulk_wait_counters();
-    if (!rp.waits) return cudaErrorSymbolNotFound;
-    const BulkParams bp = bulk_params(rp);
-    p.waits = rp.waits;
-    p.hold = bp.hold;
-    p.spin = bp.spin;
     cudaLaunchAttribute attr[2]{};
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -433,8 +426,27 @@ cudaError_t launch_muon_small(MuonSmallParams& p, cudaStream_t s)
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, muon_small_kernel, p);
+    e = cudaLaunchKernelEx(&cfg, muon_small_kernel<P>, p);
     return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_muon_small(MuonSmallParams& p, cudaStream_t s)
+{
+    RankParams rp{};
+    rp.waits = bulk_wait_counters();
+    if (!rp.waits) return cudaErrorSymbolNotFound;
+    const BulkParams bp = bulk_params(rp);
+    p.waits = rp.waits;
+    p.hold = bp.hold;
+    p.spin = bp.spin;
+    if (p.n > kMuonMatsSmall || p.n * p.nranks > kMuonPtrsSmall) return launch_as(p, s);
+    MuonSmallParamsT<kMuonMatsSmall, kMuonPtrsSmall> q;
+    static_cast<MuonSmallHead&>(q) = p;
+    std::copy_n(p.mat, p.n, q.mat);
+    std::copy_n(p.out, p.n * p.nranks, q.out);
+    return launch_as(q, s);
 }
 
 }  // namespace rr

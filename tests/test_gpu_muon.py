@@ -380,3 +380,19 @@ def test_small_fp32_weights_keep_their_precision(r, c):
     rrv.muon_step([w], [g], [m], lr=0.02, weight_decay=0.01)
     err = float((w.double() - want).norm())
     assert err <= f * 2e-5 * float(o.norm()) + 2.0 ** -23 * float(want.norm()), (err, float(o.norm()), float(want.norm()))
+
+
+@pytest.mark.parametrize("count", [25, 128, 150])
+def test_many_matrices_some_of_them_alike(count):
+    """More than a small parameter block and a group hold; shapes and types that come again, in no order."""
+    xs = [gradient(130 + i * i % 5, 140 + i % 3 * 130, TYPES[("f32", "bf16", "f16")[i % 7 % 3]], seed=i) for i in range(count)]
+    got = rrv.orthogonalize(xs)
+    for g, x in zip(got, xs):
+        check(g, x)
+    again = rrv.orthogonalize(xs)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+
+
+@pytest.mark.parametrize("ranks,count,side", [(64, 20, 40), (64, 20, 140), (9, 130, 20), (9, 130, 130)])
+def test_more_replicas_than_a_launch_writes(ranks, count, side):
+    step(ranks, [(side + i % 2, side + i % 3) for i in range(count)], torch.float32, torch.float32)
