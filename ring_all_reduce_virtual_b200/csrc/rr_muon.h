@@ -141,7 +141,9 @@ struct MuonMat {
     Halves x;
     uint32_t tile0;        // first tile of the launch, 128 rows x 64 columns
     uint8_t dtype, out_dtype;
-    uint8_t vec, out_vec;  // whole vectors: gradient and momentum, outputs
+    // Neighbours in a row that lie on their common size everywhere, 8 (on 16 bytes), 2
+    // or 1: of gradient and momentum, of the outputs.
+    uint8_t vec, out_vec;
     uint32_t out;          // muon: index of its first pointer in MuonFinishParams::out
     float factor;          // muon: lr * the shape's factor
 };

@@ -271,7 +271,13 @@ float shape_factor(const Shape& s, int adjust)
     return (float)std::sqrt(std::max(1.0, (double)s.rows / s.cols));
 }
 
-bool on16(const void* p) { return (uintptr_t)p % 16 == 0; }
+// How many neighbours of a row of `cols` elements of `es` bytes lie on 16 bytes (8 of
+// them) or on their common size (2) in every row.
+uint8_t neighbours(const void* p, uint64_t es, uint32_t cols)
+{
+    if (cols % 8 == 0 && (uintptr_t)p % 16 == 0) return 8;
+    return cols % 2 == 0 && (uintptr_t)p % (2 * es) == 0 ? 2 : 1;
+}
 
 // Stages of 64 of K between the roundings of a sum.  Error of five steps in
 // fp32, chunks of 1 / 2 / 4, from 128 x 128 to 8192 x 2048: 0.7e-6..2.0e-6 /
@@ -362,12 +368,13 @@ void place_matrix(const Job& job, int t, MuonMat& m, void** out, uint32_t at)
     m.dtype = (uint8_t)job.in->dtypes[t];
     m.out_dtype = (uint8_t)job.out->dtypes[t];
     m.factor = job.lr * shape_factor(s, job.adjust);
-    m.vec = s.cols % 8 == 0 && on16(m.g) && (!m.m || on16(m.m));
-    m.out_vec = s.cols % 8 == 0;
+    m.vec = neighbours(m.g, esize(job.in->dtypes[t]), s.cols);
+    if (m.m) m.vec = std::min(m.vec, neighbours(m.m, 4, s.cols));
+    m.out_vec = 8;
     m.out = at;
     for (int r = 0; out && r < job.out->nranks; ++r) {
         out[at + r] = job.out->ptrs[(size_t)r * job.out->nmatrices + t];
-        m.out_vec = m.out_vec && on16(out[at + r]);
+        m.out_vec = std::min(m.out_vec, neighbours(out[at + r], esize(job.out->dtypes[t]), s.cols));
     }
 }
 

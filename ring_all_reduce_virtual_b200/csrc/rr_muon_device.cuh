@@ -57,6 +57,29 @@ __device__ __forceinline__ void muon_store8(typename Ty::T* p, bool vec, uint32_
     }
 }
 
+// W neighbouring values that lie on their common size.
+template <class Ty, int W>
+__device__ __forceinline__ void muon_load_few(const typename Ty::T* p, float (&v)[W])
+{
+    if constexpr (W == 1) {
+        v[0] = Ty::ld1(p);
+    } else if constexpr (sizeof(typename Ty::T) == 2) {
+        Ty::unpack2(*reinterpret_cast<const uint32_t*>(p), v[0], v[1]);
+    } else {
+        const float2 a = *reinterpret_cast<const float2*>(p);
+        v[0] = a.x;
+        v[1] = a.y;
+    }
+}
+
+template <class Ty, int W>
+__device__ __forceinline__ void muon_store_few(typename Ty::T* p, const float (&v)[W])
+{
+    if constexpr (W == 1) Ty::st1(p, v[0]);
+    else if constexpr (sizeof(typename Ty::T) == 2) *reinterpret_cast<uint32_t*>(p) = Ty::pack2(v[0], v[1]);
+    else *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
+}
+
 // scale / den as two factors that multiply a value one after the other: a power of
 // two and one of 1..2, so that neither product leaves fp32's range where the
 // result does not.

@@ -214,8 +214,8 @@ __global__ void __launch_bounds__(kThreads, 1) muon_small_kernel(const __grid_co
                 c[u] = (k - r[u] * per) * 8;
                 left[u] = r[u] < prows ? min(8u, pcols - c[u]) : 0;
                 const uint64_t e = first + (uint64_t)r[u] * t.cols + c[u];
-                muon_load8<Ty>(g + e, t.vec, left[u], v[u]);
-                if (t.m) muon_load8<F32T>(t.m + e, t.vec, left[u], mo[u]);
+                muon_load8<Ty>(g + e, t.vec == 8, left[u], v[u]);
+                if (t.m) muon_load8<F32T>(t.m + e, t.vec == 8, left[u], mo[u]);
             }
 #pragma unroll
             for (uint32_t u = 0; u < kAtOnce; ++u) {
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1) muon_small_kernel(const __grid_co
                         mo[u][l] = __fmaf_rn(p.momentum, mo[u][l], v[u][l]);
                         v[u][l] = p.nesterov ? __fmaf_rn(p.momentum, mo[u][l], v[u][l]) : mo[u][l];
                     }
-                    muon_store8<F32T>(t.m + first + (uint64_t)r[u] * t.cols + c[u], t.vec, left[u], mo[u]);
+                    muon_store8<F32T>(t.m + first + (uint64_t)r[u] * t.cols + c[u], t.vec == 8, left[u], mo[u]);
                 }
 #pragma unroll
                 for (int l = 0; l < 8; ++l)
@@ -357,6 +357,32 @@ __global__ void __launch_bounds__(kThreads, 1) muon_small_kernel(const __grid_co
 
     muon_with_type(t.out_dtype, [&]<class Ty>() {
         using T = typename Ty::T;
+        // Rows that do not begin on 16 bytes: neighbours in neighbouring lanes where many
+        // replicas are written (four layers of width 90, fp32, eight replicas: 121 -> 90
+        // us), else eight a lane, which starts more loads at once (17 of 105, fp16, four
+        // replicas: 208 -> 194).
+        if (t.out_vec < 8 && p.nranks > 4) {
+#pragma unroll 1
+            for (uint32_t r0 = warp; r0 < prows; r0 += 4 * (kThreads / 32)) {
+                float w[16];
+#pragma unroll
+                for (uint32_t k = 0; k < 16; ++k) {
+                    const uint32_t r = r0 + k / 4 * (kThreads / 32), c = k % 4 * 32 + lane;
+                    const bool in = r < prows && c < pcols;
+                    w[k] = in && t.m ? Ty::ld1(static_cast<const T*>(p.out[t.out]) + first + (uint64_t)r * t.cols + c) : 0.0f;
+                }
+#pragma unroll
+                for (uint32_t k = 0; k < 16; ++k) {
+                    const uint32_t r = r0 + k / 4 * (kThreads / 32), c = k % 4 * 32 + lane;
+                    if (r >= prows || c >= pcols) continue;
+                    float v = *(wide ? word(S, r, c) : word(S, c, r)) * p.inv;
+                    if (t.m) v = __fmaf_rn(-t.factor, v, p.keep * w[k]);
+                    const uint64_t e = first + (uint64_t)r * t.cols + c;
+                    for (int o = 0; o < p.nranks; ++o) Ty::st1(static_cast<T*>(p.out[t.out + o]) + e, v);
+                }
+            }
+            return;
+        }
 #pragma unroll 1
         for (uint32_t k0 = tid; k0 < prows * per; k0 += kAtOnce * kThreads) {
             float w[kAtOnce][8];
@@ -368,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1) muon_small_kernel(const __grid_co
                 c[u] = (k - r[u] * per) * 8;
                 left[u] = r[u] < prows ? min(8u, pcols - c[u]) : 0;
                 if (t.m)  // weights: rank 0's, updated, to every rank
-                    muon_load8<Ty>(static_cast<const T*>(p.out[t.out]) + first + (uint64_t)r[u] * t.cols + c[u], t.out_vec, left[u], w[u]);
+                    muon_load8<Ty>(static_cast<const T*>(p.out[t.out]) + first + (uint64_t)r[u] * t.cols + c[u], t.out_vec == 8, left[u], w[u]);
             }
 #pragma unroll
             for (uint32_t u = 0; u < kAtOnce; ++u) {
@@ -382,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1) muon_small_kernel(const __grid_co
                     for (int l = 0; l < 8; ++l) v[l] = __fmaf_rn(-t.factor, v[l], p.keep * w[u][l]);
                 }
                 const uint64_t e = first + (uint64_t)r[u] * t.cols + c[u];
-                for (int o = 0; o < p.nranks; ++o) muon_store8<Ty>(static_cast<T*>(p.out[t.out + o]) + e, t.out_vec, left[u], v);
+                for (int o = 0; o < p.nranks; ++o) muon_store8<Ty>(static_cast<T*>(p.out[t.out + o]) + e, t.out_vec == 8, left[u], v);
             }
         }
     });

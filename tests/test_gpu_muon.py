@@ -396,3 +396,26 @@ def test_many_matrices_some_of_them_alike(count):
 @pytest.mark.parametrize("ranks,count,side", [(64, 20, 40), (64, 20, 140), (9, 130, 20), (9, 130, 130)])
 def test_more_replicas_than_a_launch_writes(ranks, count, side):
     step(ranks, [(side + i % 2, side + i % 3) for i in range(count)], torch.float32, torch.float32)
+
+
+@pytest.mark.parametrize("ranks", [2, 6])
+@pytest.mark.parametrize("offset", [0, 1, 2, 8])
+def test_rows_on_no_common_boundary(ranks, offset):
+    """Columns that 8, 2 or nothing divides, from addresses that are and are not on 16 bytes."""
+    shapes = [(270, 90), (91, 93), (258, 130), (257, 131), (140, 264), (1, 301), (299, 2)]
+    for dt, gdt in (("f32", "bf16"), ("bf16", "f32"), ("f16", "f16")):
+        step(ranks, shapes, TYPES[dt], TYPES[gdt], offset=offset)
+
+
+@pytest.mark.parametrize("r,c", [(131, 260), (260, 131), (140, 8192), (150, 134), (33, 18)])
+def test_results_at_odd_places_leave_the_neighbours_alone(r, c):
+    for dt in TYPES.values():
+        x = gradient(r, c, dt, seed=r)
+        want = rrv.orthogonalize([x])[0]
+        for at in (1, 2, 3):
+            flats = [torch.full((r * c + 16,), 7.0, dtype=dt, device="cuda") for _ in range(6)]
+            outs = [[f[at:at + r * c].view(r, c)] for f in flats]
+            rrv.orthogonalize([x], outs)
+            for f in flats:
+                assert torch.equal(f[at:at + r * c].view(r, c), want)
+                assert (f[:at] == 7).all() and (f[at + r * c:] == 7).all()
