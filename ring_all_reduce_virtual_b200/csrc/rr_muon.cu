@@ -163,8 +163,10 @@ __global__ void __launch_bounds__(kThreads) muon_squares_kernel(const __grid_con
     if (threadIdx.x == 0) p.partial[blockIdx.x] = acc;
 }
 
-// 128 rows x 64 columns of X, split into halves.
-template <class P>
+// 128 rows x 64 columns of X, split into halves.  ALL: every matrix's rows begin on
+// 16 bytes; without the other code it takes 32 registers instead of 39 (one layer of
+// width 2048, bf16: 79 and 85 us).
+template <class P, bool ALL>
 __global__ void __launch_bounds__(kThreads) muon_pack_kernel(const __grid_constant__ P p)
 {
     __shared__ double sh[kThreads / 32];
@@ -183,7 +185,7 @@ __global__ void __launch_bounds__(kThreads) muon_pack_kernel(const __grid_consta
             const uint32_t k = u * kThreads + threadIdx.x;
             const uint32_t r = ti * 128 + k / 8, c = tj * kBlk + (k % 8) * 8;
             float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-            if (t.vec < 8) {
+            if (!ALL && t.vec < 8) {
                 if (t.vec == 2) read_rows<Ty, 2>(p, t, r - lane / 8, tj * kBlk, lane, mine);
                 else read_rows<Ty, 1>(p, t, r - lane / 8, tj * kBlk, lane, mine);
                 __syncwarp();
@@ -214,8 +216,9 @@ __global__ void __launch_bounds__(kThreads) muon_pack_kernel(const __grid_consta
     });
 }
 
-// 128 rows x 64 columns of the result.
-template <class P>
+// 128 rows x 64 columns of the result.  ALL as above (31 registers and 64; 78 and
+// 101 us).
+template <class P, bool ALL>
 __global__ void __launch_bounds__(kThreads) muon_finish_kernel(const __grid_constant__ P p)
 {
     pdl_begin();
@@ -237,7 +240,7 @@ __global__ void __launch_bounds__(kThreads) muon_finish_kernel(const __grid_cons
             F16T::unpack(*reinterpret_cast<const uint4*>(t.x.lo + at), l8);
 #pragma unroll
             for (int l = 0; l < 8; ++l) h[l] = (h[l] + l8[l]) * p.inv;
-            if (t.out_vec < 8) {
+            if (!ALL && t.out_vec < 8) {
                 mine.put(lane, h);
                 __syncwarp();
                 if (t.out_vec == 2) write_rows<Ty, 2>(p, t, r - lane / 8, tj * kBlk, lane, mine);
@@ -277,19 +280,25 @@ cudaError_t launch_muon_squares(const MuonPrepParams& p, uint32_t parts, cudaStr
 
 cudaError_t launch_muon_pack(const MuonPrepParams& p, uint32_t tiles, cudaStream_t s)
 {
-    return with_prep(p, [&]<class P>(const P& q) { return launch_pdl(muon_pack_kernel<P>, dim3(tiles), kThreads, 0, s, q); });
+    const bool all = std::all_of(p.mat, p.mat + p.n, [](const MuonMat& t) { return t.vec == 8; });
+    return with_prep(p, [&]<class P>(const P& q) {
+        return launch_pdl(all ? muon_pack_kernel<P, true> : muon_pack_kernel<P, false>, dim3(tiles), kThreads, 0, s, q);
+    });
 }
 
 cudaError_t launch_muon_finish(const MuonFinishParams& p, uint32_t tiles, cudaStream_t s)
 {
-    if (p.n > kMuonMatsSmall || p.n * p.nranks > kMuonPtrsSmall)
-        return launch_pdl(muon_finish_kernel<MuonFinishParams>, dim3(tiles), kThreads, 0, s, p);
+    const bool all = std::all_of(p.mat, p.mat + p.n, [](const MuonMat& t) { return t.out_vec == 8; });
+    const auto launch = [&]<class P>(const P& q) {
+        return launch_pdl(all ? muon_finish_kernel<P, true> : muon_finish_kernel<P, false>, dim3(tiles), kThreads, 0, s, q);
+    };
+    if (p.n > kMuonMatsSmall || p.n * p.nranks > kMuonPtrsSmall) return launch(p);
     using Few = MuonFinishParamsT<kMuonMatsSmall, kMuonPtrsSmall>;
     Few q;
     static_cast<MuonFinishHead&>(q) = p;
     std::copy_n(p.mat, p.n, q.mat);
     std::copy_n(p.out, p.n * p.nranks, q.out);
-    return launch_pdl(muon_finish_kernel<Few>, dim3(tiles), kThreads, 0, s, q);
+    return launch(q);
 }
 
 }  // namespace rr
