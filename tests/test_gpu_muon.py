@@ -419,3 +419,22 @@ def test_results_at_odd_places_leave_the_neighbours_alone(r, c):
             for f in flats:
                 assert torch.equal(f[at:at + r * c].view(r, c), want)
                 assert (f[:at] == 7).all() and (f[at + r * c:] == 7).all()
+
+
+@pytest.mark.parametrize("side", [30, 150])
+def test_many_matrices_captured(side):
+    """Launches with large parameter blocks in a graph, replayed after the inputs changed."""
+    xs = [gradient(side + i % 4, side + i % 3 * 50, torch.float32, seed=i) for i in range(60)]
+    first = [x.clone() for x in xs]
+    outs = [[torch.empty_like(x) for x in xs] for _ in range(5)]
+    rrv.orthogonalize(xs, outs)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        rrv.orthogonalize(xs, outs)
+    for inputs in ([x.flip(0) for x in first], first):
+        for x, v in zip(xs, inputs):
+            x.copy_(v)
+        graph.replay()
+        want = rrv.orthogonalize(xs)
+        assert all(torch.equal(a, b) for rank in outs for a, b in zip(rank, want))
