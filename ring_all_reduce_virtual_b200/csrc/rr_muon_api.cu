@@ -212,47 +212,80 @@ bool is_small(uint64_t rows, uint64_t cols)
     return std::min(rows, cols) <= kMuonSmallSide && std::max(rows, cols) <= kMuonSmallSide * kMuonSmallCtas;
 }
 
+// What a matrix's products follow from, beside its shape: lists of products are
+// made once for every kind of a group.
+struct Kind {
+    std::vector<int> segments;
+    bool exact;
+    bool operator==(const Kind& o) const { return exact == o.exact && segments == o.segments; }
+};
+
+// Matrices of one shape and kind, whatever their types: they follow one another
+// in the launches, and each of their products is listed once for all of them.
+struct Alike {
+    Shape shape;
+    size_t kind;
+    std::vector<int> matrices;
+};
+
+// Matrices that run in the same launches.
+struct Group {
+    std::vector<Kind> kinds;
+    std::vector<Alike> alike;
+    int matrices = 0;
+    int ops = 0;     // different products: of every kind once
+    int listed = 0;  // entries of MuonGemmParams::seq: of every Alike once
+    uint64_t used = kHeadBytes;
+};
+
 // The groups of a list's other matrices (those with elements), in order.
-std::vector<std::vector<int>> groups_of(const rr_matrix_list_t* l, const Plan& plan, bool weights, uint64_t* bytes)
+std::vector<Group> groups_of(const rr_matrix_list_t* l, const Plan& plan, bool weights, uint64_t* bytes)
 {
-    std::vector<std::vector<int>> groups;
-    std::vector<std::pair<std::vector<int>, bool>> kinds;
-    std::vector<std::pair<Shape, size_t>> classes;  // and kind
-    uint64_t used = 0;
-    int listed = 0, ops = 0;
+    std::vector<Group> groups;
     *bytes = 256;
     for (int t = 0; t < l->nmatrices; ++t) {
         const Shape s{(uint32_t)l->rows[t], (uint32_t)l->cols[t]};
         if (s.numel() == 0 || is_small(s.rows, s.cols)) continue;
-        const std::vector<int> segments = segments_for(plan, l, t, weights);
-        const uint64_t need = room_of(s, segments).bytes();
-        const int products = products_in(segments);
-        const std::pair<std::vector<int>, bool> kind{segments, exactness(l, t, weights) == kExact};
-        const auto number = [&] { return (size_t)(std::find(kinds.begin(), kinds.end(), kind) - kinds.begin()); };
-        const auto like = [&] {
-            return std::any_of(classes.begin(), classes.end(),
-                               [&](const auto& e) { return e.first.rows == s.rows && e.first.cols == s.cols && e.second == number(); });
+        const Kind kind{segments_for(plan, l, t, weights), exactness(l, t, weights) == kExact};
+        const uint64_t need = room_of(s, kind.segments).bytes();
+        const int products = products_in(kind.segments);
+        size_t k = 0, a = 0;  // its kind and its like in the last group
+        const auto look = [&] {
+            const Group& g = groups.back();
+            k = (size_t)(std::find(g.kinds.begin(), g.kinds.end(), kind) - g.kinds.begin());
+            a = (size_t)(std::find_if(g.alike.begin(), g.alike.end(), [&](const Alike& e) {
+                             return e.shape.rows == s.rows && e.shape.cols == s.cols && e.kind == k;
+                         }) - g.alike.begin());
         };
-        if (groups.empty() || groups.back().size() == kMuonMats || used + need > kGroupBytes ||
-            (!like() && listed + products > kMuonSeq) || (number() == kinds.size() && ops + products > kMuonOps)) {
+        const auto fits = [&] {
+            const Group& g = groups.back();
+            return g.matrices < kMuonMats && g.used + need <= kGroupBytes &&
+                   (a < g.alike.size() || g.listed + products <= kMuonSeq) && (k < g.kinds.size() || g.ops + products <= kMuonOps);
+        };
+        if (!groups.empty()) look();
+        if (groups.empty() || !fits()) {
             groups.emplace_back();
-            used = kHeadBytes;
-            listed = ops = 0;
-            kinds.clear();
-            classes.clear();
+            look();
         }
-        if (!like()) {
-            listed += products;
-            classes.push_back({s, number()});
+        Group& g = groups.back();
+        if (k == g.kinds.size()) {
+            g.kinds.push_back(kind);
+            g.ops += products;
         }
-        if (number() == kinds.size()) {
-            kinds.push_back(kind);
-            ops += products;
+        if (a == g.alike.size()) {
+            g.alike.push_back({s, k, {}});
+            g.listed += products;
         }
-        groups.back().push_back(t);
-        used += need;
-        *bytes = std::max(*bytes, used);
+        g.alike[a].matrices.push_back(t);
+        g.matrices += 1;
+        g.used += need;
+        *bytes = std::max(*bytes, g.used);
     }
+    // smaller matrices of a group first
+    for (Group& g : groups)
+        std::stable_sort(g.alike.begin(), g.alike.end(), [](const Alike& x, const Alike& y) {
+            return std::tie(x.shape.rows, x.shape.cols) < std::tie(y.shape.rows, y.shape.cols);
+        });
     return groups;
 }
 
@@ -412,20 +445,16 @@ rr_status_t run_small(const Job& job, const Plan& plan, const std::vector<int>& 
     return RR_OK;
 }
 
-rr_status_t run_group(const Job& job, const Plan& plan, std::vector<int> group, char* ws, cudaStream_t stream)
+rr_status_t run_group(const Job& job, const Plan& plan, const Group& group, char* ws, cudaStream_t stream)
 {
-    const int n = (int)group.size();
-    // matrices alike follow one another, and are listed as one
-    std::stable_sort(group.begin(), group.end(), [&](int a, int b) {
-        const rr_matrix_list_t& l = *job.out;
-        return std::tie(l.rows[a], l.cols[a], l.dtypes[a]) < std::tie(l.rows[b], l.cols[b], l.dtypes[b]);
-    });
+    const int n = group.matrices;
+    // groups_of counts what is listed here; more would pass the ends of the parameters' arrays
+    const auto too_many = [] { return fail(RR_ERR_UNSUPPORTED, "a group of matrices has more products than a launch takes"); };
+    if (n > kMuonMats) return too_many();
     std::unique_ptr<MuonPrepParams> prep(new MuonPrepParams{});
     std::unique_ptr<MuonGemmParams> gemm(new MuonGemmParams);  // as it comes: every field that counts is set
     std::vector<Halves> result(n);
-    using Kind = std::pair<std::vector<int>, bool>;  // segments, exactly or not
-    std::vector<std::pair<Kind, std::pair<int, int>>> known;  // first product, result's buffer
-    int nops = 0;
+    std::vector<int> matrix(n);  // of the list, in the launches' order
     uint64_t at = kHeadBytes;
     const auto take = [&](uint64_t bytes) {
         uint16_t* const p = reinterpret_cast<uint16_t*>(ws + at);
@@ -439,48 +468,19 @@ rr_status_t run_group(const Job& job, const Plan& plan, std::vector<int> group, 
     prep->nesterov = job.nesterov;
     prep->eps = job.eps;
     prep->scale = (float)scale_for(plan.rho[0]);
-    uint32_t parts = 0, tiles = 0;
-    std::vector<Shape> shape(n);
-    for (int k = 0; k < n; ++k) {
-        const int t = group[k];
-        const Shape s = shape[k] = {(uint32_t)job.in->rows[t], (uint32_t)job.in->cols[t]};
-        const std::vector<int> segments = segments_for(plan, job.out, t, job.mom != nullptr);
-        const Room room = room_of(s, segments);
-        const Kind kind{segments, exactness(job.out, t, job.mom != nullptr) == kExact};
-        auto same = std::find_if(known.begin(), known.end(), [&](const auto& e) { return e.first == kind; });
-        if (same == known.end()) {
-            int last = 0;
-            const std::vector<MuonOp> ops = products_of(plan, segments, kind.second, &last);
-            std::copy(ops.begin(), ops.end(), gemm->op + nops);
-            known.push_back({kind, {nops, last}});
-            same = known.end() - 1;
-            nops += (int)ops.size();
-        }
-        MuonWork& w = gemm->work[k];
-        for (int i = 0; i < 2; ++i) w.x[i] = i < room.xs ? take(2 * room.x) : nullptr;
-        w.squares = take(2 * room.square * room.squares);
-        w.rows = s.rows;
-        w.cols = s.cols;
-        w.op0 = (uint16_t)same->second.first;
-        w.ops = (uint16_t)products_in(segments);
-        uint16_t* const last = w.x[same->second.second];
-        result[k] = {last, last + room.x / 2};
-        const Halves first{w.x[0], w.x[0] + room.x / 2};
-        MuonMat& m = prep->mat[k];
-        place_matrix(job, t, m, nullptr, 0);
-        m.part0 = parts;
-        m.parts = parts_of(s);
-        m.x = first;
-        m.tile0 = tiles;
-        parts += m.parts;
-        tiles += pad_up(s.rows) / 128 * (pad_up(s.cols) / kBlk);
+    // every kind's products, and the buffer that their result is in
+    std::vector<std::vector<MuonOp>> products;
+    std::vector<uint16_t> op0;
+    std::vector<int> last;
+    int nops = 0;
+    for (const Kind& kind : group.kinds) {
+        last.push_back(0);
+        products.push_back(products_of(plan, kind.segments, kind.exact, &last.back()));
+        op0.push_back((uint16_t)nops);
+        if (nops + products.back().size() > (size_t)kMuonOps) return too_many();
+        std::copy(products.back().begin(), products.back().end(), gemm->op + nops);
+        nops += (int)products.back().size();
     }
-    cudaError_t e = timed_launch([&] { return launch_muon_squares(*prep, parts, stream); });
-    if (e != cudaSuccess) return cuda_fail(e, "Muon norm launch");
-    e = timed_launch([&] { return launch_muon_pack(*prep, tiles, stream); });
-    if (e != cudaSuccess) return cuda_fail(e, "Muon pack launch");
-    t_stats.launches += 2;
-
     // The list of products: level by level, in each the longest first, so that the
     // end of a level is short tiles.
     struct Item {
@@ -488,16 +488,46 @@ rr_status_t run_group(const Job& job, const Plan& plan, std::vector<int> group, 
         uint32_t depth, at;
     };
     std::vector<Item> list;
-    for (int k = 0, next; k < n; k = next) {
-        const MuonWork& w = gemm->work[k];
-        for (next = k + 1; next < n && gemm->work[next].rows == w.rows && gemm->work[next].cols == w.cols && gemm->work[next].op0 == w.op0;)
-            ++next;
-        for (int o = 0; o < w.ops; ++o) {
-            const MuonOp& q = gemm->op[w.op0 + o];
-            const uint32_t depth = q.kind == kGram ? std::max(w.rows, w.cols) : shape[k].small();
-            list.push_back({q.level, depth, (uint32_t)(k | (next - k) << 8 | o << 16)});
+    list.reserve(group.listed);
+    uint32_t parts = 0, tiles = 0;
+    int k = 0;
+    for (const Alike& like : group.alike) {
+        const Shape& s = like.shape;
+        const Room room = room_of(s, group.kinds[like.kind].segments);
+        const std::vector<MuonOp>& ops = products[like.kind];
+        for (size_t o = 0; o < ops.size(); ++o) {
+            const uint32_t depth = ops[o].kind == kGram ? std::max(s.rows, s.cols) : s.small();
+            list.push_back({ops[o].level, depth, (uint32_t)k | (uint32_t)like.matrices.size() << 8 | (uint32_t)o << 16});
+        }
+        for (const int t : like.matrices) {
+            MuonWork& w = gemm->work[k];
+            for (int i = 0; i < 2; ++i) w.x[i] = i < room.xs ? take(2 * room.x) : nullptr;
+            w.squares = take(2 * room.square * room.squares);
+            w.rows = s.rows;
+            w.cols = s.cols;
+            w.op0 = op0[like.kind];
+            w.ops = (uint16_t)ops.size();
+            uint16_t* const res = w.x[last[like.kind]];
+            result[k] = {res, res + room.x / 2};
+            matrix[k] = t;
+            MuonMat& m = prep->mat[k];
+            place_matrix(job, t, m, nullptr, 0);
+            m.part0 = parts;
+            m.parts = parts_of(s);
+            m.x = {w.x[0], w.x[0] + room.x / 2};
+            m.tile0 = tiles;
+            parts += m.parts;
+            tiles += pad_up(s.rows) / 128 * (pad_up(s.cols) / kBlk);
+            ++k;
         }
     }
+    if (list.size() > (size_t)kMuonSeq) return too_many();
+    cudaError_t e = timed_launch([&] { return launch_muon_squares(*prep, parts, stream); });
+    if (e != cudaSuccess) return cuda_fail(e, "Muon norm launch");
+    e = timed_launch([&] { return launch_muon_pack(*prep, tiles, stream); });
+    if (e != cudaSuccess) return cuda_fail(e, "Muon pack launch");
+    t_stats.launches += 2;
+
     std::stable_sort(list.begin(), list.end(),
                      [](const Item& a, const Item& b) { return a.level != b.level ? a.level < b.level : a.depth > b.depth; });
     gemm->n = (uint32_t)n;
@@ -516,9 +546,8 @@ rr_status_t run_group(const Job& job, const Plan& plan, std::vector<int> group, 
         fin->n = std::min(most, n - k0);
         uint32_t todo = 0;
         for (int k = 0; k < fin->n; ++k) {
-            const int t = group[k0 + k];
             MuonMat& m = fin->mat[k];
-            place_matrix(job, t, m, fin->out, (uint32_t)(k * nr));
+            place_matrix(job, matrix[k0 + k], m, fin->out, (uint32_t)(k * nr));
             m.x = result[k0 + k];
             m.tile0 = todo;
             todo += pad_up(m.rows) / 128 * (pad_up(m.cols) / kBlk);
