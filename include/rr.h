@@ -568,7 +568,7 @@ typedef struct rr_muon {
  *     U = G + momentum * M (nesterov) or M
  *     W_r = round((1 - lr * weight_decay) * W_0 - lr * f * O)   on every rank r
  * with O = U orthogonalised (rr_orthogonalize; U in fp32, O not rounded on the
- * way, and as near as for fp16 results or nearer for fp32 weights) and f the
+ * way, and as near as for results of the weights' type) and f the
  * shape's factor.  params: nranks replicas, of
  * which rank 0's is read and all are written; grads: rank 0's are read;
  * momenta: one rank, fp32, kept by the caller from step to step (zeros at

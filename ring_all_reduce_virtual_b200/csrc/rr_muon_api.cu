@@ -138,20 +138,18 @@ rr_status_t make_plan(const rr_newton_schulz_t* ns, Plan* p)
 // the side): 2e-6..4e-4 / 2e-6..2e-5 / 2e-6..1e-5 / 1e-6..7e-6, the same steps in
 // plain fp32 2e-6..2e-5.  So A's errors may grow by 3e4 (5 steps of the usual
 // coefficients) for bf16 results, which are rounded by 1.7e-3; by 200 (3 steps) for
-// fp16's (2e-4) and for fp32 weights of 512 rows and more, of which the result is a
-// small part (three layers of width 512 / 1024: 442 / 1466 us, with 2 steps 490 /
-// 1686); by 12.5 (2 steps) for smaller ones, whose part is larger (width 230: the
-// weights 6.6e-7 off in 269 us, with 3 steps 1.8e-6 in 261), and for results of fp32
-// from 192 rows on (4 layers of width 2048 in 17.3 ms instead of 22.7), below which
-// plain fp32 errs less than that.
-enum Exactness { kExact, kWeight, kClose, kCoarse };
+// fp16's (2e-4); and by 12.5 (2 steps) for fp32's from 192 rows on (4 layers of width
+// 2048 in 17.3 ms instead of 22.7), below which plain fp32 errs less than that.
+// Weights are treated as results of their type are: how large a part of a weight the
+// update is depends on the caller's lr, factor and weights, which may begin at zero.
+// (fp32 weights on 3 + 2 steps, their sums in chunks of 256 of K, were 3 to 11 times
+// as far off as the same steps in plain fp32, up to 6e-5 of O; a layer of width 700 /
+// 1024: 450 / 1500 us then, 600 / 2060 now.)
+enum Exactness { kExact, kClose, kCoarse };
 
 std::vector<int> segments_of(const Plan& plan, uint32_t m, uint32_t n, Exactness exact)
 {
-    const double limit = exact == kExact    ? (m < 192 ? 0.0 : 12.5)
-                         : exact == kWeight ? (m < 512 ? 12.5 : 200.0)
-                         : exact == kClose  ? 200.0
-                                            : 3e4;
+    const double limit = exact == kExact ? (m < 192 ? 0.0 : 12.5) : exact == kClose ? 200.0 : 3e4;
     const double grow = std::max(1.0, (double)plan.a * plan.a);
     int most = 1;
     for (double g = grow; g <= limit && most < plan.steps; g *= grow) ++most;
@@ -192,19 +190,8 @@ int products_in(const std::vector<int>& segments)
     return n;
 }
 
-// How exactly a list's matrix t has to come out.
-Exactness exactness(const rr_matrix_list_t* out, int t, bool weights)
-{
-    if (out->dtypes[t] == RR_BF16) return kCoarse;
-    if (out->dtypes[t] == RR_F16) return kClose;
-    return weights ? kWeight : kExact;
-}
-
-std::vector<int> segments_for(const Plan& plan, const rr_matrix_list_t* out, int t, bool weights)
-{
-    const uint32_t r = (uint32_t)out->rows[t], c = (uint32_t)out->cols[t];
-    return segments_of(plan, std::min(r, c), std::max(r, c), exactness(out, t, weights));
-}
+// How exactly a result, or the update of a weight, has to come out for its type.
+Exactness exactness(rr_dtype_t type) { return type == RR_BF16 ? kCoarse : type == RR_F16 ? kClose : kExact; }
 
 // Whether a cluster takes the matrix whole (rr_muon_small.cu).
 bool is_small(uint64_t rows, uint64_t cols)
@@ -239,14 +226,15 @@ struct Group {
 };
 
 // The groups of a list's other matrices (those with elements), in order.
-std::vector<Group> groups_of(const rr_matrix_list_t* l, const Plan& plan, bool weights, uint64_t* bytes)
+std::vector<Group> groups_of(const rr_matrix_list_t* l, const Plan& plan, uint64_t* bytes)
 {
     std::vector<Group> groups;
     *bytes = 256;
     for (int t = 0; t < l->nmatrices; ++t) {
         const Shape s{(uint32_t)l->rows[t], (uint32_t)l->cols[t]};
         if (s.numel() == 0 || is_small(s.rows, s.cols)) continue;
-        const Kind kind{segments_for(plan, l, t, weights), exactness(l, t, weights) == kExact};
+        const Exactness exact = exactness(l->dtypes[t]);
+        const Kind kind{segments_of(plan, s.small(), std::max(s.rows, s.cols), exact), exact == kExact};
         const uint64_t need = room_of(s, kind.segments).bytes();
         const int products = products_in(kind.segments);
         size_t k = 0, a = 0;  // its kind and its like in the last group
@@ -562,7 +550,7 @@ rr_status_t run_group(const Job& job, const Plan& plan, const Group& group, char
 rr_status_t run(const Job& job, const Plan& plan, std::vector<Span>& spans, void* ws, size_t ws_bytes, cudaStream_t stream)
 {
     uint64_t need = 0, S = 0, total = 0;
-    const auto groups = groups_of(job.out, plan, job.mom != nullptr, &need);
+    const auto groups = groups_of(job.out, plan, &need);
     for (int t = 0; t < job.in->nmatrices; ++t) {
         const uint64_t numel = job.in->rows[t] * job.in->cols[t];
         S += numel * esize(job.out->dtypes[t]);
@@ -666,7 +654,8 @@ rr_status_t muon_step(const rr_matrix_list_t* params, const rr_matrix_list_t* gr
 
 extern "C" {
 
-rr_status_t rr_muon_workspace(const rr_matrix_list_t* results, int weights, const rr_newton_schulz_t* ns, size_t* bytes)
+// Weights come out as exactly as results of their type: both calls need the same.
+rr_status_t rr_muon_workspace(const rr_matrix_list_t* results, int /* weights */, const rr_newton_schulz_t* ns, size_t* bytes)
 {
     return guarded([&]() -> rr_status_t {
         if (!bytes) return fail(RR_ERR_INVALID_ARG, "NULL workspace size output");
@@ -675,7 +664,7 @@ rr_status_t rr_muon_workspace(const rr_matrix_list_t* results, int weights, cons
         if (st == RR_OK) st = check_list(results, "results");
         if (st != RR_OK) return st;
         uint64_t need = 0;
-        groups_of(results, plan, weights != 0, &need);
+        groups_of(results, plan, &need);
         *bytes = (size_t)need;
         return RR_OK;
     });
