@@ -543,10 +543,10 @@ rr_status_t rr_muon_workspace(const rr_matrix_list_t* results, int weights, cons
  * matrix itself where the types agree; other buffers must not overlap.  The
  * products run on the tensor cores with operands of 22 bits and fp32 sums; the
  * result is rounded once to its type.  fp32 results are as near to the exact
- * polynomial as the same steps in fp32 are (about 1e-6 to 1e-5 of the matrix's
+ * polynomial as the same steps in fp32 are (about 1e-6 to 2e-5 of the matrix's
  * norm); for bf16 and fp16 results of matrices that are not square several
- * steps share one A, whose roundings then count up to 4e-4 and 2e-5 of it (the
- * types' own: 1.7e-3 and 2e-4).  A matrix of zeros stays
+ * steps share one A, whose roundings then count up to 1e-4 of it (the types'
+ * own: 1.7e-3 and 2e-4).  A matrix of zeros stays
  * zero; one with a NaN or an infinity gives NaN.  The same call gives the same
  * bits. */
 rr_status_t rr_orthogonalize(const rr_matrix_list_t* matrices, const rr_matrix_list_t* results, const rr_newton_schulz_t* ns,

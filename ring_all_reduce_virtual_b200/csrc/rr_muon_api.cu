@@ -133,23 +133,24 @@ rr_status_t make_plan(const rr_newton_schulz_t* ns, Plan* p)
 // whole 1.5 (r - 1) a segment and 2 a step: the fewer segments the better, the
 // more so the longer the matrix, and none for a square one.  But D (D A)
 // multiplies what A was rounded by, up to a^2 a step, where its eigenvalues are
-// small.  Measured error of five steps against 64 bits, segments of 5 / 3 + 2 /
-// 2 + 2 + 1 / 1 each, from noise to few directions in little noise (rank 1/16 of
-// the side): 2e-6..4e-4 / 2e-6..2e-5 / 2e-6..1e-5 / 1e-6..7e-6, the same steps in
-// plain fp32 2e-6..2e-5.  So A's errors may grow by 3e4 (5 steps of the usual
-// coefficients) for bf16 results, which are rounded by 1.7e-3; by 200 (3 steps) for
-// fp16's (2e-4); and by 12.5 (2 steps) for fp32's from 192 rows on (4 layers of width
-// 2048 in 17.3 ms instead of 22.7), below which plain fp32 errs less than that.
+// small: five steps on one A of 2^-22 are off by up to 2e4 * 1.4 * 2^-22 = 7e-3 of a
+// result that one strong direction dominates, more than bf16's own 1.7e-3.
+// Measured error of five steps against 64 bits in segments of 3 + 2 (chunk 4) / 2 + 2
+// + 1 / 1 each (chunk 1), from noise to one direction in 1 % of noise: 7e-6..7e-5 /
+// 2e-6..2e-5 / 1e-6..1e-5, the same steps in plain fp32 2e-6..5e-5; of 5 steps
+// (chunk 4) 4e-6..7e-3.  So A's errors may grow by 200 (3 steps of the usual
+// coefficients) for bf16 and fp16 results, which are rounded by 1.7e-3 and 2e-4 (four
+// layers of width 2048, bf16: 12.6 ms, on one A 10.4), and by 12.5 (2 steps) for
+// fp32's from 192 rows on (4 layers of width 2048 in 17.3 ms instead of 22.7), below
+// which plain fp32 errs less than that.
 // Weights are treated as results of their type are: how large a part of a weight the
 // update is depends on the caller's lr, factor and weights, which may begin at zero.
 // (fp32 weights on 3 + 2 steps, their sums in chunks of 256 of K, were 3 to 11 times
 // as far off as the same steps in plain fp32, up to 6e-5 of O; a layer of width 700 /
 // 1024: 450 / 1500 us then, 600 / 2060 now.)
-enum Exactness { kExact, kClose, kCoarse };
-
-std::vector<int> segments_of(const Plan& plan, uint32_t m, uint32_t n, Exactness exact)
+std::vector<int> segments_of(const Plan& plan, uint32_t m, uint32_t n, bool exact)
 {
-    const double limit = exact == kExact ? (m < 192 ? 0.0 : 12.5) : exact == kClose ? 200.0 : 3e4;
+    const double limit = exact ? (m < 192 ? 0.0 : 12.5) : 200.0;
     const double grow = std::max(1.0, (double)plan.a * plan.a);
     int most = 1;
     for (double g = grow; g <= limit && most < plan.steps; g *= grow) ++most;
@@ -190,8 +191,8 @@ int products_in(const std::vector<int>& segments)
     return n;
 }
 
-// How exactly a result, or the update of a weight, has to come out for its type.
-Exactness exactness(rr_dtype_t type) { return type == RR_BF16 ? kCoarse : type == RR_F16 ? kClose : kExact; }
+// fp32 results, and updates of fp32 weights, come out as exactly as fp32 holds them.
+bool is_exact(rr_dtype_t type) { return type == RR_F32; }
 
 // Whether a cluster takes the matrix whole (rr_muon_small.cu).
 bool is_small(uint64_t rows, uint64_t cols)
@@ -233,8 +234,8 @@ std::vector<Group> groups_of(const rr_matrix_list_t* l, const Plan& plan, uint64
     for (int t = 0; t < l->nmatrices; ++t) {
         const Shape s{(uint32_t)l->rows[t], (uint32_t)l->cols[t]};
         if (s.numel() == 0 || is_small(s.rows, s.cols)) continue;
-        const Exactness exact = exactness(l->dtypes[t]);
-        const Kind kind{segments_of(plan, s.small(), std::max(s.rows, s.cols), exact), exact == kExact};
+        const bool exact = is_exact(l->dtypes[t]);
+        const Kind kind{segments_of(plan, s.small(), std::max(s.rows, s.cols), exact), exact};
         const uint64_t need = room_of(s, kind.segments).bytes();
         const int products = products_in(kind.segments);
         size_t k = 0, a = 0;  // its kind and its like in the last group
