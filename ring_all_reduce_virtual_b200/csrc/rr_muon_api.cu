@@ -135,12 +135,12 @@ rr_status_t make_plan(const rr_newton_schulz_t* ns, Plan* p)
 // multiplies what A was rounded by, up to a^2 a step, where its eigenvalues are
 // small: five steps on one A of 2^-22 are off by up to 2e4 * 1.4 * 2^-22 = 7e-3 of a
 // result that one strong direction dominates, more than bf16's own 1.7e-3.
-// Measured error of five steps against 64 bits in segments of 3 + 2 (chunk 4) / 2 + 2
-// + 1 / 1 each (chunk 1), from noise to one direction in 1 % of noise: 7e-6..7e-5 /
+// Measured error of five steps against 64 bits in segments of 3 + 2 (chunk 2) / 2 + 2
+// + 1 / 1 each (chunk 1), from noise to one direction in 1 % of noise: 4e-6..4e-5 /
 // 2e-6..2e-5 / 1e-6..1e-5, the same steps in plain fp32 2e-6..5e-5; of 5 steps
 // (chunk 4) 4e-6..7e-3.  So A's errors may grow by 200 (3 steps of the usual
 // coefficients) for bf16 and fp16 results, which are rounded by 1.7e-3 and 2e-4 (four
-// layers of width 2048, bf16: 12.6 ms, on one A 10.4), and by 12.5 (2 steps) for
+// layers of width 2048, bf16: 12.7 ms, on one A 10.4), and by 12.5 (2 steps) for
 // fp32's from 192 rows on (4 layers of width 2048 in 17.3 ms instead of 22.7), below
 // which plain fp32 errs less than that.
 // Weights are treated as results of their type are: how large a part of a weight the
@@ -301,11 +301,12 @@ uint8_t neighbours(const void* p, uint64_t es, uint32_t cols)
     return cols % 2 == 0 && (uintptr_t)p % (2 * es) == 0 ? 2 : 1;
 }
 
-// Stages of 64 of K between the roundings of a sum.  Error of five steps in
-// fp32, chunks of 1 / 2 / 4, from 128 x 128 to 8192 x 2048: 0.7e-6..2.0e-6 /
-// 1.2e-6..3.4e-6 / 1.3e-6..4.5e-6 (the same steps in plain fp32: 1.3e-6..6e-6);
-// time of 8 x 2048 x 2048, one step: 860 / 759 / 723 us.
-constexpr uint8_t kExactChunk = 1, kChunk = 4;
+// Stages of 64 of K between the roundings of a sum, of exact results and of others.
+// Error of five steps in fp32, chunks of 1 / 2 / 4, from 128 x 128 to 8192 x 2048:
+// 0.7e-6..2.0e-6 / 1.2e-6..3.4e-6 / 1.3e-6..4.5e-6 (the same steps in plain fp32:
+// 1.3e-6..6e-6); of three and two on one A 2e-6..2e-5 / 4e-6..4e-5 / 7e-6..7e-5.  Four
+// layers of width 2048, bf16: 15.4 / 12.7 / 12.5 ms, 24 of 256: 475 / 453 / 461 us.
+constexpr uint8_t kExactChunk = 1, kChunk = 2;
 
 // The products of a matrix of m <= n sides, in the order of their levels; X
 // begins in buffer 0.  *last: the result's buffer.
