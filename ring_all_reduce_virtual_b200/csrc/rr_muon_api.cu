@@ -141,8 +141,9 @@ rr_status_t make_plan(const rr_newton_schulz_t* ns, Plan* p)
 // (chunk 4) 4e-6..7e-3.  So A's errors may grow by 200 (3 steps of the usual
 // coefficients) for bf16 and fp16 results, which are rounded by 1.7e-3 and 2e-4 (four
 // layers of width 2048, bf16: 12.7 ms, on one A 10.4), and by 12.5 (2 steps) for
-// fp32's from 192 rows on (4 layers of width 2048 in 17.3 ms instead of 22.7), below
-// which plain fp32 errs less than that.
+// fp32's from 512 rows on (0.2 to 1.4 times plain fp32's error; 4 layers of width 2048
+// in 18.8 ms instead of 24), below which plain fp32 errs less than that (up to 2.1
+// times; 192 x 288 to 384 x 1536: 172..276 us, one step each 165..295).
 // Weights are treated as results of their type are: how large a part of a weight the
 // update is depends on the caller's lr, factor and weights, which may begin at zero.
 // (fp32 weights on 3 + 2 steps, their sums in chunks of 256 of K, were 3 to 11 times
@@ -150,7 +151,7 @@ rr_status_t make_plan(const rr_newton_schulz_t* ns, Plan* p)
 // 1024: 450 / 1500 us then, 600 / 2060 now.)
 std::vector<int> segments_of(const Plan& plan, uint32_t m, uint32_t n, bool exact)
 {
-    const double limit = exact ? (m < 192 ? 0.0 : 12.5) : 200.0;
+    const double limit = exact ? (m < 512 ? 0.0 : 12.5) : 200.0;
     const double grow = std::max(1.0, (double)plan.a * plan.a);
     int most = 1;
     for (double g = grow; g <= limit && most < plan.steps; g *= grow) ++most;
