@@ -116,7 +116,9 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, Bars* b
     return false;
 }
 
-// The same for a whole warp, one lane of which looks.
+// The same for a whole warp, one lane of which looks.  (A shuffle orders no memory:
+// what the others read or copy next is ordered by a warp's barrier or an instruction
+// of the whole warp behind this.)
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Bars* b, unsigned int* waits, uint32_t spin)
 {
     uint32_t ok = 0;
@@ -470,6 +472,7 @@ __device__ __forceinline__ uint32_t copy_tiles(const P& p, Bars* b, uint32_t ops
         if (s.seq != last || s.mat != of) {  // what the operands come from is finished
             uint32_t fine = 1;
             if (lane == 0 && t.op->level > 0) fine = parts_done(p.counters + 1 + t.mat, parts_before(p, t), b, p.waits, p.spin);
+            __syncwarp();  // the lanes that copy are behind the one that looked
             if (!__shfl_sync(kFull, fine, 0)) return it;
             last = s.seq;
             of = s.mat;
