@@ -82,15 +82,17 @@ __device__ __forceinline__ void muon_store_few(typename Ty::T* p, const float (&
 
 // scale / den as two factors that multiply a value one after the other: a power of
 // two and one of 1..2, so that neither product leaves fp32's range where the
-// result does not.
+// result does not.  den is infinite or NaN where a value is (norms of fp32 values are
+// within fp64's range): NaN for all of the matrix, also for what den alone would take to 0.
 struct MuonScale {
     float a, b;
 };
 
 __device__ __forceinline__ MuonScale muon_scale(double den, float scale)
 {
+    if (!isfinite(den)) return {NAN, NAN};
     int ex = 0;
-    const double frac = isfinite(den) ? frexp(den, &ex) : den;  // den = frac * 2^ex, frac in [0.5, 1)
+    const double frac = frexp(den, &ex);  // den = frac * 2^ex, frac in [0.5, 1)
     if (ex > -100 && ex < 100) return {ldexpf(1.0f, -ex) * scale, (float)(1.0 / frac)};
     return {ldexpf(1.0f, -ex / 2), ldexpf((float)(1.0 / frac), -(ex - ex / 2)) * scale};
 }
