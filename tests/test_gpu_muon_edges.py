@@ -22,3 +22,33 @@ def test_an_infinity_or_nan_makes_every_element_nan(shape, steps):
             o = rrv.orthogonalize([x, good], steps=steps)
             assert o[0].isnan().all(), (bad, dt)
             check(o[1], good, steps=steps)
+
+
+@pytest.mark.parametrize("steps,coef", [(0, COEF), (1, COEF), (2, COEF), (3, COEF), (4, COEF), (6, COEF), (7, COEF), (8, COEF), (11, COEF),
+                                        (5, (2.0, -1.5, 0.5)), (4, (1.5, -0.5, 0.0)), (3, (1.0, 0.0, 0.0)), (50, (1.0, 0.0, 0.0)),
+                                        (6, (-1.5, 0.5, 0.0))])
+def test_other_iterations_as_tiles(steps, coef):
+    """Segments of one, two and three steps, with and without a shorter last one, and no product at all."""
+    for r, c in ((200, 520), (520, 200), (513, 1600), (300, 300)):
+        for dt in TYPES.values():
+            x = gradient(r, c, dt, seed=steps)
+            check(rrv.orthogonalize([x], steps=steps, coefficients=coef)[0], x, steps=steps, coef=coef)
+
+
+@pytest.mark.parametrize("shape", [(100, 300), (600, 200), (512, 2048)])
+@pytest.mark.parametrize("norm", [1e-8, 1e-10, 1e-12, 1e-14])
+def test_matrices_whose_norm_is_below_eps(shape, norm):
+    """X begins small against its bound of 1, for which its halves are scaled by 2^15: they end at 2^-24 / 2^15, so
+    every element is off by 2^-40 at most, and by as much again in every step, which multiplies it by a = 3.4445."""
+    x = gradient(*shape, torch.float32)
+    x = x / x.norm() * norm
+    for dt in TYPES.values():
+        out = torch.empty(shape, dtype=dt, device="cuda")
+        rrv.orthogonalize([x], [out], eps=1e-7)
+        want, _ = iterate(x, eps=1e-7)
+        N = math.sqrt(shape[0] * shape[1])
+        lost = 2.0 ** -40 * N * sum(COEF[0] ** k for k in range(6))
+        near = 2e-5 if dt == torch.float32 else 6e-5  # test_gpu_muon_precision.py
+        step = float(((want.to(dt).double() - want).abs() * (1 + 4 / N)).norm())
+        err = float((out.double() - want).norm())
+        assert err <= lost + near * float(want.norm()) + step, (dt, err, lost, float(want.norm()))
