@@ -468,8 +468,8 @@ rr_status_t rr_embedding_grad(const void* const* ids, rr_id_type_t id_type, cons
  * launch and one pass over them.  logits[r]: ntokens rows of vocab values of
  * dtype (RR_F32, RR_BF16 or RR_F16), row_stride elements from row to row (a
  * padded LM head's further columns are not read); ids[r]: the ntokens given
- * tokens, of id_type.  With z = scale * x (scale: 1 / temperature, finite and
- * above 0), for row i = r * ntokens + t of the outputs:
+ * tokens, of id_type.  With z = scale * x (scale: 1 / temperature, 2^-64 to
+ * 2^64), for row i = r * ntokens + t of the outputs:
  *     lse[i]         = ln sum_j e^z_j
  *     logprob[i]     = z_id - lse, 0 for an id outside [0, vocab) (a padded token)
  *     entropy[i]     = - sum_j p_j ln p_j, p = e^(z - lse)     (NULL: not wanted)
@@ -479,9 +479,10 @@ rr_status_t rr_embedding_grad(const void* const* ids, rr_id_type_t id_type, cons
  *                      the pointers are not looked at)
  * all fp32 (top_id int32), sums in fp32.  Entries of -inf have probability 0.
  * A row whose every z is -inf has no distribution: lse and every log
- * probability of it are -inf, its entropy 0, its top ids the lowest.  A row
- * with a NaN or whose largest z is +inf has NaN for all of them but its top
- * ids (and the 0 of a padded token).  Rows may start on any element.  At most 2^31-1 rows in all,
+ * probability of it are -inf, its entropy 0 (its top ids are the largest logits'
+ * all the same).  A row with a NaN or whose largest z is +inf has NaN for all of
+ * them but its top ids (and the 0 of a padded token).  Rows may start on any
+ * element.  At most 2^31-1 rows in all,
  * vocab and row_stride up to 2^31-2.  Outputs must overlap nothing; a logits
  * buffer counts from its first row's first to its last row's last element. */
 rr_status_t rr_token_logprobs(const void* const* logits, size_t row_stride, const void* const* ids, rr_id_type_t id_type,

@@ -137,6 +137,13 @@ __device__ __forceinline__ float value_of(uint32_t order)
     return __uint_as_float(order & 0x80000000u ? order & 0x7fffffffu : ~order);  // NaN's order gives a NaN
 }
 
+// z - the row's largest z, also where the logits' difference leaves fp32.
+__device__ __forceinline__ float z_below(float x, float top, float scale)
+{
+    const float d = x - top;
+    return d == -INFINITY ? x * scale - top * scale : d * scale;
+}
+
 // ------------------------------------------------------- softmax statistics
 
 // A thread's sums relative to the largest value m that it has read: s of 2^y, t
@@ -483,14 +490,14 @@ __global__ void __launch_bounds__(kThreads) logprob_kernel(const __grid_constant
     if (lane == 0) {
         const int64_t id = id_at(p.ids[r], p.ids64, tok);
         float lp = 0.0f;
-        if (id >= 0 && id < (int64_t)p.V) lp = empty ? -INFINITY : (Ty::ld1(x + id) - top) * p.scale - ln_s;
+        if (id >= 0 && id < (int64_t)p.V) lp = empty ? -INFINITY : z_below(Ty::ld1(x + id), top, p.scale) - ln_s;
         p.logprob[row] = lp;
         p.lse[row] = empty ? -INFINITY : __fmaf_rn(top, p.scale, ln_s);
         if (ENT) p.entropy[row] = empty ? 0.0f : ln_s - kLn2 * (st.t / st.s);
     }
     if (TOP && lane < p.k) {
         const float v = value_of((uint32_t)(best >> 32));
-        p.top_logprob[row * p.k + lane] = empty ? -INFINITY : (v - top) * p.scale - ln_s;
+        p.top_logprob[row * p.k + lane] = empty ? -INFINITY : z_below(v, top, p.scale) - ln_s;
         p.top_id[row * p.k + lane] = (int32_t)~(uint32_t)best;
     }
 }

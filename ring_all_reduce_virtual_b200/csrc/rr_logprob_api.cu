@@ -1,8 +1,6 @@
 // rr_logprob_api.cu -- host side of the token log probabilities
 // (rr_token_logprobs, rr_token_logprobs_grad in include/rr.h): argument checks
 // and the rows' split.
-#include <cmath>
-
 #include "rr_host.h"
 #include "rr_logprob.h"
 
@@ -12,6 +10,10 @@ namespace {
 
 constexpr uint64_t kMaxRows = 0x7fffffffull;   // rows of all ranks
 constexpr uint64_t kMaxWidth = 0x7ffffffeull;  // vocabulary, and elements from row to row
+
+// Factors of log2 e and more stay within fp32, and where two logits differ by more than
+// fp32 holds (2^128), their z differ by more than an exponential can show.
+constexpr float kLeastScale = 0x1p-64f, kMostScale = 0x1p64f;
 
 struct Rows {
     int n;
@@ -30,7 +32,7 @@ rr_status_t check_rows(const Rows& s)
     if (s.V < 1 || s.V > kMaxWidth) return fail(RR_ERR_INVALID_ARG, "the vocabulary must be in 1..2^31-2");
     if (s.ld < s.V || s.ld > kMaxWidth) return fail(RR_ERR_INVALID_ARG, "the row stride must be in vocab..2^31-2");
     if (s.T > kMaxRows || s.T * (uint64_t)s.n > kMaxRows) return fail(RR_ERR_INVALID_ARG, "more than 2^31-1 tokens in all");
-    if (!(s.scale > 0.0f) || std::isinf(s.scale)) return fail(RR_ERR_INVALID_ARG, "scale must be finite and above 0");
+    if (!(s.scale >= kLeastScale && s.scale <= kMostScale)) return fail(RR_ERR_INVALID_ARG, "scale must be in 2^-64..2^64");
     return RR_OK;
 }
 

@@ -1,0 +1,59 @@
+"""Token log probabilities and their gradient at the ends of their range
+(tolerances: test_gpu_logprob.py)."""
+import math
+
+import pytest
+import torch
+
+import ring_all_reduce_virtual_b200 as rrv
+from test_gpu_logprob import E24, TYPES, check_backward, check_forward, formulas, make
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("power", [-64, -40, 40, 64])
+def test_scales_at_the_ends(power):
+    """Logits that a scale of 2^power takes to ordinary z, the same as those z give with a scale of 1."""
+    xs, ids = make(1, 6, 3001, torch.float32, seed=2)
+    plain = rrv.token_logprobs(xs, ids, entropy=True, top_k=5)
+    x = xs[0] * 2.0 ** -power
+    got = check_forward([x], ids, 2.0 ** power, 5)
+    check_backward([x], ids, 2.0 ** power, got, True)
+    assert torch.equal(got.top_id, plain.top_id)
+    equal = torch.full((3, 3001), 7.0 * 2.0 ** -power, device="cuda")
+    got = rrv.token_logprobs([equal], [torch.zeros(3, dtype=torch.int64, device="cuda")], scale=2.0 ** power, entropy=True)
+    assert ((got.logprob + math.log(3001)).abs() <= E24 * (3001 / 512 + 128 + 16)).all()
+
+
+def test_scales_beyond_are_refused():
+    xs, ids = make(1, 2, 10, torch.float32)
+    for scale in (2.0 ** 65, 3e38, 2.0 ** -65, 1e-40):
+        with pytest.raises(rrv.RRError):
+            rrv.token_logprobs(xs, ids, scale=scale)
+        with pytest.raises(rrv.RRError):
+            rrv.token_logprobs_grad(xs, ids, torch.zeros(2, device="cuda"), torch.zeros(2, device="cuda"), scale=scale)
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -60, 2.0 ** -20, 1.0])
+def test_logits_further_apart_than_fp32_reaches(scale):
+    """3e38 and -3e38 in one row: their difference leaves fp32, the log probability of a small scale does not."""
+    V = 1500
+    x = torch.randn(4, V, device="cuda")
+    x[0, 3], x[0, 9] = 3e38, -3e38
+    x[1, 3], x[1, 9], x[1, 10] = 3e38, 2.9e38, -3.4e38
+    x[2, :] = -3e38
+    x[2, 700] = 3.3e38
+    t = torch.tensor([9, 10, 8, 1], device="cuda")
+    got = rrv.token_logprobs([x], [t], scale=scale, entropy=True, top_k=3)
+    z = x.double() * scale
+    logp = torch.log_softmax(z, -1)
+    want = logp[torch.arange(4, device="cuda"), t]
+    reach = torch.where(want < -3.4e38, -math.inf, want)  # below fp32's range
+    fine = reach.isinf() == got.logprob[0].isinf()
+    near = (got.logprob[0].double() - want).abs() <= 1e-4 + 2.0 ** -21 * want.abs()
+    assert (fine & (near | reach.isinf())).all(), (got.logprob, want)
+    best = torch.sort(x, dim=-1, descending=True, stable=True).indices[:, :3]
+    assert torch.equal(got.top_id[0].long(), best)
+    w = logp.gather(1, best)
+    assert (((got.top_logprob[0].double() - w).abs() <= 1e-4 + 2.0 ** -21 * w.abs()) | (w < -3.4e38)).all()
+    assert not got.entropy.isnan().any()

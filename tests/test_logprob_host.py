@@ -74,3 +74,10 @@ def test_python_calls_check_their_tensors():
         rrv.token_logprobs([], [])
     with pytest.raises(TypeError, match="int32 or int64"):
         rrv.token_logprobs([x], [x])
+
+
+@pytest.mark.parametrize("call", [forward, backward])
+def test_scales_outside_their_range_are_refused(call):
+    for scale in (2.0 ** 65, 3e38, 2.0 ** -65, 1e-40):
+        assert call(scale=scale) == INVALID, scale
+    assert call(scale=2.0 ** 64, T=0) == 0 and call(scale=2.0 ** -64, T=0) == 0
