@@ -499,8 +499,12 @@ rr_status_t rr_token_logprobs(const void* const* logits, size_t row_stride, cons
  * may be logits[r] itself with the same stride (each logit is read before its
  * gradient is written), and otherwise overlaps nothing.  Rows whose lse is
  * -inf, and rows with g = h = 0 (padded tokens), get zeros, whatever they hold.
- * p is e^(z - lse), so lse must be this row's; where |lse| is above 2^24 it no
- * longer holds the sum's logarithm and p is 1 for every logit at the maximum. */
+ * p is e^(z - lse), so lse must be this row's.  It is one fp32 number, half a
+ * step of which is a relative error of p: p is off by (|lse| + |ln p|) * 2^-24
+ * of itself (1e-6 at |lse| = 20, 6e-5 at 1000, 4e-3 at fp16's lowest value; above
+ * 2^24 lse no longer holds the sum's logarithm and p is 1 for every logit at the
+ * maximum).  Where a row's logits share a large offset, take it off before both
+ * calls: neither log probabilities nor gradients change by it. */
 rr_status_t rr_token_logprobs_grad(const void* const* logits, size_t row_stride, const void* const* ids,
                                    rr_id_type_t id_type, int nranks, size_t ntokens, size_t vocab, rr_dtype_t dtype,
                                    float scale, const float* lse, const float* entropy, const float* dlogprob,

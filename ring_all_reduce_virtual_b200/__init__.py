@@ -632,7 +632,9 @@ def token_logprobs_grad(logits, tokens, lse, dlogprob, entropy=None, dentropy=No
     ``dentropy`` is given) it returned for the same logits and scale.
     ``dlogprob``, ``dentropy``: float32 [ranks, tokens], the loss's gradients
     with respect to each log probability and entropy (-1 / tokens for a mean
-    cross entropy).  ``outs``: one tensor per rank like its logits -- the
+    cross entropy).  Probabilities are e^(z - lse), off by ``|lse|`` 2^-24 of
+    themselves: a large offset that a row's logits share is better taken off
+    before both calls.  ``outs``: one tensor per rank like its logits -- the
     logits themselves, say -- or None for new ones.  Returns ``outs``."""
     ids, id_type, n, T, dev = _id_set(tokens, "token_logprobs_grad")
     x, xn, rows, V, stride, d, xdev = _logit_set(logits, "token_logprobs_grad")

@@ -514,7 +514,8 @@ struct GradRow {
     float scale, lse, g, h, H, at_target;
     uint32_t target;
 
-    // z - lse rounds once, at its own size: an error of p of half a step of ln p
+    // z - lse rounds once, at its own size, and lse came rounded at its: p is off by
+    // (|ln p| + |lse|) 2^-24 of itself, beside the exponential's 2^-22
     __device__ __forceinline__ float at(float x) const
     {
         const float lp = __fmaf_rn(x, scale, -lse);

@@ -57,3 +57,40 @@ def test_logits_further_apart_than_fp32_reaches(scale):
     w = logp.gather(1, best)
     assert (((got.top_logprob[0].double() - w).abs() <= 1e-4 + 2.0 ** -21 * w.abs()) | (w < -3.4e38)).all()
     assert not got.entropy.isnan().any()
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("offset", [0.0, 40.0, -1000.0, 6e4])
+def test_gradients_of_rows_with_a_common_offset(dtype, offset):
+    """Against the 64-bit formula of the logits alone, lse included: half a step of the lse that the gradient is given
+    (|lse| 2^-24), what the forward pass errs by (its ln s: 2^-24 (V / 512 + 128)) and the difference's own rounding
+    are p's relative error."""
+    if dtype == "bf16" and abs(offset) > 1000:
+        offset = 8192.0
+    T, V, dt = 5, 2000, TYPES[dtype]
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    x = (torch.randn(T, V, generator=gen, device="cuda") * 2 + offset).to(dt)
+    x[2] = torch.finfo(torch.float16).min if dtype == "f16" else offset  # a uniform row
+    t = torch.tensor([5, -1, 7, 8, 1999], device="cuda")
+    g, h = torch.randn(2, T, generator=gen, device="cuda")
+    fwd = rrv.token_logprobs([x], [t], entropy=True)
+    _, lse, H, logp, p, known = formulas(x, t, 1.0)
+    base = E24 * (V / 512 + 128)
+    off = base + E24 * (lse.abs()[:, None] + logp.abs() + 16)
+    for ent in (False, True):
+        got = rrv.token_logprobs_grad([x], [t], fwd.lse, g[None], entropy=fwd.entropy if ent else None,
+                                      dentropy=h[None] if ent else None)[0].double()
+        gk = torch.where(known, g.double(), 0.0)[:, None]
+        want = -gk * p
+        want[known, t[known]] += gk[known, 0]
+        tol = gk.abs() * p * off
+        if ent:
+            want -= h.double()[:, None] * p * (logp + H[:, None])
+            # ln p and the entropy are off, too, the latter by up to ln V times ln s's error
+            tol = tol + h.abs()[:, None] * p * (off * ((logp + H[:, None]).abs() + 1) + base * (2 + math.log(V)))
+        step = torch.finfo(dt).eps / 2
+        tiny = torch.finfo(dt).tiny * (torch.finfo(dt).eps if dt == torch.float16 else 1.0)
+        # the target's element is the sum of two terms, of at most g each before its rounding
+        tol = tol * (1 + 2 * off) + want.abs() * step * (1 + 1e-3) + gk.abs() * 2 * E24 + tiny
+        bad = (got - want).abs() > tol
+        assert not bad.any(), (ent, bad.nonzero()[:4], got[bad][:4], want[bad][:4], tol[bad][:4])
