@@ -94,3 +94,28 @@ def test_gradients_of_rows_with_a_common_offset(dtype, offset):
         tol = tol * (1 + 2 * off) + want.abs() * step * (1 + 1e-3) + gk.abs() * 2 * E24 + tiny
         bad = (got - want).abs() > tol
         assert not bad.any(), (ent, bad.nonzero()[:4], got[bad][:4], want[bad][:4], tol[bad][:4])
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("T,V", [(3, 50003), (64, 20000), (1, 128000), (900, 4001), (1300, 1024)])
+@pytest.mark.parametrize("left", [0, 1, 5, 19])
+def test_masks_that_leave_fewer_tokens_than_alternatives(dtype, T, V, left):
+    """-inf, or the type's lowest value, everywhere but at a few tokens, some of them alike: these first, then the lowest
+    of the masked ids."""
+    dt, k = TYPES[dtype], 20
+    gen = torch.Generator(device="cuda").manual_seed(left)
+    for low in (-math.inf, torch.finfo(dt).min, 1.5):  # 1.5: a constant row with a few larger values
+        x = torch.full((T, V), low, dtype=dt, device="cuda")
+        if left:
+            at = torch.stack([torch.randperm(V, generator=gen, device="cuda")[:left] for _ in range(min(T, 8))]).repeat(-(-T // 8), 1)[:T]
+            x.scatter_(1, at, (torch.randint(4, (T, left), generator=gen, device="cuda") + 2.0).to(dt))
+        t = torch.randint(V, (T,), generator=gen, device="cuda")
+        got = rrv.token_logprobs([x], [t], entropy=True, top_k=k)
+        want = torch.sort(x.float(), dim=-1, descending=True, stable=True).indices[:, :k]
+        assert torch.equal(got.top_id[0].long(), want), low
+        if left or low > -math.inf:
+            w = torch.log_softmax(x.double(), -1).gather(1, want)
+            tol = E24 * (V / 512 + 128) + E24 * 8 * w.abs()
+            assert ((got.top_logprob[0] == w) | ((got.top_logprob[0] - w).abs() <= tol)).all(), low
+        else:
+            assert (got.top_logprob == -math.inf).all()
