@@ -320,6 +320,18 @@ __device__ __forceinline__ void pdl_begin()
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// A CTA's shared memory as another CTA of its cluster sees it.
+template <class T>
+__device__ __forceinline__ T* cluster_at(T* p, uint32_t rank)
+{
+    uint64_t r;
+    asm("mapa.u64 %0, %1, %2;" : "=l"(r) : "l"(p), "r"(rank));
+    return reinterpret_cast<T*>(r);
+}
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }  // release
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }      // acquire
+
 // The segment owning work item w: the last s with prefix[s] <= w (segments
 // without tiles have prefix[s] == prefix[s + 1] and are never returned).
 __device__ __forceinline__ int find_segment(const uint64_t* prefix, int nseg, uint64_t w)

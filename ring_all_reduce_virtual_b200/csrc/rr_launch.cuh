@@ -2,6 +2,7 @@
 // work item, and the dispatch from (dtype, op) codes to kernel templates.
 #pragma once
 
+#include <atomic>
 #include <type_traits>
 
 #include "rr_device.cuh"
@@ -39,6 +40,42 @@ inline cudaError_t launch_pdl(void (*kernel)(A...), dim3 grid, unsigned threads,
     cfg.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a...);
     return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// The same in clusters of `size` neighbouring CTAs.
+template <class... A>
+inline cudaError_t launch_pdl_clusters(void (*kernel)(A...), unsigned ctas, unsigned threads, uint32_t smem, unsigned size,
+                                       cudaStream_t s, const A&... a)
+{
+    cudaLaunchAttribute attr[2]{};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = size;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a...);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// Asks for a kernel's dynamic shared memory, once on each device.
+template <auto KERNEL>
+cudaError_t allow_smem(uint32_t bytes)
+{
+    constexpr int kMaxDevices = 64;
+    static std::atomic<bool> asked[kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < kMaxDevices && asked[dev].load(std::memory_order_acquire))) return e;
+    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess && dev < kMaxDevices) asked[dev].store(true, std::memory_order_release);
+    return e;
 }
 
 template <class F>

@@ -282,17 +282,6 @@ struct TopList {
 
 // ---------------------------------------------------------------- the pass
 
-template <class T>
-__device__ __forceinline__ T* cluster_at(T* p, uint32_t rank)
-{
-    uint64_t r;
-    asm("mapa.u64 %0, %1, %2;" : "=l"(r) : "l"(p), "r"(rank));
-    return reinterpret_cast<T*>(r);
-}
-
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }  // release
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }      // acquire
-
 struct Shared {
     uint32_t order[kThreads / 32], best[32];
     float2 sums[kThreads / 32];
@@ -629,20 +618,7 @@ cudaError_t launch_logprob_as(const LogprobParams& p, bool warp, cudaStream_t s)
     if (warp)
         return launch_pdl(logprob_kernel<Ty, 32, ENT, TOP>, dim3((unsigned)((p.M + kThreads / 32 - 1) / (kThreads / 32))), kThreads, 0, s, p);
     if (p.split == 1) return launch_pdl(logprob_kernel<Ty, kThreads, ENT, TOP>, dim3(p.M), kThreads, 0, s, p);
-    cudaLaunchAttribute attr[2]{};
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)p.split;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(p.M * (unsigned)p.split);
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, logprob_kernel<Ty, kThreads, ENT, TOP>, p);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return launch_pdl_clusters(logprob_kernel<Ty, kThreads, ENT, TOP>, p.M * (unsigned)p.split, kThreads, 0, (unsigned)p.split, s, p);
 }
 
 template <class F>

@@ -597,7 +597,7 @@ rr_status_t orthogonalize(const rr_matrix_list_t* in, const rr_matrix_list_t* ou
     if ((st = check_list(in, "matrices")) != RR_OK) return st;
     if ((st = check_list(out, "results")) != RR_OK) return st;
     if ((st = same_shapes(in, out)) != RR_OK) return st;
-    std::vector<Span> spans, read;
+    std::vector<Span> spans;
     spans.reserve((size_t)(out->nranks + 1) * out->nmatrices + 1);
     if ((st = add_spans(out, out->nranks, true, spans)) != RR_OK) return st;
     for (int t = 0; t < in->nmatrices; ++t) {  // a result of its type may take its matrix's place

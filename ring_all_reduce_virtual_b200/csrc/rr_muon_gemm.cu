@@ -33,7 +33,6 @@
 // warps stop, wait (bounded) for copies and products in flight, give their
 // tensor memory back and leave; what the call writes is then undefined.
 #include <algorithm>
-#include <atomic>
 #include <cstddef>
 
 #include <cuda_fp16.h>
@@ -662,8 +661,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) muon_gemm_kernel(const __grid
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     }
-    asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // both CTAs' barriers are set up
+    cluster_arrive();
+    cluster_wait();  // both CTAs' barriers are set up
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = b->tmem;
     pdl_begin();
@@ -716,8 +715,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) muon_gemm_kernel(const __grid
         __syncwarp();
     }
     // neither CTA leaves while the other may read its operands or arrive on its barriers
-    asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    cluster_arrive();
+    cluster_wait();
     if (warp == 1)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
@@ -725,31 +724,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) muon_gemm_kernel(const __grid
 template <bool WIDE, class P>
 cudaError_t launch_as(const P& p, uint32_t pairs, cudaStream_t s)
 {
-    constexpr int kMaxDevices = 64;
-    static std::atomic<bool> asked[kMaxDevices];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev >= kMaxDevices || !asked[dev].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(muon_gemm_kernel<WIDE, P>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
-        if (e != cudaSuccess) return e;
-        if (dev < kMaxDevices) asked[dev].store(true, std::memory_order_release);
-    }
-    cudaLaunchAttribute attr[2]{};
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 2;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(2 * pairs);
-    cfg.blockDim = dim3(kGemmThreads);
-    cfg.dynamicSmemBytes = kSmem;
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, muon_gemm_kernel<WIDE, P>, p);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    const cudaError_t e = allow_smem<muon_gemm_kernel<WIDE, P>>(kSmem);
+    return e != cudaSuccess ? e : launch_pdl_clusters(muon_gemm_kernel<WIDE, P>, 2 * pairs, kGemmThreads, kSmem, 2, s, p);
 }
 
 // Tiles of one product of each matrix.

@@ -17,7 +17,6 @@
 // barriers.  As tiles of rr_muon_gemm.cu a level of such a matrix takes 8 us, most
 // of it the way through L2: one layer of width 128 (fp32) 155 us against 70.
 #include <algorithm>
-#include <atomic>
 
 #include <cuda_fp16.h>
 
@@ -46,16 +45,8 @@ struct SmallShared {
 
 __device__ __forceinline__ void cluster_sync()
 {
-    asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-}
-
-template <class T>
-__device__ __forceinline__ T* in_cta(T* p, uint32_t rank)
-{
-    uint64_t r;
-    asm("mapa.u64 %0, %1, %2;" : "=l"(r) : "l"(p), "r"(rank));
-    return reinterpret_cast<T*>(r);
+    cluster_arrive();
+    cluster_wait();
 }
 
 // The 16-byte piece of an m x 128 half that begins at (r, c): blocks of 64 x 64,
@@ -190,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1) muon_small_kernel(const __grid_co
     }
     pdl_begin();
 
-    // this CTA's columns, momentum and all, as fp32 in A's and B's place
+    // this CTA's columns, momentum and all, as fp32 in A's place
     uint8_t* S = A;
     const uint32_t prows = wide ? m : width, pcols = wide ? width : m;  // its part of the matrix as it lies
     const uint64_t first = wide ? n0 : (uint64_t)n0 * t.cols;
@@ -240,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1) muon_small_kernel(const __grid_co
     });
     squares = cta_sum(squares, sh.sums);
     cluster_sync();  // every CTA runs, so its shared memory may be written
-    if (tid < used) *in_cta(&sh.part[rank], tid) = squares;
+    if (tid < used) *cluster_at(&sh.part[rank], tid) = squares;
     cluster_sync();
     double total = 0.0;
     for (uint32_t k = 0; k < used; ++k) total += sh.part[k];
@@ -294,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1) muon_small_kernel(const __grid_co
                         const uint32_t r = (group + u * used) * 16 + tid / 16;
                         x[u][k][0] = x[u][k][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                         if (k0 + k < used && r < kSide) {
-                            uint8_t* const of = in_cta(B, k0 + k);
+                            uint8_t* const of = cluster_at(B, k0 + k);
                             x[u][k][0] = *quad(of, r, c / 4);
                             x[u][k][1] = *quad(of, r, c / 4 + 1);
                         }
@@ -324,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1) muon_small_kernel(const __grid_co
                 for (int l = 0; l < 8; ++l) w[l] = v[u][l] - w[l];
                 const uint4 lo = F16T::pack(w);
                 for (uint32_t k = 0; k < used; ++k) {
-                    uint8_t* const of = in_cta(A, k);
+                    uint8_t* const of = cluster_at(A, k);
                     *piece(of, r, c) = hi;
                     *piece(of + kPlaneBytes, r, c) = lo;
                 }
@@ -429,31 +420,8 @@ __global__ void __launch_bounds__(kThreads, 1) muon_small_kernel(const __grid_co
 template <class P>
 cudaError_t launch_as(const P& p, cudaStream_t s)
 {
-    constexpr int kMaxDevices = 64;
-    static std::atomic<bool> asked[kMaxDevices];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev >= kMaxDevices || !asked[dev].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(muon_small_kernel<P>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmallSmem);
-        if (e != cudaSuccess) return e;
-        if (dev < kMaxDevices) asked[dev].store(true, std::memory_order_release);
-    }
-    cudaLaunchAttribute attr[2]{};
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = p.ctas;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(p.ctas * (unsigned)p.n);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmallSmem;
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, muon_small_kernel<P>, p);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    const cudaError_t e = allow_smem<muon_small_kernel<P>>(kSmallSmem);
+    return e != cudaSuccess ? e : launch_pdl_clusters(muon_small_kernel<P>, p.ctas * (unsigned)p.n, kThreads, kSmallSmem, p.ctas, s, p);
 }
 
 }  // namespace
