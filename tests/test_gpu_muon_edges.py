@@ -52,3 +52,13 @@ def test_matrices_whose_norm_is_below_eps(shape, norm):
         step = float(((want.to(dt).double() - want).abs() * (1 + 4 / N)).norm())
         err = float((out.double() - want).norm())
         assert err <= lost + near * float(want.norm()) + step, (dt, err, lost, float(want.norm()))
+
+
+@pytest.mark.parametrize("shape", [(1, 1 << 20), (1 << 20, 3), (5, 200003), (131, 70001)])
+def test_the_longest_matrices(shape):
+    """Up to 2^20 rows or columns, where X X^T goes through 16384 blocks of K."""
+    for dt in (torch.float32, torch.bfloat16):
+        x = gradient(*shape, dt, seed=4)
+        check(rrv.orthogonalize([x])[0], x)
+        rrv.check_timeouts()
+    torch.cuda.empty_cache()
