@@ -79,7 +79,7 @@ struct MuonWork {
 
 // Matrices per group, and per launch that takes them whole.  While one waits for a
 // level of its own, others have tiles: 24 layers of width 256, bf16, in groups of 24
-// / 128: 907 / 442 us, 12 of 1024: 4448 / 4398.
+// / 128: 960 / 450 us, 12 of 1024: 5620 / 5570.
 constexpr int kMuonMats = 128;
 constexpr int kMuonOps = 200;         // different products of a launch, at most
 constexpr int kMuonSeq = 768;         // products of a launch, those of like matrices counted once

@@ -142,7 +142,7 @@ rr_status_t make_plan(const rr_newton_schulz_t* ns, Plan* p)
 // coefficients) for bf16 and fp16 results, which are rounded by 1.7e-3 and 2e-4 (four
 // layers of width 2048, bf16: 12.7 ms, on one A 10.4), and by 12.5 (2 steps) for
 // fp32's from 512 rows on (0.2 to 1.4 times plain fp32's error; 4 layers of width 2048
-// in 18.8 ms instead of 24), below which plain fp32 errs less than that (up to 2.1
+// in 17.8 ms instead of 24), below which plain fp32 errs less than that (up to 2.1
 // times; 192 x 288 to 384 x 1536: 172..276 us, one step each 165..295).
 // Weights are treated as results of their type are: how large a part of a weight the
 // update is depends on the caller's lr, factor and weights, which may begin at zero.

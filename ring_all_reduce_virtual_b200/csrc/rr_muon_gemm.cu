@@ -753,8 +753,8 @@ cudaError_t launch_muon_gemm(MuonGemmParams& p, int nops, cudaStream_t s)
     // Tiles of 256 columns where those of a square product, which most levels are,
     // keep half of the pairs of SMs busy, and for Q X where every pair has one;
     // narrower ones, twice as many, are done sooner.  One / four layers of width 512,
-    // bf16, in tiles of 256: 302 / 377 us, of 128: 245 / 408; two of 1000, fp16: 924
-    // and 1108.
+    // bf16, in tiles of 256: 351 / 444 us, of 128: 297 / 467; two of 1000, fp16: 975
+    // and 1218.
     const bool wide = tiles_of_all(p, kSquare, 256) >= kPairs / 2;
     uint32_t widest = 0;
     for (int kind = 0; kind < 3; ++kind) {
