@@ -549,7 +549,7 @@ rr_status_t rr_muon_workspace(const rr_matrix_list_t* results, int weights, cons
  * products run on the tensor cores with operands of 22 bits and fp32 sums; the
  * result is rounded once to its type.  fp32 results are as near to the exact
  * polynomial as the same steps in fp32 are (about 1e-6 to 2e-5 of the matrix's
- * norm); for bf16 and fp16 results of matrices that are not square several
+ * norm, most where singular values are far apart); for bf16 and fp16 results of matrices that are not square several
  * steps share one A, whose roundings then count up to 5e-5 of it (the types'
  * own: 1.7e-3 and 2e-4).  Of a matrix whose norm is far below eps little is
  * left, which is off by about 1e-8 of an orthogonal matrix's norm.  A matrix of
