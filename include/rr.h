@@ -540,7 +540,8 @@ typedef struct rr_newton_schulz {
 /* The bytes of device workspace the calls below need (host only) for their
  * list of results (weights 0: rr_orthogonalize) or weights (1: rr_muon_step):
  * 256-byte aligned, contents neither used nor kept, one call at a time (see
- * rr_clip_workspace).  Matrices run in groups of up to 128 and 5 GiB of it. */
+ * rr_clip_workspace).  Matrices run in groups of up to 128 and 5 GiB of it; both sides of one
+ * that is not at most 128 x 1024 count as multiples of 128. */
 rr_status_t rr_muon_workspace(const rr_matrix_list_t* results, int weights, const rr_newton_schulz_t* ns, size_t* bytes);
 
 /* Orthogonalises every matrix of `matrices` (its rank 0) into every rank's
@@ -549,12 +550,12 @@ rr_status_t rr_muon_workspace(const rr_matrix_list_t* results, int weights, cons
  * products run on the tensor cores with operands of 22 bits and fp32 sums; the
  * result is rounded once to its type.  fp32 results are as near to the exact
  * polynomial as the same steps in fp32 are (about 1e-6 to 2e-5 of the matrix's
- * norm, most where singular values are far apart); for bf16 and fp16 results of matrices that are not square several
- * steps share one A, whose roundings then count up to 5e-5 of it (the types'
- * own: 1.7e-3 and 2e-4).  Of a matrix whose norm is far below eps little is
- * left, which is off by about 1e-8 of an orthogonal matrix's norm.  A matrix of
- * zeros stays zero; one with a NaN or an infinity gives NaN.  The same call gives
- * the same bits. */
+ * norm, most where singular values are far apart); for bf16 and fp16 results of
+ * matrices that are not square several steps share one A, whose roundings then
+ * count up to 5e-5 of it (the types' own: 1.7e-3 and 2e-4).  Of a matrix whose
+ * norm is far below eps little is left, which is off by about 1e-8 of an
+ * orthogonal matrix's norm.  A matrix of zeros stays zero; one with a NaN or an
+ * infinity gives NaN.  The same call gives the same bits. */
 rr_status_t rr_orthogonalize(const rr_matrix_list_t* matrices, const rr_matrix_list_t* results, const rr_newton_schulz_t* ns,
                              void* workspace, size_t workspace_bytes, cudaStream_t stream);
 

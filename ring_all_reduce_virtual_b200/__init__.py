@@ -579,7 +579,8 @@ def token_logprobs(logits, tokens, scale: float = 1.0, entropy: bool = False, to
     every rank's rows in one launch and one pass (``rr_token_logprobs``).
     ``logits``: one tensor [tokens, vocabulary] per rank (float32, bfloat16 or
     float16; any row stride); ``tokens``: one int32 or int64 tensor per rank, or
-    a RankSet; ``scale``: 1 / temperature, 2^-64 to 2^64.  A token outside the vocabulary (padding) has log probability 0.
+    a RankSet; ``scale``: 1 / temperature, 2^-64 to 2^64.  A token outside the
+    vocabulary (padding) has log probability 0.
     ``entropy`` adds each row's entropy, ``top_k`` (up to 32) its most likely
     ids, equal logits with the lowest id first, and their log probabilities.
     The values of a call share one storage, its top ids another."""

@@ -9,6 +9,7 @@ import pytest
 import ring_all_reduce_virtual_b200 as rrv
 
 PACKAGE = os.path.dirname(os.path.abspath(rrv.__file__))
+QUIET = dict(os.environ, ASAN_OPTIONS="detect_leaks=0")  # which wants to trace the process
 
 PROGRAM = r"""
 #include "rr_muon_api.cu"
@@ -268,11 +269,11 @@ def program(tmp_path_factory):
 
 def test_lists_that_have_every_shape_in_three_types(program):
     """Each product of each matrix is listed once, within the launch's parameters and in the order of its levels."""
-    out = subprocess.run([program], capture_output=True, text=True, timeout=300)
+    out = subprocess.run([program], env=QUIET, capture_output=True, text=True, timeout=300)
     assert out.returncode == 0 and "bad 0" in out.stdout, out.stdout + out.stderr[:4000]
 
 
 def test_any_list(program):
     """Lists of any shapes, types, replicas and iterations: every matrix once, workspaces apart and within what was asked for."""
-    out = subprocess.run([program, "any"], capture_output=True, text=True, timeout=300)
+    out = subprocess.run([program, "any"], env=QUIET, capture_output=True, text=True, timeout=300)
     assert out.returncode == 0 and "bad 0" in out.stdout, out.stdout + out.stderr[:4000]
