@@ -552,7 +552,7 @@ rr_status_t rr_muon_workspace(const rr_matrix_list_t* results, int weights, cons
  * polynomial as the same steps in fp32 are (about 1e-6 to 2e-5 of the matrix's
  * norm, most where singular values are far apart); for bf16 and fp16 results of
  * matrices that are not square several steps share one A, whose roundings then
- * count up to 5e-5 of it (the types' own: 1.7e-3 and 2e-4).  Of a matrix whose
+ * count up to about 5e-5 of it (the types' own: 1.7e-3 and 2e-4).  Of a matrix whose
  * norm is far below eps little is left, which is off by about 1e-8 of an
  * orthogonal matrix's norm.  A matrix of zeros stays zero; one with a NaN or an
  * infinity gives NaN.  The same call gives the same bits. */

@@ -143,9 +143,11 @@ rr_status_t make_plan(const rr_newton_schulz_t* ns, Plan* p)
 // layers of width 2048, bf16: 12.7 ms, on one A 10.4), and by 12.5 (2 steps) for
 // fp32's from 512 rows on (0.2 to 1.4 times plain fp32's error; 4 layers of width 2048
 // in 17.8 ms instead of 24), below which plain fp32 errs less than that (up to 2.1
-// times; 192 x 288 to 384 x 1536: 172..276 us, one step each 165..295).  fp32's take no
-// more than two on one A where a is small, either: Q's roundings add up (20 steps of 1,
-// -0.3, 0.1 on one A: 2.9e-5, plain fp32 4e-7).
+// times; 192 x 288 to 384 x 1536: 172..276 us, one step each 165..295).  A polynomial
+// of a small a takes many steps, and the roundings of Q, which has a's part in the
+// tensor cores' sums, add up over those on one A: no more than three (two) share one
+// there, either, and below a^2 = 2 fp32's none (40 steps of 1, 0.6, -0.55 in fp32, two
+// on one A: 3e-5, plain fp32 5e-7; 50 of 1, -0.3, 0.1 in fp16, all on one A: 2e-4).
 // Weights are treated as results of their type are: how large a part of a weight the
 // update is depends on the caller's lr, factor and weights, which may begin at zero.
 // (fp32 weights on 3 + 2 steps, their sums in chunks of 256 of K, were 3 to 11 times
@@ -153,9 +155,9 @@ rr_status_t make_plan(const rr_newton_schulz_t* ns, Plan* p)
 // 1024: 450 / 1500 us then, 600 / 2060 now.)
 std::vector<int> segments_of(const Plan& plan, uint32_t m, uint32_t n, bool exact)
 {
-    const double limit = exact ? (m < 512 ? 0.0 : 12.5) : 200.0;
     const double grow = std::max(1.0, (double)plan.a * plan.a);
-    const int longest = exact ? std::min(2, plan.steps) : plan.steps;
+    const double limit = exact ? (m < 512 || grow < 2.0 ? 0.0 : 12.5) : 200.0;
+    const int longest = std::min(exact ? 2 : 3, plan.steps);
     int most = 1;
     for (double g = grow; g <= limit && most < longest; g *= grow) ++most;
     // nearly square matrices would gain less than a twentieth
